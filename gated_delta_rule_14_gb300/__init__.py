@@ -12,10 +12,11 @@ variantes de atencion lineal de la familia DeltaNet", sections "Gated DeltaNet" 
 
 ``chunk_fwd`` runs the chunkwise prefill, ``decode_step`` one fused single-token
 step and ``chunk_bwd`` the backward pass (gradients of a loss given dL/do and
-dL/dS_T). Both call the C ABI of ``include/kla.h`` through ctypes; torch
-only supplies device memory and the current CUDA stream. Every step of the
-computation runs in this package's CUDA kernels; if the library is missing the
-calls raise.
+dL/dS_T). ``layer`` has what a layer and a decoding loop need next to them: linear
+attention with one decay per head, layer norm, beam search. All call the C ABI of
+``include/kla.h`` and ``include/kla_layer.h`` through ctypes; torch only supplies device
+memory and the current CUDA stream. Every step of the computation runs in this
+package's CUDA kernels; if the library is missing the calls raise.
 """
 from __future__ import annotations
 
@@ -25,9 +26,12 @@ import torch
 
 from . import _native
 from ._native import KlaError  # noqa: F401
+from .layer import (beam_select, layer_norm_bwd, layer_norm_fwd, linear_bwd, linear_fwd, linear_step,  # noqa: F401
+                    linear_workspace_size, reorder_states)
 
 __all__ = ["chunk_fwd", "chunk_fwd_host", "chunk_bwd", "decode_step", "workspace_size", "bwd_workspace_size",
-           "device_status", "KlaError"]
+           "device_status", "KlaError", "linear_fwd", "linear_bwd", "linear_step", "linear_workspace_size",
+           "layer_norm_fwd", "layer_norm_bwd", "beam_select", "reorder_states"]
 
 
 def _dtype_code(t: torch.Tensor) -> int:

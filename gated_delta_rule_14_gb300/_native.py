@@ -65,6 +65,23 @@ def _declare(lib):
     lib.kla_chunk_bwd_workspace_size.restype = sz
     lib.kla_chunk_bwd_workspace_size_ex.argtypes = [i, i, i, i, i, i, i]
     lib.kla_chunk_bwd_workspace_size_ex.restype = sz
+    i64, f = ctypes.c_int64, ctypes.c_float
+    lib.kla_linear_fwd.argtypes = [vp, vp, vp, vp, fp, vp, fp, vp, fp, i, i, i, i, i, i, f, vp, sz, vp]
+    lib.kla_linear_fwd_workspace_size.argtypes = [i, i, i, i, i, i]
+    lib.kla_linear_bwd.argtypes = [vp, vp, vp, vp, vp, fp, vp, fp, fp, vp, vp, vp, fp, i, i, i, i, i, i, f, vp, sz, vp]
+    lib.kla_linear_bwd_workspace_size.argtypes = [i, i, i, i, i, i]
+    lib.kla_linear_step.argtypes = [vp, vp, vp, fp, vp, fp, fp, vp, i, i, i, i, i, i, f, vp]
+    lib.kla_layer_norm_fwd.argtypes = [vp, fp, fp, vp, fp, fp, i64, i, i, i, f, vp]
+    lib.kla_layer_norm_bwd.argtypes = [vp, vp, fp, fp, fp, vp, fp, fp, i64, i, i, i, vp, sz, vp]
+    lib.kla_layer_norm_bwd_workspace_size.argtypes = [i64, i, i, i]
+    lib.kla_beam_select.argtypes = [vp, i64, fp, vp, i, fp, vp, vp, vp, i, i, i, i, vp, sz, vp]
+    lib.kla_beam_select_workspace_size.argtypes = [i, i, i, i]
+    lib.kla_reorder_states.argtypes = [vp, vp, vp, i, i, sz, vp]
+    for name in ("linear_fwd", "linear_bwd", "linear_step", "layer_norm_fwd", "layer_norm_bwd", "beam_select",
+                 "reorder_states"):
+        getattr(lib, "kla_" + name).restype = ctypes.c_int
+    for name in ("linear_fwd", "linear_bwd", "layer_norm_bwd", "beam_select"):
+        getattr(lib, f"kla_{name}_workspace_size").restype = sz
     lib.kla_selftest_wait_timeout.argtypes = [ctypes.c_uint, vp]
     lib.kla_selftest_wait_timeout.restype = ctypes.c_int
     lib.kla_device_status.argtypes = [vp]

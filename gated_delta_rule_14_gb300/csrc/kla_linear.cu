@@ -1,0 +1,484 @@
+// kla_linear.cu -- linear attention with one decay per head: the C entry points, the fp32 scan for
+// every size, type and stride, and the single-token step.
+//
+// The recurrence S_t = g S_{t-1} + k_t v_t^T needs no solve: a chunk's own contribution to the
+// state and its products among its own tokens do not depend on the state that enters it, so chunks
+// only meet in S' = g^n S + Z. Long sequences with few heads are therefore cut into segments: one
+// launch takes each segment's own Z from a zero state, an elementwise pass turns the Z into start
+// states, and the second launch writes the outputs. All powers of g have exponents >= 0.
+#include <climits>
+
+#include "kla_linear.cuh"
+
+namespace kla {
+
+namespace {
+
+constexpr int kC = 32;        // tokens per chunk
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ size_t s_index(const LinScan &p, int chain, int d, int z) {
+    return static_cast<size_t>(chain) * p.dx * p.dz +
+           (p.s_t ? static_cast<size_t>(z) * p.dx + d : static_cast<size_t>(d) * p.dz + z);
+}
+
+// fp32 scan of one segment of one (sequence, head) and kZ value channels: chunk by chunk, all
+// operands in shared memory as fp32. `states`: only the segment's own contribution, from zero.
+template <typename T, int kZ>
+__global__ void __launch_bounds__(kThreads) lin_scan_kernel(const LinScan p, const int states) {
+    extern __shared__ float sm[];
+    const int ld = p.dx + 1;
+    float *X = sm, *Y = X + kC * ld, *Z = Y + kC * ld, *P = Z + kC * (kZ + 1), *S = P + kC * (kC + 1);
+    float *gp = S + p.dx * (kZ + 1);   // g^0 .. g^kC
+    const int tid = threadIdx.x, nz = p.dz / kZ;
+    const int chain = blockIdx.x / nz, z0 = (blockIdx.x % nz) * kZ, seg = blockIdx.y;
+    const int b = chain / p.H, h = chain % p.H;
+    const int n = lin_length(p.lengths, b, p.T);
+    int t_begin;
+    const int valid = lin_segment(p, seg, n, t_begin);
+    const int t_stop = min(p.T, t_begin + p.seg_len);   // outputs past `valid` are zeros
+    const float g = p.decay[h];
+    if (tid <= kC) gp[tid] = powf(g, static_cast<float>(tid));
+
+    for (int i = tid; i < p.dx * kZ; i += kThreads) {
+        const int d = i / kZ, z = i % kZ;
+        float s = 0.f;
+        if (!states) {
+            if (seg > 0)
+                s = p.seg_states[((static_cast<size_t>(chain) * (p.nseg - 1) + seg - 1) * p.dx + d) * p.dz + z0 + z];
+            else if (p.S0)
+                s = p.S0[s_index(p, chain, d, z0 + z)];
+        }
+        S[d * (kZ + 1) + z] = s;
+    }
+    const T *xg = static_cast<const T *>(p.x) + b * p.xs[0] + h * p.xs[2];
+    const T *yg = static_cast<const T *>(p.y) + b * p.ys[0] + h * p.ys[2];
+    const T *zg = static_cast<const T *>(p.z) + b * p.zs[0] + h * p.zs[2] + z0;
+    T *og = static_cast<T *>(p.out);
+
+    const int nchunk = (t_stop - t_begin + kC - 1) / kC;
+    for (int ci = 0; ci < nchunk; ++ci) {
+        const int c = p.reverse ? nchunk - 1 - ci : ci;
+        const int t0 = t_begin + c * kC;
+        const int cnt = max(0, min(kC, t_begin + valid - t0));   // valid tokens of the chunk
+        if (states && cnt == 0) continue;
+        __syncthreads();
+        for (int i = tid; i < kC * p.dx; i += kThreads) {   // masked tokens are read as zeros
+            const int r = i / p.dx, d = i % p.dx;
+            const bool ok = r < cnt;
+            if (!states) X[r * ld + d] = ok ? to_f32(xg[(t0 + r) * p.xs[1] + d]) : 0.f;
+            Y[r * ld + d] = ok ? to_f32(yg[(t0 + r) * p.ys[1] + d]) : 0.f;
+        }
+        for (int i = tid; i < kC * kZ; i += kThreads) {
+            const int r = i / kZ, z = i % kZ;
+            Z[r * (kZ + 1) + z] = r < cnt ? to_f32(zg[(t0 + r) * p.zs[1] + z]) : 0.f;
+        }
+        __syncthreads();
+        if (!states) {
+            const int i = tid / 8;
+            {   // P: four columns a thread
+                float a[4] = {0.f, 0.f, 0.f, 0.f};
+                const int j0 = tid % 8;
+                for (int d = 0; d < p.dx; ++d) {
+                    const float x = X[i * ld + d];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) a[u] = fmaf(x, Y[(j0 + 8 * u) * ld + d], a[u]);
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int dist = p.reverse ? j0 + 8 * u - i : i - j0 - 8 * u;
+                    P[i * (kC + 1) + j0 + 8 * u] = dist >= 0 ? p.a_intra * gp[dist] * a[u] : 0.f;
+                }
+            }
+            __syncthreads();
+            constexpr int kU = kZ / 8;
+            float o[kU] = {}, e[kU] = {};
+            const int c0 = tid % 8;
+            for (int j = 0; j < kC; ++j) {
+                const float w = P[i * (kC + 1) + j];
+#pragma unroll
+                for (int u = 0; u < kU; ++u) o[u] = fmaf(w, Z[j * (kZ + 1) + c0 + 8 * u], o[u]);
+            }
+            for (int d = 0; d < p.dx; ++d) {
+                const float x = X[i * ld + d];
+#pragma unroll
+                for (int u = 0; u < kU; ++u) e[u] = fmaf(x, S[d * (kZ + 1) + c0 + 8 * u], e[u]);
+            }
+            if (t0 + i < t_stop) {
+                const float w = i < cnt ? p.a_inter * gp[p.reverse ? cnt - 1 - i : i + 1] : 0.f;
+                T *dst = og + ((static_cast<size_t>(b) * p.T + t0 + i) * p.H + h) * p.dz + z0;
+#pragma unroll
+                for (int u = 0; u < kU; ++u)
+                    dst[c0 + 8 * u] = from_f32<T>(i < cnt ? fmaf(w, e[u], o[u]) : 0.f);
+            }
+            __syncthreads();
+        }
+        if (cnt > 0) {
+            for (int j = tid; j < kC * kZ; j += kThreads) {   // weights of the update, on the values
+                const int r = j / kZ;
+                const float w = r < cnt ? p.a_upd * gp[p.reverse ? r + 1 : cnt - 1 - r] : 0.f;
+                Z[r * (kZ + 1) + j % kZ] *= w;
+            }
+            __syncthreads();
+            const float gn = gp[cnt];
+            for (int i = tid; i < p.dx * kZ; i += kThreads) {
+                const int d = i / kZ, z = i % kZ;
+                float s = gn * S[d * (kZ + 1) + z];
+                for (int j = 0; j < kC; ++j) s = fmaf(Y[j * ld + d], Z[j * (kZ + 1) + z], s);
+                S[d * (kZ + 1) + z] = s;
+            }
+        }
+    }
+    __syncthreads();
+    if (!states && !(p.ST && seg == p.nseg - 1)) return;
+    for (int i = tid; i < p.dx * kZ; i += kThreads) {
+        const int d = i / kZ, z = i % kZ;
+        const float s = S[d * (kZ + 1) + z];
+        if (states)
+            p.seg_states[((static_cast<size_t>(chain) * (p.nseg - 1) + seg) * p.dx + d) * p.dz + z0 + z] = s;
+        else
+            p.ST[s_index(p, chain, d, z0 + z)] = s;
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) lin_combine_kernel(const LinScan p) {
+    const int chain = blockIdx.x, b = chain / p.H, h = chain % p.H;
+    const int i = blockIdx.y * kThreads + threadIdx.x, elems = p.dx * p.dz;
+    if (i >= elems) return;
+    const int n = lin_length(p.lengths, b, p.T);
+    const float g = p.decay[h];
+    float s = p.S0 ? p.S0[s_index(p, chain, i / p.dz, i % p.dz)] : 0.f;
+    float *slot = p.seg_states + static_cast<size_t>(chain) * (p.nseg - 1) * elems + i;
+    for (int k = 0; k < p.nseg - 1; ++k) {
+        int t0;
+        const int m = lin_segment(p, k, n, t0);
+        s = fmaf(powf(g, static_cast<float>(m)), s, slot[static_cast<size_t>(k) * elems]);
+        slot[static_cast<size_t>(k) * elems] = s;
+    }
+}
+
+template <typename T, int kZ>
+cudaError_t launch_scan_as(const LinScan &p, cudaStream_t stream) {
+    const int bytes = (2 * kC * (p.dx + 1) + kC * (kZ + 1) + kC * (kC + 1) + p.dx * (kZ + 1) + kC + 1) * 4;
+    auto kern = lin_scan_kernel<T, kZ>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    const int ctas = p.B * p.H * (p.dz / kZ);
+    if (p.nseg > 1) {
+        kern<<<dim3(ctas, p.nseg - 1), kThreads, bytes, stream>>>(p, 1);
+        if ((e = cudaGetLastError()) != cudaSuccess || (e = launch_lin_combine(p, stream)) != cudaSuccess) return e;
+    }
+    kern<<<dim3(ctas, p.nseg), kThreads, bytes, stream>>>(p, 0);
+    return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------------------- single-token step
+// One CTA per (sequence, head) and kZ value channels: every state element is read once, decayed,
+// written to and reduced against the query on the way out.
+template <typename T, int kZ>
+__global__ void __launch_bounds__(kThreads) lin_step_kernel(const T *q, const T *k, const T *v, const float *decay,
+                                                            const int *parent, const float *S, float *S_out, T *o,
+                                                            int H, int dk, int dv, int n_states, float q_scale) {
+    constexpr int kVec = kZ / 4, kRows = kThreads / kVec;   // float4 of a row, rows in flight
+    __shared__ float qs[128], ks[128], part[kThreads / 32][kZ];
+    const int tid = threadIdx.x, nz = dv / kZ;
+    const int bh = blockIdx.x / nz, z0 = (blockIdx.x % nz) * kZ;
+    const int b = bh / H, h = bh % H;
+    const int from = parent ? parent[b] : b;
+    const bool live = from >= 0 && from < n_states;
+    const int c = tid % kVec, r = tid / kVec;
+    const float *src = S + ((static_cast<size_t>(live ? from : 0) * H + h) * dk) * dv + z0 + 4 * c;
+    float *dst = S_out + (static_cast<size_t>(bh) * dk) * dv + z0 + 4 * c;
+    constexpr int kMost = 128 / kRows > 0 ? 128 / kRows : 1;
+    float4 s[kMost];
+#pragma unroll
+    for (int u = 0; u < kMost; ++u) {
+        const int d = r + u * kRows;
+        s[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (d < dk && live) s[u] = *reinterpret_cast<const float4 *>(src + static_cast<size_t>(d) * dv);
+    }
+    for (int d = tid; d < dk; d += kThreads) {
+        qs[d] = to_f32(q[static_cast<size_t>(bh) * dk + d]) * q_scale;
+        ks[d] = to_f32(k[static_cast<size_t>(bh) * dk + d]);
+    }
+    const float g = decay[h];
+    float vv[4], acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int u = 0; u < 4; ++u) vv[u] = to_f32(v[static_cast<size_t>(bh) * dv + z0 + 4 * c + u]);
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kMost; ++u) {
+        const int d = r + u * kRows;
+        if (d < dk) {
+            const float kd = ks[d], qd = qs[d];
+            s[u].x = fmaf(kd, vv[0], g * s[u].x);
+            s[u].y = fmaf(kd, vv[1], g * s[u].y);
+            s[u].z = fmaf(kd, vv[2], g * s[u].z);
+            s[u].w = fmaf(kd, vv[3], g * s[u].w);
+            *reinterpret_cast<float4 *>(dst + static_cast<size_t>(d) * dv) = s[u];
+            acc[0] = fmaf(qd, s[u].x, acc[0]);
+            acc[1] = fmaf(qd, s[u].y, acc[1]);
+            acc[2] = fmaf(qd, s[u].z, acc[2]);
+            acc[3] = fmaf(qd, s[u].w, acc[3]);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int off = kVec; off < 32; off <<= 1) acc[u] += __shfl_xor_sync(0xffffffffu, acc[u], off);
+    if ((tid & 31) < kVec)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) part[tid / 32][4 * c + u] = acc[u];
+    __syncthreads();
+    if (tid < kZ) {
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) sum += part[w][tid];
+        o[static_cast<size_t>(bh) * dv + z0 + tid] = from_f32<T>(sum);
+    }
+}
+
+template <typename T>
+cudaError_t launch_step(const void *q, const void *k, const void *v, const float *decay, const int *parent,
+                        const float *S, float *S_out, void *o, int B, int H, int dk, int dv, int n_states,
+                        float q_scale, cudaStream_t stream) {
+    const T *qq = static_cast<const T *>(q), *kk = static_cast<const T *>(k), *vv = static_cast<const T *>(v);
+    if (dv % 32 == 0)
+        lin_step_kernel<T, 32><<<B * H * (dv / 32), kThreads, 0, stream>>>(
+            qq, kk, vv, decay, parent, S, S_out, static_cast<T *>(o), H, dk, dv, n_states, q_scale);
+    else
+        lin_step_kernel<T, 16><<<B * H * (dv / 16), kThreads, 0, stream>>>(
+            qq, kk, vv, decay, parent, S, S_out, static_cast<T *>(o), H, dk, dv, n_states, q_scale);
+    return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------------------------ host side
+bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+bool supported_d(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
+bool finite(float x) { return x - x == 0.0f; }
+
+struct Span {
+    uintptr_t lo, hi;
+};
+Span span(const void *p, size_t bytes) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    return {a, p ? a + bytes : a};
+}
+bool overlaps(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi; }
+// The bytes that a strided [B, T, H, d] tensor reaches over.
+Span reach(const void *p, const int64_t *st, int B, int T, int H, int d, size_t esz) {
+    if (B < 1 || T < 1 || H < 1) return span(p, 0);
+    return span(p, (static_cast<size_t>(B - 1) * st[0] + static_cast<size_t>(T - 1) * st[1] +
+                    static_cast<size_t>(H - 1) * st[2] + d) * esz);
+}
+
+// Segments of the fp32 scan: enough CTAs for every SM twice, each with four chunks or more.
+void plan(LinScan &p, int chunk, int ctas_per_chain, int want, int least) {
+    const int nchunk = (p.T + chunk - 1) / chunk;
+    const long ctas = static_cast<long>(p.B) * p.H * ctas_per_chain;
+    long n = ctas >= want ? 1 : want / ctas;
+    if (n > nchunk / least) n = nchunk / least;
+    if (n < 1) n = 1;
+    const int len = static_cast<int>((nchunk + n - 1) / n);
+    p.seg_len = (len > 0 ? len : 1) * chunk;
+    p.nseg = nchunk > 0 ? (nchunk + len - 1) / len : 1;
+}
+
+constexpr int kSms = 152;
+
+size_t seg_bytes(const LinScan &p) {
+    return static_cast<size_t>(p.B) * p.H * (p.nseg - 1) * p.dx * p.dz * sizeof(float);
+}
+
+void plan_scan(LinScan &p) { plan(p, kC, p.dz / (p.dz < 32 ? 16 : 32), 2 * kSms, 4); }
+
+void set_strides(int64_t (&to)[3], const int64_t *from, int T, int H, int d) {
+    to[0] = from ? from[0] : static_cast<int64_t>(T) * H * d;
+    to[1] = from ? from[1] : static_cast<int64_t>(H) * d;
+    to[2] = from ? from[2] : d;
+}
+
+// Sizes, type and scale common to both directions; `ntens` strided tensors.
+kla_status check_sizes(int B, int T, int H, int d_k, int d_v, kla_dtype dtype, float q_scale, const int64_t *strides,
+                       int ntens) {
+    if (B < 1 || T < 0 || H < 1 || d_k < 1 || d_v < 1) return KLA_ERR_INVALID_ARG;
+    if (dtype != KLA_DTYPE_F32 && dtype != KLA_DTYPE_BF16) return KLA_ERR_INVALID_ARG;
+    if (!finite(q_scale)) return KLA_ERR_INVALID_ARG;
+    for (int i = 0; strides && i < 3 * ntens; ++i)
+        if (strides[i] < 0) return KLA_ERR_INVALID_ARG;
+    if (!supported_d(d_k) || !supported_d(d_v)) return KLA_ERR_UNSUPPORTED;
+    // chains times value tiles index the grid
+    if (static_cast<int64_t>(B) * H * 8 > INT_MAX) return KLA_ERR_UNSUPPORTED;
+    return KLA_OK;
+}
+
+}  // namespace
+
+cudaError_t launch_lin_combine(const LinScan &p, cudaStream_t stream) {
+    lin_combine_kernel<<<dim3(p.B * p.H, (p.dx * p.dz + kThreads - 1) / kThreads), kThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_lin_scan(const LinScan &p, kla_dtype dtype, cudaStream_t stream) {
+    if (dtype == KLA_DTYPE_BF16)
+        return p.dz < 32 ? launch_scan_as<__nv_bfloat16, 16>(p, stream) : launch_scan_as<__nv_bfloat16, 32>(p, stream);
+    return p.dz < 32 ? launch_scan_as<float, 16>(p, stream) : launch_scan_as<float, 32>(p, stream);
+}
+
+}  // namespace kla
+
+using kla::LinScan;
+
+extern "C" {
+
+size_t kla_linear_fwd_workspace_size(int B, int T, int H, int d_k, int d_v, kla_dtype dtype) {
+    if (B < 1 || T < 1 || H < 1 || !kla::supported_d(d_k) || !kla::supported_d(d_v)) return 0;
+    LinScan p{};
+    p.B = B; p.T = T; p.H = H; p.dx = d_k; p.dz = d_v;
+    kla::plan_scan(p);
+    return kla::seg_bytes(p);
+}
+
+size_t kla_linear_bwd_workspace_size(int B, int T, int H, int d_k, int d_v, kla_dtype dtype) {
+    const size_t a = kla_linear_fwd_workspace_size(B, T, H, d_k, d_v, dtype);
+    const size_t b = kla_linear_fwd_workspace_size(B, T, H, d_v, d_k, dtype);
+    return a > b ? a : b;
+}
+
+kla_status kla_linear_fwd(const void *q, const void *k, const void *v, const int64_t *strides, const float *decay,
+                          const int *lengths, const float *S0, void *o, float *S_T, int B, int T, int H, int d_k,
+                          int d_v, kla_dtype dtype, float q_scale, void *workspace, size_t workspace_bytes,
+                          void *stream) {
+    using namespace kla;
+    kla_status st = check_sizes(B, T, H, d_k, d_v, dtype, q_scale, strides, 3);
+    if (st != KLA_OK) return st;
+    if (!decay || (T > 0 && (!q || !k || !v || !o))) return KLA_ERR_INVALID_ARG;
+    const size_t esz = dtype == KLA_DTYPE_BF16 ? 2 : 4;
+    if (!aligned(q, esz) || !aligned(k, esz) || !aligned(v, esz) || !aligned(o, esz) || !aligned(decay, 4) ||
+        !aligned(lengths, 4) || !aligned(S0, 16) || !aligned(S_T, 16) || !aligned(workspace, 16))
+        return KLA_ERR_INVALID_ARG;
+    const size_t need = kla_linear_fwd_workspace_size(B, T, H, d_k, d_v, dtype);
+    if (workspace_bytes < need || (need > 0 && !workspace)) return KLA_ERR_INVALID_ARG;
+    LinScan p{};
+    p.x = q; p.y = k; p.z = v;
+    set_strides(p.xs, strides, T, H, d_k);
+    set_strides(p.ys, strides ? strides + 3 : nullptr, T, H, d_k);
+    set_strides(p.zs, strides ? strides + 6 : nullptr, T, H, d_v);
+    const size_t sbytes = static_cast<size_t>(B) * H * d_k * d_v * 4;
+    const size_t obytes = static_cast<size_t>(B) * T * H * d_v * esz;
+    const Span outs[] = {span(o, obytes), span(S_T, sbytes), span(workspace, need)};
+    const Span ins[] = {reach(q, p.xs, B, T, H, d_k, esz), reach(k, p.ys, B, T, H, d_k, esz),
+                        reach(v, p.zs, B, T, H, d_v, esz), span(decay, 4ull * H), span(lengths, 4ull * B),
+                        span(S0, sbytes)};
+    for (int i = 0; i < 3; ++i) {
+        for (int j = 0; j < 6; ++j)
+            if (overlaps(outs[i], ins[j]) && !(i == 1 && j == 5 && S0 == S_T)) return KLA_ERR_INVALID_ARG;
+        for (int j = i + 1; j < 3; ++j)
+            if (overlaps(outs[i], outs[j])) return KLA_ERR_INVALID_ARG;
+    }
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (T == 0) {   // no tokens: the final state is the initial one
+        if (!S_T || S_T == S0) return KLA_OK;
+        const cudaError_t e = S0 ? cudaMemcpyAsync(S_T, S0, sbytes, cudaMemcpyDeviceToDevice, cs)
+                                 : cudaMemsetAsync(S_T, 0, sbytes, cs);
+        return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+    }
+    p.out = o; p.decay = decay; p.lengths = lengths; p.S0 = S0; p.ST = S_T;
+    p.B = B; p.T = T; p.H = H; p.dx = d_k; p.dz = d_v;
+    p.a_intra = p.a_inter = q_scale;
+    p.a_upd = 1.0f;
+    p.seg_states = static_cast<float *>(workspace);
+    plan_scan(p);
+    return launch_lin_scan(p, dtype, cs) == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+}
+
+kla_status kla_linear_bwd(const void *q, const void *k, const void *v, const void *dO, const int64_t *strides,
+                          const float *decay, const int *lengths, const float *S0, const float *dS_T, void *dq,
+                          void *dk, void *dv, float *dS0, int B, int T, int H, int d_k, int d_v, kla_dtype dtype,
+                          float q_scale, void *workspace, size_t workspace_bytes, void *stream) {
+    using namespace kla;
+    kla_status st = check_sizes(B, T, H, d_k, d_v, dtype, q_scale, strides, 4);
+    if (st != KLA_OK) return st;
+    if (!decay || (T > 0 && (!q || !k || !v || !dO || !dq || !dk || !dv))) return KLA_ERR_INVALID_ARG;
+    const size_t esz = dtype == KLA_DTYPE_BF16 ? 2 : 4;
+    if (!aligned(q, esz) || !aligned(k, esz) || !aligned(v, esz) || !aligned(dO, esz) || !aligned(dq, esz) ||
+        !aligned(dk, esz) || !aligned(dv, esz) || !aligned(decay, 4) || !aligned(lengths, 4) || !aligned(S0, 16) ||
+        !aligned(dS_T, 16) || !aligned(dS0, 16) || !aligned(workspace, 16))
+        return KLA_ERR_INVALID_ARG;
+    const size_t need = kla_linear_bwd_workspace_size(B, T, H, d_k, d_v, dtype);
+    if (workspace_bytes < need || (need > 0 && !workspace)) return KLA_ERR_INVALID_ARG;
+    int64_t qs[3], ks[3], vs[3], os[3];
+    set_strides(qs, strides, T, H, d_k);
+    set_strides(ks, strides ? strides + 3 : nullptr, T, H, d_k);
+    set_strides(vs, strides ? strides + 6 : nullptr, T, H, d_v);
+    set_strides(os, strides ? strides + 9 : nullptr, T, H, d_v);
+    const size_t sbytes = static_cast<size_t>(B) * H * d_k * d_v * 4;
+    const size_t n = static_cast<size_t>(B) * T * H;
+    const Span outs[] = {span(dq, n * d_k * esz), span(dk, n * d_k * esz), span(dv, n * d_v * esz), span(dS0, sbytes),
+                         span(workspace, need)};
+    const Span ins[] = {reach(q, qs, B, T, H, d_k, esz), reach(k, ks, B, T, H, d_k, esz),
+                        reach(v, vs, B, T, H, d_v, esz), reach(dO, os, B, T, H, d_v, esz), span(decay, 4ull * H),
+                        span(lengths, 4ull * B), span(S0, sbytes), span(dS_T, sbytes)};
+    for (int i = 0; i < 5; ++i) {
+        for (const Span &x : ins)
+            if (overlaps(outs[i], x)) return KLA_ERR_INVALID_ARG;
+        for (int j = i + 1; j < 5; ++j)
+            if (overlaps(outs[i], outs[j])) return KLA_ERR_INVALID_ARG;
+    }
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (T == 0) {   // no tokens: dL/dS0 = dL/dS_T
+        if (!dS0) return KLA_OK;
+        const cudaError_t e = dS_T ? cudaMemcpyAsync(dS0, dS_T, sbytes, cudaMemcpyDeviceToDevice, cs)
+                                   : cudaMemsetAsync(dS0, 0, sbytes, cs);
+        return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+    }
+    auto scan = [&](const void *x, const int64_t *xs, const void *y, const int64_t *ys, const void *z,
+                    const int64_t *zs, void *out, const float *s0, float *sT, int s_t, int dx, int dz, int reverse) {
+        LinScan p{};
+        p.x = x; p.y = y; p.z = z;
+        for (int i = 0; i < 3; ++i) { p.xs[i] = xs[i]; p.ys[i] = ys[i]; p.zs[i] = zs[i]; }
+        p.out = out; p.decay = decay; p.lengths = lengths; p.S0 = s0; p.ST = sT; p.s_t = s_t;
+        p.B = B; p.T = T; p.H = H; p.dx = dx; p.dz = dz; p.reverse = reverse;
+        p.a_intra = q_scale;
+        p.a_inter = reverse ? 1.0f : q_scale;
+        p.a_upd = reverse ? q_scale : 1.0f;
+        p.seg_states = static_cast<float *>(workspace);
+        plan_scan(p);
+        return launch_lin_scan(p, dtype, cs);
+    };
+    if (scan(dO, os, v, vs, k, ks, dq, S0, nullptr, 1, d_v, d_k, 0) != cudaSuccess ||
+        scan(v, vs, dO, os, q, qs, dk, dS_T, nullptr, 1, d_v, d_k, 1) != cudaSuccess ||
+        scan(k, ks, q, qs, dO, os, dv, dS_T, dS0, 0, d_k, d_v, 1) != cudaSuccess)
+        return KLA_ERR_CUDA;
+    return KLA_OK;
+}
+
+kla_status kla_linear_step(const void *q, const void *k, const void *v, const float *decay, const int *parent,
+                           const float *S, float *S_out, void *o, int B, int H, int d_k, int d_v, int n_states,
+                           kla_dtype dtype, float q_scale, void *stream) {
+    using namespace kla;
+    kla_status st = check_sizes(B, 1, H, d_k, d_v, dtype, q_scale, nullptr, 0);
+    if (st != KLA_OK) return st;
+    if (!q || !k || !v || !decay || !S || !S_out || !o || n_states < 1 || (!parent && n_states != B))
+        return KLA_ERR_INVALID_ARG;
+    const size_t esz = dtype == KLA_DTYPE_BF16 ? 2 : 4;
+    if (!aligned(q, esz) || !aligned(k, esz) || !aligned(v, esz) || !aligned(o, esz) || !aligned(decay, 4) ||
+        !aligned(parent, 4) || !aligned(S, 16) || !aligned(S_out, 16))
+        return KLA_ERR_INVALID_ARG;
+    const size_t nh = static_cast<size_t>(B) * H, one = static_cast<size_t>(H) * d_k * d_v * 4;
+    const Span outs[] = {span(S_out, B * one), span(o, nh * d_v * esz)};
+    const Span ins[] = {span(S, n_states * one), span(q, nh * d_k * esz), span(k, nh * d_k * esz),
+                        span(v, nh * d_v * esz), span(decay, 4ull * H), span(parent, 4ull * B)};
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 6; ++j)
+            if (overlaps(outs[i], ins[j]) && !(i == 0 && j == 0 && !parent && S == S_out)) return KLA_ERR_INVALID_ARG;
+    if (overlaps(outs[0], outs[1])) return KLA_ERR_INVALID_ARG;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const cudaError_t e =
+        dtype == KLA_DTYPE_BF16
+            ? launch_step<__nv_bfloat16>(q, k, v, decay, parent, S, S_out, o, B, H, d_k, d_v, n_states, q_scale, cs)
+            : launch_step<float>(q, k, v, decay, parent, S, S_out, o, B, H, d_k, d_v, n_states, q_scale, cs);
+    return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+}
+
+}  // extern "C"

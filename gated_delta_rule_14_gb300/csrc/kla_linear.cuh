@@ -1,0 +1,56 @@
+// kla_linear.cuh -- the scan that every direction of the decayed linear attention is made of.
+//
+// With roles x (query), y (key), z (value) and a state S (dx x dz) the scan computes, along time,
+//     out_i = sum_{j <= i} a_intra g^{i-j} (x_i.y_j) z_j + a_inter g^{i+1} S0^T x_i
+//     S_end = g^n S0 + a_upd sum_j g^{n-1-j} y_j z_j^T
+// and against time (j >= i, g^{j-i}; the entering state undecayed at the last token: g^{n-1-i} in
+// the read, g^{j+1} in the update, so that S_end is the gradient of the state before the first
+// token). The four directions, with s the query scale:
+//     o  = scan(q, k, v, S0)            intra s, inter s, update 1        S_end = S_T
+//     dq = scan(dO, v, k, S0^T)         intra s, inter s, update 1
+//     dk = back(v, dO, q, dS_T^T)       intra s, inter 1, update s
+//     dv = back(k, q, dO, dS_T)         intra s, inter 1, update s        S_end = dS0
+#pragma once
+
+#include "kla_internal.cuh"
+#include "../../include/kla_layer.h"
+
+namespace kla {
+
+struct LinScan {
+    const void *x, *y, *z;
+    int64_t xs[3], ys[3], zs[3];   // element strides of batch, token, head
+    void *out;                     // [B, T, H, dz] contiguous, the inputs' dtype
+    const float *decay;
+    const int *lengths;            // or NULL
+    const float *S0;               // or NULL (zeros)
+    float *ST;                     // or NULL
+    int s_t;                       // 1: S0 and ST are stored [dz][dx]
+    int B, T, H, dx, dz;
+    int reverse;
+    float a_intra, a_inter, a_upd;
+    float *seg_states;             // [chains][nseg - 1][dx][dz] scratch
+    int nseg, seg_len;             // segments in processing order, tokens each
+};
+
+// Valid tokens of sequence b.
+__device__ __forceinline__ int lin_length(const int *lengths, int b, int T) {
+    if (!lengths) return T;
+    const int n = lengths[b];
+    return n < 0 ? 0 : n < T ? n : T;
+}
+// Valid tokens of the segment that is s-th in processing order, and its first token.
+__device__ __forceinline__ int lin_segment(const LinScan &p, int s, int n, int &t0) {
+    const int at = p.reverse ? p.nseg - 1 - s : s;
+    t0 = at * p.seg_len;
+    const int left = n - t0;
+    return left < 0 ? 0 : left < p.seg_len ? left : p.seg_len;
+}
+
+// The start states of the segments: slot s holds segment s's own contribution and is turned into
+// the state after segment s.
+cudaError_t launch_lin_combine(const LinScan &p, cudaStream_t stream);
+// Any size, type, stride and alignment, fp32 arithmetic (kla_linear.cu).
+cudaError_t launch_lin_scan(const LinScan &p, kla_dtype dtype, cudaStream_t stream);
+
+}  // namespace kla
