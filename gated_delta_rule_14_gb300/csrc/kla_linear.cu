@@ -292,6 +292,18 @@ size_t seg_bytes(const LinScan &p) {
 
 void plan_scan(LinScan &p) { plan(p, kC, p.dz / (p.dz < 32 ? 16 : 32), 2 * kSms, 4); }
 
+// Scratch of `scans` scans of these sizes on whichever path they take (the tensor-core path depends on
+// alignment too): side by side on the tensor cores, one after the other in fp32.
+size_t scratch(LinScan p, kla_dtype dtype, int scans) {
+    plan_scan(p);
+    size_t most = seg_bytes(p);
+    if (dtype == KLA_DTYPE_BF16 && p.dx == 128 && p.dz == 128) {
+        lin_tc_plan(p, scans);
+        if (scans * seg_bytes(p) > most) most = scans * seg_bytes(p);
+    }
+    return most;
+}
+
 void set_strides(int64_t (&to)[3], const int64_t *from, int T, int H, int d) {
     to[0] = from ? from[0] : static_cast<int64_t>(T) * H * d;
     to[1] = from ? from[1] : static_cast<int64_t>(H) * d;
@@ -335,14 +347,18 @@ size_t kla_linear_fwd_workspace_size(int B, int T, int H, int d_k, int d_v, kla_
     if (B < 1 || T < 1 || H < 1 || !kla::supported_d(d_k) || !kla::supported_d(d_v)) return 0;
     LinScan p{};
     p.B = B; p.T = T; p.H = H; p.dx = d_k; p.dz = d_v;
-    kla::plan_scan(p);
-    return kla::seg_bytes(p);
+    return kla::scratch(p, dtype, 1);
 }
 
 size_t kla_linear_bwd_workspace_size(int B, int T, int H, int d_k, int d_v, kla_dtype dtype) {
-    const size_t a = kla_linear_fwd_workspace_size(B, T, H, d_k, d_v, dtype);
-    const size_t b = kla_linear_fwd_workspace_size(B, T, H, d_v, d_k, dtype);
-    return a > b ? a : b;
+    if (B < 1 || T < 1 || H < 1 || !kla::supported_d(d_k) || !kla::supported_d(d_v)) return 0;
+    LinScan p{}, q{};
+    p.B = q.B = B; p.T = q.T = T; p.H = q.H = H;
+    p.dx = q.dz = d_k;
+    p.dz = q.dx = d_v;
+    const size_t a = kla::scratch(p, dtype, 3), b = kla::scratch(q, dtype, 3);
+    const size_t fwd = kla::scratch(p, dtype, 1);   // one buffer serves both directions
+    return a > b ? (a > fwd ? a : fwd) : (b > fwd ? b : fwd);
 }
 
 kla_status kla_linear_fwd(const void *q, const void *k, const void *v, const int64_t *strides, const float *decay,
@@ -388,8 +404,15 @@ kla_status kla_linear_fwd(const void *q, const void *k, const void *v, const int
     p.a_intra = p.a_inter = q_scale;
     p.a_upd = 1.0f;
     p.seg_states = static_cast<float *>(workspace);
-    plan_scan(p);
-    return launch_lin_scan(p, dtype, cs) == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+    cudaError_t e;
+    if (lin_tc_supports(p, dtype)) {
+        lin_tc_plan(p, 1);
+        e = launch_lin_tc(&p, 1, cs);
+    } else {
+        plan_scan(p);
+        e = launch_lin_scan(p, dtype, cs);
+    }
+    return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
 }
 
 kla_status kla_linear_bwd(const void *q, const void *k, const void *v, const void *dO, const int64_t *strides,
@@ -432,7 +455,7 @@ kla_status kla_linear_bwd(const void *q, const void *k, const void *v, const voi
                                    : cudaMemsetAsync(dS0, 0, sbytes, cs);
         return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
     }
-    auto scan = [&](const void *x, const int64_t *xs, const void *y, const int64_t *ys, const void *z,
+    auto set = [&](const void *x, const int64_t *xs, const void *y, const int64_t *ys, const void *z,
                     const int64_t *zs, void *out, const float *s0, float *sT, int s_t, int dx, int dz, int reverse) {
         LinScan p{};
         p.x = x; p.y = y; p.z = z;
@@ -443,13 +466,22 @@ kla_status kla_linear_bwd(const void *q, const void *k, const void *v, const voi
         p.a_inter = reverse ? 1.0f : q_scale;
         p.a_upd = reverse ? q_scale : 1.0f;
         p.seg_states = static_cast<float *>(workspace);
-        plan_scan(p);
-        return launch_lin_scan(p, dtype, cs);
+        return p;
     };
-    if (scan(dO, os, v, vs, k, ks, dq, S0, nullptr, 1, d_v, d_k, 0) != cudaSuccess ||
-        scan(v, vs, dO, os, q, qs, dk, dS_T, nullptr, 1, d_v, d_k, 1) != cudaSuccess ||
-        scan(k, ks, q, qs, dO, os, dv, dS_T, dS0, 0, d_k, d_v, 1) != cudaSuccess)
-        return KLA_ERR_CUDA;
+    LinScan p[3] = {set(k, ks, q, qs, dO, os, dv, dS_T, dS0, 0, d_k, d_v, 1),
+                    set(v, vs, dO, os, q, qs, dk, dS_T, nullptr, 1, d_v, d_k, 1),
+                    set(dO, os, v, vs, k, ks, dq, S0, nullptr, 1, d_v, d_k, 0)};
+    if (lin_tc_supports(p[0], dtype) && lin_tc_supports(p[1], dtype) && lin_tc_supports(p[2], dtype)) {
+        for (int i = 0; i < 3; ++i) {
+            lin_tc_plan(p[i], 3);
+            p[i].seg_states += i * seg_bytes(p[i]) / sizeof(float);
+        }
+        return launch_lin_tc(p, 3, cs) == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+    }
+    for (int i = 0; i < 3; ++i) {
+        plan_scan(p[i]);
+        if (launch_lin_scan(p[i], dtype, cs) != cudaSuccess) return KLA_ERR_CUDA;
+    }
     return KLA_OK;
 }
 

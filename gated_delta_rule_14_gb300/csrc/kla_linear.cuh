@@ -50,6 +50,12 @@ __device__ __forceinline__ int lin_segment(const LinScan &p, int s, int n, int &
 // The start states of the segments: slot s holds segment s's own contribution and is turned into
 // the state after segment s.
 cudaError_t launch_lin_combine(const LinScan &p, cudaStream_t stream);
+// Tensor-core form: bf16, dx = dz = 128, rows that TMA can read (kla_linear_tc.cu). Runs up to three
+// scans of the same sizes side by side in one launch, each with segments (and a scratch) of its own.
+bool lin_tc_supports(const LinScan &p, kla_dtype dtype);
+void lin_tc_plan(LinScan &p, int scans);
+cudaError_t launch_lin_tc(const LinScan *p, int scans, cudaStream_t stream);
+cudaError_t device_error_word(unsigned **out);   // kla_api.cu
 // Any size, type, stride and alignment, fp32 arithmetic (kla_linear.cu).
 cudaError_t launch_lin_scan(const LinScan &p, kla_dtype dtype, cudaStream_t stream);
 
