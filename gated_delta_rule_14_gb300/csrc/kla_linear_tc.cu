@@ -15,15 +15,17 @@
 //   O   A = P (TMEM, over D)          B = Z (smem, MN-major)
 //   U   A = (diag(w) Y)^T (TMEM)      B = Z (smem, MN-major)
 // Operands that threads compute and that would be read from shared memory once per product sit in
-// TMEM instead: P replaces D column by column, and the weighted keys are written transposed.
+// TMEM instead: P replaces D column by column, and the weighted keys are written transposed. So does
+// the fp32 state: U accumulates onto g^n S in place.
 // (diag(w) Y)^T is kept as two bf16 terms (hi + lo, 2^-17 relative): the fp32 state is an output of
 // its own, and one term (2^-9) would be its error. S as an operand and P are rounded to one bf16
 // term: they only enter O, which is stored with 8 bits itself.
 //
-// Warps: 0-3 turn D into P; 4-7 scale the first half of O and write the outputs; 8-15 own S in fp32
-// registers (thread = one x channel, 64 z channels), weigh the keys and update S; 16 loads (TMA, two
-// stages of X, Y, Z tiles); 17 issues the products. They hand over through mbarriers that complete
-// once per chunk.
+// Warps: 0-7 turn D into P; 8-15 copy and decay the state, scale the first half of O and send the
+// outputs out through the X tile; 16-23 weigh the keys; 24 loads (TMA, two stages of X, Y, Z tiles);
+// 25 issues the products, in the order D, X S, U, P Z, which leaves P's conversion the time of X S
+// and U. They hand over through mbarriers that complete once per chunk. Eight warps per role: with
+// four, and keys and state on the same eight, the chain of conversions took 6900 cycles a chunk.
 #include <cuda.h>
 
 #include "kla_linear.cuh"
@@ -35,7 +37,7 @@ namespace {
 using namespace ptx;
 
 constexpr int kC = 128, kD = 128;
-constexpr int kThreads = 18 * 32;
+constexpr int kThreads = 26 * 32;
 constexpr uint32_t kWaitLimit = 100000;   // x 20 us: a stuck wait gives up after ~2 s
 constexpr uint32_t kTile = 32768, kHalf = 16384;   // a 128 x 128 bf16 tile: two blocks of 64 channels
 constexpr uint32_t OFF_STAGE = 0, STAGE = 3 * kTile;
@@ -49,22 +51,24 @@ constexpr uint32_t kBarKeys = 1;   // named barrier of warps 8-15
 struct Small {
     uint64_t full[2];   // X, Y, Z tiles landed, by stage
     uint64_t free[2];   // every product that reads the stage is done
+    uint64_t out[2];    // the outputs, which leave through the X tile, are out
     uint64_t end;       // after an abort: the products that were issued are done
     uint64_t d, p;      // D computed, P written
     uint64_t xs, sc;    // X S computed, scaled
     uint64_t o, ord;    // O computed, O read
-    uint64_t y, u, urd; // weighted keys written, U computed, U read
-    uint64_t s;         // operand copy of S written
+    uint64_t y, u;      // weighted keys written, U added
+    uint64_t s;         // operand copy of S written, S decayed
     uint32_t tmem_base;
     volatile int abort;
-    float gp[kC + 1];   // g^0 .. g^128
-    float gb[32];       // g of the distance within a 32-column block, from its near side
-    alignas(16) float w[kC];
+    float gp[kC + 1];              // g^0 .. g^128
+    float diag[64];                // a_intra g^distance at 32 + column - row of a diagonal 32 x 32 block, 0 off the mask
+    alignas(16) float near[32];    // g^distance of a block's columns from its side near the diagonal
+    alignas(16) uint2 w[kC / 2];   // weights of the keys, two tokens each: bf16 pairs of w and of what w lacks
 };
 static_assert(sizeof(Small) <= 2048, "small area");
 
 struct Job {
-    CUtensorMap x, y, z;
+    CUtensorMap x, y, z, o;
     LinScan p;
 };
 struct TcParams {
@@ -73,10 +77,20 @@ struct TcParams {
     unsigned *err;
 };
 
-__device__ __forceinline__ void st_global_v8(void *p, const uint32_t *r) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
-                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
+__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t addr) {
+    unsigned short v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
 }
 
 template <bool kStates>   // only the segment's own contribution to the state
@@ -101,30 +115,36 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     const bool want_s = kStates || (p.ST && seg == p.nseg - 1);
 
     const uint32_t b_full = smem_u32(&sm.full[0]), b_free = smem_u32(&sm.free[0]), b_end = smem_u32(&sm.end);
+    const uint32_t b_out = smem_u32(&sm.out[0]);
     const uint32_t b_d = smem_u32(&sm.d), b_p = smem_u32(&sm.p), b_xs = smem_u32(&sm.xs), b_sc = smem_u32(&sm.sc);
     const uint32_t b_o = smem_u32(&sm.o), b_ord = smem_u32(&sm.ord), b_y = smem_u32(&sm.y), b_u = smem_u32(&sm.u);
-    const uint32_t b_urd = smem_u32(&sm.urd), b_s = smem_u32(&sm.s);
+    const uint32_t b_s = smem_u32(&sm.s);
     if (tid == 0) {
         mbar_init(b_full, 1);
         mbar_init(b_full + 8, 1);
         mbar_init(b_free, 1);
         mbar_init(b_free + 8, 1);
         mbar_init(b_end, 1);
+        mbar_init(b_out, 8);
+        mbar_init(b_out + 8, 8);
         mbar_init(b_d, 1);
-        mbar_init(b_p, 4);
+        mbar_init(b_p, 8);
         mbar_init(b_xs, 1);
-        mbar_init(b_sc, 4);
+        mbar_init(b_sc, 8);
         mbar_init(b_o, 1);
-        mbar_init(b_ord, 4);
+        mbar_init(b_ord, 8);
         mbar_init(b_y, 8);
         mbar_init(b_u, 1);
-        mbar_init(b_urd, 8);
         mbar_init(b_s, 8);
         sm.abort = 0;
         fence_mbar_init();
     }
     if (tid <= kC) sm.gp[tid] = powf(g, static_cast<float>(tid));
-    if (warp == 5) sm.gb[lane] = powf(g, static_cast<float>(p.reverse ? lane : 31 - lane));
+    if (tid < 64) {
+        const int dist = p.reverse ? tid - 32 : 32 - tid;
+        sm.diag[tid] = dist >= 0 ? p.a_intra * powf(g, static_cast<float>(dist)) : 0.f;
+        if (tid < 32) sm.near[tid] = powf(g, static_cast<float>(p.reverse ? tid : 31 - tid));
+    }
     if (warp == 0) {
         tmem_alloc(smem_u32(&sm.tmem_base), 512);
         tmem_relinquish();
@@ -148,10 +168,45 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
     };
-    auto chunk_of = [&](int c) { return p.reverse ? nchunk - 1 - c : c; };
+    const bool back = p.reverse;
+    auto chunk_of = [&](int c) { return back ? nchunk - 1 - c : c; };
     auto count_of = [&](int c) { return min(kC, valid - chunk_of(c) * kC); };
 
-    if (warp == 16) {
+    // warps 8-15: O of chunk c leaves through the X tile, which its products have read; each warp's 32
+    // rows x 64 channels are one box, and rows past T are cut off by the tensor's bounds
+    auto put_out = [&](int c) {
+        const int half = (warp - 8) >> 2, cnt = count_of(c);
+        const uint32_t tile = sbase + OFF_STAGE + (c & 1) * STAGE + half * kHalf;
+        tc_fence_after();
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+            uint32_t r[32];
+            tmem_ld32(tlane + TM_O + 64 * half + 32 * k, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t pk[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    pk[u] = row < cnt ? pack_bf16(__uint_as_float(r[8 * i + 2 * u]), __uint_as_float(r[8 * i + 2 * u + 1]))
+                                      : 0u;
+                st_shared_v4(tile + sw128_off(row, 64 * k + 16 * i), pk[0], pk[1], pk[2], pk[3]);
+            }
+        }
+        tc_fence_before();
+        fence_proxy_async_smem();
+        arrive(b_ord);
+        if (lane == 0) {
+            const int t = t_begin + chunk_of(c) * kC + 32 * (warp & 3);
+            if (t < p.T) tma_store_4d(&job.o, tile + (warp & 3) * 4096, 64 * half, h, t, b);
+            tma_store_commit();
+            tma_store_wait_read_all();
+            mbar_arrive(b_out + 8 * (c & 1));
+        }
+        __syncwarp();
+    };
+
+    if (warp == 24) {
         // ---------------------------------------------------------------- loads
         int issued = 0, seen = 0;
         if (lane == 0) {
@@ -160,18 +215,20 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                 const uint32_t st = sbase + OFF_STAGE + (c & 1) * STAGE, bar = b_full + 8 * (c & 1);
                 const int t0 = t_begin + chunk_of(c) * kC;
                 mbar_arrive_expect_tx(bar, (kStates ? 2 : 3) * kTile);
-                for (int i = 0; i < 2; ++i) {
-                    if (!kStates) tma_load_4d(st + i * kHalf, &job.x, bar, 64 * i, h, t0, b);
-                    tma_load_4d(st + kTile + i * kHalf, &job.y, bar, 64 * i, h, t0, b);
-                }
+                for (int i = 0; i < 2; ++i) tma_load_4d(st + kTile + i * kHalf, &job.y, bar, 64 * i, h, t0, b);
                 for (int i = 0; i < 2; ++i) tma_load_4d(st + 2 * kTile + i * kHalf, &job.z, bar, 64 * i, h, t0, b);
+                if (!kStates) {
+                    // an abort from here leaves the stage's barrier short of X's bytes: its wait below gives up
+                    const bool ok = c < 2 || wait(b_out + 8 * (c & 1), (c - 2) >> 1);
+                    for (int i = 0; ok && i < 2; ++i) tma_load_4d(st + i * kHalf, &job.x, bar, 64 * i, h, t0, b);
+                }
                 ++issued;
             }
             // nothing of this CTA's may be in flight when it ends, an abort included
             for (seen = issued > 2 ? issued - 2 : 0; seen < issued; ++seen)
                 mbar_wait_bounded(b_full + 8 * (seen & 1), (seen >> 1) & 1, kWaitLimit);
         }
-    } else if (warp == 17) {
+    } else if (warp == 25) {
         // ---------------------------------------------------------------- products
         const bool lead = elect_one();
         const uint32_t id_kk = idesc_bf16(128, 128, 0, 0), id_km = idesc_bf16(128, 128, 0, 1);
@@ -195,13 +252,28 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                     mma_commit(b_d);
                 }
             }
-            if (!wait(b_y, c) || (c > 0 && !wait(b_urd, c - 1))) break;
+            if (!wait(b_s, c)) break;
+            if (!kStates) {
+                if (c > 0 && !wait(b_ord, c - 1)) break;
+                tc_fence_after();
+                if (lead) {
+                    if (inter) {
+#pragma unroll
+                        for (int s = 0; s < 8; ++s)
+                            mma_bf16(tbase + TM_O, desc_add(dx, (s >> 2) * kHalf + (s & 3) * 32),
+                                     desc_add(ds, s * 2048), id_km, s);
+                    }
+                    mma_commit(b_xs);
+                }
+            }
+            if (!wait(b_y, c)) break;
             tc_fence_after();
             if (lead) {
                 if (update) {
 #pragma unroll
                     for (int s = 0; s < 8; ++s)
-                        mma_bf16_ta(tbase + TM_U, tbase + TM_YH + 8 * s, desc_add(dz, s * 2048), id_km, s);
+                        mma_bf16_ta(tbase + TM_U, tbase + TM_YH + 8 * s, desc_add(dz, s * 2048), id_km,
+                                    c > 0 || have || s > 0);
 #pragma unroll
                     for (int s = 0; s < 8; ++s)
                         mma_bf16_ta(tbase + TM_U, tbase + TM_YL + 8 * s, desc_add(dz, s * 2048), id_km, 1);
@@ -211,39 +283,33 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
             }
             __syncwarp();
             if (kStates) continue;
-            if (!wait(b_s, c) || (c > 0 && !wait(b_ord, c - 1))) break;
-            tc_fence_after();
-            if (lead) {
-                if (inter) {
-#pragma unroll
-                    for (int s = 0; s < 8; ++s)
-                        mma_bf16(tbase + TM_O, desc_add(dx, (s >> 2) * kHalf + (s & 3) * 32), desc_add(ds, s * 2048),
-                                 id_km, s);
-                }
-                mma_commit(b_xs);
-            }
             if (!wait(b_p, c) || !wait(b_sc, c)) break;
             tc_fence_after();
             if (lead) {
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
-                    mma_bf16_ta(tbase + TM_O, tbase + TM_P + 8 * s, desc_add(dz, s * 2048), id_km, inter || s > 0);
+                    mma_bf16_ta(tbase + TM_O, tbase + TM_P + 64 * (s >> 2) + 8 * (s & 3),
+                                desc_add(dz, s * 2048), id_km, inter || s > 0);
                 mma_commit(b_o);
                 mma_commit(b_free + 8 * (c & 1));
             }
             __syncwarp();
         }
-    } else if (warp < 4) {
+    } else if (warp < 8) {
         // ---------------------------------------------------------------- D -> P
-        const int w = warp;
+        const int w = warp & 3, half = warp >> 2;   // rows 32 w .., columns 64 half ..
+        const bool reverse = p.reverse;
+        const float a_intra = p.a_intra;
+        const float *diag = sm.diag + 32 - lane;
         for (int c = 0; !kStates && c < nchunk; ++c) {
             const int cnt = count_of(c);
             if (!wait(b_d, c)) break;
             tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {   // ascending: P's columns lie over columns of D already read
+            // ascending: P's columns lie over columns of D already read
+#pragma unroll 1
+            for (int k = 2 * half; k < 2 * half + 2; ++k) {
                 uint32_t pk[16];
-                if (p.reverse ? k < w : k > w) {
+                if (reverse ? k < w : k > w) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) pk[i] = 0u;
                 } else {
@@ -252,132 +318,180 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                     tmem_ld_wait();
                     if (k == w) {   // the diagonal block: every distance from the table
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int dist = p.reverse ? i - lane : lane - i;
-                            const float f = dist >= 0 ? p.a_intra * sm.gp[dist & 31] : 0.f;
-                            const float v = f * __uint_as_float(r[i]);
-                            r[i] = __float_as_uint(dist >= 0 && 32 * k + i < cnt ? v : 0.f);
-                        }
+                        for (int i = 0; i < 16; ++i)
+                            pk[i] = pack_bf16(diag[2 * i] * __uint_as_float(r[2 * i]),
+                                              diag[2 * i + 1] * __uint_as_float(r[2 * i + 1]));
                     } else {        // distance to the block's near side times distance within the block
-                        const float f = p.a_intra * sm.gp[p.reverse ? 32 * k - row : row - 32 * k - 31];
+                        const float f = a_intra * sm.gp[reverse ? 32 * k - row : row - 32 * k - 31];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float v = (f * sm.gb[i]) * __uint_as_float(r[i]);
-                            r[i] = __float_as_uint(32 * k + i < cnt ? v : 0.f);
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 e = *reinterpret_cast<const float4 *>(&sm.near[4 * i]);
+                            pk[2 * i] = pack_bf16((f * e.x) * __uint_as_float(r[4 * i]),
+                                                  (f * e.y) * __uint_as_float(r[4 * i + 1]));
+                            pk[2 * i + 1] = pack_bf16((f * e.z) * __uint_as_float(r[4 * i + 2]),
+                                                      (f * e.w) * __uint_as_float(r[4 * i + 3]));
                         }
                     }
+                    if (32 * k + 32 > cnt) {   // masked tokens: whatever D holds there, P is zero
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        pk[i] = pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+                        for (int i = 0; i < 16; ++i) {
+                            if (32 * k + 2 * i >= cnt) pk[i] = 0u;
+                            else if (32 * k + 2 * i + 1 >= cnt) pk[i] &= 0xFFFFu;
+                        }
+                    }
+                    // an entry off the mask of the diagonal block is 0 x D, NaN where D overflows
+                    if (k == w)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const bool keep0 = reverse ? 2 * i >= lane : 2 * i <= lane;
+                            const bool keep1 = reverse ? 2 * i + 1 >= lane : 2 * i + 1 <= lane;
+                            pk[i] &= (keep0 ? 0xFFFFu : 0u) | (keep1 ? 0xFFFF0000u : 0u);
+                        }
                 }
-                tmem_st16(tlane + TM_P + 16 * k, pk);
+                tmem_st16(tlane + TM_P + 64 * half + 16 * (k & 1), pk);
             }
             tmem_st_wait();
             tc_fence_before();
             arrive(b_p);
         }
-    } else if (warp < 8) {
-        // ---------------------------------------------------------------- O
-        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
-        const bool wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
-        for (int c = 0; !kStates && c < nchunk; ++c) {
+    } else if (warp < 16) {
+        // ---------------------------------------------------------------- S and O
+        const int half = (warp - 8) >> 2, T = p.T;   // columns 64 half ..
+        const bool reverse = p.reverse;
+        const float a_inter = p.a_inter;
+        const size_t sdd = static_cast<size_t>(kD) * kD;
+        const float *src = !have ? nullptr
+                           : seg > 0 ? p.seg_states + (static_cast<size_t>(chain) * (p.nseg - 1) + seg - 1) * sdd
+                                     : p.S0 + chain * sdd;
+        const bool src_t = seg == 0 && p.s_t;
+        float *dst = !want_s ? nullptr
+                     : kStates ? p.seg_states + (static_cast<size_t>(chain) * (p.nseg - 1) + seg) * sdd
+                               : p.ST + chain * sdd;
+        const bool dst_t = !kStates && p.s_t;
+        auto at = [&](bool tr, int z) { return tr ? z * kD + row : row * kD + z; };
+        const uint32_t t_s = tlane + TM_U + 64 * half;
+        const uint32_t copy = sbase + OFF_S + half * kHalf;
+
+        for (int c = 0; c < nchunk; ++c) {
             const int cnt = count_of(c);
+            const bool update = c < nchunk - 1 || want_s;
+            if (c > 0 && !wait(b_u, c - 1)) break;   // X S of the last chunk, issued before U, is done as well
+            tc_fence_after();
+            if (c > 0 || have) {
+                const float gn = sm.gp[cnt];
+#pragma unroll 1
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t r[32];
+                    if (c > 0) {
+                        tmem_ld32(t_s + 32 * k, r);
+                        tmem_ld_wait();
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(src[at(src_t, 64 * half + 32 * k + i)]);
+                    }
+                    if (!kStates) {   // operand copy: row = x channel, 128-byte swizzled rows of 64 z channels
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t pk[4];
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+                                pk[u] = pack_bf16(__uint_as_float(r[8 * i + 2 * u]),
+                                                  __uint_as_float(r[8 * i + 2 * u + 1]));
+                            st_shared_v4(copy + sw128_off(row, 64 * k + 16 * i), pk[0], pk[1], pk[2], pk[3]);
+                        }
+                    }
+                    if (update) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(gn * __uint_as_float(r[i]));
+                        tmem_st32(t_s + 32 * k, r);
+                    }
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                fence_proxy_async_smem();
+            }
+            arrive(b_s);
+            if (kStates) continue;
+            if (c > 0) {   // outputs of the last chunk
+                if (!wait(b_o, c - 1)) break;
+                put_out(c - 1);
+            }
             if (c > 0 || have) {
                 if (!wait(b_xs, c)) break;
                 tc_fence_after();
-                const float f = p.a_inter * sm.gp[p.reverse ? max(0, cnt - 1 - row) : row + 1];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    uint32_t r[16];
-                    tmem_ld16(tlane + TM_O + 16 * k, r);
+                const float f = a_inter * sm.gp[reverse ? max(0, cnt - 1 - row) : row + 1];
+#pragma unroll 1
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t r[32];
+                    tmem_ld32(tlane + TM_O + 64 * half + 32 * k, r);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(f * __uint_as_float(r[i]));
-                    tmem_st16(tlane + TM_O + 16 * k, r);
+                    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(f * __uint_as_float(r[i]));
+                    tmem_st32(tlane + TM_O + 64 * half + 32 * k, r);
                 }
                 tmem_st_wait();
                 tc_fence_before();
             }
             arrive(b_sc);
-            if (!wait(b_o, c)) break;
-            tc_fence_after();
-            const int t = t_begin + chunk_of(c) * kC + row;
-            __nv_bfloat16 *dst = out + ((static_cast<size_t>(b) * p.T + t) * p.H + h) * kD;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                uint32_t r[32], pk[16];
-                tmem_ld32(tlane + TM_O + 32 * k, r);
-                tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    pk[i] = row < cnt ? pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])) : 0u;
-                if (t < t_stop) {
-                    if (wide) {
-                        st_global_v8(dst + 32 * k, pk);
-                        st_global_v8(dst + 32 * k + 16, pk + 8);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            reinterpret_cast<uint4 *>(dst + 32 * k)[i] =
-                                make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-                    }
-                }
-                __syncwarp();
-            }
-            tc_fence_before();
-            arrive(b_ord);
         }
-        // outputs of tokens past the valid chunks
-        for (int t = t_begin + nchunk * kC + row; !kStates && t < t_stop; t += kC) {
-            uint4 *dst = reinterpret_cast<uint4 *>(out + ((static_cast<size_t>(b) * p.T + t) * p.H + h) * kD);
+        if (!kStates && nchunk > 0 && wait(b_o, nchunk - 1)) put_out(nchunk - 1);
+        if (want_s && (nchunk == 0 || wait(b_u, nchunk - 1))) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int k = 0; k < 2; ++k) {
+                uint32_t r[32];
+                if (nchunk > 0) {
+                    tmem_ld32(t_s + 32 * k, r);
+                    tmem_ld_wait();
+                } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+                    for (int i = 0; i < 32; ++i)
+                        r[i] = src ? __float_as_uint(src[at(src_t, 64 * half + 32 * k + i)]) : 0u;
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i) dst[at(dst_t, 64 * half + 32 * k + i)] = __uint_as_float(r[i]);
+            }
+        }
+        if (!kStates) {
+            if (lane == 0) tma_store_wait_all();
+            // outputs of tokens past the valid chunks
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + (static_cast<size_t>(b) * T * p.H + h) * kD;
+            for (int t = t_begin + nchunk * kC + row; t < t_stop; t += kC) {
+                uint4 *to = reinterpret_cast<uint4 *>(out + static_cast<size_t>(t) * p.H * kD + 64 * half);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) to[i] = make_uint4(0u, 0u, 0u, 0u);
+            }
         }
     } else {
-        // ---------------------------------------------------------------- keys and state
-        const int half = (warp - 8) >> 2, gt = tid - 256;
-        float s[64];
-        const size_t sdd = static_cast<size_t>(kD) * kD;
-        {
-            const float *src = nullptr;
-            bool tr = false;
-            if (have) {
-                src = seg > 0 ? p.seg_states + (static_cast<size_t>(chain) * (p.nseg - 1) + seg - 1) * sdd
-                              : p.S0 + chain * sdd;
-                tr = seg == 0 && p.s_t;
-            }
-#pragma unroll
-            for (int i = 0; i < 64; ++i)
-                s[i] = !src ? 0.f : tr ? src[(64 * half + i) * kD + row] : src[row * kD + 64 * half + i];
-        }
-        auto put_s = [&]() {   // bf16 copy of S: row = x channel, 128-byte swizzled rows of 64 z channels
-            const uint32_t base = sbase + OFF_S + half * kHalf;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                st_shared_v4(base + sw128_off(row, 16 * i), pack_bf16(s[8 * i], s[8 * i + 1]),
-                             pack_bf16(s[8 * i + 2], s[8 * i + 3]), pack_bf16(s[8 * i + 4], s[8 * i + 5]),
-                             pack_bf16(s[8 * i + 6], s[8 * i + 7]));
-            fence_proxy_async_smem();
-        };
-        if (!kStates) {
-            if (have) put_s();
-            arrive(b_s);
-        }
+        // ---------------------------------------------------------------- keys
+        const int half = (warp - 16) >> 2, gt = tid - 512, T = p.T;   // tokens 64 half .. of the chunk
+        const bool reverse = p.reverse;
+        const float a_upd = p.a_upd;
         int wcnt = -1;
         for (int c = 0; c < nchunk; ++c) {
             const int cnt = count_of(c);
             const bool update = c < nchunk - 1 || want_s;
             if (cnt != wcnt) {
                 named_sync(kBarKeys, 256);
-                if (gt < kC)
-                    sm.w[gt] = gt < cnt ? p.a_upd * sm.gp[p.reverse ? gt + 1 : cnt - 1 - gt] : 0.f;
+                if (gt < kC / 2) {
+                    float w[2], lo[2];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int j = 2 * gt + u;
+                        w[u] = j < cnt ? a_upd * sm.gp[reverse ? j + 1 : cnt - 1 - j] : 0.f;
+                    }
+                    const uint32_t hi = pack_bf16(w[0], w[1]);
+                    lo[0] = w[0] - __uint_as_float(hi << 16);
+                    lo[1] = w[1] - __uint_as_float(hi & 0xFFFF0000u);
+                    sm.w[gt] = make_uint2(hi, pack_bf16(lo[0], lo[1]));
+                }
                 named_sync(kBarKeys, 256);
                 wcnt = cnt;
             }
             if (!wait(b_full + 8 * (c & 1), c >> 1)) break;
             const uint32_t st = sbase + OFF_STAGE + (c & 1) * STAGE;
             const int t0 = t_begin + chunk_of(c) * kC;
-            if (cnt < kC && t0 + cnt < p.T) {
+            if (cnt < kC && t0 + cnt < T) {
                 // masked tokens that the tile holds: a zero weight does not silence a NaN in Z
                 for (int i = gt; i < (kC - cnt) * 16; i += 256) {
                     const int r = cnt + (i >> 4), k = i & 15;
@@ -385,21 +499,35 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                 }
                 fence_proxy_async_smem();
             }
+            if (c > 0 && !wait(b_u, c - 1)) break;   // the last keys are read
             if (update) {   // weighted keys, transposed: lane = x channel, columns = tokens of this half
-                const uint32_t yb = st + kTile + (row >> 6) * kHalf;
-#pragma unroll
+                const uint32_t yb = st + kTile + (row >> 6) * kHalf + 64 * half * 128 + 2 * (row & 7);
+                const uint32_t y16 = (row & 63) >> 3;   // 16-byte word of the row, swizzled by the token below
+                const uint4 *wt = reinterpret_cast<const uint4 *>(sm.w + 32 * half);
+#pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
                     uint32_t hi[8], lo[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int j = 64 * half + 16 * q + 2 * i;
-                        const float2 w = *reinterpret_cast<const float2 *>(&sm.w[j]);
-                        float a = ld_shared_bf16(yb + sw128_off(j, (row & 63) * 2));
-                        float e = ld_shared_bf16(yb + sw128_off(j + 1, (row & 63) * 2));
-                        a = j < cnt ? a * w.x : 0.f;
-                        e = j + 1 < cnt ? e * w.y : 0.f;
-                        hi[i] = pack_bf16(a, e);
-                        lo[i] = pack_bf16(a - __uint_as_float(hi[i] << 16), e - __uint_as_float(hi[i] & 0xFFFF0000u));
+                    for (int i = 0; i < 4; ++i) {   // four tokens
+                        const uint4 w = wt[4 * q + i];
+                        const uint32_t from = yb + (16 * q + 4 * i) * 128;
+                        uint32_t v[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            v[u] = ld_shared_u16(from + u * 128 + ((y16 ^ ((4 * i + u) & 7)) << 4));
+                        if (cnt < kC)   // masked tokens: zero whatever the keys hold
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+                                if (64 * half + 16 * q + 4 * i + u >= cnt) v[u] = 0u;
+                        // w y = hi + lo: hi rounds w1 y, lo takes its exact rest and w2 y (w = w1 + w2)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const uint32_t y = __byte_perm(v[2 * u], v[2 * u + 1], 0x5410);
+                            const uint32_t w1 = u ? w.z : w.x, w2 = u ? w.w : w.y;
+                            const uint32_t a = mul_bf16x2(w1, y);
+                            hi[2 * i + u] = a;
+                            lo[2 * i + u] = fma_bf16x2(w2, y, fma_bf16x2(w1, y, a ^ 0x80008000u));
+                        }
                     }
                     tmem_st8(tlane + TM_YH + 32 * half + 8 * q, hi);
                     tmem_st8(tlane + TM_YL + 32 * half + 8 * q, lo);
@@ -408,39 +536,11 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                 tc_fence_before();
             }
             arrive(b_y);
-            if (!wait(b_u, c)) break;
-            tc_fence_after();
-            if (update) {
-                const float gn = sm.gp[cnt];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t r[16];
-                    tmem_ld16(tlane + TM_U + 64 * half + 16 * k, r);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) s[16 * k + i] = fmaf(gn, s[16 * k + i], __uint_as_float(r[i]));
-                }
-                tc_fence_before();
-            }
-            arrive(b_urd);
-            if (!kStates && c < nchunk - 1) {
-                if (!wait(b_xs, c)) break;   // the copy in use is read
-                put_s();
-                arrive(b_s);
-            }
-        }
-        if (want_s && !sm.abort) {
-            float *dst = kStates ? p.seg_states + (static_cast<size_t>(chain) * (p.nseg - 1) + seg) * sdd
-                                 : p.ST + chain * sdd;
-            const bool tr = !kStates && p.s_t;
-#pragma unroll
-            for (int i = 0; i < 64; ++i)
-                dst[tr ? (64 * half + i) * kD + row : row * kD + 64 * half + i] = s[i];
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (sm.abort && warp == 17) {   // products of an aborted pass: wait for what was issued
+    if (sm.abort && warp == 25) {   // products of an aborted pass: wait for what was issued
         if (elect_one()) {
             mma_commit(b_end);
             mbar_wait_bounded(b_end, 0, kWaitLimit);
@@ -472,8 +572,8 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-// Strided [B, T, H, 128] bf16 tensor; box = 64 channels x 128 tokens of one (b, h).
-bool make_map(CUtensorMap *m, const void *base, const int64_t (&st)[3], int B, int T, int H) {
+// Strided [B, T, H, 128] bf16 tensor; box = 64 channels x `tokens` tokens of one (b, h).
+bool make_map(CUtensorMap *m, const void *base, const int64_t (&st)[3], int B, int T, int H, int tokens) {
     const EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[4] = {kD, static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(T), static_cast<cuuint64_t>(B)};
@@ -481,7 +581,7 @@ bool make_map(CUtensorMap *m, const void *base, const int64_t (&st)[3], int B, i
     const cuuint64_t strides[3] = {H > 1 ? static_cast<cuuint64_t>(st[2]) * 2 : 256,
                                    T > 1 ? static_cast<cuuint64_t>(st[1]) * 2 : 256,
                                    B > 1 ? static_cast<cuuint64_t>(st[0]) * 2 : 256};
-    const cuuint32_t box[4] = {64, 1, kC, 1}, estr[4] = {1, 1, 1, 1};
+    const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(tokens), 1}, estr[4] = {1, 1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -519,9 +619,12 @@ cudaError_t launch_lin_tc(const LinScan *p, int scans, cudaStream_t stream) {
     tp.scans = scans;
     for (int i = 0; i < scans; ++i) {
         tp.job[i].p = p[i];
-        if (!make_map(&tp.job[i].x, p[i].x, p[i].xs, p[i].B, p[i].T, p[i].H) ||
-            !make_map(&tp.job[i].y, p[i].y, p[i].ys, p[i].B, p[i].T, p[i].H) ||
-            !make_map(&tp.job[i].z, p[i].z, p[i].zs, p[i].B, p[i].T, p[i].H))
+        const LinScan &q = p[i];
+        const int64_t dense[3] = {static_cast<int64_t>(q.T) * q.H * kD, static_cast<int64_t>(q.H) * kD, kD};
+        if (!make_map(&tp.job[i].x, q.x, q.xs, q.B, q.T, q.H, kC) ||
+            !make_map(&tp.job[i].y, q.y, q.ys, q.B, q.T, q.H, kC) ||
+            !make_map(&tp.job[i].z, q.z, q.zs, q.B, q.T, q.H, kC) ||
+            !make_map(&tp.job[i].o, q.out, dense, q.B, q.T, q.H, 32))
             return cudaErrorInvalidValue;
     }
     cudaError_t e;
