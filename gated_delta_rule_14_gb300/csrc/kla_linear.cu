@@ -44,8 +44,8 @@ __global__ void __launch_bounds__(kThreads) lin_scan_kernel(const LinScan p, con
         const int d = i / kZ, z = i % kZ;
         float s = 0.f;
         if (!states) {
-            if (seg > 0)
-                s = p.seg_states[((static_cast<size_t>(chain) * (p.nseg - 1) + seg - 1) * p.dx + d) * p.dz + z0 + z];
+            if (p.nseg > 1)
+                s = p.seg_states[lin_slot(p, chain, lin_start_slot(p, seg)) + d * p.dz + z0 + z];
             else if (p.S0)
                 s = p.S0[s_index(p, chain, d, z0 + z)];
         }
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kThreads) lin_scan_kernel(const LinScan p, con
         const int d = i / kZ, z = i % kZ;
         const float s = S[d * (kZ + 1) + z];
         if (states)
-            p.seg_states[((static_cast<size_t>(chain) * (p.nseg - 1) + seg) * p.dx + d) * p.dz + z0 + z] = s;
+            p.seg_states[lin_slot(p, chain, seg) + d * p.dz + z0 + z] = s;
         else
             p.ST[s_index(p, chain, d, z0 + z)] = s;
     }
@@ -147,8 +147,10 @@ __global__ void __launch_bounds__(kThreads) lin_combine_kernel(const LinScan p) 
     if (i >= elems) return;
     const int n = lin_length(p.lengths, b, p.T);
     const float g = p.decay[h];
-    float s = p.S0 ? p.S0[s_index(p, chain, i / p.dz, i % p.dz)] : 0.f;
-    float *slot = p.seg_states + static_cast<size_t>(chain) * (p.nseg - 1) * elems + i;
+    const int d = p.seg_t ? i % p.dx : i / p.dz, z = p.seg_t ? i / p.dx : i % p.dz;
+    float s = p.S0 ? p.S0[s_index(p, chain, d, z)] : 0.f;
+    float *slot = p.seg_states + lin_slot(p, chain, 0) + i;
+    slot[static_cast<size_t>(p.nseg - 1) * elems] = s;
     for (int k = 0; k < p.nseg - 1; ++k) {
         int t0;
         const int m = lin_segment(p, k, n, t0);
@@ -287,7 +289,7 @@ void plan(LinScan &p, int chunk, int ctas_per_chain, int want, int least) {
 constexpr int kSms = 152;
 
 size_t seg_bytes(const LinScan &p) {
-    return static_cast<size_t>(p.B) * p.H * (p.nseg - 1) * p.dx * p.dz * sizeof(float);
+    return p.nseg > 1 ? static_cast<size_t>(p.B) * p.H * p.nseg * p.dx * p.dz * sizeof(float) : 0;
 }
 
 void plan_scan(LinScan &p) { plan(p, kC, p.dz / (p.dz < 32 ? 16 : 32), 2 * kSms, 4); }

@@ -29,7 +29,8 @@ struct LinScan {
     int B, T, H, dx, dz;
     int reverse;
     float a_intra, a_inter, a_upd;
-    float *seg_states;             // [chains][nseg - 1][dx][dz] scratch
+    float *seg_states;             // scratch of nseg > 1 segments: [chains][nseg][dx][dz], or [dz][dx]; the
+    int seg_t;                     // 1: the latter                 start state of segment s at lin_slot(s)
     int nseg, seg_len;             // segments in processing order, tokens each
 };
 
@@ -47,8 +48,14 @@ __device__ __forceinline__ int lin_segment(const LinScan &p, int s, int n, int &
     return left < 0 ? 0 : left < p.seg_len ? left : p.seg_len;
 }
 
-// The start states of the segments: slot s holds segment s's own contribution and is turned into
-// the state after segment s.
+// Slot k < nseg - 1 holds segment k's own contribution to the state, then the state after segment k;
+// the last slot holds S0, which the last segment may overwrite (S_T in place) while the first reads it.
+__device__ __forceinline__ size_t lin_slot(const LinScan &p, int chain, int k) {
+    return (static_cast<size_t>(chain) * p.nseg + k) * p.dx * p.dz;
+}
+__device__ __forceinline__ int lin_start_slot(const LinScan &p, int seg) { return seg > 0 ? seg - 1 : p.nseg - 1; }
+
+// Turns the contributions into start states.
 cudaError_t launch_lin_combine(const LinScan &p, cudaStream_t stream);
 // Tensor-core form: bf16, dx = dz = 128, rows that TMA can read (kla_linear_tc.cu). Runs up to three
 // scans of the same sizes side by side in one launch, each with segments (and a scratch) of its own.

@@ -28,6 +28,8 @@
 // four, and keys and state on the same eight, the chain of conversions took 6900 cycles a chunk.
 #include <cuda.h>
 
+#include <atomic>
+
 #include "kla_linear.cuh"
 #include "sm103_ptx.cuh"
 
@@ -119,7 +121,22 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     const uint32_t b_d = smem_u32(&sm.d), b_p = smem_u32(&sm.p), b_xs = smem_u32(&sm.xs), b_sc = smem_u32(&sm.sc);
     const uint32_t b_o = smem_u32(&sm.o), b_ord = smem_u32(&sm.ord), b_y = smem_u32(&sm.y), b_u = smem_u32(&sm.u);
     const uint32_t b_s = smem_u32(&sm.s);
-    if (tid == 0) {
+    const bool back = p.reverse;
+    auto chunk_of = [&](int c) { return back ? nchunk - 1 - c : c; };
+    auto count_of = [&](int c) { return min(kC, valid - chunk_of(c) * kC); };
+    auto load_yz = [&](int c) {   // one thread
+        const uint32_t st = sbase + OFF_STAGE + (c & 1) * STAGE, bar = b_full + 8 * (c & 1);
+        const int t0 = t_begin + chunk_of(c) * kC;
+        mbar_arrive_expect_tx(bar, (kStates ? 2 : 3) * kTile);
+        for (int i = 0; i < 2; ++i) tma_load_4d(st + kTile + i * kHalf, &job.y, bar, 64 * i, h, t0, b);
+        for (int i = 0; i < 2; ++i) tma_load_4d(st + 2 * kTile + i * kHalf, &job.z, bar, 64 * i, h, t0, b);
+    };
+    auto load_x = [&](int c) {
+        const uint32_t st = sbase + OFF_STAGE + (c & 1) * STAGE, bar = b_full + 8 * (c & 1);
+        const int t0 = t_begin + chunk_of(c) * kC;
+        for (int i = 0; i < 2; ++i) tma_load_4d(st + i * kHalf, &job.x, bar, 64 * i, h, t0, b);
+    };
+    if (warp == 24 && lane == 0) {   // the first loads leave before the rest of the CTA is set up
         mbar_init(b_full, 1);
         mbar_init(b_full + 8, 1);
         mbar_init(b_free, 1);
@@ -138,6 +155,10 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         mbar_init(b_s, 8);
         sm.abort = 0;
         fence_mbar_init();
+        for (int c = 0; c < 2 && c < nchunk; ++c) {
+            load_yz(c);
+            if (!kStates) load_x(c);
+        }
     }
     if (tid <= kC) sm.gp[tid] = powf(g, static_cast<float>(tid));
     if (tid < 64) {
@@ -168,9 +189,6 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
     };
-    const bool back = p.reverse;
-    auto chunk_of = [&](int c) { return back ? nchunk - 1 - c : c; };
-    auto count_of = [&](int c) { return min(kC, valid - chunk_of(c) * kC); };
 
     // warps 8-15: O of chunk c leaves through the X tile, which its products have read; each warp's 32
     // rows x 64 channels are one box, and rows past T are cut off by the tensor's bounds
@@ -208,24 +226,17 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
 
     if (warp == 24) {
         // ---------------------------------------------------------------- loads
-        int issued = 0, seen = 0;
         if (lane == 0) {
-            for (int c = 0; c < nchunk; ++c) {
-                if (c >= 2 && !wait(b_free + 8 * (c & 1), (c - 2) >> 1)) break;
-                const uint32_t st = sbase + OFF_STAGE + (c & 1) * STAGE, bar = b_full + 8 * (c & 1);
-                const int t0 = t_begin + chunk_of(c) * kC;
-                mbar_arrive_expect_tx(bar, (kStates ? 2 : 3) * kTile);
-                for (int i = 0; i < 2; ++i) tma_load_4d(st + kTile + i * kHalf, &job.y, bar, 64 * i, h, t0, b);
-                for (int i = 0; i < 2; ++i) tma_load_4d(st + 2 * kTile + i * kHalf, &job.z, bar, 64 * i, h, t0, b);
-                if (!kStates) {
-                    // an abort from here leaves the stage's barrier short of X's bytes: its wait below gives up
-                    const bool ok = c < 2 || wait(b_out + 8 * (c & 1), (c - 2) >> 1);
-                    for (int i = 0; ok && i < 2; ++i) tma_load_4d(st + i * kHalf, &job.x, bar, 64 * i, h, t0, b);
-                }
+            int issued = min(nchunk, 2);
+            for (int c = 2; c < nchunk; ++c) {
+                if (!wait(b_free + 8 * (c & 1), (c - 2) >> 1)) break;
+                load_yz(c);
                 ++issued;
+                // an abort here leaves the stage's barrier short of X's bytes: its wait below gives up
+                if (!kStates && wait(b_out + 8 * (c & 1), (c - 2) >> 1)) load_x(c);
             }
             // nothing of this CTA's may be in flight when it ends, an abort included
-            for (seen = issued > 2 ? issued - 2 : 0; seen < issued; ++seen)
+            for (int seen = issued > 2 ? issued - 2 : 0; seen < issued; ++seen)
                 mbar_wait_bounded(b_full + 8 * (seen & 1), (seen >> 1) & 1, kWaitLimit);
         }
     } else if (warp == 25) {
@@ -361,14 +372,28 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         const float a_inter = p.a_inter;
         const size_t sdd = static_cast<size_t>(kD) * kD;
         const float *src = !have ? nullptr
-                           : seg > 0 ? p.seg_states + (static_cast<size_t>(chain) * (p.nseg - 1) + seg - 1) * sdd
-                                     : p.S0 + chain * sdd;
-        const bool src_t = seg == 0 && p.s_t;
+                           : p.nseg > 1 ? p.seg_states + lin_slot(p, chain, lin_start_slot(p, seg))
+                                        : p.S0 + chain * sdd;
+        const bool src_t = p.nseg > 1 || p.s_t;   // [z][d]: a warp's lanes are neighbours; the scratch is kept so
         float *dst = !want_s ? nullptr
-                     : kStates ? p.seg_states + (static_cast<size_t>(chain) * (p.nseg - 1) + seg) * sdd
+                     : kStates ? p.seg_states + lin_slot(p, chain, seg)
                                : p.ST + chain * sdd;
-        const bool dst_t = !kStates && p.s_t;
-        auto at = [&](bool tr, int z) { return tr ? z * kD + row : row * kD + z; };
+        const bool dst_t = kStates || p.s_t;
+        auto get = [&](uint32_t (&r)[32], int z) {   // 32 z channels from z of this thread's x channel
+            if (src_t) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(src[(z + i) * kD + row]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(src + row * kD + z + 4 * i);
+                    r[4 * i] = v.x;
+                    r[4 * i + 1] = v.y;
+                    r[4 * i + 2] = v.z;
+                    r[4 * i + 3] = v.w;
+                }
+            }
+        };
         const uint32_t t_s = tlane + TM_U + 64 * half;
         const uint32_t copy = sbase + OFF_S + half * kHalf;
 
@@ -386,8 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                         tmem_ld32(t_s + 32 * k, r);
                         tmem_ld_wait();
                     } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(src[at(src_t, 64 * half + 32 * k + i)]);
+                        get(r, 64 * half + 32 * k);
                     }
                     if (!kStates) {   // operand copy: row = x channel, 128-byte swizzled rows of 64 z channels
 #pragma unroll
@@ -443,13 +467,22 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                 if (nchunk > 0) {
                     tmem_ld32(t_s + 32 * k, r);
                     tmem_ld_wait();
+                } else if (src) {
+                    get(r, 64 * half + 32 * k);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        r[i] = src ? __float_as_uint(src[at(src_t, 64 * half + 32 * k + i)]) : 0u;
+                    for (int i = 0; i < 32; ++i) r[i] = 0u;
                 }
+                const int z = 64 * half + 32 * k;
+                if (dst_t) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) dst[at(dst_t, 64 * half + 32 * k + i)] = __uint_as_float(r[i]);
+                    for (int i = 0; i < 32; ++i) dst[(z + i) * kD + row] = __uint_as_float(r[i]);
+                } else {   // 16 bytes a lane and row: one value at a time took 12 us
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint4 *>(dst + row * kD + z + 4 * i) =
+                            make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+                }
             }
         }
         if (!kStates) {
@@ -594,6 +627,23 @@ bool tma_rows(const void *base, const int64_t (&st)[3], int B, int T, int H) {
     return (reinterpret_cast<uintptr_t>(base) & 15) == 0;
 }
 
+// The kernels' shared memory, asked for once per device: the attribute outlasts the call.
+cudaError_t allow_smem() {
+    constexpr int kMaxDevices = 64;
+    static std::atomic<bool> done[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev < 0 || dev >= kMaxDevices) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+    if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    for (const void *k : {reinterpret_cast<const void *>(lin_tc_kernel<true>),
+                          reinterpret_cast<const void *>(lin_tc_kernel<false>)})
+        if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(SMEM_BYTES))) !=
+            cudaSuccess)
+            return e;
+    done[dev].store(true, std::memory_order_release);
+    return cudaSuccess;
+}
+
 }  // namespace
 
 bool lin_tc_supports(const LinScan &p, kla_dtype dtype) {
@@ -619,27 +669,35 @@ cudaError_t launch_lin_tc(const LinScan *p, int scans, cudaStream_t stream) {
     tp.scans = scans;
     for (int i = 0; i < scans; ++i) {
         tp.job[i].p = p[i];
+        tp.job[i].p.seg_t = 1;
         const LinScan &q = p[i];
         const int64_t dense[3] = {static_cast<int64_t>(q.T) * q.H * kD, static_cast<int64_t>(q.H) * kD, kD};
-        if (!make_map(&tp.job[i].x, q.x, q.xs, q.B, q.T, q.H, kC) ||
-            !make_map(&tp.job[i].y, q.y, q.ys, q.B, q.T, q.H, kC) ||
-            !make_map(&tp.job[i].z, q.z, q.zs, q.B, q.T, q.H, kC) ||
+        auto tile = [&](CUtensorMap *m, const void *base, const int64_t (&st)[3]) {
+            for (int k = 0; k < i; ++k) {   // the directions of a backward pass share their inputs
+                const LinScan &o = p[k];
+                const void *had[3] = {o.x, o.y, o.z};
+                const int64_t *hs[3] = {o.xs, o.ys, o.zs};
+                const CUtensorMap *hm[3] = {&tp.job[k].x, &tp.job[k].y, &tp.job[k].z};
+                for (int u = 0; u < 3; ++u)
+                    if (had[u] == base && hs[u][0] == st[0] && hs[u][1] == st[1] && hs[u][2] == st[2]) {
+                        *m = *hm[u];
+                        return true;
+                    }
+            }
+            return make_map(m, base, st, q.B, q.T, q.H, kC);
+        };
+        if (!tile(&tp.job[i].x, q.x, q.xs) || !tile(&tp.job[i].y, q.y, q.ys) || !tile(&tp.job[i].z, q.z, q.zs) ||
             !make_map(&tp.job[i].o, q.out, dense, q.B, q.T, q.H, 32))
             return cudaErrorInvalidValue;
     }
     cudaError_t e;
-    if ((e = device_error_word(&tp.err)) != cudaSuccess) return e;
-    if ((e = cudaFuncSetAttribute(lin_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  static_cast<int>(SMEM_BYTES))) != cudaSuccess ||
-        (e = cudaFuncSetAttribute(lin_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  static_cast<int>(SMEM_BYTES))) != cudaSuccess)
-        return e;
+    if ((e = device_error_word(&tp.err)) != cudaSuccess || (e = allow_smem()) != cudaSuccess) return e;
     const int chains = p[0].B * p[0].H, nseg = p[0].nseg;
     if (nseg > 1) {
         lin_tc_kernel<true><<<dim3(chains * scans, nseg - 1), kThreads, SMEM_BYTES, stream>>>(tp);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         for (int i = 0; i < scans; ++i)
-            if ((e = launch_lin_combine(p[i], stream)) != cudaSuccess) return e;
+            if ((e = launch_lin_combine(tp.job[i].p, stream)) != cudaSuccess) return e;
     }
     lin_tc_kernel<false><<<dim3(chains * scans, nseg), kThreads, SMEM_BYTES, stream>>>(tp);
     return cudaGetLastError();

@@ -170,6 +170,16 @@ def test_state_in_place_and_continuation():
     assert rel(torch.cat(parts, 1), o) <= 6e-3 and rel(S2, S) <= 1e-5
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_state_in_place_over_segments(dtype):
+    import gated_delta_rule_14_gb300 as kla
+    d = make(1, 3000, 2, 128, 128, dtype, seed=12)
+    o, S = run_fwd(d)
+    S2 = d["S0"].clone()
+    o2, _ = kla.linear_fwd(d["q"], d["k"], d["v"], d["g"], S2, q_scale=d["s"], S_T=S2)
+    assert torch.equal(o, o2) and torch.equal(S, S2)
+
+
 def test_no_tokens():
     import gated_delta_rule_14_gb300 as kla
     d = make(2, 0, 2, 64, 32, torch.float32, seed=8)
