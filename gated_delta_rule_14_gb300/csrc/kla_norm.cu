@@ -3,40 +3,71 @@
 //   forward    y = xh w[g] + b[g],  xh = (x - mean) rstd
 //   backward   dx = rstd (u - mean(u) - xh mean(u xh)),  u = dy w[g];  dw[g] = sum dy xh;  db[g] = sum dy
 //
-// Every value is read once and stays in registers: a row belongs to one team of threads (16 or 32
-// lanes, or a whole CTA), each with kE values at fixed columns. Teams are persistent and keep to one
-// group, so that weight and bias, and in the backward pass the sums of dw and db, stay in registers
-// too; the sums leave as one partial row per CTA and a second launch adds those in a fixed order.
-// Rows longer than a CTA's registers (n > 16384) are walked in pieces of that size.
+// Every value is read once: a row belongs to one team of threads (16 or 32 lanes up to 512 values, a
+// whole CTA above), each with kE values at fixed columns. Teams are persistent and keep to one group,
+// so that weight and bias, and in the backward pass the sums of dw and db, stay in registers; the sums
+// leave as one partial row per CTA and a second launch adds those in a fixed order.
+// What bounds it is the memory, and to keep it busy ~70 KB have to be on the way to every SM. Rows of a
+// CTA therefore come and go through shared memory by bulk copies, several rows ahead, which cost no
+// registers and take rows of any width and alignment at full speed: a copy takes the 16-byte granules
+// that the row touches, and threads pick their columns from there. (Loads one row ahead into registers
+// reached half of that.) Rows longer than 8192 values are walked in pieces and read again for each use.
+#include <atomic>
 #include <climits>
 
 #include "kla_internal.cuh"
+#include "sm103_ptx.cuh"
 #include "../../include/kla_layer.h"
 
 namespace kla {
+cudaError_t device_error_word(unsigned **out);   // kla_api.cu
 namespace {
 
 constexpr int kSms = 152;
 constexpr int kE = 16;                 // values of one thread
 constexpr int kMaxBlock = 1024;
-constexpr int kHeld = kE * kMaxBlock;  // longest row held in registers
+constexpr int kTeamMost = 32 * kE;     // longest row of a part of a warp
+constexpr int kRingMostN = 8192;       // longest row that goes through shared memory
+constexpr int kRingMost = 4;           // rows on the way to a team, at most
+// Values of one thread: the backward pass keeps five arrays of them, the forward pass three. The more, the
+// less the sums and hand-overs of a row weigh.
+constexpr int ring_values(bool bwd) { return bwd ? 16 : 32; }
+// Threads of a CTA: the backward pass takes one CTA an SM, so that an SM leaves one partial row; the
+// forward pass two.
+constexpr int ring_block(bool bwd) { return bwd ? 512 : 256; }
 
-// kV consecutive values of type T at p as fp32; one access.
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n.reg .b64 a, b, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nadd.rn.f32x2 d, a, b;\n"
+        "mov.b64 {%0, %1}, d;\n}" : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n.reg .b64 a, b, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmul.rn.f32x2 d, a, b;\n"
+        "mov.b64 {%0, %1}, d;\n}" : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n.reg .b64 a, b, c, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmov.b64 c, {%6, %7};\n"
+        "fma.rn.f32x2 d, a, b, c;\nmov.b64 {%0, %1}, d;\n}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
+// kV consecutive values of type T, moved in one access.
 template <typename T, int kV>
-__device__ __forceinline__ void load(const T *p, float *x) {
+__device__ __forceinline__ void load(const T *p, T *x) {
     if constexpr (sizeof(T) * kV == 16) {
-        const uint4 r = *reinterpret_cast<const uint4 *>(p);
-        const T *e = reinterpret_cast<const T *>(&r);
-#pragma unroll
-        for (int i = 0; i < kV; ++i) x[i] = to_f32(e[i]);
-    } else if constexpr (sizeof(T) * kV == 4 && kV == 2) {
-        const uint32_t r = *reinterpret_cast<const uint32_t *>(p);
-        const T *e = reinterpret_cast<const T *>(&r);
-        x[0] = to_f32(e[0]);
-        x[1] = to_f32(e[1]);
+        *reinterpret_cast<uint4 *>(x) = *reinterpret_cast<const uint4 *>(p);
+    } else if constexpr (sizeof(T) * kV == 4) {
+        *reinterpret_cast<uint32_t *>(x) = *reinterpret_cast<const uint32_t *>(p);
     } else {
 #pragma unroll
-        for (int i = 0; i < kV; ++i) x[i] = to_f32(p[i]);
+        for (int i = 0; i < kV; ++i) x[i] = p[i];
     }
 }
 template <typename T, int kV>
@@ -47,7 +78,7 @@ __device__ __forceinline__ void store(T *p, const float *x) {
 #pragma unroll
         for (int i = 0; i < kV; ++i) e[i] = from_f32<T>(x[i]);
         *reinterpret_cast<uint4 *>(p) = r;
-    } else if constexpr (sizeof(T) * kV == 4 && kV == 2) {
+    } else if constexpr (kV == 2) {
         uint32_t r;
         T *e = reinterpret_cast<T *>(&r);
         e[0] = from_f32<T>(x[0]);
@@ -59,57 +90,76 @@ __device__ __forceinline__ void store(T *p, const float *x) {
     }
 }
 
-// Sum over the row's team: kTeam lanes of a warp, or the CTA (kTeam = 0), where two buffers let
-// one barrier a sum do.
-template <int kTeam>
-struct TeamSum {
-    int turn = 0;
-    __device__ __forceinline__ float2 operator()(float2 v) {
-        constexpr int kLanes = kTeam ? kTeam : 32;
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ float2 add(float2 a, float2 b) { return make_float2(a.x + b.x, a.y + b.y); }
+__device__ __forceinline__ float across(float v, int off) { return __shfl_xor_sync(0xffffffffu, v, off); }
+__device__ __forceinline__ float2 across(float2 v, int off) { return make_float2(across(v.x, off), across(v.y, off)); }
+
+// Sum over the `lanes` lanes of a row's team.
+template <int kLanes, typename V>
+__device__ __forceinline__ V lane_sum(V v) {
 #pragma unroll
-        for (int off = kLanes / 2; off; off >>= 1) {
-            v.x += __shfl_xor_sync(0xffffffffu, v.x, off);
-            v.y += __shfl_xor_sync(0xffffffffu, v.y, off);
-        }
-        if constexpr (kTeam == 0) {
-            __shared__ float2 part[2][kMaxBlock / 32];
-            const int nw = blockDim.x / 32;
-            if ((threadIdx.x & 31) == 0) part[turn][threadIdx.x / 32] = v;
-            __syncthreads();
-            v = make_float2(0.f, 0.f);
-            for (int w = 0; w < nw; ++w) {
-                v.x += part[turn][w].x;
-                v.y += part[turn][w].y;
-            }
-            turn ^= 1;
-        }
+    for (int off = kLanes / 2; off; off >>= 1) v = add(v, across(v, off));
+    return v;
+}
+// Sum over kWarps warps that share a named barrier; calls alternate between two buffers, so that one
+// barrier a sum does.
+template <int kWarps>
+struct WarpsSum {
+    float2 (*part)[kMaxBlock / 32];   // [2][warps of the CTA]
+    int first, bar, turn;             // the team's first warp and barrier
+    template <typename V>
+    __device__ __forceinline__ V operator()(V v) {
+        v = lane_sum<32>(v);
+        V *slot = reinterpret_cast<V *>(part[turn] + first);
+        if ((threadIdx.x & 31) == 0) slot[(threadIdx.x / 32) % kWarps] = v;
+        ptx::named_sync(bar, 32 * kWarps);
+        v = slot[0];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) v = add(v, slot[w]);
+        turn ^= 1;
         return v;
     }
 };
 
-// Which rows a thread's team walks: rows first, first + step, .. of group g.
-template <int kTeam>
+// Which rows a thread's team of `width` threads walks: rows first, first + step, .. of group g.
 struct Walk {
     int lane, width, g;
     int64_t first, step;
-    __device__ Walk(int groups) {
-        const int parts = gridDim.x / groups;
+    __device__ Walk(int groups, int threads) {
         g = blockIdx.x % groups;
-        width = kTeam ? kTeam : blockDim.x;
-        lane = kTeam ? threadIdx.x % kTeam : threadIdx.x;
-        const int teams = kTeam ? blockDim.x / kTeam : 1;
-        first = static_cast<int64_t>(blockIdx.x / groups) * teams + (kTeam ? threadIdx.x / kTeam : 0);
-        step = static_cast<int64_t>(parts) * teams;
+        width = threads;
+        lane = threadIdx.x % threads;
+        const int teams = blockDim.x / threads;
+        first = static_cast<int64_t>(blockIdx.x / groups) * teams + threadIdx.x / threads;
+        step = static_cast<int64_t>(gridDim.x / groups) * teams;
+    }
+};
+
+// One thread's values of a row as they are in memory.
+template <typename T, int kV>
+struct Held {
+    alignas(16) T v[kE];
+    __device__ __forceinline__ void get(const T *row, int lane, int width, int n, bool live) {
+#pragma unroll
+        for (int k = 0; k < kE / kV; ++k) {
+            const int c = (k * width + lane) * kV;
+            if (live && c < n) {
+                load<T, kV>(row + c, v + k * kV);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kV; ++i) v[k * kV + i] = from_f32<T>(0.f);
+            }
+        }
     }
 };
 
 template <typename T, int kV, int kTeam>
-__global__ void __launch_bounds__(kTeam ? 256 : kMaxBlock)
+__global__ void __launch_bounds__(256)
 norm_fwd_kernel(const T *x, const float *w, const float *b, T *y, float *mean, float *rstd, int64_t rows, int groups,
                 int n, float eps) {
     constexpr int kK = kE / kV;
-    const Walk<kTeam> at(groups);
-    TeamSum<kTeam> sum;
+    const Walk at(groups, kTeam);
     float wr[kE], br[kE];
 #pragma unroll
     for (int k = 0; k < kK; ++k)
@@ -122,23 +172,21 @@ norm_fwd_kernel(const T *x, const float *w, const float *b, T *y, float *mean, f
     // every lane of a warp takes the same number of turns (the sums use whole warps)
     const int64_t turns = (rows + at.step - 1) / at.step;
     const float inv = 1.f / n;
+    Held<T, kV> next;   // the next row is on its way while this one is worked on
+    next.get(x + (at.first * groups + at.g) * n, at.lane, at.width, n, at.first < rows);
     for (int64_t t = 0; t < turns; ++t) {
         const int64_t r = at.first + t * at.step;
         const bool live = r < rows;
         const int64_t row = r * groups + at.g;
-        const T *xr = x + row * n;
         float v[kE];
         float s = 0.f;
 #pragma unroll
-        for (int k = 0; k < kK; ++k) {
-            const int c = (k * at.width + at.lane) * kV;
-#pragma unroll
-            for (int i = 0; i < kV; ++i) v[k * kV + i] = 0.f;
-            if (live && c < n) load<T, kV>(xr + c, v + k * kV);
+        for (int i = 0; i < kE; ++i) {
+            v[i] = to_f32(next.v[i]);
+            s += v[i];
         }
-#pragma unroll
-        for (int i = 0; i < kE; ++i) s += v[i];
-        const float mu = sum(make_float2(s, 0.f)).x * inv;
+        next.get(x + (row + at.step * groups) * n, at.lane, at.width, n, r + at.step < rows);
+        const float mu = lane_sum<kTeam>(s) * inv;
         float q = 0.f;
 #pragma unroll
         for (int k = 0; k < kK; ++k)
@@ -148,7 +196,7 @@ norm_fwd_kernel(const T *x, const float *w, const float *b, T *y, float *mean, f
                     const float d = v[k * kV + i] - mu;
                     q = fmaf(d, d, q);
                 }
-        const float rs = 1.f / sqrtf(sum(make_float2(q, 0.f)).x * inv + eps);
+        const float rs = 1.f / sqrtf(lane_sum<kTeam>(q) * inv + eps);
         if (!live) continue;
         if (at.lane == 0) {
             if (mean) mean[row] = mu;
@@ -168,12 +216,11 @@ norm_fwd_kernel(const T *x, const float *w, const float *b, T *y, float *mean, f
 }
 
 template <typename T, int kV, int kTeam>
-__global__ void __launch_bounds__(kTeam ? 256 : kMaxBlock)
+__global__ void __launch_bounds__(256)
 norm_bwd_kernel(const T *dy, const T *x, const float *w, const float *mean, const float *rstd, T *dx, float *part,
                 int64_t rows, int groups, int n) {
     constexpr int kK = kE / kV;
-    const Walk<kTeam> at(groups);
-    TeamSum<kTeam> sum;
+    const Walk at(groups, kTeam);
     float wr[kE], dw[kE], db[kE];
 #pragma unroll
     for (int k = 0; k < kK; ++k)
@@ -185,26 +232,31 @@ norm_bwd_kernel(const T *dy, const T *x, const float *w, const float *mean, cons
         }
     const int64_t turns = (rows + at.step - 1) / at.step;
     const float inv = 1.f / n;
+    Held<T, kV> nx, nd;   // the next row is on its way while this one is worked on
+    float nmu = 0.f, nrs = 0.f;
+    auto fetch = [&](int64_t r) {
+        const int64_t row = r * groups + at.g;
+        const bool live = r < rows;
+        nx.get(x + row * n, at.lane, at.width, n, live);
+        nd.get(dy + row * n, at.lane, at.width, n, live);
+        if (live) {
+            nmu = mean[row];
+            nrs = rstd[row];
+        }
+    };
+    fetch(at.first);
     for (int64_t t = 0; t < turns; ++t) {
         const int64_t r = at.first + t * at.step;
         const bool live = r < rows;
         const int64_t row = r * groups + at.g;
+        const float mu = nmu, rs = nrs;
         float xh[kE], d[kE];
 #pragma unroll
-        for (int i = 0; i < kE; ++i) xh[i] = d[i] = 0.f;
-        float mu = 0.f, rs = 0.f;
-        if (live) {
-            mu = mean[row];
-            rs = rstd[row];
+        for (int i = 0; i < kE; ++i) {
+            xh[i] = to_f32(nx.v[i]);
+            d[i] = to_f32(nd.v[i]);
         }
-#pragma unroll
-        for (int k = 0; k < kK; ++k) {
-            const int c = (k * at.width + at.lane) * kV;
-            if (live && c < n) {
-                load<T, kV>(x + row * n + c, xh + k * kV);
-                load<T, kV>(dy + row * n + c, d + k * kV);
-            }
-        }
+        fetch(r + at.step);
         float2 s = make_float2(0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < kK; ++k)
@@ -218,7 +270,7 @@ norm_bwd_kernel(const T *dy, const T *x, const float *w, const float *mean, cons
                     s.x += d[i];
                     s.y = fmaf(d[i], xh[i], s.y);
                 }
-        s = sum(s);
+        s = lane_sum<kTeam>(s);
         if (!live) continue;
         s.x *= inv;
         s.y *= inv;
@@ -236,83 +288,349 @@ norm_bwd_kernel(const T *dy, const T *x, const float *w, const float *mean, cons
     if (!part) return;
     // one partial row of dw and of db per CTA
     float *pw = part + static_cast<int64_t>(blockIdx.x) * 2 * n, *pb = pw + n;
-    if constexpr (kTeam == 0) {
+    __shared__ float acc[256 * kE];   // [team][column]
+    constexpr int kTeams = 256 / kTeam, kCols = kTeam * kE;
+#pragma unroll
+    for (int pass = 0; pass < 2; ++pass) {
+        __syncthreads();
 #pragma unroll
         for (int k = 0; k < kK; ++k)
 #pragma unroll
-            for (int i = 0; i < kV; ++i) {
-                const int c = (k * at.width + at.lane) * kV + i;
-                if (c < n) {
-                    pw[c] = dw[k * kV + i];
-                    pb[c] = db[k * kV + i];
-                }
+            for (int i = 0; i < kV; ++i)
+                acc[threadIdx.x / kTeam * kCols + (k * kTeam + at.lane) * kV + i] =
+                    pass ? db[k * kV + i] : dw[k * kV + i];
+        __syncthreads();
+        for (int c = threadIdx.x; c < n; c += 256) {
+            float s = 0.f;
+#pragma unroll
+            for (int q = 0; q < kTeams; ++q) s += acc[q * kCols + c];
+            (pass ? pb : pw)[c] = s;
+        }
+    }
+}
+
+// ---- rows of a CTA, through shared memory
+// A row's buffer mirrors the memory around it: the 16-byte granules that the row touches, copied in one
+// bulk copy. Granules that reach past the tensor's ends are left out; their few values are read directly.
+template <typename T>
+struct Row {
+    const T *base;
+    int shift;          // values from the buffer's start to the row's
+    int skip, have;     // columns [skip, have) are in the buffer
+    uint32_t lead, bytes;   // what the copy leaves out at the front, and brings
+    __device__ __forceinline__ Row(const T *tensor, const T *end, const T *row, int n) : base(row) {
+        constexpr int kSize = sizeof(T), kG = 16 / kSize;
+        shift = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15) / kSize;
+        int lo = 0, hi = (shift + n + kG - 1) / kG;   // granules
+        if (row - tensor < shift) ++lo;
+        if (end - row < hi * kG - shift) --hi;
+        if (hi < lo) hi = lo;
+        skip = lo * kG - shift;
+        have = hi * kG - shift;
+        lead = lo * 16;
+        bytes = (hi - lo) * 16;
+    }
+    __device__ __forceinline__ void fetch(uint32_t buf, uint32_t bar) const {   // one thread; bytes are expected already
+        if (bytes)
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                             buf + lead),
+                         "l"(reinterpret_cast<uintptr_t>(base - shift) + lead), "r"(bytes), "r"(bar)
+                         : "memory");
+    }
+};
+// Whether the columns of a thread's k-th access exist for every lane: a row has more than half of the
+// values that its team holds (the narrowest team: more than kTeamMost).
+__device__ __forceinline__ constexpr bool always(int k, int width, int v, int e) {
+    return (k + 1) * width * v <= kTeamMost || 2 * (k + 1) * v <= e;
+}
+// kN values, kV at a time, of a thread; zero from column n on. kV > 1: rows start on 16 bytes.
+template <typename T, int kV, int kWidth, int kN>
+__device__ __forceinline__ void get_row(const T *tensor, const T *end, const T *row, const uint8_t *buf, int lane,
+                                        int n, float2 (&x)[kN / 2]) {
+    float *f = reinterpret_cast<float *>(x);
+    if constexpr (kV > 1) {
+        const T *v = reinterpret_cast<const T *>(buf) + lane * kV;
+#pragma unroll
+        for (int k = 0; k < kN / kV; ++k) {
+            alignas(16) T e[kV];
+            if (always(k, kWidth, kV, kN) || (k * kWidth + lane) * kV < n) {
+                load<T, kV>(v + k * kWidth * kV, e);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kV; ++i) e[i] = from_f32<T>(0.f);
             }
+#pragma unroll
+            for (int i = 0; i < kV; ++i) f[k * kV + i] = to_f32(e[i]);
+        }
     } else {
-        __shared__ float acc[256 * kE];   // [team][column]
-        constexpr int kTeams = 256 / kTeam, kCols = kTeam * kE;
+        const Row<T> r(tensor, end, row, n);
+        const T *v = reinterpret_cast<const T *>(buf) + r.shift + lane;
 #pragma unroll
-        for (int pass = 0; pass < 2; ++pass) {
-            __syncthreads();
+        for (int k = 0; k < kN; ++k)
+            f[k] = always(k, kWidth, 1, kN) || k * kWidth + lane < n ? to_f32(v[k * kWidth]) : 0.f;
+        if (r.skip > 0 || r.have < n)   // the tensor's first or last row, off the 16-byte grid
 #pragma unroll
-            for (int k = 0; k < kK; ++k)
+            for (int k = 0; k < kN; ++k) {
+                const int c = k * kWidth + lane;
+                if (c < n && (c < r.skip || c >= r.have)) f[k] = to_f32(row[c]);
+            }
+    }
+}
+
+// A row on its way out: whole granules inside the row leave by one bulk store from a buffer that
+// mirrors the memory, the few values at its ends directly.
+template <typename T>
+struct OutRow {
+    T *row;
+    int shift, lo, hi;   // columns [lo, hi) leave by the bulk store
+    __device__ __forceinline__ OutRow(T *r, int n) : row(r) {
+        constexpr int kSize = sizeof(T), kG = 16 / kSize;
+        shift = static_cast<int>(reinterpret_cast<uintptr_t>(r) & 15) / kSize;
+        lo = (kG - shift) % kG;
+        hi = (shift + n) / kG * kG - shift;
+        if (hi < lo) hi = lo;
+    }
+    __device__ __forceinline__ void send(uint32_t buf) const {   // one thread
+        if (hi > lo)
+            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                             reinterpret_cast<uintptr_t>(row + lo)),
+                         "r"(buf + static_cast<uint32_t>((shift + lo) * sizeof(T))),
+                         "r"(static_cast<uint32_t>((hi - lo) * sizeof(T)))
+                         : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+};
+
+// kBwd: x and dy in, dx out, else x in, y out. A CTA holds one or more teams of `width` threads, each
+// with buffers and a named barrier of its own. The barrier of a sum over the row also tells that the
+// row's buffer is read and that the last row's output is written.
+template <typename T, int kV, int kWidth, bool kBwd>
+__global__ void __launch_bounds__(ring_block(kBwd), kBwd ? 1 : 2)
+norm_ring_kernel(const T *x, const T *dy, const float *w, const float *b, T *out, float *mean, float *rstd,
+                 float *part, int64_t rows, int groups, int n, float eps, int stages, int pitch, unsigned *err) {
+    using namespace ptx;
+    constexpr int kN = ring_values(kBwd), kK = kN / kV, kIns = kBwd ? 2 : 1;
+    extern __shared__ __align__(128) uint8_t sm[];
+    __shared__ uint64_t full[ring_block(kBwd) / kWidth][kRingMost];
+    __shared__ float2 sums[2][kMaxBlock / 32];
+    __shared__ int lost;
+    const Walk at(groups, kWidth);
+    const int team = threadIdx.x / kWidth, lane = at.lane;
+    WarpsSum<kWidth / 32> sum{sums, team * (kWidth / 32), 1 + team, 0};
+    const bool lead = lane == 0;
+    uint8_t *ring = sm + team * (stages * kIns + 2) * pitch, *outs = ring + stages * kIns * pitch;
+    const uint32_t s_ring = smem_u32(ring), s_outs = smem_u32(outs), bar0 = smem_u32(full[team]);
+    const T *end_x = x + rows * groups * n, *end_d = kBwd ? dy + rows * groups * n : nullptr;
+    const int turns = at.first < rows ? static_cast<int>((rows - at.first + at.step - 1) / at.step) : 0;
+    const int64_t o0 = (at.first * groups + at.g) * n, hop = at.step * groups * n;   // values between rows
+    auto fetch = [&](int64_t o, int st) {   // one thread of the team
+        const uint32_t bar = bar0 + 8 * st, buf = s_ring + st * kIns * pitch;
+        const Row<T> rx(x, end_x, x + o, n);
+        if constexpr (kBwd) {
+            const Row<T> rd(dy, end_d, dy + o, n);
+            mbar_arrive_expect_tx(bar, rx.bytes + rd.bytes);
+            rd.fetch(buf + pitch, bar);
+        } else {
+            mbar_arrive_expect_tx(bar, rx.bytes);
+        }
+        rx.fetch(buf, bar);
+    };
+    if (threadIdx.x == 0) lost = 0;
+    if (lead) {
+        for (int i = 0; i < stages; ++i) mbar_init(bar0 + 8 * i, 1);
+        fence_mbar_init();
+        for (int i = 0; i < stages && i < turns; ++i) fetch(o0 + i * hop, i);
+    }
+    float2 wr[kN / 2], acc_w[kN / 2], acc_b[kN / 2];   // forward: acc_b is the bias
 #pragma unroll
-                for (int i = 0; i < kV; ++i)
-                    acc[threadIdx.x / kTeam * kCols + (k * kTeam + at.lane) * kV + i] =
-                        pass ? db[k * kV + i] : dw[k * kV + i];
-            __syncthreads();
-            for (int c = threadIdx.x; c < n; c += 256) {
-                float s = 0.f;
+    for (int k = 0; k < kK; ++k)
 #pragma unroll
-                for (int q = 0; q < kTeams; ++q) s += acc[q * kCols + c];
-                (pass ? pb : pw)[c] = s;
+        for (int i = 0; i < kV; ++i) {
+            const int c = (k * kWidth + lane) * kV + i, u = k * kV + i;
+            reinterpret_cast<float *>(wr)[u] = w && c < n ? w[static_cast<int64_t>(at.g) * n + c] : 1.f;
+            reinterpret_cast<float *>(acc_w)[u] = 0.f;
+            reinterpret_cast<float *>(acc_b)[u] =
+                !kBwd && b && c < n ? b[static_cast<int64_t>(at.g) * n + c] : 0.f;
+        }
+    __syncthreads();
+    const float inv = 1.f / n;
+    int64_t row = at.first * groups + at.g, o = o0;
+    float nmu = 0.f, nrs = 0.f;   // backward: the next row's mean and rstd
+    if (kBwd && turns > 0) {
+        nmu = mean[row];
+        nrs = rstd[row];
+    }
+    int t = 0, st = 0;
+    uint32_t phase = 0;
+    for (; t < turns; ++t, row += at.step * groups, o += hop) {
+        float mu = nmu, rs = nrs;
+        if (kBwd && t + 1 < turns) {
+            nmu = mean[row + at.step * groups];
+            nrs = rstd[row + at.step * groups];
+        }
+        if (!mbar_wait_bounded(bar0 + 8 * st, phase, 100000u)) lost = 1;
+        const uint8_t *buf = ring + st * kIns * pitch;
+        float2 v[kN / 2], d[kN / 2];
+        get_row<T, kV, kWidth, kN>(x, end_x, x + o, buf, lane, n, v);
+        if constexpr (kBwd) get_row<T, kV, kWidth, kN>(dy, end_d, dy + o, buf + pitch, lane, n, d);
+        float2 s = make_float2(0.f, 0.f);
+        if constexpr (kBwd) {
+            float2 s0 = s, s1 = s;
+#pragma unroll
+            for (int i = 0; i < kN / 2; ++i) {   // columns past n have d = 0 and add nothing
+                v[i] = mul2(add2(v[i], both(-mu)), both(rs));
+                acc_w[i] = fma2(d[i], v[i], acc_w[i]);
+                acc_b[i] = add2(acc_b[i], d[i]);
+                d[i] = mul2(d[i], wr[i]);
+                s0 = add2(s0, d[i]);
+                s1 = fma2(d[i], v[i], s1);
+            }
+            s = make_float2(s0.x + s0.y, s1.x + s1.y);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kN / 2; ++i) s = add2(s, v[i]);
+            s.x += s.y;
+        }
+        fence_proxy_async_smem();   // this thread's part of the last output row, before the barrier
+        if (lead)                   // the output buffer of two rows ago is read
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        if constexpr (kBwd) s = sum(s);
+        else s.x = sum(s.x);
+        if (lost) break;
+        if (lead) {
+            if (t > 0) OutRow<T>(out + o - hop, n).send(s_outs + ((t - 1) & 1) * pitch);
+            if (t + stages < turns) fetch(o + stages * hop, st);
+        }
+        if (++st == stages) {
+            st = 0;
+            phase ^= 1;
+        }
+        if constexpr (kBwd) {
+            s.x *= inv;
+            s.y *= inv;
+        } else {
+            mu = s.x * inv;
+            float2 q = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < kN / 2; ++i) {
+                v[i] = add2(v[i], both(-mu));
+                float2 e = v[i];   // columns past n are no part of the sum
+                const int c0 = ((2 * i) / kV * kWidth + lane) * kV, c1 = ((2 * i + 1) / kV * kWidth + lane) * kV;
+                if (!always((2 * i) / kV, kWidth, kV, kN) && c0 >= n) e.x = 0.f;
+                if (!always((2 * i + 1) / kV, kWidth, kV, kN) && c1 >= n) e.y = 0.f;
+                q = fma2(e, e, q);
+            }
+            rs = 1.f / sqrtf(sum(q.x + q.y) * inv + eps);
+            if (lead) {
+                if (mean) mean[row] = mu;
+                if (rstd) rstd[row] = rs;
+            }
+        }
+        uint8_t *to = outs + (t & 1) * pitch;
+        const OutRow<T> ro(out + o, n);
+        T *line = reinterpret_cast<T *>(to) + (kV > 1 ? 0 : ro.shift) + lane * kV;
+        const float2 p0 = both(rs), p1 = both(-rs * s.x), p2 = both(-rs * s.y);
+#pragma unroll
+        for (int i = 0; i < kN / 2; ++i)
+            v[i] = kBwd ? fma2(p0, d[i], fma2(p2, v[i], p1)) : fma2(mul2(v[i], p0), wr[i], acc_b[i]);
+        const float *f = reinterpret_cast<const float *>(v);
+#pragma unroll
+        for (int k = 0; k < kK; ++k) {
+            const int c = (k * kWidth + lane) * kV;
+            if (always(k, kWidth, kV, kN) || c < n) {
+                if (kV > 1 || (c >= ro.lo && c < ro.hi))
+                    store<T, kV>(line + k * kWidth * kV, f + k * kV);
+                else
+                    ro.row[c] = from_f32<T>(f[k]);
             }
         }
     }
-}
-
-// dweight and dbias of group blockIdx.y, 32 columns a CTA: 8 rows of threads walk the partial rows
-// in a fixed order.
-__global__ void __launch_bounds__(256) norm_sum_kernel(const float *part, float *dw, float *db, int parts, int groups,
-                                                       int n) {
-    __shared__ float sw[8][33], sb[8][33];
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), r = threadIdx.x / 32, g = blockIdx.y;
-    float a = 0.f, b = 0.f;
-    if (c < n)
-        for (int p = r; p < parts; p += 8) {
-            const float *row = part + (static_cast<int64_t>(p) * groups + g) * 2 * n;
-            a += row[c];
-            b += row[n + c];
-        }
-    sw[r][threadIdx.x & 31] = a;
-    sb[r][threadIdx.x & 31] = b;
+    fence_proxy_async_smem();
     __syncthreads();
-    if (r == 0 && c < n) {
-        for (int q = 1; q < 8; ++q) {
-            a += sw[q][threadIdx.x];
-            b += sb[q][threadIdx.x];
+    if (lead) {
+        if (turns > 0 && t == turns) OutRow<T>(out + o - hop, n).send(s_outs + ((turns - 1) & 1) * pitch);
+        if (lost)   // nothing may land after the CTA has ended
+            for (int i = 0; i < stages; ++i)
+                for (uint32_t q = 0; q < 2; ++q) mbar_wait_bounded(bar0 + 8 * i, q, 100000u);
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
+    if (lost && threadIdx.x == 0) atomicOr(err, kErrTimeout);
+    if (kBwd && part) {   // one partial row of dw and of db per CTA: the teams add up one after the other
+        float *fw = reinterpret_cast<float *>(sm), *fb = fw + n;
+        for (int q = 0; q < static_cast<int>(blockDim.x) / kWidth; ++q) {
+            __syncthreads();
+            if (team == q)
+#pragma unroll
+                for (int k = 0; k < kK; ++k)
+#pragma unroll
+                    for (int i = 0; i < kV; ++i) {
+                        const int c = (k * kWidth + lane) * kV + i, u = k * kV + i;
+                        const float aw = reinterpret_cast<const float *>(acc_w)[u];
+                        const float ab = reinterpret_cast<const float *>(acc_b)[u];
+                        if (c < n) {
+                            fw[c] = q ? fw[c] + aw : aw;
+                            fb[c] = q ? fb[c] + ab : ab;
+                        }
+                    }
         }
-        if (dw) dw[static_cast<int64_t>(g) * n + c] = a;
-        if (db) db[static_cast<int64_t>(g) * n + c] = b;
+        __syncthreads();
+        float *p = part + static_cast<int64_t>(blockIdx.x) * 2 * n;
+        for (int c = threadIdx.x; c < 2 * n; c += blockDim.x) p[c] = fw[c];
     }
 }
 
-// ---- rows longer than kHeld: pieces of the row per thread, read again for each use
+// dweight and dbias of group blockIdx.y, 32 columns a CTA: 32 rows of threads walk the partial rows, eight
+// loads in flight each (one at a time took 43 us for 1216 partial rows of 2048 columns), in a fixed order.
+__global__ void __launch_bounds__(1024) norm_sum_kernel(const float *part, float *dw, float *db, int parts, int groups,
+                                                        int n) {
+    __shared__ float sw[32][33], sb[32][33];
+    const int x = threadIdx.x & 31, c = blockIdx.x * 32 + x, r = threadIdx.x / 32, g = blockIdx.y;
+    float a = 0.f, b = 0.f;
+    if (c < n) {
+        const float *row = part + (static_cast<int64_t>(r) * groups + g) * 2 * n + c;
+        const int64_t step = static_cast<int64_t>(32) * groups * 2 * n;
+#pragma unroll 8
+        for (int p = r; p < parts; p += 32, row += step) {
+            a += row[0];
+            b += row[n];
+        }
+    }
+    sw[r][x] = a;
+    sb[r][x] = b;
+    __syncthreads();
+    // warp r takes column r: lane x holds the sum of its row of threads
+    a = sw[x][r];
+    b = sb[x][r];
+#pragma unroll
+    for (int off = 16; off; off >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, off);
+        b += __shfl_xor_sync(0xffffffffu, b, off);
+    }
+    const int col = blockIdx.x * 32 + r;
+    if (x == 0 && col < n) {
+        if (dw) dw[static_cast<int64_t>(g) * n + col] = a;
+        if (db) db[static_cast<int64_t>(g) * n + col] = b;
+    }
+}
+
+// ---- rows longer than kRingMostN: pieces of the row per thread, read again for each use
 template <typename T>
 __global__ void __launch_bounds__(kMaxBlock) norm_fwd_long_kernel(const T *x, const float *w, const float *b, T *y,
                                                                   float *mean, float *rstd, int groups, int n,
                                                                   float eps) {
-    TeamSum<0> sum;
+    __shared__ float2 sums[2][kMaxBlock / 32];
+    WarpsSum<kMaxBlock / 32> sum{sums, 0, 1, 0};
     const int64_t row = blockIdx.x;
     const int64_t g = row % groups;
     const T *xr = x + row * n;
     float s = 0.f, q = 0.f;
     for (int c = threadIdx.x; c < n; c += kMaxBlock) s += to_f32(xr[c]);
-    const float mu = sum(make_float2(s, 0.f)).x / n;
+    const float mu = sum(s) / n;
     for (int c = threadIdx.x; c < n; c += kMaxBlock) {
         const float d = to_f32(xr[c]) - mu;
         q = fmaf(d, d, q);
     }
-    const float rs = 1.f / sqrtf(sum(make_float2(q, 0.f)).x / n + eps);
+    const float rs = 1.f / sqrtf(sum(q) / n + eps);
     if (threadIdx.x == 0) {
         if (mean) mean[row] = mu;
         if (rstd) rstd[row] = rs;
@@ -327,8 +645,9 @@ template <typename T>
 __global__ void __launch_bounds__(kMaxBlock) norm_bwd_long_kernel(const T *dy, const T *x, const float *w,
                                                                   const float *mean, const float *rstd, T *dx,
                                                                   float *part, int64_t rows, int groups, int n) {
-    TeamSum<0> sum;
-    const Walk<0> at(groups);
+    __shared__ float2 sums[2][kMaxBlock / 32];
+    WarpsSum<kMaxBlock / 32> sum{sums, 0, 1, 0};
+    const Walk at(groups, kMaxBlock);
     float *pw = part ? part + static_cast<int64_t>(blockIdx.x) * 2 * n : nullptr;
     if (pw)
         for (int c = threadIdx.x; c < 2 * n; c += kMaxBlock) pw[c] = 0.f;
@@ -359,22 +678,45 @@ __global__ void __launch_bounds__(kMaxBlock) norm_bwd_long_kernel(const T *dy, c
 }
 
 // ------------------------------------------------------------------------------------ host side
+enum Form { kTeams, kRing, kLong };
 struct Plan {
-    int team;      // 16, 32, or 0 for the CTA
+    Form form;
+    int width;           // threads of a row's team
     int block, grid;
-    bool held;
+    int stages, pitch, smem;   // kRing: rows on the way to a team, bytes of a row's buffer, bytes of a CTA
 };
 
-// The smallest team whose registers hold the row; CTAs for every SM a few times over, a multiple of
+// The smallest team that holds the row; persistent CTAs as many as the SMs hold at once, a multiple of
 // the groups, none without a row.
-Plan plan(int64_t rows, int groups, int n) {
+Plan plan(int64_t rows, int groups, int n, kla_dtype dtype, bool bwd) {
     Plan p{};
-    p.held = n <= kHeld;
-    p.team = n <= 16 * kE ? 16 : n <= 32 * kE ? 32 : 0;
-    p.block = p.team ? 256 : p.held ? (((n + kE - 1) / kE + 31) / 32) * 32 : kMaxBlock;
-    const int64_t per_cta = p.team ? 256 / p.team : 1;
+    p.form = n <= kTeamMost ? kTeams : n <= kRingMostN ? kRing : kLong;
+    int per_sm = 1;
+    if (p.form == kTeams) {
+        p.width = n <= 16 * kE ? 16 : 32;
+        p.block = 256;
+        per_sm = bwd ? 2 : 3;
+    } else if (p.form == kRing) {
+        const int least = 32 * ring_values(bwd);   // what a warp holds
+        p.width = n <= 2 * least ? (n <= least ? 32 : 64) : n <= 4 * least ? 128 : n <= 8 * least ? 256 : 512;
+        const int most = ring_block(bwd);
+        int teams = most / p.width;
+        // teams that would have no row only cost shared memory
+        if (teams > rows) teams = static_cast<int>(rows);
+        p.block = teams * p.width;
+        per_sm = bwd ? 1 : 2;
+        p.pitch = (n * (dtype == KLA_DTYPE_BF16 ? 2 : 4) + 31) / 16 * 16;
+        const int bytes = 216 * 1024 / per_sm - 4096;
+        p.stages = (bytes / teams / p.pitch - 2) / (bwd ? 2 : 1);
+        p.stages = p.stages > kRingMost ? kRingMost : p.stages < 1 ? 1 : p.stages;
+        p.smem = teams * (p.stages * (bwd ? 2 : 1) + 2) * p.pitch;
+        if (bwd && p.smem < 8 * n) p.smem = 8 * n;   // the sums of dw and db at the end
+    } else {
+        p.width = p.block = kMaxBlock;
+    }
+    const int64_t per_cta = p.block / p.width;
     const int64_t most = (rows + per_cta - 1) / per_cta;   // CTAs of one group
-    int64_t want = (static_cast<int64_t>(kSms) * 1024 / p.block + groups - 1) / groups;
+    int64_t want = (static_cast<int64_t>(kSms) * per_sm + groups - 1) / groups;
     if (want > most) want = most;
     if (want < 1) want = 1;
     p.grid = static_cast<int>(want * groups);
@@ -410,59 +752,95 @@ int width(int n, const void *a, const void *b, const void *c) {
     return fits(kFull) ? kFull : sizeof(T) == 2 && fits(2) ? 2 : 1;
 }
 
-template <typename T, int kV>
-void run_fwd(const Plan &p, const T *x, const float *w, const float *b, T *y, float *mean, float *rstd, int64_t rows,
-             int groups, int n, float eps, cudaStream_t s) {
-    if (p.team == 16)
-        norm_fwd_kernel<T, kV, 16><<<p.grid, p.block, 0, s>>>(x, w, b, y, mean, rstd, rows, groups, n, eps);
-    else if (p.team == 32)
-        norm_fwd_kernel<T, kV, 32><<<p.grid, p.block, 0, s>>>(x, w, b, y, mean, rstd, rows, groups, n, eps);
-    else
-        norm_fwd_kernel<T, kV, 0><<<p.grid, p.block, 0, s>>>(x, w, b, y, mean, rstd, rows, groups, n, eps);
+template <typename T, int kV, int kWidth, bool kBwd>
+cudaError_t run_ring_as(const Plan &p, const T *x, const T *dy, const float *w, const float *b, T *out, float *mean,
+                        float *rstd, float *part, int64_t rows, int groups, int n, float eps, cudaStream_t s) {
+    unsigned *err = nullptr;
+    cudaError_t e = device_error_word(&err);
+    if (e != cudaSuccess) return e;
+    auto kern = norm_ring_kernel<T, kV, kWidth, kBwd>;
+    if (p.smem > 48 * 1024) {   // asked for once per device and kernel: the attribute outlasts the call
+        constexpr int kMaxDevices = 64;
+        static std::atomic<bool> done[kMaxDevices];
+        int dev = 0;
+        if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+        if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+        if (!done[dev].load(std::memory_order_acquire)) {
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 222 * 1024);
+            if (e != cudaSuccess) return e;
+            done[dev].store(true, std::memory_order_release);
+        }
+    }
+    kern<<<p.grid, p.block, p.smem, s>>>(x, dy, w, b, out, mean, rstd, part, rows, groups, n, eps, p.stages, p.pitch,
+                                         err);
+    return cudaGetLastError();
 }
-template <typename T, int kV>
-void run_bwd(const Plan &p, const T *dy, const T *x, const float *w, const float *mean, const float *rstd, T *dx,
-             float *part, int64_t rows, int groups, int n, cudaStream_t s) {
-    if (p.team == 16)
-        norm_bwd_kernel<T, kV, 16><<<p.grid, p.block, 0, s>>>(dy, x, w, mean, rstd, dx, part, rows, groups, n);
-    else if (p.team == 32)
-        norm_bwd_kernel<T, kV, 32><<<p.grid, p.block, 0, s>>>(dy, x, w, mean, rstd, dx, part, rows, groups, n);
-    else
-        norm_bwd_kernel<T, kV, 0><<<p.grid, p.block, 0, s>>>(dy, x, w, mean, rstd, dx, part, rows, groups, n);
+template <typename T, int kV, bool kBwd, typename... A>
+cudaError_t run_ring(const Plan &p, A... a) {
+    constexpr int kLeast = kBwd ? 64 : 32;   // 16 or 32 values a thread, rows from 513 values
+    if (p.width == kLeast) return run_ring_as<T, kV, kLeast, kBwd>(p, a...);
+    if (p.width == 2 * kLeast) return run_ring_as<T, kV, 2 * kLeast, kBwd>(p, a...);
+    if (p.width == 4 * kLeast) return run_ring_as<T, kV, 4 * kLeast, kBwd>(p, a...);
+    return run_ring_as<T, kV, 8 * kLeast, kBwd>(p, a...);
 }
 
-template <typename T>
-void fwd_as(const void *xv, const float *w, const float *b, void *yv, float *mean, float *rstd, int64_t rows,
-            int groups, int n, float eps, cudaStream_t s) {
-    const T *x = static_cast<const T *>(xv);
-    T *y = static_cast<T *>(yv);
-    const Plan p = plan(rows, groups, n);
-    const int v = width<T>(n, x, y, y);
-    if (!p.held)
+template <typename T, int kV>
+cudaError_t fwd_as(const Plan &p, const T *x, const float *w, const float *b, T *y, float *mean, float *rstd,
+                   int64_t rows, int groups, int n, float eps, cudaStream_t s) {
+    if (p.form == kRing)
+        return run_ring<T, kV == 16 / sizeof(T) ? kV : 1, false>(p, x, static_cast<const T *>(nullptr), w, b, y, mean,
+                                                                  rstd, static_cast<float *>(nullptr), rows, groups,
+                                                                  n, eps, s);
+    if (p.form == kLong)
         norm_fwd_long_kernel<T><<<static_cast<int>(rows * groups), kMaxBlock, 0, s>>>(x, w, b, y, mean, rstd, groups,
                                                                                      n, eps);
-    else if (v == 16 / sizeof(T))
-        run_fwd<T, 16 / sizeof(T)>(p, x, w, b, y, mean, rstd, rows, groups, n, eps, s);
-    else if (sizeof(T) == 2 && v == 2)
-        run_fwd<T, sizeof(T) == 2 ? 2 : 1>(p, x, w, b, y, mean, rstd, rows, groups, n, eps, s);
+    else if (p.width == 16)
+        norm_fwd_kernel<T, kV, 16><<<p.grid, p.block, 0, s>>>(x, w, b, y, mean, rstd, rows, groups, n, eps);
     else
-        run_fwd<T, 1>(p, x, w, b, y, mean, rstd, rows, groups, n, eps, s);
+        norm_fwd_kernel<T, kV, 32><<<p.grid, p.block, 0, s>>>(x, w, b, y, mean, rstd, rows, groups, n, eps);
+    return cudaGetLastError();
+}
+template <typename T, int kV>
+cudaError_t bwd_as(const Plan &p, const T *dy, const T *x, const float *w, const float *mean, const float *rstd,
+                   T *dx, float *part, int64_t rows, int groups, int n, cudaStream_t s) {
+    if (p.form == kRing)
+        return run_ring<T, kV == 16 / sizeof(T) ? kV : 1, true>(p, x, dy, w, static_cast<const float *>(nullptr), dx,
+                                                                 const_cast<float *>(mean),
+                                                                 const_cast<float *>(rstd), part, rows, groups, n,
+                                                                 0.f, s);
+    if (p.form == kLong)
+        norm_bwd_long_kernel<T><<<p.grid, kMaxBlock, 0, s>>>(dy, x, w, mean, rstd, dx, part, rows, groups, n);
+    else if (p.width == 16)
+        norm_bwd_kernel<T, kV, 16><<<p.grid, p.block, 0, s>>>(dy, x, w, mean, rstd, dx, part, rows, groups, n);
+    else
+        norm_bwd_kernel<T, kV, 32><<<p.grid, p.block, 0, s>>>(dy, x, w, mean, rstd, dx, part, rows, groups, n);
+    return cudaGetLastError();
+}
+
+// By type and width of access.
+template <typename T>
+cudaError_t fwd_typed(const void *xv, const float *w, const float *b, void *yv, float *mean, float *rstd,
+                      int64_t rows, int groups, int n, float eps, kla_dtype dtype, cudaStream_t s) {
+    const T *x = static_cast<const T *>(xv);
+    T *y = static_cast<T *>(yv);
+    const Plan p = plan(rows, groups, n, dtype, false);
+    const int v = width<T>(n, x, y, y);
+    if (v == 16 / sizeof(T)) return fwd_as<T, 16 / sizeof(T)>(p, x, w, b, y, mean, rstd, rows, groups, n, eps, s);
+    if (sizeof(T) == 2 && v == 2)
+        return fwd_as<T, sizeof(T) == 2 ? 2 : 1>(p, x, w, b, y, mean, rstd, rows, groups, n, eps, s);
+    return fwd_as<T, 1>(p, x, w, b, y, mean, rstd, rows, groups, n, eps, s);
 }
 template <typename T>
-void bwd_as(const void *dyv, const void *xv, const float *w, const float *mean, const float *rstd, void *dxv,
-            float *part, int64_t rows, int groups, int n, cudaStream_t s) {
+cudaError_t bwd_typed(const void *dyv, const void *xv, const float *w, const float *mean, const float *rstd,
+                      void *dxv, float *part, int64_t rows, int groups, int n, kla_dtype dtype, cudaStream_t s) {
     const T *dy = static_cast<const T *>(dyv), *x = static_cast<const T *>(xv);
     T *dx = static_cast<T *>(dxv);
-    const Plan p = plan(rows, groups, n);
+    const Plan p = plan(rows, groups, n, dtype, true);
     const int v = width<T>(n, x, dy, dx);
-    if (!p.held)
-        norm_bwd_long_kernel<T><<<p.grid, kMaxBlock, 0, s>>>(dy, x, w, mean, rstd, dx, part, rows, groups, n);
-    else if (v == 16 / sizeof(T))
-        run_bwd<T, 16 / sizeof(T)>(p, dy, x, w, mean, rstd, dx, part, rows, groups, n, s);
-    else if (sizeof(T) == 2 && v == 2)
-        run_bwd<T, sizeof(T) == 2 ? 2 : 1>(p, dy, x, w, mean, rstd, dx, part, rows, groups, n, s);
-    else
-        run_bwd<T, 1>(p, dy, x, w, mean, rstd, dx, part, rows, groups, n, s);
+    if (v == 16 / sizeof(T)) return bwd_as<T, 16 / sizeof(T)>(p, dy, x, w, mean, rstd, dx, part, rows, groups, n, s);
+    if (sizeof(T) == 2 && v == 2)
+        return bwd_as<T, sizeof(T) == 2 ? 2 : 1>(p, dy, x, w, mean, rstd, dx, part, rows, groups, n, s);
+    return bwd_as<T, 1>(p, dy, x, w, mean, rstd, dx, part, rows, groups, n, s);
 }
 
 }  // namespace
@@ -493,16 +871,16 @@ kla_status kla_layer_norm_fwd(const void *x, const float *weight, const float *b
     }
     if (rows == 0) return KLA_OK;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    if (dtype == KLA_DTYPE_BF16)
-        fwd_as<__nv_bfloat16>(x, weight, bias, y, mean, rstd, rows, groups, n, eps, cs);
-    else
-        fwd_as<float>(x, weight, bias, y, mean, rstd, rows, groups, n, eps, cs);
-    return cudaGetLastError() == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+    const cudaError_t e =
+        dtype == KLA_DTYPE_BF16
+            ? fwd_typed<__nv_bfloat16>(x, weight, bias, y, mean, rstd, rows, groups, n, eps, dtype, cs)
+            : fwd_typed<float>(x, weight, bias, y, mean, rstd, rows, groups, n, eps, dtype, cs);
+    return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
 }
 
 size_t kla_layer_norm_bwd_workspace_size(int64_t rows, int groups, int n, kla_dtype dtype) {
     if (kla::check(rows, groups, n, dtype) != KLA_OK || rows == 0) return 0;
-    return static_cast<size_t>(kla::plan(rows, groups, n).grid) * 2 * n * sizeof(float);
+    return static_cast<size_t>(kla::plan(rows, groups, n, dtype, true).grid) * 2 * n * sizeof(float);
 }
 
 kla_status kla_layer_norm_bwd(const void *dy, const void *x, const float *weight, const float *mean,
@@ -536,14 +914,15 @@ kla_status kla_layer_norm_bwd(const void *dy, const void *x, const float *weight
         return KLA_OK;
     }
     float *part = sums ? static_cast<float *>(workspace) : nullptr;
-    if (dtype == KLA_DTYPE_BF16)
-        bwd_as<__nv_bfloat16>(dy, x, weight, mean, rstd, dx, part, rows, groups, n, cs);
-    else
-        bwd_as<float>(dy, x, weight, mean, rstd, dx, part, rows, groups, n, cs);
-    if (cudaGetLastError() != cudaSuccess) return KLA_ERR_CUDA;
+    const cudaError_t e =
+        dtype == KLA_DTYPE_BF16
+            ? bwd_typed<__nv_bfloat16>(dy, x, weight, mean, rstd, dx, part, rows, groups, n, dtype, cs)
+            : bwd_typed<float>(dy, x, weight, mean, rstd, dx, part, rows, groups, n, dtype, cs);
+    if (e != cudaSuccess) return KLA_ERR_CUDA;
     if (!sums) return KLA_OK;
-    norm_sum_kernel<<<dim3((n + 31) / 32, groups), 256, 0, cs>>>(part, dweight, dbias,
-                                                                 plan(rows, groups, n).grid / groups, groups, n);
+    norm_sum_kernel<<<dim3((n + 31) / 32, groups), 1024, 0, cs>>>(part, dweight, dbias,
+                                                                 plan(rows, groups, n, dtype, true).grid / groups,
+                                                                  groups, n);
     return cudaGetLastError() == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
 }
 
