@@ -14,134 +14,236 @@ namespace kla {
 
 namespace {
 
-constexpr int kC = 32;        // tokens per chunk
+constexpr int kC = 64;        // tokens per chunk
 constexpr int kThreads = 256;
+constexpr int kPitch = kC + 4;   // rows of 64 floats, 16-byte aligned, one bank group apart
+
+struct Scans {   // up to three scans of one shape in one launch, by blockIdx.z
+    LinScan s[3];
+};
 
 __device__ __forceinline__ size_t s_index(const LinScan &p, int chain, int d, int z) {
     return static_cast<size_t>(chain) * p.dx * p.dz +
            (p.s_t ? static_cast<size_t>(z) * p.dx + d : static_cast<size_t>(d) * p.dz + z);
 }
 
-// fp32 scan of one segment of one (sequence, head) and kZ value channels: chunk by chunk, all
-// operands in shared memory as fp32. `states`: only the segment's own contribution, from zero.
-template <typename T, int kZ>
-__global__ void __launch_bounds__(kThreads) lin_scan_kernel(const LinScan p, const int states) {
-    extern __shared__ float sm[];
-    const int ld = p.dx + 1;
-    float *X = sm, *Y = X + kC * ld, *Z = Y + kC * ld, *P = Z + kC * (kZ + 1), *S = P + kC * (kC + 1);
-    float *gp = S + p.dx * (kZ + 1);   // g^0 .. g^kC
-    const int tid = threadIdx.x, nz = p.dz / kZ;
+// Four consecutive values as fp32, in one access where `whole`.
+__device__ __forceinline__ void four(const float *p, bool whole, float (&x)[4]) {
+    if (whole) {
+        const float4 v = *reinterpret_cast<const float4 *>(p);
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = p[u];
+    }
+}
+__device__ __forceinline__ void four(const __nv_bfloat16 *p, bool whole, float (&x)[4]) {
+    if (whole) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xFFFF0000u);
+        x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xFFFF0000u);
+    } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = to_f32(p[u]);
+    }
+}
+// Whether every row of a tensor can be read four values at a time.
+template <typename T>
+__device__ __forceinline__ bool fours(const T *p, const int64_t (&st)[3]) {
+    return ((reinterpret_cast<uintptr_t>(p) / sizeof(T)) | st[0] | st[1] | st[2]) % 4 == 0;
+}
+
+// kN consecutive floats of shared memory.
+template <int kN>
+__device__ __forceinline__ void take(const float *p, float (&x)[kN]) {
+    if constexpr (kN % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < kN; i += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(p + i);
+            x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) x[i] = p[i];
+    }
+}
+
+// fp32 scan of one segment of one (sequence, head) and kZ value channels, chunk by chunk. Bound by the
+// fp32 pipe: each of the products (X Y^T, P Z, X S and Y^T Z) is a 16 x 16 grid of threads with a tile of
+// registers each, fed with 16-byte loads from operands laid out along the tile (X and Y also transposed),
+// one load for eight multiply-adds. `states`: only the segment's own contribution, from zero.
+template <typename T, int kX, int kZ>
+__global__ void __launch_bounds__(kThreads) lin_scan_kernel(const __grid_constant__ Scans all, const int states) {
+    constexpr int kR = kX / 16, kU = kZ / 16;   // state rows and columns of a thread
+    constexpr int kYp = kX + 4, kZp = kZ + 4;
+    extern __shared__ __align__(16) float sm[];
+    float *Xt = sm;                    // [x][token]
+    float *Yt = Xt + kX * kPitch;      // [x][token]
+    float *Y = Yt + kX * kPitch;       // [token][x]
+    float *Z = Y + kC * kYp;           // [token][z]
+    float *Pt = Z + kC * kZp;          // [column][row]
+    float *S = Pt + kC * kPitch;       // [x][z]
+    float *gp = S + kX * kZp;          // g^0 .. g^kC
+    const LinScan &p = all.s[blockIdx.z];
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, nz = p.dz / kZ;
     const int chain = blockIdx.x / nz, z0 = (blockIdx.x % nz) * kZ, seg = blockIdx.y;
     const int b = chain / p.H, h = chain % p.H;
     const int n = lin_length(p.lengths, b, p.T);
     int t_begin;
     const int valid = lin_segment(p, seg, n, t_begin);
     const int t_stop = min(p.T, t_begin + p.seg_len);   // outputs past `valid` are zeros
-    const float g = p.decay[h];
-    if (tid <= kC) gp[tid] = powf(g, static_cast<float>(tid));
+    const bool reverse = p.reverse;
+    if (tid <= kC) gp[tid] = powf(p.decay[h], static_cast<float>(tid));
 
-    for (int i = tid; i < p.dx * kZ; i += kThreads) {
-        const int d = i / kZ, z = i % kZ;
-        float s = 0.f;
-        if (!states) {
-            if (p.nseg > 1)
-                s = p.seg_states[lin_slot(p, chain, lin_start_slot(p, seg)) + d * p.dz + z0 + z];
-            else if (p.S0)
-                s = p.S0[s_index(p, chain, d, z0 + z)];
+    float s[kR][kU];   // state rows ty * kR .., columns tx * kU ..
+#pragma unroll
+    for (int r = 0; r < kR; ++r)
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int d = ty * kR + r, z = z0 + tx * kU + u;
+            s[r][u] = 0.f;
+            if (!states && p.nseg > 1)
+                s[r][u] = p.seg_states[lin_slot(p, chain, lin_start_slot(p, seg)) + d * p.dz + z];
+            else if (!states && p.S0)
+                s[r][u] = p.S0[s_index(p, chain, d, z)];
         }
-        S[d * (kZ + 1) + z] = s;
-    }
     const T *xg = static_cast<const T *>(p.x) + b * p.xs[0] + h * p.xs[2];
     const T *yg = static_cast<const T *>(p.y) + b * p.ys[0] + h * p.ys[2];
     const T *zg = static_cast<const T *>(p.z) + b * p.zs[0] + h * p.zs[2] + z0;
-    T *og = static_cast<T *>(p.out);
+    T *og = static_cast<T *>(p.out) + (static_cast<size_t>(b) * p.T * p.H + h) * p.dz + z0;
+    const bool xw = fours(static_cast<const T *>(p.x), p.xs), yw = fours(static_cast<const T *>(p.y), p.ys);
+    const bool zw = fours(static_cast<const T *>(p.z), p.zs);
+    const int64_t x_step = p.xs[1], y_step = p.ys[1], z_step = p.zs[1], o_step = static_cast<int64_t>(p.H) * p.dz;
+    const float a_intra = p.a_intra, a_inter = p.a_inter, a_upd = p.a_upd;
 
     const int nchunk = (t_stop - t_begin + kC - 1) / kC;
     for (int ci = 0; ci < nchunk; ++ci) {
-        const int c = p.reverse ? nchunk - 1 - ci : ci;
+        const int c = reverse ? nchunk - 1 - ci : ci;
         const int t0 = t_begin + c * kC;
         const int cnt = max(0, min(kC, t_begin + valid - t0));   // valid tokens of the chunk
         if (states && cnt == 0) continue;
         __syncthreads();
-        for (int i = tid; i < kC * p.dx; i += kThreads) {   // masked tokens are read as zeros
-            const int r = i / p.dx, d = i % p.dx;
-            const bool ok = r < cnt;
-            if (!states) X[r * ld + d] = ok ? to_f32(xg[(t0 + r) * p.xs[1] + d]) : 0.f;
-            Y[r * ld + d] = ok ? to_f32(yg[(t0 + r) * p.ys[1] + d]) : 0.f;
-        }
-        for (int i = tid; i < kC * kZ; i += kThreads) {
-            const int r = i / kZ, z = i % kZ;
-            Z[r * (kZ + 1) + z] = r < cnt ? to_f32(zg[(t0 + r) * p.zs[1] + z]) : 0.f;
-        }
-        __syncthreads();
-        if (!states) {
-            const int i = tid / 8;
-            {   // P: four columns a thread
-                float a[4] = {0.f, 0.f, 0.f, 0.f};
-                const int j0 = tid % 8;
-                for (int d = 0; d < p.dx; ++d) {
-                    const float x = X[i * ld + d];
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) a[u] = fmaf(x, Y[(j0 + 8 * u) * ld + d], a[u]);
-                }
+        for (int i = tid; i < kC * (kX / 4); i += kThreads) {   // masked tokens are read as zeros
+            const int t = i % kC, d = i / kC * 4;
+            const bool ok = t < cnt;
+            float x[4] = {}, y[4] = {};
+            if (ok && !states) four(xg + (t0 + t) * x_step + d, xw, x);
+            if (ok) four(yg + (t0 + t) * y_step + d, yw, y);
+            *reinterpret_cast<float4 *>(Y + t * kYp + d) = make_float4(y[0], y[1], y[2], y[3]);
+            if (!states)
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    const int dist = p.reverse ? j0 + 8 * u - i : i - j0 - 8 * u;
-                    P[i * (kC + 1) + j0 + 8 * u] = dist >= 0 ? p.a_intra * gp[dist] * a[u] : 0.f;
+                    Xt[(d + u) * kPitch + t] = x[u];
+                    Yt[(d + u) * kPitch + t] = y[u];
+                }
+        }
+        for (int i = tid; i < kC * (kZ / 4); i += kThreads) {
+            const int t = i / (kZ / 4), z = i % (kZ / 4) * 4;
+            float v[4] = {};
+            if (t < cnt) four(zg + (t0 + t) * z_step + z, zw, v);
+            *reinterpret_cast<float4 *>(Z + t * kZp + z) = make_float4(v[0], v[1], v[2], v[3]);
+        }
+        if (!states)
+#pragma unroll
+            for (int r = 0; r < kR; ++r)
+#pragma unroll
+                for (int u = 0; u < kU; ++u) S[(ty * kR + r) * kZp + tx * kU + u] = s[r][u];
+        __syncthreads();
+        if (!states) {
+            float a[4][4] = {};
+#pragma unroll 4
+            for (int d = 0; d < kX; ++d) {
+                float x[4], y[4];
+                take<4>(Xt + d * kPitch + 4 * ty, x);
+                take<4>(Yt + d * kPitch + 4 * tx, y);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) a[i][q] = fmaf(x[i], y[q], a[i][q]);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int dist = reverse ? 4 * tx + q - 4 * ty - i : 4 * ty + i - 4 * tx - q;
+                    w[i] = dist >= 0 ? a_intra * gp[dist] * a[i][q] : 0.f;
+                }
+                *reinterpret_cast<float4 *>(Pt + (4 * tx + q) * kPitch + 4 * ty) = make_float4(w[0], w[1], w[2], w[3]);
+            }
+            __syncthreads();
+            float o[4][kU] = {}, e[4][kU] = {};
+            // a warp's eight rows: columns on the mask's side only
+            const int row0 = (tid >> 5) * 8, j0 = reverse ? row0 : 0, j1 = reverse ? kC : row0 + 8;
+#pragma unroll 4
+            for (int q = j0; q < j1; ++q) {
+                float w[4], z[kU];
+                take<4>(Pt + q * kPitch + 4 * ty, w);
+                take<kU>(Z + q * kZp + kU * tx, z);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int u = 0; u < kU; ++u) o[i][u] = fmaf(w[i], z[u], o[i][u]);
+            }
+#pragma unroll 4
+            for (int d = 0; d < kX; ++d) {
+                float x[4], z[kU];
+                take<4>(Xt + d * kPitch + 4 * ty, x);
+                take<kU>(S + d * kZp + kU * tx, z);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int u = 0; u < kU; ++u) e[i][u] = fmaf(x[i], z[u], e[i][u]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = 4 * ty + i;
+                if (t0 + t < t_stop) {
+                    const bool ok = t < cnt;
+                    const float w = ok ? a_inter * gp[reverse ? cnt - 1 - t : t + 1] : 0.f;
+                    T *dst = og + (t0 + t) * o_step + kU * tx;
+#pragma unroll
+                    for (int u = 0; u < kU; ++u) dst[u] = from_f32<T>(ok ? fmaf(w, e[i][u], o[i][u]) : 0.f);
                 }
             }
-            __syncthreads();
-            constexpr int kU = kZ / 8;
-            float o[kU] = {}, e[kU] = {};
-            const int c0 = tid % 8;
-            for (int j = 0; j < kC; ++j) {
-                const float w = P[i * (kC + 1) + j];
-#pragma unroll
-                for (int u = 0; u < kU; ++u) o[u] = fmaf(w, Z[j * (kZ + 1) + c0 + 8 * u], o[u]);
-            }
-            for (int d = 0; d < p.dx; ++d) {
-                const float x = X[i * ld + d];
-#pragma unroll
-                for (int u = 0; u < kU; ++u) e[u] = fmaf(x, S[d * (kZ + 1) + c0 + 8 * u], e[u]);
-            }
-            if (t0 + i < t_stop) {
-                const float w = i < cnt ? p.a_inter * gp[p.reverse ? cnt - 1 - i : i + 1] : 0.f;
-                T *dst = og + ((static_cast<size_t>(b) * p.T + t0 + i) * p.H + h) * p.dz + z0;
-#pragma unroll
-                for (int u = 0; u < kU; ++u)
-                    dst[c0 + 8 * u] = from_f32<T>(i < cnt ? fmaf(w, e[u], o[u]) : 0.f);
-            }
-            __syncthreads();
         }
         if (cnt > 0) {
-            for (int j = tid; j < kC * kZ; j += kThreads) {   // weights of the update, on the values
-                const int r = j / kZ;
-                const float w = r < cnt ? p.a_upd * gp[p.reverse ? r + 1 : cnt - 1 - r] : 0.f;
-                Z[r * (kZ + 1) + j % kZ] *= w;
-            }
-            __syncthreads();
             const float gn = gp[cnt];
-            for (int i = tid; i < p.dx * kZ; i += kThreads) {
-                const int d = i / kZ, z = i % kZ;
-                float s = gn * S[d * (kZ + 1) + z];
-                for (int j = 0; j < kC; ++j) s = fmaf(Y[j * ld + d], Z[j * (kZ + 1) + z], s);
-                S[d * (kZ + 1) + z] = s;
+            float upd[kR][kU] = {};
+#pragma unroll 4
+            for (int q = 0; q < kC; ++q) {
+                float y[kR], z[kU];
+                take<kR>(Y + q * kYp + kR * ty, y);
+                take<kU>(Z + q * kZp + kU * tx, z);
+                const float w = q < cnt ? gp[reverse ? q + 1 : cnt - 1 - q] : 0.f;
+#pragma unroll
+                for (int u = 0; u < kU; ++u) z[u] *= w;
+#pragma unroll
+                for (int r = 0; r < kR; ++r)
+#pragma unroll
+                    for (int u = 0; u < kU; ++u) upd[r][u] = fmaf(y[r], z[u], upd[r][u]);
             }
+#pragma unroll
+            for (int r = 0; r < kR; ++r)
+#pragma unroll
+                for (int u = 0; u < kU; ++u) s[r][u] = fmaf(gn, s[r][u], a_upd * upd[r][u]);
         }
     }
-    __syncthreads();
     if (!states && !(p.ST && seg == p.nseg - 1)) return;
-    for (int i = tid; i < p.dx * kZ; i += kThreads) {
-        const int d = i / kZ, z = i % kZ;
-        const float s = S[d * (kZ + 1) + z];
-        if (states)
-            p.seg_states[lin_slot(p, chain, seg) + d * p.dz + z0 + z] = s;
-        else
-            p.ST[s_index(p, chain, d, z0 + z)] = s;
-    }
+#pragma unroll
+    for (int r = 0; r < kR; ++r)
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int d = ty * kR + r, z = z0 + tx * kU + u;
+            if (states)
+                p.seg_states[lin_slot(p, chain, seg) + d * p.dz + z] = s[r][u];
+            else
+                p.ST[s_index(p, chain, d, z)] = s[r][u];
+        }
 }
 
-__global__ void __launch_bounds__(kThreads) lin_combine_kernel(const LinScan p) {
+__global__ void __launch_bounds__(kThreads) lin_combine_kernel(const __grid_constant__ Scans all) {
+    const LinScan &p = all.s[blockIdx.z];
     const int chain = blockIdx.x, b = chain / p.H, h = chain % p.H;
     const int i = blockIdx.y * kThreads + threadIdx.x, elems = p.dx * p.dz;
     if (i >= elems) return;
@@ -150,28 +252,57 @@ __global__ void __launch_bounds__(kThreads) lin_combine_kernel(const LinScan p) 
     const int d = p.seg_t ? i % p.dx : i / p.dz, z = p.seg_t ? i / p.dx : i % p.dz;
     float s = p.S0 ? p.S0[s_index(p, chain, d, z)] : 0.f;
     float *slot = p.seg_states + lin_slot(p, chain, 0) + i;
+    const float g_full = powf(g, static_cast<float>(p.seg_len));
     slot[static_cast<size_t>(p.nseg - 1) * elems] = s;
-    for (int k = 0; k < p.nseg - 1; ++k) {
-        int t0;
-        const int m = lin_segment(p, k, n, t0);
-        s = fmaf(powf(g, static_cast<float>(m)), s, slot[static_cast<size_t>(k) * elems]);
-        slot[static_cast<size_t>(k) * elems] = s;
+    constexpr int kAhead = 8;   // slots read before the first of them is replaced
+    for (int k = 0; k < p.nseg - 1; k += kAhead) {
+        float v[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            v[u] = k + u < p.nseg - 1 ? slot[static_cast<size_t>(k + u) * elems] : 0.f;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (k + u < p.nseg - 1) {
+                int t0;
+                const int m = lin_segment(p, k + u, n, t0);
+                s = fmaf(m == p.seg_len ? g_full : powf(g, static_cast<float>(m)), s, v[u]);
+                slot[static_cast<size_t>(k + u) * elems] = s;
+            }
     }
 }
 
-template <typename T, int kZ>
-cudaError_t launch_scan_as(const LinScan &p, cudaStream_t stream) {
-    const int bytes = (2 * kC * (p.dx + 1) + kC * (kZ + 1) + kC * (kC + 1) + p.dx * (kZ + 1) + kC + 1) * 4;
-    auto kern = lin_scan_kernel<T, kZ>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+template <typename T, int kX, int kZ>
+cudaError_t launch_scan_as(const LinScan *p, int scans, cudaStream_t stream) {
+    constexpr int kBytes =
+        (2 * kX * kPitch + kC * (kX + 4) + kC * (kZ + 4) + kC * kPitch + kX * (kZ + 4) + kC + 1) * 4;
+    auto kern = lin_scan_kernel<T, kX, kZ>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return e;
-    const int ctas = p.B * p.H * (p.dz / kZ);
-    if (p.nseg > 1) {
-        kern<<<dim3(ctas, p.nseg - 1), kThreads, bytes, stream>>>(p, 1);
-        if ((e = cudaGetLastError()) != cudaSuccess || (e = launch_lin_combine(p, stream)) != cudaSuccess) return e;
+    Scans all;
+    for (int i = 0; i < scans; ++i) all.s[i] = p[i];
+    const int ctas = p->B * p->H * (p->dz / kZ);
+    if (p->nseg > 1) {
+        kern<<<dim3(ctas, p->nseg - 1, scans), kThreads, kBytes, stream>>>(all, 1);
+        if ((e = cudaGetLastError()) != cudaSuccess || (e = launch_lin_combine(p, scans, stream)) != cudaSuccess)
+            return e;
     }
-    kern<<<dim3(ctas, p.nseg), kThreads, bytes, stream>>>(p, 0);
+    kern<<<dim3(ctas, p->nseg, scans), kThreads, kBytes, stream>>>(all, 0);
     return cudaGetLastError();
+}
+template <typename T, int kX>
+cudaError_t launch_scan_x(const LinScan *p, int scans, cudaStream_t stream) {
+    return p->dz >= 64   ? launch_scan_as<T, kX, 64>(p, scans, stream)
+           : p->dz == 32 ? launch_scan_as<T, kX, 32>(p, scans, stream)
+                         : launch_scan_as<T, kX, 16>(p, scans, stream);
+}
+template <typename T>
+cudaError_t launch_scan(const LinScan *p, int scans, cudaStream_t stream) {
+    switch (p->dx) {
+        case 128: return launch_scan_x<T, 128>(p, scans, stream);
+        case 64: return launch_scan_x<T, 64>(p, scans, stream);
+        case 32: return launch_scan_x<T, 32>(p, scans, stream);
+        default: return launch_scan_x<T, 16>(p, scans, stream);
+    }
 }
 
 // ---------------------------------------------------------------------------- single-token step
@@ -274,31 +405,28 @@ Span reach(const void *p, const int64_t *st, int B, int T, int H, int d, size_t 
                     static_cast<size_t>(H - 1) * st[2] + d) * esz);
 }
 
-// Segments of the fp32 scan: enough CTAs for every SM twice, each with four chunks or more.
-void plan(LinScan &p, int chunk, int ctas_per_chain, int want, int least) {
-    const int nchunk = (p.T + chunk - 1) / chunk;
-    const long ctas = static_cast<long>(p.B) * p.H * ctas_per_chain;
-    long n = ctas >= want ? 1 : want / ctas;
-    if (n > nchunk / least) n = nchunk / least;
-    if (n < 1) n = 1;
-    const int len = static_cast<int>((nchunk + n - 1) / n);
-    p.seg_len = (len > 0 ? len : 1) * chunk;
-    p.nseg = nchunk > 0 ? (nchunk + len - 1) / len : 1;
-}
-
 constexpr int kSms = 152;
 
 size_t seg_bytes(const LinScan &p) {
     return p.nseg > 1 ? static_cast<size_t>(p.B) * p.H * p.nseg * p.dx * p.dz * sizeof(float) : 0;
 }
 
-void plan_scan(LinScan &p) { plan(p, kC, p.dz / (p.dz < 32 ? 16 : 32), 2 * kSms, 4); }
+// Segments of the fp32 scan: CTAs for every SM twice, down to one chunk a segment.
+void plan_scan(LinScan &p, int scans) {
+    const int nchunk = (p.T + kC - 1) / kC;
+    const long ctas = static_cast<long>(p.B) * p.H * (p.dz < 64 ? 1 : p.dz / 64) * scans;
+    long n = 2 * kSms / ctas;
+    n = n > nchunk ? nchunk : n < 1 ? 1 : n;
+    const int len = n > 0 ? static_cast<int>((nchunk + n - 1) / n) : 1;
+    p.seg_len = len * kC;
+    p.nseg = nchunk > 0 ? (nchunk + len - 1) / len : 1;
+}
 
 // Scratch of `scans` scans of these sizes on whichever path they take (the tensor-core path depends on
-// alignment too): side by side on the tensor cores, one after the other in fp32.
+// alignment too); they run side by side.
 size_t scratch(LinScan p, kla_dtype dtype, int scans) {
-    plan_scan(p);
-    size_t most = seg_bytes(p);
+    plan_scan(p, scans);
+    size_t most = scans * seg_bytes(p);
     if (dtype == KLA_DTYPE_BF16 && p.dx == 128 && p.dz == 128) {
         lin_tc_plan(p, scans);
         if (scans * seg_bytes(p) > most) most = scans * seg_bytes(p);
@@ -328,15 +456,17 @@ kla_status check_sizes(int B, int T, int H, int d_k, int d_v, kla_dtype dtype, f
 
 }  // namespace
 
-cudaError_t launch_lin_combine(const LinScan &p, cudaStream_t stream) {
-    lin_combine_kernel<<<dim3(p.B * p.H, (p.dx * p.dz + kThreads - 1) / kThreads), kThreads, 0, stream>>>(p);
+cudaError_t launch_lin_combine(const LinScan *p, int scans, cudaStream_t stream) {
+    Scans all;
+    for (int i = 0; i < scans; ++i) all.s[i] = p[i];
+    lin_combine_kernel<<<dim3(p->B * p->H, (p->dx * p->dz + kThreads - 1) / kThreads, scans), kThreads, 0, stream>>>(
+        all);
     return cudaGetLastError();
 }
 
-cudaError_t launch_lin_scan(const LinScan &p, kla_dtype dtype, cudaStream_t stream) {
-    if (dtype == KLA_DTYPE_BF16)
-        return p.dz < 32 ? launch_scan_as<__nv_bfloat16, 16>(p, stream) : launch_scan_as<__nv_bfloat16, 32>(p, stream);
-    return p.dz < 32 ? launch_scan_as<float, 16>(p, stream) : launch_scan_as<float, 32>(p, stream);
+cudaError_t launch_lin_scan(const LinScan *p, int scans, kla_dtype dtype, cudaStream_t stream) {
+    return dtype == KLA_DTYPE_BF16 ? launch_scan<__nv_bfloat16>(p, scans, stream)
+                                   : launch_scan<float>(p, scans, stream);
 }
 
 }  // namespace kla
@@ -411,8 +541,8 @@ kla_status kla_linear_fwd(const void *q, const void *k, const void *v, const int
         lin_tc_plan(p, 1);
         e = launch_lin_tc(&p, 1, cs);
     } else {
-        plan_scan(p);
-        e = launch_lin_scan(p, dtype, cs);
+        plan_scan(p, 1);
+        e = launch_lin_scan(&p, 1, dtype, cs);
     }
     return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
 }
@@ -467,24 +597,28 @@ kla_status kla_linear_bwd(const void *q, const void *k, const void *v, const voi
         p.a_intra = q_scale;
         p.a_inter = reverse ? 1.0f : q_scale;
         p.a_upd = reverse ? q_scale : 1.0f;
-        p.seg_states = static_cast<float *>(workspace);
         return p;
     };
     LinScan p[3] = {set(k, ks, q, qs, dO, os, dv, dS_T, dS0, 0, d_k, d_v, 1),
                     set(v, vs, dO, os, q, qs, dk, dS_T, nullptr, 1, d_v, d_k, 1),
                     set(dO, os, v, vs, k, ks, dq, S0, nullptr, 1, d_v, d_k, 0)};
-    if (lin_tc_supports(p[0], dtype) && lin_tc_supports(p[1], dtype) && lin_tc_supports(p[2], dtype)) {
-        for (int i = 0; i < 3; ++i) {
-            lin_tc_plan(p[i], 3);
-            p[i].seg_states += i * seg_bytes(p[i]) / sizeof(float);
-        }
-        return launch_lin_tc(p, 3, cs) == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
-    }
+    const bool tc = lin_tc_supports(p[0], dtype) && lin_tc_supports(p[1], dtype) && lin_tc_supports(p[2], dtype);
+    float *scratch = static_cast<float *>(workspace);
     for (int i = 0; i < 3; ++i) {
-        plan_scan(p[i]);
-        if (launch_lin_scan(p[i], dtype, cs) != cudaSuccess) return KLA_ERR_CUDA;
+        tc ? lin_tc_plan(p[i], 3) : plan_scan(p[i], 3);
+        p[i].seg_states = scratch;
+        scratch += seg_bytes(p[i]) / sizeof(float);
     }
-    return KLA_OK;
+    cudaError_t e;
+    if (tc) {
+        e = launch_lin_tc(p, 3, cs);
+    } else if (d_k == d_v) {
+        e = launch_lin_scan(p, 3, dtype, cs);
+    } else {   // dv's state is the transpose of the others'
+        e = launch_lin_scan(p, 1, dtype, cs);
+        if (e == cudaSuccess) e = launch_lin_scan(p + 1, 2, dtype, cs);
+    }
+    return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
 }
 
 kla_status kla_linear_step(const void *q, const void *k, const void *v, const float *decay, const int *parent,

@@ -56,7 +56,7 @@ __device__ __forceinline__ size_t lin_slot(const LinScan &p, int chain, int k) {
 __device__ __forceinline__ int lin_start_slot(const LinScan &p, int seg) { return seg > 0 ? seg - 1 : p.nseg - 1; }
 
 // Turns the contributions into start states.
-cudaError_t launch_lin_combine(const LinScan &p, cudaStream_t stream);
+cudaError_t launch_lin_combine(const LinScan *p, int scans, cudaStream_t stream);
 // Tensor-core form: bf16, dx = dz = 128, rows that TMA can read (kla_linear_tc.cu). Runs up to three
 // scans of the same sizes side by side in one launch, each with segments (and a scratch) of its own.
 bool lin_tc_supports(const LinScan &p, kla_dtype dtype);
@@ -64,6 +64,6 @@ void lin_tc_plan(LinScan &p, int scans);
 cudaError_t launch_lin_tc(const LinScan *p, int scans, cudaStream_t stream);
 cudaError_t device_error_word(unsigned **out);   // kla_api.cu
 // Any size, type, stride and alignment, fp32 arithmetic (kla_linear.cu).
-cudaError_t launch_lin_scan(const LinScan &p, kla_dtype dtype, cudaStream_t stream);
+cudaError_t launch_lin_scan(const LinScan *p, int scans, kla_dtype dtype, cudaStream_t stream);
 
 }  // namespace kla

@@ -696,8 +696,9 @@ cudaError_t launch_lin_tc(const LinScan *p, int scans, cudaStream_t stream) {
     if (nseg > 1) {
         lin_tc_kernel<true><<<dim3(chains * scans, nseg - 1), kThreads, SMEM_BYTES, stream>>>(tp);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        for (int i = 0; i < scans; ++i)
-            if ((e = launch_lin_combine(tp.job[i].p, stream)) != cudaSuccess) return e;
+        LinScan all[3];
+        for (int i = 0; i < scans; ++i) all[i] = tp.job[i].p;
+        if ((e = launch_lin_combine(all, scans, stream)) != cudaSuccess) return e;
     }
     lin_tc_kernel<false><<<dim3(chains * scans, nseg), kThreads, SMEM_BYTES, stream>>>(tp);
     return cudaGetLastError();
