@@ -96,6 +96,8 @@ def _declare(lib):
 def lib():
     """Load libkla_gb300.so once; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = library_path()

@@ -94,6 +94,8 @@ __global__ void __launch_bounds__(kThreads) lin_scan_kernel(const __grid_constan
     const int t_stop = min(p.T, t_begin + p.seg_len);   // outputs past `valid` are zeros
     const bool reverse = p.reverse;
     if (tid <= kC) gp[tid] = powf(p.decay[h], static_cast<float>(tid));
+    dependency_release();
+    dependency_wait();   // the start states
 
     float s[kR][kU];   // state rows ty * kR .., columns tx * kU ..
 #pragma unroll
@@ -244,6 +246,8 @@ __global__ void __launch_bounds__(kThreads) lin_scan_kernel(const __grid_constan
 
 __global__ void __launch_bounds__(kThreads) lin_combine_kernel(const __grid_constant__ Scans all) {
     const LinScan &p = all.s[blockIdx.z];
+    dependency_release();
+    dependency_wait();
     const int chain = blockIdx.x, b = chain / p.H, h = chain % p.H;
     const int i = blockIdx.y * kThreads + threadIdx.x, elems = p.dx * p.dz;
     if (i >= elems) return;
@@ -285,8 +289,9 @@ cudaError_t launch_scan_as(const LinScan *p, int scans, cudaStream_t stream) {
         kern<<<dim3(ctas, p->nseg - 1, scans), kThreads, kBytes, stream>>>(all, 1);
         if ((e = cudaGetLastError()) != cudaSuccess || (e = launch_lin_combine(p, scans, stream)) != cudaSuccess)
             return e;
+        return launch_dependent(kern, dim3(ctas, p->nseg, scans), kThreads, kBytes, stream, all, 0);
     }
-    kern<<<dim3(ctas, p->nseg, scans), kThreads, kBytes, stream>>>(all, 0);
+    kern<<<dim3(ctas, 1, scans), kThreads, kBytes, stream>>>(all, 0);
     return cudaGetLastError();
 }
 template <typename T, int kX>
@@ -412,7 +417,8 @@ size_t seg_bytes(const LinScan &p) {
 }
 
 // Segments of the fp32 scan: CTAs for every SM twice, down to one chunk a segment.
-void plan_scan(LinScan &p, int scans) {
+void plan_scan(LinScan &p, kla_dtype dtype, int scans) {
+    if (dtype == KLA_DTYPE_BF16 && p.dx == 128 && p.dz == 128) return lin_tc_plan(p, scans);   // one scratch size
     const int nchunk = (p.T + kC - 1) / kC;
     const long ctas = static_cast<long>(p.B) * p.H * (p.dz < 64 ? 1 : p.dz / 64) * scans;
     long n = 2 * kSms / ctas;
@@ -422,16 +428,10 @@ void plan_scan(LinScan &p, int scans) {
     p.nseg = nchunk > 0 ? (nchunk + len - 1) / len : 1;
 }
 
-// Scratch of `scans` scans of these sizes on whichever path they take (the tensor-core path depends on
-// alignment too); they run side by side.
+// Scratch of `scans` scans of these sizes, which run side by side.
 size_t scratch(LinScan p, kla_dtype dtype, int scans) {
-    plan_scan(p, scans);
-    size_t most = scans * seg_bytes(p);
-    if (dtype == KLA_DTYPE_BF16 && p.dx == 128 && p.dz == 128) {
-        lin_tc_plan(p, scans);
-        if (scans * seg_bytes(p) > most) most = scans * seg_bytes(p);
-    }
-    return most;
+    plan_scan(p, dtype, scans);
+    return scans * seg_bytes(p);
 }
 
 void set_strides(int64_t (&to)[3], const int64_t *from, int T, int H, int d) {
@@ -459,9 +459,8 @@ kla_status check_sizes(int B, int T, int H, int d_k, int d_v, kla_dtype dtype, f
 cudaError_t launch_lin_combine(const LinScan *p, int scans, cudaStream_t stream) {
     Scans all;
     for (int i = 0; i < scans; ++i) all.s[i] = p[i];
-    lin_combine_kernel<<<dim3(p->B * p->H, (p->dx * p->dz + kThreads - 1) / kThreads, scans), kThreads, 0, stream>>>(
-        all);
-    return cudaGetLastError();
+    return launch_dependent(lin_combine_kernel, dim3(p->B * p->H, (p->dx * p->dz + kThreads - 1) / kThreads, scans),
+                            kThreads, 0, stream, all);
 }
 
 cudaError_t launch_lin_scan(const LinScan *p, int scans, kla_dtype dtype, cudaStream_t stream) {
@@ -537,13 +536,8 @@ kla_status kla_linear_fwd(const void *q, const void *k, const void *v, const int
     p.a_upd = 1.0f;
     p.seg_states = static_cast<float *>(workspace);
     cudaError_t e;
-    if (lin_tc_supports(p, dtype)) {
-        lin_tc_plan(p, 1);
-        e = launch_lin_tc(&p, 1, cs);
-    } else {
-        plan_scan(p, 1);
-        e = launch_lin_scan(&p, 1, dtype, cs);
-    }
+    plan_scan(p, dtype, 1);
+    e = lin_tc_supports(p, dtype) ? launch_lin_tc(&p, 1, cs) : launch_lin_scan(&p, 1, dtype, cs);
     return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
 }
 
@@ -605,7 +599,7 @@ kla_status kla_linear_bwd(const void *q, const void *k, const void *v, const voi
     const bool tc = lin_tc_supports(p[0], dtype) && lin_tc_supports(p[1], dtype) && lin_tc_supports(p[2], dtype);
     float *scratch = static_cast<float *>(workspace);
     for (int i = 0; i < 3; ++i) {
-        tc ? lin_tc_plan(p[i], 3) : plan_scan(p[i], 3);
+        plan_scan(p[i], dtype, 3);
         p[i].seg_states = scratch;
         scratch += seg_bytes(p[i]) / sizeof(float);
     }

@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
             if (!kStates) load_x(c);
         }
     }
+    dependency_release();
     if (tid <= kC) sm.gp[tid] = powf(g, static_cast<float>(tid));
     if (tid < 64) {
         const int dist = p.reverse ? tid - 32 : 32 - tid;
@@ -173,6 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    dependency_wait();   // the start states; inputs were there before the call's first launch
     const uint32_t tbase = sm.tmem_base;
     const uint32_t tlane = tbase + (static_cast<uint32_t>((warp & 3) * 32) << 16);
 
@@ -700,7 +702,9 @@ cudaError_t launch_lin_tc(const LinScan *p, int scans, cudaStream_t stream) {
         for (int i = 0; i < scans; ++i) all[i] = tp.job[i].p;
         if ((e = launch_lin_combine(all, scans, stream)) != cudaSuccess) return e;
     }
-    lin_tc_kernel<false><<<dim3(chains * scans, nseg), kThreads, SMEM_BYTES, stream>>>(tp);
+    if (nseg > 1)
+        return launch_dependent(lin_tc_kernel<false>, dim3(chains * scans, nseg), kThreads, SMEM_BYTES, stream, tp);
+    lin_tc_kernel<false><<<chains * scans, kThreads, SMEM_BYTES, stream>>>(tp);
     return cudaGetLastError();
 }
 

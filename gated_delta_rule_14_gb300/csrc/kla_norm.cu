@@ -219,6 +219,7 @@ template <typename T, int kV, int kTeam>
 __global__ void __launch_bounds__(256)
 norm_bwd_kernel(const T *dy, const T *x, const float *w, const float *mean, const float *rstd, T *dx, float *part,
                 int64_t rows, int groups, int n) {
+    dependency_release();
     constexpr int kK = kE / kV;
     const Walk at(groups, kTeam);
     float wr[kE], dw[kE], db[kE];
@@ -409,6 +410,7 @@ __global__ void __launch_bounds__(ring_block(kBwd), kBwd ? 1 : 2)
 norm_ring_kernel(const T *x, const T *dy, const float *w, const float *b, T *out, float *mean, float *rstd,
                  float *part, int64_t rows, int groups, int n, float eps, int stages, int pitch, unsigned *err) {
     using namespace ptx;
+    dependency_release();
     constexpr int kN = ring_values(kBwd), kK = kN / kV, kIns = kBwd ? 2 : 1;
     extern __shared__ __align__(128) uint8_t sm[];
     __shared__ uint64_t full[ring_block(kBwd) / kWidth][kRingMost];
@@ -584,6 +586,7 @@ norm_ring_kernel(const T *x, const T *dy, const float *w, const float *b, T *out
 __global__ void __launch_bounds__(1024) norm_sum_kernel(const float *part, float *dw, float *db, int parts, int groups,
                                                         int n) {
     __shared__ float sw[32][33], sb[32][33];
+    dependency_wait();
     const int x = threadIdx.x & 31, c = blockIdx.x * 32 + x, r = threadIdx.x / 32, g = blockIdx.y;
     float a = 0.f, b = 0.f;
     if (c < n) {
@@ -920,10 +923,10 @@ kla_status kla_layer_norm_bwd(const void *dy, const void *x, const float *weight
             : bwd_typed<float>(dy, x, weight, mean, rstd, dx, part, rows, groups, n, dtype, cs);
     if (e != cudaSuccess) return KLA_ERR_CUDA;
     if (!sums) return KLA_OK;
-    norm_sum_kernel<<<dim3((n + 31) / 32, groups), 1024, 0, cs>>>(part, dweight, dbias,
-                                                                 plan(rows, groups, n, dtype, true).grid / groups,
-                                                                  groups, n);
-    return cudaGetLastError() == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+    return launch_dependent(norm_sum_kernel, dim3((n + 31) / 32, groups), 1024, 0, cs, part, dweight, dbias,
+                            plan(rows, groups, n, dtype, true).grid / groups, groups, n) == cudaSuccess
+               ? KLA_OK
+               : KLA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -4,11 +4,14 @@ with its gradients (``layer_norm_fwd``, ``layer_norm_bwd``) and beam search's se
 following their beams (``beam_select``, ``reorder_states``).
 
 The binding checks and marshals; every operation runs in this package's CUDA kernels on the current
-stream of the tensors' device.
+stream of the tensors' device. Small calls are bound by the host, so each function first asks in one
+expression whether everything is as it should be, and only where it is not goes through the arguments
+one by one to name the one at fault.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Tuple
 
 import torch
@@ -28,16 +31,19 @@ def _code(name: str, t: torch.Tensor) -> int:
 
 
 def _check(name: str, t: torch.Tensor, shape, dtype, device, contiguous: bool = True) -> None:
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device.index and (
+                not contiguous or t.is_contiguous()):
+            return
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
+    if t.shape != tuple(shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device} (got {t.device})")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _device(name: str, t: torch.Tensor) -> torch.device:
@@ -56,6 +62,12 @@ def _stream(device: torch.device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+@functools.lru_cache(maxsize=256)
+def _size(query: str, *sizes) -> int:
+    """Scratch bytes of a call: they follow from its sizes alone."""
+    return getattr(_native.lib(), f"kla_{query}_workspace_size")(*sizes)
+
+
 def _scratch(need: int, given: Optional[torch.Tensor], device: torch.device) -> Tuple[Optional[torch.Tensor], int]:
     if given is None:
         return (torch.empty(need, dtype=torch.uint8, device=device), need) if need else (None, 0)
@@ -65,9 +77,7 @@ def _scratch(need: int, given: Optional[torch.Tensor], device: torch.device) -> 
 
 
 def _token_strides(kind, *tensors):
-    """None for contiguous tensors, else their batch, token and head strides; the last axis is dense."""
-    if all(t.is_contiguous() for t in tensors):
-        return None
+    """Batch, token and head strides of tensors whose last axis is dense."""
     out = []
     for t in tensors:
         st = t.stride()
@@ -81,28 +91,37 @@ def _token_strides(kind, *tensors):
 
 
 def _linear_shapes(q, k, v, decay, S0, lengths):
-    device = _device("q", q)
-    code = _code("q", q)
-    if q.dim() != 4 or not isinstance(v, torch.Tensor) or v.dim() != 4:
-        raise ValueError("q and k must be [B, T, H, d_k] and v [B, T, H, d_v]")
-    B, T, H, d_k = q.shape
+    """Sizes of the call, and whether q, k and v are contiguous and v is shaped like q."""
+    try:
+        shape, dtype, at = q.shape, q.dtype, q.get_device()
+        alike = (at >= 0 and len(shape) == 4 and k.shape == shape and v.shape == shape and k.dtype is dtype and
+                 v.dtype is dtype and k.get_device() == at and v.get_device() == at and q.is_contiguous() and
+                 k.is_contiguous() and v.is_contiguous() and decay.dtype is _F32 and decay.shape == shape[2:3] and
+                 decay.get_device() == at and decay.is_contiguous() and dtype in _CODE)
+    except AttributeError:
+        alike = False
+    if not alike:
+        device = _device("q", q)
+        _code("q", q)
+        if q.dim() != 4 or not isinstance(v, torch.Tensor) or v.dim() != 4:
+            raise ValueError("q and k must be [B, T, H, d_k] and v [B, T, H, d_v]")
+        _check("k", k, q.shape, q.dtype, device, False)
+        _check("v", v, (*q.shape[:3], v.shape[3]), q.dtype, device, False)
+        _check("decay", decay, q.shape[2:3], _F32, device)
+    device = q.device
+    B, T, H, d_k = shape
     d_v = v.shape[3]
-    _check("k", k, q.shape, q.dtype, device, False)
-    _check("v", v, (B, T, H, d_v), q.dtype, device, False)
-    _check("decay", decay, (H,), _F32, device)
     if S0 is not None:
         _check("S0", S0, (B, H, d_k, d_v), _F32, device)
     if lengths is not None:
         _check("lengths", lengths, (B,), torch.int32, device)
-    return device, code, B, T, H, d_k, d_v
+    return device, _CODE[dtype], B, T, H, d_k, d_v, alike
 
 
 def linear_workspace_size(B: int, T: int, H: int, d_k: int, d_v: int, dtype: torch.dtype = _BF16,
                           backward: bool = False) -> int:
     """Device scratch bytes ``linear_fwd`` (or ``linear_bwd``) needs for these sizes."""
-    lib = _native.lib()
-    f = lib.kla_linear_bwd_workspace_size if backward else lib.kla_linear_fwd_workspace_size
-    return f(B, T, H, d_k, d_v, _CODE[dtype])
+    return _size("linear_bwd" if backward else "linear_fwd", B, T, H, d_k, d_v, _CODE[dtype])
 
 
 def linear_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: torch.Tensor,
@@ -117,20 +136,20 @@ def linear_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: torch.T
     (int32 [B]) masks the tokens from lengths[b] on: they leave the state alone and their outputs are 0.
     Returns (o [B,T,H,d_v] in q's dtype, S_T fp32 or None); ``S_T`` may be passed, and may be ``S0``.
     """
-    device, code, B, T, H, d_k, d_v = _linear_shapes(q, k, v, decay, S0, lengths)
+    device, code, B, T, H, d_k, d_v, dense = _linear_shapes(q, k, v, decay, S0, lengths)
     if out is None:
-        out = torch.empty((B, T, H, d_v), dtype=q.dtype, device=device)
+        out = torch.empty_like(v) if dense else torch.empty((B, T, H, d_v), dtype=q.dtype, device=device)
     else:
         _check("out", out, (B, T, H, d_v), q.dtype, device)
     if S_T is not None:
         _check("S_T", S_T, (B, H, d_k, d_v), _F32, device)
     elif final_state:
         S_T = torch.empty((B, H, d_k, d_v), dtype=_F32, device=device)
-    lib = _native.lib()
-    workspace, size = _scratch(lib.kla_linear_fwd_workspace_size(B, T, H, d_k, d_v, code), workspace, device)
-    st = lib.kla_linear_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _token_strides(_Strides3, q, k, v),
-                            decay.data_ptr(), _ptr(lengths), _ptr(S0), out.data_ptr(), _ptr(S_T), B, T, H, d_k, d_v,
-                            code, q_scale, _ptr(workspace), size, _stream(device))
+    workspace, size = _scratch(_size("linear_fwd", B, T, H, d_k, d_v, code), workspace, device)
+    st = _native.lib().kla_linear_fwd(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), None if dense else _token_strides(_Strides3, q, k, v),
+        decay.data_ptr(), _ptr(lengths), _ptr(S0), out.data_ptr(), _ptr(S_T), B, T, H, d_k, d_v, code, q_scale,
+        _ptr(workspace), size, _stream(device))
     if st:
         _native.check(st, "kla_linear_fwd")
     return out, S_T
@@ -145,19 +164,20 @@ def linear_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: torch.T
     Returns dq, dk [B,T,H,d_k] and dv [B,T,H,d_v] in q's dtype (zero at masked tokens) and dS0 fp32
     [B,H,d_k,d_v] (None unless ``want_dS0``). ``decay`` is a constant and gets no gradient.
     """
-    device, code, B, T, H, d_k, d_v = _linear_shapes(q, k, v, decay, S0, lengths)
+    device, code, B, T, H, d_k, d_v, dense = _linear_shapes(q, k, v, decay, S0, lengths)
     _check("dO", dO, (B, T, H, d_v), q.dtype, device, False)
+    dense = dense and dO.is_contiguous()
     if dS_T is not None:
         _check("dS_T", dS_T, (B, H, d_k, d_v), _F32, device)
     dq = torch.empty((B, T, H, d_k), dtype=q.dtype, device=device)
     dk, dv = torch.empty_like(dq), torch.empty((B, T, H, d_v), dtype=q.dtype, device=device)
     dS0 = torch.empty((B, H, d_k, d_v), dtype=_F32, device=device) if want_dS0 else None
-    lib = _native.lib()
-    workspace, size = _scratch(lib.kla_linear_bwd_workspace_size(B, T, H, d_k, d_v, code), workspace, device)
-    st = lib.kla_linear_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), dO.data_ptr(),
-                            _token_strides(_Strides4, q, k, v, dO), decay.data_ptr(), _ptr(lengths), _ptr(S0),
-                            _ptr(dS_T), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(dS0), B, T, H, d_k, d_v,
-                            code, q_scale, _ptr(workspace), size, _stream(device))
+    workspace, size = _scratch(_size("linear_bwd", B, T, H, d_k, d_v, code), workspace, device)
+    st = _native.lib().kla_linear_bwd(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), dO.data_ptr(),
+        None if dense else _token_strides(_Strides4, q, k, v, dO), decay.data_ptr(), _ptr(lengths), _ptr(S0),
+        _ptr(dS_T), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(dS0), B, T, H, d_k, d_v, code, q_scale,
+        _ptr(workspace), size, _stream(device))
     if st:
         _native.check(st, "kla_linear_bwd")
     return {"dq": dq, "dk": dk, "dv": dv, "dS0": dS0}
@@ -173,16 +193,26 @@ def linear_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: torch.
     states; an index outside of them starts from zeros) and its new state goes to ``S_out[b]``, which is then
     required: a beam search's states follow their beams without a pass of their own. Returns o [B,H,d_v].
     """
-    device = _device("q", q)
-    code = _code("q", q)
-    if q.dim() != 3 or not isinstance(v, torch.Tensor) or v.dim() != 3:
-        raise ValueError("q and k must be [B, H, d_k] and v [B, H, d_v]")
-    B, H, d_k = q.shape
-    d_v = v.shape[2]
-    _check("q", q, q.shape, q.dtype, device)
-    _check("k", k, q.shape, q.dtype, device)
-    _check("v", v, (B, H, d_v), q.dtype, device)
-    _check("decay", decay, (H,), _F32, device)
+    try:
+        shape, dtype, at = q.shape, q.dtype, q.get_device()
+        B, H, d_k = shape
+        d_v = v.shape[2]
+        ok = (at >= 0 and k.shape == shape and v.shape[:2] == shape[:2] and k.dtype is dtype and v.dtype is dtype and
+              k.get_device() == at and v.get_device() == at and q.is_contiguous() and k.is_contiguous() and
+              v.is_contiguous() and decay.dtype is _F32 and decay.shape == shape[1:2] and decay.get_device() == at and
+              decay.is_contiguous() and dtype in _CODE)
+    except (AttributeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        device = _device("q", q)
+        _code("q", q)
+        if q.dim() != 3 or not isinstance(v, torch.Tensor) or v.dim() != 3:
+            raise ValueError("q and k must be [B, H, d_k] and v [B, H, d_v]")
+        _check("q", q, q.shape, q.dtype, device)
+        _check("k", k, q.shape, q.dtype, device)
+        _check("v", v, (*q.shape[:2], v.shape[2]), q.dtype, device)
+        _check("decay", decay, q.shape[1:2], _F32, device)
+    device = q.device
     n = B
     if parent is not None:
         _check("parent", parent, (B,), torch.int32, device)
@@ -195,12 +225,12 @@ def linear_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: torch.
     else:
         _check("S_out", S_out, (B, H, d_k, d_v), _F32, device)
     if out is None:
-        out = torch.empty((B, H, d_v), dtype=q.dtype, device=device)
+        out = torch.empty_like(v)
     else:
-        _check("out", out, (B, H, d_v), q.dtype, device)
+        _check("out", out, v.shape, dtype, device)
     st = _native.lib().kla_linear_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), _ptr(parent),
-                                       S.data_ptr(), S_out.data_ptr(), out.data_ptr(), B, H, d_k, d_v, n, code,
-                                       q_scale, _stream(device))
+                                       S.data_ptr(), S_out.data_ptr(), out.data_ptr(), B, H, d_k, d_v, n,
+                                       _CODE[dtype], q_scale, _stream(device))
     if st:
         _native.check(st, "kla_linear_step")
     return out
@@ -215,14 +245,12 @@ def _norm_shape(x: torch.Tensor, weight, bias):
         raise ValueError("x must have an axis to normalise")
     param = weight if weight is not None else bias
     n = x.shape[-1]
-    groups = 1
     if param is not None and param.dim() == 2:
         if x.dim() < 2:
             raise ValueError("weights of two axes need an x of two axes or more")
         groups = x.shape[-2]
-    shape = (groups, n) if param is not None and param.dim() == 2 else (n,)
-    rows = x.numel() // (groups * n) if groups * n else 0
-    return rows, groups, n, shape
+        return x.numel() // max(1, groups * n), groups, n, (groups, n)
+    return x.numel() // max(1, n), 1, n, (n,)
 
 
 def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
@@ -236,7 +264,8 @@ def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias:
     device = _device("x", x)
     code = _code("x", x)
     rows, groups, n, shape = _norm_shape(x, weight, bias)
-    _check("x", x, x.shape, x.dtype, device)
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
     if weight is not None:
         _check("weight", weight, shape, _F32, device)
     if bias is not None:
@@ -248,7 +277,7 @@ def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias:
     mean = rstd = None
     if stats:
         mean = torch.empty(x.shape[:-1], dtype=_F32, device=device)
-        rstd = torch.empty(x.shape[:-1], dtype=_F32, device=device)
+        rstd = torch.empty_like(mean)
     st = _native.lib().kla_layer_norm_fwd(x.data_ptr(), _ptr(weight), _ptr(bias), out.data_ptr(), _ptr(mean),
                                           _ptr(rstd), rows, groups, n, code, eps, _stream(device))
     if st:
@@ -263,7 +292,8 @@ def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Ten
     device = _device("x", x)
     code = _code("x", x)
     rows, groups, n, shape = _norm_shape(x, weight, None)
-    _check("x", x, x.shape, x.dtype, device)
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
     _check("dy", dy, x.shape, x.dtype, device)
     if weight is not None:
         _check("weight", weight, shape, _F32, device)
@@ -271,12 +301,11 @@ def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Ten
     _check("rstd", rstd, x.shape[:-1], _F32, device)
     dx = torch.empty_like(x)
     dw = torch.empty(shape, dtype=_F32, device=device)
-    db = torch.empty(shape, dtype=_F32, device=device)
-    lib = _native.lib()
-    workspace, size = _scratch(lib.kla_layer_norm_bwd_workspace_size(rows, groups, n, code), workspace, device)
-    st = lib.kla_layer_norm_bwd(dy.data_ptr(), x.data_ptr(), _ptr(weight), mean.data_ptr(), rstd.data_ptr(),
-                                dx.data_ptr(), dw.data_ptr(), db.data_ptr(), rows, groups, n, code, _ptr(workspace),
-                                size, _stream(device))
+    db = torch.empty_like(dw)
+    workspace, size = _scratch(_size("layer_norm_bwd", rows, groups, n, code), workspace, device)
+    st = _native.lib().kla_layer_norm_bwd(dy.data_ptr(), x.data_ptr(), _ptr(weight), mean.data_ptr(),
+                                          rstd.data_ptr(), dx.data_ptr(), dw.data_ptr(), db.data_ptr(), rows, groups,
+                                          n, code, _ptr(workspace), size, _stream(device))
     if st:
         _native.check(st, "kla_layer_norm_bwd")
     return dx, dw, db
@@ -309,15 +338,14 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, finished: Optional[t
     _check("scores", scores, (B, W), _F32, device)
     if finished is not None:
         _check("finished", finished, (B, W), torch.bool, device)
-    new_scores = torch.empty((B, W), dtype=_F32, device=device)
+    new_scores = torch.empty_like(scores)
     parents = torch.empty((B, W), dtype=torch.int32, device=device)
-    tokens = torch.empty((B, W), dtype=torch.int32, device=device)
+    tokens = torch.empty_like(parents)
     done = torch.empty((B, W), dtype=torch.bool, device=device)
-    lib = _native.lib()
-    workspace, size = _scratch(lib.kla_beam_select_workspace_size(B, W, V, code), workspace, device)
-    st = lib.kla_beam_select(logits.data_ptr(), stride, scores.data_ptr(), _ptr(finished), eos,
-                             new_scores.data_ptr(), parents.data_ptr(), tokens.data_ptr(), done.data_ptr(), B, W, V,
-                             code, _ptr(workspace), size, _stream(device))
+    workspace, size = _scratch(_size("beam_select", B, W, V, code), workspace, device)
+    st = _native.lib().kla_beam_select(logits.data_ptr(), stride, scores.data_ptr(), _ptr(finished), eos,
+                                       new_scores.data_ptr(), parents.data_ptr(), tokens.data_ptr(),
+                                       done.data_ptr(), B, W, V, code, _ptr(workspace), size, _stream(device))
     if st:
         _native.check(st, "kla_beam_select")
     return new_scores, parents, tokens, done
@@ -330,13 +358,15 @@ def reorder_states(S: torch.Tensor, parents: torch.Tensor, *, out: Optional[torc
     device = _device("S", S)
     if S.dim() < 3:
         raise ValueError("S must be [B, W, ...]")
-    _check("S", S, S.shape, S.dtype, device)
-    B, W = S.shape[:2]
+    if not S.is_contiguous():
+        raise ValueError("S must be contiguous")
+    shape = S.shape
+    B, W = shape[:2]
     _check("parents", parents, (B, W), torch.int32, device)
     if out is None:
         out = torch.empty_like(S)
     else:
-        _check("out", out, S.shape, S.dtype, device)
+        _check("out", out, shape, S.dtype, device)
     st = _native.lib().kla_reorder_states(S.data_ptr(), parents.data_ptr(), out.data_ptr(), B, W,
                                           S.stride(1) * S.element_size(), _stream(device))
     if st:
