@@ -32,6 +32,7 @@
 
 #include "kla_linear.cuh"
 #include "sm103_ptx.cuh"
+#include "warp_mma.cuh"
 
 namespace kla {
 namespace {
@@ -64,6 +65,7 @@ struct Small {
     volatile int abort;
     float gp[kC + 1];              // g^0 .. g^128
     float diag[64];                // a_intra g^distance at 32 + column - row of a diagonal 32 x 32 block, 0 off the mask
+    uint32_t keep[64];             // the mask of that column and its right neighbour, as bf16 pairs
     alignas(16) float near[32];    // g^distance of a block's columns from its side near the diagonal
     alignas(16) uint2 w[kC / 2];   // weights of the keys, two tokens each: bf16 pairs of w and of what w lacks
 };
@@ -79,11 +81,6 @@ struct TcParams {
     unsigned *err;
 };
 
-__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t addr) {
-    unsigned short v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
-    return v;
-}
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -165,6 +162,8 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     if (tid < 64) {
         const int dist = p.reverse ? tid - 32 : 32 - tid;
         sm.diag[tid] = dist >= 0 ? p.a_intra * powf(g, static_cast<float>(dist)) : 0.f;
+        const int next = p.reverse ? dist + 1 : dist - 1;
+        sm.keep[tid] = (dist >= 0 ? 0xFFFFu : 0u) | (next >= 0 ? 0xFFFF0000u : 0u);
         if (tid < 32) sm.near[tid] = powf(g, static_cast<float>(p.reverse ? tid : 31 - tid));
     }
     if (warp == 0) {
@@ -203,13 +202,15 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
             uint32_t r[32];
             tmem_ld32(tlane + TM_O + 64 * half + 32 * k, r);
             tmem_ld_wait();
+            if (row >= cnt)   // masked: zero whatever the products left
+#pragma unroll
+                for (int i = 0; i < 32; ++i) r[i] = 0u;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 uint32_t pk[4];
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
-                    pk[u] = row < cnt ? pack_bf16(__uint_as_float(r[8 * i + 2 * u]), __uint_as_float(r[8 * i + 2 * u + 1]))
-                                      : 0u;
+                    pk[u] = pack_bf16(__uint_as_float(r[8 * i + 2 * u]), __uint_as_float(r[8 * i + 2 * u + 1]));
                 st_shared_v4(tile + sw128_off(row, 64 * k + 16 * i), pk[0], pk[1], pk[2], pk[3]);
             }
         }
@@ -314,6 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         const bool reverse = p.reverse;
         const float a_intra = p.a_intra;
         const float *diag = sm.diag + 32 - lane;
+        const uint32_t *keep = sm.keep + 32 - lane;
         for (int c = 0; !kStates && c < nchunk; ++c) {
             const int cnt = count_of(c);
             if (!wait(b_d, c)) break;
@@ -329,20 +331,23 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                     uint32_t r[32];
                     tmem_ld32(tlane + TM_D + 32 * k, r);
                     tmem_ld_wait();
+                    const float2 *d2 = reinterpret_cast<const float2 *>(r);
                     if (k == w) {   // the diagonal block: every distance from the table
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            pk[i] = pack_bf16(diag[2 * i] * __uint_as_float(r[2 * i]),
-                                              diag[2 * i + 1] * __uint_as_float(r[2 * i + 1]));
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 v = mul2(make_float2(diag[2 * i], diag[2 * i + 1]), d2[i]);
+                            // off the mask the table's 0 would leave NaN where D overflows
+                            pk[i] = pack_bf16(v.x, v.y) & keep[2 * i];
+                        }
                     } else {        // distance to the block's near side times distance within the block
-                        const float f = a_intra * sm.gp[reverse ? 32 * k - row : row - 32 * k - 31];
+                        const float2 f = both(a_intra * sm.gp[reverse ? 32 * k - row : row - 32 * k - 31]);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const float4 e = *reinterpret_cast<const float4 *>(&sm.near[4 * i]);
-                            pk[2 * i] = pack_bf16((f * e.x) * __uint_as_float(r[4 * i]),
-                                                  (f * e.y) * __uint_as_float(r[4 * i + 1]));
-                            pk[2 * i + 1] = pack_bf16((f * e.z) * __uint_as_float(r[4 * i + 2]),
-                                                      (f * e.w) * __uint_as_float(r[4 * i + 3]));
+                            const float2 v0 = mul2(mul2(make_float2(e.x, e.y), f), d2[2 * i]);
+                            const float2 v1 = mul2(mul2(make_float2(e.z, e.w), f), d2[2 * i + 1]);
+                            pk[2 * i] = pack_bf16(v0.x, v0.y);
+                            pk[2 * i + 1] = pack_bf16(v1.x, v1.y);
                         }
                     }
                     if (32 * k + 32 > cnt) {   // masked tokens: whatever D holds there, P is zero
@@ -352,14 +357,6 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                             else if (32 * k + 2 * i + 1 >= cnt) pk[i] &= 0xFFFFu;
                         }
                     }
-                    // an entry off the mask of the diagonal block is 0 x D, NaN where D overflows
-                    if (k == w)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const bool keep0 = reverse ? 2 * i >= lane : 2 * i <= lane;
-                            const bool keep1 = reverse ? 2 * i + 1 >= lane : 2 * i + 1 <= lane;
-                            pk[i] &= (keep0 ? 0xFFFFu : 0u) | (keep1 ? 0xFFFF0000u : 0u);
-                        }
                 }
                 tmem_st16(tlane + TM_P + 64 * half + 16 * (k & 1), pk);
             }
@@ -428,7 +425,10 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                     }
                     if (update) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(gn * __uint_as_float(r[i]));
+                        for (int i = 0; i < 16; ++i) {
+                            float2 &v = reinterpret_cast<float2 *>(r)[i];
+                            v = mul2(v, both(gn));
+                        }
                         tmem_st32(t_s + 32 * k, r);
                     }
                 }
@@ -452,7 +452,10 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                     tmem_ld32(tlane + TM_O + 64 * half + 32 * k, r);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(f * __uint_as_float(r[i]));
+                    for (int i = 0; i < 16; ++i) {
+                        float2 &v = reinterpret_cast<float2 *>(r)[i];
+                        v = mul2(v, both(f));
+                    }
                     tmem_st32(tlane + TM_O + 64 * half + 32 * k, r);
                 }
                 tmem_st_wait();
@@ -536,36 +539,37 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
             }
             if (c > 0 && !wait(b_u, c - 1)) break;   // the last keys are read
             if (update) {   // weighted keys, transposed: lane = x channel, columns = tokens of this half
-                const uint32_t yb = st + kTile + (row >> 6) * kHalf + 64 * half * 128 + 2 * (row & 7);
-                const uint32_t y16 = (row & 63) >> 3;   // 16-byte word of the row, swizzled by the token below
-                const uint4 *wt = reinterpret_cast<const uint4 *>(sm.w + 32 * half);
+                // ldmatrix turns 8 x 8 blocks around: thread t gets channel t / 4 and token pair t % 4 of each,
+                // which is how tensor memory takes 16 lanes x 4 columns. 16 channels x 64 tokens at a time.
 #pragma unroll 1
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t hi[8], lo[8];
+                for (int g16 = 0; g16 < 2; ++g16) {
+                    const int ch = (warp & 3) * 32 + 16 * g16;   // first channel
+                    // lane l gives the address of one row of block l / 8: tokens +8 for blocks 2 and 3,
+                    // channels +8 for blocks 1 and 3
+                    const int tok = 64 * half + (lane & 7) + ((lane >> 4) << 3), c8 = ch + ((lane >> 3) & 1) * 8;
+                    const uint32_t from = st + kTile + (c8 >> 6) * kHalf + sw128_off(tok, (c8 & 63) * 2);
+                    uint32_t hi[16], lo[16];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {   // four tokens
-                        const uint4 w = wt[4 * q + i];
-                        const uint32_t from = yb + (16 * q + 4 * i) * 128;
-                        uint32_t v[4];
+                    for (int i = 0; i < 4; ++i) {   // 16 tokens
+                        uint32_t y[4];
+                        wmma16::ldsm4t(from + i * 16 * 128, y);
 #pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            v[u] = ld_shared_u16(from + u * 128 + ((y16 ^ ((4 * i + u) & 7)) << 4));
-                        if (cnt < kC)   // masked tokens: zero whatever the keys hold
-#pragma unroll
-                            for (int u = 0; u < 4; ++u)
-                                if (64 * half + 16 * q + 4 * i + u >= cnt) v[u] = 0u;
-                        // w y = hi + lo: hi rounds w1 y, lo takes its exact rest and w2 y (w = w1 + w2)
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const uint32_t y = __byte_perm(v[2 * u], v[2 * u + 1], 0x5410);
-                            const uint32_t w1 = u ? w.z : w.x, w2 = u ? w.w : w.y;
-                            const uint32_t a = mul_bf16x2(w1, y);
-                            hi[2 * i + u] = a;
-                            lo[2 * i + u] = fma_bf16x2(w2, y, fma_bf16x2(w1, y, a ^ 0x80008000u));
+                        for (int u = 0; u < 4; ++u) {
+                            const int pair = 32 * half + 8 * i + 4 * (u >> 1) + (lane & 3);
+                            if (cnt < kC) {   // masked tokens: zero whatever the keys hold
+                                if (2 * pair >= cnt) y[u] = 0u;
+                                else if (2 * pair + 1 >= cnt) y[u] &= 0xFFFFu;
+                            }
+                            // w y = hi + lo: hi rounds w1 y, lo takes its exact rest and w2 y (w = w1 + w2)
+                            const uint2 w = sm.w[pair];
+                            const uint32_t a = mul_bf16x2(w.x, y[u]);
+                            hi[4 * i + u] = a;
+                            lo[4 * i + u] = fma_bf16x2(w.y, y[u], fma_bf16x2(w.x, y[u], a ^ 0x80008000u));
                         }
                     }
-                    tmem_st8(tlane + TM_YH + 32 * half + 8 * q, hi);
-                    tmem_st8(tlane + TM_YL + 32 * half + 8 * q, lo);
+                    const uint32_t to = tlane + (static_cast<uint32_t>(16 * g16) << 16) + 32 * half;
+                    tmem_st_frag16(to + TM_YH, hi);
+                    tmem_st_frag16(to + TM_YL, lo);
                 }
                 tmem_st_wait();
                 tc_fence_before();
