@@ -22,7 +22,8 @@
 // term: they only enter O, which is stored with 8 bits itself.
 //
 // Warps: 0-7 turn D into P; 8-15 copy and decay the state, scale the first half of O and send the
-// outputs out through the X tile; 16-23 weigh the keys; 24 loads (TMA, two stages of X, Y, Z tiles);
+// outputs out through the Z tile; 16-23 weigh the keys; 24 loads (TMA, two stages of X, Y, Z tiles, each
+// tile refilled as soon as its own readers are done: Y first, Z, which is needed last, last);
 // 25 issues the products, in the order D, X S, U, P Z, which leaves P's conversion the time of X S
 // and U. They hand over through mbarriers that complete once per chunk. Eight warps per role: with
 // four, and keys and state on the same eight, the chain of conversions took 6900 cycles a chunk.
@@ -52,9 +53,10 @@ constexpr uint32_t TM_D = 0, TM_P = 0, TM_O = 128, TM_U = 256, TM_YH = 384, TM_Y
 constexpr uint32_t kBarKeys = 1;   // named barrier of warps 8-15
 
 struct Small {
-    uint64_t full[2];   // X, Y, Z tiles landed, by stage
-    uint64_t free[2];   // every product that reads the stage is done
-    uint64_t out[2];    // the outputs, which leave through the X tile, are out
+    // by stage: a tile has landed, and may be filled again
+    uint64_t fy[2], yfree[2];   // Y: D is computed and the keys are weighed
+    uint64_t fx[2], xfree[2];   // X: X S is computed
+    uint64_t fz[2], zfree[2];   // Z: U and P Z are computed; the outputs, which leave through it, are out
     uint64_t end;       // after an abort: the products that were issued are done
     uint64_t d, p;      // D computed, P written
     uint64_t xs, sc;    // X S computed, scaled
@@ -113,34 +115,31 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     const bool have = !kStates && (seg > 0 || p.S0 != nullptr);   // S is not zero at the start
     const bool want_s = kStates || (p.ST && seg == p.nseg - 1);
 
-    const uint32_t b_full = smem_u32(&sm.full[0]), b_free = smem_u32(&sm.free[0]), b_end = smem_u32(&sm.end);
-    const uint32_t b_out = smem_u32(&sm.out[0]);
+    const uint32_t b_fy = smem_u32(&sm.fy[0]), b_fx = smem_u32(&sm.fx[0]), b_fz = smem_u32(&sm.fz[0]);
+    const uint32_t b_yfree = smem_u32(&sm.yfree[0]), b_xfree = smem_u32(&sm.xfree[0]);
+    const uint32_t b_zfree = smem_u32(&sm.zfree[0]), b_end = smem_u32(&sm.end);
     const uint32_t b_d = smem_u32(&sm.d), b_p = smem_u32(&sm.p), b_xs = smem_u32(&sm.xs), b_sc = smem_u32(&sm.sc);
     const uint32_t b_o = smem_u32(&sm.o), b_ord = smem_u32(&sm.ord), b_y = smem_u32(&sm.y), b_u = smem_u32(&sm.u);
     const uint32_t b_s = smem_u32(&sm.s);
     const bool back = p.reverse;
     auto chunk_of = [&](int c) { return back ? nchunk - 1 - c : c; };
     auto count_of = [&](int c) { return min(kC, valid - chunk_of(c) * kC); };
-    auto load_yz = [&](int c) {   // one thread
-        const uint32_t st = sbase + OFF_STAGE + (c & 1) * STAGE, bar = b_full + 8 * (c & 1);
+    auto load = [&](const CUtensorMap &map, uint32_t tile, uint32_t full, int c) {   // one thread
+        const uint32_t to = sbase + OFF_STAGE + (c & 1) * STAGE + tile, bar = full + 8 * (c & 1);
         const int t0 = t_begin + chunk_of(c) * kC;
-        mbar_arrive_expect_tx(bar, (kStates ? 2 : 3) * kTile);
-        for (int i = 0; i < 2; ++i) tma_load_4d(st + kTile + i * kHalf, &job.y, bar, 64 * i, h, t0, b);
-        for (int i = 0; i < 2; ++i) tma_load_4d(st + 2 * kTile + i * kHalf, &job.z, bar, 64 * i, h, t0, b);
-    };
-    auto load_x = [&](int c) {
-        const uint32_t st = sbase + OFF_STAGE + (c & 1) * STAGE, bar = b_full + 8 * (c & 1);
-        const int t0 = t_begin + chunk_of(c) * kC;
-        for (int i = 0; i < 2; ++i) tma_load_4d(st + i * kHalf, &job.x, bar, 64 * i, h, t0, b);
+        mbar_arrive_expect_tx(bar, kTile);
+        for (int i = 0; i < 2; ++i) tma_load_4d(to + i * kHalf, &map, bar, 64 * i, h, t0, b);
     };
     if (warp == 24 && lane == 0) {   // the first loads leave before the rest of the CTA is set up
-        mbar_init(b_full, 1);
-        mbar_init(b_full + 8, 1);
-        mbar_init(b_free, 1);
-        mbar_init(b_free + 8, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(b_fy + 8 * i, 1);
+            mbar_init(b_fx + 8 * i, 1);
+            mbar_init(b_fz + 8 * i, 1);
+            mbar_init(b_yfree + 8 * i, kStates ? 8 : 9);   // the warps that weigh, and the product D
+            mbar_init(b_xfree + 8 * i, 1);
+            mbar_init(b_zfree + 8 * i, kStates ? 1 : 8);   // the products, or the warps that send O out
+        }
         mbar_init(b_end, 1);
-        mbar_init(b_out, 8);
-        mbar_init(b_out + 8, 8);
         mbar_init(b_d, 1);
         mbar_init(b_p, 8);
         mbar_init(b_xs, 1);
@@ -153,8 +152,9 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         sm.abort = 0;
         fence_mbar_init();
         for (int c = 0; c < 2 && c < nchunk; ++c) {
-            load_yz(c);
-            if (!kStates) load_x(c);
+            load(job.y, kTile, b_fy, c);
+            if (!kStates) load(job.x, 0, b_fx, c);
+            load(job.z, 2 * kTile, b_fz, c);
         }
     }
     dependency_release();
@@ -191,11 +191,12 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         if (lane == 0) mbar_arrive(bar);
     };
 
-    // warps 8-15: O of chunk c leaves through the X tile, which its products have read; each warp's 32
-    // rows x 64 channels are one box, and rows past T are cut off by the tensor's bounds
+    // warps 8-15: O of chunk c leaves through the Z tile, the last that its products read and the last that
+    // the next chunk needs; each warp's 32 rows x 64 channels are one box, and rows past T are cut off by the
+    // tensor's bounds
     auto put_out = [&](int c) {
         const int half = (warp - 8) >> 2, cnt = count_of(c);
-        const uint32_t tile = sbase + OFF_STAGE + (c & 1) * STAGE + half * kHalf;
+        const uint32_t tile = sbase + OFF_STAGE + (c & 1) * STAGE + 2 * kTile + half * kHalf;
         tc_fence_after();
 #pragma unroll 1
         for (int k = 0; k < 2; ++k) {
@@ -222,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
             if (t < p.T) tma_store_4d(&job.o, tile + (warp & 3) * 4096, 64 * half, h, t, b);
             tma_store_commit();
             tma_store_wait_read_all();
-            mbar_arrive(b_out + 8 * (c & 1));
+            mbar_arrive(b_zfree + 8 * (c & 1));
         }
         __syncwarp();
     };
@@ -230,17 +231,28 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     if (warp == 24) {
         // ---------------------------------------------------------------- loads
         if (lane == 0) {
-            int issued = min(nchunk, 2);
+            int last[3] = {nchunk, nchunk, nchunk};   // loads issued of each kind
             for (int c = 2; c < nchunk; ++c) {
-                if (!wait(b_free + 8 * (c & 1), (c - 2) >> 1)) break;
-                load_yz(c);
-                ++issued;
-                // an abort here leaves the stage's barrier short of X's bytes: its wait below gives up
-                if (!kStates && wait(b_out + 8 * (c & 1), (c - 2) >> 1)) load_x(c);
+                const int before = (c - 2) >> 1;
+                last[0] = last[1] = last[2] = c;
+                if (!wait(b_yfree + 8 * (c & 1), before)) break;
+                load(job.y, kTile, b_fy, c);
+                last[0] = c + 1;
+                if (!kStates) {
+                    if (!wait(b_xfree + 8 * (c & 1), before)) break;
+                    load(job.x, 0, b_fx, c);
+                    last[1] = c + 1;
+                }
+                if (!wait(b_zfree + 8 * (c & 1), before)) break;
+                load(job.z, 2 * kTile, b_fz, c);
+                last[2] = c + 1;
             }
             // nothing of this CTA's may be in flight when it ends, an abort included
-            for (int seen = issued > 2 ? issued - 2 : 0; seen < issued; ++seen)
-                mbar_wait_bounded(b_full + 8 * (seen & 1), (seen >> 1) & 1, kWaitLimit);
+            for (int i = 0; i < 3; ++i)
+                for (int c = max(0, last[i] - 2); c < last[i]; ++c)
+                    if (i != 1 || !kStates)
+                        mbar_wait_bounded((i == 0 ? b_fy : i == 1 ? b_fx : b_fz) + 8 * (c & 1), (c >> 1) & 1,
+                                          kWaitLimit);
         }
     } else if (warp == 25) {
         // ---------------------------------------------------------------- products
@@ -253,8 +265,8 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
             const uint64_t dz = sw128_desc(st + 2 * kTile, kHalf, 1024);
             const bool update = c < nchunk - 1 || want_s;
             const bool inter = !kStates && (c > 0 || have);
-            if (!wait(b_full + 8 * (c & 1), c >> 1)) break;
             if (!kStates) {
+                if (!wait(b_fy + 8 * (c & 1), c >> 1) || !wait(b_fx + 8 * (c & 1), c >> 1)) break;
                 if (c > 0 && !wait(b_o, c - 1)) break;   // P of the last chunk, which lies over D, is done with
                 tc_fence_after();
                 if (lead) {
@@ -264,6 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                         mma_bf16(tbase + TM_D, desc_add(dx, off), desc_add(dy, off), id_kk, s);
                     }
                     mma_commit(b_d);
+                    mma_commit(b_yfree + 8 * (c & 1));
                 }
             }
             if (!wait(b_s, c)) break;
@@ -278,9 +291,10 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                                      desc_add(ds, s * 2048), id_km, s);
                     }
                     mma_commit(b_xs);
+                    mma_commit(b_xfree + 8 * (c & 1));
                 }
             }
-            if (!wait(b_y, c)) break;
+            if (!wait(b_fz + 8 * (c & 1), c >> 1) || !wait(b_y, c)) break;
             tc_fence_after();
             if (lead) {
                 if (update) {
@@ -293,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                         mma_bf16_ta(tbase + TM_U, tbase + TM_YL + 8 * s, desc_add(dz, s * 2048), id_km, 1);
                 }
                 mma_commit(b_u);
-                if (kStates) mma_commit(b_free + 8 * (c & 1));
+                if (kStates) mma_commit(b_zfree + 8 * (c & 1));
             }
             __syncwarp();
             if (kStates) continue;
@@ -305,7 +319,6 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                     mma_bf16_ta(tbase + TM_O, tbase + TM_P + 64 * (s >> 2) + 8 * (s & 3),
                                 desc_add(dz, s * 2048), id_km, inter || s > 0);
                 mma_commit(b_o);
-                mma_commit(b_free + 8 * (c & 1));
             }
             __syncwarp();
         }
@@ -526,11 +539,12 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                 named_sync(kBarKeys, 256);
                 wcnt = cnt;
             }
-            if (!wait(b_full + 8 * (c & 1), c >> 1)) break;
+            if (!wait(b_fy + 8 * (c & 1), c >> 1)) break;
             const uint32_t st = sbase + OFF_STAGE + (c & 1) * STAGE;
             const int t0 = t_begin + chunk_of(c) * kC;
             if (cnt < kC && t0 + cnt < T) {
                 // masked tokens that the tile holds: a zero weight does not silence a NaN in Z
+                if (!wait(b_fz + 8 * (c & 1), c >> 1)) break;
                 for (int i = gt; i < (kC - cnt) * 16; i += 256) {
                     const int r = cnt + (i >> 4), k = i & 15;
                     st_shared_v4(st + 2 * kTile + (k >> 3) * kHalf + r * 128 + (k & 7) * 16, 0u, 0u, 0u, 0u);
@@ -575,6 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                 tc_fence_before();
             }
             arrive(b_y);
+            arrive(b_yfree + 8 * (c & 1));
         }
     }
     tc_fence_before();
