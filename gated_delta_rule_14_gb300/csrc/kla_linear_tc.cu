@@ -44,19 +44,18 @@ constexpr int kC = 128, kD = 128;
 constexpr int kThreads = 26 * 32;
 constexpr uint32_t kWaitLimit = 100000;   // x 20 us: a stuck wait gives up after ~2 s
 constexpr uint32_t kTile = 32768, kHalf = 16384;   // a 128 x 128 bf16 tile: two blocks of 64 channels
-constexpr uint32_t OFF_STAGE = 0, STAGE = 3 * kTile;
-constexpr uint32_t OFF_S = 2 * STAGE;
+constexpr uint32_t OFF_S = 6 * kTile;   // after two stages of X, Y, Z tiles, or three of Y, Z
 constexpr uint32_t OFF_SMALL = OFF_S + kTile;
 constexpr uint32_t SMEM_BYTES = OFF_SMALL + 2048 + 1024;   // + alignment slack
 static_assert(SMEM_BYTES <= 232448, "shared memory");
-constexpr uint32_t TM_D = 0, TM_P = 0, TM_O = 128, TM_U = 256, TM_YH = 384, TM_YL = 448;
+constexpr uint32_t TM_D = 0, TM_P = 0, TM_O = 128, TM_U = 256, TM_YH = 384;   // keys: hi, then lo 64 columns on
 constexpr uint32_t kBarKeys = 1;   // named barrier of warps 8-15
 
 struct Small {
     // by stage: a tile has landed, and may be filled again
-    uint64_t fy[2], yfree[2];   // Y: D is computed and the keys are weighed
+    uint64_t fy[3], yfree[3];   // Y: D is computed and the keys are weighed
     uint64_t fx[2], xfree[2];   // X: X S is computed
-    uint64_t fz[2], zfree[2];   // Z: U and P Z are computed; the outputs, which leave through it, are out
+    uint64_t fz[3], zfree[3];   // Z: U and P Z are computed; the outputs, which leave through it, are out
     uint64_t end;       // after an abort: the products that were issued are done
     uint64_t d, p;      // D computed, P written
     uint64_t xs, sc;    // X S computed, scaled
@@ -124,19 +123,30 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     const bool back = p.reverse;
     auto chunk_of = [&](int c) { return back ? nchunk - 1 - c : c; };
     auto count_of = [&](int c) { return min(kC, valid - chunk_of(c) * kC); };
+    // stages: two of X, Y, Z tiles, or three of Y, Z where only the state is wanted
+    constexpr int kNs = kStates ? 3 : 2;
+    constexpr uint32_t kY = kStates ? 0 : kTile, kZt = kY + kTile;
+    // Where only the state is wanted, the columns of D hold a second set of weighted keys, so that those of
+    // the next chunk are written while this chunk's product runs; each set has barriers of its own.
+    auto keys_at = [&](int c) { return kStates && (c & 1) ? TM_D : TM_YH; };
+    auto keys_ready = [&](int c) { return kStates && (c & 1) ? b_p : b_y; };
+    auto keys_phase = [&](int c) { return kStates ? c >> 1 : c; };
+    auto stage_of = [&](int c) { return sbase + (c % kNs) * (kZt + kTile); };
     auto load = [&](const CUtensorMap &map, uint32_t tile, uint32_t full, int c) {   // one thread
-        const uint32_t to = sbase + OFF_STAGE + (c & 1) * STAGE + tile, bar = full + 8 * (c & 1);
+        const uint32_t to = stage_of(c) + tile, bar = full + 8 * (c % kNs);
         const int t0 = t_begin + chunk_of(c) * kC;
         mbar_arrive_expect_tx(bar, kTile);
         for (int i = 0; i < 2; ++i) tma_load_4d(to + i * kHalf, &map, bar, 64 * i, h, t0, b);
     };
     if (warp == 24 && lane == 0) {   // the first loads leave before the rest of the CTA is set up
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kNs; ++i) {
             mbar_init(b_fy + 8 * i, 1);
-            mbar_init(b_fx + 8 * i, 1);
             mbar_init(b_fz + 8 * i, 1);
             mbar_init(b_yfree + 8 * i, kStates ? 8 : 9);   // the warps that weigh, and the product D
-            mbar_init(b_xfree + 8 * i, 1);
+            if (i < 2) {
+                mbar_init(b_fx + 8 * i, 1);
+                mbar_init(b_xfree + 8 * i, 1);
+            }
             mbar_init(b_zfree + 8 * i, kStates ? 1 : 8);   // the products, or the warps that send O out
         }
         mbar_init(b_end, 1);
@@ -151,10 +161,10 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         mbar_init(b_s, 8);
         sm.abort = 0;
         fence_mbar_init();
-        for (int c = 0; c < 2 && c < nchunk; ++c) {
-            load(job.y, kTile, b_fy, c);
+        for (int c = 0; c < kNs && c < nchunk; ++c) {
+            load(job.y, kY, b_fy, c);
             if (!kStates) load(job.x, 0, b_fx, c);
-            load(job.z, 2 * kTile, b_fz, c);
+            load(job.z, kZt, b_fz, c);
         }
     }
     dependency_release();
@@ -196,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     // tensor's bounds
     auto put_out = [&](int c) {
         const int half = (warp - 8) >> 2, cnt = count_of(c);
-        const uint32_t tile = sbase + OFF_STAGE + (c & 1) * STAGE + 2 * kTile + half * kHalf;
+        const uint32_t tile = stage_of(c) + kZt + half * kHalf;
         tc_fence_after();
 #pragma unroll 1
         for (int k = 0; k < 2; ++k) {
@@ -223,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
             if (t < p.T) tma_store_4d(&job.o, tile + (warp & 3) * 4096, 64 * half, h, t, b);
             tma_store_commit();
             tma_store_wait_read_all();
-            mbar_arrive(b_zfree + 8 * (c & 1));
+            mbar_arrive(b_zfree + 8 * (c % kNs));
         }
         __syncwarp();
     };
@@ -232,26 +242,26 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         // ---------------------------------------------------------------- loads
         if (lane == 0) {
             int last[3] = {nchunk, nchunk, nchunk};   // loads issued of each kind
-            for (int c = 2; c < nchunk; ++c) {
-                const int before = (c - 2) >> 1;
+            for (int c = kNs; c < nchunk; ++c) {
+                const int before = c / kNs - 1, at = 8 * (c % kNs);
                 last[0] = last[1] = last[2] = c;
-                if (!wait(b_yfree + 8 * (c & 1), before)) break;
-                load(job.y, kTile, b_fy, c);
+                if (!wait(b_yfree + at, before)) break;
+                load(job.y, kY, b_fy, c);
                 last[0] = c + 1;
                 if (!kStates) {
-                    if (!wait(b_xfree + 8 * (c & 1), before)) break;
+                    if (!wait(b_xfree + at, before)) break;
                     load(job.x, 0, b_fx, c);
                     last[1] = c + 1;
                 }
-                if (!wait(b_zfree + 8 * (c & 1), before)) break;
-                load(job.z, 2 * kTile, b_fz, c);
+                if (!wait(b_zfree + at, before)) break;
+                load(job.z, kZt, b_fz, c);
                 last[2] = c + 1;
             }
             // nothing of this CTA's may be in flight when it ends, an abort included
             for (int i = 0; i < 3; ++i)
-                for (int c = max(0, last[i] - 2); c < last[i]; ++c)
+                for (int c = max(0, last[i] - kNs); c < last[i]; ++c)
                     if (i != 1 || !kStates)
-                        mbar_wait_bounded((i == 0 ? b_fy : i == 1 ? b_fx : b_fz) + 8 * (c & 1), (c >> 1) & 1,
+                        mbar_wait_bounded((i == 0 ? b_fy : i == 1 ? b_fx : b_fz) + 8 * (c % kNs), (c / kNs) & 1,
                                           kWaitLimit);
         }
     } else if (warp == 25) {
@@ -260,13 +270,13 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         const uint32_t id_kk = idesc_bf16(128, 128, 0, 0), id_km = idesc_bf16(128, 128, 0, 1);
         const uint64_t ds = sw128_desc(sbase + OFF_S, kHalf, 1024);
         for (int c = 0; c < nchunk; ++c) {
-            const uint32_t st = sbase + OFF_STAGE + (c & 1) * STAGE;
-            const uint64_t dx = sw128_desc(st, 16, 1024), dy = sw128_desc(st + kTile, 16, 1024);
-            const uint64_t dz = sw128_desc(st + 2 * kTile, kHalf, 1024);
+            const uint32_t st = stage_of(c), at = 8 * (c % kNs);
+            const uint64_t dx = sw128_desc(st, 16, 1024), dy = sw128_desc(st + kY, 16, 1024);
+            const uint64_t dz = sw128_desc(st + kZt, kHalf, 1024);
             const bool update = c < nchunk - 1 || want_s;
             const bool inter = !kStates && (c > 0 || have);
             if (!kStates) {
-                if (!wait(b_fy + 8 * (c & 1), c >> 1) || !wait(b_fx + 8 * (c & 1), c >> 1)) break;
+                if (!wait(b_fy + at, c / kNs) || !wait(b_fx + at, c / kNs)) break;
                 if (c > 0 && !wait(b_o, c - 1)) break;   // P of the last chunk, which lies over D, is done with
                 tc_fence_after();
                 if (lead) {
@@ -276,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                         mma_bf16(tbase + TM_D, desc_add(dx, off), desc_add(dy, off), id_kk, s);
                     }
                     mma_commit(b_d);
-                    mma_commit(b_yfree + 8 * (c & 1));
+                    mma_commit(b_yfree + at);
                 }
             }
             if (!wait(b_s, c)) break;
@@ -291,23 +301,26 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                                      desc_add(ds, s * 2048), id_km, s);
                     }
                     mma_commit(b_xs);
-                    mma_commit(b_xfree + 8 * (c & 1));
+                    mma_commit(b_xfree + at);
                 }
             }
-            if (!wait(b_fz + 8 * (c & 1), c >> 1) || !wait(b_y, c)) break;
+            if (!wait(b_fz + at, c / kNs) || !wait(keys_ready(c), keys_phase(c))) break;
             tc_fence_after();
             if (lead) {
+                const uint32_t keys = tbase + keys_at(c);
                 if (update) {
 #pragma unroll
                     for (int s = 0; s < 8; ++s)
-                        mma_bf16_ta(tbase + TM_U, tbase + TM_YH + 8 * s, desc_add(dz, s * 2048), id_km,
-                                    c > 0 || have || s > 0);
+                        mma_bf16_ta(tbase + TM_U, keys + 8 * s, desc_add(dz, s * 2048), id_km, c > 0 || have || s > 0);
 #pragma unroll
                     for (int s = 0; s < 8; ++s)
-                        mma_bf16_ta(tbase + TM_U, tbase + TM_YL + 8 * s, desc_add(dz, s * 2048), id_km, 1);
+                        mma_bf16_ta(tbase + TM_U, keys + 64 + 8 * s, desc_add(dz, s * 2048), id_km, 1);
                 }
                 mma_commit(b_u);
-                if (kStates) mma_commit(b_zfree + 8 * (c & 1));
+                if (kStates) {
+                    mma_commit(b_zfree + at);
+                    mma_commit(b_xfree + 8 * (c & 1));   // this set of keys is read
+                }
             }
             __syncwarp();
             if (kStates) continue;
@@ -539,19 +552,20 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                 named_sync(kBarKeys, 256);
                 wcnt = cnt;
             }
-            if (!wait(b_fy + 8 * (c & 1), c >> 1)) break;
-            const uint32_t st = sbase + OFF_STAGE + (c & 1) * STAGE;
+            const uint32_t st = stage_of(c), stage = 8 * (c % kNs);
+            if (!wait(b_fy + stage, c / kNs)) break;
             const int t0 = t_begin + chunk_of(c) * kC;
             if (cnt < kC && t0 + cnt < T) {
                 // masked tokens that the tile holds: a zero weight does not silence a NaN in Z
-                if (!wait(b_fz + 8 * (c & 1), c >> 1)) break;
+                if (!wait(b_fz + stage, c / kNs)) break;
                 for (int i = gt; i < (kC - cnt) * 16; i += 256) {
                     const int r = cnt + (i >> 4), k = i & 15;
-                    st_shared_v4(st + 2 * kTile + (k >> 3) * kHalf + r * 128 + (k & 7) * 16, 0u, 0u, 0u, 0u);
+                    st_shared_v4(st + kZt + (k >> 3) * kHalf + r * 128 + (k & 7) * 16, 0u, 0u, 0u, 0u);
                 }
                 fence_proxy_async_smem();
             }
-            if (c > 0 && !wait(b_u, c - 1)) break;   // the last keys are read
+            // the keys that these replace are read
+            if (kStates ? c > 1 && !wait(b_xfree + 8 * (c & 1), (c - 2) >> 1) : c > 0 && !wait(b_u, c - 1)) break;
             if (update) {   // weighted keys, transposed: lane = x channel, columns = tokens of this half
                 // ldmatrix turns 8 x 8 blocks around: thread t gets channel t / 4 and token pair t % 4 of each,
                 // which is how tensor memory takes 16 lanes x 4 columns. 16 channels x 64 tokens at a time.
@@ -561,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                     // lane l gives the address of one row of block l / 8: tokens +8 for blocks 2 and 3,
                     // channels +8 for blocks 1 and 3
                     const int tok = 64 * half + (lane & 7) + ((lane >> 4) << 3), c8 = ch + ((lane >> 3) & 1) * 8;
-                    const uint32_t from = st + kTile + (c8 >> 6) * kHalf + sw128_off(tok, (c8 & 63) * 2);
+                    const uint32_t from = st + kY + (c8 >> 6) * kHalf + sw128_off(tok, (c8 & 63) * 2);
                     uint32_t hi[16], lo[16];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {   // 16 tokens
@@ -581,15 +595,15 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                             lo[4 * i + u] = fma_bf16x2(w.y, y[u], fma_bf16x2(w.x, y[u], a ^ 0x80008000u));
                         }
                     }
-                    const uint32_t to = tlane + (static_cast<uint32_t>(16 * g16) << 16) + 32 * half;
-                    tmem_st_frag16(to + TM_YH, hi);
-                    tmem_st_frag16(to + TM_YL, lo);
+                    const uint32_t to = tlane + (static_cast<uint32_t>(16 * g16) << 16) + keys_at(c) + 32 * half;
+                    tmem_st_frag16(to, hi);
+                    tmem_st_frag16(to + 64, lo);
                 }
                 tmem_st_wait();
                 tc_fence_before();
             }
-            arrive(b_y);
-            arrive(b_yfree + 8 * (c & 1));
+            arrive(keys_ready(c));
+            arrive(b_yfree + stage);
         }
     }
     tc_fence_before();
