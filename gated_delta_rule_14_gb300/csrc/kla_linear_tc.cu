@@ -49,7 +49,6 @@ constexpr uint32_t OFF_SMALL = OFF_S + kTile;
 constexpr uint32_t SMEM_BYTES = OFF_SMALL + 2048 + 1024;   // + alignment slack
 static_assert(SMEM_BYTES <= 232448, "shared memory");
 constexpr uint32_t TM_D = 0, TM_P = 0, TM_O = 128, TM_U = 256, TM_YH = 384;   // keys: hi, then lo 64 columns on
-constexpr uint32_t kBarKeys = 1;   // named barrier of warps 8-15
 
 struct Small {
     // by stage: a tile has landed, and may be filled again
@@ -68,7 +67,6 @@ struct Small {
     float diag[64];                // a_intra g^distance at 32 + column - row of a diagonal 32 x 32 block, 0 off the mask
     uint32_t keep[64];             // the mask of that column and its right neighbour, as bf16 pairs
     alignas(16) float near[32];    // g^distance of a block's columns from its side near the diagonal
-    alignas(16) uint2 w[kC / 2];   // weights of the keys, two tokens each: bf16 pairs of w and of what w lacks
 };
 static_assert(sizeof(Small) <= 2048, "small area");
 
@@ -208,26 +206,26 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         const int half = (warp - 8) >> 2, cnt = count_of(c);
         const uint32_t tile = stage_of(c) + kZt + half * kHalf;
         tc_fence_after();
-#pragma unroll 1
+        uint32_t pk[32];
+#pragma unroll
         for (int k = 0; k < 2; ++k) {
             uint32_t r[32];
             tmem_ld32(tlane + TM_O + 64 * half + 32 * k, r);
             tmem_ld_wait();
-            if (row >= cnt)   // masked: zero whatever the products left
 #pragma unroll
-                for (int i = 0; i < 32; ++i) r[i] = 0u;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t pk[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    pk[u] = pack_bf16(__uint_as_float(r[8 * i + 2 * u]), __uint_as_float(r[8 * i + 2 * u + 1]));
-                st_shared_v4(tile + sw128_off(row, 64 * k + 16 * i), pk[0], pk[1], pk[2], pk[3]);
-            }
+            for (int i = 0; i < 16; ++i)
+                pk[16 * k + i] = pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
         }
         tc_fence_before();
+        arrive(b_ord);   // the next X S may go: shared memory, which the products keep busy, comes after
+        if (row >= cnt)  // masked: zero whatever the products left
+#pragma unroll
+            for (int i = 0; i < 32; ++i) pk[i] = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            st_shared_v4(tile + sw128_off(row, 16 * i), pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
         fence_proxy_async_smem();
-        arrive(b_ord);
+        __syncwarp();
         if (lane == 0) {
             const int t = t_begin + chunk_of(c) * kC + 32 * (warp & 3);
             if (t < p.T) tma_store_4d(&job.o, tile + (warp & 3) * 4096, 64 * half, h, t, b);
@@ -532,24 +530,23 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         const bool reverse = p.reverse;
         const float a_upd = p.a_upd;
         int wcnt = -1;
+        uint2 w[8];   // of this thread's token pairs: 4 q + lane % 4 of the half, q < 8
         for (int c = 0; c < nchunk; ++c) {
             const int cnt = count_of(c);
             const bool update = c < nchunk - 1 || want_s;
             if (cnt != wcnt) {
-                named_sync(kBarKeys, 256);
-                if (gt < kC / 2) {
-                    float w[2], lo[2];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    float f[2];
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        const int j = 2 * gt + u;
-                        w[u] = j < cnt ? a_upd * sm.gp[reverse ? j + 1 : cnt - 1 - j] : 0.f;
+                        const int t = 64 * half + 8 * q + 2 * (lane & 3) + u;
+                        f[u] = t < cnt ? a_upd * sm.gp[reverse ? t + 1 : cnt - 1 - t] : 0.f;
                     }
-                    const uint32_t hi = pack_bf16(w[0], w[1]);
-                    lo[0] = w[0] - __uint_as_float(hi << 16);
-                    lo[1] = w[1] - __uint_as_float(hi & 0xFFFF0000u);
-                    sm.w[gt] = make_uint2(hi, pack_bf16(lo[0], lo[1]));
+                    w[q].x = pack_bf16(f[0], f[1]);
+                    w[q].y = pack_bf16(f[0] - __uint_as_float(w[q].x << 16),
+                                       f[1] - __uint_as_float(w[q].x & 0xFFFF0000u));
                 }
-                named_sync(kBarKeys, 256);
                 wcnt = cnt;
             }
             const uint32_t st = stage_of(c), stage = 8 * (c % kNs);
@@ -564,14 +561,13 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                 }
                 fence_proxy_async_smem();
             }
-            // the keys that these replace are read
-            if (kStates ? c > 1 && !wait(b_xfree + 8 * (c & 1), (c - 2) >> 1) : c > 0 && !wait(b_u, c - 1)) break;
+            bool ok = true;
             if (update) {   // weighted keys, transposed: lane = x channel, columns = tokens of this half
                 // ldmatrix turns 8 x 8 blocks around: thread t gets channel t / 4 and token pair t % 4 of each,
                 // which is how tensor memory takes 16 lanes x 4 columns. 16 channels x 64 tokens at a time.
 #pragma unroll 1
                 for (int g16 = 0; g16 < 2; ++g16) {
-                    const int ch = (warp & 3) * 32 + 16 * g16;   // first channel
+                    const int ch = (warp & 3) * 32 + 16 * g16;
                     // lane l gives the address of one row of block l / 8: tokens +8 for blocks 2 and 3,
                     // channels +8 for blocks 1 and 3
                     const int tok = 64 * half + (lane & 7) + ((lane >> 4) << 3), c8 = ch + ((lane >> 3) & 1) * 8;
@@ -583,25 +579,33 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                         wmma16::ldsm4t(from + i * 16 * 128, y);
 #pragma unroll
                         for (int u = 0; u < 4; ++u) {
-                            const int pair = 32 * half + 8 * i + 4 * (u >> 1) + (lane & 3);
                             if (cnt < kC) {   // masked tokens: zero whatever the keys hold
-                                if (2 * pair >= cnt) y[u] = 0u;
-                                else if (2 * pair + 1 >= cnt) y[u] &= 0xFFFFu;
+                                const int t = 64 * half + 16 * i + 8 * (u >> 1) + 2 * (lane & 3);
+                                if (t >= cnt) y[u] = 0u;
+                                else if (t + 1 >= cnt) y[u] &= 0xFFFFu;
                             }
                             // w y = hi + lo: hi rounds w1 y, lo takes its exact rest and w2 y (w = w1 + w2)
-                            const uint2 w = sm.w[pair];
-                            const uint32_t a = mul_bf16x2(w.x, y[u]);
+                            const uint2 f = w[2 * i + (u >> 1)];
+                            const uint32_t a = mul_bf16x2(f.x, y[u]);
                             hi[4 * i + u] = a;
-                            lo[4 * i + u] = fma_bf16x2(w.y, y[u], fma_bf16x2(w.x, y[u], a ^ 0x80008000u));
+                            lo[4 * i + u] = fma_bf16x2(f.y, y[u], fma_bf16x2(f.x, y[u], a ^ 0x80008000u));
                         }
                     }
+                    // the keys that these replace are read
+                    if (g16 == 0)
+                        ok = kStates ? c < 2 || wait(b_xfree + 8 * (c & 1), (c - 2) >> 1) : c == 0 || wait(b_u, c - 1);
+                    if (!ok) break;
+                    tc_fence_after();
                     const uint32_t to = tlane + (static_cast<uint32_t>(16 * g16) << 16) + keys_at(c) + 32 * half;
                     tmem_st_frag16(to, hi);
                     tmem_st_frag16(to + 64, lo);
                 }
                 tmem_st_wait();
                 tc_fence_before();
+            } else if (!kStates && c > 0) {
+                ok = wait(b_u, c - 1);
             }
+            if (!ok) break;
             arrive(keys_ready(c));
             arrive(b_yfree + stage);
         }
