@@ -309,25 +309,21 @@ struct Row {
         lead = lo * 16;
         bytes = (hi - lo) * 16;
     }
-    __device__ __forceinline__ void fetch(uint32_t buf, uint32_t bar) const {   // one thread; bytes are expected already
-        if (bytes)
-            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                             buf + lead),
-                         "l"(reinterpret_cast<uintptr_t>(base - shift) + lead), "r"(bytes), "r"(bar)
-                         : "memory");
-    }
 };
 // Whether the columns of a thread's k-th access exist for every lane: a row has more than half of the
 // values that its team holds (the narrowest team: more than kTeamMost).
 __device__ __forceinline__ constexpr bool always(int k, int width, int v, int e) {
     return (k + 1) * width * v <= kTeamMost || 2 * (k + 1) * v <= e;
 }
-// kN values, kV at a time, of a thread; zero from column n on. kV > 1: rows start on 16 bytes.
+// kN values, kV at a time, of a thread; zero from column n on. Accesses of 16 bytes: every row starts and
+// ends on 16 bytes, and its buffer starts with it.
+template <typename T, int kV>
+constexpr bool whole_rows() { return sizeof(T) * kV == 16; }
 template <typename T, int kV, int kWidth, int kN>
 __device__ __forceinline__ void get_row(const T *tensor, const T *end, const T *row, const uint8_t *buf, int lane,
                                         int n, float2 (&x)[kN / 2]) {
     float *f = reinterpret_cast<float *>(x);
-    if constexpr (kV > 1) {
+    if constexpr (whole_rows<T, kV>()) {
         const T *v = reinterpret_cast<const T *>(buf) + lane * kV;
 #pragma unroll
         for (int k = 0; k < kN / kV; ++k) {
@@ -343,14 +339,20 @@ __device__ __forceinline__ void get_row(const T *tensor, const T *end, const T *
         }
     } else {
         const Row<T> r(tensor, end, row, n);
-        const T *v = reinterpret_cast<const T *>(buf) + r.shift + lane;
+        const T *v = reinterpret_cast<const T *>(buf) + r.shift + lane * kV;
 #pragma unroll
-        for (int k = 0; k < kN; ++k)
-            f[k] = always(k, kWidth, 1, kN) || k * kWidth + lane < n ? to_f32(v[k * kWidth]) : 0.f;
+        for (int k = 0; k < kN / kV; ++k) {
+            T e[kV];
+#pragma unroll
+            for (int i = 0; i < kV; ++i) e[i] = from_f32<T>(0.f);
+            if (always(k, kWidth, kV, kN) || (k * kWidth + lane) * kV < n) load<T, kV>(v + k * kWidth * kV, e);
+#pragma unroll
+            for (int i = 0; i < kV; ++i) f[k * kV + i] = to_f32(e[i]);
+        }
         if (r.skip > 0 || r.have < n)   // the tensor's first or last row, off the 16-byte grid
 #pragma unroll
             for (int k = 0; k < kN; ++k) {
-                const int c = k * kWidth + lane;
+                const int c = (k / kV * kWidth + lane) * kV + k % kV;
                 if (c < n && (c < r.skip || c >= r.have)) f[k] = to_f32(row[c]);
             }
     }
@@ -369,16 +371,17 @@ struct OutRow {
         hi = (shift + n) / kG * kG - shift;
         if (hi < lo) hi = lo;
     }
-    __device__ __forceinline__ void send(uint32_t buf) const {   // one thread
-        if (hi > lo)
-            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
-                             reinterpret_cast<uintptr_t>(row + lo)),
-                         "r"(buf + static_cast<uint32_t>((shift + lo) * sizeof(T))),
-                         "r"(static_cast<uint32_t>((hi - lo) * sizeof(T)))
-                         : "memory");
-        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-    }
 };
+
+__device__ __forceinline__ void bulk_in(uint32_t to, const void *from, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
+                 "l"(from), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_out(void *to, uint32_t from, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(from), "r"(bytes)
+                 : "memory");
+}
 
 // kBwd: x and dy in, dx out, else x in, y out. A CTA holds one or more teams of `width` threads, each
 // with buffers and a named barrier of its own. The barrier of a sum over the row also tells that the
@@ -403,17 +406,32 @@ norm_ring_kernel(const T *x, const T *dy, const float *w, const float *b, T *out
     const T *end_x = x + rows * groups * n, *end_d = kBwd ? dy + rows * groups * n : nullptr;
     const int turns = at.first < rows ? static_cast<int>((rows - at.first + at.step - 1) / at.step) : 0;
     const int64_t o0 = (at.first * groups + at.g) * n, hop = at.step * groups * n;   // values between rows
-    auto fetch = [&](int64_t o, int st) {   // one thread of the team
+    // one thread of the team
+    auto fetch = [&](int64_t o, int st) {
         const uint32_t bar = bar0 + 8 * st, buf = s_ring + st * kIns * pitch;
-        const Row<T> rx(x, end_x, x + o, n);
-        if constexpr (kBwd) {
-            const Row<T> rd(dy, end_d, dy + o, n);
-            mbar_arrive_expect_tx(bar, rx.bytes + rd.bytes);
-            rd.fetch(buf + pitch, bar);
+        if constexpr (whole_rows<T, kV>()) {
+            const uint32_t bytes = n * static_cast<uint32_t>(sizeof(T));
+            mbar_arrive_expect_tx(bar, kIns * bytes);
+            bulk_in(buf, x + o, bytes, bar);
+            if constexpr (kBwd) bulk_in(buf + pitch, dy + o, bytes, bar);
         } else {
-            mbar_arrive_expect_tx(bar, rx.bytes);
+            const Row<T> rx(x, end_x, x + o, n), rd(kBwd ? dy : x, kBwd ? end_d : end_x, (kBwd ? dy : x) + o, n);
+            mbar_arrive_expect_tx(bar, rx.bytes + (kBwd ? rd.bytes : 0u));
+            if (rx.bytes) bulk_in(buf + rx.lead, reinterpret_cast<const char *>(rx.base - rx.shift) + rx.lead, rx.bytes, bar);
+            if (kBwd && rd.bytes)
+                bulk_in(buf + pitch + rd.lead, reinterpret_cast<const char *>(rd.base - rd.shift) + rd.lead, rd.bytes, bar);
         }
-        rx.fetch(buf, bar);
+    };
+    auto send = [&](T *to, uint32_t buf) {
+        if constexpr (whole_rows<T, kV>()) {
+            bulk_out(to, buf, n * static_cast<uint32_t>(sizeof(T)));
+        } else {
+            const OutRow<T> r(to, n);
+            if (r.hi > r.lo)
+                bulk_out(r.row + r.lo, buf + (r.shift + r.lo) * static_cast<uint32_t>(sizeof(T)),
+                         (r.hi - r.lo) * static_cast<uint32_t>(sizeof(T)));
+        }
+        tma_store_commit();
     };
     if (threadIdx.x == 0) lost = 0;
     if (lead) {
@@ -473,12 +491,12 @@ norm_ring_kernel(const T *x, const T *dy, const float *w, const float *b, T *out
         }
         fence_proxy_async_smem();   // this thread's part of the last output row, before the barrier
         if (lead)                   // the output buffer of two rows ago is read
-            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            tma_store_wait_read_all();
         if constexpr (kBwd) s = sum(s);
         else s.x = sum(s.x);
         if (lost) break;
         if (lead) {
-            if (t > 0) OutRow<T>(out + o - hop, n).send(s_outs + ((t - 1) & 1) * pitch);
+            if (t > 0) send(out + o - hop, s_outs + ((t - 1) & 1) * pitch);
             if (t + stages < turns) fetch(o + stages * hop, st);
         }
         if (++st == stages) {
@@ -507,8 +525,8 @@ norm_ring_kernel(const T *x, const T *dy, const float *w, const float *b, T *out
             }
         }
         uint8_t *to = outs + (t & 1) * pitch;
-        const OutRow<T> ro(out + o, n);
-        T *line = reinterpret_cast<T *>(to) + (kV > 1 ? 0 : ro.shift) + lane * kV;
+        const OutRow<T> ro(out + o, n);   // of whole rows not used
+        T *line = reinterpret_cast<T *>(to) + (whole_rows<T, kV>() ? 0 : ro.shift) + lane * kV;
         const float2 p0 = both(rs), p1 = both(-rs * s.x), p2 = both(-rs * s.y);
 #pragma unroll
         for (int i = 0; i < kN / 2; ++i)
@@ -518,21 +536,23 @@ norm_ring_kernel(const T *x, const T *dy, const float *w, const float *b, T *out
         for (int k = 0; k < kK; ++k) {
             const int c = (k * kWidth + lane) * kV;
             if (always(k, kWidth, kV, kN) || c < n) {
-                if (kV > 1 || (c >= ro.lo && c < ro.hi))
+                if (whole_rows<T, kV>() || (c >= ro.lo && c < ro.hi)) {
                     store<T, kV>(line + k * kWidth * kV, f + k * kV);
-                else
-                    ro.row[c] = from_f32<T>(f[k]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kV; ++i) ro.row[c + i] = from_f32<T>(f[k * kV + i]);
+                }
             }
         }
     }
     fence_proxy_async_smem();
     __syncthreads();
     if (lead) {
-        if (turns > 0 && t == turns) OutRow<T>(out + o - hop, n).send(s_outs + ((turns - 1) & 1) * pitch);
+        if (turns > 0 && t == turns) send(out + o - hop, s_outs + ((turns - 1) & 1) * pitch);
         if (lost)   // nothing may land after the CTA has ended
             for (int i = 0; i < stages; ++i)
                 for (uint32_t q = 0; q < 2; ++q) mbar_wait_bounded(bar0 + 8 * i, q, 100000u);
-        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        tma_store_wait_all();
     }
     if (lost && threadIdx.x == 0) atomicOr(err, kErrTimeout);
     if (kBwd && part) {   // one partial row of dw and of db per CTA: the teams add up one after the other
@@ -769,7 +789,7 @@ template <typename T, int kV>
 cudaError_t fwd_as(const Plan &p, const T *x, const float *w, const float *b, T *y, float *mean, float *rstd,
                    int64_t rows, int groups, int n, float eps, cudaStream_t s) {
     if (p.form == kRing)
-        return run_ring<T, kV == 16 / sizeof(T) ? kV : 1, false>(p, x, static_cast<const T *>(nullptr), w, b, y, mean,
+        return run_ring<T, kV, false>(p, x, static_cast<const T *>(nullptr), w, b, y, mean,
                                                                   rstd, static_cast<float *>(nullptr), rows, groups,
                                                                   n, eps, s);
     if (p.form == kLong)
@@ -785,7 +805,7 @@ template <typename T, int kV>
 cudaError_t bwd_as(const Plan &p, const T *dy, const T *x, const float *w, const float *mean, const float *rstd,
                    T *dx, float *part, int64_t rows, int groups, int n, cudaStream_t s) {
     if (p.form == kRing)
-        return run_ring<T, kV == 16 / sizeof(T) ? kV : 1, true>(p, x, dy, w, static_cast<const float *>(nullptr), dx,
+        return run_ring<T, kV, true>(p, x, dy, w, static_cast<const float *>(nullptr), dx,
                                                                  const_cast<float *>(mean),
                                                                  const_cast<float *>(rstd), part, rows, groups, n,
                                                                  0.f, s);
