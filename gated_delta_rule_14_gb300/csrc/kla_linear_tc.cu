@@ -406,6 +406,9 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
             if (src_t) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(src[(z + i) * kD + row]);
+            } else if ((reinterpret_cast<uintptr_t>(src) & 31) == 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) ld_global_v8(src + row * kD + z + 8 * i, r + 8 * i);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -419,6 +422,20 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         };
         const uint32_t t_s = tlane + TM_U + 64 * half;
         const uint32_t copy = sbase + OFF_S + half * kHalf;
+        if (have || (want_s && nchunk == 0)) {   // the start state; the first U replaces it where it is zero
+#pragma unroll 1
+            for (int k = 0; k < 2; ++k) {
+                uint32_t r[32];
+                if (have) {
+                    get(r, 64 * half + 32 * k);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) r[i] = 0u;
+                }
+                tmem_st32(t_s + 32 * k, r);
+            }
+            tmem_st_wait();
+        }
 
         for (int c = 0; c < nchunk; ++c) {
             const int cnt = count_of(c);
@@ -430,12 +447,8 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
 #pragma unroll 1
                 for (int k = 0; k < 2; ++k) {
                     uint32_t r[32];
-                    if (c > 0) {
-                        tmem_ld32(t_s + 32 * k, r);
-                        tmem_ld_wait();
-                    } else {
-                        get(r, 64 * half + 32 * k);
-                    }
+                    tmem_ld32(t_s + 32 * k, r);
+                    tmem_ld_wait();
                     if (!kStates) {   // operand copy: row = x channel, 128-byte swizzled rows of 64 z channels
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -493,20 +506,16 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
 #pragma unroll 1
             for (int k = 0; k < 2; ++k) {
                 uint32_t r[32];
-                if (nchunk > 0) {
-                    tmem_ld32(t_s + 32 * k, r);
-                    tmem_ld_wait();
-                } else if (src) {
-                    get(r, 64 * half + 32 * k);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) r[i] = 0u;
-                }
+                tmem_ld32(t_s + 32 * k, r);
+                tmem_ld_wait();
                 const int z = 64 * half + 32 * k;
                 if (dst_t) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) dst[(z + i) * kD + row] = __uint_as_float(r[i]);
-                } else {   // 16 bytes a lane and row: one value at a time took 12 us
+                } else if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {   // whole sectors of a row
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) st_global_v8(dst + row * kD + z + 8 * i, r + 8 * i);
+                } else {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         *reinterpret_cast<uint4 *>(dst + row * kD + z + 4 * i) =
