@@ -16,7 +16,7 @@
 #include <cfloat>
 #include <climits>
 
-#include "kla_internal.cuh"
+#include "layer_dev.cuh"
 #include "../../include/kla_layer.h"
 
 namespace kla {
@@ -337,16 +337,6 @@ __global__ void __launch_bounds__(kThreads) reorder_kernel(const uint4 *S, const
         if (i < words) out[static_cast<int64_t>(row) * words + i] = v[u];
     }
 }
-
-bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-struct Span {
-    uintptr_t lo, hi;
-};
-Span span(const void *p, size_t bytes) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return {a, p ? a + bytes : a};
-}
-bool overlaps(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi; }
 
 }  // namespace
 }  // namespace kla

@@ -418,18 +418,9 @@ cudaError_t launch_step(const void *q, const void *k, const void *v, const float
 }
 
 // ------------------------------------------------------------------------------------ host side
-bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool supported_d(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
 bool finite(float x) { return x - x == 0.0f; }
 
-struct Span {
-    uintptr_t lo, hi;
-};
-Span span(const void *p, size_t bytes) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return {a, p ? a + bytes : a};
-}
-bool overlaps(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi; }
 // The bytes that a strided [B, T, H, d] tensor reaches over.
 Span reach(const void *p, const int64_t *st, int B, int T, int H, int d, size_t esz) {
     if (B < 1 || T < 1 || H < 1) return span(p, 0);

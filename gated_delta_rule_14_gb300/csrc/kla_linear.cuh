@@ -12,7 +12,7 @@
 //     dv = back(k, q, dO, dS_T)         intra s, inter 1, update s        S_end = dS0
 #pragma once
 
-#include "kla_internal.cuh"
+#include "layer_dev.cuh"
 #include "../../include/kla_layer.h"
 
 namespace kla {

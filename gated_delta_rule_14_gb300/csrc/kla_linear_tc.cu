@@ -32,7 +32,6 @@
 #include <atomic>
 
 #include "kla_linear.cuh"
-#include "sm103_ptx.cuh"
 #include "warp_mma.cuh"
 
 namespace kla {

@@ -15,8 +15,7 @@
 #include <atomic>
 #include <climits>
 
-#include "kla_internal.cuh"
-#include "sm103_ptx.cuh"
+#include "layer_dev.cuh"
 #include "../../include/kla_layer.h"
 
 namespace kla {
@@ -723,16 +722,6 @@ Plan plan(int64_t rows, int groups, int n, kla_dtype dtype, bool bwd) {
     p.grid = static_cast<int>(want * groups);
     return p;
 }
-
-bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-struct Span {
-    uintptr_t lo, hi;
-};
-Span span(const void *p, size_t bytes) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return {a, p ? a + bytes : a};
-}
-bool overlaps(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi; }
 
 kla_status check(int64_t rows, int groups, int n, kla_dtype dtype) {
     if (rows < 0 || groups < 1 || n < 1) return KLA_ERR_INVALID_ARG;
