@@ -6,9 +6,9 @@
 // rises, the W best candidates of a request are among those lists: a second launch merges them by
 // (score, lowest beam, logit, lowest token).
 //
-// Both launches pick the W best of many in the same way. Among the eight warps' own bests (for W > 8:
-// second bests) the least is a threshold that W values or more reach; a random piece has ~22 of them
-// (~45). They are gathered in shared memory and each counts those ahead of it, which is its place.
+// Both launches pick the W best of many in the same way. The W-th best of the warps' best lanes (of eight
+// warps: best and second best) is a threshold that W values or more reach, and not many more. They are
+// gathered in shared memory and each counts those ahead of it, which is its place.
 // Only where more reach the threshold than fit (long runs of equal values) the W best are taken one
 // after the other. Taking them so everywhere cost 22.6 us for 64 rows of 100003 fp32 logits.
 //
@@ -36,7 +36,7 @@ __device__ __forceinline__ float value_of(uint32_t r) {
     return __uint_as_float(r & 0x80000000u ? r & 0x7fffffffu : ~r);
 }
 __device__ __forceinline__ float clean(float x) {   // NaN: -inf; +inf: the largest finite value
-    return x == x ? fminf(x, FLT_MAX) : -INFINITY;
+    return fminf(fmaxf(x, -INFINITY), FLT_MAX);
 }
 
 struct BeamScratch {   // per (beam, chunk): [B * W][nchunk] and the lists [..][W]
@@ -58,29 +58,31 @@ __device__ __forceinline__ Pair warp_best(Pair x) {
     return x;
 }
 
-// The threshold of the CTA: the least of its warps' `k`-th best lanes (k = 1 or 2; 0 where a warp has
-// fewer), and the best of all. One barrier; `slot` is two rows of kWarps.
-__device__ __forceinline__ void thresholds(uint32_t mine, int k, uint32_t (*slot)[kWarps], uint32_t &low,
-                                           uint32_t &high) {
+// The best value of the CTA, and a threshold that W <= 16 values or more reach: the W-th of its 32 warps'
+// best lanes, or of 8 warps' best and second best (0 where there are fewer). One barrier.
+template <int kCount>
+__device__ __forceinline__ void thresholds(uint32_t mine, int W, uint32_t (&slot)[32], uint32_t &low, uint32_t &high) {
+    static_assert(kCount == 32 || kCount == 8, "warps of the CTA");
+    constexpr int kPer = kCount == 32 ? 1 : 2;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     const uint32_t best = __reduce_max_sync(0xffffffffu, mine);
-    uint32_t kth = best;
-    if (k == 2) {
+    uint32_t second = 0;
+    if (kPer == 2) {
         const unsigned who = __ballot_sync(0xffffffffu, mine == best);
-        const bool first = mine == best && (threadIdx.x & 31) == __ffs(who) - 1;
-        kth = __reduce_max_sync(0xffffffffu, first ? 0u : mine);
+        second = __reduce_max_sync(0xffffffffu, lane == __ffs(who) - 1 ? 0u : mine);
     }
-    if ((threadIdx.x & 31) == 0) {
-        slot[0][threadIdx.x / 32] = best;
-        slot[1][threadIdx.x / 32] = kth;
-    }
+    if (lane < kPer) slot[warp * kPer + lane] = lane ? second : best;
     __syncthreads();
-    high = slot[0][0];
-    low = slot[1][0];
+    const uint32_t v = lane < kPer * kCount ? slot[lane] : 0u;
+    int ahead_of = 0;
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) {
-        high = max(high, slot[0][w]);
-        low = min(low, slot[1][w]);
+    for (int k = 0; k < kPer * kCount; ++k) {
+        const uint32_t o = __shfl_sync(0xffffffffu, v, k);
+        ahead_of += o > v || (o == v && k < lane);
     }
+    const unsigned at = __ballot_sync(0xffffffffu, lane < kPer * kCount && ahead_of == W - 1);
+    low = __shfl_sync(0xffffffffu, v, __ffs(at) - 1);
+    high = __reduce_max_sync(0xffffffffu, v);
 }
 
 constexpr int kGather = 256;   // values at or above the threshold that are ranked at once
@@ -111,36 +113,40 @@ beam_scan_kernel(const T *logits, int64_t row_stride, const unsigned char *finis
         }
         return;
     }
-    __shared__ uint32_t slot[2][kWarps];
+    __shared__ uint32_t slot[32];
     __shared__ unsigned long long got[kGather];
     __shared__ float part[kWarps];
     __shared__ int count;
     if (tid == 0) count = 0;
-    const T *x = logits + static_cast<int64_t>(row) * row_stride + c * kChunk + tid;
-    const int left = V - c * kChunk - tid;   // tokens from this thread's first on
-    // a whole piece is read without conditions: sixteen loads on their way (a condition on each had them wait
-    // for one another, 31 us for 64 rows of 100003 fp32 logits)
+    const T *x = logits + static_cast<int64_t>(row) * row_stride;   // V < 2^31: tokens in 32 bits
+    const int first = c * kChunk + tid, left = V - first;   // this thread's tokens are first, first + kThreads, ..
+    // sixteen loads on their way at once, of the last token where there is none (a condition on each had them
+    // wait for one another: 31 us for 64 rows of 100003 fp32 logits)
+    const bool whole = c * kChunk + kChunk <= V;
     T raw[kE];
-    if (c * kChunk + kChunk <= V) {
+    float e[kE];
+    if (whole) {
 #pragma unroll
-        for (int u = 0; u < kE; ++u) raw[u] = x[u * kThreads];
+        for (int u = 0; u < kE; ++u) raw[u] = x[first + u * kThreads];
+#pragma unroll
+        for (int u = 0; u < kE; ++u) e[u] = clean(to_f32(raw[u]));
     } else {
 #pragma unroll
-        for (int u = 0; u < kE; ++u) raw[u] = u * kThreads < left ? x[u * kThreads] : from_f32<T>(-INFINITY);
-    }
-    float e[kE];
+        for (int u = 0; u < kE; ++u) raw[u] = x[min(first + u * kThreads, V - 1)];
 #pragma unroll
-    for (int u = 0; u < kE; ++u) e[u] = clean(to_f32(raw[u]));
+        for (int u = 0; u < kE; ++u) e[u] = u * kThreads < left ? clean(to_f32(raw[u])) : -INFINITY;
+    }
     float own = e[0];
 #pragma unroll
     for (int u = 1; u < kE; ++u) own = fmaxf(own, e[u]);
     uint32_t low, high;
-    thresholds(left > 0 ? rank_of(own) : 0u, W > kWarps ? 2 : 1, slot, low, high);
+    thresholds<kWarps>(left > 0 ? rank_of(own) : 0u, W, slot, low, high);
     const float m = value_of(high), from = low ? value_of(low) : -INFINITY;
     float s = 0.f;
     if (m > -INFINITY) {
 #pragma unroll
-        for (int u = 0; u < kE; ++u) s += expf(e[u] - m);   // nothing: e^-inf
+        // e^(x - m), x - m rounded once; its error in units of the last place grows with m - x, as the term falls
+        for (int u = 0; u < kE; ++u) s += __expf(e[u] - m);   // nothing: e^-inf
     }
 #pragma unroll
     for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
@@ -210,11 +216,13 @@ beam_scan_kernel(const T *logits, int64_t row_stride, const unsigned char *finis
 }
 
 // One CTA per request: totals of the beams, then the W best of the lists' entries.
-__global__ void __launch_bounds__(kThreads)
+constexpr int kMerge = 1024;   // threads: 8192 entries are on their way at once
+
+__global__ void __launch_bounds__(kMerge)
 beam_merge_kernel(BeamScratch sc, const float *scores, const unsigned char *finished, int eos, float *new_scores,
                   int *parents, int *tokens, unsigned char *new_finished, int W, int nchunk) {
     __shared__ float Ms[kMaxW], logs[kMaxW], given[kMaxW];
-    __shared__ uint32_t slot[2][kWarps];
+    __shared__ uint32_t slot[32];
     __shared__ Pair got[kGather];
     __shared__ int count;
     const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
@@ -226,8 +234,8 @@ beam_merge_kernel(BeamScratch sc, const float *scores, const unsigned char *fini
     if (tid < W) given[tid] = scores[b * W + tid];
     dependency_wait();
 #pragma unroll
-    for (int u = 0; u < kFirst; ++u) first[u] = sc.rank[base * W + min(tid + u * kThreads, entries - 1)];
-    for (int w = warp; w < W; w += kWarps) {
+    for (int u = 0; u < kFirst; ++u) first[u] = sc.rank[base * W + min(tid + u * kMerge, entries - 1)];
+    for (int w = warp; w < W; w += kMerge / 32) {
         const float *m = sc.m + base + w * nchunk, *s = sc.s + base + w * nchunk;
         float M = -INFINITY, t = 0.f;
         for (int c = lane; c < nchunk; c += 32) M = fmaxf(M, m[c]);
@@ -268,14 +276,14 @@ beam_merge_kernel(BeamScratch sc, const float *scores, const unsigned char *fini
     uint32_t own = 0;
 #pragma unroll
     for (int u = 0; u < kFirst; ++u) {
-        const int i = tid + u * kThreads;
+        const int i = tid + u * kMerge;
         first[u] = i < entries ? key_of(i, first[u]) : 0u;
         own = max(own, first[u]);
     }
-    for (int i = tid + kFirst * kThreads; i < entries; i += kThreads)
+    for (int i = tid + kFirst * kMerge; i < entries; i += kMerge)
         own = max(own, key_of(i, sc.rank[base * W + i]));
     uint32_t low, high;
-    thresholds(own, W > kWarps ? 2 : 1, slot, low, high);
+    thresholds<kMerge / 32>(own, W, slot, low, high);
     auto gather = [&](int i, uint32_t key) {
         if (key && key >= low) {
             const int k = atomicAdd(&count, 1);
@@ -283,8 +291,8 @@ beam_merge_kernel(BeamScratch sc, const float *scores, const unsigned char *fini
         }
     };
 #pragma unroll
-    for (int u = 0; u < kFirst; ++u) gather(tid + u * kThreads, first[u]);
-    for (int i = tid + kFirst * kThreads; i < entries; i += kThreads) gather(i, key_of(i, sc.rank[base * W + i]));
+    for (int u = 0; u < kFirst; ++u) gather(tid + u * kMerge, first[u]);
+    for (int i = tid + kFirst * kMerge; i < entries; i += kMerge) gather(i, key_of(i, sc.rank[base * W + i]));
     __syncthreads();
     const int n = count;
     if (n <= kGather) {
@@ -300,7 +308,7 @@ beam_merge_kernel(BeamScratch sc, const float *scores, const unsigned char *fini
     Pair last{~0ull, ~0ull};
     for (int k = 0; k < W; ++k) {
         Pair p{0, 0};
-        for (int i = tid; i < entries; i += kThreads) {
+        for (int i = tid; i < entries; i += kMerge) {
             const Pair q = entry(i);
             if (q.a && ahead(last, q)) p = larger(p, q);
         }
@@ -309,7 +317,7 @@ beam_merge_kernel(BeamScratch sc, const float *scores, const unsigned char *fini
         __syncthreads();
         p = got[0];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) p = larger(p, got[w]);
+        for (int w = 1; w < kMerge / 32; ++w) p = larger(p, got[w]);
         last = p;
         if (tid == 0) put(k, p);
         __syncthreads();
@@ -392,7 +400,7 @@ kla_status kla_beam_select(const void *logits, int64_t row_stride, const float *
         beam_scan_kernel<<<grid, kThreads, 0, cs>>>(static_cast<const float *>(logits), row_stride, finished, eos, sc,
                                                     W, V, nchunk);
     if (cudaGetLastError() != cudaSuccess) return KLA_ERR_CUDA;
-    return launch_dependent(beam_merge_kernel, B, kThreads, 0, cs, sc, scores, finished, eos, new_scores, parents,
+    return launch_dependent(beam_merge_kernel, B, kMerge, 0, cs, sc, scores, finished, eos, new_scores, parents,
                             tokens, new_finished, W, nchunk) == cudaSuccess
                ? KLA_OK
                : KLA_ERR_CUDA;

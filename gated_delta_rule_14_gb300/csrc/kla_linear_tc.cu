@@ -699,16 +699,31 @@ bool lin_tc_supports(const LinScan &p, kla_dtype dtype) {
            tma_rows(p.z, p.zs, p.B, p.T, p.H);
 }
 
+// Segments by their cost in microseconds, as measured: a launch starts and ends in ~8 and the three launches
+// of a cut sequence in ~17; a chunk takes 1.9, or its share of the memory's rate (128 KB, of which the
+// segment's own state takes half, in 0.95; four fifths where the scans of a backward pass share tiles in L2).
+// 48 chains of 1000 tokens: 25 in one piece, 38 in two; 16 of 2000: 36 in one, 27 in eight; backward, 8
+// chains of 16384: 136 in four, 105 in six.
 void lin_tc_plan(LinScan &p, int scans) {
     constexpr int kSms = 152;
     const int nchunk = (p.T + kC - 1) / kC;
     const long ctas = static_cast<long>(p.B) * p.H * scans;
-    long n = ctas >= kSms ? 1 : kSms / ctas;
-    if (n > nchunk / 4) n = nchunk / 4;
-    if (n < 1) n = 1;
-    const int len = static_cast<int>((nchunk + n - 1) / n);
-    p.seg_len = (len > 0 ? len : 1) * kC;
-    p.nseg = nchunk > 0 ? (nchunk + len - 1) / len : 1;
+    auto chunk_us = [scans](double least, double kb, long on) {
+        const double fed = (scans > 1 ? 0.8 : 1.0) * kb * 1e-3 * static_cast<double>(on) / 6.78;
+        return fed > least ? fed : least;
+    };
+    int best = nchunk > 0 ? nchunk : 1;
+    double least = 8 + chunk_us(1.9, 131, ctas) * nchunk;
+    for (int n = 2; n <= nchunk && n * ctas <= kSms; ++n) {
+        const int len = (nchunk + n - 1) / n;
+        const double cost = 17 + (chunk_us(1.9, 131, n * ctas) + chunk_us(0.95, 66, n * ctas)) * len;
+        if (cost < 1.02 * least) {   // of equals the one on more SMs
+            if (cost < least) least = cost;
+            best = len;
+        }
+    }
+    p.seg_len = best * kC;
+    p.nseg = nchunk > 0 ? (nchunk + best - 1) / best : 1;
 }
 
 cudaError_t launch_lin_tc(const LinScan *p, int scans, cudaStream_t stream) {
