@@ -3,9 +3,9 @@
 //   forward    y = xh w[g] + b[g],  xh = (x - mean) rstd
 //   backward   dx = rstd (u - mean(u) - xh mean(u xh)),  u = dy w[g];  dw[g] = sum dy xh;  db[g] = sum dy
 //
-// Every value is read once: a row belongs to one team of threads (16 or 32 lanes up to 512 values, a
-// whole CTA above), each with kE values at fixed columns. Teams are persistent and keep to one group,
-// so that weight and bias, and in the backward pass the sums of dw and db, stay in registers; the sums
+// Here rows of more than 512 values; shorter ones are in kla_norm_rows.cu. Every value is read once: a row
+// belongs to a team of threads, each with values at fixed columns. Teams are persistent and keep to one
+// group, so that weight and bias, and in the backward pass the sums of dw and db, stay in registers; the sums
 // leave as one partial row per CTA and a second launch adds those in a fixed order.
 // What bounds it is the memory, and to keep it busy ~70 KB have to be on the way to every SM. Rows of a
 // CTA therefore come and go through shared memory by bulk copies, several rows ahead, which cost no
@@ -15,17 +15,16 @@
 #include <atomic>
 #include <climits>
 
-#include "layer_dev.cuh"
-#include "../../include/kla_layer.h"
+#include "kla_norm.cuh"
 
 namespace kla {
 cudaError_t device_error_word(unsigned **out);   // kla_api.cu
 namespace {
 
+using namespace norm;
+
 constexpr int kSms = 152;
-constexpr int kE = 16;                 // values of one thread
 constexpr int kMaxBlock = 1024;
-constexpr int kTeamMost = 32 * kE;     // longest row of a part of a warp
 constexpr int kRingMostN = 8192;       // longest row that goes through shared memory
 constexpr int kRingMost = 4;           // rows on the way to a team, at most
 // Values of one thread: the backward pass keeps five arrays of them, the forward pass three. The more, the
@@ -35,50 +34,6 @@ constexpr int ring_values(bool bwd) { return bwd ? 16 : 32; }
 // forward pass two.
 constexpr int ring_block(bool bwd) { return bwd ? 512 : 256; }
 
-// kV consecutive values of type T, moved in one access.
-template <typename T, int kV>
-__device__ __forceinline__ void load(const T *p, T *x) {
-    if constexpr (sizeof(T) * kV == 16) {
-        *reinterpret_cast<uint4 *>(x) = *reinterpret_cast<const uint4 *>(p);
-    } else if constexpr (sizeof(T) * kV == 4) {
-        *reinterpret_cast<uint32_t *>(x) = *reinterpret_cast<const uint32_t *>(p);
-    } else {
-#pragma unroll
-        for (int i = 0; i < kV; ++i) x[i] = p[i];
-    }
-}
-template <typename T, int kV>
-__device__ __forceinline__ void store(T *p, const float *x) {
-    if constexpr (sizeof(T) * kV == 16) {
-        uint4 r;
-        T *e = reinterpret_cast<T *>(&r);
-#pragma unroll
-        for (int i = 0; i < kV; ++i) e[i] = from_f32<T>(x[i]);
-        *reinterpret_cast<uint4 *>(p) = r;
-    } else if constexpr (kV == 2) {
-        uint32_t r;
-        T *e = reinterpret_cast<T *>(&r);
-        e[0] = from_f32<T>(x[0]);
-        e[1] = from_f32<T>(x[1]);
-        *reinterpret_cast<uint32_t *>(p) = r;
-    } else {
-#pragma unroll
-        for (int i = 0; i < kV; ++i) p[i] = from_f32<T>(x[i]);
-    }
-}
-
-__device__ __forceinline__ float add(float a, float b) { return a + b; }
-__device__ __forceinline__ float2 add(float2 a, float2 b) { return make_float2(a.x + b.x, a.y + b.y); }
-__device__ __forceinline__ float across(float v, int off) { return __shfl_xor_sync(0xffffffffu, v, off); }
-__device__ __forceinline__ float2 across(float2 v, int off) { return make_float2(across(v.x, off), across(v.y, off)); }
-
-// Sum over the `lanes` lanes of a row's team.
-template <int kLanes, typename V>
-__device__ __forceinline__ V lane_sum(V v) {
-#pragma unroll
-    for (int off = kLanes / 2; off; off >>= 1) v = add(v, across(v, off));
-    return v;
-}
 // Sum over kWarps warps that share a named barrier; calls alternate between two buffers, so that one
 // barrier a sum does.
 template <int kWarps>
@@ -98,194 +53,6 @@ struct WarpsSum {
         return v;
     }
 };
-
-// Which rows a thread's team of `width` threads walks: rows first, first + step, .. of group g.
-struct Walk {
-    int lane, width, g;
-    int64_t first, step;
-    __device__ Walk(int groups, int threads) {
-        g = blockIdx.x % groups;
-        width = threads;
-        lane = threadIdx.x % threads;
-        const int teams = blockDim.x / threads;
-        first = static_cast<int64_t>(blockIdx.x / groups) * teams + threadIdx.x / threads;
-        step = static_cast<int64_t>(gridDim.x / groups) * teams;
-    }
-};
-
-// One thread's values of a row as they are in memory.
-template <typename T, int kV>
-struct Held {
-    alignas(16) T v[kE];
-    __device__ __forceinline__ void get(const T *row, int lane, int width, int n, bool live) {
-#pragma unroll
-        for (int k = 0; k < kE / kV; ++k) {
-            const int c = (k * width + lane) * kV;
-            if (live && c < n) {
-                load<T, kV>(row + c, v + k * kV);
-            } else {
-#pragma unroll
-                for (int i = 0; i < kV; ++i) v[k * kV + i] = from_f32<T>(0.f);
-            }
-        }
-    }
-};
-
-template <typename T, int kV, int kTeam>
-__global__ void __launch_bounds__(256)
-norm_fwd_kernel(const T *x, const float *w, const float *b, T *y, float *mean, float *rstd, int64_t rows, int groups,
-                int n, float eps) {
-    constexpr int kK = kE / kV;
-    const Walk at(groups, kTeam);
-    float wr[kE], br[kE];
-#pragma unroll
-    for (int k = 0; k < kK; ++k)
-#pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            const int c = (k * at.width + at.lane) * kV + i;
-            wr[k * kV + i] = w && c < n ? w[static_cast<int64_t>(at.g) * n + c] : 1.f;
-            br[k * kV + i] = b && c < n ? b[static_cast<int64_t>(at.g) * n + c] : 0.f;
-        }
-    // every lane of a warp takes the same number of turns (the sums use whole warps)
-    const int64_t turns = (rows + at.step - 1) / at.step;
-    const float inv = 1.f / n;
-    Held<T, kV> next;   // the next row is on its way while this one is worked on
-    next.get(x + (at.first * groups + at.g) * n, at.lane, at.width, n, at.first < rows);
-    for (int64_t t = 0; t < turns; ++t) {
-        const int64_t r = at.first + t * at.step;
-        const bool live = r < rows;
-        const int64_t row = r * groups + at.g;
-        float v[kE];
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < kE; ++i) {
-            v[i] = to_f32(next.v[i]);
-            s += v[i];
-        }
-        next.get(x + (row + at.step * groups) * n, at.lane, at.width, n, r + at.step < rows);
-        const float mu = lane_sum<kTeam>(s) * inv;
-        float q = 0.f;
-#pragma unroll
-        for (int k = 0; k < kK; ++k)
-            if ((k * at.width + at.lane) * kV < n)
-#pragma unroll
-                for (int i = 0; i < kV; ++i) {
-                    const float d = v[k * kV + i] - mu;
-                    q = fmaf(d, d, q);
-                }
-        const float rs = 1.f / sqrtf(lane_sum<kTeam>(q) * inv + eps);
-        if (!live) continue;
-        if (at.lane == 0) {
-            if (mean) mean[row] = mu;
-            if (rstd) rstd[row] = rs;
-        }
-#pragma unroll
-        for (int k = 0; k < kK; ++k) {
-            const int c = (k * at.width + at.lane) * kV;
-            if (c < n) {
-                float o[kV];
-#pragma unroll
-                for (int i = 0; i < kV; ++i) o[i] = fmaf((v[k * kV + i] - mu) * rs, wr[k * kV + i], br[k * kV + i]);
-                store<T, kV>(y + row * n + c, o);
-            }
-        }
-    }
-}
-
-template <typename T, int kV, int kTeam>
-__global__ void __launch_bounds__(256)
-norm_bwd_kernel(const T *dy, const T *x, const float *w, const float *mean, const float *rstd, T *dx, float *part,
-                int64_t rows, int groups, int n) {
-    dependency_release();
-    constexpr int kK = kE / kV;
-    const Walk at(groups, kTeam);
-    float wr[kE], dw[kE], db[kE];
-#pragma unroll
-    for (int k = 0; k < kK; ++k)
-#pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            const int c = (k * at.width + at.lane) * kV + i;
-            wr[k * kV + i] = w && c < n ? w[static_cast<int64_t>(at.g) * n + c] : 1.f;
-            dw[k * kV + i] = db[k * kV + i] = 0.f;
-        }
-    const int64_t turns = (rows + at.step - 1) / at.step;
-    const float inv = 1.f / n;
-    Held<T, kV> nx, nd;   // the next row is on its way while this one is worked on
-    float nmu = 0.f, nrs = 0.f;
-    auto fetch = [&](int64_t r) {
-        const int64_t row = r * groups + at.g;
-        const bool live = r < rows;
-        nx.get(x + row * n, at.lane, at.width, n, live);
-        nd.get(dy + row * n, at.lane, at.width, n, live);
-        if (live) {
-            nmu = mean[row];
-            nrs = rstd[row];
-        }
-    };
-    fetch(at.first);
-    for (int64_t t = 0; t < turns; ++t) {
-        const int64_t r = at.first + t * at.step;
-        const bool live = r < rows;
-        const int64_t row = r * groups + at.g;
-        const float mu = nmu, rs = nrs;
-        float xh[kE], d[kE];
-#pragma unroll
-        for (int i = 0; i < kE; ++i) {
-            xh[i] = to_f32(nx.v[i]);
-            d[i] = to_f32(nd.v[i]);
-        }
-        fetch(r + at.step);
-        float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < kK; ++k)
-            if ((k * at.width + at.lane) * kV < n)
-#pragma unroll
-                for (int i = k * kV; i < k * kV + kV; ++i) {
-                    xh[i] = (xh[i] - mu) * rs;
-                    dw[i] = fmaf(d[i], xh[i], dw[i]);
-                    db[i] += d[i];
-                    d[i] *= wr[i];
-                    s.x += d[i];
-                    s.y = fmaf(d[i], xh[i], s.y);
-                }
-        s = lane_sum<kTeam>(s);
-        if (!live) continue;
-        s.x *= inv;
-        s.y *= inv;
-#pragma unroll
-        for (int k = 0; k < kK; ++k) {
-            const int c = (k * at.width + at.lane) * kV;
-            if (c < n) {
-                float o[kV];
-#pragma unroll
-                for (int i = 0; i < kV; ++i) o[i] = rs * (d[k * kV + i] - s.x - xh[k * kV + i] * s.y);
-                store<T, kV>(dx + row * n + c, o);
-            }
-        }
-    }
-    if (!part) return;
-    // one partial row of dw and of db per CTA
-    float *pw = part + static_cast<int64_t>(blockIdx.x) * 2 * n, *pb = pw + n;
-    __shared__ float acc[256 * kE];   // [team][column]
-    constexpr int kTeams = 256 / kTeam, kCols = kTeam * kE;
-#pragma unroll
-    for (int pass = 0; pass < 2; ++pass) {
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kK; ++k)
-#pragma unroll
-            for (int i = 0; i < kV; ++i)
-                acc[threadIdx.x / kTeam * kCols + (k * kTeam + at.lane) * kV + i] =
-                    pass ? db[k * kV + i] : dw[k * kV + i];
-        __syncthreads();
-        for (int c = threadIdx.x; c < n; c += 256) {
-            float s = 0.f;
-#pragma unroll
-            for (int q = 0; q < kTeams; ++q) s += acc[q * kCols + c];
-            (pass ? pb : pw)[c] = s;
-        }
-    }
-}
 
 // ---- rows of a CTA, through shared memory
 // A row's buffer mirrors the memory around it: the 16-byte granules that the row touches, copied in one
@@ -310,9 +77,9 @@ struct Row {
     }
 };
 // Whether the columns of a thread's k-th access exist for every lane: a row has more than half of the
-// values that its team holds (the narrowest team: more than kTeamMost).
+// values that its team holds (the narrowest team: more than kRowsMost).
 __device__ __forceinline__ constexpr bool always(int k, int width, int v, int e) {
-    return (k + 1) * width * v <= kTeamMost || 2 * (k + 1) * v <= e;
+    return (k + 1) * width * v <= kRowsMost || 2 * (k + 1) * v <= e;
 }
 // kN values, kV at a time, of a thread; zero from column n on. Accesses of 16 bytes: every row starts and
 // ends on 16 bytes, and its buffer starts with it.
@@ -678,7 +445,7 @@ __global__ void __launch_bounds__(kMaxBlock) norm_bwd_long_kernel(const T *dy, c
 }
 
 // ------------------------------------------------------------------------------------ host side
-enum Form { kTeams, kRing, kLong };
+enum Form { kRows, kRing, kLong };
 struct Plan {
     Form form;
     int width;           // threads of a row's team
@@ -686,17 +453,17 @@ struct Plan {
     int stages, pitch, smem;   // kRing: rows on the way to a team, bytes of a row's buffer, bytes of a CTA
 };
 
-// The smallest team that holds the row; persistent CTAs as many as the SMs hold at once, a multiple of
+// The smallest team that holds the row (of a row in the ring); persistent CTAs as many as the SMs hold at once, a multiple of
 // the groups, none without a row.
 Plan plan(int64_t rows, int groups, int n, kla_dtype dtype, bool bwd) {
     Plan p{};
-    p.form = n <= kTeamMost ? kTeams : n <= kRingMostN ? kRing : kLong;
+    p.form = n <= kRowsMost ? kRows : n <= kRingMostN ? kRing : kLong;
+    if (p.form == kRows) {
+        if (bwd) p.grid = norm_rows_bwd_grid(rows, groups);   // the forward pass launches by itself
+        return p;
+    }
     int per_sm = 1;
-    if (p.form == kTeams) {
-        p.width = n <= 16 * kE ? 16 : 32;
-        p.block = 256;
-        per_sm = bwd ? 2 : 3;
-    } else if (p.form == kRing) {
+    if (p.form == kRing) {
         const int least = 32 * ring_values(bwd);   // what a warp holds
         p.width = n <= 2 * least ? (n <= least ? 32 : 64) : n <= 4 * least ? 128 : n <= 8 * least ? 256 : 512;
         const int most = ring_block(bwd);
@@ -781,13 +548,8 @@ cudaError_t fwd_as(const Plan &p, const T *x, const float *w, const float *b, T 
         return run_ring<T, kV, false>(p, x, static_cast<const T *>(nullptr), w, b, y, mean,
                                                                   rstd, static_cast<float *>(nullptr), rows, groups,
                                                                   n, eps, s);
-    if (p.form == kLong)
-        norm_fwd_long_kernel<T><<<static_cast<int>(rows * groups), kMaxBlock, 0, s>>>(x, w, b, y, mean, rstd, groups,
-                                                                                     n, eps);
-    else if (p.width == 16)
-        norm_fwd_kernel<T, kV, 16><<<p.grid, p.block, 0, s>>>(x, w, b, y, mean, rstd, rows, groups, n, eps);
-    else
-        norm_fwd_kernel<T, kV, 32><<<p.grid, p.block, 0, s>>>(x, w, b, y, mean, rstd, rows, groups, n, eps);
+    norm_fwd_long_kernel<T><<<static_cast<int>(rows * groups), kMaxBlock, 0, s>>>(x, w, b, y, mean, rstd, groups, n,
+                                                                                 eps);
     return cudaGetLastError();
 }
 template <typename T, int kV>
@@ -798,12 +560,7 @@ cudaError_t bwd_as(const Plan &p, const T *dy, const T *x, const float *w, const
                                                                  const_cast<float *>(mean),
                                                                  const_cast<float *>(rstd), part, rows, groups, n,
                                                                  0.f, s);
-    if (p.form == kLong)
-        norm_bwd_long_kernel<T><<<p.grid, kMaxBlock, 0, s>>>(dy, x, w, mean, rstd, dx, part, rows, groups, n);
-    else if (p.width == 16)
-        norm_bwd_kernel<T, kV, 16><<<p.grid, p.block, 0, s>>>(dy, x, w, mean, rstd, dx, part, rows, groups, n);
-    else
-        norm_bwd_kernel<T, kV, 32><<<p.grid, p.block, 0, s>>>(dy, x, w, mean, rstd, dx, part, rows, groups, n);
+    norm_bwd_long_kernel<T><<<p.grid, kMaxBlock, 0, s>>>(dy, x, w, mean, rstd, dx, part, rows, groups, n);
     return cudaGetLastError();
 }
 
@@ -815,6 +572,7 @@ cudaError_t fwd_typed(const void *xv, const float *w, const float *b, void *yv, 
     T *y = static_cast<T *>(yv);
     const Plan p = plan(rows, groups, n, dtype, false);
     const int v = width<T>(n, x, y, y);
+    if (p.form == kRows) return norm_rows_fwd(x, w, b, y, mean, rstd, rows, groups, n, dtype, v, eps, s);
     if (v == 16 / sizeof(T)) return fwd_as<T, 16 / sizeof(T)>(p, x, w, b, y, mean, rstd, rows, groups, n, eps, s);
     if (sizeof(T) == 2 && v == 2)
         return fwd_as<T, sizeof(T) == 2 ? 2 : 1>(p, x, w, b, y, mean, rstd, rows, groups, n, eps, s);
@@ -827,6 +585,7 @@ cudaError_t bwd_typed(const void *dyv, const void *xv, const float *w, const flo
     T *dx = static_cast<T *>(dxv);
     const Plan p = plan(rows, groups, n, dtype, true);
     const int v = width<T>(n, x, dy, dx);
+    if (p.form == kRows) return norm_rows_bwd(dy, x, w, mean, rstd, dx, part, rows, groups, n, dtype, v, s);
     if (v == 16 / sizeof(T)) return bwd_as<T, 16 / sizeof(T)>(p, dy, x, w, mean, rstd, dx, part, rows, groups, n, s);
     if (sizeof(T) == 2 && v == 2)
         return bwd_as<T, sizeof(T) == 2 ? 2 : 1>(p, dy, x, w, mean, rstd, dx, part, rows, groups, n, s);
