@@ -93,7 +93,7 @@ kla_status kla_linear_step(const void *q, const void *k, const void *v, const fl
  *   mean, rstd  fp32 [rows, groups], written (NULL: not wanted)
  *   rows >= 0, groups >= 1, 3 <= n <= 65536 (the normalised values of one or two values do not
  *   depend on them but for eps, and their gradient is what rounding leaves: KLA_ERR_UNSUPPORTED)
- * Statistics are taken in fp32 about the mean (two passes over the values, which stay on the SM).
+ * Statistics are taken in fp32 about the mean: squares are summed of differences, never of values.
  */
 kla_status kla_layer_norm_fwd(const void *x, const float *weight, const float *bias, void *y, float *mean,
                               float *rstd, int64_t rows, int groups, int n, kla_dtype dtype, float eps,
@@ -102,7 +102,8 @@ kla_status kla_layer_norm_fwd(const void *x, const float *weight, const float *b
 /*
  * Gradients of kla_layer_norm_fwd given dy [rows, groups, n] and the forward's mean and rstd:
  * dx (dtype), dweight and dbias (fp32 [groups, n]; NULL: not wanted). The sums over the rows are
- * taken in a fixed order: equal calls give equal bits.
+ * taken in a fixed order: equal calls give equal bits. The workspace may be NULL where n <= 8192 and
+ * neither dweight nor dbias is wanted.
  */
 kla_status kla_layer_norm_bwd(const void *dy, const void *x, const float *weight, const float *mean,
                               const float *rstd, void *dx, float *dweight, float *dbias, int64_t rows, int groups,

@@ -167,3 +167,40 @@ def test_refusals():
         kla.layer_norm_bwd(x[:2], x, w, mean, rstd)
     with pytest.raises(kla.KlaError):
         kla.layer_norm_bwd(x.clone(), x, w, mean, rstd, workspace=torch.empty(8, device=DEV))
+
+
+# rows longer than a CTA holds: few and many rows, whose sums of dw and db come from several CTAs
+@pytest.mark.parametrize("rows", [1, 5, 1300])
+@pytest.mark.parametrize("n,dtype", [(8200, torch.bfloat16), (8202, torch.bfloat16), (8193, torch.float32)])
+def test_many_long_rows(rows, n, dtype):
+    check((rows, n), (n,), dtype, seed=rows)
+
+
+def test_long_rows_whose_weights_fit_no_wide_access():
+    """The weights start 4 bytes past a 16-byte boundary; the same values on one give the same gradients to
+    the sums' order (fp32, 1e-5) and y to one bf16 rounding (4e-3)."""
+    import gated_delta_rule_14_gb300 as kla
+    gen = torch.Generator(device=DEV).manual_seed(9)
+    n = 8208
+    x, dy = (torch.randn((37, n), generator=gen, device=DEV).bfloat16() for _ in range(2))
+    flat = torch.randn(2 * n + 1, generator=gen, device=DEV)
+    w, b = flat[1:n + 1], flat[n + 1:]
+    y, mean, rstd = kla.layer_norm_fwd(x, w, b)
+    dx, dw, db = kla.layer_norm_bwd(dy, x, w, mean, rstd)
+    ref = reference(x, w, b, 1e-5, dy)
+    for got, want, t in zip((y, mean, rstd, dx, dw, db), ref, (4e-3, 1e-5, 1e-5, 4e-3, 1e-5, 1e-5)):
+        assert rel(got, want) <= t
+
+
+def test_long_rows_without_weights_and_with_a_large_offset():
+    """As test_large_offset: the offset of 1000 costs 6e-5 of the spread through the mean's rounding, 2e-4."""
+    import gated_delta_rule_14_gb300 as kla
+    x = torch.randn(33, 9001, device=DEV) + 1000
+    y, mean, rstd = kla.layer_norm_fwd(x)
+    d = x.double()
+    want = (d - d.mean(-1, keepdim=True)) / (d.var(-1, correction=0, keepdim=True) + 1e-5).sqrt()
+    assert rel(y, want) <= 2e-4
+    c = torch.full((4, 8201), 3.0, device=DEV)
+    y, mean, rstd = kla.layer_norm_fwd(c)
+    dx, dw, db = kla.layer_norm_bwd(torch.ones_like(c), c, None, mean, rstd)
+    assert not y.any() and not dx.any() and not dw.any() and torch.equal(db, torch.full((8201,), 4.0, device=DEV))
