@@ -12,6 +12,10 @@
 // Only where more reach the threshold than fit (long runs of equal values) the W best are taken one
 // after the other. Taking them so everywhere cost 22.6 us for 64 rows of 100003 fp32 logits.
 //
+// Measured with cold caches, 8 requests of 8 such beams: 13 us for the pass (26 MB, 29 % of a copy's rate; bound by
+// instructions and by the pieces' barriers, 2.1 issued a cycle) and 9 us for the merge (eight CTAs, one after the other
+// dependent steps behind barriers), whose launch overlaps the pass; 15 to 18 us together.
+//
 // Logits are ranked through an order-preserving map to 32-bit whole numbers (0 marks "nothing").
 #include <cfloat>
 #include <climits>
@@ -324,6 +328,7 @@ beam_merge_kernel(BeamScratch sc, const float *scores, const unsigned char *fini
     }
 }
 
+// A copy through an index, bound by the memory: 64 beams of 8 MB, of which 42 are read, 132 us (6.8 TB/s).
 constexpr int kCopy = 4;   // 16-byte words of one thread and turn
 
 __global__ void __launch_bounds__(kThreads) reorder_kernel(const uint4 *S, const int *parents, uint4 *out, int W,

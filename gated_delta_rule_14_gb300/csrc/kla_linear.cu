@@ -72,6 +72,9 @@ __device__ __forceinline__ void take(const float *p, float (&x)[kN]) {
 // fp32 pipe: each of the products (X Y^T, P Z, X S and Y^T Z) is a 16 x 16 grid of threads with a tile of
 // registers each, fed with 16-byte loads from operands laid out along the tile (X and Y also transposed),
 // one load for eight multiply-adds. `states`: only the segment's own contribution, from zero.
+// Measured, 2 x 1000 tokens of 4 heads of 64: forward 33 us, backward 64 us, each cut into one chunk a CTA; the launch
+// over all chunks takes 19 us of which the products are ~4 at the fp32 pipe's rate: one chunk's chain of loads and
+// barriers, with one or two CTAs an SM.
 template <typename T, int kX, int kZ>
 __global__ void __launch_bounds__(kThreads) lin_scan_kernel(const __grid_constant__ Scans all, const int states) {
     constexpr int kR = kX / 16, kU = kZ / 16;   // state rows and columns of a thread
@@ -271,6 +274,8 @@ __global__ void __launch_bounds__(kThreads) lin_scan_kernel(const __grid_constan
         }
 }
 
+// Start states of a chain's segments, S' = g^n S + Z, one element a thread: the loads of a chain do not depend on one
+// another. 8 us for nine segments of 16 heads of 128 x 128.
 __global__ void __launch_bounds__(kThreads) lin_combine_kernel(const __grid_constant__ Scans all) {
     const LinScan &p = all.s[blockIdx.z];
     dependency_release();
@@ -339,7 +344,8 @@ cudaError_t launch_scan(const LinScan *p, int scans, cudaStream_t stream) {
 
 // ---------------------------------------------------------------------------- single-token step
 // One CTA per (sequence, head) and kZ value channels: every state element is read once, decayed,
-// written to and reduced against the query on the way out.
+// written to and reduced against the query on the way out. Bound by the memory: 128 x 24 states of 128 x 128 take
+// 60 us (6.75 TB/s, 99 % of a copy's rate); 64 x 16, which L2 holds, 14 us; 1 x 16 2.2 us, a launch's latency.
 template <typename T, int kZ>
 __global__ void __launch_bounds__(kThreads) lin_step_kernel(const T *q, const T *k, const T *v, const float *decay,
                                                             const int *parent, const float *S, float *S_out, T *o,
