@@ -70,22 +70,28 @@ __device__ __forceinline__ void take(const float *p, float (&x)[kN]) {
 
 // fp32 scan of one segment of one (sequence, head) and kZ value channels, chunk by chunk. Bound by the
 // fp32 pipe: each of the products (X Y^T, P Z, X S and Y^T Z) is a 16 x 16 grid of threads with a tile of
-// registers each, fed with 16-byte loads from operands laid out along the tile (X and Y also transposed),
-// one load for eight multiply-adds. `states`: only the segment's own contribution, from zero.
-// Measured, 2 x 1000 tokens of 4 heads of 64: forward 33 us, backward 64 us, each cut into one chunk a CTA; the launch
-// over all chunks takes 19 us of which the products are ~4 at the fp32 pipe's rate: one chunk's chain of loads and
-// barriers, with one or two CTAs an SM.
+// registers each, fed with 16-byte loads from operands laid out along the tile (X and Y transposed; P takes Y's
+// place), one load for eight to eleven multiply-adds. `states`: only the segment's own contribution, from zero.
+// Measured, 2 x 1000 tokens of 4 heads of 64, cut into one chunk a CTA: forward 32 us, backward 62 us, in three
+// launches each that are one chunk's chain of loads and barriers long; 8 x 1024 tokens of 16 heads of 128: 575 and
+// 1680 us, a third of the fp32 pipe's rate. Y in both orders, P beside it, X read once for each of its products and the
+// last chunk's state always taken took 34, 64, 653 and 1932; registers for three CTAs an SM of the 64 x 64 tiles
+// (80, some spilled) 593 instead of 443 for 8 x 2048 tokens of 16 heads.
+template <int kX, int kZ>
+constexpr int kScanFloats = (kX + (kX > kC ? kX : kC)) * kPitch + (kC + kX) * (kZ + 4) + kC + 1;
+
+constexpr int scan_ctas(int x, int z) { return x < 128 || z < 64 ? 2 : 1; }   // an SM's shared memory holds
+
 template <typename T, int kX, int kZ>
-__global__ void __launch_bounds__(kThreads) lin_scan_kernel(const __grid_constant__ Scans all, const int states) {
+__global__ void __launch_bounds__(kThreads, scan_ctas(kX, kZ)) lin_scan_kernel(const __grid_constant__ Scans all, const int states) {
     constexpr int kR = kX / 16, kU = kZ / 16;   // state rows and columns of a thread
-    constexpr int kYp = kX + 4, kZp = kZ + 4;
+    constexpr int kZp = kZ + 4;
     extern __shared__ __align__(16) float sm[];
     float *Xt = sm;                    // [x][token]
     float *Yt = Xt + kX * kPitch;      // [x][token]
-    float *Y = Yt + kX * kPitch;       // [token][x]
-    float *Z = Y + kC * kYp;           // [token][z]
-    float *Pt = Z + kC * kZp;          // [column][row]
-    float *S = Pt + kC * kPitch;       // [x][z]
+    float *Pt = Yt;                    // [column][row], once Y is used up
+    float *Z = Yt + (kX > kC ? kX : kC) * kPitch;   // [token][z]
+    float *S = Z + kC * kZp;           // [x][z]
     float *gp = S + kX * kZp;          // g^0 .. g^kC
     const LinScan &p = all.s[blockIdx.z];
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4, nz = p.dz / kZ;
@@ -122,6 +128,7 @@ __global__ void __launch_bounds__(kThreads) lin_scan_kernel(const __grid_constan
     const float a_intra = p.a_intra, a_inter = p.a_inter, a_upd = p.a_upd;
 
     const int nchunk = (t_stop - t_begin + kC - 1) / kC;
+    const bool wanted = p.ST && seg == p.nseg - 1;
     for (int ci = 0; ci < nchunk; ++ci) {
         const int c = reverse ? nchunk - 1 - ci : ci;
         const int t0 = t_begin + c * kC;
@@ -160,13 +167,11 @@ __global__ void __launch_bounds__(kThreads) lin_scan_kernel(const __grid_constan
                 x[q][u] = ok ? x[q][u] : 0.f;
                 y[q][u] = ok ? y[q][u] : 0.f;
             }
-            *reinterpret_cast<float4 *>(Y + t * kYp + d) = make_float4(y[q][0], y[q][1], y[q][2], y[q][3]);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) Yt[(d + u) * kPitch + t] = y[q][u];
             if (!states)
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    Xt[(d + u) * kPitch + t] = x[q][u];
-                    Yt[(d + u) * kPitch + t] = y[q][u];
-                }
+                for (int u = 0; u < 4; ++u) Xt[(d + u) * kPitch + t] = x[q][u];
         }
 #pragma unroll
         for (int q = 0; q < kNz; ++q) {
@@ -181,87 +186,90 @@ __global__ void __launch_bounds__(kThreads) lin_scan_kernel(const __grid_constan
 #pragma unroll
                 for (int u = 0; u < kU; ++u) S[(ty * kR + r) * kZp + tx * kU + u] = s[r][u];
         __syncthreads();
+        float a[4][4] = {}, e[4][kU] = {};   // X Y^T and X S, which take the same values of X
         if (!states) {
-            float a[4][4] = {};
 #pragma unroll 4
             for (int d = 0; d < kX; ++d) {
-                float x[4], y[4];
+                float x[4], y[4], z[kU];
                 take<4>(Xt + d * kPitch + 4 * ty, x);
                 take<4>(Yt + d * kPitch + 4 * tx, y);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) a[i][q] = fmaf(x[i], y[q], a[i][q]);
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float w[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int dist = reverse ? 4 * tx + q - 4 * ty - i : 4 * ty + i - 4 * tx - q;
-                    w[i] = dist >= 0 ? a_intra * gp[dist] * a[i][q] : 0.f;
-                }
-                *reinterpret_cast<float4 *>(Pt + (4 * tx + q) * kPitch + 4 * ty) = make_float4(w[0], w[1], w[2], w[3]);
-            }
-            __syncthreads();
-            float o[4][kU] = {}, e[4][kU] = {};
-            // a warp's eight rows: columns on the mask's side only
-            const int row0 = (tid >> 5) * 8, j0 = reverse ? row0 : 0, j1 = reverse ? kC : row0 + 8;
-#pragma unroll 4
-            for (int q = j0; q < j1; ++q) {
-                float w[4], z[kU];
-                take<4>(Pt + q * kPitch + 4 * ty, w);
-                take<kU>(Z + q * kZp + kU * tx, z);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int u = 0; u < kU; ++u) o[i][u] = fmaf(w[i], z[u], o[i][u]);
-            }
-#pragma unroll 4
-            for (int d = 0; d < kX; ++d) {
-                float x[4], z[kU];
-                take<4>(Xt + d * kPitch + 4 * ty, x);
                 take<kU>(S + d * kZp + kU * tx, z);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) a[i][q] = fmaf(x[i], y[q], a[i][q]);
 #pragma unroll
                     for (int u = 0; u < kU; ++u) e[i][u] = fmaf(x[i], z[u], e[i][u]);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = 4 * ty + i;
-                if (t0 + t < t_stop) {
-                    const bool ok = t < cnt;
-                    const float w = ok ? a_inter * gp[reverse ? cnt - 1 - t : t + 1] : 0.f;
-                    T *dst = og + (t0 + t) * o_step + kU * tx;
-#pragma unroll
-                    for (int u = 0; u < kU; ++u) dst[u] = from_f32<T>(ok ? fmaf(w, e[i][u], o[i][u]) : 0.f);
                 }
             }
         }
-        if (cnt > 0) {
+        // the state moves on, where it is taken up again: a segment's last one only at the sequence's end
+        if (cnt > 0 && (states || wanted || ci + 1 < nchunk)) {
             const float gn = gp[cnt];
             float upd[kR][kU] = {};
-#pragma unroll 4
-            for (int q = 0; q < kC; ++q) {
-                float y[kR], z[kU];
-                take<kR>(Y + q * kYp + kR * ty, y);
-                take<kU>(Z + q * kZp + kU * tx, z);
-                const float w = q < cnt ? gp[reverse ? q + 1 : cnt - 1 - q] : 0.f;
+#pragma unroll 2
+            for (int q0 = 0; q0 < kC; q0 += 4) {
+                float y[kR][4];
 #pragma unroll
-                for (int u = 0; u < kU; ++u) z[u] *= w;
+                for (int r = 0; r < kR; ++r) take<4>(Yt + (kR * ty + r) * kPitch + q0, y[r]);
 #pragma unroll
-                for (int r = 0; r < kR; ++r)
+                for (int j = 0; j < 4; ++j) {
+                    const int q = q0 + j;
+                    float z[kU];
+                    take<kU>(Z + q * kZp + kU * tx, z);
+                    const float w = q < cnt ? gp[reverse ? q + 1 : cnt - 1 - q] : 0.f;
 #pragma unroll
-                    for (int u = 0; u < kU; ++u) upd[r][u] = fmaf(y[r], z[u], upd[r][u]);
+                    for (int u = 0; u < kU; ++u) z[u] *= w;
+#pragma unroll
+                    for (int r = 0; r < kR; ++r)
+#pragma unroll
+                        for (int u = 0; u < kU; ++u) upd[r][u] = fmaf(y[r][j], z[u], upd[r][u]);
+                }
             }
 #pragma unroll
             for (int r = 0; r < kR; ++r)
 #pragma unroll
                 for (int u = 0; u < kU; ++u) s[r][u] = fmaf(gn, s[r][u], a_upd * upd[r][u]);
         }
+        if (states) continue;
+        __syncthreads();   // Y is used up
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int dist = reverse ? 4 * tx + q - 4 * ty - i : 4 * ty + i - 4 * tx - q;
+                w[i] = dist >= 0 ? a_intra * gp[dist] * a[i][q] : 0.f;
+            }
+            *reinterpret_cast<float4 *>(Pt + (4 * tx + q) * kPitch + 4 * ty) = make_float4(w[0], w[1], w[2], w[3]);
+        }
+        __syncthreads();
+        float o[4][kU] = {};
+        // a warp's eight rows: columns on the mask's side only
+        const int row0 = (tid >> 5) * 8, j0 = reverse ? row0 : 0, j1 = reverse ? kC : row0 + 8;
+#pragma unroll 4
+        for (int q = j0; q < j1; ++q) {
+            float w[4], z[kU];
+            take<4>(Pt + q * kPitch + 4 * ty, w);
+            take<kU>(Z + q * kZp + kU * tx, z);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int u = 0; u < kU; ++u) o[i][u] = fmaf(w[i], z[u], o[i][u]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = 4 * ty + i;
+            if (t0 + t < t_stop) {
+                const bool ok = t < cnt;
+                const float w = ok ? a_inter * gp[reverse ? cnt - 1 - t : t + 1] : 0.f;
+                T *dst = og + (t0 + t) * o_step + kU * tx;
+#pragma unroll
+                for (int u = 0; u < kU; ++u) dst[u] = from_f32<T>(ok ? fmaf(w, e[i][u], o[i][u]) : 0.f);
+            }
+        }
     }
-    if (!states && !(p.ST && seg == p.nseg - 1)) return;
+    if (!states && !wanted) return;
 #pragma unroll
     for (int r = 0; r < kR; ++r)
 #pragma unroll
@@ -309,8 +317,7 @@ __global__ void __launch_bounds__(kThreads) lin_combine_kernel(const __grid_cons
 
 template <typename T, int kX, int kZ>
 cudaError_t launch_scan_as(const LinScan *p, int scans, cudaStream_t stream) {
-    constexpr int kBytes =
-        (2 * kX * kPitch + kC * (kX + 4) + kC * (kZ + 4) + kC * kPitch + kX * (kZ + 4) + kC + 1) * 4;
+    constexpr int kBytes = kScanFloats<kX, kZ> * 4;
     auto kern = lin_scan_kernel<T, kX, kZ>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return e;

@@ -4,9 +4,9 @@ with its gradients (``layer_norm_fwd``, ``layer_norm_bwd``) and beam search's se
 following their beams (``beam_select``, ``reorder_states``).
 
 The binding checks and marshals; every operation runs in this package's CUDA kernels on the current
-stream of the tensors' device. Small calls are bound by the host, so each function first asks in one
-expression whether everything is as it should be, and only where it is not goes through the arguments
-one by one to name the one at fault.
+stream of the tensors' device. Small calls are bound by the host, so linear attention's functions first
+ask in one expression whether everything is as it should be, and only where it is not go through the
+arguments one by one to name the one at fault.
 """
 from __future__ import annotations
 
@@ -257,9 +257,9 @@ def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias:
                    eps: float = 1e-5, *, out: Optional[torch.Tensor] = None, stats: bool = True):
     """Layer norm over the last axis: ``y = (x - mean) / sqrt(var + eps) * weight + bias``.
 
-    x: [..., n] bf16 or fp32, 3 <= n <= 65536; weight, bias: fp32 [n], or [H, n] for x [..., H, n] (every head's output with
-    weights of its own). Returns (y in x's dtype, mean, rstd fp32 [...] for the backward pass, or None, None
-    without ``stats``).
+    x: [..., n] bf16 or fp32, 3 <= n <= 65536; weight, bias: fp32 [n], or [H, n] for x [..., H, n] (every head's
+    output with weights of its own). Returns (y in x's dtype, mean, rstd fp32 [...] for the backward pass, or
+    None, None without ``stats``).
     """
     device = _device("x", x)
     code = _code("x", x)
