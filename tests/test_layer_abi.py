@@ -114,3 +114,16 @@ def test_beam(lib):
     assert r(A, A + M, A, 1, 2, 64, None) == 1 and r(A, A + M, A + 2 * M, 1, 2, 24, None) == 1
     assert r(A, None, A + 2 * M, 1, 2, 64, None) == 1 and r(A + 8, A + M, A + 2 * M, 1, 2, 64, None) == 1
     assert r(A, A + M, A + 2 * M, 0, 2, 64, None) == 1 and r(A, A + M, A + 2 * M, 70000, 1, 64, None) == 2
+
+
+def test_long_norm_rows_need_their_workspace(lib):
+    """Rows of more than 8192 values keep two sums of each row in the workspace, wanted weights' gradients or
+    not; its size is those sums, to 16 bytes, and the partial rows in front of which they lie."""
+    def g(dw, ws, wb, n=9000, rows=3):
+        return lib.kla_layer_norm_bwd(A, A + M, None, A + 2 * M, A + 3 * M, A + 4 * M, dw, None, rows, 1, n, 1, ws, wb,
+                                      None)
+    assert g(None, None, 0) == 1 and g(None, A + 8 * M, 31) == 1 and g(A + 6 * M, A + 8 * M, 32) == 1
+    assert g(None, A, 32) == 1   # over dy
+    size = lib.kla_layer_norm_bwd_workspace_size(3, 1, 9000, 1)
+    assert size >= 32 + 2 * 9000 * 4 and (size - 32) % (2 * 9000 * 4) == 0
+    assert g(A + 6 * M, A + 8 * M, size - 1) == 1
