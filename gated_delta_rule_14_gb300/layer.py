@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 from typing import Optional, Tuple
 
 import torch
@@ -367,8 +368,9 @@ def reorder_states(S: torch.Tensor, parents: torch.Tensor, *, out: Optional[torc
         out = torch.empty_like(S)
     else:
         _check("out", out, shape, S.dtype, device)
+    # from the shape: an axis of one element may have any stride in a contiguous tensor
     st = _native.lib().kla_reorder_states(S.data_ptr(), parents.data_ptr(), out.data_ptr(), B, W,
-                                          S.stride(1) * S.element_size(), _stream(device))
+                                          math.prod(shape[2:]) * S.element_size(), _stream(device))
     if st:
         _native.check(st, "kla_reorder_states")
     return out

@@ -1,0 +1,48 @@
+"""What the Python binding of include/kla_layer.h passes to the native library, on the CPU: a stand-in for the
+library records every call, and host tensors stand for device ones."""
+import pytest
+import torch
+
+from gated_delta_rule_14_gb300 import _native, layer
+
+
+class Library:
+    """Answers every entry point with success and keeps its arguments; workspaces are empty."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def entry(*args):
+            if name.endswith("_workspace_size"):
+                return 0
+            self.calls.append((name, args))
+            return 0
+        return entry
+
+
+@pytest.fixture
+def library(monkeypatch):
+    lib = Library()
+    monkeypatch.setattr(_native, "lib", lambda: lib)
+    monkeypatch.setattr(layer, "_device", lambda name, t: t.device)
+    monkeypatch.setattr(layer, "_check", lambda *a: None)
+    monkeypatch.setattr(layer, "_stream", lambda device: 0)
+    layer._size.cache_clear()
+    yield lib
+    layer._size.cache_clear()
+
+
+@pytest.mark.parametrize("make", [
+    lambda: torch.zeros(1, 3, 2, 16, 16).transpose(0, 1),   # three requests of one beam
+    lambda: torch.zeros(1, 4, 2, 16, 16)[:, ::4],           # the first beam of one request
+    lambda: torch.zeros(3, 1, 2, 16, 16),
+    lambda: torch.zeros(2, 4, 2, 16, 16),
+])
+def test_a_state_has_the_bytes_of_its_shape(library, make):
+    """An axis of one element may have any stride in a contiguous tensor, so a state's size is not a stride."""
+    S = make()
+    assert S.is_contiguous()
+    layer.reorder_states(S, torch.zeros(S.shape[:2], dtype=torch.int32))
+    (name, args), = library.calls
+    assert name == "kla_reorder_states" and args[3:6] == (S.shape[0], S.shape[1], 2 * 16 * 16 * 4)
