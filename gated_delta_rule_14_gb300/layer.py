@@ -287,17 +287,22 @@ def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias:
 
 
 def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor], mean: torch.Tensor,
-                   rstd: torch.Tensor, *, workspace: Optional[torch.Tensor] = None):
+                   rstd: torch.Tensor, *, bias: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None):
     """Gradients of ``layer_norm_fwd`` given its x, weight, mean and rstd: (dx in x's dtype, dweight, dbias
-    fp32, shaped like weight; [n] without a weight). Equal calls give equal bits."""
+    fp32, shaped like the parameters). ``bias``: the forward's, whose values are not read; it is needed where
+    there is no weight and the bias is one of [H, n], as it alone says then that heads have gradients of their
+    own (with neither, dweight and dbias are [n]). Equal calls give equal bits."""
     device = _device("x", x)
     code = _code("x", x)
-    rows, groups, n, shape = _norm_shape(x, weight, None)
+    rows, groups, n, shape = _norm_shape(x, weight, bias)
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
     _check("dy", dy, x.shape, x.dtype, device)
     if weight is not None:
         _check("weight", weight, shape, _F32, device)
+    if bias is not None:
+        _check("bias", bias, shape, _F32, device)
     _check("mean", mean, x.shape[:-1], _F32, device)
     _check("rstd", rstd, x.shape[:-1], _F32, device)
     dx = torch.empty_like(x)

@@ -204,3 +204,29 @@ def test_long_rows_without_weights_and_with_a_large_offset():
     y, mean, rstd = kla.layer_norm_fwd(c)
     dx, dw, db = kla.layer_norm_bwd(torch.ones_like(c), c, None, mean, rstd)
     assert not y.any() and not dx.any() and not dw.any() and torch.equal(db, torch.full((8201,), 4.0, device=DEV))
+
+
+@pytest.mark.parametrize("shape", [(7, 5, 64), (3, 4, 2, 640), (2, 3, 8200)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_bias_per_head_without_a_weight(shape, dtype):
+    """The bias' axes say how the forward took x apart; its gradient, and the unit weight's, are per head too."""
+    import gated_delta_rule_14_gb300 as kla
+    gen = torch.Generator(device=DEV).manual_seed(shape[-1])
+    x, dy = (torch.randn(shape, generator=gen, device=DEV).to(dtype) for _ in range(2))
+    b = torch.randn(shape[-2:], generator=gen, device=DEV)
+    y, mean, rstd = kla.layer_norm_fwd(x, None, b)
+    dx, dw, db = kla.layer_norm_bwd(dy, x, None, mean, rstd, bias=b)
+    ref = reference(x, torch.ones_like(b), b, 1e-5, dy)
+    tol = 4e-3 if dtype == torch.bfloat16 else 1e-5
+    for got, want, t in zip((y, mean, rstd, dx, dw, db), ref, (tol, 1e-5, 1e-5, tol, 1e-5, 1e-5)):
+        assert got.shape == want.shape and rel(got, want) <= t
+
+
+def test_backward_checks_the_bias():
+    import gated_delta_rule_14_gb300 as kla
+    x = torch.randn(4, 6, 32, device=DEV)
+    _, mean, rstd = kla.layer_norm_fwd(x)
+    with pytest.raises(ValueError):
+        kla.layer_norm_bwd(x, x.clone(), None, mean, rstd, bias=torch.ones(5, 32, device=DEV))
+    with pytest.raises(ValueError):
+        kla.layer_norm_bwd(x, x.clone(), torch.ones(32, device=DEV), mean, rstd, bias=torch.ones(6, 32, device=DEV))

@@ -46,3 +46,14 @@ def test_a_state_has_the_bytes_of_its_shape(library, make):
     layer.reorder_states(S, torch.zeros(S.shape[:2], dtype=torch.int32))
     (name, args), = library.calls
     assert name == "kla_reorder_states" and args[3:6] == (S.shape[0], S.shape[1], 2 * 16 * 16 * 4)
+
+
+def test_bias_per_head_without_a_weight_has_its_gradient(library):
+    """The forward takes heads apart by the bias' axes where there is no weight, and the backward has to do the same."""
+    x, b = torch.randn(4, 6, 32), torch.zeros(6, 32)
+    y, mean, rstd = layer.layer_norm_fwd(x, None, b)
+    dx, dw, db = layer.layer_norm_bwd(x.clone(), x, None, mean, rstd, bias=b)
+    (_, fwd), (_, bwd) = library.calls
+    assert fwd[6:9] == bwd[8:11] == (4, 6, 32) and dw.shape == db.shape == (6, 32)
+    _, dw, db = layer.layer_norm_bwd(x.clone(), x, None, mean, rstd)   # no parameters, or those of the last axis
+    assert library.calls[-1][1][8:11] == (24, 1, 32) and dw.shape == db.shape == (32,)
