@@ -84,6 +84,8 @@ def _declare(lib):
         getattr(lib, f"kla_{name}_workspace_size").restype = sz
     lib.kla_selftest_wait_timeout.argtypes = [ctypes.c_uint, vp]
     lib.kla_selftest_wait_timeout.restype = ctypes.c_int
+    lib.kla_selftest_team_timeout.argtypes = [ctypes.c_uint, vp, vp]
+    lib.kla_selftest_team_timeout.restype = ctypes.c_int
     lib.kla_device_status.argtypes = [vp]
     lib.kla_device_status.restype = ctypes.c_int
     lib.kla_status_string.argtypes = [ctypes.c_int]

@@ -27,7 +27,6 @@ namespace {
 using namespace norm;
 
 constexpr int kSms = 152;
-constexpr int kMaxBlock = 1024;
 constexpr int kRingMostN = 8192;       // longest row that goes through shared memory
 constexpr int kRingMost = 4;           // rows on the way to a team, at most
 // Values of one thread: the backward pass keeps five arrays of them, the forward pass three. The more, the
@@ -36,26 +35,6 @@ constexpr int ring_values(bool bwd) { return bwd ? 16 : 32; }
 // Threads of a CTA: the backward pass takes one CTA an SM, so that an SM leaves one partial row; the
 // forward pass two.
 constexpr int ring_block(bool bwd) { return bwd ? 512 : 256; }
-
-// Sum over kWarps warps that share a named barrier; calls alternate between two buffers, so that one
-// barrier a sum does.
-template <int kWarps>
-struct WarpsSum {
-    float2 (*part)[kMaxBlock / 32];   // [2][warps of the CTA]
-    int first, bar, turn;             // the team's first warp and barrier
-    template <typename V>
-    __device__ __forceinline__ V operator()(V v) {
-        v = lane_sum<32>(v);
-        V *slot = reinterpret_cast<V *>(part[turn] + first);
-        if ((threadIdx.x & 31) == 0) slot[(threadIdx.x / 32) % kWarps] = v;
-        ptx::named_sync(bar, 32 * kWarps);
-        v = slot[0];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) v = add(v, slot[w]);
-        turn ^= 1;
-        return v;
-    }
-};
 
 // ---- rows of a CTA, through shared memory
 // A row's buffer mirrors the memory around it: the 16-byte granules that the row touches, copied in one
@@ -165,9 +144,10 @@ norm_ring_kernel(const T *x, const T *dy, const float *w, const float *b, T *out
     extern __shared__ __align__(128) uint8_t sm[];
     __shared__ uint64_t full[ring_block(kBwd) / kWidth][kRingMost];
     __shared__ float2 sums[2][kMaxBlock / 32];
-    __shared__ int lost;
+    __shared__ int lost[ring_block(kBwd) / kWidth][2];
     const Walk at(groups, kWidth);
     const int team = threadIdx.x / kWidth, lane = at.lane;
+    const TeamLost gave_up{lost[team]};
     WarpsSum<kWidth / 32> sum{sums, team * (kWidth / 32), 1 + team, 0};
     const bool lead = lane == 0;
     uint8_t *ring = sm + team * (stages * kIns + 2) * pitch, *outs = ring + stages * kIns * pitch;
@@ -204,8 +184,8 @@ norm_ring_kernel(const T *x, const T *dy, const float *w, const float *b, T *out
         }
         tma_store_commit();
     };
-    if (threadIdx.x == 0) lost = 0;
     if (lead) {
+        gave_up.init();
         for (int i = 0; i < stages; ++i) mbar_init(bar0 + 8 * i, 1);
         fence_mbar_init();
         for (int i = 0; i < stages && i < turns; ++i) fetch(o0 + i * hop, i);
@@ -237,7 +217,7 @@ norm_ring_kernel(const T *x, const T *dy, const float *w, const float *b, T *out
             nmu = mean[row + at.step * groups];
             nrs = rstd[row + at.step * groups];
         }
-        if (!mbar_wait_bounded(bar0 + 8 * st, phase, 100000u)) lost = 1;
+        if (!mbar_wait_bounded(bar0 + 8 * st, phase, 100000u)) gave_up.note(t);
         const uint8_t *buf = ring + st * kIns * pitch;
         float2 v[kN / 2], d[kN / 2];
         get_row<T, kV, kWidth, kN>(x, end_x, x + o, buf, lane, n, v);
@@ -265,7 +245,7 @@ norm_ring_kernel(const T *x, const T *dy, const float *w, const float *b, T *out
             tma_store_wait_read_all();
         if constexpr (kBwd) s = sum(s);
         else s.x = sum(s.x);
-        if (lost) break;
+        if (gave_up.read(t)) break;
         if (lead) {
             if (t > 0) send(out + o - hop, s_outs + ((t - 1) & 1) * pitch);
             if (t + stages < turns) fetch(o + stages * hop, st);
@@ -320,12 +300,18 @@ norm_ring_kernel(const T *x, const T *dy, const float *w, const float *b, T *out
     __syncthreads();
     if (lead) {
         if (turns > 0 && t == turns) send(out + o - hop, s_outs + ((turns - 1) & 1) * pitch);
-        if (lost)   // nothing may land after the CTA has ended
-            for (int i = 0; i < stages; ++i)
-                for (uint32_t q = 0; q < 2; ++q) mbar_wait_bounded(bar0 + 8 * i, q, 100000u);
+        if (t < turns) {   // a wait gave up in turn t
+            atomicOr(err, kErrTimeout);
+            for (int u = t; u < turns && u < t + stages; ++u) {   // nothing may land after the CTA has ended
+                mbar_wait_bounded(bar0 + 8 * st, phase, 100000u);
+                if (++st == stages) {
+                    st = 0;
+                    phase ^= 1;
+                }
+            }
+        }
         tma_store_wait_all();
     }
-    if (lost && threadIdx.x == 0) atomicOr(err, kErrTimeout);
     if (kBwd && part) {   // one partial row of dw and of db per CTA: the teams add up one after the other
         float *fw = reinterpret_cast<float *>(sm), *fb = fw + n;
         for (int q = 0; q < static_cast<int>(blockDim.x) / kWidth; ++q) {

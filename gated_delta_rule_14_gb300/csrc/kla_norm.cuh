@@ -8,6 +8,7 @@
 namespace kla {
 
 constexpr int kRowsMost = 512;   // longest row that a part of a warp holds
+constexpr int kMaxBlock = 1024;
 
 // CTAs of the backward pass over rows of up to kRowsMost values: a multiple of the groups, and the same for
 // every width of access, so that its scratch is.
@@ -77,6 +78,36 @@ struct Walk {
         first = static_cast<int64_t>(blockIdx.x / groups) * teams + threadIdx.x / threads;
         step = static_cast<int64_t>(gridDim.x / groups) * teams;
     }
+};
+
+// Sum over kWarps warps that share a named barrier; calls alternate between two buffers, so that one
+// barrier a sum does.
+template <int kWarps>
+struct WarpsSum {
+    float2 (*part)[kMaxBlock / 32];   // [2][warps of the CTA]
+    int first, bar, turn;             // the team's first warp and barrier
+    template <typename V>
+    __device__ __forceinline__ V operator()(V v) {
+        v = lane_sum<32>(v);
+        V *slot = reinterpret_cast<V *>(part[turn] + first);
+        if ((threadIdx.x & 31) == 0) slot[(threadIdx.x / 32) % kWarps] = v;
+        ptx::named_sync(bar, 32 * kWarps);
+        v = slot[0];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) v = add(v, slot[w]);
+        turn ^= 1;
+        return v;
+    }
+};
+// Whether a wait of the team has given up, which its threads decide alike: one that left alone would leave the
+// others at a barrier that it never reaches. A thread notes its own time-out before the barrier of the turn's
+// sum and reads the team's word after it. Turns alternate between two words: a thread may be on its way through
+// the next turn while another still reads, but passes that turn's barrier only with it.
+struct TeamLost {
+    volatile int *word;   // [2]
+    __device__ void init() const { word[0] = word[1] = 0; }
+    __device__ __forceinline__ void note(int turn) const { word[turn & 1] = 1; }
+    __device__ __forceinline__ bool read(int turn) const { return word[turn & 1] != 0; }
 };
 
 }  // namespace norm

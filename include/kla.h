@@ -316,6 +316,15 @@ kla_status kla_device_status(void *stream);
  */
 kla_status kla_selftest_wait_timeout(unsigned limit_polls, void *stream);
 
+/*
+ * The same for teams of threads that share a CTA, as in the layer norm's kernels (kla_layer.h): four teams
+ * of 64 threads walk 20000 turns of a wait, a sum and a barrier of their own; the first team's wait of its
+ * second turn is one that nothing completes. That team leaves as one, the others finish.
+ *   turns   device int32 [256], written: turns that each thread has completed (1 for the first team's 64,
+ *           20000 for the others)
+ */
+kla_status kla_selftest_team_timeout(unsigned limit_polls, int *turns, void *stream);
+
 /* Static, human-readable name of a status code. */
 const char *kla_status_string(kla_status status);
 

@@ -25,3 +25,21 @@ def test_bounded_wait_timeout_is_reported_and_recovered():
     o_ref, s_ref = oracle_chains(inp)
     assert oracle.rel_l2(o[0].transpose(1, 0, 2), o_ref) <= 1e-2
     assert oracle.rel_l2(S[0], s_ref) <= 1e-2
+
+
+@pytest.mark.parametrize("limit", [20, 50, 100])   # the time-out falls on different turns of the other teams
+def test_a_team_that_gives_up_leaves_as_one(limit):
+    """Four teams of one CTA with barriers of their own: the first gives up in its second turn, and every one
+    of its threads leaves there; the other teams finish their turns, and the time-out is reported once."""
+    import torch
+
+    import gated_delta_rule_14_gb300 as kla
+    lib = kla._native.lib()
+    stream = torch.cuda.current_stream(DEV).cuda_stream
+    kla.device_status(DEV)
+    for _ in range(20):
+        turns = torch.full((256,), -1, dtype=torch.int32, device=DEV)
+        assert lib.kla_selftest_team_timeout(limit, turns.data_ptr(), stream) == 0
+        assert lib.kla_device_status(stream) == kla._native.KLA_ERR_TIMEOUT
+        assert turns.tolist() == [1] * 64 + [20000] * 192
+    assert lib.kla_device_status(stream) == kla._native.KLA_OK

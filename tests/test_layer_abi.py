@@ -127,3 +127,8 @@ def test_long_norm_rows_need_their_workspace(lib):
     size = lib.kla_layer_norm_bwd_workspace_size(3, 1, 9000, 1)
     assert size >= 32 + 2 * 9000 * 4 and (size - 32) % (2 * 9000 * 4) == 0
     assert g(A + 6 * M, A + 8 * M, size - 1) == 1
+
+
+def test_team_selftest_rejects_its_arguments_on_host(lib):
+    assert lib.kla_selftest_team_timeout(0, A, None) == 1 and lib.kla_selftest_team_timeout(100001, A, None) == 1
+    assert lib.kla_selftest_team_timeout(10, None, None) == 1 and lib.kla_selftest_team_timeout(10, A + 2, None) == 1
