@@ -86,6 +86,8 @@ def _declare(lib):
     lib.kla_selftest_wait_timeout.restype = ctypes.c_int
     lib.kla_selftest_team_timeout.argtypes = [ctypes.c_uint, vp, vp]
     lib.kla_selftest_team_timeout.restype = ctypes.c_int
+    lib.kla_selftest_warp_timeout.argtypes = [ctypes.c_uint, vp, vp]
+    lib.kla_selftest_warp_timeout.restype = ctypes.c_int
     lib.kla_device_status.argtypes = [vp]
     lib.kla_device_status.restype = ctypes.c_int
     lib.kla_status_string.argtypes = [ctypes.c_int]

@@ -9,6 +9,8 @@ namespace kla {
 cudaError_t launch_selftest_wait(unsigned *err, unsigned limit, cudaStream_t stream);
 // one team of a CTA gives up, the others go on (kla_selftest.cu)
 cudaError_t launch_selftest_teams(unsigned *err, int *turns, unsigned limit, cudaStream_t stream);
+// one warp of a CTA gives up and calls the others out of their waits (kla_selftest.cu)
+cudaError_t launch_selftest_warps(unsigned *err, int *turns, unsigned limit, cudaStream_t stream);
 // several tokens per call on the pipelined decode tile walk (kla_decode.cu): T <= kShortSeqMaxT,
 // d_k = 128, d_v a multiple of 32, 16-byte aligned q, k, v, states and per-channel gates
 bool tokens_pipe_supports(const ChunkArgs &a);
@@ -328,6 +330,16 @@ kla_status kla_selftest_team_timeout(unsigned limit_polls, int *turns, void *str
     unsigned *err = nullptr;
     if (err_word(&err) != cudaSuccess) return KLA_ERR_CUDA;
     return kla::launch_selftest_teams(err, turns, limit_polls, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? KLA_OK
+               : KLA_ERR_CUDA;
+}
+
+kla_status kla_selftest_warp_timeout(unsigned limit_polls, int *turns, void *stream) {
+    if (limit_polls < 1 || limit_polls > 100000 || !turns || reinterpret_cast<uintptr_t>(turns) % 4)
+        return KLA_ERR_INVALID_ARG;
+    unsigned *err = nullptr;
+    if (err_word(&err) != cudaSuccess) return KLA_ERR_CUDA;
+    return kla::launch_selftest_warps(err, turns, limit_polls, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? KLA_OK
                : KLA_ERR_CUDA;
 }

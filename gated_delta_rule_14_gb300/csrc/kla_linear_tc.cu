@@ -192,8 +192,9 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     const uint32_t tbase = sm.tmem_base;
     const uint32_t tlane = tbase + (static_cast<uint32_t>((warp & 3) * 32) << 16);
 
-    // False once any wait of the CTA has given up: every loop then ends.
-    auto wait = [&](uint32_t bar, int phase) {
+    // False once any wait of the CTA has given up: every loop then ends. By whole warps.
+    auto wait = [&](uint32_t bar, int phase) { return warp_wait(bar, phase & 1, kWaitLimit, &sm.abort); };
+    auto wait_alone = [&](uint32_t bar, int phase) {   // one thread, with nobody to agree with
         for (uint32_t i = 0; i < kWaitLimit; ++i) {
             if (mbar_try_wait_sleep(bar, phase & 1, 20000u)) return true;
             if (sm.abort) return false;
@@ -250,15 +251,15 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
             for (int c = kNs; c < nchunk; ++c) {
                 const int before = c / kNs - 1, at = 8 * (c % kNs);
                 last[0] = last[1] = last[2] = c;
-                if (!wait(b_yfree + at, before)) break;
+                if (!wait_alone(b_yfree + at, before)) break;
                 load(job.y, kY, b_fy, c);
                 last[0] = c + 1;
                 if (!kStates) {
-                    if (!wait(b_xfree + at, before)) break;
+                    if (!wait_alone(b_xfree + at, before)) break;
                     load(job.x, 0, b_fx, c);
                     last[1] = c + 1;
                 }
-                if (!wait(b_zfree + at, before)) break;
+                if (!wait_alone(b_zfree + at, before)) break;
                 load(job.z, kZt, b_fz, c);
                 last[2] = c + 1;
             }

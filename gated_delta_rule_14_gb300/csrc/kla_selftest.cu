@@ -4,8 +4,8 @@
 // gives up, the kernel records kErrTimeout in the device error word, skips its remaining work
 // and exits cleanly, so the context stays usable and kla_device_status reports
 // KLA_ERR_TIMEOUT. These kernels run that path on purpose: one thread waits, with the same
-// bounded wait, on a barrier phase that nothing completes; and one team of a CTA does, beside
-// teams that go on.
+// bounded wait, on a barrier phase that nothing completes; one team of a CTA does, beside teams that
+// go on; and one warp does, which calls the CTA's other warps out of waits of their own.
 #include "kla_internal.cuh"
 #include "kla_norm.cuh"
 #include "sm103_ptx.cuh"
@@ -56,6 +56,34 @@ __global__ void __launch_bounds__(kTeamWidth *kTeams) selftest_teams_kernel(unsi
     done[threadIdx.x] = t;
 }
 
+// Warps that wait as those of the tensor-core scan do (kla_linear_tc.cu). Each completes its own phases up to
+// turn kWarpTurns; the first warp none but that of turn 0, and it alone has the short limit.
+constexpr int kWarps = 8, kWarpTurns = 100;
+
+__global__ void __launch_bounds__(32 * kWarps) selftest_warps_kernel(unsigned *err, int *done, uint32_t limit) {
+    using namespace kla;
+    __shared__ uint64_t bars[kWarps];
+    __shared__ int abort;
+    const int warp = threadIdx.x / 32, last = warp ? kWarpTurns : 1;
+    const bool lead = threadIdx.x % 32 == 0;
+    const uint32_t bar = ptx::smem_u32(&bars[warp]);
+    if (threadIdx.x == 0) abort = 0;
+    if (lead) {
+        ptx::mbar_init(bar, 1);
+        ptx::fence_mbar_init();
+    }
+    __syncthreads();
+    int t = 0;
+    for (; t < 2 * kWarpTurns; ++t) {
+        if (lead && t < last) ptx::mbar_arrive(bar);
+        if (!ptx::warp_wait(bar, t & 1, warp ? 100000u : limit, &abort)) break;
+        __syncwarp();
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && abort) atomicOr(err, kErrTimeout);
+    done[threadIdx.x] = t;
+}
+
 }  // namespace
 
 namespace kla {
@@ -67,6 +95,11 @@ cudaError_t launch_selftest_wait(unsigned *err, unsigned limit, cudaStream_t str
 
 cudaError_t launch_selftest_teams(unsigned *err, int *turns, unsigned limit, cudaStream_t stream) {
     selftest_teams_kernel<<<1, kTeamWidth * kTeams, 0, stream>>>(err, turns, limit);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_selftest_warps(unsigned *err, int *turns, unsigned limit, cudaStream_t stream) {
+    selftest_warps_kernel<<<1, 32 * kWarps, 0, stream>>>(err, turns, limit);
     return cudaGetLastError();
 }
 

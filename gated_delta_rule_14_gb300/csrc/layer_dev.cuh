@@ -64,6 +64,18 @@ __device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 
 namespace ptx {
 
+// A wait for phase `parity` by a whole warp, of at most limit x 20 us; false where it gave up, or where another
+// warp did, which *abort tells. The lanes decide alike: what follows are instructions that only a whole warp
+// may run, and lanes that saw the flag on either side of its being set would not meet there again.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_t limit, volatile int *abort) {
+    for (uint32_t i = 0; i < limit; ++i) {
+        if (__all_sync(0xffffffffu, mbar_try_wait_sleep(bar, parity, 20000u))) return true;
+        if (__any_sync(0xffffffffu, *abort)) return false;
+    }
+    *abort = 1;
+    return false;
+}
+
 // 32 or 16 consecutive 32-bit TMEM columns of this thread's lane, written (shape 32x32b).
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
     asm volatile(

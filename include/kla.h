@@ -325,6 +325,15 @@ kla_status kla_selftest_wait_timeout(unsigned limit_polls, void *stream);
  */
 kla_status kla_selftest_team_timeout(unsigned limit_polls, int *turns, void *stream);
 
+/*
+ * The same for warps that share a CTA and leave together, as in the tensor-core scan of kla_layer.h: eight
+ * warps wait turn by turn on barriers of their own; the first warp's second wait gives up after `limit_polls`,
+ * which calls the others out of the waits of their 101st turn, that nothing completes.
+ *   turns   device int32 [256], written: waits that each thread has passed (1 for the first warp's 32, 100
+ *           for the others)
+ */
+kla_status kla_selftest_warp_timeout(unsigned limit_polls, int *turns, void *stream);
+
 /* Static, human-readable name of a status code. */
 const char *kla_status_string(kla_status status);
 

@@ -43,3 +43,23 @@ def test_a_team_that_gives_up_leaves_as_one(limit):
         assert lib.kla_device_status(stream) == kla._native.KLA_ERR_TIMEOUT
         assert turns.tolist() == [1] * 64 + [20000] * 192
     assert lib.kla_device_status(stream) == kla._native.KLA_OK
+
+
+def test_a_warp_that_gives_up_calls_the_others_out():
+    """Eight warps of one CTA wait on barriers of their own: the first gives up, and every warp leaves its wait
+    as one, long before the 2 s that the others would wait by themselves."""
+    import torch
+
+    import gated_delta_rule_14_gb300 as kla
+    lib = kla._native.lib()
+    stream = torch.cuda.current_stream(DEV).cuda_stream
+    kla.device_status(DEV)
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    for _ in range(20):
+        turns = torch.full((256,), -1, dtype=torch.int32, device=DEV)
+        start.record()
+        assert lib.kla_selftest_warp_timeout(200, turns.data_ptr(), stream) == 0   # 4 ms
+        end.record()
+        assert lib.kla_device_status(stream) == kla._native.KLA_ERR_TIMEOUT
+        assert turns.tolist() == [1] * 32 + [100] * 224 and start.elapsed_time(end) < 1000
+    assert lib.kla_device_status(stream) == kla._native.KLA_OK

@@ -132,3 +132,8 @@ def test_long_norm_rows_need_their_workspace(lib):
 def test_team_selftest_rejects_its_arguments_on_host(lib):
     assert lib.kla_selftest_team_timeout(0, A, None) == 1 and lib.kla_selftest_team_timeout(100001, A, None) == 1
     assert lib.kla_selftest_team_timeout(10, None, None) == 1 and lib.kla_selftest_team_timeout(10, A + 2, None) == 1
+
+
+def test_warp_selftest_rejects_its_arguments_on_host(lib):
+    assert lib.kla_selftest_warp_timeout(0, A, None) == 1 and lib.kla_selftest_warp_timeout(100001, A, None) == 1
+    assert lib.kla_selftest_warp_timeout(10, None, None) == 1 and lib.kla_selftest_warp_timeout(10, A + 2, None) == 1
