@@ -9,6 +9,8 @@ import ctypes
 import os
 import threading
 
+import torch
+
 from . import build as _build
 
 KLA_OK = 0
@@ -111,6 +113,30 @@ def lib():
                     "`python -c 'import __graft_entry__ as g; g.build()'` (needs nvcc)")
             _lib = _declare(ctypes.CDLL(path))
         return _lib
+
+
+class _OnDevice:
+    """The library's entry points with a device made current around each call."""
+
+    def __init__(self, index: int):
+        self._index = index
+
+    def __getattr__(self, name):
+        entry = getattr(lib(), name)
+
+        def call(*args):
+            with torch.cuda.device(self._index):
+                return entry(*args)
+        return call
+
+
+def on(device: torch.device):
+    """The library, for calls on tensors of ``device``: launches, kernel attributes and the error word go by the
+    current device, whichever one the pointers and the stream belong to."""
+    index = device.index
+    if index is None or index == torch._C._cuda_getDevice():   # without an index: the current one
+        return lib()
+    return _OnDevice(index)
 
 
 def status_string(status: int) -> str:

@@ -4,9 +4,9 @@ with its gradients (``layer_norm_fwd``, ``layer_norm_bwd``) and beam search's se
 following their beams (``beam_select``, ``reorder_states``).
 
 The binding checks and marshals; every operation runs in this package's CUDA kernels on the current
-stream of the tensors' device. Small calls are bound by the host, so linear attention's functions first
-ask in one expression whether everything is as it should be, and only where it is not go through the
-arguments one by one to name the one at fault.
+stream of the tensors' device, whether or not that device is the current one. Small calls are bound by
+the host, so linear attention's functions first ask in one expression whether everything is as it should
+be, and only where it is not go through the arguments one by one to name the one at fault.
 """
 from __future__ import annotations
 
@@ -147,7 +147,7 @@ def linear_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: torch.T
     elif final_state:
         S_T = torch.empty((B, H, d_k, d_v), dtype=_F32, device=device)
     workspace, size = _scratch(_size("linear_fwd", B, T, H, d_k, d_v, code), workspace, device)
-    st = _native.lib().kla_linear_fwd(
+    st = _native.on(device).kla_linear_fwd(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), None if dense else _token_strides(_Strides3, q, k, v),
         decay.data_ptr(), _ptr(lengths), _ptr(S0), out.data_ptr(), _ptr(S_T), B, T, H, d_k, d_v, code, q_scale,
         _ptr(workspace), size, _stream(device))
@@ -174,7 +174,7 @@ def linear_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: torch.T
     dk, dv = torch.empty_like(dq), torch.empty((B, T, H, d_v), dtype=q.dtype, device=device)
     dS0 = torch.empty((B, H, d_k, d_v), dtype=_F32, device=device) if want_dS0 else None
     workspace, size = _scratch(_size("linear_bwd", B, T, H, d_k, d_v, code), workspace, device)
-    st = _native.lib().kla_linear_bwd(
+    st = _native.on(device).kla_linear_bwd(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), dO.data_ptr(),
         None if dense else _token_strides(_Strides4, q, k, v, dO), decay.data_ptr(), _ptr(lengths), _ptr(S0),
         _ptr(dS_T), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(dS0), B, T, H, d_k, d_v, code, q_scale,
@@ -229,9 +229,9 @@ def linear_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: torch.
         out = torch.empty_like(v)
     else:
         _check("out", out, v.shape, dtype, device)
-    st = _native.lib().kla_linear_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), _ptr(parent),
-                                       S.data_ptr(), S_out.data_ptr(), out.data_ptr(), B, H, d_k, d_v, n,
-                                       _CODE[dtype], q_scale, _stream(device))
+    st = _native.on(device).kla_linear_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), _ptr(parent),
+                                            S.data_ptr(), S_out.data_ptr(), out.data_ptr(), B, H, d_k, d_v, n,
+                                            _CODE[dtype], q_scale, _stream(device))
     if st:
         _native.check(st, "kla_linear_step")
     return out
@@ -279,8 +279,8 @@ def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias:
     if stats:
         mean = torch.empty(x.shape[:-1], dtype=_F32, device=device)
         rstd = torch.empty_like(mean)
-    st = _native.lib().kla_layer_norm_fwd(x.data_ptr(), _ptr(weight), _ptr(bias), out.data_ptr(), _ptr(mean),
-                                          _ptr(rstd), rows, groups, n, code, eps, _stream(device))
+    st = _native.on(device).kla_layer_norm_fwd(x.data_ptr(), _ptr(weight), _ptr(bias), out.data_ptr(), _ptr(mean),
+                                               _ptr(rstd), rows, groups, n, code, eps, _stream(device))
     if st:
         _native.check(st, "kla_layer_norm_fwd")
     return out, mean, rstd
@@ -309,9 +309,9 @@ def layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Ten
     dw = torch.empty(shape, dtype=_F32, device=device)
     db = torch.empty_like(dw)
     workspace, size = _scratch(_size("layer_norm_bwd", rows, groups, n, code), workspace, device)
-    st = _native.lib().kla_layer_norm_bwd(dy.data_ptr(), x.data_ptr(), _ptr(weight), mean.data_ptr(),
-                                          rstd.data_ptr(), dx.data_ptr(), dw.data_ptr(), db.data_ptr(), rows, groups,
-                                          n, code, _ptr(workspace), size, _stream(device))
+    st = _native.on(device).kla_layer_norm_bwd(dy.data_ptr(), x.data_ptr(), _ptr(weight), mean.data_ptr(),
+                                               rstd.data_ptr(), dx.data_ptr(), dw.data_ptr(), db.data_ptr(), rows,
+                                               groups, n, code, _ptr(workspace), size, _stream(device))
     if st:
         _native.check(st, "kla_layer_norm_bwd")
     return dx, dw, db
@@ -349,9 +349,9 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, finished: Optional[t
     tokens = torch.empty_like(parents)
     done = torch.empty((B, W), dtype=torch.bool, device=device)
     workspace, size = _scratch(_size("beam_select", B, W, V, code), workspace, device)
-    st = _native.lib().kla_beam_select(logits.data_ptr(), stride, scores.data_ptr(), _ptr(finished), eos,
-                                       new_scores.data_ptr(), parents.data_ptr(), tokens.data_ptr(),
-                                       done.data_ptr(), B, W, V, code, _ptr(workspace), size, _stream(device))
+    st = _native.on(device).kla_beam_select(logits.data_ptr(), stride, scores.data_ptr(), _ptr(finished), eos,
+                                            new_scores.data_ptr(), parents.data_ptr(), tokens.data_ptr(),
+                                            done.data_ptr(), B, W, V, code, _ptr(workspace), size, _stream(device))
     if st:
         _native.check(st, "kla_beam_select")
     return new_scores, parents, tokens, done
@@ -374,8 +374,8 @@ def reorder_states(S: torch.Tensor, parents: torch.Tensor, *, out: Optional[torc
     else:
         _check("out", out, shape, S.dtype, device)
     # from the shape: an axis of one element may have any stride in a contiguous tensor
-    st = _native.lib().kla_reorder_states(S.data_ptr(), parents.data_ptr(), out.data_ptr(), B, W,
-                                          math.prod(shape[2:]) * S.element_size(), _stream(device))
+    st = _native.on(device).kla_reorder_states(S.data_ptr(), parents.data_ptr(), out.data_ptr(), B, W,
+                                               math.prod(shape[2:]) * S.element_size(), _stream(device))
     if st:
         _native.check(st, "kla_reorder_states")
     return out

@@ -27,7 +27,9 @@ def library(monkeypatch):
     monkeypatch.setattr(_native, "lib", lambda: lib)
     monkeypatch.setattr(layer, "_device", lambda name, t: t.device)
     monkeypatch.setattr(layer, "_check", lambda *a: None)
-    monkeypatch.setattr(layer, "_stream", lambda device: 0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0, raising=False)
     layer._size.cache_clear()
     yield lib
     layer._size.cache_clear()
