@@ -131,7 +131,7 @@ def chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: torch.Te
     if ws_need and workspace is None:
         workspace = torch.empty(ws_need, dtype=torch.uint8, device=q.device)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = _native.lib().kla_chunk_fwd_ex(
+    st = _native.on(q.device).kla_chunk_fwd_ex(
         _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(eta), float(eps), _ptr(S0), _ptr(out), _ptr(S_T),
         B, T, H, d_k, d_v, int(chunk), dcode, gate, bcode, float(q_scale), _ptr(workspace), ws_bytes,
         _stream_ptr(q.device))
@@ -186,7 +186,7 @@ def chunk_fwd_host(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: tor
     if S_T is None and final_state:
         S_T = torch.empty((B, H, d_k, d_v), dtype=torch.float32, pin_memory=True)
     parts = parts or min(B, 8)
-    st = _native.lib().kla_chunk_fwd_host(
+    st = _native.on(dev).kla_chunk_fwd_host(
         _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(eta), _ptr(S0), _ptr(out), _ptr(S_T),
         _ptr(buffers["q"]), _ptr(buffers["k"]), _ptr(buffers["v"]), _ptr(buffers["alpha"]), _ptr(buffers["eta"]),
         _ptr(buffers.get("S0") if S0 is not None else None), _ptr(buffers["o"]),
@@ -272,7 +272,7 @@ def chunk_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: torch.Te
     if need and workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = _native.lib().kla_chunk_bwd(
+    st = _native.on(q.device).kla_chunk_bwd(
         _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(eta), float(eps), _ptr(S0), _ptr(dO), _ptr(dS_T),
         _ptr(g["dq"]), _ptr(g["dk"]), _ptr(g["dv"]), _ptr(g["dalpha"]), _ptr(g["deta"]), _ptr(g["dS0"]),
         B, T, H, d_k, d_v, dcode, gate, bcode, float(q_scale), _ptr(workspace), ws_bytes, _stream_ptr(q.device))
@@ -311,7 +311,7 @@ def decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: torch.
         out = torch.empty((B, H, d_v), dtype=q.dtype, device=q.device)
     else:
         _check_dev("out", out, q.dtype)
-    st = _native.lib().kla_decode_step_ex(
+    st = _native.on(q.device).kla_decode_step_ex(
         _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(eta), float(eps), _ptr(S), _ptr(out),
         B, H, d_k, d_v, dcode, gate, bcode, float(q_scale), _stream_ptr(q.device))
     _native.check(st, "kla_decode_step_ex")
@@ -321,4 +321,4 @@ def decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: torch.
 def device_status(device=None) -> None:
     """Synchronise the current stream and raise if a bounded device wait or range check fired."""
     dev = torch.device("cuda") if device is None else torch.device(device)
-    _native.check(_native.lib().kla_device_status(_stream_ptr(dev)), "kla_device_status")
+    _native.check(_native.on(dev).kla_device_status(_stream_ptr(dev)), "kla_device_status")

@@ -76,3 +76,27 @@ def test_layer_operators(calls):
     assert calls == [(f"kla_{name}", 1, 101) for name in (
         "linear_fwd", "linear_bwd", "linear_step", "layer_norm_fwd", "layer_norm_bwd", "beam_select",
         "reorder_states")]
+
+
+def test_recurrence(calls):
+    q, a = place(torch.zeros(2, 4, 3, 16)), place(torch.zeros(2, 4, 3))
+    kla.chunk_fwd(q, q, q, a, a)
+    kla.chunk_bwd(q, q, q, a, a, q)
+    one, S = place(torch.zeros(2, 3, 16)), place(torch.zeros(2, 3, 16, 16))
+    kla.decode_step(one, one, one, a[:, 0].contiguous(), a[:, 0].contiguous(), S)
+    kla.device_status(torch.device("cuda", 1))
+    assert calls == [(f"kla_{name}", 1, 101) for name in ("chunk_fwd_ex", "chunk_bwd", "decode_step_ex",
+                                                          "device_status")]
+
+
+def test_recurrence_of_host_tensors(calls):
+    q, a = torch.zeros(2, 4, 3, 16), torch.zeros(2, 4, 3)
+    buffers = {n: torch.zeros(1) for n in ("q", "k", "v", "alpha", "eta", "o", "S_T")}
+    kla.chunk_fwd_host(q, q, q, a, a, device="cuda:1", buffers=buffers, out=torch.zeros(2, 4, 3, 16),
+                       S_T=torch.zeros(2, 3, 16, 16))
+    assert calls == [("kla_chunk_fwd_host", 1, 101)]
+
+
+def test_status_of_the_current_device(calls):
+    kla.device_status()
+    assert calls == [("kla_device_status", 0, 100)]
