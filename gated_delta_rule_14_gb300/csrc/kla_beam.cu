@@ -30,6 +30,7 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kE = 16;                    // logits of one thread
 constexpr int kChunk = kThreads * kE;     // tokens of one CTA
 constexpr int kMaxW = 16;
+constexpr int kMostV = 512 * kChunk;      // the merge numbers its entries in 32 bits
 
 // Order-preserving map of floats (no NaN) to whole numbers above 0, and back.
 __device__ __forceinline__ uint32_t rank_of(float x) {
@@ -358,7 +359,7 @@ extern "C" {
 
 size_t kla_beam_select_workspace_size(int B, int W, int V, kla_dtype dtype) {
     (void)dtype;
-    if (B < 1 || W < 1 || W > kla::kMaxW || V < 1) return 0;
+    if (B < 1 || W < 1 || W > kla::kMaxW || V < 1 || V > kla::kMostV) return 0;
     const size_t pieces = static_cast<size_t>(B) * W * ((V + kla::kChunk - 1) / kla::kChunk);
     return pieces * (2 + 2 * static_cast<size_t>(W)) * 4;
 }
@@ -375,9 +376,9 @@ kla_status kla_beam_select(const void *logits, int64_t row_stride, const float *
     if (!aligned(logits, esz) || !aligned(scores, 4) || !aligned(new_scores, 4) || !aligned(parents, 4) ||
         !aligned(tokens, 4) || !aligned(workspace, 16))
         return KLA_ERR_INVALID_ARG;
+    // the beams index the grid
+    if (W > kMaxW || static_cast<int64_t>(B) * W > 65535 || V > kMostV) return KLA_ERR_UNSUPPORTED;
     const int nchunk = (V + kChunk - 1) / kChunk;
-    // the beams index the grid; the merge numbers its entries in 32 bits
-    if (W > kMaxW || static_cast<int64_t>(B) * W > 65535 || nchunk > 512) return KLA_ERR_UNSUPPORTED;
     const size_t need = kla_beam_select_workspace_size(B, W, V, dtype);
     if (workspace_bytes < need) return KLA_ERR_INVALID_ARG;
     const size_t n = static_cast<size_t>(B) * W;

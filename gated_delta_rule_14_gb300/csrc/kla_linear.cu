@@ -442,6 +442,10 @@ Span reach(const void *p, const int64_t *st, int B, int T, int H, int d, size_t 
 }
 
 constexpr int kSms = 152;
+// Tokens are numbered in 32 bits up to the end of the last segment's last chunk. At most 2 kSms segments are
+// asked for, each a whole number of chunks of up to 128 tokens: they reach less than 2 kSms chunks past T.
+constexpr int kMostTokens = INT_MAX - 65536;
+static_assert((2 * kSms + 1) * 128 < 65536, "segments past the last token");
 
 size_t seg_bytes(const LinScan &p) {
     return p.nseg > 1 ? static_cast<size_t>(p.B) * p.H * p.nseg * p.dx * p.dz * sizeof(float) : 0;
@@ -479,7 +483,7 @@ kla_status check_sizes(int B, int T, int H, int d_k, int d_v, kla_dtype dtype, f
     if (!finite(q_scale)) return KLA_ERR_INVALID_ARG;
     for (int i = 0; strides && i < 3 * ntens; ++i)
         if (strides[i] < 0) return KLA_ERR_INVALID_ARG;
-    if (!supported_d(d_k) || !supported_d(d_v)) return KLA_ERR_UNSUPPORTED;
+    if (!supported_d(d_k) || !supported_d(d_v) || T > kMostTokens) return KLA_ERR_UNSUPPORTED;
     // chains times value tiles index the grid
     if (static_cast<int64_t>(B) * H * 8 > INT_MAX) return KLA_ERR_UNSUPPORTED;
     return KLA_OK;
@@ -506,14 +510,14 @@ using kla::LinScan;
 extern "C" {
 
 size_t kla_linear_fwd_workspace_size(int B, int T, int H, int d_k, int d_v, kla_dtype dtype) {
-    if (B < 1 || T < 1 || H < 1 || !kla::supported_d(d_k) || !kla::supported_d(d_v)) return 0;
+    if (B < 1 || T < 1 || T > kla::kMostTokens || H < 1 || !kla::supported_d(d_k) || !kla::supported_d(d_v)) return 0;
     LinScan p{};
     p.B = B; p.T = T; p.H = H; p.dx = d_k; p.dz = d_v;
     return kla::scratch(p, dtype, 1);
 }
 
 size_t kla_linear_bwd_workspace_size(int B, int T, int H, int d_k, int d_v, kla_dtype dtype) {
-    if (B < 1 || T < 1 || H < 1 || !kla::supported_d(d_k) || !kla::supported_d(d_v)) return 0;
+    if (B < 1 || T < 1 || T > kla::kMostTokens || H < 1 || !kla::supported_d(d_k) || !kla::supported_d(d_v)) return 0;
     LinScan p{}, q{};
     p.B = q.B = B; p.T = q.T = T; p.H = q.H = H;
     p.dx = q.dz = d_k;

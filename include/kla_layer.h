@@ -39,7 +39,7 @@ extern "C" {
  *   o        [B, T, H, d_v] dtype, contiguous, written
  *   S_T      fp32 [B, H, d_k, d_v] or NULL; may be S0 itself
  *   q_scale  the finite scale s
- *   sizes    d_k, d_v in {16, 32, 64, 128}; T >= 0 (T = 0 writes S_T only)
+ *   sizes    d_k, d_v in {16, 32, 64, 128}; 0 <= T <= 2^31 - 1 - 65536 (T = 0 writes S_T only)
  *   alignment: q, k, v, o their element; S0, S_T, workspace 16 bytes
  *
  * bf16 with d_k = d_v = 128 and 16-byte aligned rows runs on the tensor cores (bf16 operands, fp32
@@ -123,7 +123,7 @@ size_t kla_layer_norm_bwd_workspace_size(int64_t rows, int groups, int n, kla_dt
  *   scores      fp32 [B, W]            finished  uint8 [B, W] (0 / 1) or NULL (none)
  *   eos         token that finishes a beam, or -1 (then `finished` must be NULL)
  *   new_scores  fp32 [B, W], parents, tokens int32 [B, W], new_finished uint8 [B, W] or NULL: written
- *   1 <= W <= 16, V >= 1
+ *   1 <= W <= 16, 1 <= V <= 2^21, B W <= 65535
  */
 kla_status kla_beam_select(const void *logits, int64_t row_stride, const float *scores, const unsigned char *finished,
                            int eos, float *new_scores, int *parents, int *tokens, unsigned char *new_finished, int B,

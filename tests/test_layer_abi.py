@@ -137,3 +137,25 @@ def test_team_selftest_rejects_its_arguments_on_host(lib):
 def test_warp_selftest_rejects_its_arguments_on_host(lib):
     assert lib.kla_selftest_warp_timeout(0, A, None) == 1 and lib.kla_selftest_warp_timeout(100001, A, None) == 1
     assert lib.kla_selftest_warp_timeout(10, None, None) == 1 and lib.kla_selftest_warp_timeout(10, A + 2, None) == 1
+
+
+FAR = 1 << 40   # buffers of tens of GB that do not overlap
+
+
+@pytest.mark.parametrize("T", [2**31 - 1, 2**31 - 64, 2**31 - 65536])
+def test_lengths_whose_chunks_pass_32_bits_are_refused(lib, T):
+    """Tokens are numbered in 32 bits, up to the end of the last segment's last chunk."""
+    q, k, v, g, o = (A + i * FAR for i in range(5))
+    assert fwd(lib, q=q, k=k, v=v, g=g, o=o, T=T, H=1, dt=1, st=strides(*[0, 0, 16] * 3)) == 2
+    a = [A + i * FAR for i in range(8)]
+    assert bwd(lib, q=a[0], k=a[1], v=a[2], dO=a[3], g=a[4], dq=a[5], dk=a[6], dv=a[7], T=T, H=1, dt=1,
+               st=strides(*[0, 0, 16] * 4)) == 2
+    for size in (lib.kla_linear_fwd_workspace_size, lib.kla_linear_bwd_workspace_size):
+        assert size(1, T, 1, 16, 16, 1) == 0 and size(1, T, 1, 128, 128, 1) == 0
+
+
+@pytest.mark.parametrize("V", [2**31 - 1, 2**31 - 4000])
+def test_vocabularies_whose_pieces_pass_32_bits_are_refused(lib, V):
+    assert lib.kla_beam_select(A, V, A + FAR, None, -1, A + 2 * FAR, A + 3 * FAR, A + 4 * FAR, None, 1, 1, V, 1,
+                               A + 5 * FAR, 1 << 39, None) == 2
+    assert lib.kla_beam_select_workspace_size(1, 1, V, 1) == 0
