@@ -63,9 +63,18 @@ def _stream(device: torch.device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+_MOST = 2**31 - 1   # of a C int: ctypes would cut a larger number to its low 32 bits
+
+
+def _refuse(entry: str, status: int):
+    raise _native.KlaError(status, entry)
+
+
 @functools.lru_cache(maxsize=256)
 def _size(query: str, *sizes) -> int:
     """Scratch bytes of a call: they follow from its sizes alone."""
+    if max(sizes) > _MOST:
+        _refuse(f"kla_{query}", _native.KLA_ERR_UNSUPPORTED)
     return getattr(_native.lib(), f"kla_{query}_workspace_size")(*sizes)
 
 
@@ -265,6 +274,8 @@ def layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias:
     device = _device("x", x)
     code = _code("x", x)
     rows, groups, n, shape = _norm_shape(x, weight, bias)
+    if n > _MOST or groups > _MOST:
+        _refuse("kla_layer_norm_fwd", _native.KLA_ERR_UNSUPPORTED)
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
     if weight is not None:
@@ -344,6 +355,8 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, finished: Optional[t
     _check("scores", scores, (B, W), _F32, device)
     if finished is not None:
         _check("finished", finished, (B, W), torch.bool, device)
+    if not -1 <= eos < V:
+        _refuse("kla_beam_select", _native.KLA_ERR_INVALID_ARG)
     new_scores = torch.empty_like(scores)
     parents = torch.empty((B, W), dtype=torch.int32, device=device)
     tokens = torch.empty_like(parents)
@@ -368,6 +381,8 @@ def reorder_states(S: torch.Tensor, parents: torch.Tensor, *, out: Optional[torc
         raise ValueError("S must be contiguous")
     shape = S.shape
     B, W = shape[:2]
+    if B > _MOST or W > _MOST:
+        _refuse("kla_reorder_states", _native.KLA_ERR_UNSUPPORTED)
     _check("parents", parents, (B, W), torch.int32, device)
     if out is None:
         out = torch.empty_like(S)

@@ -16,6 +16,8 @@ class Library:
         def entry(*args):
             if name.endswith("_workspace_size"):
                 return 0
+            if name == "kla_status_string":
+                return b""
             self.calls.append((name, args))
             return 0
         return entry
@@ -59,3 +61,35 @@ def test_bias_per_head_without_a_weight_has_its_gradient(library):
     assert fwd[6:9] == bwd[8:11] == (4, 6, 32) and dw.shape == db.shape == (6, 32)
     _, dw, db = layer.layer_norm_bwd(x.clone(), x, None, mean, rstd)   # no parameters, or those of the last axis
     assert library.calls[-1][1][8:11] == (24, 1, 32) and dw.shape == db.shape == (32,)
+
+
+WIDE = 2**32 + 64   # 64 once cut to 32 bits
+
+
+def meta(*shape, dtype=torch.bfloat16):
+    return torch.empty(shape, device="meta", dtype=dtype)
+
+
+@pytest.mark.parametrize("call", [
+    lambda: layer.linear_fwd(*[meta(1, WIDE, 1, 16)] * 3, meta(1)),
+    lambda: layer.linear_bwd(*[meta(1, WIDE, 1, 16)] * 3, meta(1), meta(1, WIDE, 1, 16)),
+    lambda: layer.layer_norm_fwd(meta(3, WIDE)),
+    lambda: layer.layer_norm_fwd(meta(3, WIDE, 32), meta(WIDE, 32)),
+    lambda: layer.layer_norm_bwd(meta(3, WIDE), meta(3, WIDE), None, meta(3), meta(3)),
+    lambda: layer.beam_select(meta(1, 1, WIDE), meta(1, 1)),
+    lambda: layer.beam_select(meta(WIDE, 1, 10), meta(WIDE, 1)),
+    lambda: layer.reorder_states(meta(WIDE, 1, 16), meta(WIDE, 1)),
+    lambda: layer.reorder_states(meta(1, WIDE, 16), meta(1, WIDE)),
+    lambda: layer.beam_select(meta(1, 1, 100), meta(1, 1), eos=2**32 + 5),
+    lambda: layer.beam_select(meta(1, 1, 100), meta(1, 1), eos=-2**32 + 5),
+])
+def test_numbers_past_32_bits_do_not_reach_the_library(library, call):
+    """ctypes would cut them without a word, and the call would be one on other sizes."""
+    with pytest.raises(_native.KlaError):
+        call()
+    assert not library.calls
+
+
+def test_rows_are_64_bit(library):
+    layer.layer_norm_fwd(meta(2**31, 3, 4), stats=False)   # the library's own limit refuses these rows
+    assert library.calls[0][1][6:9] == (3 * 2**31, 1, 4)
