@@ -160,3 +160,23 @@ def test_refusals():
     S = torch.zeros(1, 2, 4, device=DEV)
     with pytest.raises(kla.KlaError):
         kla.reorder_states(S, torch.zeros(1, 2, dtype=torch.int32, device=DEV), out=S)
+
+
+@pytest.mark.parametrize("score", [-1.0, -math.inf])
+def test_more_equal_candidates_than_are_ranked_at_once(score):
+    """Every logit and every score equal: 2560 list entries reach the merge's threshold, which ranks 256 at once,
+    and beam 0's lowest tokens are taken one after the other."""
+    check(torch.zeros(1, 16, 40000, device=DEV), torch.full((1, 16), score, device=DEV))
+
+
+def test_more_entries_than_a_merge_starts_with():
+    """35 pieces of 16 beams leave 8960 entries; 8192 are on their way from the start."""
+    check(*draw(1, 16, 140001, torch.float32, 8))
+
+
+def test_long_runs_of_equal_values_in_many_pieces():
+    gen = torch.Generator(device=DEV).manual_seed(9)
+    row = torch.randint(0, 3, (140001,), generator=gen, device=DEV).float()
+    logits = row.expand(1, 16, 140001).contiguous()
+    check(logits, torch.zeros(1, 16, device=DEV))                              # equal beams
+    check(logits, -0.5 * torch.arange(16., device=DEV).flip(0)[None])          # the last beam is the best

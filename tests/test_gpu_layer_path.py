@@ -111,3 +111,32 @@ def test_operators_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(S, state) and all(torch.equal(x, y) for x, y in zip(out, eager))
+
+
+def test_calls_of_several_launches_in_a_graph():
+    """A training step whose calls launch kernels that depend on one another (sequences cut into segments, partial
+    sums of the norm's gradients), captured as one CUDA graph, gives the eager step's results."""
+    import gated_delta_rule_14_gb300 as kla
+    gen = torch.Generator(device=DEV).manual_seed(31)
+    q, k, v, dy = (torch.randn(1, 3000, 2, 128, generator=gen, device=DEV).bfloat16() for _ in range(4))
+    g, w = torch.tensor([0.97, 0.999], device=DEV), torch.randn(2, 128, generator=gen, device=DEV)
+
+    def step():
+        o, S = kla.linear_fwd(q, k, v, g, q_scale=0.1)
+        y, mean, rstd = kla.layer_norm_fwd(o, w)
+        do, dw, db = kla.layer_norm_bwd(dy, o, w, mean, rstd)
+        d = kla.linear_bwd(q, k, v, g, do, q_scale=0.1)
+        return o, S, y, do, dw, db, *d.values()
+    eager = step()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for _ in range(2):
+        graph.replay()
+    kla.device_status(DEV)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, eager))

@@ -305,3 +305,17 @@ def test_refusals():
         kla.linear_step(*st, d["S0"], parent=torch.zeros(1, dtype=torch.int32, device=DEV))
     with pytest.raises(kla.KlaError):
         kla.linear_step(*st, d["S0"], parent=torch.zeros(1, dtype=torch.int32, device=DEV), S_out=d["S0"])
+
+
+# around the fp32 scan's chunk of 64 tokens
+@pytest.mark.parametrize("T", [63, 64, 65])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_lengths_around_the_fp32_chunk(T, dtype):
+    check(make(2, T, 3, 64, 64, dtype, seed=T))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dk,dv", [(64, 128), (128, 32)])
+def test_uneven_heads_over_segments(dk, dv, dtype):
+    """Long sequences of few heads whose lengths end inside segments; dv's state is the transpose of the others'."""
+    check(make(3, 1300, 2, dk, dv, dtype, seed=dk, lengths=[1111, 0, 700]))

@@ -230,3 +230,49 @@ def test_backward_checks_the_bias():
         kla.layer_norm_bwd(x, x.clone(), None, mean, rstd, bias=torch.ones(5, 32, device=DEV))
     with pytest.raises(ValueError):
         kla.layer_norm_bwd(x, x.clone(), torch.ones(32, device=DEV), mean, rstd, bias=torch.ones(6, 32, device=DEV))
+
+
+# Rows of 513 to 8192 values go through shared memory, several at a time for every team of threads: enough rows here
+# that each team walks four or more, so that stages are filled again, their phases flip and the two output
+# buffers alternate, in fp32 with one to four stages, and off the 16-byte grid, where a row's first and last
+# values go by themselves between rows of other teams.
+@pytest.mark.parametrize("rows,n,dtype", [
+    (10007, 1024, torch.float32), (10007, 1023, torch.float32), (5003, 2048, torch.float32),
+    (2600, 4095, torch.float32), (1300, 8192, torch.float32), (1300, 8192, torch.bfloat16),
+    (5003, 1537, torch.bfloat16), (2600, 2050, torch.bfloat16)])
+def test_many_rows_through_shared_memory(rows, n, dtype):
+    check((rows, n), (n,), dtype, seed=n)
+
+
+@pytest.mark.parametrize("view", [1, 2, 3])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_many_rows_from_unaligned_starts(view, dtype):
+    check((10007, 640), (640,), dtype, view=view)
+
+
+@pytest.mark.parametrize("G,n", [(3, 700), (2, 2049)])
+def test_many_heads_through_shared_memory(G, n):
+    check((4001, G, n), (G, n), torch.float32, seed=G)
+
+
+@pytest.mark.parametrize("n", [128, 1001, 8200])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_tensors_with_different_starts(n, dtype):
+    """x, dy and the output each start at another place against 16 bytes; what lies around the output stays."""
+    import gated_delta_rule_14_gb300 as kla
+    rows = 3000 if n < 8192 else 40
+    gen = torch.Generator(device=DEV).manual_seed(n)
+
+    def at(k, fill=None):
+        flat = torch.randn(rows * n + 8, generator=gen, device=DEV).to(dtype)
+        if fill is not None:
+            flat.fill_(fill)
+        return flat, flat[k:k + rows * n].view(rows, n)
+    (_, x), (_, dy), (around, out) = at(1), at(2), at(3, 7.0)
+    w, b = (torch.randn(n, generator=gen, device=DEV) for _ in range(2))
+    y, mean, rstd = kla.layer_norm_fwd(x, w, b, out=out)
+    dx, dw, db = kla.layer_norm_bwd(dy, x, w, mean, rstd)
+    assert y is out and bool((around[:3] == 7).all()) and bool((around[3 + rows * n:] == 7).all())
+    tol = 4e-3 if dtype == torch.bfloat16 else 1e-5
+    for got, want, t in zip((y, mean, rstd, dx, dw, db), reference(x, w, b, 1e-5, dy), (tol, 1e-5, 1e-5, tol, 1e-5, 1e-5)):
+        assert rel(got, want) <= t
