@@ -13,8 +13,9 @@
 // after the other. Taking them so everywhere cost 22.6 us for 64 rows of 100003 fp32 logits.
 //
 // Measured with cold caches, 8 requests of 8 such beams: 13 us for the pass (26 MB, 29 % of a copy's rate; bound by
-// instructions and by the pieces' barriers, 2.1 issued a cycle) and 9 us for the merge (eight CTAs, one after the other
-// dependent steps behind barriers), whose launch overlaps the pass; 15 to 18 us together.
+// the latency of its loads and of the pieces' barriers, 2.1 of 4 instructions issued a cycle) and 9 us for the merge
+// (eight CTAs, one after the other dependent steps behind barriers), whose launch overlaps the pass; 15 to 18 us
+// together.
 //
 // Logits are ranked through an order-preserving map to 32-bit whole numbers (0 marks "nothing").
 #include <cfloat>

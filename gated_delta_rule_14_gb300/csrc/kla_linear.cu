@@ -76,7 +76,7 @@ __device__ __forceinline__ void take(const float *p, float (&x)[kN]) {
 // launches each that are one chunk's chain of loads and barriers long; 8 x 1024 tokens of 16 heads of 128: 575 and
 // 1680 us, a third of the fp32 pipe's rate. Y in both orders, P beside it, X read once for each of its products and the
 // last chunk's state always taken took 34, 64, 653 and 1932; registers for three CTAs an SM of the 64 x 64 tiles
-// (80, some spilled) 593 instead of 443 for 8 x 2048 tokens of 16 heads.
+// (80, some spilled) 593 for 8 x 2048 tokens of 16 heads, which took 443 then and take 410 now.
 template <int kX, int kZ>
 constexpr int kScanFloats = (kX + (kX > kC ? kX : kC)) * kPitch + (kC + kX) * (kZ + 4) + kC + 1;
 
@@ -352,7 +352,9 @@ cudaError_t launch_scan(const LinScan *p, int scans, cudaStream_t stream) {
 // ---------------------------------------------------------------------------- single-token step
 // One CTA per (sequence, head) and kZ value channels: every state element is read once, decayed,
 // written to and reduced against the query on the way out. Bound by the memory: 128 x 24 states of 128 x 128 take
-// 60 us (6.75 TB/s, 99 % of a copy's rate); 64 x 16, which L2 holds, 14 us; 1 x 16 2.2 us, a launch's latency.
+// 59 us (6.8 TB/s, a copy's rate). 64 x 16 (67 MB) in place, again and again: 14 us, since L2 holds them; from one
+// buffer to another and back, which together it does not hold: 19 us (7.0 TB/s, a part of it from L2). 1 x 16: 2 us,
+// a launch's latency.
 template <typename T, int kZ>
 __global__ void __launch_bounds__(kThreads) lin_step_kernel(const T *q, const T *k, const T *v, const float *decay,
                                                             const int *parent, const float *S, float *S_out, T *o,

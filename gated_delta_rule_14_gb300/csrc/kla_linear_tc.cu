@@ -27,8 +27,9 @@
 // outputs out through the Z tile; 16-23 weigh the keys; 24 loads (TMA, two stages of X, Y, Z tiles, each
 // tile refilled as soon as its own readers are done: Y first, Z, which is needed last, last);
 // 25 issues the products, in the order D, X S, U, P Z, which leaves P's conversion the time of X S
-// and U. They hand over through mbarriers that complete once per chunk. Eight warps per role: with
-// four, and keys and state on the same eight, the chain of conversions took 6900 cycles a chunk.
+// and U. They hand over through mbarriers that complete once per chunk, on which whole warps wait and give up
+// as one (the votes that this takes cost 0.5 to 1 %). Eight warps per role: with four, and keys and state on the
+// same eight, the chain of conversions took 6900 cycles a chunk.
 //
 // Measured, 16 heads: outputs of 8 x 4096 tokens 92 us (537 MB, 5.8 TB/s, 86 % of a copy's rate, the tensor pipe
 // active in 49 % of the cycles): the memory. The three scans of that shape's backward pass 250 us: 384 CTAs go

@@ -8,13 +8,15 @@
 // group, so that weight and bias, and in the backward pass the sums of dw and db, stay in registers; the sums
 // leave as one partial row per CTA and a second launch adds those in a fixed order.
 // What bounds it is the memory, and to keep it busy ~70 KB have to be on the way to every SM. Rows of a
-// CTA therefore come and go through shared memory by bulk copies, several rows ahead, which cost no
-// registers and take rows of any width and alignment at full speed: a copy takes the 16-byte granules
-// that the row touches, and threads pick their columns from there. (Loads one row ahead into registers
-// reached half of that.)
+// CTA therefore come and go through shared memory by bulk copies, one to four rows ahead of every team (what
+// shared memory holds: of 2048 values in the forward pass four in bf16, one in fp32), which cost no registers
+// and take rows of any width and alignment: a copy takes the 16-byte granules that the row touches, and
+// threads pick their columns from there. (Loads one row ahead into registers reached half of that.)
 // Measured, 16397 x 2048 bf16: forward 27 us (5.0 TB/s, 74 % of a copy's rate), backward 40 us (5.0 TB/s) and 7 us
-// for the sums of dw and db; 1.85 instructions are issued a cycle, 800 a row in the forward pass and 1280 in
-// the backward, and with the barriers of the rows' sums they are what is left above the memory.
+// for the sums of dw and db. What is left above the memory is latency: a row's chain of shared-memory accesses,
+// shuffles and barriers, at 800 instructions a row in the forward pass and 1280 in the backward, of which 1.85 of 4
+// are issued a cycle. The same rows in fp32, with twice the bytes to the same chain: 45 and 68 us (88 and 87 %), so
+// one row ahead does; 16397 x 8192 fp32 167 and 249 us (95 and 96 %).
 #include <atomic>
 #include <climits>
 
@@ -374,8 +376,9 @@ __global__ void __launch_bounds__(1024) norm_sum_kernel(const float *part, float
 // ---- rows longer than kRingMostN: more than a CTA holds
 // The forward pass reads a row once for its statistics and again, from L1 or L2, for its output. A thread
 // takes pieces of kP accesses whose loads are on their way together; a piece's mean and squared deviations
-// join the thread's by (N, M, Q) + (c, m, q) = (N + c, M + d c / (N + c), Q + q + d^2 N c / (N + c)), d = m - M,
-// which subtracts the mean before it squares as two passes would. The backward pass cannot keep a row's columns
+// join the thread's by the pairwise update of Chan, Golub and LeVeque, (N, M, Q) + (c, m, q) = (N + c,
+// M + d c / (N + c), Q + q + d^2 N c / (N + c)), d = m - M, which subtracts the mean before it squares as two
+// passes would. The backward pass cannot keep a row's columns
 // and their sums in one CTA's registers either: it reads x and dy twice, by rows and then by columns.
 // Measured, 8000 x 12288 bf16: forward 111 us (3.5 TB/s), backward 162 us (3.7 TB/s of one read, 6.1 of the two);
 // walking the row value by value, with sums of dw and db in memory, took 172 and 565.

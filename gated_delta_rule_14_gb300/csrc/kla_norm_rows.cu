@@ -7,8 +7,8 @@
 // lanes a fifth of the memory's rate was reached. CTAs are persistent and keep to one group, so that
 // weight, bias and the sums of dw and db stay in registers.
 // Measured, 29296 x 16 heads of 64 bf16: forward 34 us (52 % of a copy's rate), backward 41 us (64 %); 100000 x 300
-// fp32: 46 and 75 us. Warps wait for their loads most (4.5 of them a cycle, 3.3 in the backward pass) and 2.4
-// instructions are issued a cycle (2.1): both bound it. 64 x 16 heads of 128 take 2.5 us, a launch's latency.
+// fp32: 46 and 75 us. Warps wait for their loads most (4.5 of them a cycle, 3.3 in the backward pass), at 2.4 of 4
+// instructions issued a cycle (2.1): the loads' latency bounds it. 64 x 16 heads of 128 take 2.5 us, a launch's.
 #include "kla_norm.cuh"
 
 namespace kla {

@@ -5,8 +5,9 @@
  * following their beams.
  *
  * The conventions of kla.h hold: device pointers, caller-owned buffers, calls asynchronous on
- * `stream`, argument errors found on the host before anything is launched (KLA_ERR_INVALID_ARG /
- * KLA_ERR_UNSUPPORTED, nothing written), bounded device waits reported by kla_device_status.
+ * `stream` (whose device has to be the current one), argument errors found on the host before
+ * anything is launched (KLA_ERR_INVALID_ARG / KLA_ERR_UNSUPPORTED, nothing written), bounded device
+ * waits reported by kla_device_status.
  * Outputs and workspaces must not overlap each other or any input unless said otherwise.
  */
 #ifndef KLA_LAYER_H
@@ -29,6 +30,8 @@ extern "C" {
  *
  * for t = 0 .. n_b - 1, where n_b = lengths[b] (T when lengths is NULL). Tokens t >= n_b are
  * masked: whatever q, k, v hold there (NaN included) they leave the state as it is, and o_t = 0.
+ * A valid token that holds an infinity or a NaN spoils the state from there on, and, since tokens
+ * meet in products of 64 or 128, the outputs of up to 127 tokens before it.
  *
  *   q, k     [B, T, H, d_k] dtype, v [B, T, H, d_v] dtype; last axis contiguous. `strides` gives
  *            the element strides of the batch, token and head axes of q, then k, then v (9

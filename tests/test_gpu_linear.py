@@ -89,7 +89,8 @@ def check(d):
         assert rel(got[x], want[x]) <= (1e-5 if x == "dS0" else tol), (x, rel(got[x], want[x]))
 
 
-# one token, below / at / above the chunks of both paths (32 and 128 tokens), several chunks, odd tails
+# one token, inside the fp32 scan's chunk of 64 tokens, below / at / above the tensor cores' 128, several chunks,
+# odd tails
 @pytest.mark.parametrize("T", [1, 2, 31, 32, 33, 127, 128, 129, 256, 385])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_lengths_of_one_chunk_and_more(T, dtype):

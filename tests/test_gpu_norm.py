@@ -54,8 +54,8 @@ def check(shape, wshape, dtype, offset=0.5, scale=2.0, seed=0, view=0):
         assert got.shape == want.shape and rel(got, want) <= t, (name, rel(got, want))
 
 
-# each team (16 and 32 lanes, a CTA, pieces of a row) at its borders, and widths that only pairs or single
-# values fit
+# teams of 2 to 32 lanes, of several warps (513 to 8192 values) and CTAs that take longer rows by pieces, some at
+# their borders, and widths that only pairs or single values fit
 @pytest.mark.parametrize("n", [3, 16, 31, 127, 128, 255, 256, 257, 512, 513, 514, 1000, 2048, 4099, 16384,
                                16385, 20000])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
