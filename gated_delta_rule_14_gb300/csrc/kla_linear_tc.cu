@@ -17,11 +17,12 @@
 // Operands that threads compute and that would be read from shared memory once per product sit in
 // TMEM instead: P replaces D column by column, and the weighted keys are written transposed. So does
 // the fp32 state: U accumulates onto g^n S in place.
-// (diag(w) Y)^T is kept as two bf16 terms (hi + lo, 2^-17 relative): the fp32 state is an output of
-// its own, and one term (2^-9) would be its error. S as an operand and P are rounded to one bf16
+// (diag(w) Y)^T is kept as two bf16 terms (hi + lo, up to 2^-16 off, a third of that on average): the fp32 state
+// is an output of its own, and one term (2^-8) would be its error. S as an operand and P are rounded to one bf16
 // term: they only enter O, which is stored with 8 bits itself. Against 64 bits O is off by 2.3e-3 (its own
-// rounding alone: 1.7e-3) and the state by 4e-6; a third term of the keys took the 4096-token prompt below
-// from 94 to 136 us.
+// rounding alone: 1.7e-3) and the state by 4e-6 (dS0 of a few tokens, whose weights share one error, by 7e-6, up
+// to 1.1e-5); a third term of the keys took the 4096-token prompt below from 94 to 136 us. Weighing in fp32 and
+// splitting the product leaves 2.5e-6, for 2 % more time there and 4 % more on 131072 tokens: not taken.
 //
 // Warps: 0-7 turn D into P; 8-15 copy and decay the state, scale the first half of O and send the
 // outputs out through the Z tile; 16-23 weigh the keys; 24 loads (TMA, two stages of X, Y, Z tiles, each
