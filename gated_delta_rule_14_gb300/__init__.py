@@ -13,8 +13,10 @@ variantes de atencion lineal de la familia DeltaNet", sections "Gated DeltaNet" 
 ``chunk_fwd`` runs the chunkwise prefill, ``decode_step`` one fused single-token
 step and ``chunk_bwd`` the backward pass (gradients of a loss given dL/do and
 dL/dS_T). ``layer`` has what a layer and a decoding loop need next to them: linear
-attention with one decay per head, layer norm, beam search. All call the C ABI of
-``include/kla.h`` and ``include/kla_layer.h`` through ctypes; torch only supplies device
+attention with one decay per head, layer norm, beam search; ``block`` what a block around
+the recurrences needs: a scan with one gate per channel, rotary positions, norms with gate
+and residual, verification of drafted tokens. All call the C ABI of ``include/kla.h``,
+``include/kla_layer.h`` and ``include/kla_block.h`` through ctypes; torch only supplies device
 memory and the current CUDA stream. Every step of the computation runs in this
 package's CUDA kernels; if the library is missing the calls raise.
 """
@@ -26,12 +28,17 @@ import torch
 
 from . import _native
 from ._native import KlaError  # noqa: F401
+from .block import (add_norm_bwd, add_norm_fwd, gated_norm_bwd, gated_norm_fwd, gated_scan_bwd,  # noqa: F401
+                    gated_scan_fwd, gated_scan_step, gated_scan_workspace_size, rotary_bwd, rotary_freqs, rotary_fwd,
+                    verify_draft)
 from .layer import (beam_select, layer_norm_bwd, layer_norm_fwd, linear_bwd, linear_fwd, linear_step,  # noqa: F401
                     linear_workspace_size, reorder_states)
 
 __all__ = ["chunk_fwd", "chunk_fwd_host", "chunk_bwd", "decode_step", "workspace_size", "bwd_workspace_size",
            "device_status", "KlaError", "linear_fwd", "linear_bwd", "linear_step", "linear_workspace_size",
-           "layer_norm_fwd", "layer_norm_bwd", "beam_select", "reorder_states"]
+           "layer_norm_fwd", "layer_norm_bwd", "beam_select", "reorder_states", "gated_scan_fwd", "gated_scan_bwd",
+           "gated_scan_step", "gated_scan_workspace_size", "rotary_fwd", "rotary_bwd", "rotary_freqs",
+           "gated_norm_fwd", "gated_norm_bwd", "add_norm_fwd", "add_norm_bwd", "verify_draft"]
 
 
 def _dtype_code(t: torch.Tensor) -> int:

@@ -25,6 +25,14 @@ KLA_GATE_SCALAR = 0
 KLA_GATE_CHANNEL = 1
 KLA_BETA_KACZMARZ = 0
 KLA_BETA_RAW = 1
+KLA_SCAN_SIGMOID = 0
+KLA_SCAN_LOG = 1
+KLA_ROTARY_HALF = 0
+KLA_ROTARY_INTERLEAVED = 1
+KLA_NORM_RMS = 0
+KLA_NORM_LAYER = 1
+KLA_ACT_SILU = 0
+KLA_ACT_SIGMOID = 1
 
 _lock = threading.Lock()
 _lib = None
@@ -79,10 +87,24 @@ def _declare(lib):
     lib.kla_beam_select.argtypes = [vp, i64, fp, vp, i, fp, vp, vp, vp, i, i, i, i, vp, sz, vp]
     lib.kla_beam_select_workspace_size.argtypes = [i, i, i, i]
     lib.kla_reorder_states.argtypes = [vp, vp, vp, i, i, sz, vp]
+    lib.kla_gated_scan_fwd.argtypes = [vp, vp, vp, vp, fp, vp, fp, fp, i, i, i, i, i, vp, sz, vp]
+    lib.kla_gated_scan_bwd.argtypes = [vp, vp, vp, vp, vp, fp, fp, vp, vp, fp, i, i, i, i, i, vp, sz, vp]
+    lib.kla_gated_scan_step.argtypes = [vp, i64, vp, i64, fp, vp, i, i, i, i, vp]
+    lib.kla_gated_scan_workspace_size.argtypes = [i, i, i, i]
+    lib.kla_rotary.argtypes = [vp, vp, vp, vp, vp, fp, vp, i, i, i, i, i, i, i, i, i, f, i, vp]
+    lib.kla_gated_norm_fwd.argtypes = [vp, vp, i64, fp, i, vp, fp, fp, i64, i, i, i, i, i, f, vp]
+    lib.kla_gated_norm_bwd.argtypes = [vp, vp, vp, i64, fp, i, fp, fp, vp, vp, fp, i64, i, i, i, i, vp, sz, vp]
+    lib.kla_gated_norm_bwd_workspace_size.argtypes = [i64, i, i, i, i]
+    lib.kla_add_norm_fwd.argtypes = [vp, vp, fp, fp, vp, vp, fp, fp, i64, i, i, i, f, vp]
+    lib.kla_add_norm_bwd.argtypes = [vp, vp, vp, vp, fp, fp, fp, fp, vp, vp, fp, fp, i64, i, i, vp, sz, vp]
+    lib.kla_add_norm_bwd_workspace_size.argtypes = [i64, i, i]
+    lib.kla_verify_draft.argtypes = [vp, vp, vp, vp, fp, vp, vp, vp, i, i, i, i, vp]
     for name in ("linear_fwd", "linear_bwd", "linear_step", "layer_norm_fwd", "layer_norm_bwd", "beam_select",
-                 "reorder_states"):
+                 "reorder_states", "gated_scan_fwd", "gated_scan_bwd", "gated_scan_step", "rotary", "gated_norm_fwd",
+                 "gated_norm_bwd", "add_norm_fwd", "add_norm_bwd", "verify_draft"):
         getattr(lib, "kla_" + name).restype = ctypes.c_int
-    for name in ("linear_fwd", "linear_bwd", "layer_norm_bwd", "beam_select"):
+    for name in ("linear_fwd", "linear_bwd", "layer_norm_bwd", "beam_select", "gated_scan", "gated_norm_bwd",
+                 "add_norm_bwd"):
         getattr(lib, f"kla_{name}_workspace_size").restype = sz
     lib.kla_selftest_wait_timeout.argtypes = [ctypes.c_uint, vp]
     lib.kla_selftest_wait_timeout.restype = ctypes.c_int
