@@ -13,6 +13,7 @@
 #include "../../include/kla_block.h"
 
 namespace kla {
+cudaError_t device_error_word(unsigned **out);   // kla_api.cu
 namespace {
 
 struct ScanArgs {
@@ -24,86 +25,446 @@ struct ScanArgs {
     float *h_T;                       // backward: dh0
     float *states;
     int B, T, C;
+    int blocks, tiles;                // channel blocks of a sequence, tiles along its tokens
+    struct Head *head;                // of the workspace; NULL with one tile along the tokens
+    uint2 *carry;                     // [B][tiles][C]
+    unsigned *err;
+};
+// The workspace: this, then what tiles tell each other. All bits set before the kernel starts.
+struct Head {
+    unsigned ticket, abort;
+    unsigned pad[2];
 };
 
 __device__ __forceinline__ int valid_tokens(const ScanArgs &p, int b) {
     return p.lengths ? min(max(p.lengths[b], 0), p.T) : p.T;
 }
 
-// The state's factor a and the input's w. exp(gate) is held below 2^100: w stays a normal number, a is 1.
-template <bool kLog>
-__device__ __forceinline__ void factors(float gate, float &a, float &w) {
+// exp(gate), for the sigmoid held below 2^100: w stays a normal number then, and a is 1. bf16 gates take the
+// hardware's exponential and reciprocal, off by 2^-21 at gates of 10, far below the gate's own 2^-9.
+template <typename T, bool kLog>
+__device__ __forceinline__ float gate_exp(float gate) {
+    float e;
+    if (sizeof(T) == 2) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(gate * 1.4426950408889634f));
+    else e = expf(gate);
+    return !kLog && e > 0x1p100f ? 0x1p100f : e;
+}
+// The state's factor a and the input's w.
+template <typename T, bool kLog>
+__device__ __forceinline__ void factors(float e, float &a, float &w) {
     if (kLog) {
-        a = expf(gate);
+        a = e;
         w = 1.f;
     } else {
-        float e = expf(gate);
-        e = e > 0x1p100f ? 0x1p100f : e;
-        w = 1.f / (1.f + e);
+        if (sizeof(T) == 2) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(1.f + e));
+        else w = __frcp_rn(1.f + e);
         a = e * w;
     }
 }
+// One number that says both: a where KLA_SCAN_LOG; else the smaller of w and a, the latter with its sign set.
 template <bool kLog>
-__device__ __forceinline__ float advance(float h, float x, float a, float w) {
-    if (kLog) return fmaf(a, h, x);
-    return w < 0.5f ? fmaf(w, x - h, h) : fmaf(a, h - x, x);
+__device__ __forceinline__ float coefficient(float a, float w) {
+    return kLog ? a : w < 0.5f ? w : -a;
+}
+template <bool kLog>
+__device__ __forceinline__ float advance(float h, float x, float c) {
+    return kLog ? fmaf(c, h, x) : fmaf(c, x - h, c > 0.f ? h : x);
+}
+// prod a, one factor on
+template <bool kLog>
+__device__ __forceinline__ float shrink(float A, float c) {
+    return kLog ? c * A : fmaf(-c, A, c > 0.f ? A : 0.f);
 }
 
-// A thread per channel walks all tokens.
-template <typename T, bool kLog>
-__global__ void scan_fwd_kernel(ScanArgs p) {
-    const int c = blockIdx.x * blockDim.x + threadIdx.x, b = blockIdx.y;
-    if (c >= p.C) return;
-    const T *x = static_cast<const T *>(p.x) + b * p.xb + c, *g = static_cast<const T *>(p.gate) + b * p.gb + c;
-    T *y = static_cast<T *>(p.y) + static_cast<int64_t>(b) * p.T * p.C + c;
-    const int n = valid_tokens(p, b);
-    const int64_t spans = (p.T + KLA_SCAN_SPAN - 1) / KLA_SCAN_SPAN;
-    float h = p.h0 ? p.h0[static_cast<int64_t>(b) * p.C + c] : 0.f;
-    for (int t = 0; t < n; ++t) {
-        if (p.states && t % KLA_SCAN_SPAN == 0) p.states[(b * spans + t / KLA_SCAN_SPAN) * p.C + c] = h;
-        float a, w;
-        factors<kLog>(to_f32(g[t * p.gt]), a, w);
-        h = advance<kLog>(h, to_f32(x[t * p.xt]), a, w);
-        y[static_cast<int64_t>(t) * p.C] = from_f32<T>(h);
+// kV neighbouring values of type T in one access.
+template <typename T, int kV>
+struct Pack;
+template <>
+struct Pack<__nv_bfloat16, 2> {
+    uint32_t r;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { r = *reinterpret_cast<const uint32_t *>(p); }
+    __device__ __forceinline__ float operator[](int i) const {
+        return __uint_as_float(i ? r & 0xffff0000u : r << 16);
     }
-    for (int t = n; t < p.T; ++t) y[static_cast<int64_t>(t) * p.C] = from_f32<T>(0.f);
-    if (p.h_T) p.h_T[static_cast<int64_t>(b) * p.C + c] = h;
+    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&v)[2]) {
+        *reinterpret_cast<uint32_t *>(p) = ptx::pack_bf16(v[0], v[1]);
+    }
+};
+template <>
+struct Pack<float, 2> {
+    float2 r;
+    __device__ __forceinline__ void load(const float *p) { r = *reinterpret_cast<const float2 *>(p); }
+    __device__ __forceinline__ float operator[](int i) const { return i ? r.y : r.x; }
+    static __device__ __forceinline__ void store(float *p, const float (&v)[2]) {
+        *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
+    }
+};
+template <typename T>
+struct Pack<T, 1> {
+    T r;
+    __device__ __forceinline__ void load(const T *p) { r = *p; }
+    __device__ __forceinline__ float operator[](int) const { return to_f32(r); }
+    static __device__ __forceinline__ void store(T *p, const float (&v)[1]) { *p = from_f32<T>(v[0]); }
+};
+
+// What a tile tells the next ones of a channel, in one 64-bit word (whose two halves arrive together, so that no
+// fences are needed): first how it maps the state that enters it, {A, H}: h -> A h + H; then, once that state is
+// known, {kWhole, the state that leaves it}. A workspace of set bits says nothing yet.
+constexpr unsigned kEmpty = 0xffffffffu, kWhole = 0xfffffffeu, kNan = 0x7fffffffu;
+__device__ __forceinline__ unsigned factor_bits(float a) { return a == a ? __float_as_uint(a) : kNan; }
+template <int kV>
+__device__ __forceinline__ void tell(uint2 *p, const uint2 (&v)[kV]) {
+#pragma unroll
+    for (int i = 0; i < kV; ++i)
+        asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(p + i),
+                     "l"(static_cast<unsigned long long>(v[i].y) << 32 | v[i].x)
+                     : "memory");
+}
+__device__ __forceinline__ uint2 hear(const uint2 *p) {
+    unsigned long long v;
+    asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return make_uint2(static_cast<unsigned>(v), static_cast<unsigned>(v >> 32));
 }
 
-template <typename T, bool kLog>
-__global__ void scan_bwd_kernel(ScanArgs p) {
-    const int c = blockIdx.x * blockDim.x + threadIdx.x, b = blockIdx.y;
-    if (c >= p.C) return;
-    const T *x = static_cast<const T *>(p.x) + b * p.xb + c, *g = static_cast<const T *>(p.gate) + b * p.gb + c;
-    const T *dy = static_cast<const T *>(p.dy) + b * p.db + c;
-    const int64_t out0 = static_cast<int64_t>(b) * p.T * p.C + c;
-    T *dx = static_cast<T *>(p.y) + out0, *dg = static_cast<T *>(p.dg) + out0;
-    const int n = valid_tokens(p, b);
-    const int64_t spans = (p.T + KLA_SCAN_SPAN - 1) / KLA_SCAN_SPAN;
-    for (int t = n; t < p.T; ++t) {
-        dx[static_cast<int64_t>(t) * p.C] = from_f32<T>(0.f);
-        dg[static_cast<int64_t>(t) * p.C] = from_f32<T>(0.f);
-    }
-    float e = p.h0 ? p.h0[static_cast<int64_t>(b) * p.C + c] : 0.f;   // what reaches the state after token t
-    float before[KLA_SCAN_SPAN];
-    for (int s = (n + KLA_SCAN_SPAN - 1) / KLA_SCAN_SPAN - 1; s >= 0; --s) {
-        const int t0 = s * KLA_SCAN_SPAN, m = min(n - t0, KLA_SCAN_SPAN);
-        float h = p.states[(b * spans + s) * p.C + c], a, w;
-        for (int i = 0; i < m; ++i) {
-            before[i] = h;
-            factors<kLog>(to_f32(g[(t0 + i) * p.gt]), a, w);
-            h = advance<kLog>(h, to_f32(x[(t0 + i) * p.xt]), a, w);
+// The state that enters a tile, from what the `left` tiles before it told: `p` is the nearest one's word of this
+// thread's first channel, `hop` leads to the next further one. Of the nearest kAhead tiles one has to know the state
+// that leaves it, and the maps of those in between are applied to that in their order, as they apply them
+// themselves: whatever is known when, the bits are the same. The chain's first tile tells kWhole at once. Tiles are
+// taken by ticket in the order of the chain, so that all of those are running or done and none of them waits for a
+// later one: the wait ends. Its limit is for what cannot be foreseen. Run by a whole warp; false where it gave up.
+template <int kV>
+__device__ __forceinline__ bool entering(const uint2 *p, int64_t hop, int left, bool live, const Head *head,
+                                         float (&h)[kV]) {
+    constexpr int kAhead = 8;
+    constexpr unsigned kLimit = 1u << 21;
+#pragma unroll
+    for (int v = 0; v < kV; ++v) h[v] = 0.f;
+    for (unsigned polls = 0; polls < kLimit; ++polls) {
+        uint2 w[kAhead][kV];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+            for (int v = 0; v < kV; ++v) w[j][v] = live && j < left ? hear(p + j * hop + v) : make_uint2(kEmpty, 0u);
+        int found[kV];
+        bool known = true;
+#pragma unroll
+        for (int v = 0; v < kV; ++v) {
+            found[v] = -1;
+            bool told = true;
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                if (told && found[v] < 0 && w[j][v].x == kWhole) found[v] = j;
+                told &= w[j][v].x != kEmpty;
+            }
+            known &= found[v] >= 0;
         }
-        for (int i = m - 1; i >= 0; --i) {
-            const int64_t t = t0 + i;
-            factors<kLog>(to_f32(g[t * p.gt]), a, w);
-            const float dh = to_f32(dy[t * p.dt]) + e;
-            dx[t * p.C] = from_f32<T>(w * dh);
-            dg[t * p.C] = from_f32<T>(kLog ? a * before[i] * dh : a * w * (before[i] - to_f32(x[t * p.xt])) * dh);
-            e = a * dh;
+        if (__all_sync(0xffffffffu, known || !live)) {
+#pragma unroll
+            for (int j = kAhead - 1; j >= 0; --j)
+#pragma unroll
+                for (int v = 0; v < kV; ++v) {
+                    const float y = __uint_as_float(w[j][v].y);
+                    if (j == found[v]) h[v] = y;
+                    else if (j < found[v]) h[v] = fmaf(__uint_as_float(w[j][v].x), h[v], y);
+                }
+            return true;
         }
+        if ((polls & 63u) == 63u && *reinterpret_cast<const volatile unsigned *>(&head->abort) == 0u) return false;
     }
-    if (p.h_T) p.h_T[static_cast<int64_t>(b) * p.C + c] = e;
+    return false;
+}
+
+// Which tile a CTA has: `at` tiles along the chain (forward: from the first token on), of channels c0 ..
+struct Tile {
+    int b, c0, at;
+    __device__ __forceinline__ Tile(const ScanArgs &p, int width) {
+        unsigned ticket = blockIdx.x;
+        if (p.head) {
+            __shared__ unsigned mine;
+            if (threadIdx.x == 0) mine = atomicAdd(&p.head->ticket, 1u) + 1u;   // from all bits set
+            __syncthreads();
+            ticket = mine;
+        }
+        const unsigned chains = static_cast<unsigned>(p.B) * p.blocks, rest = ticket % chains;
+        at = ticket / chains;
+        b = rest / p.blocks;
+        c0 = rest % p.blocks * width;
+    }
+};
+
+// A tile is kWarps x kTok tokens of 32 kV channels; a thread holds kTok tokens of kV channels in registers, all of its
+// loads on their way at once. Every warp finds how its tokens map a state, the last one joins those maps, tells
+// the tile's own, hears the state that enters the tile and tells the one that leaves it; then every warp walks its tokens.
+template <typename T, bool kLog, int kV, int kTok, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps) scan_fwd_kernel(ScanArgs p) {
+    constexpr int kTile = kTok * kWarps;
+    __shared__ float2 maps[kWarps][32 * kV];
+    __shared__ float enter[32 * kV];
+    const Tile at(p, 32 * kV);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int b = at.b, c = at.c0 + lane * kV, n = valid_tokens(p, b);
+    const bool live = c < p.C;
+    const int first = at.at * kTile, t0 = first + warp * kTok;
+    const int64_t row = static_cast<int64_t>(b) * p.T + t0;
+    T *y = static_cast<T *>(p.y) + row * p.C + c;
+    const int last = n > 0 ? (n - 1) / kTile : 0;
+    if (at.at > last) {   // nothing but masked tokens
+        const float zero[kV] = {};
+        if (live)
+            for (int i = 0; i < kTok && t0 + i < p.T; ++i) Pack<T, kV>::store(y + static_cast<int64_t>(i) * p.C, zero);
+        return;
+    }
+    const int m = min(max(n - t0, 0), kTok);   // of this warp's tokens, how many are valid
+    Pack<T, kV> x[kTok], g[kTok];
+    {
+        const T *px = static_cast<const T *>(p.x) + b * p.xb + t0 * p.xt + c;
+        const T *pg = static_cast<const T *>(p.gate) + b * p.gb + t0 * p.gt + c;
+#pragma unroll
+        for (int i = 0; i < kTok; ++i)
+            if (live && i < m) {
+                x[i].load(px + i * p.xt);
+                g[i].load(pg + i * p.gt);
+            }
+    }
+    float co[kTok][kV], A[kV], H[kV];
+#pragma unroll
+    for (int v = 0; v < kV; ++v) A[v] = 1.f, H[v] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kTok; ++i)
+        if (i < m) {
+#pragma unroll
+            for (int v = 0; v < kV; ++v) {
+                float a, w;
+                factors<T, kLog>(gate_exp<T, kLog>(g[i][v]), a, w);
+                co[i][v] = coefficient<kLog>(a, w);
+                A[v] = shrink<kLog>(A[v], co[i][v]);
+                H[v] = advance<kLog>(H[v], x[i][v], co[i][v]);
+            }
+        }
+#pragma unroll
+    for (int v = 0; v < kV; ++v) maps[warp][v * 32 + lane] = make_float2(A[v], H[v]);
+    __syncthreads();
+    // the map of the tile's tokens before this warp's
+    float pa[kV], ph[kV];
+#pragma unroll
+    for (int v = 0; v < kV; ++v) pa[v] = 1.f, ph[v] = 0.f;
+    for (int w = 0; w < warp; ++w)
+#pragma unroll
+        for (int v = 0; v < kV; ++v) {
+            const float2 f = maps[w][v * 32 + lane];
+            ph[v] = fmaf(f.x, ph[v], f.y);
+            pa[v] *= f.x;
+        }
+    if (warp == kWarps - 1) {
+        float in[kV];
+        uint2 word[kV];
+        uint2 *here = p.carry + (static_cast<int64_t>(b) * p.tiles + at.at) * p.C + c;
+#pragma unroll
+        for (int v = 0; v < kV; ++v) {
+            H[v] = fmaf(A[v], ph[v], H[v]);
+            A[v] *= pa[v];
+        }
+        if (at.at == 0) {
+#pragma unroll
+            for (int v = 0; v < kV; ++v) in[v] = p.h0 && live ? p.h0[static_cast<int64_t>(b) * p.C + c + v] : 0.f;
+        } else {
+#pragma unroll
+            for (int v = 0; v < kV; ++v) word[v] = make_uint2(factor_bits(A[v]), __float_as_uint(H[v]));
+            if (live && at.at < last) tell<kV>(here, word);
+            if (!entering<kV>(here - p.C, -static_cast<int64_t>(p.C), at.at, live, p.head, in)) {
+                atomicOr(p.err, kErrTimeout);
+                p.head->abort = 0u;
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < kV; ++v) {
+            enter[v * 32 + lane] = in[v];
+            H[v] = fmaf(A[v], in[v], H[v]);
+            word[v] = make_uint2(kWhole, __float_as_uint(H[v]));
+        }
+        if (live && at.at < last) tell<kV>(here, word);
+        if (live && at.at == last && p.h_T)
+#pragma unroll
+            for (int v = 0; v < kV; ++v) p.h_T[static_cast<int64_t>(b) * p.C + c + v] = H[v];
+    }
+    __syncthreads();
+    if (!live) return;
+    float h[kV];
+#pragma unroll
+    for (int v = 0; v < kV; ++v) h[v] = fmaf(pa[v], enter[v * 32 + lane], ph[v]);
+    if (p.states && m > 0 && t0 % KLA_SCAN_SPAN == 0) {
+        const int64_t spans = (p.T + KLA_SCAN_SPAN - 1) / KLA_SCAN_SPAN;
+        float *s = p.states + (b * spans + t0 / KLA_SCAN_SPAN) * p.C + c;
+#pragma unroll
+        for (int v = 0; v < kV; ++v) s[v] = h[v];
+    }
+#pragma unroll
+    for (int i = 0; i < kTok; ++i)
+        if (i < m) {
+#pragma unroll
+            for (int v = 0; v < kV; ++v) h[v] = advance<kLog>(h[v], x[i][v], co[i][v]);
+            Pack<T, kV>::store(y + static_cast<int64_t>(i) * p.C, h);
+        } else if (t0 + i < p.T) {
+            const float zero[kV] = {};
+            Pack<T, kV>::store(y + static_cast<int64_t>(i) * p.C, zero);
+        }
+}
+
+// The same against time: what reaches the state behind a token's is e_{t-1} = a_t (dy_t + e_t), and a tile's map
+// {A, D} is e -> A e + D with D = sum of dy_t times the product of the tile's gates up to t. A tile is one span, whose
+// entering state the forward pass has kept; h_{t-1} is walked from it again.
+template <typename T, bool kLog, int kV, int kTok, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(ScanArgs p) {
+    constexpr int kTile = kTok * kWarps;
+    static_assert(kTile == KLA_SCAN_SPAN, "");
+    __shared__ float2 maps[kWarps][32 * kV];
+    __shared__ float backs[kWarps][32 * kV], enter[32 * kV];
+    const Tile at(p, 32 * kV);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int b = at.b, c = at.c0 + lane * kV, n = valid_tokens(p, b), tile = p.tiles - 1 - at.at;
+    const bool live = c < p.C;
+    const int t0 = tile * kTile + warp * kTok;
+    const int64_t row = static_cast<int64_t>(b) * p.T + t0;
+    T *dx = static_cast<T *>(p.y) + row * p.C + c, *dg = static_cast<T *>(p.dg) + row * p.C + c;
+    const float zero[kV] = {};
+    const int last = n > 0 ? (n - 1) / kTile : 0;
+    if (tile > last) {
+        if (live)
+            for (int i = 0; i < kTok && t0 + i < p.T; ++i) {
+                Pack<T, kV>::store(dx + static_cast<int64_t>(i) * p.C, zero);
+                Pack<T, kV>::store(dg + static_cast<int64_t>(i) * p.C, zero);
+            }
+        return;
+    }
+    const int m = min(max(n - t0, 0), kTok);
+    Pack<T, kV> x[kTok], d[kTok];
+    float e[kTok][kV], h[kV];   // e: exp(gate)
+    {
+        Pack<T, kV> g[kTok];
+        const T *px = static_cast<const T *>(p.x) + b * p.xb + t0 * p.xt + c;
+        const T *pg = static_cast<const T *>(p.gate) + b * p.gb + t0 * p.gt + c;
+        const T *pd = static_cast<const T *>(p.dy) + b * p.db + t0 * p.dt + c;
+#pragma unroll
+        for (int i = 0; i < kTok; ++i)
+            if (live && i < m) {
+                g[i].load(pg + i * p.gt);
+                x[i].load(px + i * p.xt);
+                d[i].load(pd + i * p.dt);
+            }
+        const float *s = p.states + (static_cast<int64_t>(b) * p.tiles + tile) * p.C + c;
+#pragma unroll
+        for (int v = 0; v < kV; ++v) h[v] = live && n > 0 ? s[v] : 0.f;
+#pragma unroll
+        for (int i = 0; i < kTok; ++i)
+#pragma unroll
+            for (int v = 0; v < kV; ++v) e[i][v] = i < m ? gate_exp<T, kLog>(g[i][v]) : 0.f;
+    }
+    float A[kV], H[kV], D[kV];
+#pragma unroll
+    for (int v = 0; v < kV; ++v) A[v] = 1.f, H[v] = D[v] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kTok; ++i)
+        if (i < m) {
+#pragma unroll
+            for (int v = 0; v < kV; ++v) {
+                float a, w;
+                factors<T, kLog>(e[i][v], a, w);
+                const float co = coefficient<kLog>(a, w);
+                A[v] = shrink<kLog>(A[v], co);
+                H[v] = advance<kLog>(H[v], x[i][v], co);
+                D[v] = fmaf(A[v], d[i][v], D[v]);
+            }
+        }
+#pragma unroll
+    for (int v = 0; v < kV; ++v) {
+        maps[warp][v * 32 + lane] = make_float2(A[v], H[v]);
+        backs[warp][v * 32 + lane] = D[v];
+    }
+    __syncthreads();
+    float sa[kV], sd[kV];   // the map of the tile's tokens after this warp's
+#pragma unroll
+    for (int v = 0; v < kV; ++v) sa[v] = 1.f, sd[v] = 0.f;
+    for (int w = kWarps - 1; w > warp; --w)
+#pragma unroll
+        for (int v = 0; v < kV; ++v) {
+            const float f = maps[w][v * 32 + lane].x;
+            sd[v] = fmaf(f, sd[v], backs[w][v * 32 + lane]);
+            sa[v] *= f;
+        }
+    if (warp == 0) {
+        float in[kV];
+        uint2 word[kV];
+        uint2 *here = p.carry + (static_cast<int64_t>(b) * p.tiles + tile) * p.C + c;
+#pragma unroll
+        for (int v = 0; v < kV; ++v) {
+            D[v] = fmaf(A[v], sd[v], D[v]);
+            A[v] *= sa[v];
+        }
+        if (tile == last) {
+#pragma unroll
+            for (int v = 0; v < kV; ++v) in[v] = p.h0 && live ? p.h0[static_cast<int64_t>(b) * p.C + c + v] : 0.f;
+        } else {
+#pragma unroll
+            for (int v = 0; v < kV; ++v) word[v] = make_uint2(factor_bits(A[v]), __float_as_uint(D[v]));
+            if (live && tile > 0) tell<kV>(here, word);
+            if (!entering<kV>(here + p.C, p.C, last - tile, live, p.head, in)) {
+                atomicOr(p.err, kErrTimeout);
+                p.head->abort = 0u;
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < kV; ++v) {
+            enter[v * 32 + lane] = in[v];
+            D[v] = fmaf(A[v], in[v], D[v]);
+            word[v] = make_uint2(kWhole, __float_as_uint(D[v]));
+        }
+        if (live && tile > 0) tell<kV>(here, word);
+        if (live && tile == 0 && p.h_T)
+#pragma unroll
+            for (int v = 0; v < kV; ++v) p.h_T[static_cast<int64_t>(b) * p.C + c + v] = D[v];
+    }
+    // the states before this warp's tokens, while the first one waits
+    for (int w = 0; w < warp; ++w)
+#pragma unroll
+        for (int v = 0; v < kV; ++v) {
+            const float2 f = maps[w][v * 32 + lane];
+            h[v] = fmaf(f.x, h[v], f.y);
+        }
+    float before[kTok][kV];
+#pragma unroll
+    for (int i = 0; i < kTok; ++i)
+        if (i < m) {
+#pragma unroll
+            for (int v = 0; v < kV; ++v) {
+                float a, w;
+                factors<T, kLog>(e[i][v], a, w);
+                before[i][v] = h[v];
+                h[v] = advance<kLog>(h[v], x[i][v], coefficient<kLog>(a, w));
+            }
+        }
+    __syncthreads();
+    if (!live) return;
+#pragma unroll
+    for (int v = 0; v < kV; ++v) h[v] = fmaf(sa[v], enter[v * 32 + lane], sd[v]);   // now what reaches the state
+#pragma unroll
+    for (int i = kTok - 1; i >= 0; --i)
+        if (i < m) {
+            float ox[kV], og[kV];
+#pragma unroll
+            for (int v = 0; v < kV; ++v) {
+                float a, w;
+                factors<T, kLog>(e[i][v], a, w);
+                const float dh = d[i][v] + h[v];
+                h[v] = a * dh;
+                ox[v] = w * dh;
+                og[v] = kLog ? before[i][v] * h[v] : w * (before[i][v] - x[i][v]) * h[v];
+            }
+            Pack<T, kV>::store(dx + static_cast<int64_t>(i) * p.C, ox);
+            Pack<T, kV>::store(dg + static_cast<int64_t>(i) * p.C, og);
+        } else if (t0 + i < p.T) {
+            Pack<T, kV>::store(dx + static_cast<int64_t>(i) * p.C, zero);
+            Pack<T, kV>::store(dg + static_cast<int64_t>(i) * p.C, zero);
+        }
 }
 
 template <typename T, bool kLog>
@@ -112,17 +473,25 @@ __global__ void scan_step_kernel(const T *x, int64_t xs, const T *gate, int64_t 
     if (c >= C) return;
     const int64_t at = static_cast<int64_t>(b) * C + c;
     float a, w;
-    factors<kLog>(to_f32(gate[b * gs + c]), a, w);
-    const float v = advance<kLog>(h[at], to_f32(x[b * xs + c]), a, w);
+    factors<T, kLog>(gate_exp<T, kLog>(to_f32(gate[b * gs + c])), a, w);
+    const float v = advance<kLog>(h[at], to_f32(x[b * xs + c]), coefficient<kLog>(a, w));
     h[at] = v;
     y[at] = from_f32<T>(v);
 }
+
+// Tokens of a thread and warps of a CTA: the forward pass holds two values a token and channel, the backward five.
+constexpr int kFwdTok = 16, kFwdWarps = 8, kBwdTok = 8, kBwdWarps = 8;
+static_assert(kFwdTok * kFwdWarps % KLA_SCAN_SPAN == 0 && KLA_SCAN_SPAN % kFwdTok == 0, "");
+
+int tiles_of(int T, int tile) { return T > tile ? (T + tile - 1) / tile : 1; }
 
 kla_status check(int B, int T, int C, kla_dtype dtype, kla_scan_mode mode) {
     if (B < 1 || T < 0 || C < 1) return KLA_ERR_INVALID_ARG;
     if (dtype != KLA_DTYPE_F32 && dtype != KLA_DTYPE_BF16) return KLA_ERR_INVALID_ARG;
     if (mode != KLA_SCAN_SIGMOID && mode != KLA_SCAN_LOG) return KLA_ERR_INVALID_ARG;
     if (T > INT_MAX - 65536 || B > 65535) return KLA_ERR_UNSUPPORTED;
+    // a ticket for every tile of 32 channels
+    if (static_cast<int64_t>(B) * ((C + 31) / 32) > INT_MAX / tiles_of(T, KLA_SCAN_SPAN)) return KLA_ERR_UNSUPPORTED;
     return KLA_OK;
 }
 
@@ -130,6 +499,31 @@ kla_status check(int B, int T, int C, kla_dtype dtype, kla_scan_mode mode) {
 size_t reach(int B, int T, int C, int64_t sb, int64_t st, size_t esz) {
     return T == 0 ? 0 : (static_cast<size_t>(B - 1) * sb + static_cast<size_t>(T - 1) * st + C) * esz;
 }
+
+// Bytes of the words between tiles of `tile` tokens, and in front of them the tickets.
+size_t carry_bytes(int B, int T, int C, int tile) {
+    const int tiles = tiles_of(T, tile);
+    return tiles == 1 ? 0 : sizeof(Head) + (static_cast<size_t>(B) * tiles * C * sizeof(uint2) + 15) / 16 * 16;
+}
+
+// Whether neighbouring channels can be moved in pairs.
+bool in_pairs(const ScanArgs &p, size_t esz) {
+    for (const void *a : {p.x, p.gate, p.dy, static_cast<const void *>(p.y), static_cast<const void *>(p.dg)})
+        if (!aligned(a, 2 * esz)) return false;
+    return p.C % 2 == 0 && (p.xb | p.xt | p.gb | p.gt | p.db | p.dt) % 2 == 0;
+}
+
+// Sets up the tiles of 32 kV channels and `tile` tokens, and what they tell each other.
+cudaError_t lay_out(ScanArgs &p, int tile, int width, void *workspace, cudaStream_t s) {
+    p.blocks = (p.C + width - 1) / width;
+    p.tiles = tiles_of(p.T, tile);
+    if (p.tiles == 1) return cudaSuccess;
+    p.head = static_cast<Head *>(workspace);
+    p.carry = reinterpret_cast<uint2 *>(p.head + 1);
+    const cudaError_t e = device_error_word(&p.err);
+    return e == cudaSuccess ? cudaMemsetAsync(workspace, 0xff, carry_bytes(p.B, p.T, p.C, tile), s) : e;
+}
+unsigned grid_of(const ScanArgs &p) { return static_cast<unsigned>(p.B) * p.blocks * p.tiles; }
 
 template <typename F>
 cudaError_t by_type(kla_dtype dtype, kla_scan_mode mode, F f) {
@@ -149,8 +543,10 @@ cudaError_t by_type(kla_dtype dtype, kla_scan_mode mode, F f) {
 extern "C" {
 
 size_t kla_gated_scan_workspace_size(int B, int T, int C, kla_dtype dtype) {
-    if (kla::check(B, T, C, dtype, KLA_SCAN_SIGMOID) != KLA_OK) return 0;
-    return 0;
+    using namespace kla;
+    if (check(B, T, C, dtype, KLA_SCAN_SIGMOID) != KLA_OK) return 0;
+    const size_t f = carry_bytes(B, T, C, kFwdTok * kFwdWarps), b = carry_bytes(B, T, C, kBwdTok * kBwdWarps);
+    return f > b ? f : b;
 }
 
 kla_status kla_gated_scan_fwd(const void *x, const void *gate, const int64_t *strides, const int *lengths,
@@ -166,7 +562,8 @@ kla_status kla_gated_scan_fwd(const void *x, const void *gate, const int64_t *st
         !aligned(h_T, 4) || !aligned(states, 4) || !aligned(workspace, 16))
         return KLA_ERR_INVALID_ARG;
     const int64_t tc = static_cast<int64_t>(T) * C;
-    ScanArgs p{x, gate, nullptr, tc, C, tc, C, 0, 0, lengths, h0, y, nullptr, h_T, states, B, T, C};
+    ScanArgs p{x, gate, nullptr, tc, C, tc, C, 0, 0, lengths, h0, y, nullptr, h_T, states, B, T, C,
+               0, 0, nullptr, nullptr, nullptr};
     if (strides) {
         for (int i = 0; i < 4; ++i)
             if (strides[i] < 0) return KLA_ERR_INVALID_ARG;
@@ -186,8 +583,13 @@ kla_status kla_gated_scan_fwd(const void *x, const void *gate, const int64_t *st
             if (overlaps(outs[i], outs[j])) return KLA_ERR_INVALID_ARG;
     }
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const bool pairs = in_pairs(p, esz);
+    if (lay_out(p, kFwdTok * kFwdWarps, pairs ? 64 : 32, workspace, cs) != cudaSuccess) return KLA_ERR_CUDA;
     const cudaError_t e = by_type(dtype, mode, [&](auto t, auto log) {
-        scan_fwd_kernel<decltype(t), decltype(log)::value><<<dim3((C + 31) / 32, B), 32, 0, cs>>>(p);
+        using E = decltype(t);
+        constexpr bool kLog = decltype(log)::value;
+        if (pairs) scan_fwd_kernel<E, kLog, 2, kFwdTok, kFwdWarps><<<grid_of(p), 32 * kFwdWarps, 0, cs>>>(p);
+        else scan_fwd_kernel<E, kLog, 1, kFwdTok, kFwdWarps><<<grid_of(p), 32 * kFwdWarps, 0, cs>>>(p);
     });
     return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
 }
@@ -206,7 +608,8 @@ kla_status kla_gated_scan_bwd(const void *x, const void *gate, const void *dy, c
         !aligned(workspace, 16))
         return KLA_ERR_INVALID_ARG;
     const int64_t tc = static_cast<int64_t>(T) * C;
-    ScanArgs p{x, gate, dy, tc, C, tc, C, tc, C, lengths, dh_T, dx, dgate, dh0, const_cast<float *>(states), B, T, C};
+    ScanArgs p{x, gate, dy, tc, C, tc, C, tc, C, lengths, dh_T, dx, dgate, dh0, const_cast<float *>(states), B, T, C,
+               0, 0, nullptr, nullptr, nullptr};
     if (strides) {
         for (int i = 0; i < 6; ++i)
             if (strides[i] < 0) return KLA_ERR_INVALID_ARG;
@@ -227,8 +630,13 @@ kla_status kla_gated_scan_bwd(const void *x, const void *gate, const void *dy, c
             if (overlaps(outs[i], outs[j])) return KLA_ERR_INVALID_ARG;
     }
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const bool pairs = in_pairs(p, esz);
+    if (lay_out(p, kBwdTok * kBwdWarps, pairs ? 64 : 32, workspace, cs) != cudaSuccess) return KLA_ERR_CUDA;
     const cudaError_t e = by_type(dtype, mode, [&](auto t, auto log) {
-        scan_bwd_kernel<decltype(t), decltype(log)::value><<<dim3((C + 31) / 32, B), 32, 0, cs>>>(p);
+        using E = decltype(t);
+        constexpr bool kLog = decltype(log)::value;
+        if (pairs) scan_bwd_kernel<E, kLog, 2, kBwdTok, kBwdWarps><<<grid_of(p), 32 * kBwdWarps, 0, cs>>>(p);
+        else scan_bwd_kernel<E, kLog, 1, kBwdTok, kBwdWarps><<<grid_of(p), 32 * kBwdWarps, 0, cs>>>(p);
     });
     return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
 }
