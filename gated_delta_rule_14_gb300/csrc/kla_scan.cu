@@ -7,6 +7,7 @@
 // The sigmoid's recurrence is taken as h + w (x - h) where w is the smaller of the two factors, as x + a (h - x) where
 // a is: where a gate keeps its state for thousands of tokens a is within 2^-11 of 1 and its rounding to 24 bits would
 // leave 12 of w, and where one drops a large state nothing of it may stay behind as a difference of roundings.
+#include <atomic>
 #include <climits>
 
 #include "layer_dev.cuh"
@@ -90,15 +91,6 @@ struct Pack<__nv_bfloat16, 2> {
         *reinterpret_cast<uint32_t *>(p) = ptx::pack_bf16(v[0], v[1]);
     }
 };
-template <>
-struct Pack<float, 2> {
-    float2 r;
-    __device__ __forceinline__ void load(const float *p) { r = *reinterpret_cast<const float2 *>(p); }
-    __device__ __forceinline__ float operator[](int i) const { return i ? r.y : r.x; }
-    static __device__ __forceinline__ void store(float *p, const float (&v)[2]) {
-        *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
-    }
-};
 template <typename T>
 struct Pack<T, 1> {
     T r;
@@ -174,23 +166,24 @@ __device__ __forceinline__ bool entering(const uint2 *p, int64_t hop, int left, 
     return false;
 }
 
-// Which tile a CTA has: `at` tiles along the chain (forward: from the first token on), of channels c0 ..
+// The tile of a ticket: `at` tiles along the chain, of channels c0 ..
 struct Tile {
     int b, c0, at;
-    __device__ __forceinline__ Tile(const ScanArgs &p, int width) {
-        unsigned ticket = blockIdx.x;
-        if (p.head) {
-            __shared__ unsigned mine;
-            if (threadIdx.x == 0) mine = atomicAdd(&p.head->ticket, 1u) + 1u;   // from all bits set
-            __syncthreads();
-            ticket = mine;
-        }
+    __device__ __forceinline__ Tile(const ScanArgs &p, unsigned ticket, int width) {
         const unsigned chains = static_cast<unsigned>(p.B) * p.blocks, rest = ticket % chains;
         at = ticket / chains;
         b = rest / p.blocks;
         c0 = rest % p.blocks * width;
     }
 };
+// One ticket for a whole CTA: tiles start in the order of the tickets.
+__device__ __forceinline__ unsigned take_ticket(const ScanArgs &p) {
+    if (!p.head) return blockIdx.x;
+    __shared__ unsigned mine;
+    if (threadIdx.x == 0) mine = atomicAdd(&p.head->ticket, 1u) + 1u;   // from all bits set
+    __syncthreads();
+    return mine;
+}
 
 // A tile is kWarps x kTok tokens of 32 kV channels; a thread holds kTok tokens of kV channels in registers, all of its
 // loads on their way at once. Every warp finds how its tokens map a state, the last one joins those maps, tells
@@ -200,7 +193,7 @@ __global__ void __launch_bounds__(32 * kWarps) scan_fwd_kernel(ScanArgs p) {
     constexpr int kTile = kTok * kWarps;
     __shared__ float2 maps[kWarps][32 * kV];
     __shared__ float enter[32 * kV];
-    const Tile at(p, 32 * kV);
+    const Tile at(p, take_ticket(p), 32 * kV);
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int b = at.b, c = at.c0 + lane * kV, n = valid_tokens(p, b);
     const bool live = c < p.C;
@@ -319,7 +312,7 @@ __global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(ScanArgs p) {
     static_assert(kTile == KLA_SCAN_SPAN, "");
     __shared__ float2 maps[kWarps][32 * kV];
     __shared__ float backs[kWarps][32 * kV], enter[32 * kV];
-    const Tile at(p, 32 * kV);
+    const Tile at(p, take_ticket(p), 32 * kV);
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int b = at.b, c = at.c0 + lane * kV, n = valid_tokens(p, b), tile = p.tiles - 1 - at.at;
     const bool live = c < p.C;
@@ -467,6 +460,376 @@ __global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(ScanArgs p) {
         }
 }
 
+// ---- tiles through shared memory: rows of 128 bytes (64 channels of bf16, 32 of fp32), 4 bytes a lane
+constexpr int kRow = 128;
+template <typename T>
+struct Lane {   // the channels of a lane
+    static constexpr int kV = 4 / sizeof(T);
+    using P = Pack<T, kV>;
+};
+__device__ __forceinline__ void copy16(uint32_t to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t to, const void *from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+// Rows 0 .. m - 1 of kTok into this warp's part of a buffer; `left` bytes of a row are there.
+template <int kTok>
+__device__ __forceinline__ void copy_rows(uint8_t *to, const void *from, int64_t pitch, int m, int left, bool wide) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t s = ptx::smem_u32(to);
+    const char *f = static_cast<const char *>(from);
+    if (wide) {
+        const int off = (lane & 7) * 16;
+#pragma unroll
+        for (int i = 0; i < kTok; i += 4) {
+            const int r = i + lane / 8;
+            if (r < m && off < left) copy16(s + r * kRow + off, f + r * pitch + off);
+        }
+    } else {
+        const int off = lane * 4;
+#pragma unroll
+        for (int i = 0; i < kTok; ++i)
+            if (i < m && off < left) copy4(s + i * kRow + off, f + i * pitch + off);
+    }
+}
+
+// Tiles one after the other. A CTA takes a ticket for its next tile while it works on one, not earlier, so that where
+// tiles are few no CTA has two of them and another none.
+struct Turns {
+    const ScanArgs &p;
+    unsigned total, now;
+    __device__ __forceinline__ Turns(const ScanArgs &a) : p(a) {
+        total = static_cast<unsigned>(a.B) * a.blocks * a.tiles;
+        now = blockIdx.x;
+    }
+    __device__ __forceinline__ unsigned ask() const {   // one thread
+        return p.head ? atomicAdd(&p.head->ticket, 1u) + 1u : now + gridDim.x;
+    }
+};
+
+template <typename T, bool kLog, int kTok, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, 3) scan_fwd_ring_kernel(ScanArgs p, bool wide) {
+    constexpr int kTile = kTok * kWarps, kV = Lane<T>::kV, kWidth = 32 * kV;
+    using P = typename Lane<T>::P;
+    extern __shared__ __align__(128) uint8_t buf[];   // x twice, gate once: kTile rows each
+    __shared__ float2 maps[kWarps][kWidth];
+    __shared__ float enter[kWidth];
+    __shared__ unsigned s_next;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    uint8_t *const mine = buf + warp * kTok * kRow;
+    uint8_t *const gates = mine + 2 * kTile * kRow;
+    Turns turns(p);
+    auto fetch = [&](unsigned ticket, int stage) {
+        const Tile at(p, ticket, kWidth);
+        const int t0 = at.at * kTile + warp * kTok, m = min(valid_tokens(p, at.b) - t0, kTok);
+        const int left = min(p.C - at.c0, kWidth) * static_cast<int>(sizeof(T));
+        copy_rows<kTok>(gates, static_cast<const T *>(p.gate) + at.b * p.gb + t0 * p.gt + at.c0, p.gt * sizeof(T), m,
+                        left, wide);
+        copy_rows<kTok>(mine + stage * kTile * kRow, static_cast<const T *>(p.x) + at.b * p.xb + t0 * p.xt + at.c0,
+                        p.xt * sizeof(T), m, left, wide);
+        copies_commit();
+    };
+    unsigned ticket = blockIdx.x;
+    if (p.head) {
+        if (threadIdx.x == 0) s_next = turns.ask();
+        __syncthreads();
+        ticket = s_next;
+        __syncthreads();
+    }
+    if (ticket < turns.total) fetch(ticket, 0);
+    for (int stage = 0; ticket < turns.total; stage ^= 1) {
+        const Tile at(p, ticket, kWidth);
+        turns.now = ticket;
+        unsigned asked = 0;
+        if (threadIdx.x == 0) asked = turns.ask();
+        const int b = at.b, c = at.c0 + lane * kV, n = valid_tokens(p, b), t0 = at.at * kTile + warp * kTok;
+        const bool live = c < p.C;
+        const int last = n > 0 ? (n - 1) / kTile : 0;
+        const int m = min(max(n - t0, 0), kTok);   // of this warp's tokens, how many are valid
+        T *y = static_cast<T *>(p.y) + (static_cast<int64_t>(b) * p.T + t0) * p.C + c;
+        const uint8_t *xs = mine + stage * kTile * kRow + lane * 4, *gs = gates + lane * 4;
+        float co[kTok][kV], A[kV], H[kV];
+#pragma unroll
+        for (int v = 0; v < kV; ++v) A[v] = 1.f, H[v] = 0.f;
+        copies_wait();
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kTok; ++i)
+            if (i < m) {
+                P x, g;
+                x.load(reinterpret_cast<const T *>(xs + i * kRow));
+                g.load(reinterpret_cast<const T *>(gs + i * kRow));
+#pragma unroll
+                for (int v = 0; v < kV; ++v) {
+                    float a, w;
+                    factors<T, kLog>(gate_exp<T, kLog>(g[v]), a, w);
+                    co[i][v] = coefficient<kLog>(a, w);
+                    A[v] = shrink<kLog>(A[v], co[i][v]);
+                    H[v] = advance<kLog>(H[v], x[v], co[i][v]);
+                }
+            }
+#pragma unroll
+        for (int v = 0; v < kV; ++v) maps[warp][v * 32 + lane] = make_float2(A[v], H[v]);
+        if (threadIdx.x == 0) s_next = asked;
+        __syncthreads();
+        const unsigned next = s_next;
+        if (next < turns.total) fetch(next, stage ^ 1);
+        // the map of the tile's tokens before this warp's
+        float pa[kV], ph[kV];
+#pragma unroll
+        for (int v = 0; v < kV; ++v) pa[v] = 1.f, ph[v] = 0.f;
+        for (int w = 0; w < warp; ++w)
+#pragma unroll
+            for (int v = 0; v < kV; ++v) {
+                const float2 f = maps[w][v * 32 + lane];
+                ph[v] = fmaf(f.x, ph[v], f.y);
+                pa[v] *= f.x;
+            }
+        if (warp == kWarps - 1 && at.at <= last) {
+            float in[kV];
+            uint2 word[kV];
+            uint2 *here = p.carry + (static_cast<int64_t>(b) * p.tiles + at.at) * p.C + c;
+#pragma unroll
+            for (int v = 0; v < kV; ++v) {
+                H[v] = fmaf(A[v], ph[v], H[v]);
+                A[v] *= pa[v];
+            }
+            if (at.at == 0) {
+#pragma unroll
+                for (int v = 0; v < kV; ++v) in[v] = p.h0 && live ? p.h0[static_cast<int64_t>(b) * p.C + c + v] : 0.f;
+            } else {
+#pragma unroll
+                for (int v = 0; v < kV; ++v) word[v] = make_uint2(factor_bits(A[v]), __float_as_uint(H[v]));
+                if (live && at.at < last) tell<kV>(here, word);
+                if (!entering<kV>(here - p.C, -static_cast<int64_t>(p.C), at.at, live, p.head, in)) {
+                    atomicOr(p.err, kErrTimeout);
+                    p.head->abort = 0u;
+                }
+            }
+#pragma unroll
+            for (int v = 0; v < kV; ++v) {
+                enter[v * 32 + lane] = in[v];
+                H[v] = fmaf(A[v], in[v], H[v]);
+                word[v] = make_uint2(kWhole, __float_as_uint(H[v]));
+            }
+            if (live && at.at < last) tell<kV>(here, word);
+            if (live && at.at == last && p.h_T)
+#pragma unroll
+                for (int v = 0; v < kV; ++v) p.h_T[static_cast<int64_t>(b) * p.C + c + v] = H[v];
+        }
+        __syncthreads();
+        if (live) {
+            float h[kV];
+#pragma unroll
+            for (int v = 0; v < kV; ++v) h[v] = fmaf(pa[v], enter[v * 32 + lane], ph[v]);
+            if (p.states && m > 0 && t0 % KLA_SCAN_SPAN == 0) {
+                const int64_t spans = (p.T + KLA_SCAN_SPAN - 1) / KLA_SCAN_SPAN;
+                float *s = p.states + (b * spans + t0 / KLA_SCAN_SPAN) * p.C + c;
+#pragma unroll
+                for (int v = 0; v < kV; ++v) s[v] = h[v];
+            }
+#pragma unroll
+            for (int i = 0; i < kTok; ++i)
+                if (i < m) {
+                    P x;
+                    x.load(reinterpret_cast<const T *>(xs + i * kRow));
+#pragma unroll
+                    for (int v = 0; v < kV; ++v) h[v] = advance<kLog>(h[v], x[v], co[i][v]);
+                    P::store(y + static_cast<int64_t>(i) * p.C, h);
+                } else if (t0 + i < p.T) {
+                    const float zero[kV] = {};
+                    P::store(y + static_cast<int64_t>(i) * p.C, zero);
+                }
+        }
+        __syncwarp();
+        ticket = next;
+    }
+}
+
+template <typename T, bool kLog, int kTok, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, 3) scan_bwd_ring_kernel(ScanArgs p, bool wide) {
+    constexpr int kTile = kTok * kWarps, kV = Lane<T>::kV, kWidth = 32 * kV;
+    using P = typename Lane<T>::P;
+    static_assert(kTile == KLA_SCAN_SPAN, "");
+    extern __shared__ __align__(128) uint8_t buf[];   // x and dy twice, gate once: kTile rows each
+    __shared__ float2 maps[kWarps][kWidth];
+    __shared__ float backs[kWarps][kWidth], enter[kWidth];
+    __shared__ unsigned s_next;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    uint8_t *const mine = buf + warp * kTok * kRow;
+    uint8_t *const gates = mine + 4 * kTile * kRow;
+    Turns turns(p);
+    auto fetch = [&](unsigned ticket, int stage) {
+        const Tile at(p, ticket, kWidth);
+        const int t0 = (p.tiles - 1 - at.at) * kTile + warp * kTok, m = min(valid_tokens(p, at.b) - t0, kTok);
+        const int left = min(p.C - at.c0, kWidth) * static_cast<int>(sizeof(T));
+        uint8_t *to = mine + 2 * stage * kTile * kRow;
+        copy_rows<kTok>(gates, static_cast<const T *>(p.gate) + at.b * p.gb + t0 * p.gt + at.c0, p.gt * sizeof(T), m,
+                        left, wide);
+        copy_rows<kTok>(to, static_cast<const T *>(p.x) + at.b * p.xb + t0 * p.xt + at.c0, p.xt * sizeof(T), m, left,
+                        wide);
+        copy_rows<kTok>(to + kTile * kRow, static_cast<const T *>(p.dy) + at.b * p.db + t0 * p.dt + at.c0,
+                        p.dt * sizeof(T), m, left, wide);
+        copies_commit();
+    };
+    unsigned ticket = blockIdx.x;
+    if (p.head) {
+        if (threadIdx.x == 0) s_next = turns.ask();
+        __syncthreads();
+        ticket = s_next;
+        __syncthreads();
+    }
+    if (ticket < turns.total) fetch(ticket, 0);
+    for (int stage = 0; ticket < turns.total; stage ^= 1) {
+        const Tile at(p, ticket, kWidth);
+        turns.now = ticket;
+        unsigned asked = 0;
+        if (threadIdx.x == 0) asked = turns.ask();
+        const int b = at.b, c = at.c0 + lane * kV, n = valid_tokens(p, b), tile = p.tiles - 1 - at.at;
+        const int t0 = tile * kTile + warp * kTok;
+        const bool live = c < p.C;
+        const int last = n > 0 ? (n - 1) / kTile : 0;
+        const int m = min(max(n - t0, 0), kTok);
+        const int64_t out = (static_cast<int64_t>(b) * p.T + t0) * p.C + c;
+        T *dx = static_cast<T *>(p.y) + out, *dg = static_cast<T *>(p.dg) + out;
+        const uint8_t *xs = mine + 2 * stage * kTile * kRow + lane * 4, *ds = xs + kTile * kRow, *gs = gates + lane * 4;
+        float e[kTok][kV], A[kV], H[kV], D[kV], h[kV];   // e: exp(gate)
+        {
+            const float *s = p.states + (static_cast<int64_t>(b) * p.tiles + tile) * p.C + c;
+#pragma unroll
+            for (int v = 0; v < kV; ++v) {
+                h[v] = live && n > 0 && tile <= last ? s[v] : 0.f;
+                A[v] = 1.f;
+                H[v] = D[v] = 0.f;
+            }
+        }
+        copies_wait();
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kTok; ++i)
+            if (i < m) {
+                P x, g, d;
+                x.load(reinterpret_cast<const T *>(xs + i * kRow));
+                g.load(reinterpret_cast<const T *>(gs + i * kRow));
+                d.load(reinterpret_cast<const T *>(ds + i * kRow));
+#pragma unroll
+                for (int v = 0; v < kV; ++v) {
+                    float a, w;
+                    e[i][v] = gate_exp<T, kLog>(g[v]);
+                    factors<T, kLog>(e[i][v], a, w);
+                    const float co = coefficient<kLog>(a, w);
+                    A[v] = shrink<kLog>(A[v], co);
+                    H[v] = advance<kLog>(H[v], x[v], co);
+                    D[v] = fmaf(A[v], d[v], D[v]);
+                }
+            }
+#pragma unroll
+        for (int v = 0; v < kV; ++v) {
+            maps[warp][v * 32 + lane] = make_float2(A[v], H[v]);
+            backs[warp][v * 32 + lane] = D[v];
+        }
+        if (threadIdx.x == 0) s_next = asked;
+        __syncthreads();
+        const unsigned next = s_next;
+        if (next < turns.total) fetch(next, stage ^ 1);
+        float sa[kV], sd[kV];   // the map of the tile's tokens after this warp's
+#pragma unroll
+        for (int v = 0; v < kV; ++v) sa[v] = 1.f, sd[v] = 0.f;
+        for (int w = kWarps - 1; w > warp; --w)
+#pragma unroll
+            for (int v = 0; v < kV; ++v) {
+                const float f = maps[w][v * 32 + lane].x;
+                sd[v] = fmaf(f, sd[v], backs[w][v * 32 + lane]);
+                sa[v] *= f;
+            }
+        if (warp == 0 && tile <= last) {
+            float in[kV];
+            uint2 word[kV];
+            uint2 *here = p.carry + (static_cast<int64_t>(b) * p.tiles + tile) * p.C + c;
+#pragma unroll
+            for (int v = 0; v < kV; ++v) {
+                D[v] = fmaf(A[v], sd[v], D[v]);
+                A[v] *= sa[v];
+            }
+            if (tile == last) {
+#pragma unroll
+                for (int v = 0; v < kV; ++v) in[v] = p.h0 && live ? p.h0[static_cast<int64_t>(b) * p.C + c + v] : 0.f;
+            } else {
+#pragma unroll
+                for (int v = 0; v < kV; ++v) word[v] = make_uint2(factor_bits(A[v]), __float_as_uint(D[v]));
+                if (live && tile > 0) tell<kV>(here, word);
+                if (!entering<kV>(here + p.C, p.C, last - tile, live, p.head, in)) {
+                    atomicOr(p.err, kErrTimeout);
+                    p.head->abort = 0u;
+                }
+            }
+#pragma unroll
+            for (int v = 0; v < kV; ++v) {
+                enter[v * 32 + lane] = in[v];
+                D[v] = fmaf(A[v], in[v], D[v]);
+                word[v] = make_uint2(kWhole, __float_as_uint(D[v]));
+            }
+            if (live && tile > 0) tell<kV>(here, word);
+            if (live && tile == 0 && p.h_T)
+#pragma unroll
+                for (int v = 0; v < kV; ++v) p.h_T[static_cast<int64_t>(b) * p.C + c + v] = D[v];
+        }
+        // the states before this warp's tokens, while the first one waits
+        for (int w = 0; w < warp; ++w)
+#pragma unroll
+            for (int v = 0; v < kV; ++v) {
+                const float2 f = maps[w][v * 32 + lane];
+                h[v] = fmaf(f.x, h[v], f.y);
+            }
+        float before[kTok][kV];
+#pragma unroll
+        for (int i = 0; i < kTok; ++i)
+            if (i < m) {
+                P x;
+                x.load(reinterpret_cast<const T *>(xs + i * kRow));
+#pragma unroll
+                for (int v = 0; v < kV; ++v) {
+                    float a, w;
+                    factors<T, kLog>(e[i][v], a, w);
+                    before[i][v] = kLog ? h[v] : h[v] - x[v];
+                    h[v] = advance<kLog>(h[v], x[v], coefficient<kLog>(a, w));
+                }
+            }
+        __syncthreads();
+        if (live) {
+#pragma unroll
+            for (int v = 0; v < kV; ++v) h[v] = fmaf(sa[v], enter[v * 32 + lane], sd[v]);   // now what reaches the state
+#pragma unroll
+            for (int i = kTok - 1; i >= 0; --i)
+                if (i < m) {
+                    P d;
+                    d.load(reinterpret_cast<const T *>(ds + i * kRow));
+                    float ox[kV], og[kV];
+#pragma unroll
+                    for (int v = 0; v < kV; ++v) {
+                        float a, w;
+                        factors<T, kLog>(e[i][v], a, w);
+                        const float dh = d[v] + h[v];
+                        h[v] = a * dh;
+                        ox[v] = w * dh;
+                        og[v] = w * before[i][v] * h[v];
+                    }
+                    P::store(dx + static_cast<int64_t>(i) * p.C, ox);
+                    P::store(dg + static_cast<int64_t>(i) * p.C, og);
+                } else if (t0 + i < p.T) {
+                    const float zero[kV] = {};
+                    P::store(dx + static_cast<int64_t>(i) * p.C, zero);
+                    P::store(dg + static_cast<int64_t>(i) * p.C, zero);
+                }
+        }
+        __syncwarp();
+        ticket = next;
+    }
+}
+
 template <typename T, bool kLog>
 __global__ void scan_step_kernel(const T *x, int64_t xs, const T *gate, int64_t gs, float *h, T *y, int C) {
     const int c = blockIdx.x * blockDim.x + threadIdx.x, b = blockIdx.y;
@@ -506,11 +869,11 @@ size_t carry_bytes(int B, int T, int C, int tile) {
     return tiles == 1 ? 0 : sizeof(Head) + (static_cast<size_t>(B) * tiles * C * sizeof(uint2) + 15) / 16 * 16;
 }
 
-// Whether neighbouring channels can be moved in pairs.
-bool in_pairs(const ScanArgs &p, size_t esz) {
+// Whether every row starts on `bytes` bytes and has a multiple of them.
+bool rows_fit(const ScanArgs &p, size_t esz, int bytes) {
     for (const void *a : {p.x, p.gate, p.dy, static_cast<const void *>(p.y), static_cast<const void *>(p.dg)})
-        if (!aligned(a, 2 * esz)) return false;
-    return p.C % 2 == 0 && (p.xb | p.xt | p.gb | p.gt | p.db | p.dt) % 2 == 0;
+        if (!aligned(a, bytes)) return false;
+    return (p.C | p.xb | p.xt | p.gb | p.gt | p.db | p.dt) % (bytes / static_cast<int>(esz)) == 0;
 }
 
 // Sets up the tiles of 32 kV channels and `tile` tokens, and what they tell each other.
@@ -523,18 +886,33 @@ cudaError_t lay_out(ScanArgs &p, int tile, int width, void *workspace, cudaStrea
     const cudaError_t e = device_error_word(&p.err);
     return e == cudaSuccess ? cudaMemsetAsync(workspace, 0xff, carry_bytes(p.B, p.T, p.C, tile), s) : e;
 }
-unsigned grid_of(const ScanArgs &p) { return static_cast<unsigned>(p.B) * p.blocks * p.tiles; }
+unsigned tiles_in_all(const ScanArgs &p) { return static_cast<unsigned>(p.B) * p.blocks * p.tiles; }
+
+// kBuffers of `tile` rows a CTA; as many CTAs as the SMs hold at once.
+template <int kBuffers, auto kKernel>
+cudaError_t run_ring(const ScanArgs &p, bool wide, int tile, int block, cudaStream_t s) {
+    constexpr int kMaxDevices = 64, kSms = 152;
+    static std::atomic<bool> done[kMaxDevices];
+    const int smem = kBuffers * tile * kRow;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (smem > 40 * 1024 && !done[dev].load(std::memory_order_acquire)) {   // once per device and kernel
+        if ((e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
+            return e;
+        done[dev].store(true, std::memory_order_release);
+    }
+    const unsigned most = 3 * kSms, tiles = tiles_in_all(p);
+    kKernel<<<tiles < most ? tiles : most, block, smem, s>>>(p, wide);
+    return cudaGetLastError();
+}
 
 template <typename F>
 cudaError_t by_type(kla_dtype dtype, kla_scan_mode mode, F f) {
-    if (dtype == KLA_DTYPE_BF16) {
-        if (mode == KLA_SCAN_LOG) f(__nv_bfloat16{}, std::true_type{});
-        else f(__nv_bfloat16{}, std::false_type{});
-    } else {
-        if (mode == KLA_SCAN_LOG) f(float{}, std::true_type{});
-        else f(float{}, std::false_type{});
-    }
-    return cudaGetLastError();
+    if (dtype == KLA_DTYPE_BF16)
+        return mode == KLA_SCAN_LOG ? f(__nv_bfloat16{}, std::true_type{}) : f(__nv_bfloat16{}, std::false_type{});
+    return mode == KLA_SCAN_LOG ? f(float{}, std::true_type{}) : f(float{}, std::false_type{});
 }
 
 }  // namespace
@@ -583,13 +961,16 @@ kla_status kla_gated_scan_fwd(const void *x, const void *gate, const int64_t *st
             if (overlaps(outs[i], outs[j])) return KLA_ERR_INVALID_ARG;
     }
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    const bool pairs = in_pairs(p, esz);
-    if (lay_out(p, kFwdTok * kFwdWarps, pairs ? 64 : 32, workspace, cs) != cudaSuccess) return KLA_ERR_CUDA;
+    const bool ring = rows_fit(p, esz, 4), wide = rows_fit(p, esz, 16);
+    if (lay_out(p, kFwdTok * kFwdWarps, ring ? kRow / static_cast<int>(esz) : 32, workspace, cs) != cudaSuccess)
+        return KLA_ERR_CUDA;
     const cudaError_t e = by_type(dtype, mode, [&](auto t, auto log) {
         using E = decltype(t);
         constexpr bool kLog = decltype(log)::value;
-        if (pairs) scan_fwd_kernel<E, kLog, 2, kFwdTok, kFwdWarps><<<grid_of(p), 32 * kFwdWarps, 0, cs>>>(p);
-        else scan_fwd_kernel<E, kLog, 1, kFwdTok, kFwdWarps><<<grid_of(p), 32 * kFwdWarps, 0, cs>>>(p);
+        if (ring) return run_ring<3, scan_fwd_ring_kernel<E, kLog, kFwdTok, kFwdWarps>>(p, wide, kFwdTok * kFwdWarps, 32 * kFwdWarps, cs);
+        if constexpr (sizeof(E) == 2)   // rows of odd bf16
+            scan_fwd_kernel<E, kLog, 1, kFwdTok, kFwdWarps><<<tiles_in_all(p), 32 * kFwdWarps, 0, cs>>>(p);
+        return cudaGetLastError();
     });
     return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
 }
@@ -630,13 +1011,16 @@ kla_status kla_gated_scan_bwd(const void *x, const void *gate, const void *dy, c
             if (overlaps(outs[i], outs[j])) return KLA_ERR_INVALID_ARG;
     }
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    const bool pairs = in_pairs(p, esz);
-    if (lay_out(p, kBwdTok * kBwdWarps, pairs ? 64 : 32, workspace, cs) != cudaSuccess) return KLA_ERR_CUDA;
+    const bool ring = rows_fit(p, esz, 4), wide = rows_fit(p, esz, 16);
+    if (lay_out(p, kBwdTok * kBwdWarps, ring ? kRow / static_cast<int>(esz) : 32, workspace, cs) != cudaSuccess)
+        return KLA_ERR_CUDA;
     const cudaError_t e = by_type(dtype, mode, [&](auto t, auto log) {
         using E = decltype(t);
         constexpr bool kLog = decltype(log)::value;
-        if (pairs) scan_bwd_kernel<E, kLog, 2, kBwdTok, kBwdWarps><<<grid_of(p), 32 * kBwdWarps, 0, cs>>>(p);
-        else scan_bwd_kernel<E, kLog, 1, kBwdTok, kBwdWarps><<<grid_of(p), 32 * kBwdWarps, 0, cs>>>(p);
+        if (ring) return run_ring<5, scan_bwd_ring_kernel<E, kLog, kBwdTok, kBwdWarps>>(p, wide, kBwdTok * kBwdWarps, 32 * kBwdWarps, cs);
+        if constexpr (sizeof(E) == 2)   // rows of odd bf16
+            scan_bwd_kernel<E, kLog, 1, kBwdTok, kBwdWarps><<<tiles_in_all(p), 32 * kBwdWarps, 0, cs>>>(p);
+        return cudaGetLastError();
     });
     return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
 }
@@ -658,6 +1042,7 @@ kla_status kla_gated_scan_step(const void *x, int64_t x_stride, const void *gate
         using E = decltype(t);
         scan_step_kernel<E, decltype(log)::value><<<dim3((C + 255) / 256, B), 256, 0, cs>>>(
             static_cast<const E *>(x), x_stride, static_cast<const E *>(gate), gate_stride, h, static_cast<E *>(y), C);
+        return cudaGetLastError();
     });
     return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
 }
