@@ -80,17 +80,6 @@ __device__ __forceinline__ float shrink(float A, float c) {
 // kV neighbouring values of type T in one access.
 template <typename T, int kV>
 struct Pack;
-template <>
-struct Pack<__nv_bfloat16, 2> {
-    uint32_t r;
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { r = *reinterpret_cast<const uint32_t *>(p); }
-    __device__ __forceinline__ float operator[](int i) const {
-        return __uint_as_float(i ? r & 0xffff0000u : r << 16);
-    }
-    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&v)[2]) {
-        *reinterpret_cast<uint32_t *>(p) = ptx::pack_bf16(v[0], v[1]);
-    }
-};
 template <typename T>
 struct Pack<T, 1> {
     T r;
@@ -112,6 +101,38 @@ __device__ __forceinline__ void tell(uint2 *p, const uint2 (&v)[kV]) {
                      "l"(static_cast<unsigned long long>(v[i].y) << 32 | v[i].x)
                      : "memory");
 }
+template <int kV>
+__device__ __forceinline__ void tell_map(uint2 *p, const float (&A)[kV], const float (&H)[kV]) {
+    uint2 w[kV];
+#pragma unroll
+    for (int v = 0; v < kV; ++v) w[v] = make_uint2(factor_bits(A[v]), __float_as_uint(H[v]));
+    tell<kV>(p, w);
+}
+template <int kV>
+__device__ __forceinline__ void tell_state(uint2 *p, const float (&h)[kV]) {
+    uint2 w[kV];
+#pragma unroll
+    for (int v = 0; v < kV; ++v) w[v] = make_uint2(kWhole, __float_as_uint(h[v]));
+    tell<kV>(p, w);
+}
+// The state at the chain's start (zeros where none is given), and at its end where that is wanted.
+template <int kV>
+__device__ __forceinline__ void start(const ScanArgs &p, int b, int c, bool live, float (&h)[kV]) {
+#pragma unroll
+    for (int v = 0; v < kV; ++v) h[v] = p.h0 && live ? p.h0[static_cast<int64_t>(b) * p.C + c + v] : 0.f;
+}
+template <int kV>
+__device__ __forceinline__ void finish(const ScanArgs &p, int b, int c, const float (&h)[kV]) {
+    if (p.h_T)
+#pragma unroll
+        for (int v = 0; v < kV; ++v) p.h_T[static_cast<int64_t>(b) * p.C + c + v] = h[v];
+}
+__device__ __forceinline__ void give_up(const ScanArgs &p) {
+    if ((threadIdx.x & 31) == 0) {
+        atomicOr(p.err, kErrTimeout);
+        *const_cast<volatile unsigned *>(&p.head->abort) = 0u;
+    }
+}
 __device__ __forceinline__ uint2 hear(const uint2 *p) {
     unsigned long long v;
     asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
@@ -127,7 +148,7 @@ __device__ __forceinline__ uint2 hear(const uint2 *p) {
 template <int kV>
 __device__ __forceinline__ bool entering(const uint2 *p, int64_t hop, int left, bool live, const Head *head,
                                          float (&h)[kV]) {
-    constexpr int kAhead = 8;
+    constexpr int kAhead = 4;
     constexpr unsigned kLimit = 1u << 21;
 #pragma unroll
     for (int v = 0; v < kV; ++v) h[v] = 0.f;
@@ -192,7 +213,7 @@ template <typename T, bool kLog, int kV, int kTok, int kWarps>
 __global__ void __launch_bounds__(32 * kWarps) scan_fwd_kernel(ScanArgs p) {
     constexpr int kTile = kTok * kWarps;
     __shared__ float2 maps[kWarps][32 * kV];
-    __shared__ float enter[32 * kV];
+    __shared__ float enter[kV][32];
     const Tile at(p, take_ticket(p), 32 * kV);
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int b = at.b, c = at.c0 + lane * kV, n = valid_tokens(p, b);
@@ -248,43 +269,30 @@ __global__ void __launch_bounds__(32 * kWarps) scan_fwd_kernel(ScanArgs p) {
             ph[v] = fmaf(f.x, ph[v], f.y);
             pa[v] *= f.x;
         }
+    float in[kV];
     if (warp == kWarps - 1) {
-        float in[kV];
-        uint2 word[kV];
         uint2 *here = p.carry + (static_cast<int64_t>(b) * p.tiles + at.at) * p.C + c;
 #pragma unroll
         for (int v = 0; v < kV; ++v) {
             H[v] = fmaf(A[v], ph[v], H[v]);
             A[v] *= pa[v];
         }
-        if (at.at == 0) {
-#pragma unroll
-            for (int v = 0; v < kV; ++v) in[v] = p.h0 && live ? p.h0[static_cast<int64_t>(b) * p.C + c + v] : 0.f;
-        } else {
-#pragma unroll
-            for (int v = 0; v < kV; ++v) word[v] = make_uint2(factor_bits(A[v]), __float_as_uint(H[v]));
-            if (live && at.at < last) tell<kV>(here, word);
-            if (!entering<kV>(here - p.C, -static_cast<int64_t>(p.C), at.at, live, p.head, in)) {
-                atomicOr(p.err, kErrTimeout);
-                p.head->abort = 0u;
-            }
-        }
+        if (at.at > 0 && at.at < last && live) tell_map<kV>(here, A, H);
+        if (at.at == 0) start<kV>(p, b, c, live, in);
+        else if (!entering<kV>(here - p.C, -static_cast<int64_t>(p.C), at.at, live, p.head, in)) give_up(p);
 #pragma unroll
         for (int v = 0; v < kV; ++v) {
-            enter[v * 32 + lane] = in[v];
+            enter[v][lane] = in[v];
             H[v] = fmaf(A[v], in[v], H[v]);
-            word[v] = make_uint2(kWhole, __float_as_uint(H[v]));
         }
-        if (live && at.at < last) tell<kV>(here, word);
-        if (live && at.at == last && p.h_T)
-#pragma unroll
-            for (int v = 0; v < kV; ++v) p.h_T[static_cast<int64_t>(b) * p.C + c + v] = H[v];
+        if (live && at.at < last) tell_state<kV>(here, H);
+        else if (live) finish<kV>(p, b, c, H);
     }
     __syncthreads();
     if (!live) return;
     float h[kV];
 #pragma unroll
-    for (int v = 0; v < kV; ++v) h[v] = fmaf(pa[v], enter[v * 32 + lane], ph[v]);
+    for (int v = 0; v < kV; ++v) h[v] = fmaf(pa[v], enter[v][lane], ph[v]);
     if (p.states && m > 0 && t0 % KLA_SCAN_SPAN == 0) {
         const int64_t spans = (p.T + KLA_SCAN_SPAN - 1) / KLA_SCAN_SPAN;
         float *s = p.states + (b * spans + t0 / KLA_SCAN_SPAN) * p.C + c;
@@ -311,7 +319,7 @@ __global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(ScanArgs p) {
     constexpr int kTile = kTok * kWarps;
     static_assert(kTile == KLA_SCAN_SPAN, "");
     __shared__ float2 maps[kWarps][32 * kV];
-    __shared__ float backs[kWarps][32 * kV], enter[32 * kV];
+    __shared__ float backs[kWarps][32 * kV], enter[kV][32];
     const Tile at(p, take_ticket(p), 32 * kV);
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int b = at.b, c = at.c0 + lane * kV, n = valid_tokens(p, b), tile = p.tiles - 1 - at.at;
@@ -386,37 +394,24 @@ __global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(ScanArgs p) {
         }
     if (warp == 0) {
         float in[kV];
-        uint2 word[kV];
         uint2 *here = p.carry + (static_cast<int64_t>(b) * p.tiles + tile) * p.C + c;
 #pragma unroll
         for (int v = 0; v < kV; ++v) {
             D[v] = fmaf(A[v], sd[v], D[v]);
             A[v] *= sa[v];
         }
-        if (tile == last) {
-#pragma unroll
-            for (int v = 0; v < kV; ++v) in[v] = p.h0 && live ? p.h0[static_cast<int64_t>(b) * p.C + c + v] : 0.f;
-        } else {
-#pragma unroll
-            for (int v = 0; v < kV; ++v) word[v] = make_uint2(factor_bits(A[v]), __float_as_uint(D[v]));
-            if (live && tile > 0) tell<kV>(here, word);
-            if (!entering<kV>(here + p.C, p.C, last - tile, live, p.head, in)) {
-                atomicOr(p.err, kErrTimeout);
-                p.head->abort = 0u;
-            }
-        }
+        if (tile > 0 && tile < last && live) tell_map<kV>(here, A, D);
+        if (tile == last) start<kV>(p, b, c, live, in);
+        else if (!entering<kV>(here + p.C, p.C, last - tile, live, p.head, in)) give_up(p);
 #pragma unroll
         for (int v = 0; v < kV; ++v) {
-            enter[v * 32 + lane] = in[v];
+            enter[v][lane] = in[v];
             D[v] = fmaf(A[v], in[v], D[v]);
-            word[v] = make_uint2(kWhole, __float_as_uint(D[v]));
         }
-        if (live && tile > 0) tell<kV>(here, word);
-        if (live && tile == 0 && p.h_T)
-#pragma unroll
-            for (int v = 0; v < kV; ++v) p.h_T[static_cast<int64_t>(b) * p.C + c + v] = D[v];
+        if (live && tile > 0) tell_state<kV>(here, D);
+        else if (live) finish<kV>(p, b, c, D);
     }
-    // the states before this warp's tokens, while the first one waits
+    // the states before this warp's tokens
     for (int w = 0; w < warp; ++w)
 #pragma unroll
         for (int v = 0; v < kV; ++v) {
@@ -438,7 +433,7 @@ __global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(ScanArgs p) {
     __syncthreads();
     if (!live) return;
 #pragma unroll
-    for (int v = 0; v < kV; ++v) h[v] = fmaf(sa[v], enter[v * 32 + lane], sd[v]);   // now what reaches the state
+    for (int v = 0; v < kV; ++v) h[v] = fmaf(sa[v], enter[v][lane], sd[v]);   // now what reaches the state
 #pragma unroll
     for (int i = kTok - 1; i >= 0; --i)
         if (i < m) {
@@ -460,13 +455,83 @@ __global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(ScanArgs p) {
         }
 }
 
+// Tokens of a thread, warps of a CTA and CTAs of an SM.
+constexpr int kFwdTok = 32, kFwdWarps = 8, kFwdCtas = 2, kBwdTok = 16, kBwdWarps = 4, kBwdCtas = 4;
+
 // ---- tiles through shared memory: rows of 128 bytes (64 channels of bf16, 32 of fp32), 4 bytes a lane
 constexpr int kRow = 128;
-template <typename T>
-struct Lane {   // the channels of a lane
-    static constexpr int kV = 4 / sizeof(T);
-    using P = Pack<T, kV>;
+// What a lane has of a row: two channels of bf16, whose arithmetic is paired, or one of fp32. A gate is kept as one
+// number: bf16: w, or a where KLA_SCAN_LOG, with h = a h + w x and a = 1 - w, whose rounding of 2^-25 is that of a
+// itself where it is near 1 (and whose exponential and reciprocal are the hardware's, off by 2^-21 at gates of 10, far
+// below the gate's own 2^-9). fp32: the coefficient of above in the forward pass; exp(gate) in the backward pass, from
+// which both factors come to their last bits.
+template <typename T, bool kLog, bool kBwd>
+struct Lane;
+template <bool kLog, bool kBwd>
+struct Lane<__nv_bfloat16, kLog, kBwd> {
+    static constexpr int kV = 2;
+    using V = float2;
+    static __device__ __forceinline__ V load(const uint8_t *p) {
+        const uint32_t r = *reinterpret_cast<const uint32_t *>(p);
+        return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16 *p, V v) {
+        *reinterpret_cast<uint32_t *>(p) = ptx::pack_bf16(v.x, v.y);
+    }
+    static __device__ __forceinline__ V all(float x) { return both(x); }
+    static __device__ __forceinline__ V fma(V a, V b, V c) { return fma2(a, b, c); }
+    static __device__ __forceinline__ V mul(V a, V b) { return mul2(a, b); }
+    static __device__ __forceinline__ V add(V a, V b) { return add2(a, b); }
+    static __device__ __forceinline__ V keep(V gate) {
+        V e = mul2(gate, both(1.4426950408889634f));
+        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+        if (kLog) return e;
+        e = add2(e, both(1.f));
+        asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+        asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+        return e;
+    }
+    static __device__ __forceinline__ V a(V k) { return kLog ? k : fma2(k, both(-1.f), both(1.f)); }
+    static __device__ __forceinline__ V w(V k) { return kLog ? both(1.f) : k; }
+    // h, a token on; prod a, a token on
+    static __device__ __forceinline__ V advance(V h, V x, V k) { return fma2(a(k), h, kLog ? x : mul2(k, x)); }
+    static __device__ __forceinline__ V shrink(V A, V k) { return mul2(A, a(k)); }
 };
+template <bool kLog, bool kBwd>
+struct Lane<float, kLog, kBwd> {
+    static constexpr int kV = 1;
+    using V = float;
+    static __device__ __forceinline__ V load(const uint8_t *p) { return *reinterpret_cast<const float *>(p); }
+    static __device__ __forceinline__ void store(float *p, V v) { *p = v; }
+    static __device__ __forceinline__ V all(float x) { return x; }
+    static __device__ __forceinline__ V fma(V a, V b, V c) { return fmaf(a, b, c); }
+    static __device__ __forceinline__ V mul(V a, V b) { return a * b; }
+    static __device__ __forceinline__ V add(V a, V b) { return a + b; }
+    static __device__ __forceinline__ V keep(V gate) {
+        const float e = gate_exp<float, kLog>(gate);
+        return kBwd ? e : coefficient<kLog>(a(e), w(e));
+    }
+    static __device__ __forceinline__ V a(V e) { return kLog ? e : e * w(e); }
+    static __device__ __forceinline__ V w(V e) { return kLog ? 1.f : __frcp_rn(1.f + e); }
+    static __device__ __forceinline__ V advance(V h, V x, V k) {
+        return kla::advance<kLog>(h, x, kBwd ? coefficient<kLog>(a(k), w(k)) : k);
+    }
+    static __device__ __forceinline__ V shrink(V A, V k) {
+        return kla::shrink<kLog>(A, kBwd ? coefficient<kLog>(a(k), w(k)) : k);
+    }
+};
+__device__ __forceinline__ float part(float v, int) { return v; }
+__device__ __forceinline__ float part(float2 v, int i) { return i ? v.y : v.x; }
+using One = float[1];
+using Two = float[2];
+__device__ __forceinline__ const One &parts(const float &v) { return reinterpret_cast<const One &>(v); }
+__device__ __forceinline__ const Two &parts(const float2 &v) { return reinterpret_cast<const Two &>(v); }
+template <int kV>
+__device__ __forceinline__ auto whole(const float (&v)[kV]) {
+    if constexpr (kV == 1) return v[0];
+    else return make_float2(v[0], v[1]);
+}
 __device__ __forceinline__ void copy16(uint32_t to, const void *from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
@@ -510,13 +575,22 @@ struct Turns {
     }
 };
 
+// Runs f with whether all of a warp's kTok tokens are valid: the loops over them have no conditions then.
+template <typename F>
+__device__ __forceinline__ void by_full(bool full, F f) {
+    if (full) f(std::true_type{});
+    else f(std::false_type{});
+}
+
+// As above, with tiles one after the other: while a CTA waits for the state that enters one and writes its outputs, the
+// next one's rows are on their way.
 template <typename T, bool kLog, int kTok, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps, 3) scan_fwd_ring_kernel(ScanArgs p, bool wide) {
-    constexpr int kTile = kTok * kWarps, kV = Lane<T>::kV, kWidth = 32 * kV;
-    using P = typename Lane<T>::P;
+__global__ void __launch_bounds__(32 * kWarps, kFwdCtas) scan_fwd_ring_kernel(ScanArgs p, bool wide) {
+    using L = Lane<T, kLog, false>;
+    using V = typename L::V;
+    constexpr int kTile = kTok * kWarps, kV = L::kV, kWidth = 32 * kV;
     extern __shared__ __align__(128) uint8_t buf[];   // x twice, gate once: kTile rows each
-    __shared__ float2 maps[kWarps][kWidth];
-    __shared__ float enter[kWidth];
+    __shared__ V map_a[kWarps][32], map_h[kWarps][32], enter[32];
     __shared__ unsigned s_next;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     uint8_t *const mine = buf + warp * kTok * kRow;
@@ -544,105 +618,72 @@ __global__ void __launch_bounds__(32 * kWarps, 3) scan_fwd_ring_kernel(ScanArgs 
         const Tile at(p, ticket, kWidth);
         turns.now = ticket;
         unsigned asked = 0;
-        if (threadIdx.x == 0) asked = turns.ask();
         const int b = at.b, c = at.c0 + lane * kV, n = valid_tokens(p, b), t0 = at.at * kTile + warp * kTok;
         const bool live = c < p.C;
         const int last = n > 0 ? (n - 1) / kTile : 0;
         const int m = min(max(n - t0, 0), kTok);   // of this warp's tokens, how many are valid
-        T *y = static_cast<T *>(p.y) + (static_cast<int64_t>(b) * p.T + t0) * p.C + c;
         const uint8_t *xs = mine + stage * kTile * kRow + lane * 4, *gs = gates + lane * 4;
-        float co[kTok][kV], A[kV], H[kV];
-#pragma unroll
-        for (int v = 0; v < kV; ++v) A[v] = 1.f, H[v] = 0.f;
+        V k[kTok], A = L::all(1.f), H = L::all(0.f);
         copies_wait();
         __syncwarp();
+        if (threadIdx.x == 0) asked = turns.ask();
+        by_full(m == kTok, [&](auto full) {
 #pragma unroll
-        for (int i = 0; i < kTok; ++i)
-            if (i < m) {
-                P x, g;
-                x.load(reinterpret_cast<const T *>(xs + i * kRow));
-                g.load(reinterpret_cast<const T *>(gs + i * kRow));
-#pragma unroll
-                for (int v = 0; v < kV; ++v) {
-                    float a, w;
-                    factors<T, kLog>(gate_exp<T, kLog>(g[v]), a, w);
-                    co[i][v] = coefficient<kLog>(a, w);
-                    A[v] = shrink<kLog>(A[v], co[i][v]);
-                    H[v] = advance<kLog>(H[v], x[v], co[i][v]);
+            for (int i = 0; i < kTok; ++i)
+                if (full || i < m) {
+                    k[i] = L::keep(L::load(gs + i * kRow));
+                    A = L::shrink(A, k[i]);
+                    H = L::advance(H, L::load(xs + i * kRow), k[i]);
                 }
-            }
-#pragma unroll
-        for (int v = 0; v < kV; ++v) maps[warp][v * 32 + lane] = make_float2(A[v], H[v]);
+        });
+        map_a[warp][lane] = A;
+        map_h[warp][lane] = H;
         if (threadIdx.x == 0) s_next = asked;
         __syncthreads();
         const unsigned next = s_next;
-        if (next < turns.total) fetch(next, stage ^ 1);
         // the map of the tile's tokens before this warp's
-        float pa[kV], ph[kV];
-#pragma unroll
-        for (int v = 0; v < kV; ++v) pa[v] = 1.f, ph[v] = 0.f;
-        for (int w = 0; w < warp; ++w)
-#pragma unroll
-            for (int v = 0; v < kV; ++v) {
-                const float2 f = maps[w][v * 32 + lane];
-                ph[v] = fmaf(f.x, ph[v], f.y);
-                pa[v] *= f.x;
-            }
-        if (warp == kWarps - 1 && at.at <= last) {
+        V pa = L::all(1.f), ph = L::all(0.f);
+        for (int w = 0; w < warp; ++w) {
+            ph = L::fma(map_a[w][lane], ph, map_h[w][lane]);
+            pa = L::mul(pa, map_a[w][lane]);
+        }
+        const bool teller = warp == kWarps - 1 && at.at <= last;
+        uint2 *here = p.carry + (static_cast<int64_t>(b) * p.tiles + at.at) * p.C + c;
+        if (teller) {
+            H = L::fma(A, ph, H);
+            A = L::mul(A, pa);
+            if (at.at > 0 && at.at < last && live) tell_map<kV>(here, parts(A), parts(H));
+        }
+        if (next < turns.total) fetch(next, stage ^ 1);
+        if (teller) {
             float in[kV];
-            uint2 word[kV];
-            uint2 *here = p.carry + (static_cast<int64_t>(b) * p.tiles + at.at) * p.C + c;
-#pragma unroll
-            for (int v = 0; v < kV; ++v) {
-                H[v] = fmaf(A[v], ph[v], H[v]);
-                A[v] *= pa[v];
-            }
-            if (at.at == 0) {
-#pragma unroll
-                for (int v = 0; v < kV; ++v) in[v] = p.h0 && live ? p.h0[static_cast<int64_t>(b) * p.C + c + v] : 0.f;
-            } else {
-#pragma unroll
-                for (int v = 0; v < kV; ++v) word[v] = make_uint2(factor_bits(A[v]), __float_as_uint(H[v]));
-                if (live && at.at < last) tell<kV>(here, word);
-                if (!entering<kV>(here - p.C, -static_cast<int64_t>(p.C), at.at, live, p.head, in)) {
-                    atomicOr(p.err, kErrTimeout);
-                    p.head->abort = 0u;
-                }
-            }
-#pragma unroll
-            for (int v = 0; v < kV; ++v) {
-                enter[v * 32 + lane] = in[v];
-                H[v] = fmaf(A[v], in[v], H[v]);
-                word[v] = make_uint2(kWhole, __float_as_uint(H[v]));
-            }
-            if (live && at.at < last) tell<kV>(here, word);
-            if (live && at.at == last && p.h_T)
-#pragma unroll
-                for (int v = 0; v < kV; ++v) p.h_T[static_cast<int64_t>(b) * p.C + c + v] = H[v];
+            if (at.at == 0) start<kV>(p, b, c, live, in);
+            else if (!entering<kV>(here - p.C, -static_cast<int64_t>(p.C), at.at, live, p.head, in)) give_up(p);
+            enter[lane] = whole<kV>(in);
+            H = L::fma(A, enter[lane], H);
+            if (live && at.at < last) tell_state<kV>(here, parts(H));
+            else if (live) finish<kV>(p, b, c, parts(H));
         }
         __syncthreads();
         if (live) {
-            float h[kV];
-#pragma unroll
-            for (int v = 0; v < kV; ++v) h[v] = fmaf(pa[v], enter[v * 32 + lane], ph[v]);
+            V h = L::fma(pa, enter[lane], ph);
             if (p.states && m > 0 && t0 % KLA_SCAN_SPAN == 0) {
                 const int64_t spans = (p.T + KLA_SCAN_SPAN - 1) / KLA_SCAN_SPAN;
                 float *s = p.states + (b * spans + t0 / KLA_SCAN_SPAN) * p.C + c;
 #pragma unroll
-                for (int v = 0; v < kV; ++v) s[v] = h[v];
+                for (int v = 0; v < kV; ++v) s[v] = part(h, v);
             }
+            T *y = static_cast<T *>(p.y) + (static_cast<int64_t>(b) * p.T + t0) * p.C + c;
+            by_full(m == kTok, [&](auto full) {
 #pragma unroll
-            for (int i = 0; i < kTok; ++i)
-                if (i < m) {
-                    P x;
-                    x.load(reinterpret_cast<const T *>(xs + i * kRow));
-#pragma unroll
-                    for (int v = 0; v < kV; ++v) h[v] = advance<kLog>(h[v], x[v], co[i][v]);
-                    P::store(y + static_cast<int64_t>(i) * p.C, h);
-                } else if (t0 + i < p.T) {
-                    const float zero[kV] = {};
-                    P::store(y + static_cast<int64_t>(i) * p.C, zero);
-                }
+                for (int i = 0; i < kTok; ++i, y += p.C)
+                    if (full || i < m) {
+                        h = L::advance(h, L::load(xs + i * kRow), k[i]);
+                        L::store(y, h);
+                    } else if (t0 + i < p.T) {
+                        L::store(y, L::all(0.f));
+                    }
+            });
         }
         __syncwarp();
         ticket = next;
@@ -650,13 +691,13 @@ __global__ void __launch_bounds__(32 * kWarps, 3) scan_fwd_ring_kernel(ScanArgs 
 }
 
 template <typename T, bool kLog, int kTok, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps, 3) scan_bwd_ring_kernel(ScanArgs p, bool wide) {
-    constexpr int kTile = kTok * kWarps, kV = Lane<T>::kV, kWidth = 32 * kV;
-    using P = typename Lane<T>::P;
+__global__ void __launch_bounds__(32 * kWarps, kBwdCtas) scan_bwd_ring_kernel(ScanArgs p, bool wide) {
+    using L = Lane<T, kLog, true>;
+    using V = typename L::V;
+    constexpr int kTile = kTok * kWarps, kV = L::kV, kWidth = 32 * kV;
     static_assert(kTile == KLA_SCAN_SPAN, "");
     extern __shared__ __align__(128) uint8_t buf[];   // x and dy twice, gate once: kTile rows each
-    __shared__ float2 maps[kWarps][kWidth];
-    __shared__ float backs[kWarps][kWidth], enter[kWidth];
+    __shared__ V map_a[kWarps][32], map_h[kWarps][32], map_d[kWarps][32], enter[32];
     __shared__ unsigned s_next;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     uint8_t *const mine = buf + warp * kTok * kRow;
@@ -687,143 +728,92 @@ __global__ void __launch_bounds__(32 * kWarps, 3) scan_bwd_ring_kernel(ScanArgs 
         const Tile at(p, ticket, kWidth);
         turns.now = ticket;
         unsigned asked = 0;
-        if (threadIdx.x == 0) asked = turns.ask();
         const int b = at.b, c = at.c0 + lane * kV, n = valid_tokens(p, b), tile = p.tiles - 1 - at.at;
         const int t0 = tile * kTile + warp * kTok;
         const bool live = c < p.C;
         const int last = n > 0 ? (n - 1) / kTile : 0;
         const int m = min(max(n - t0, 0), kTok);
-        const int64_t out = (static_cast<int64_t>(b) * p.T + t0) * p.C + c;
-        T *dx = static_cast<T *>(p.y) + out, *dg = static_cast<T *>(p.dg) + out;
         const uint8_t *xs = mine + 2 * stage * kTile * kRow + lane * 4, *ds = xs + kTile * kRow, *gs = gates + lane * 4;
-        float e[kTok][kV], A[kV], H[kV], D[kV], h[kV];   // e: exp(gate)
+        V k[kTok], A = L::all(1.f), H = L::all(0.f), D = H, h;
         {
             const float *s = p.states + (static_cast<int64_t>(b) * p.tiles + tile) * p.C + c;
+            float in[kV];
 #pragma unroll
-            for (int v = 0; v < kV; ++v) {
-                h[v] = live && n > 0 && tile <= last ? s[v] : 0.f;
-                A[v] = 1.f;
-                H[v] = D[v] = 0.f;
-            }
+            for (int v = 0; v < kV; ++v) in[v] = live && n > 0 && tile <= last ? s[v] : 0.f;
+            h = whole<kV>(in);
         }
         copies_wait();
         __syncwarp();
+        if (threadIdx.x == 0) asked = turns.ask();
+        by_full(m == kTok, [&](auto full) {
 #pragma unroll
-        for (int i = 0; i < kTok; ++i)
-            if (i < m) {
-                P x, g, d;
-                x.load(reinterpret_cast<const T *>(xs + i * kRow));
-                g.load(reinterpret_cast<const T *>(gs + i * kRow));
-                d.load(reinterpret_cast<const T *>(ds + i * kRow));
-#pragma unroll
-                for (int v = 0; v < kV; ++v) {
-                    float a, w;
-                    e[i][v] = gate_exp<T, kLog>(g[v]);
-                    factors<T, kLog>(e[i][v], a, w);
-                    const float co = coefficient<kLog>(a, w);
-                    A[v] = shrink<kLog>(A[v], co);
-                    H[v] = advance<kLog>(H[v], x[v], co);
-                    D[v] = fmaf(A[v], d[v], D[v]);
+            for (int i = 0; i < kTok; ++i)
+                if (full || i < m) {
+                    k[i] = L::keep(L::load(gs + i * kRow));
+                    A = L::shrink(A, k[i]);
+                    H = L::advance(H, L::load(xs + i * kRow), k[i]);
+                    D = L::fma(A, L::load(ds + i * kRow), D);
                 }
-            }
-#pragma unroll
-        for (int v = 0; v < kV; ++v) {
-            maps[warp][v * 32 + lane] = make_float2(A[v], H[v]);
-            backs[warp][v * 32 + lane] = D[v];
-        }
+        });
+        map_a[warp][lane] = A;
+        map_h[warp][lane] = H;
+        map_d[warp][lane] = D;
         if (threadIdx.x == 0) s_next = asked;
         __syncthreads();
         const unsigned next = s_next;
-        if (next < turns.total) fetch(next, stage ^ 1);
-        float sa[kV], sd[kV];   // the map of the tile's tokens after this warp's
-#pragma unroll
-        for (int v = 0; v < kV; ++v) sa[v] = 1.f, sd[v] = 0.f;
-        for (int w = kWarps - 1; w > warp; --w)
-#pragma unroll
-            for (int v = 0; v < kV; ++v) {
-                const float f = maps[w][v * 32 + lane].x;
-                sd[v] = fmaf(f, sd[v], backs[w][v * 32 + lane]);
-                sa[v] *= f;
-            }
-        if (warp == 0 && tile <= last) {
-            float in[kV];
-            uint2 word[kV];
-            uint2 *here = p.carry + (static_cast<int64_t>(b) * p.tiles + tile) * p.C + c;
-#pragma unroll
-            for (int v = 0; v < kV; ++v) {
-                D[v] = fmaf(A[v], sd[v], D[v]);
-                A[v] *= sa[v];
-            }
-            if (tile == last) {
-#pragma unroll
-                for (int v = 0; v < kV; ++v) in[v] = p.h0 && live ? p.h0[static_cast<int64_t>(b) * p.C + c + v] : 0.f;
-            } else {
-#pragma unroll
-                for (int v = 0; v < kV; ++v) word[v] = make_uint2(factor_bits(A[v]), __float_as_uint(D[v]));
-                if (live && tile > 0) tell<kV>(here, word);
-                if (!entering<kV>(here + p.C, p.C, last - tile, live, p.head, in)) {
-                    atomicOr(p.err, kErrTimeout);
-                    p.head->abort = 0u;
-                }
-            }
-#pragma unroll
-            for (int v = 0; v < kV; ++v) {
-                enter[v * 32 + lane] = in[v];
-                D[v] = fmaf(A[v], in[v], D[v]);
-                word[v] = make_uint2(kWhole, __float_as_uint(D[v]));
-            }
-            if (live && tile > 0) tell<kV>(here, word);
-            if (live && tile == 0 && p.h_T)
-#pragma unroll
-                for (int v = 0; v < kV; ++v) p.h_T[static_cast<int64_t>(b) * p.C + c + v] = D[v];
+        V sa = L::all(1.f), sd = L::all(0.f);   // the map of the tile's tokens after this warp's
+        for (int w = kWarps - 1; w > warp; --w) {
+            sd = L::fma(map_a[w][lane], sd, map_d[w][lane]);
+            sa = L::mul(sa, map_a[w][lane]);
         }
-        // the states before this warp's tokens, while the first one waits
-        for (int w = 0; w < warp; ++w)
+        const bool teller = warp == 0 && tile <= last;
+        uint2 *here = p.carry + (static_cast<int64_t>(b) * p.tiles + tile) * p.C + c;
+        if (teller) {
+            D = L::fma(A, sd, D);
+            A = L::mul(A, sa);
+            if (tile > 0 && tile < last && live) tell_map<kV>(here, parts(A), parts(D));
+        }
+        if (next < turns.total) fetch(next, stage ^ 1);
+        if (teller) {
+            float in[kV];
+            if (tile == last) start<kV>(p, b, c, live, in);
+            else if (!entering<kV>(here + p.C, p.C, last - tile, live, p.head, in)) give_up(p);
+            enter[lane] = whole<kV>(in);
+            D = L::fma(A, enter[lane], D);
+            if (live && tile > 0) tell_state<kV>(here, parts(D));
+            else if (live) finish<kV>(p, b, c, parts(D));
+        }
+        // the states before this warp's tokens
+        for (int w = 0; w < warp; ++w) h = L::fma(map_a[w][lane], h, map_h[w][lane]);
+        V lead[kTok];   // h_{t-1}, of which the sigmoid's gradient takes x_t
+        by_full(m == kTok, [&](auto full) {
 #pragma unroll
-            for (int v = 0; v < kV; ++v) {
-                const float2 f = maps[w][v * 32 + lane];
-                h[v] = fmaf(f.x, h[v], f.y);
-            }
-        float before[kTok][kV];
-#pragma unroll
-        for (int i = 0; i < kTok; ++i)
-            if (i < m) {
-                P x;
-                x.load(reinterpret_cast<const T *>(xs + i * kRow));
-#pragma unroll
-                for (int v = 0; v < kV; ++v) {
-                    float a, w;
-                    factors<T, kLog>(e[i][v], a, w);
-                    before[i][v] = kLog ? h[v] : h[v] - x[v];
-                    h[v] = advance<kLog>(h[v], x[v], coefficient<kLog>(a, w));
+            for (int i = 0; i < kTok; ++i)
+                if (full || i < m) {
+                    const V x = L::load(xs + i * kRow);
+                    lead[i] = kLog ? h : L::fma(x, L::all(-1.f), h);
+                    h = L::advance(h, x, k[i]);
                 }
-            }
+        });
         __syncthreads();
         if (live) {
+            V e = L::fma(sa, enter[lane], sd);   // what reaches the state behind the token
+            const int64_t out = (static_cast<int64_t>(b) * p.T + t0) * p.C + c;
+            T *dx = static_cast<T *>(p.y) + out + (kTok - 1) * static_cast<int64_t>(p.C);
+            T *dg = static_cast<T *>(p.dg) + out + (kTok - 1) * static_cast<int64_t>(p.C);
+            by_full(m == kTok, [&](auto full) {
 #pragma unroll
-            for (int v = 0; v < kV; ++v) h[v] = fmaf(sa[v], enter[v * 32 + lane], sd[v]);   // now what reaches the state
-#pragma unroll
-            for (int i = kTok - 1; i >= 0; --i)
-                if (i < m) {
-                    P d;
-                    d.load(reinterpret_cast<const T *>(ds + i * kRow));
-                    float ox[kV], og[kV];
-#pragma unroll
-                    for (int v = 0; v < kV; ++v) {
-                        float a, w;
-                        factors<T, kLog>(e[i][v], a, w);
-                        const float dh = d[v] + h[v];
-                        h[v] = a * dh;
-                        ox[v] = w * dh;
-                        og[v] = w * before[i][v] * h[v];
+                for (int i = kTok - 1; i >= 0; --i, dx -= p.C, dg -= p.C)
+                    if (full || i < m) {
+                        const V dh = L::add(L::load(ds + i * kRow), e), w = L::w(k[i]);
+                        e = L::mul(L::a(k[i]), dh);
+                        L::store(dx, kLog ? dh : L::mul(w, dh));
+                        L::store(dg, L::mul(kLog ? lead[i] : L::mul(w, lead[i]), e));
+                    } else if (t0 + i < p.T) {
+                        L::store(dx, L::all(0.f));
+                        L::store(dg, L::all(0.f));
                     }
-                    P::store(dx + static_cast<int64_t>(i) * p.C, ox);
-                    P::store(dg + static_cast<int64_t>(i) * p.C, og);
-                } else if (t0 + i < p.T) {
-                    const float zero[kV] = {};
-                    P::store(dx + static_cast<int64_t>(i) * p.C, zero);
-                    P::store(dg + static_cast<int64_t>(i) * p.C, zero);
-                }
+            });
         }
         __syncwarp();
         ticket = next;
@@ -842,8 +832,6 @@ __global__ void scan_step_kernel(const T *x, int64_t xs, const T *gate, int64_t 
     y[at] = from_f32<T>(v);
 }
 
-// Tokens of a thread and warps of a CTA: the forward pass holds two values a token and channel, the backward five.
-constexpr int kFwdTok = 16, kFwdWarps = 8, kBwdTok = 8, kBwdWarps = 8;
 static_assert(kFwdTok * kFwdWarps % KLA_SCAN_SPAN == 0 && KLA_SCAN_SPAN % kFwdTok == 0, "");
 
 int tiles_of(int T, int tile) { return T > tile ? (T + tile - 1) / tile : 1; }
@@ -889,7 +877,7 @@ cudaError_t lay_out(ScanArgs &p, int tile, int width, void *workspace, cudaStrea
 unsigned tiles_in_all(const ScanArgs &p) { return static_cast<unsigned>(p.B) * p.blocks * p.tiles; }
 
 // kBuffers of `tile` rows a CTA; as many CTAs as the SMs hold at once.
-template <int kBuffers, auto kKernel>
+template <int kBuffers, int kCtas, auto kKernel>
 cudaError_t run_ring(const ScanArgs &p, bool wide, int tile, int block, cudaStream_t s) {
     constexpr int kMaxDevices = 64, kSms = 152;
     static std::atomic<bool> done[kMaxDevices];
@@ -898,12 +886,12 @@ cudaError_t run_ring(const ScanArgs &p, bool wide, int tile, int block, cudaStre
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    if (smem > 40 * 1024 && !done[dev].load(std::memory_order_acquire)) {   // once per device and kernel
+    if (!done[dev].load(std::memory_order_acquire)) {   // once per device and kernel
         if ((e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
             return e;
         done[dev].store(true, std::memory_order_release);
     }
-    const unsigned most = 3 * kSms, tiles = tiles_in_all(p);
+    const unsigned most = kCtas * kSms, tiles = tiles_in_all(p);
     kKernel<<<tiles < most ? tiles : most, block, smem, s>>>(p, wide);
     return cudaGetLastError();
 }
@@ -967,7 +955,7 @@ kla_status kla_gated_scan_fwd(const void *x, const void *gate, const int64_t *st
     const cudaError_t e = by_type(dtype, mode, [&](auto t, auto log) {
         using E = decltype(t);
         constexpr bool kLog = decltype(log)::value;
-        if (ring) return run_ring<3, scan_fwd_ring_kernel<E, kLog, kFwdTok, kFwdWarps>>(p, wide, kFwdTok * kFwdWarps, 32 * kFwdWarps, cs);
+        if (ring) return run_ring<3, kFwdCtas, scan_fwd_ring_kernel<E, kLog, kFwdTok, kFwdWarps>>(p, wide, kFwdTok * kFwdWarps, 32 * kFwdWarps, cs);
         if constexpr (sizeof(E) == 2)   // rows of odd bf16
             scan_fwd_kernel<E, kLog, 1, kFwdTok, kFwdWarps><<<tiles_in_all(p), 32 * kFwdWarps, 0, cs>>>(p);
         return cudaGetLastError();
@@ -1017,7 +1005,7 @@ kla_status kla_gated_scan_bwd(const void *x, const void *gate, const void *dy, c
     const cudaError_t e = by_type(dtype, mode, [&](auto t, auto log) {
         using E = decltype(t);
         constexpr bool kLog = decltype(log)::value;
-        if (ring) return run_ring<5, scan_bwd_ring_kernel<E, kLog, kBwdTok, kBwdWarps>>(p, wide, kBwdTok * kBwdWarps, 32 * kBwdWarps, cs);
+        if (ring) return run_ring<5, kBwdCtas, scan_bwd_ring_kernel<E, kLog, kBwdTok, kBwdWarps>>(p, wide, kBwdTok * kBwdWarps, 32 * kBwdWarps, cs);
         if constexpr (sizeof(E) == 2)   // rows of odd bf16
             scan_bwd_kernel<E, kLog, 1, kBwdTok, kBwdWarps><<<tiles_in_all(p), 32 * kBwdWarps, 0, cs>>>(p);
         return cudaGetLastError();
