@@ -23,7 +23,7 @@ _MODES = {"sigmoid": _native.KLA_SCAN_SIGMOID, "log": _native.KLA_SCAN_LOG}
 _LAYOUTS = {"half": _native.KLA_ROTARY_HALF, "interleaved": _native.KLA_ROTARY_INTERLEAVED}
 _NORMS = {"rms": _native.KLA_NORM_RMS, "layer": _native.KLA_NORM_LAYER}
 _ACTS = {"silu": _native.KLA_ACT_SILU, "sigmoid": _native.KLA_ACT_SIGMOID}
-SCAN_SPAN = 64   # tokens between the states that gated_scan_fwd keeps for gated_scan_bwd
+SCAN_SPAN = 128   # tokens between the states that gated_scan_fwd keeps for gated_scan_bwd
 
 
 def _choice(name: str, table: dict, value) -> int:

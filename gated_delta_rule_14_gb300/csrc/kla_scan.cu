@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(ScanArgs p) {
 }
 
 // Tokens of a thread, warps of a CTA and CTAs of an SM.
-constexpr int kFwdTok = 32, kFwdWarps = 8, kFwdCtas = 2, kBwdTok = 16, kBwdWarps = 4, kBwdCtas = 4;
+constexpr int kFwdTok = 32, kFwdWarps = 8, kFwdCtas = 2, kBwdTok = 16, kBwdWarps = 8, kBwdCtas = 2;
 
 // ---- tiles through shared memory: rows of 128 bytes (64 channels of bf16, 32 of fp32), 4 bytes a lane
 constexpr int kRow = 128;

@@ -45,7 +45,7 @@ extern "C" {
  *   sizes    B, C >= 1, 0 <= T <= 2^31 - 1 - 65536 (T = 0 writes h_T only)
  *   alignment: x, gate, y their element; fp32 tensors 4 bytes; workspace 16 bytes
  */
-#define KLA_SCAN_SPAN 64
+#define KLA_SCAN_SPAN 128
 
 typedef enum { KLA_SCAN_SIGMOID = 0, KLA_SCAN_LOG = 1 } kla_scan_mode;
 
