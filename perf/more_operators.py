@@ -355,7 +355,8 @@ def _own(s):
                                               stats=train)
         r = {"y": y, "res": res}
         if train:
-            dx, dres, dw, dscale = kla.add_norm_bwd(s["dy"], s["dres"], s["x"], res, s["w"], s["scale"], mean, rstd)
+            dx, dres, dw, dscale = kla.add_norm_bwd(s["dy"], s["dres"], s["x"], s["res"], s["w"], s["scale"], mean,
+                                                   rstd)
             r |= {"dres": dres, "dw": dw}
             if s["scale"] is not None:
                 r |= {"dx": dx, "dscale": dscale}
