@@ -353,22 +353,20 @@ def gated_norm_bwd(dy: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, weight
     return dx, dgate, dw
 
 
-def _added_inputs(entry, x, like, name, weight, scale):
-    device = _device(name, like)
-    code = _code(name, like)
-    if like.dim() < 1:
-        raise ValueError(f"{name} must have an axis to normalise")
-    n = like.shape[-1]
+def _added_inputs(entry, x, residual, weight, scale):
+    device = _device("residual", residual)
+    code = _code("residual", residual)
+    if residual.dim() < 1:
+        raise ValueError("residual must have an axis to normalise")
+    n = residual.shape[-1]
     if n > _MOST:
         _refuse(entry, _native.KLA_ERR_UNSUPPORTED)
-    if not like.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if x is not None:
-        _check("x", x, like.shape, like.dtype, device)
+    _check("residual", residual, residual.shape, residual.dtype, device)
+    _check("x", x, residual.shape, residual.dtype, device)
     for label, t in (("weight", weight), ("scale", scale)):
         if t is not None:
             _check(label, t, (n,), _F32, device)
-    return device, code, like.numel() // max(1, n), n
+    return device, code, residual.numel() // max(1, n), n
 
 
 def add_norm_fwd(x: torch.Tensor, residual: torch.Tensor, weight: Optional[torch.Tensor] = None,
@@ -378,11 +376,11 @@ def add_norm_fwd(x: torch.Tensor, residual: torch.Tensor, weight: Optional[torch
 
     x, residual: [..., n] bf16 or fp32, contiguous, 3 <= n <= 65536; weight, scale: fp32 [n] or None (1). Returns (y,
     the sum, both in x's dtype, mean, rstd fp32 [...] for the backward pass): mean is None with norm "rms", both
-    without ``stats``. The norm is taken of the sum before it is rounded. ``out_residual`` may be ``residual``.
+    without ``stats``. The norm is taken of the sum before it is rounded. ``out_residual`` may be ``residual``
+    where no ``add_norm_bwd`` follows.
     """
     norm = _choice("norm", _NORMS, norm)
-    device, code, rows, n = _added_inputs("kla_add_norm_fwd", x, residual, "residual", weight, scale)
-    _check("x", x, residual.shape, residual.dtype, device)
+    device, code, rows, n = _added_inputs("kla_add_norm_fwd", x, residual, weight, scale)
     if out is None:
         out = torch.empty_like(residual)
     else:
@@ -400,22 +398,21 @@ def add_norm_fwd(x: torch.Tensor, residual: torch.Tensor, weight: Optional[torch
     return out, out_residual, mean, rstd
 
 
-def add_norm_bwd(dy: torch.Tensor, dresidual: Optional[torch.Tensor], x: Optional[torch.Tensor],
-                 residual: torch.Tensor, weight: Optional[torch.Tensor], scale: Optional[torch.Tensor],
+def add_norm_bwd(dy: torch.Tensor, dresidual: Optional[torch.Tensor], x: torch.Tensor, residual: torch.Tensor,
+                 weight: Optional[torch.Tensor], scale: Optional[torch.Tensor],
                  mean: Optional[torch.Tensor], rstd: torch.Tensor, *, workspace: Optional[torch.Tensor] = None):
-    """Gradients of ``add_norm_fwd`` given dy, dresidual (of the sum it returned; None: nothing reaches it), its x
-    (None where there is no scale), the sum it returned as ``residual``, mean (None: "rms") and rstd.
+    """Gradients of ``add_norm_fwd`` given dy, dresidual (of the sum it returned; None: nothing reaches it), its x,
+    residual, weight, scale, mean (None: "rms") and rstd. The sum is formed again from x and residual: a forward call
+    that this one follows keeps its ``residual``.
 
     Returns (dx, the gradient of the residual, dweight, dscale): without a scale dx is the residual's gradient itself
     and dscale is None. Equal calls give equal bits.
     """
-    device, code, rows, n = _added_inputs("kla_add_norm_bwd", x, residual, "residual", weight, scale)
+    device, code, rows, n = _added_inputs("kla_add_norm_bwd", x, residual, weight, scale)
     shape, dtype = residual.shape, residual.dtype
     _check("dy", dy, shape, dtype, device)
     if dresidual is not None:
         _check("dresidual", dresidual, shape, dtype, device)
-    if scale is not None:
-        _check("x", x, shape, dtype, device)
     if mean is not None:
         _check("mean", mean, shape[:-1], _F32, device)
     _check("rstd", rstd, shape[:-1], _F32, device)
@@ -425,7 +422,7 @@ def add_norm_bwd(dy: torch.Tensor, dresidual: Optional[torch.Tensor], x: Optiona
         dx, dscale = torch.empty_like(dr), torch.empty((n,), dtype=_F32, device=device)
     dw = torch.empty((n,), dtype=_F32, device=device)
     workspace, size = _scratch(_size("add_norm_bwd", rows, n, code), workspace, device)
-    st = _native.on(device).kla_add_norm_bwd(dy.data_ptr(), _ptr(dresidual), _ptr(x), residual.data_ptr(),
+    st = _native.on(device).kla_add_norm_bwd(dy.data_ptr(), _ptr(dresidual), x.data_ptr(), residual.data_ptr(),
                                              _ptr(weight), _ptr(scale), _ptr(mean), rstd.data_ptr(), _ptr(dx),
                                              dr.data_ptr(), dw.data_ptr(), _ptr(dscale), rows, n, code,
                                              _ptr(workspace), size, _stream(device))

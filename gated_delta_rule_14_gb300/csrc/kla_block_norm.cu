@@ -4,63 +4,386 @@
 //   gated   y = xh w act(z)                 dx = N(dy w act(z)),  dz = dy xh w act'(z),  dw = sum dy act(z) xh
 //   added   s = r + l x,  y = xh(s) w       dr = ds + N(dy w),  dx = l dr,  dw = sum dy xh,  dl = sum x dr
 //   xh = (x - mean) rstd, N(u) = rstd (u - mean(u) - xh mean(u xh)); without the means' terms where mean = 0 (RMS)
+#include <atomic>
 #include <climits>
+#include <type_traits>
 
-#include "kla_norm.cuh"
+#include "layer_dev.cuh"
 #include "../../include/kla_block.h"
 
 namespace kla {
 namespace {
 
-using namespace norm;
+enum Op { kGatedFwd, kGatedBwd, kAddFwd, kAddBwd };
+constexpr bool gated(Op op) { return op == kGatedFwd || op == kGatedBwd; }
+constexpr bool backward(Op op) { return op == kGatedBwd || op == kAddBwd; }
+// What a row is read of, in this order: gated x, z, dy; added x, residual, dy, dsum.
+constexpr int inputs(Op op) { return op == kAddBwd ? 4 : op == kGatedBwd ? 3 : 2; }
 
 struct NormArgs {
-    const void *dy, *x, *z;   // added: z is the residual in the forward pass, dsum in the backward pass
-    const void *sum;          // added, backward
-    int64_t z_stride;         // between rows of `groups` of them
+    const void *in[4];        // added, backward: dsum may be NULL
+    int64_t z_stride;         // gated: between rows of `groups` of z
     const float *w, *l;
     int w_groups;             // weights [groups, n]
-    void *y, *y2;             // gated: y; dx, dz. added: y, sum; dr, dx
+    void *out[2];             // gated: y; dx, dz. added: y, sum; dresidual, dx (or NULL)
     float *mean, *rstd;
-    float *part;              // [parts][2][n]
+    float *part;              // [parts][sums][n] of dw (and dl), or NULL
     int64_t rows;             // of all groups
     int groups, n;
     float eps;
     int layer, silu;
 };
 
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ float2 add(float2 a, float2 b) { return add2(a, b); }
+__device__ __forceinline__ float across(float v, int off) { return __shfl_xor_sync(0xffffffffu, v, off); }
+__device__ __forceinline__ float2 across(float2 v, int off) { return make_float2(across(v.x, off), across(v.y, off)); }
+
+template <typename T>
+__device__ __forceinline__ float sigmoid(float z) {
+    if (sizeof(T) == 4) return 1.f / (1.f + expf(-z));
+    // bf16: the hardware's exponential and reciprocal, off by 2^-21 at z of 10, far below z's own 2^-9
+    float e = z * -1.4426950408889634f;
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e));
+    e += 1.f;
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e));
+    return e;
+}
+// act(z), and act'(z)
+template <typename T>
+__device__ __forceinline__ float activation(float z, int silu, float &slope) {
+    const float s = sigmoid<T>(z);
+    slope = silu ? s * fmaf(z, 1.f - s, 1.f) : s * (1.f - s);
+    return silu ? z * s : s;
+}
+
+template <int kBytes>
+__device__ __forceinline__ void copy_in(void *to, const void *from) {
+    if constexpr (kBytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(to)), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ptx::smem_u32(to)), "l"(from) : "memory");
+}
+template <int kGroups>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kGroups) : "memory");
+}
+
+// kBytes of a row as values, and back
+template <typename T, int kBytes>
+__device__ __forceinline__ void unpack(const void *p, float *v) {
+    uint32_t r[kBytes / 4];
+    if constexpr (kBytes == 16) {
+        const uint4 q = *static_cast<const uint4 *>(p);
+        r[0] = q.x, r[1] = q.y, r[2] = q.z, r[3] = q.w;
+    } else {
+        r[0] = *static_cast<const uint32_t *>(p);
+    }
+#pragma unroll
+    for (int i = 0; i < kBytes / 4; ++i) {
+        if (sizeof(T) == 4) {
+            v[i] = __uint_as_float(r[i]);
+        } else {
+            v[2 * i] = __uint_as_float(r[i] << 16);
+            v[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
+        }
+    }
+}
+template <typename T, int kBytes>
+__device__ __forceinline__ void pack(void *p, const float *v) {
+    uint32_t r[kBytes / 4];
+#pragma unroll
+    for (int i = 0; i < kBytes / 4; ++i)
+        r[i] = sizeof(T) == 4 ? __float_as_uint(v[i]) : ptx::pack_bf16(v[2 * i], v[2 * i + 1]);
+    if constexpr (kBytes == 16) *static_cast<uint4 *>(p) = make_uint4(r[0], r[1], r[2], r[3]);
+    else *static_cast<uint32_t *>(p) = r[0];
+}
+
+// ---- rows that a team of threads holds in registers
+// A row belongs to a team of `width` threads (8 to 32 lanes of a warp, or whole warps up to the CTA), each with kNV
+// accesses of kBytes at fixed columns, so that weights and the sums of dw and dl stay in registers. Every thread
+// copies its own values of the next kStages - 1 rows into shared memory and takes them from there: no barrier stands
+// between copy and use, and what is on its way does not cost registers. CTAs are persistent.
+constexpr int kBlock = 512;
+// of the values of a thread: how many CTAs an SM's registers and shared memory hold
+constexpr int ctas(int values) { return values <= 8 ? 2 : 1; }
+constexpr int stages(Op op, int values, int bytes) {   // bytes: of a thread's row of one input
+    const int most = 200 * 1024 / (ctas(values) * kBlock) / (inputs(op) * bytes + (backward(op) ? 8 : 0));
+    return most > 6 ? 6 : most < 2 ? 2 : most;
+}
+
+template <typename T, int kBytes, int kNV, Op kOp>
+__global__ void __launch_bounds__(kBlock, ctas(kNV *kBytes / static_cast<int>(sizeof(T))))
+block_norm_kernel(NormArgs p, int width) {
+    constexpr int kV = kBytes / sizeof(T), kE = kV * kNV, kIns = inputs(kOp);
+    constexpr int kStages = stages(kOp, kE, kNV * kBytes);
+    constexpr bool kGated = gated(kOp), kBwd = backward(kOp);
+    dependency_release();
+    extern __shared__ __align__(16) uint8_t ring[];   // [stage][input][access][thread], then [stage][thread] of stats
+    __shared__ float2 sums[2][kBlock / 32];
+    const int team = threadIdx.x / width, lane = threadIdx.x % width, teams = kBlock / width;
+    const int groups = p.w_groups ? p.groups : 1, g = blockIdx.x % groups;   // whose weights this CTA has
+    const int64_t ctas_here = gridDim.x / groups, first = static_cast<int64_t>(blockIdx.x / groups) * teams;
+    const int64_t mine = p.rows / groups, step = ctas_here * teams;
+    const int turns = first < mine ? static_cast<int>((mine - first + step - 1) / step) : 0;
+    const bool four = kOp == kAddBwd && p.in[3] != nullptr;
+    float *const stats = reinterpret_cast<float *>(ring + kStages * kIns * kNV * kBlock * kBytes);
+    auto slot = [&](int stage, int i, int k) {
+        return ring + (((stage * kIns + i) * kNV + k) * kBlock + threadIdx.x) * kBytes;
+    };
+    auto row_of = [&](int turn) { return (first + team + turn * step) * groups + g; };
+    auto fetch = [&](int turn, int stage) {
+        const int64_t row = row_of(turn);
+        if (turn < turns && row < p.rows) {
+#pragma unroll
+            for (int i = 0; i < kIns; ++i) {
+                if (i == 3 && !four) break;
+                int64_t o = row * p.n;
+                if (kGated && i == 1 && p.z_stride)
+                    o = row / p.groups * p.z_stride + row % p.groups * p.n;
+                const T *from = static_cast<const T *>(p.in[i]) + o + lane * kV;
+#pragma unroll
+                for (int k = 0; k < kNV; ++k)
+                    if ((k * width + lane) * kV < p.n) copy_in<kBytes>(slot(stage, i, k), from + k * width * kV);
+            }
+            if (kBwd) {
+                copy_in<4>(stats + (stage * 2) * kBlock + threadIdx.x, p.rstd + row);
+                if (p.layer) copy_in<4>(stats + (stage * 2 + 1) * kBlock + threadIdx.x, p.mean + row);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch(i, i);
+    float w[kE], l[kGated ? 1 : kE], dw[kBwd ? kE : 1], dl[kOp == kAddBwd ? kE : 1];
+#pragma unroll
+    for (int u = 0; u < kE; ++u) {
+        const int c = (u / kV * width + lane) * kV + u % kV;
+        w[u] = p.w && c < p.n ? p.w[static_cast<int64_t>(g) * p.n + c] : 1.f;
+        if (!kGated) l[u] = p.l && c < p.n ? p.l[c] : 1.f;
+        if (kBwd) dw[u] = 0.f;
+        if (kOp == kAddBwd) dl[u] = 0.f;
+    }
+    const float inv = 1.f / p.n;
+    int turn_sum = 0;
+    auto sum = [&](auto v) {   // over the team; all of the CTA's threads take part in the same calls
+        const int lanes = width < 32 ? width : 32;
+        for (int off = lanes / 2; off; off >>= 1) v = add(v, across(v, off));
+        if (width > 32) {
+            using V = decltype(v);
+            const int warps = width / 32, at = team * warps;
+            if ((threadIdx.x & 31) == 0) reinterpret_cast<V &>(sums[turn_sum][threadIdx.x / 32]) = v;
+            ptx::named_sync(1 + team, width);
+            v = reinterpret_cast<const V &>(sums[turn_sum][at]);
+            for (int i = 1; i < warps; ++i) v = add(v, reinterpret_cast<const V &>(sums[turn_sum][at + i]));
+            turn_sum ^= 1;   // the next sum's words, while others still read these
+        }
+        return v;
+    };
+    for (int t = 0, stage = 0; t < turns; ++t) {
+        fetch(t + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
+        copies_wait<kStages - 1>();
+        const int64_t row = row_of(t);
+        const bool live = row < p.rows;
+        auto get = [&](int i, int k, float *v) {   // zeros past the row's end
+            if (live && (k * width + lane) * kV < p.n) {
+                unpack<T, kBytes>(slot(stage, i, k), v);
+            } else {
+#pragma unroll
+                for (int e = 0; e < kV; ++e) v[e] = 0.f;
+            }
+        };
+        auto put = [&](int i, int k, const float *v) {
+            const int c = (k * width + lane) * kV;
+            if (live && c < p.n) pack<T, kBytes>(static_cast<T *>(p.out[i]) + row * p.n + c, v);
+        };
+        float x[kE];   // what the norm is of, then xh
+#pragma unroll
+        for (int k = 0; k < kNV; ++k) {
+            get(0, k, x + k * kV);
+            if (!kGated) {
+                float r[kV];
+                get(1, k, r);
+#pragma unroll
+                for (int e = 0; e < kV; ++e) x[k * kV + e] = fmaf(l[k * kV + e], x[k * kV + e], r[e]);
+            }
+        }
+        if constexpr (!kBwd) {
+            if (kOp == kAddFwd)
+#pragma unroll
+                for (int k = 0; k < kNV; ++k) put(1, k, x + k * kV);
+            float mu = 0.f;
+            if (p.layer) {
+                float s = 0.f;
+#pragma unroll
+                for (int u = 0; u < kE; ++u) s += x[u];
+                mu = sum(s) * inv;
+#pragma unroll
+                for (int u = 0; u < kE; ++u)
+                    x[u] = (u / kV * width + lane) * kV < p.n ? x[u] - mu : 0.f;
+            }
+            float q = 0.f;
+#pragma unroll
+            for (int u = 0; u < kE; ++u) q = fmaf(x[u], x[u], q);
+            const float rs = 1.f / sqrtf(sum(q) * inv + p.eps);
+            if (live && lane == 0) {
+                if (p.mean) p.mean[row] = mu;
+                if (p.rstd) p.rstd[row] = rs;
+            }
+#pragma unroll
+            for (int k = 0; k < kNV; ++k) {
+                float y[kV], z[kV];
+                if (kGated) get(1, k, z);
+#pragma unroll
+                for (int e = 0; e < kV; ++e) {
+                    y[e] = x[k * kV + e] * rs * w[k * kV + e];
+                    float slope;
+                    if (kGated) y[e] *= activation<T>(z[e], p.silu, slope);
+                }
+                put(0, k, y);
+            }
+        } else {
+            const float rs = live ? stats[(stage * 2) * kBlock + threadIdx.x] : 0.f;
+            const float mu = live && p.layer ? stats[(stage * 2 + 1) * kBlock + threadIdx.x] : 0.f;
+            float d[kE];   // dL/dxh; zero past the row's end, where nothing is added to any sum then
+            float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kNV; ++k) {
+                float dy[kV], z[kV];
+                get(2, k, dy);
+                if (kGated) get(1, k, z);
+#pragma unroll
+                for (int e = 0; e < kV; ++e) {
+                    const int u = k * kV + e;
+                    x[u] = (x[u] - mu) * rs;
+                    if (kGated) {
+                        float slope;
+                        const float a = activation<T>(z[e], p.silu, slope), dyx = dy[e] * x[u];
+                        dw[u] = fmaf(dyx, a, dw[u]);
+                        z[e] = dyx * w[u] * slope;
+                        d[u] = dy[e] * w[u] * a;
+                    } else {
+                        dw[u] = fmaf(dy[e], x[u], dw[u]);
+                        d[u] = dy[e] * w[u];
+                    }
+                    s.x += d[u];
+                    s.y = fmaf(d[u], x[u], s.y);
+                }
+                if (kGated) put(1, k, z);
+            }
+            float m1 = 0.f, m2;
+            if (p.layer) {
+                s = sum(s);
+                m1 = s.x * inv;
+                m2 = s.y * inv;
+            } else {
+                m2 = sum(s.y) * inv;
+            }
+#pragma unroll
+            for (int k = 0; k < kNV; ++k) {
+                float o[kV], r[kV];
+                if (kOp == kAddBwd) {
+                    if (four) get(3, k, r);
+                    else
+#pragma unroll
+                        for (int e = 0; e < kV; ++e) r[e] = 0.f;
+                }
+#pragma unroll
+                for (int e = 0; e < kV; ++e) {
+                    const int u = k * kV + e;
+                    o[e] = rs * (d[u] - m1 - x[u] * m2);
+                    if (kOp == kAddBwd) o[e] += r[e];
+                }
+                put(0, k, o);
+                if (kOp == kAddBwd && p.l) {
+                    float v[kV];
+                    get(0, k, v);
+#pragma unroll
+                    for (int e = 0; e < kV; ++e) {
+                        const int u = k * kV + e;
+                        dl[u] = fmaf(o[e], v[e], dl[u]);
+                        o[e] *= l[u];
+                    }
+                    put(1, k, o);
+                }
+            }
+        }
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+    if constexpr (kBwd) {
+        copies_wait<0>();
+        if (!p.part) return;
+        // the teams add up one after the other, so that a CTA leaves one row of each sum
+        constexpr int kSums = kOp == kAddBwd ? 2 : 1;
+        float *const acc = reinterpret_cast<float *>(ring);   // [kSums][n]
+        for (int q = 0; q < teams; ++q) {
+            __syncthreads();
+            if (team == q)
+#pragma unroll
+                for (int u = 0; u < kE; ++u) {
+                    const int c = (u / kV * width + lane) * kV + u % kV;
+                    if (c < p.n) {
+                        acc[c] = q ? acc[c] + dw[u] : dw[u];
+                        if (kSums == 2) acc[p.n + c] = q ? acc[p.n + c] + dl[u] : dl[u];
+                    }
+                }
+        }
+        __syncthreads();
+        float *to = p.part + static_cast<int64_t>(blockIdx.x) * kSums * p.n;
+        for (int c = threadIdx.x; c < kSums * p.n; c += kBlock) to[c] = acc[c];
+    }
+}
+
+// ---- any other row, of any length and alignment: a CTA takes rows one after the other and reads each from memory and
+// then from L1 or L2
+constexpr int kAnyBlock = 512;
 template <typename V>
-__device__ __forceinline__ V block_sum(V v, V *slots) {
-    v = lane_sum<32>(v);
+__device__ __forceinline__ V block_sum(V v, float2 *slots) {
+    for (int off = 16; off; off >>= 1) v = add(v, across(v, off));
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) slots[threadIdx.x / 32] = v;
+    if ((threadIdx.x & 31) == 0) reinterpret_cast<V &>(slots[threadIdx.x / 32]) = v;
     __syncthreads();
-    v = slots[0];
-    for (int i = 1; i < static_cast<int>(blockDim.x) / 32; ++i) v = add(v, slots[i]);
+    v = reinterpret_cast<const V &>(slots[0]);
+    for (int i = 1; i < kAnyBlock / 32; ++i) v = add(v, reinterpret_cast<const V &>(slots[i]));
     return v;
 }
-__device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
 
-// A CTA takes rows one after the other.
-template <typename T, bool kGated>
-__global__ void block_norm_fwd_kernel(NormArgs p) {
-    __shared__ float slots[32];
+// One column of a row: what the norm is of; and dL/dxh with what else the gate's gradient takes.
+template <typename T, Op kOp>
+struct Column {
+    const NormArgs &p;
+    int64_t o, oz;
+    const float *w;
+    __device__ __forceinline__ Column(const NormArgs &a, int64_t row) : p(a), o(row * a.n), oz(o), w(a.w) {
+        if (gated(kOp) && p.z_stride) oz = row / p.groups * p.z_stride + row % p.groups * p.n;
+        if (w && p.w_groups) w += row % p.groups * p.n;
+    }
+    __device__ __forceinline__ float in(int i, int64_t at) const { return to_f32(static_cast<const T *>(p.in[i])[at]); }
+    __device__ __forceinline__ float value(int c) const {
+        return gated(kOp) ? in(0, o + c) : fmaf(p.l ? p.l[c] : 1.f, in(0, o + c), in(1, o + c));
+    }
+    __device__ __forceinline__ float weight(int c) const { return w ? w[c] : 1.f; }
+    __device__ __forceinline__ float act(int c, float &slope) const {
+        slope = 0.f;
+        return gated(kOp) ? activation<T>(in(1, oz + c), p.silu, slope) : 1.f;
+    }
+    __device__ __forceinline__ void put(int i, int c, float v) const {
+        static_cast<T *>(p.out[i])[o + c] = from_f32<T>(v);
+    }
+};
+
+template <typename T, Op kOp>
+__global__ void __launch_bounds__(kAnyBlock) block_norm_any_fwd_kernel(NormArgs p) {
+    __shared__ float2 slots[32];
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        const int64_t o = row * p.n;
-        const T *x = static_cast<const T *>(p.x) + o;
-        const T *z = static_cast<const T *>(p.z) +
-                     (kGated ? row / p.groups * p.z_stride + row % p.groups * p.n : o);
-        const float *w = p.w ? p.w + (p.w_groups ? row % p.groups * p.n : 0) : nullptr;
-        auto value = [&](int c) {
-            return kGated ? to_f32(x[c]) : fmaf(p.l ? p.l[c] : 1.f, to_f32(x[c]), to_f32(z[c]));
-        };
-        float mu = 0.f, q = 0.f;
+        const Column<T, kOp> at(p, row);
+        float mu = 0.f, q = 0.f, slope;
         if (p.layer) {
-            for (int c = threadIdx.x; c < p.n; c += blockDim.x) mu += value(c);
+            for (int c = threadIdx.x; c < p.n; c += kAnyBlock) mu += at.value(c);
             mu = block_sum(mu, slots) / p.n;
         }
-        for (int c = threadIdx.x; c < p.n; c += blockDim.x) {
-            const float d = value(c) - mu;
+        for (int c = threadIdx.x; c < p.n; c += kAnyBlock) {
+            const float d = at.value(c) - mu;
             q = fmaf(d, d, q);
         }
         const float rs = 1.f / sqrtf(block_sum(q, slots) / p.n + p.eps);
@@ -68,91 +391,109 @@ __global__ void block_norm_fwd_kernel(NormArgs p) {
             if (p.mean) p.mean[row] = mu;
             if (p.rstd) p.rstd[row] = rs;
         }
-        for (int c = threadIdx.x; c < p.n; c += blockDim.x) {
-            const float v = value(c);
-            float y = (v - mu) * rs * (w ? w[c] : 1.f);
-            if (kGated) {
-                const float g = to_f32(z[c]), s = sigmoid(g);
-                y *= p.silu ? g * s : s;
-            } else {
-                static_cast<T *>(p.y2)[o + c] = from_f32<T>(v);
-            }
-            static_cast<T *>(p.y)[o + c] = from_f32<T>(y);
+        for (int c = threadIdx.x; c < p.n; c += kAnyBlock) {
+            const float v = at.value(c);
+            if (kOp == kAddFwd) at.put(1, c, v);
+            at.put(0, c, (v - mu) * rs * at.weight(c) * at.act(c, slope));
         }
     }
 }
 
-template <typename T, bool kGated>
-__global__ void block_norm_bwd_kernel(NormArgs p) {
+template <typename T, Op kOp>
+__global__ void __launch_bounds__(kAnyBlock) block_norm_any_bwd_kernel(NormArgs p) {
     __shared__ float2 slots[32];
+    dependency_release();
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        const int64_t o = row * p.n;
-        const T *v = static_cast<const T *>(kGated ? p.x : p.sum) + o, *dy = static_cast<const T *>(p.dy) + o;
-        const T *z = static_cast<const T *>(p.z);
-        if (z) z += kGated ? row / p.groups * p.z_stride + row % p.groups * p.n : o;
-        const float *w = p.w ? p.w + (p.w_groups ? row % p.groups * p.n : 0) : nullptr;
+        const Column<T, kOp> at(p, row);
         const float mu = p.mean ? p.mean[row] : 0.f, rs = p.rstd[row];
-        auto part = [&](int c, float &xh, float &u, float &slope) {   // u = dL/dxh
-            xh = (to_f32(v[c]) - mu) * rs;
-            u = to_f32(dy[c]) * (w ? w[c] : 1.f);
-            if (kGated) {
-                const float g = to_f32(z[c]), s = sigmoid(g);
-                slope = (p.silu ? s * fmaf(g, 1.f - s, 1.f) : s * (1.f - s)) * u;
-                u *= p.silu ? g * s : s;
-            }
-        };
         float2 s = make_float2(0.f, 0.f);
-        float xh, u, slope;
-        for (int c = threadIdx.x; c < p.n; c += blockDim.x) {
-            part(c, xh, u, slope);
-            s.x += u;
-            s.y = fmaf(u, xh, s.y);
+        float slope;
+        for (int c = threadIdx.x; c < p.n; c += kAnyBlock) {
+            const float d = at.in(2, at.o + c) * at.weight(c) * at.act(c, slope);
+            s.x += d;
+            s.y = fmaf(d, (at.value(c) - mu) * rs, s.y);
         }
         s = block_sum(s, slots);
         const float m1 = p.layer ? s.x / p.n : 0.f, m2 = s.y / p.n;
-        for (int c = threadIdx.x; c < p.n; c += blockDim.x) {
-            part(c, xh, u, slope);
-            float d = rs * (u - m1 - xh * m2);
-            if (kGated) {
-                static_cast<T *>(p.y)[o + c] = from_f32<T>(d);
-                static_cast<T *>(p.y2)[o + c] = from_f32<T>(slope * xh);
+        for (int c = threadIdx.x; c < p.n; c += kAnyBlock) {
+            const float xh = (at.value(c) - mu) * rs, dyw = at.in(2, at.o + c) * at.weight(c);
+            const float d = dyw * at.act(c, slope);
+            float o = rs * (d - m1 - xh * m2);
+            if (kOp == kAddBwd) {
+                if (p.in[3]) o += at.in(3, at.o + c);
+                at.put(0, c, o);
+                if (p.l) at.put(1, c, o * p.l[c]);
             } else {
-                if (z) d += to_f32(z[c]);
-                static_cast<T *>(p.y)[o + c] = from_f32<T>(d);
-                if (p.y2) static_cast<T *>(p.y2)[o + c] = from_f32<T>(d * p.l[c]);
+                at.put(0, c, o);
+                at.put(1, c, dyw * xh * slope);
             }
         }
+        if (kOp == kAddBwd && threadIdx.x == 0 && p.part)   // the means, for dl
+            reinterpret_cast<float2 *>(p.part)[row] = make_float2(m1, m2);
     }
 }
 
-// Sums over the rows of one group (or of all, where they share weights): a CTA per 32 columns, its lanes along them.
-template <typename T, bool kGated>
-__global__ void block_norm_sums_kernel(NormArgs p, float *dw, float *dl) {
+// dw and dl of those: a CTA's lanes along 32 columns, its warps along the rows of one part of them.
+template <typename T, Op kOp>
+__global__ void __launch_bounds__(1024) block_norm_any_sums_kernel(NormArgs p, const float2 *means, float *part) {
+    constexpr int kSums = kOp == kAddBwd ? 2 : 1;
     __shared__ float2 slots[32][33];
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), warp = threadIdx.x / 32;
-    const int64_t step = p.w_groups ? p.groups : 1;
+    dependency_release();
+    dependency_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
+    const int groups = p.w_groups ? p.groups : 1;
+    const int64_t each = (p.rows / groups + gridDim.z - 1) / gridDim.z, r0 = blockIdx.z * each;
+    const int64_t r1 = r0 + each < p.rows / groups ? r0 + each : p.rows / groups;
     float2 s = make_float2(0.f, 0.f);
-    for (int64_t row = blockIdx.y + warp * step; c < p.n && row < p.rows; row += 32 * step) {
-        const int64_t o = row * p.n + c;
-        const float mu = p.mean ? p.mean[row] : 0.f, rs = p.rstd[row];
-        const float xh = (to_f32(static_cast<const T *>(kGated ? p.x : p.sum)[o]) - mu) * rs;
-        float d = to_f32(static_cast<const T *>(p.dy)[o]);
-        if (kGated) {
-            const float g =
-                to_f32(static_cast<const T *>(p.z)[row / p.groups * p.z_stride + row % p.groups * p.n + c]);
-            d *= p.silu ? g * sigmoid(g) : sigmoid(g);
+    for (int64_t r = r0 + warp; c < p.n && r < r1; r += 32) {
+        const int64_t row = r * groups + blockIdx.y;
+        const Column<T, kOp> at(p, row);
+        const float mu = p.mean ? p.mean[row] : 0.f, rs = p.rstd[row], xh = (at.value(c) - mu) * rs;
+        const float dy = at.in(2, at.o + c);
+        float slope;
+        s.x = fmaf(dy * xh, at.act(c, slope), s.x);
+        if (kSums == 2 && p.l) {
+            const float2 m = means[row];
+            float o = rs * (dy * at.weight(c) - m.x - xh * m.y);
+            if (p.in[3]) o += at.in(3, at.o + c);
+            s.y = fmaf(o, at.in(0, at.o + c), s.y);
         }
-        s.x = fmaf(d, xh, s.x);
-        if (!kGated && dl) s.y = fmaf(to_f32(static_cast<const T *>(p.x)[o]), to_f32(static_cast<const T *>(p.y)[o]), s.y);
     }
-    slots[warp][threadIdx.x & 31] = s;
+    slots[warp][lane] = s;
     __syncthreads();
     if (warp == 0 && c < p.n) {
-        for (int i = 1; i < 32; ++i) s = add(s, slots[i][threadIdx.x & 31]);
-        if (dw) dw[blockIdx.y * static_cast<int64_t>(p.n) + c] = s.x;
-        if (!kGated && dl) dl[c] = s.y;
+        for (int i = 1; i < 32; ++i) s = add(s, slots[i][lane]);
+        float *to = part + (static_cast<int64_t>(blockIdx.z) * groups + blockIdx.y) * kSums * p.n + c;
+        to[0] = s.x;
+        if (kSums == 2) to[p.n] = s.y;
     }
 }
+
+// The parts' rows added up in their order: part i of group g is row i * groups + g.
+__global__ void __launch_bounds__(1024) block_norm_join_kernel(const float *part, float *dw, float *dl, int parts,
+                                                               int groups, int n, int sums) {
+    __shared__ float2 slots[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
+    dependency_wait();
+    float2 s = make_float2(0.f, 0.f);
+    if (c < n)
+#pragma unroll 4
+        for (int i = warp; i < parts; i += 32) {
+            const float *from = part + (static_cast<int64_t>(i) * groups + blockIdx.y) * sums * n + c;
+            s.x += from[0];
+            if (sums == 2) s.y += from[n];
+        }
+    slots[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && c < n) {
+        for (int i = 1; i < 32; ++i) s = add(s, slots[i][lane]);
+        if (dw) dw[static_cast<int64_t>(blockIdx.y) * n + c] = s.x;
+        if (dl) dl[c] = s.y;
+    }
+}
+
+// ------------------------------------------------------------------------------------ host side
+constexpr int kSms = 152;
 
 kla_status check(int64_t rows, int groups, int n, kla_dtype dtype) {
     if (rows < 0 || groups < 1 || n < 1) return KLA_ERR_INVALID_ARG;
@@ -172,19 +513,117 @@ bool apart(const Span (&outs)[kOuts], const Span (&ins)[kIns]) {
     return true;
 }
 
-template <typename T, bool kGated>
-cudaError_t fwd(const NormArgs &p, cudaStream_t s) {
-    const int grid = static_cast<int>(p.rows < 152 * 8 ? p.rows : 152 * 8);
-    block_norm_fwd_kernel<T, kGated><<<grid, 256, 0, s>>>(p);
+// How rows are taken: `bytes` of an access (0: value by value), accesses of a thread, threads of a team.
+struct Plan {
+    int bytes, nv, width;
+    int grid;   // CTAs of the rows' kernel, a multiple of the groups with weights of their own
+};
+// Rows start on `bytes` bytes. A thread holds at most kNV accesses (16 bytes: 2, 4 bytes: 8, 32 bytes either way).
+Plan plan(int64_t rows, int groups, int n, int esz, int bytes) {
+    Plan p{bytes, 0, 0, 0};
+    const int accesses = bytes ? n * esz / bytes : 0, full = bytes == 16 ? 2 : 8;
+    if (bytes == 0 || accesses > kBlock * full) {
+        p.bytes = 0;
+        const int64_t most = kSms * 4;
+        p.grid = static_cast<int>(rows < most ? rows : most);
+        return p;
+    }
+    // one access a thread as long as a warp holds the row so: more rows are on their way then
+    const int least = bytes == 16 ? 1 : 2;
+    p.nv = accesses <= 32 * least ? least : full;
+    p.width = 8;
+    while (p.width * p.nv < accesses) p.width *= 2;
+    const int64_t teams = kBlock / p.width, of_group = (rows / groups + teams - 1) / teams;
+    int64_t want = (static_cast<int64_t>(kSms) * ctas(p.nv * bytes / esz) + groups - 1) / groups;
+    if (want > of_group) want = of_group;
+    p.grid = static_cast<int>((want < 1 ? 1 : want) * groups);
+    return p;
+}
+// Parts of the rows that block_norm_any_sums_kernel takes side by side.
+int any_parts(int64_t rows, int groups, int n) {
+    const int64_t tiles = static_cast<int64_t>((n + 31) / 32) * groups, most = (rows / groups + 255) / 256;
+    int64_t parts = 2 * kSms / tiles;
+    if (parts > most) parts = most;
+    return static_cast<int>(parts < 1 ? 1 : parts);
+}
+size_t any_means_bytes(int64_t rows) { return (static_cast<size_t>(rows) * sizeof(float2) + 15) / 16 * 16; }
+// Scratch of the backward pass, for whatever alignment the call has.
+size_t workspace_bytes_of(int64_t rows, int groups, int n, int esz, int sums) {
+    size_t most = any_means_bytes(rows) + static_cast<size_t>(any_parts(rows, groups, n)) * groups * sums * n * 4;
+    for (int bytes : {16, 4}) {
+        const Plan p = plan(rows, groups, n, esz, bytes);
+        const size_t need = p.bytes ? static_cast<size_t>(p.grid) * sums * n * 4 : 0;
+        if (need > most) most = need;
+    }
+    return most;
+}
+
+template <typename T, int kBytes, int kNV, Op kOp>
+cudaError_t run_rows(const NormArgs &a, const Plan &p, cudaStream_t s) {
+    constexpr int kMaxDevices = 64;
+    static std::atomic<bool> done[kMaxDevices];
+    constexpr int kS = stages(kOp, kNV * kBytes / static_cast<int>(sizeof(T)), kNV * kBytes);
+    constexpr int kRing = kS * kBlock * (inputs(kOp) * kNV * kBytes + (backward(kOp) ? 8 : 0));
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    auto kernel = block_norm_kernel<T, kBytes, kNV, kOp>;
+    if (!done[dev].load(std::memory_order_acquire)) {   // once per device and kernel: the attribute outlasts the call
+        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing)) != cudaSuccess)
+            return e;
+        done[dev].store(true, std::memory_order_release);
+    }
+    static_assert(!backward(kOp) || kRing >= 2 * kBlock * kNV * kBytes / static_cast<int>(sizeof(T)) * 4, "sums");
+    kernel<<<p.grid, kBlock, kRing, s>>>(a, p.width);
     return cudaGetLastError();
 }
-template <typename T, bool kGated>
-cudaError_t bwd(const NormArgs &p, float *dw, float *dl, cudaStream_t s) {
-    const int grid = static_cast<int>(p.rows < 152 * 8 ? p.rows : 152 * 8);
-    block_norm_bwd_kernel<T, kGated><<<grid, 256, 0, s>>>(p);
-    if (dw || dl)
-        block_norm_sums_kernel<T, kGated><<<dim3((p.n + 31) / 32, p.w_groups ? p.groups : 1), 1024, 0, s>>>(p, dw, dl);
-    return cudaGetLastError();
+
+// The rows' kernel, and in the backward pass the sums over its parts. `workspace` is NULL where no sum is wanted.
+template <typename T, Op kOp>
+cudaError_t run(NormArgs a, float *dw, float *dl, void *workspace, cudaStream_t s) {
+    constexpr int kSums = kOp == kAddBwd ? 2 : 1;
+    const int groups = a.w_groups ? a.groups : 1, esz = sizeof(T);
+    auto fits = [&](int bytes) {
+        if (a.n * esz % bytes || (a.z_stride * esz) % bytes) return false;
+        for (const void *q : {a.in[0], a.in[1], a.in[2], a.in[3], static_cast<const void *>(a.out[0]),
+                              static_cast<const void *>(a.out[1])})
+            if (!aligned(q, bytes)) return false;
+        return true;
+    };
+    const Plan p = plan(a.rows, groups, a.n, esz, fits(16) ? 16 : fits(4) ? 4 : 0);
+    cudaError_t e;
+    if (p.bytes) {
+        a.part = static_cast<float *>(workspace);
+        if (p.bytes == 16) e = p.nv == 1 ? run_rows<T, 16, 1, kOp>(a, p, s) : run_rows<T, 16, 2, kOp>(a, p, s);
+        else e = p.nv == 2 ? run_rows<T, 4, 2, kOp>(a, p, s) : run_rows<T, 4, 8, kOp>(a, p, s);
+        if (e != cudaSuccess || !workspace) return e;
+        return launch_dependent(block_norm_join_kernel, dim3((a.n + 31) / 32, groups), 1024, 0, s, a.part, dw, dl,
+                                p.grid / groups, groups, a.n, kSums);
+    }
+    if constexpr (!backward(kOp)) {
+        block_norm_any_fwd_kernel<T, kOp><<<p.grid, kAnyBlock, 0, s>>>(a);
+        return cudaGetLastError();
+    } else {
+        float *part = workspace ? reinterpret_cast<float *>(static_cast<char *>(workspace) + any_means_bytes(a.rows))
+                                : nullptr;
+        a.part = static_cast<float *>(workspace);
+        block_norm_any_bwd_kernel<T, kOp><<<p.grid, kAnyBlock, 0, s>>>(a);
+        if ((e = cudaGetLastError()) != cudaSuccess || !workspace) return e;
+        const int parts = any_parts(a.rows, groups, a.n);
+        e = launch_dependent(block_norm_any_sums_kernel<T, kOp>, dim3((a.n + 31) / 32, groups, parts), 1024, 0, s, a,
+                             static_cast<const float2 *>(workspace), part);
+        if (e != cudaSuccess) return e;
+        return launch_dependent(block_norm_join_kernel, dim3((a.n + 31) / 32, groups), 1024, 0, s, part, dw, dl, parts,
+                                groups, a.n, kSums);
+    }
+}
+template <Op kOp>
+kla_status run(const NormArgs &a, kla_dtype dtype, float *dw, float *dl, void *workspace, void *stream) {
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = dtype == KLA_DTYPE_BF16 ? run<__nv_bfloat16, kOp>(a, dw, dl, workspace, s)
+                                                  : run<float, kOp>(a, dw, dl, workspace, s);
+    return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
 }
 
 }  // namespace
@@ -215,17 +654,16 @@ kla_status kla_gated_norm_fwd(const void *x, const void *gate, int64_t gate_stri
                         span(weight, 4ull * (weight_groups ? row : n))};
     if (!apart(outs, ins)) return KLA_ERR_INVALID_ARG;
     NormArgs p{};
-    p.x = x; p.z = gate; p.z_stride = gate_stride; p.w = weight; p.w_groups = weight_groups != 0; p.y = y;
+    p.in[0] = x; p.in[1] = gate; p.w = weight; p.w_groups = weight_groups != 0; p.out[0] = y;
+    p.z_stride = gate_stride == static_cast<int64_t>(row) ? 0 : gate_stride;
     p.mean = mean; p.rstd = rstd; p.rows = rows * groups; p.groups = groups; p.n = n; p.eps = eps;
     p.layer = norm == KLA_NORM_LAYER; p.silu = act == KLA_ACT_SILU;
-    cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = dtype == KLA_DTYPE_BF16 ? fwd<__nv_bfloat16, true>(p, cs) : fwd<float, true>(p, cs);
-    return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+    return run<kGatedFwd>(p, dtype, nullptr, nullptr, nullptr, stream);
 }
 
 size_t kla_gated_norm_bwd_workspace_size(int64_t rows, int groups, int n, kla_dtype dtype, int weight_groups) {
     if (kla::check(rows, groups, n, dtype) != KLA_OK || rows == 0) return 0;
-    return 0;
+    return kla::workspace_bytes_of(rows * groups, weight_groups ? groups : 1, n, dtype == KLA_DTYPE_BF16 ? 2 : 4, 1);
 }
 
 kla_status kla_gated_norm_bwd(const void *dy, const void *x, const void *gate, int64_t gate_stride,
@@ -255,12 +693,11 @@ kla_status kla_gated_norm_bwd(const void *dy, const void *x, const void *gate, i
                         span(weight, par), span(mean, stat), span(rstd, stat)};
     if (!apart(outs, ins)) return KLA_ERR_INVALID_ARG;
     NormArgs p{};
-    p.dy = dy; p.x = x; p.z = gate; p.z_stride = gate_stride; p.w = weight; p.w_groups = weight_groups != 0;
-    p.y = dx; p.y2 = dgate; p.mean = const_cast<float *>(mean); p.rstd = const_cast<float *>(rstd);
+    p.in[0] = x; p.in[1] = gate; p.in[2] = dy; p.w = weight; p.w_groups = weight_groups != 0;
+    p.z_stride = gate_stride == static_cast<int64_t>(row) ? 0 : gate_stride;
+    p.out[0] = dx; p.out[1] = dgate; p.mean = const_cast<float *>(mean); p.rstd = const_cast<float *>(rstd);
     p.rows = rows * groups; p.groups = groups; p.n = n; p.layer = mean != nullptr; p.silu = act == KLA_ACT_SILU;
-    const cudaError_t e = dtype == KLA_DTYPE_BF16 ? bwd<__nv_bfloat16, true>(p, dweight, nullptr, cs)
-                                                  : bwd<float, true>(p, dweight, nullptr, cs);
-    return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+    return run<kGatedBwd>(p, dtype, dweight, nullptr, dweight ? workspace : nullptr, stream);
 }
 
 kla_status kla_add_norm_fwd(const void *x, const void *residual, const float *weight, const float *scale, void *y,
@@ -284,30 +721,28 @@ kla_status kla_add_norm_fwd(const void *x, const void *residual, const float *we
                         sum == residual ? span(nullptr, 0) : span(residual, all)};
     if (!apart(outs, ins)) return KLA_ERR_INVALID_ARG;
     NormArgs p{};
-    p.x = x; p.z = residual; p.w = weight; p.l = scale; p.y = y; p.y2 = sum; p.mean = mean; p.rstd = rstd;
-    p.rows = rows; p.groups = 1; p.n = n; p.eps = eps; p.layer = norm == KLA_NORM_LAYER;
-    cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = dtype == KLA_DTYPE_BF16 ? fwd<__nv_bfloat16, false>(p, cs) : fwd<float, false>(p, cs);
-    return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+    p.in[0] = x; p.in[1] = residual; p.w = weight; p.l = scale; p.out[0] = y; p.out[1] = sum; p.mean = mean;
+    p.rstd = rstd; p.rows = rows; p.groups = 1; p.n = n; p.eps = eps; p.layer = norm == KLA_NORM_LAYER;
+    return run<kAddFwd>(p, dtype, nullptr, nullptr, nullptr, stream);
 }
 
 size_t kla_add_norm_bwd_workspace_size(int64_t rows, int n, kla_dtype dtype) {
     if (kla::check(rows, 1, n, dtype) != KLA_OK || rows == 0) return 0;
-    return 0;
+    return kla::workspace_bytes_of(rows, 1, n, dtype == KLA_DTYPE_BF16 ? 2 : 4, 2);
 }
 
-kla_status kla_add_norm_bwd(const void *dy, const void *dsum, const void *x, const void *sum, const float *weight,
-                            const float *scale, const float *mean, const float *rstd, void *dx, void *dresidual,
-                            float *dweight, float *dscale, int64_t rows, int n, kla_dtype dtype, void *workspace,
-                            size_t workspace_bytes, void *stream) {
+kla_status kla_add_norm_bwd(const void *dy, const void *dsum, const void *x, const void *residual,
+                            const float *weight, const float *scale, const float *mean, const float *rstd, void *dx,
+                            void *dresidual, float *dweight, float *dscale, int64_t rows, int n, kla_dtype dtype,
+                            void *workspace, size_t workspace_bytes, void *stream) {
     using namespace kla;
     const kla_status st = check(rows, 1, n, dtype);
     if (st != KLA_OK) return st;
     if (!scale && (dx || dscale)) return KLA_ERR_INVALID_ARG;
-    if (rows > 0 && (!dy || !sum || !rstd || !dresidual || (scale && !dx) || (dscale && !x))) return KLA_ERR_INVALID_ARG;
+    if (rows > 0 && (!dy || !x || !residual || !rstd || !dresidual || (scale && !dx))) return KLA_ERR_INVALID_ARG;
     const size_t esz = dtype == KLA_DTYPE_BF16 ? 2 : 4;
-    if (!aligned(dy, esz) || !aligned(dsum, esz) || !aligned(x, esz) || !aligned(sum, esz) || !aligned(dx, esz) ||
-        !aligned(dresidual, esz) || !aligned(weight, 4) || !aligned(scale, 4) || !aligned(mean, 4) ||
+    if (!aligned(dy, esz) || !aligned(dsum, esz) || !aligned(x, esz) || !aligned(residual, esz) ||
+        !aligned(dx, esz) || !aligned(dresidual, esz) || !aligned(weight, 4) || !aligned(scale, 4) || !aligned(mean, 4) ||
         !aligned(rstd, 4) || !aligned(dweight, 4) || !aligned(dscale, 4) || !aligned(workspace, 16))
         return KLA_ERR_INVALID_ARG;
     const size_t par = 4ull * n;
@@ -323,16 +758,14 @@ kla_status kla_add_norm_bwd(const void *dy, const void *dsum, const void *x, con
     const size_t all = static_cast<size_t>(rows) * n * esz, stat = 4ull * rows;
     const Span outs[] = {span(dx, all), span(dresidual, all), span(dweight, par), span(dscale, par),
                          span(workspace, need)};
-    const Span ins[] = {span(dy, all), span(dsum, all), span(dscale ? x : nullptr, all), span(sum, all),
+    const Span ins[] = {span(dy, all), span(dsum, all), span(x, all), span(residual, all),
                         span(weight, par), span(scale, par), span(mean, stat), span(rstd, stat)};
     if (!apart(outs, ins)) return KLA_ERR_INVALID_ARG;
     NormArgs p{};
-    p.dy = dy; p.x = x; p.z = dsum; p.sum = sum; p.w = weight; p.l = scale; p.y = dresidual; p.y2 = dx;
-    p.mean = const_cast<float *>(mean); p.rstd = const_cast<float *>(rstd);
+    p.in[0] = x; p.in[1] = residual; p.in[2] = dy; p.in[3] = dsum; p.w = weight; p.l = scale; p.out[0] = dresidual;
+    p.out[1] = dx; p.mean = const_cast<float *>(mean); p.rstd = const_cast<float *>(rstd);
     p.rows = rows; p.groups = 1; p.n = n; p.layer = mean != nullptr;
-    const cudaError_t e = dtype == KLA_DTYPE_BF16 ? bwd<__nv_bfloat16, false>(p, dweight, dscale, cs)
-                                                  : bwd<float, false>(p, dweight, dscale, cs);
-    return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+    return run<kAddBwd>(p, dtype, dweight, dscale, dweight || dscale ? workspace : nullptr, stream);
 }
 
 }  // extern "C"

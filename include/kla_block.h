@@ -151,17 +151,18 @@ kla_status kla_add_norm_fwd(const void *x, const void *residual, const float *we
                             kla_norm_kind norm, float eps, void *stream);
 
 /*
- * Its gradients given dy, dsum (what reaches the sum from further on; NULL: nothing), the forward's
- * sum, mean (NULL: KLA_NORM_RMS) and rstd: dresidual = dsum + the norm's gradient, dx = scale
- * dresidual, dscale = sum over the rows of x dresidual (from the unrounded dresidual).
- *   x         read for dscale alone; NULL where scale is
+ * Its gradients given dy, dsum (what reaches the sum from further on; NULL: nothing), the forward's x,
+ * residual, mean (NULL: KLA_NORM_RMS) and rstd: dresidual = dsum + the norm's gradient, dx = scale
+ * dresidual, dscale = sum over the rows of x dresidual. The sum is formed again from x and residual, as
+ * a rounded one would cost dweight all but 9 of its bits: a forward call that is followed by this one
+ * does not write its sum over the residual. Equal calls give equal bits.
  *   dx        NULL where scale is: then dresidual is the gradient of x too
  *   dweight, dscale  fp32 [n] or NULL (not wanted; dscale is NULL where scale is)
  */
-kla_status kla_add_norm_bwd(const void *dy, const void *dsum, const void *x, const void *sum, const float *weight,
-                            const float *scale, const float *mean, const float *rstd, void *dx, void *dresidual,
-                            float *dweight, float *dscale, int64_t rows, int n, kla_dtype dtype, void *workspace,
-                            size_t workspace_bytes, void *stream);
+kla_status kla_add_norm_bwd(const void *dy, const void *dsum, const void *x, const void *residual,
+                            const float *weight, const float *scale, const float *mean, const float *rstd, void *dx,
+                            void *dresidual, float *dweight, float *dscale, int64_t rows, int n, kla_dtype dtype,
+                            void *workspace, size_t workspace_bytes, void *stream);
 size_t kla_add_norm_bwd_workspace_size(int64_t rows, int n, kla_dtype dtype);
 
 /* ------------------------------------------------------------------------- drafted tokens

@@ -43,6 +43,8 @@ def scan(lib, **kw):
     (dict(h0=A + 3 * M, hT=A + 3 * M + 4), 1),              # h_T over a part of h0
     (dict(st=strides(M // 4, 16, 128, 16)), 1),             # x reaches into the gate's buffer, and y's
     (dict(T=2**31 - 1), 2), (dict(T=2**31 - 65536), 2), (dict(B=1 << 20), 2),
+    (dict(T=1000, ws=None, wb=0), 1), (dict(T=1000, wb=64), 1), (dict(T=1000, ws=A + 9 * M + 8), 1),
+    (dict(T=1000, ws=A), 1),
 ])
 def test_gated_scan_fwd(lib, kw, code):
     if kw.get("st") and code == 1 and kw["st"][0] == M // 4:
@@ -127,7 +129,8 @@ def test_gated_norm(lib):
     assert b(dg=A + 5 * M) == 1 and b(dw=A + 4 * M) == 1 and b(act=5) == 1 and b(gs=8) == 1 and b(n=1) == 2
     assert lib.kla_gated_norm_bwd_workspace_size(0, 2, 32, 1, 1) == 0
     need = lib.kla_gated_norm_bwd_workspace_size(4, 2, 32, 1, 1)
-    assert need == 0 or (b(ws=None, wb=need) == 1 and b(wb=need - 1) == 1 and b(ws=A) == 1)
+    assert need > 0 and b(ws=None, wb=need) == 1 and b(wb=need - 1) == 1 and b(ws=A) == 1
+    assert b(ws=A + 8 * M + 8) == 1
 
 
 def test_add_norm(lib):
@@ -150,12 +153,12 @@ def test_add_norm(lib):
         return lib.kla_add_norm_bwd(a["dy"], a["ds"], a["x"], a["s"], a["w"], a["l"], a["m"], a["r"], a["dx"],
                                     a["dr"], a["dw"], a["dl"], a["rows"], a["n"], a["dt"], a["ws"], a["wb"], None)
     assert b(dy=None) == 1 and b(s=None) == 1 and b(r=None) == 1 and b(dr=None) == 1 and b(dx=None) == 1
-    assert b(x=None) == 1                                    # dscale without the values it is summed of
+    assert b(x=None) == 1 and b(x=None, dl=None) == 1
     assert b(l=None) == 1 and b(l=None, dx=None) == 1 and b(l=None, dl=None) == 1
     assert b(dr=A + M) == 1 and b(dx=A + 8 * M) == 1 and b(dl=A + 9 * M) == 1 and b(n=2) == 2
     assert lib.kla_add_norm_bwd_workspace_size(0, 32, 1) == 0
     need = lib.kla_add_norm_bwd_workspace_size(4, 32, 1)
-    assert need == 0 or (b(ws=None, wb=need) == 1 and b(wb=need - 1) == 1 and b(ws=A) == 1)
+    assert need > 0 and b(ws=None, wb=need) == 1 and b(wb=need - 1) == 1 and b(ws=A) == 1
 
 
 def test_verify_draft(lib):

@@ -61,7 +61,7 @@ def meta(*shape, dtype=torch.bfloat16):
     lambda: block.gated_norm_fwd(meta(3, WIDE, 32), meta(3, WIDE, 32), meta(WIDE, 32)),
     lambda: block.gated_norm_bwd(meta(3, WIDE), meta(3, WIDE), meta(3, WIDE), None, None, meta(3)),
     lambda: block.add_norm_fwd(meta(3, WIDE), meta(3, WIDE)),
-    lambda: block.add_norm_bwd(meta(3, WIDE), None, None, meta(3, WIDE), None, None, None, meta(3)),
+    lambda: block.add_norm_bwd(meta(3, WIDE), None, meta(3, WIDE), meta(3, WIDE), None, None, None, meta(3)),
     lambda: block.verify_draft(meta(1, 1), None, meta(1, 2, WIDE), meta(1, 2)),
     lambda: block.verify_draft(meta(1, WIDE), None, meta(1, WIDE, 10), meta(1, WIDE)),
     lambda: block.verify_draft(meta(WIDE, 1), None, meta(WIDE, 2, 10), meta(WIDE, 2)),
@@ -193,8 +193,8 @@ def test_calls_run_on_their_tensors_device(calls):
     kla.rotary_bwd(q, None, f)
     y, mean, rstd = kla.gated_norm_fwd(x, x)
     kla.gated_norm_bwd(x, x, x, None, mean, rstd)
-    y, total, mean, rstd = kla.add_norm_fwd(x, x)
-    kla.add_norm_bwd(x, None, None, total, None, None, mean, rstd)
+    y, _, mean, rstd = kla.add_norm_fwd(x, x)
+    kla.add_norm_bwd(x, None, x, x, None, None, mean, rstd)
     kla.verify_draft(place(torch.zeros(2, 3, dtype=torch.int32)), None, x, place(torch.zeros(2, 4)))
     assert calls == [(f"kla_{name}", 1, 101) for name in (
         "gated_scan_fwd", "gated_scan_bwd", "gated_scan_step", "rotary", "rotary", "gated_norm_fwd", "gated_norm_bwd",
