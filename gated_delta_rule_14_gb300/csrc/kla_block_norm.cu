@@ -5,6 +5,7 @@
 //   added   s = r + l x,  y = xh(s) w       dr = ds + N(dy w),  dx = l dr,  dw = sum dy xh,  dl = sum x dr
 //   xh = (x - mean) rstd, N(u) = rstd (u - mean(u) - xh mean(u xh)); without the means' terms where mean = 0 (RMS)
 #include <atomic>
+#include <cfloat>
 #include <climits>
 #include <type_traits>
 
@@ -40,26 +41,39 @@ __device__ __forceinline__ float across(float v, int off) { return __shfl_xor_sy
 __device__ __forceinline__ float2 across(float2 v, int off) { return make_float2(across(v.x, off), across(v.y, off)); }
 
 template <typename T>
-__device__ __forceinline__ float sigmoid(float z) {
-    if (sizeof(T) == 4) return 1.f / (1.f + expf(-z));
+__device__ __forceinline__ float2 sigmoid(float2 z) {
+    if (sizeof(T) == 4) return make_float2(1.f / (1.f + expf(-z.x)), 1.f / (1.f + expf(-z.y)));
     // bf16: the hardware's exponential and reciprocal, off by 2^-21 at z of 10, far below z's own 2^-9
-    float e = z * -1.4426950408889634f;
-    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e));
-    e += 1.f;
-    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e));
+    float2 e = mul2(z, both(-1.4426950408889634f));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+    e = add2(e, both(1.f));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.y));
     return e;
 }
 // act(z), and act'(z)
 template <typename T>
-__device__ __forceinline__ float activation(float z, int silu, float &slope) {
-    const float s = sigmoid<T>(z);
-    slope = silu ? s * fmaf(z, 1.f - s, 1.f) : s * (1.f - s);
-    return silu ? z * s : s;
+__device__ __forceinline__ float2 activation(float2 z, int silu) {
+    const float2 s = sigmoid<T>(z);
+    return silu ? mul2(z, s) : s;
+}
+template <typename T>
+__device__ __forceinline__ float2 activation(float2 z, int silu, float2 &slope) {
+    const float2 s = sigmoid<T>(z), rest = fma2(s, both(-1.f), both(1.f));
+    slope = mul2(s, silu ? fma2(z, rest, both(1.f)) : rest);
+    return silu ? mul2(z, s) : s;
+}
+// 1 / sqrt(v): the hardware's, off by 2^-22, and one step of Newton's iteration
+__device__ __forceinline__ float reciprocal_root(float v) {
+    const float r = rsqrtf(v);
+    return v > 0.f && v <= FLT_MAX ? fmaf(r * fmaf(-v * r, r, 1.f), 0.5f, r) : r;
 }
 
 template <int kBytes>
 __device__ __forceinline__ void copy_in(void *to, const void *from) {
-    if constexpr (kBytes == 16)
+    if constexpr (kBytes == 2) return;
+    else if constexpr (kBytes == 16)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(to)), "l"(from) : "memory");
     else
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ptx::smem_u32(to)), "l"(from) : "memory");
@@ -69,15 +83,20 @@ __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kGroups) : "memory");
 }
 
+__device__ __forceinline__ void set(float2 &v, int i, float x) { (i ? v.y : v.x) = x; }
+__device__ __forceinline__ float part(const float2 &v, int i) { return i ? v.y : v.x; }
+
 // kBytes of a row as values, and back
 template <typename T, int kBytes>
 __device__ __forceinline__ void unpack(const void *p, float *v) {
-    uint32_t r[kBytes / 4];
+    uint32_t r[(kBytes + 2) / 4];
     if constexpr (kBytes == 16) {
         const uint4 q = *static_cast<const uint4 *>(p);
         r[0] = q.x, r[1] = q.y, r[2] = q.z, r[3] = q.w;
-    } else {
+    } else if constexpr (kBytes == 4) {
         r[0] = *static_cast<const uint32_t *>(p);
+    } else {
+        v[0] = to_f32(*static_cast<const T *>(p));
     }
 #pragma unroll
     for (int i = 0; i < kBytes / 4; ++i) {
@@ -91,84 +110,104 @@ __device__ __forceinline__ void unpack(const void *p, float *v) {
 }
 template <typename T, int kBytes>
 __device__ __forceinline__ void pack(void *p, const float *v) {
-    uint32_t r[kBytes / 4];
+    uint32_t r[(kBytes + 2) / 4];
 #pragma unroll
     for (int i = 0; i < kBytes / 4; ++i)
         r[i] = sizeof(T) == 4 ? __float_as_uint(v[i]) : ptx::pack_bf16(v[2 * i], v[2 * i + 1]);
     if constexpr (kBytes == 16) *static_cast<uint4 *>(p) = make_uint4(r[0], r[1], r[2], r[3]);
-    else *static_cast<uint32_t *>(p) = r[0];
+    else if constexpr (kBytes == 4) *static_cast<uint32_t *>(p) = r[0];
+    else *static_cast<T *>(p) = from_f32<T>(v[0]);
 }
 
 // ---- rows that a team of threads holds in registers
-// A row belongs to a team of `width` threads (8 to 32 lanes of a warp, or whole warps up to the CTA), each with kNV
+// A row belongs to a team of `width` threads (4 to 32 lanes of a warp, or whole warps up to the CTA), each with kNV
 // accesses of kBytes at fixed columns, so that weights and the sums of dw and dl stay in registers. Every thread
 // copies its own values of the next kStages - 1 rows into shared memory and takes them from there: no barrier stands
-// between copy and use, and what is on its way does not cost registers. CTAs are persistent.
-constexpr int kBlock = 512;
-// of the values of a thread: how many CTAs an SM's registers and shared memory hold
-constexpr int ctas(int values) { return values <= 8 ? 2 : 1; }
-constexpr int stages(Op op, int values, int bytes) {   // bytes: of a thread's row of one input
-    const int most = 200 * 1024 / (ctas(values) * kBlock) / (inputs(op) * bytes + (backward(op) ? 8 : 0));
+// between copy and use, and what is on its way does not cost registers. CTAs are persistent. Rows that start on odd
+// bf16, which no such copy takes, and rows of which shared memory holds no two, are loaded as they are needed
+// (kDirect).
+constexpr int kMostBlock = 512;
+// Of the operation and the values of a thread: how many CTAs an SM's registers and shared memory hold.
+constexpr int ctas(Op op, int values, int block) {
+    const int of_256 = values <= 8 ? (backward(op) ? 3 : 4) : 2;
+    return block == 256 ? of_256 : of_256 / 2;
+}
+constexpr int stages(Op op, int values, int bytes, int block) {   // bytes: of a thread's row of one input
+    const int most = 200 * 1024 / (ctas(op, values, block) * block) / (inputs(op) * bytes + (backward(op) ? 8 : 0));
     return most > 6 ? 6 : most < 2 ? 2 : most;
 }
 
-template <typename T, int kBytes, int kNV, Op kOp>
-__global__ void __launch_bounds__(kBlock, ctas(kNV *kBytes / static_cast<int>(sizeof(T))))
+template <typename T, int kBytes, int kNV, Op kOp, int kBlock, bool kDirect>
+__global__ void __launch_bounds__(kBlock, ctas(kOp, kNV *kBytes / static_cast<int>(sizeof(T)), kBlock))
 block_norm_kernel(NormArgs p, int width) {
-    constexpr int kV = kBytes / sizeof(T), kE = kV * kNV, kIns = inputs(kOp);
-    constexpr int kStages = stages(kOp, kE, kNV * kBytes);
+    constexpr int kV = kBytes / sizeof(T), kE = kV * kNV, kP = kE / 2, kIns = inputs(kOp);
+    constexpr int kStages = stages(kOp, kE, kNV * kBytes, kBlock);
     constexpr bool kGated = gated(kOp), kBwd = backward(kOp);
     dependency_release();
-    extern __shared__ __align__(16) uint8_t ring[];   // [stage][input][access][thread], then [stage][thread] of stats
+    extern __shared__ __align__(16) uint8_t ring[];   // [stage][input][access][thread], then [stage][2][thread] of stats
     __shared__ float2 sums[2][kBlock / 32];
     const int team = threadIdx.x / width, lane = threadIdx.x % width, teams = kBlock / width;
     const int groups = p.w_groups ? p.groups : 1, g = blockIdx.x % groups;   // whose weights this CTA has
-    const int64_t ctas_here = gridDim.x / groups, first = static_cast<int64_t>(blockIdx.x / groups) * teams;
-    const int64_t mine = p.rows / groups, step = ctas_here * teams;
-    const int turns = first < mine ? static_cast<int>((mine - first + step - 1) / step) : 0;
+    const int first = blockIdx.x / groups * teams, mine = static_cast<int>(p.rows) / groups;
+    const int step = gridDim.x / groups * teams;
+    const int turns = first < mine ? (mine - first + step - 1) / step : 0;
     const bool four = kOp == kAddBwd && p.in[3] != nullptr;
     float *const stats = reinterpret_cast<float *>(ring + kStages * kIns * kNV * kBlock * kBytes);
     auto slot = [&](int stage, int i, int k) {
         return ring + (((stage * kIns + i) * kNV + k) * kBlock + threadIdx.x) * kBytes;
     };
-    auto row_of = [&](int turn) { return (first + team + turn * step) * groups + g; };
-    auto fetch = [&](int turn, int stage) {
-        const int64_t row = row_of(turn);
-        if (turn < turns && row < p.rows) {
+    bool there[kNV];   // columns of this thread
+#pragma unroll
+    for (int k = 0; k < kNV; ++k) there[k] = (k * width + lane) * kV < p.n;
+    // the next row to be copied, and the one at hand: their index, and the first of their values of this thread
+    const int row0 = (first + team) * groups + g, hop = step * groups, rows = static_cast<int>(p.rows);
+    const int64_t off0 = static_cast<int64_t>(row0) * p.n + lane * kV, off_hop = static_cast<int64_t>(hop) * p.n;
+    int64_t ahead = row0, ahead_off = off0;   // 64 bits: it runs past the last row
+    auto source = [&](int i, int64_t row, int64_t off) {   // this thread's first values of a row
+        if (kGated && i == 1 && p.z_stride) {
+            const unsigned r = static_cast<unsigned>(row), outer = r / static_cast<unsigned>(p.groups);
+            off = outer * p.z_stride + static_cast<int64_t>(r - outer * p.groups) * p.n + lane * kV;
+        }
+        return static_cast<const T *>(p.in[i]) + off;
+    };
+    auto fetch = [&](int stage) {
+        if (kDirect) return;
+        if (ahead < rows) {
 #pragma unroll
             for (int i = 0; i < kIns; ++i) {
                 if (i == 3 && !four) break;
-                int64_t o = row * p.n;
-                if (kGated && i == 1 && p.z_stride)
-                    o = row / p.groups * p.z_stride + row % p.groups * p.n;
-                const T *from = static_cast<const T *>(p.in[i]) + o + lane * kV;
+                const T *from = source(i, ahead, ahead_off);
 #pragma unroll
                 for (int k = 0; k < kNV; ++k)
-                    if ((k * width + lane) * kV < p.n) copy_in<kBytes>(slot(stage, i, k), from + k * width * kV);
+                    if (there[k]) copy_in<kBytes>(slot(stage, i, k), from + k * width * kV);
             }
             if (kBwd) {
-                copy_in<4>(stats + (stage * 2) * kBlock + threadIdx.x, p.rstd + row);
-                if (p.layer) copy_in<4>(stats + (stage * 2 + 1) * kBlock + threadIdx.x, p.mean + row);
+                copy_in<4>(stats + (stage * 2) * kBlock + threadIdx.x, p.rstd + ahead);
+                if (p.layer) copy_in<4>(stats + (stage * 2 + 1) * kBlock + threadIdx.x, p.mean + ahead);
             }
         }
+        ahead += hop;
+        ahead_off += off_hop;
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) fetch(i, i);
-    float w[kE], l[kGated ? 1 : kE], dw[kBwd ? kE : 1], dl[kOp == kAddBwd ? kE : 1];
+    for (int i = 0; i < kStages - 1; ++i) fetch(i);
+    float2 w[kP], l[kGated ? 1 : kP], dw[kBwd ? kP : 1], dl[kOp == kAddBwd ? kP : 1];
 #pragma unroll
     for (int u = 0; u < kE; ++u) {
         const int c = (u / kV * width + lane) * kV + u % kV;
-        w[u] = p.w && c < p.n ? p.w[static_cast<int64_t>(g) * p.n + c] : 1.f;
-        if (!kGated) l[u] = p.l && c < p.n ? p.l[c] : 1.f;
-        if (kBwd) dw[u] = 0.f;
-        if (kOp == kAddBwd) dl[u] = 0.f;
+        set(w[u / 2], u % 2, p.w && c < p.n ? p.w[static_cast<int64_t>(g) * p.n + c] : 1.f);
+        if (!kGated) set(l[u / 2], u % 2, p.l && c < p.n ? p.l[c] : 1.f);
+    }
+#pragma unroll
+    for (int u = 0; u < kP; ++u) {
+        if (kBwd) dw[u] = both(0.f);
+        if (kOp == kAddBwd) dl[u] = both(0.f);
     }
     const float inv = 1.f / p.n;
     int turn_sum = 0;
     auto sum = [&](auto v) {   // over the team; all of the CTA's threads take part in the same calls
-        const int lanes = width < 32 ? width : 32;
-        for (int off = lanes / 2; off; off >>= 1) v = add(v, across(v, off));
+        for (int off = width < 32 ? width / 2 : 16; off; off >>= 1) v = add(v, across(v, off));
         if (width > 32) {
             using V = decltype(v);
             const int warps = width / 32, at = team * warps;
@@ -180,132 +219,133 @@ block_norm_kernel(NormArgs p, int width) {
         }
         return v;
     };
-    for (int t = 0, stage = 0; t < turns; ++t) {
-        fetch(t + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
+    int64_t row = row0, off = off0;
+    for (int t = 0, stage = 0; t < turns; ++t, row += hop, off += off_hop) {
+        fetch(stage == 0 ? kStages - 1 : stage - 1);
         copies_wait<kStages - 1>();
-        const int64_t row = row_of(t);
-        const bool live = row < p.rows;
-        auto get = [&](int i, int k, float *v) {   // zeros past the row's end
-            if (live && (k * width + lane) * kV < p.n) {
-                unpack<T, kBytes>(slot(stage, i, k), v);
-            } else {
+        const bool live = row < rows;
+        auto get = [&](int i, float2 (&v)[kP]) {   // zeros past the row's end
 #pragma unroll
-                for (int e = 0; e < kV; ++e) v[e] = 0.f;
+            for (int k = 0; k < kNV; ++k) {
+                float e[kV];
+                if (live && there[k]) {
+                    if (kDirect) unpack<T, kBytes>(source(i, row, off) + k * width * kV, e);
+                    else unpack<T, kBytes>(slot(stage, i, k), e);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kV; ++j) e[j] = 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < kV; ++j) set(v[(k * kV + j) / 2], (k * kV + j) % 2, e[j]);
             }
         };
-        auto put = [&](int i, int k, const float *v) {
-            const int c = (k * width + lane) * kV;
-            if (live && c < p.n) pack<T, kBytes>(static_cast<T *>(p.out[i]) + row * p.n + c, v);
-        };
-        float x[kE];   // what the norm is of, then xh
+        auto put = [&](int i, const float2 (&v)[kP]) {
+            T *to = static_cast<T *>(p.out[i]) + off;
 #pragma unroll
-        for (int k = 0; k < kNV; ++k) {
-            get(0, k, x + k * kV);
-            if (!kGated) {
-                float r[kV];
-                get(1, k, r);
+            for (int k = 0; k < kNV; ++k) {
+                float e[kV];
 #pragma unroll
-                for (int e = 0; e < kV; ++e) x[k * kV + e] = fmaf(l[k * kV + e], x[k * kV + e], r[e]);
+                for (int j = 0; j < kV; ++j) e[j] = part(v[(k * kV + j) / 2], (k * kV + j) % 2);
+                if (live && there[k]) pack<T, kBytes>(to + k * width * kV, e);
             }
+        };
+        float2 x[kP];   // what the norm is of, then xh
+        get(0, x);
+        if (!kGated) {
+            float2 r[kP];
+            get(1, r);
+#pragma unroll
+            for (int u = 0; u < kP; ++u) x[u] = fma2(l[u], x[u], r[u]);
         }
         if constexpr (!kBwd) {
-            if (kOp == kAddFwd)
-#pragma unroll
-                for (int k = 0; k < kNV; ++k) put(1, k, x + k * kV);
+            if (kOp == kAddFwd) put(1, x);
             float mu = 0.f;
             if (p.layer) {
-                float s = 0.f;
+                float2 s = both(0.f);
 #pragma unroll
-                for (int u = 0; u < kE; ++u) s += x[u];
-                mu = sum(s) * inv;
+                for (int u = 0; u < kP; ++u) s = add2(s, x[u]);
+                mu = sum(s.x + s.y) * inv;
 #pragma unroll
-                for (int u = 0; u < kE; ++u)
-                    x[u] = (u / kV * width + lane) * kV < p.n ? x[u] - mu : 0.f;
+                for (int u = 0; u < kP; ++u) {
+                    x[u] = add2(x[u], both(-mu));
+                    if (!there[2 * u / kV]) x[u].x = 0.f;
+                    if (!there[(2 * u + 1) / kV]) x[u].y = 0.f;
+                }
             }
-            float q = 0.f;
+            float2 q = both(0.f);
 #pragma unroll
-            for (int u = 0; u < kE; ++u) q = fmaf(x[u], x[u], q);
-            const float rs = 1.f / sqrtf(sum(q) * inv + p.eps);
+            for (int u = 0; u < kP; ++u) q = fma2(x[u], x[u], q);
+            const float rs = reciprocal_root(sum(q.x + q.y) * inv + p.eps);
             if (live && lane == 0) {
                 if (p.mean) p.mean[row] = mu;
                 if (p.rstd) p.rstd[row] = rs;
             }
+            float2 z[kP];
+            if (kGated) get(1, z);
 #pragma unroll
-            for (int k = 0; k < kNV; ++k) {
-                float y[kV], z[kV];
-                if (kGated) get(1, k, z);
-#pragma unroll
-                for (int e = 0; e < kV; ++e) {
-                    y[e] = x[k * kV + e] * rs * w[k * kV + e];
-                    float slope;
-                    if (kGated) y[e] *= activation<T>(z[e], p.silu, slope);
-                }
-                put(0, k, y);
+            for (int u = 0; u < kP; ++u) {
+                x[u] = mul2(mul2(x[u], both(rs)), w[u]);
+                if (kGated) x[u] = mul2(x[u], activation<T>(z[u], p.silu));
             }
+            put(0, x);
         } else {
-            const float rs = live ? stats[(stage * 2) * kBlock + threadIdx.x] : 0.f;
-            const float mu = live && p.layer ? stats[(stage * 2 + 1) * kBlock + threadIdx.x] : 0.f;
-            float d[kE];   // dL/dxh; zero past the row's end, where nothing is added to any sum then
-            float2 s = make_float2(0.f, 0.f);
+            const float rs = !live ? 0.f : kDirect ? p.rstd[row] : stats[(stage * 2) * kBlock + threadIdx.x];
+            const float mu =
+                !live || !p.layer ? 0.f : kDirect ? p.mean[row] : stats[(stage * 2 + 1) * kBlock + threadIdx.x];
+            float2 d[kP];   // dL/dxh; zero past the row's end, where nothing is added to any sum then
+            float2 s0 = both(0.f), s1 = s0;
+            get(2, d);
+            if (kGated) {
+                float2 z[kP];
+                get(1, z);
 #pragma unroll
-            for (int k = 0; k < kNV; ++k) {
-                float dy[kV], z[kV];
-                get(2, k, dy);
-                if (kGated) get(1, k, z);
-#pragma unroll
-                for (int e = 0; e < kV; ++e) {
-                    const int u = k * kV + e;
-                    x[u] = (x[u] - mu) * rs;
-                    if (kGated) {
-                        float slope;
-                        const float a = activation<T>(z[e], p.silu, slope), dyx = dy[e] * x[u];
-                        dw[u] = fmaf(dyx, a, dw[u]);
-                        z[e] = dyx * w[u] * slope;
-                        d[u] = dy[e] * w[u] * a;
-                    } else {
-                        dw[u] = fmaf(dy[e], x[u], dw[u]);
-                        d[u] = dy[e] * w[u];
-                    }
-                    s.x += d[u];
-                    s.y = fmaf(d[u], x[u], s.y);
+                for (int u = 0; u < kP; ++u) {
+                    float2 slope;
+                    const float2 a = activation<T>(z[u], p.silu, slope);
+                    x[u] = mul2(add2(x[u], both(-mu)), both(rs));
+                    const float2 dyx = mul2(d[u], x[u]);
+                    dw[u] = fma2(dyx, a, dw[u]);
+                    z[u] = mul2(mul2(dyx, w[u]), slope);
+                    d[u] = mul2(mul2(d[u], w[u]), a);
+                    s0 = add2(s0, d[u]);
+                    s1 = fma2(d[u], x[u], s1);
                 }
-                if (kGated) put(1, k, z);
+                put(1, z);
+            } else {
+#pragma unroll
+                for (int u = 0; u < kP; ++u) {
+                    x[u] = mul2(add2(x[u], both(-mu)), both(rs));
+                    dw[u] = fma2(d[u], x[u], dw[u]);
+                    d[u] = mul2(d[u], w[u]);
+                    s0 = add2(s0, d[u]);
+                    s1 = fma2(d[u], x[u], s1);
+                }
             }
             float m1 = 0.f, m2;
             if (p.layer) {
-                s = sum(s);
-                m1 = s.x * inv;
-                m2 = s.y * inv;
+                const float2 m = sum(make_float2(s0.x + s0.y, s1.x + s1.y));
+                m1 = m.x * inv;
+                m2 = m.y * inv;
             } else {
-                m2 = sum(s.y) * inv;
+                m2 = sum(s1.x + s1.y) * inv;
             }
+            const float2 c0 = both(rs), c1 = both(-rs * m1), c2 = both(-rs * m2);
 #pragma unroll
-            for (int k = 0; k < kNV; ++k) {
-                float o[kV], r[kV];
-                if (kOp == kAddBwd) {
-                    if (four) get(3, k, r);
-                    else
+            for (int u = 0; u < kP; ++u) d[u] = fma2(c0, d[u], fma2(c2, x[u], c1));
+            if (four) {
+                get(3, x);
 #pragma unroll
-                        for (int e = 0; e < kV; ++e) r[e] = 0.f;
+                for (int u = 0; u < kP; ++u) d[u] = add2(d[u], x[u]);
+            }
+            put(0, d);
+            if (kOp == kAddBwd && p.l) {
+                get(0, x);
+#pragma unroll
+                for (int u = 0; u < kP; ++u) {
+                    dl[u] = fma2(d[u], x[u], dl[u]);
+                    d[u] = mul2(d[u], l[u]);
                 }
-#pragma unroll
-                for (int e = 0; e < kV; ++e) {
-                    const int u = k * kV + e;
-                    o[e] = rs * (d[u] - m1 - x[u] * m2);
-                    if (kOp == kAddBwd) o[e] += r[e];
-                }
-                put(0, k, o);
-                if (kOp == kAddBwd && p.l) {
-                    float v[kV];
-                    get(0, k, v);
-#pragma unroll
-                    for (int e = 0; e < kV; ++e) {
-                        const int u = k * kV + e;
-                        dl[u] = fmaf(o[e], v[e], dl[u]);
-                        o[e] *= l[u];
-                    }
-                    put(1, k, o);
-                }
+                put(1, d);
             }
         }
         stage = stage + 1 == kStages ? 0 : stage + 1;
@@ -313,24 +353,29 @@ block_norm_kernel(NormArgs p, int width) {
     if constexpr (kBwd) {
         copies_wait<0>();
         if (!p.part) return;
-        // the teams add up one after the other, so that a CTA leaves one row of each sum
+        // one row of each sum a CTA: first over the teams of a warp, which have the same columns, then over the rest
         constexpr int kSums = kOp == kAddBwd ? 2 : 1;
-        float *const acc = reinterpret_cast<float *>(ring);   // [kSums][n]
-        for (int q = 0; q < teams; ++q) {
-            __syncthreads();
-            if (team == q)
-#pragma unroll
-                for (int u = 0; u < kE; ++u) {
-                    const int c = (u / kV * width + lane) * kV + u % kV;
-                    if (c < p.n) {
-                        acc[c] = q ? acc[c] + dw[u] : dw[u];
-                        if (kSums == 2) acc[p.n + c] = q ? acc[p.n + c] + dl[u] : dl[u];
-                    }
-                }
-        }
-        __syncthreads();
+        const int owners = width < 32 ? kBlock / 32 : teams, owner = width < 32 ? threadIdx.x / 32 : team;
+        float *const acc = reinterpret_cast<float *>(ring);   // [owners][n]
         float *to = p.part + static_cast<int64_t>(blockIdx.x) * kSums * p.n;
-        for (int c = threadIdx.x; c < kSums * p.n; c += kBlock) to[c] = acc[c];
+#pragma unroll
+        for (int which = 0; which < kSums; ++which, to += p.n) {
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < kE; ++u) {
+                const float2 &pair = which ? dl[kOp == kAddBwd ? u / 2 : 0] : dw[u / 2];
+                float v = part(pair, u % 2);
+                for (int off = width; off < 32; off *= 2) v += across(v, off);
+                const int c = (u / kV * width + lane) * kV + u % kV;
+                if (c < p.n && (threadIdx.x & 31) == lane % 32) acc[owner * p.n + c] = v;
+            }
+            __syncthreads();
+            for (int c = threadIdx.x; c < p.n; c += kBlock) {
+                float v = acc[c];
+                for (int q = 1; q < owners; ++q) v += acc[q * p.n + c];
+                to[c] = v;
+            }
+        }
     }
 }
 
@@ -365,7 +410,11 @@ struct Column {
     __device__ __forceinline__ float weight(int c) const { return w ? w[c] : 1.f; }
     __device__ __forceinline__ float act(int c, float &slope) const {
         slope = 0.f;
-        return gated(kOp) ? activation<T>(in(1, oz + c), p.silu, slope) : 1.f;
+        if (!gated(kOp)) return 1.f;
+        float2 both_slopes;
+        const float a = activation<T>(both(in(1, oz + c)), p.silu, both_slopes).x;
+        slope = both_slopes.x;
+        return a;
     }
     __device__ __forceinline__ void put(int i, int c, float v) const {
         static_cast<T *>(p.out[i])[o + c] = from_f32<T>(v);
@@ -386,7 +435,7 @@ __global__ void __launch_bounds__(kAnyBlock) block_norm_any_fwd_kernel(NormArgs 
             const float d = at.value(c) - mu;
             q = fmaf(d, d, q);
         }
-        const float rs = 1.f / sqrtf(block_sum(q, slots) / p.n + p.eps);
+        const float rs = reciprocal_root(block_sum(q, slots) / p.n + p.eps);
         if (threadIdx.x == 0) {
             if (p.mean) p.mean[row] = mu;
             if (p.rstd) p.rstd[row] = rs;
@@ -513,28 +562,30 @@ bool apart(const Span (&outs)[kOuts], const Span (&ins)[kIns]) {
     return true;
 }
 
-// How rows are taken: `bytes` of an access (0: value by value), accesses of a thread, threads of a team.
+// How rows are taken: `bytes` of an access (0: by block_norm_any_*), accesses of a thread, threads of a team and of a
+// CTA.
 struct Plan {
-    int bytes, nv, width;
-    int grid;   // CTAs of the rows' kernel, a multiple of the groups with weights of their own
+    int bytes, nv, width, block;
+    int grid;   // CTAs, a multiple of the groups with weights of their own
+    bool direct() const { return bytes == 2 || nv > (bytes == 16 ? 2 : 8); }
 };
-// Rows start on `bytes` bytes. A thread holds at most kNV accesses (16 bytes: 2, 4 bytes: 8, 32 bytes either way).
-Plan plan(int64_t rows, int groups, int n, int esz, int bytes) {
-    Plan p{bytes, 0, 0, 0};
-    const int accesses = bytes ? n * esz / bytes : 0, full = bytes == 16 ? 2 : 8;
-    if (bytes == 0 || accesses > kBlock * full) {
+// Rows start on `bytes` bytes. A thread takes 32 bytes of a row, so that a row's share of the sums, the addresses and
+// the loop is spread over many values (with 16 bytes 32768 x 16 heads of 128 took 85 us instead of 78, and 124
+// instead of 120), or 64 of rows of fp32 that shared memory holds no two of.
+Plan plan(int64_t rows, int groups, int n, int esz, int bytes, Op op) {
+    Plan p{bytes, bytes == 16 ? 2 : bytes == 4 ? 8 : 16, 4, 256, 0};
+    const int accesses = n * esz / bytes;
+    if (esz == 4 && accesses > kMostBlock * p.nv) p.nv *= 2;
+    if (accesses > kMostBlock * p.nv) {
         p.bytes = 0;
         const int64_t most = kSms * 4;
         p.grid = static_cast<int>(rows < most ? rows : most);
         return p;
     }
-    // one access a thread as long as a warp holds the row so: more rows are on their way then
-    const int least = bytes == 16 ? 1 : 2;
-    p.nv = accesses <= 32 * least ? least : full;
-    p.width = 8;
     while (p.width * p.nv < accesses) p.width *= 2;
-    const int64_t teams = kBlock / p.width, of_group = (rows / groups + teams - 1) / teams;
-    int64_t want = (static_cast<int64_t>(kSms) * ctas(p.nv * bytes / esz) + groups - 1) / groups;
+    if (p.width > p.block || p.nv * bytes == 64) p.block = kMostBlock;
+    const int64_t teams = p.block / p.width, of_group = (rows / groups + teams - 1) / teams;
+    int64_t want = (static_cast<int64_t>(kSms) * ctas(op, p.nv * bytes / esz, p.block) + groups - 1) / groups;
     if (want > of_group) want = of_group;
     p.grid = static_cast<int>((want < 1 ? 1 : want) * groups);
     return p;
@@ -548,33 +599,37 @@ int any_parts(int64_t rows, int groups, int n) {
 }
 size_t any_means_bytes(int64_t rows) { return (static_cast<size_t>(rows) * sizeof(float2) + 15) / 16 * 16; }
 // Scratch of the backward pass, for whatever alignment the call has.
-size_t workspace_bytes_of(int64_t rows, int groups, int n, int esz, int sums) {
+size_t workspace_bytes_of(int64_t rows, int groups, int n, int esz, Op op) {
+    const int sums = op == kAddBwd ? 2 : 1;
     size_t most = any_means_bytes(rows) + static_cast<size_t>(any_parts(rows, groups, n)) * groups * sums * n * 4;
-    for (int bytes : {16, 4}) {
-        const Plan p = plan(rows, groups, n, esz, bytes);
+    for (int bytes : {16, 4, 2}) {
+        if (bytes < esz) continue;
+        const Plan p = plan(rows, groups, n, esz, bytes, op);
         const size_t need = p.bytes ? static_cast<size_t>(p.grid) * sums * n * 4 : 0;
         if (need > most) most = need;
     }
     return most;
 }
 
-template <typename T, int kBytes, int kNV, Op kOp>
+template <typename T, int kBytes, int kNV, Op kOp, int kBlock, bool kDirect>
 cudaError_t run_rows(const NormArgs &a, const Plan &p, cudaStream_t s) {
     constexpr int kMaxDevices = 64;
     static std::atomic<bool> done[kMaxDevices];
-    constexpr int kS = stages(kOp, kNV * kBytes / static_cast<int>(sizeof(T)), kNV * kBytes);
-    constexpr int kRing = kS * kBlock * (inputs(kOp) * kNV * kBytes + (backward(kOp) ? 8 : 0));
+    constexpr int kS = stages(kOp, kNV * kBytes / static_cast<int>(sizeof(T)), kNV * kBytes, kBlock);
+    constexpr int kSums = backward(kOp) ? kBlock * kNV * kBytes / static_cast<int>(sizeof(T)) * 4 : 0;
+    constexpr int kRing =
+        kDirect ? kSums : kS * kBlock * (inputs(kOp) * kNV * kBytes + (backward(kOp) ? 8 : 0));
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    auto kernel = block_norm_kernel<T, kBytes, kNV, kOp>;
+    auto kernel = block_norm_kernel<T, kBytes, kNV, kOp, kBlock, kDirect>;
     if (!done[dev].load(std::memory_order_acquire)) {   // once per device and kernel: the attribute outlasts the call
         if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing)) != cudaSuccess)
             return e;
         done[dev].store(true, std::memory_order_release);
     }
-    static_assert(!backward(kOp) || kRing >= 2 * kBlock * kNV * kBytes / static_cast<int>(sizeof(T)) * 4, "sums");
+    static_assert(kRing >= kSums, "a CTA's sums are joined there");
     kernel<<<p.grid, kBlock, kRing, s>>>(a, p.width);
     return cudaGetLastError();
 }
@@ -591,12 +646,24 @@ cudaError_t run(NormArgs a, float *dw, float *dl, void *workspace, cudaStream_t 
             if (!aligned(q, bytes)) return false;
         return true;
     };
-    const Plan p = plan(a.rows, groups, a.n, esz, fits(16) ? 16 : fits(4) ? 4 : 0);
+    const Plan p = plan(a.rows, groups, a.n, esz, fits(16) ? 16 : fits(4) ? 4 : 2, kOp);
     cudaError_t e;
     if (p.bytes) {
         a.part = static_cast<float *>(workspace);
-        if (p.bytes == 16) e = p.nv == 1 ? run_rows<T, 16, 1, kOp>(a, p, s) : run_rows<T, 16, 2, kOp>(a, p, s);
-        else e = p.nv == 2 ? run_rows<T, 4, 2, kOp>(a, p, s) : run_rows<T, 4, 8, kOp>(a, p, s);
+        const bool large = p.block == 512;
+        if constexpr (sizeof(T) == 4) {
+            if (p.direct())
+                e = p.bytes == 16 ? run_rows<T, 16, 4, kOp, 512, true>(a, p, s) : run_rows<T, 4, 16, kOp, 512, true>(a, p, s);
+        } else {
+            if (p.direct())
+                e = large ? run_rows<T, 2, 16, kOp, 512, true>(a, p, s) : run_rows<T, 2, 16, kOp, 256, true>(a, p, s);
+        }
+        if (p.direct()) {
+        } else if (large) {
+            e = p.bytes == 16 ? run_rows<T, 16, 2, kOp, 512, false>(a, p, s) : run_rows<T, 4, 8, kOp, 512, false>(a, p, s);
+        } else {
+            e = p.bytes == 16 ? run_rows<T, 16, 2, kOp, 256, false>(a, p, s) : run_rows<T, 4, 8, kOp, 256, false>(a, p, s);
+        }
         if (e != cudaSuccess || !workspace) return e;
         return launch_dependent(block_norm_join_kernel, dim3((a.n + 31) / 32, groups), 1024, 0, s, a.part, dw, dl,
                                 p.grid / groups, groups, a.n, kSums);
@@ -663,7 +730,8 @@ kla_status kla_gated_norm_fwd(const void *x, const void *gate, int64_t gate_stri
 
 size_t kla_gated_norm_bwd_workspace_size(int64_t rows, int groups, int n, kla_dtype dtype, int weight_groups) {
     if (kla::check(rows, groups, n, dtype) != KLA_OK || rows == 0) return 0;
-    return kla::workspace_bytes_of(rows * groups, weight_groups ? groups : 1, n, dtype == KLA_DTYPE_BF16 ? 2 : 4, 1);
+    return kla::workspace_bytes_of(rows * groups, weight_groups ? groups : 1, n, dtype == KLA_DTYPE_BF16 ? 2 : 4,
+                                   kla::kGatedBwd);
 }
 
 kla_status kla_gated_norm_bwd(const void *dy, const void *x, const void *gate, int64_t gate_stride,
@@ -728,7 +796,7 @@ kla_status kla_add_norm_fwd(const void *x, const void *residual, const float *we
 
 size_t kla_add_norm_bwd_workspace_size(int64_t rows, int n, kla_dtype dtype) {
     if (kla::check(rows, 1, n, dtype) != KLA_OK || rows == 0) return 0;
-    return kla::workspace_bytes_of(rows, 1, n, dtype == KLA_DTYPE_BF16 ? 2 : 4, 2);
+    return kla::workspace_bytes_of(rows, 1, n, dtype == KLA_DTYPE_BF16 ? 2 : 4, kla::kAddBwd);
 }
 
 kla_status kla_add_norm_bwd(const void *dy, const void *dsum, const void *x, const void *residual,
