@@ -87,24 +87,23 @@ __device__ __forceinline__ void set(float2 &v, int i, float x) { (i ? v.y : v.x)
 __device__ __forceinline__ float part(const float2 &v, int i) { return i ? v.y : v.x; }
 
 // kBytes of a row as values, and back
+template <int kBytes>
+struct alignas(kBytes) Raw {
+    typename std::conditional<kBytes == 2, uint16_t, uint32_t>::type r[kBytes == 2 ? 1 : kBytes / 4];
+};
 template <typename T, int kBytes>
-__device__ __forceinline__ void unpack(const void *p, float *v) {
-    uint32_t r[(kBytes + 2) / 4];
-    if constexpr (kBytes == 16) {
-        const uint4 q = *static_cast<const uint4 *>(p);
-        r[0] = q.x, r[1] = q.y, r[2] = q.z, r[3] = q.w;
-    } else if constexpr (kBytes == 4) {
-        r[0] = *static_cast<const uint32_t *>(p);
+__device__ __forceinline__ void unpack(const Raw<kBytes> &raw, float *v) {
+    if constexpr (kBytes == 2) {
+        v[0] = __uint_as_float(static_cast<uint32_t>(raw.r[0]) << 16);
     } else {
-        v[0] = to_f32(*static_cast<const T *>(p));
-    }
 #pragma unroll
-    for (int i = 0; i < kBytes / 4; ++i) {
-        if (sizeof(T) == 4) {
-            v[i] = __uint_as_float(r[i]);
-        } else {
-            v[2 * i] = __uint_as_float(r[i] << 16);
-            v[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
+        for (int i = 0; i < kBytes / 4; ++i) {
+            if (sizeof(T) == 4) {
+                v[i] = __uint_as_float(raw.r[i]);
+            } else {
+                v[2 * i] = __uint_as_float(raw.r[i] << 16);
+                v[2 * i + 1] = __uint_as_float(raw.r[i] & 0xffff0000u);
+            }
         }
     }
 }
@@ -225,16 +224,19 @@ block_norm_kernel(NormArgs p, int width) {
         copies_wait<kStages - 1>();
         const bool live = row < rows;
         auto get = [&](int i, float2 (&v)[kP]) {   // zeros past the row's end
+            Raw<kBytes> raw[kNV];
+            const T *from = kDirect ? source(i, row, off) : nullptr;
+#pragma unroll
+            for (int k = 0; k < kNV; ++k) {   // all loads before the first use
+                raw[k] = Raw<kBytes>{};
+                if (live && there[k])
+                    raw[k] = kDirect ? *reinterpret_cast<const Raw<kBytes> *>(from + k * width * kV)
+                                     : *reinterpret_cast<const Raw<kBytes> *>(slot(stage, i, k));
+            }
 #pragma unroll
             for (int k = 0; k < kNV; ++k) {
                 float e[kV];
-                if (live && there[k]) {
-                    if (kDirect) unpack<T, kBytes>(source(i, row, off) + k * width * kV, e);
-                    else unpack<T, kBytes>(slot(stage, i, k), e);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < kV; ++j) e[j] = 0.f;
-                }
+                unpack<T, kBytes>(raw[k], e);
 #pragma unroll
                 for (int j = 0; j < kV; ++j) set(v[(k * kV + j) / 2], (k * kV + j) % 2, e[j]);
             }
@@ -258,6 +260,8 @@ block_norm_kernel(NormArgs p, int width) {
             for (int u = 0; u < kP; ++u) x[u] = fma2(l[u], x[u], r[u]);
         }
         if constexpr (!kBwd) {
+            float2 z[kP];
+            if (kGated && kDirect) get(1, z);   // its trip beside the first sum's
             if (kOp == kAddFwd) put(1, x);
             float mu = 0.f;
             if (p.layer) {
@@ -280,8 +284,7 @@ block_norm_kernel(NormArgs p, int width) {
                 if (p.mean) p.mean[row] = mu;
                 if (p.rstd) p.rstd[row] = rs;
             }
-            float2 z[kP];
-            if (kGated) get(1, z);
+            if (kGated && !kDirect) get(1, z);
 #pragma unroll
             for (int u = 0; u < kP; ++u) {
                 x[u] = mul2(mul2(x[u], both(rs)), w[u]);
@@ -292,6 +295,12 @@ block_norm_kernel(NormArgs p, int width) {
             const float rs = !live ? 0.f : kDirect ? p.rstd[row] : stats[(stage * 2) * kBlock + threadIdx.x];
             const float mu =
                 !live || !p.layer ? 0.f : kDirect ? p.mean[row] : stats[(stage * 2 + 1) * kBlock + threadIdx.x];
+            constexpr bool kEarly = kOp == kAddBwd && kDirect && kE <= 8;   // what is used after the sums, asked for here
+            float2 x0[kEarly ? kP : 1], ds[kEarly ? kP : 1];
+            if constexpr (kEarly) {
+                get(0, x0);
+                if (four) get(3, ds);
+            }
             float2 d[kP];   // dL/dxh; zero past the row's end, where nothing is added to any sum then
             float2 s0 = both(0.f), s1 = s0;
             get(2, d);
@@ -333,16 +342,16 @@ block_norm_kernel(NormArgs p, int width) {
 #pragma unroll
             for (int u = 0; u < kP; ++u) d[u] = fma2(c0, d[u], fma2(c2, x[u], c1));
             if (four) {
-                get(3, x);
+                if constexpr (!kEarly) get(3, x);
 #pragma unroll
-                for (int u = 0; u < kP; ++u) d[u] = add2(d[u], x[u]);
+                for (int u = 0; u < kP; ++u) d[u] = add2(d[u], kEarly ? ds[kEarly ? u : 0] : x[u]);
             }
             put(0, d);
             if (kOp == kAddBwd && p.l) {
-                get(0, x);
+                if constexpr (!kEarly) get(0, x);
 #pragma unroll
                 for (int u = 0; u < kP; ++u) {
-                    dl[u] = fma2(d[u], x[u], dl[u]);
+                    dl[u] = fma2(d[u], kEarly ? x0[kEarly ? u : 0] : x[u], dl[u]);
                     d[u] = mul2(d[u], l[u]);
                 }
                 put(1, d);
@@ -573,9 +582,9 @@ struct Plan {
 // the loop is spread over many values (with 16 bytes 32768 x 16 heads of 128 took 85 us instead of 78, and 124
 // instead of 120), or 64 of rows of fp32 that shared memory holds no two of.
 Plan plan(int64_t rows, int groups, int n, int esz, int bytes, Op op) {
-    Plan p{bytes, bytes == 16 ? 2 : bytes == 4 ? 8 : 16, 4, 256, 0};
+    Plan p{bytes, bytes == 16 ? 2 : 8, 4, 256, 0};
     const int accesses = n * esz / bytes;
-    if (esz == 4 && accesses > kMostBlock * p.nv) p.nv *= 2;
+    if ((esz == 4 || bytes == 2) && accesses > kMostBlock * p.nv) p.nv *= 2;
     if (accesses > kMostBlock * p.nv) {
         p.bytes = 0;
         const int64_t most = kSms * 4;
@@ -583,7 +592,7 @@ Plan plan(int64_t rows, int groups, int n, int esz, int bytes, Op op) {
         return p;
     }
     while (p.width * p.nv < accesses) p.width *= 2;
-    if (p.width > p.block || p.nv * bytes == 64) p.block = kMostBlock;
+    if (p.width > p.block || p.nv == (bytes == 16 ? 4 : 16)) p.block = kMostBlock;
     const int64_t teams = p.block / p.width, of_group = (rows / groups + teams - 1) / teams;
     int64_t want = (static_cast<int64_t>(kSms) * ctas(op, p.nv * bytes / esz, p.block) + groups - 1) / groups;
     if (want > of_group) want = of_group;
@@ -656,7 +665,9 @@ cudaError_t run(NormArgs a, float *dw, float *dl, void *workspace, cudaStream_t 
                 e = p.bytes == 16 ? run_rows<T, 16, 4, kOp, 512, true>(a, p, s) : run_rows<T, 4, 16, kOp, 512, true>(a, p, s);
         } else {
             if (p.direct())
-                e = large ? run_rows<T, 2, 16, kOp, 512, true>(a, p, s) : run_rows<T, 2, 16, kOp, 256, true>(a, p, s);
+                e = !large      ? run_rows<T, 2, 8, kOp, 256, true>(a, p, s)
+                    : p.nv == 8 ? run_rows<T, 2, 8, kOp, 512, true>(a, p, s)
+                                : run_rows<T, 2, 16, kOp, 512, true>(a, p, s);
         }
         if (p.direct()) {
         } else if (large) {
