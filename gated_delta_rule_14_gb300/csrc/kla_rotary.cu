@@ -4,6 +4,8 @@
 // position in integers, whose overflow is whole turns. Its upper 32 bits, as a signed number of half turns, are what
 // sine and cosine take. The product in fp32 would lose a bit with every doubling of the position, and one in fp64
 // would cost tens of instructions of a pipe that does two a cycle and SM.
+#include <type_traits>
+
 #include "layer_dev.cuh"
 #include "../../include/kla_block.h"
 
@@ -29,55 +31,168 @@ __device__ __forceinline__ unsigned long long turn_rate(float freq) {
     t -= floor(t);
     return static_cast<unsigned long long>(t * 18446744073709551616.0);
 }
-__device__ __forceinline__ void angle(unsigned long long rate, long long position, float &s, float &c) {
-    const int half_turns = static_cast<int>((rate * static_cast<unsigned long long>(position)) >> 32);
-    sincospif(static_cast<float>(half_turns) * 0x1p-31f, &s, &c);
-}
-__device__ __forceinline__ long long position_of(const RotaryArgs &p, int64_t token) {
-    if (!p.positions) return token % p.T;
-    return p.wide ? static_cast<const long long *>(p.positions)[token] : static_cast<const int *>(p.positions)[token];
+// Sine and cosine of the angle at a position. bf16 takes the hardware's, whose 2^-20 of error in [-pi, pi] is far
+// below the values' 2^-9.
+template <typename T>
+__device__ __forceinline__ void turned(unsigned long long rate, long long position, float &s, float &c) {
+    const float half_turns =
+        static_cast<float>(static_cast<int>((rate * static_cast<unsigned long long>(position)) >> 32)) * 0x1p-31f;
+    if (sizeof(T) == 4) {
+        sincospif(half_turns, &s, &c);
+    } else {
+        const float a = half_turns * 3.14159265358979f;
+        asm("sin.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(a));
+        asm("cos.approx.ftz.f32 %0, %1;" : "=f"(c) : "f"(a));
+    }
 }
 
-// A CTA per token: every thread takes pairs of all heads.
-template <typename T, bool kHalf>
-__global__ void rotary_kernel(RotaryArgs p) {
-    extern __shared__ float2 turn[];   // cos, sin
-    const int64_t token = blockIdx.x;
-    const int pairs = p.rot / 2;
-    const long long at = position_of(p, token);
-    for (int i = threadIdx.x; i < pairs; i += blockDim.x) {
-        float s, c;
-        angle(turn_rate(p.freqs[i]), at, s, c);
-        turn[i] = make_float2(p.scale * c, p.inverse ? -p.scale * s : p.scale * s);
-    }
-    __syncthreads();
-    const int units = pairs + p.d - p.rot;   // pairs, then single values that are copied
-    const int64_t b = token / p.T, t = token % p.T;
+// kV neighbouring values, moved in one access.
+template <typename T, int kV>
+struct alignas(sizeof(T) * kV) Values {
+    static constexpr int kBytes = sizeof(T) * kV;
+    typename std::conditional<kBytes == 2, uint16_t, uint32_t>::type r[kBytes == 2 ? 1 : kBytes / 4];
+    __device__ __forceinline__ void get(float *v) const {
+        if constexpr (kBytes == 2) {
+            v[0] = __uint_as_float(static_cast<uint32_t>(r[0]) << 16);
+        } else if constexpr (sizeof(T) == 2) {
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
-        for (int i = threadIdx.x; i < p.H[m] * units; i += blockDim.x) {
-            const int head = i / units, u = i % units;
-            const T *x = static_cast<const T *>(p.in[m]) + b * p.is[m][0] + t * p.is[m][1] + head * p.is[m][2];
-            T *y = static_cast<T *>(p.out[m]) + b * p.os[m][0] + t * p.os[m][1] + head * p.os[m][2];
-            if (u < pairs) {
-                const int i0 = kHalf ? u : 2 * u, i1 = kHalf ? u + pairs : 2 * u + 1;
-                const float a = to_f32(x[i0]), v = to_f32(x[i1]);
-                const float2 r = turn[u];
-                y[i0] = from_f32<T>(fmaf(a, r.x, -v * r.y));
-                y[i1] = from_f32<T>(fmaf(v, r.x, a * r.y));
-            } else {
-                y[u + pairs] = x[u + pairs];
+            for (int i = 0; i < kBytes / 4; ++i) {
+                v[2 * i] = __uint_as_float(r[i] << 16);
+                v[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kV; ++i) v[i] = __uint_as_float(r[i]);
+        }
+    }
+    __device__ __forceinline__ void set(const float *v) {
+        if constexpr (kBytes == 2) {
+            r[0] = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
+        } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int i = 0; i < kBytes / 4; ++i) r[i] = ptx::pack_bf16(v[2 * i], v[2 * i + 1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kV; ++i) r[i] = __float_as_uint(v[i]);
+        }
+    }
+};
+
+// A warp takes tokens one after the other (or, where tokens are few, a part of one's heads). A lane has one unit of a
+// head, two accesses of kV values: kV pairs, whose sines and cosines it takes once for all of its heads, or values that
+// are copied. kAtOnce heads are on their way at once, the first of them while the sines are taken. Of the 64-bit rates
+// the CTA makes one table, as fp64 is slow.
+constexpr int kBlock = 256, kAtOnce = 4;
+constexpr int ctas(int bytes) { return bytes == 16 ? 3 : 4; }   // an SM's registers hold
+template <typename T, int kV, bool kHalf>
+__global__ void __launch_bounds__(kBlock, ctas(sizeof(T) * kV)) rotary_kernel(RotaryArgs p, int parts) {
+    using X = Values<T, kV>;
+    extern __shared__ unsigned long long rates[];
+    const int pairs = p.rot / 2, lane = threadIdx.x & 31, heads = p.H[0] + p.H[1];
+    for (int i = threadIdx.x; i < pairs; i += kBlock) rates[i] = turn_rate(p.freqs[i]);
+    __syncthreads();
+    const int turning = pairs / kV, rest = (p.d - p.rot) / kV, units = turning + (rest + 1) / 2;
+    const int across = units < 32 ? units : 32, side = 32 / across;   // lanes of a head, heads side by side
+    const int lane_u = lane % across, lane_h = lane / across;
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kBlock / 32), jobs = p.tokens * parts;
+    for (int64_t job = static_cast<int64_t>(blockIdx.x) * (kBlock / 32) + threadIdx.x / 32; job < jobs; job += warps) {
+        const unsigned token = static_cast<unsigned>(job / parts), slice = static_cast<unsigned>(job % parts);
+        const unsigned b = token / static_cast<unsigned>(p.T), t = token - b * p.T;
+        const long long at = !p.positions ? t
+                             : p.wide     ? static_cast<const long long *>(p.positions)[token]
+                                          : static_cast<const int *>(p.positions)[token];
+        const T *in0 = static_cast<const T *>(p.in[0]) + b * p.is[0][0] + t * p.is[0][1];
+        const T *in1 = static_cast<const T *>(p.in[1]) + b * p.is[1][0] + t * p.is[1][1] - p.H[0] * p.is[1][2];
+        T *out0 = static_cast<T *>(p.out[0]) + b * p.os[0][0] + t * p.os[0][1];
+        T *out1 = static_cast<T *>(p.out[1]) + b * p.os[1][0] + t * p.os[1][1] - p.H[0] * p.os[1][2];
+        if (lane_h >= side) continue;
+        const int h0 = slice * side + lane_h, hop = side * parts;   // this lane's heads
+        for (int u = lane_u; u < units; u += across) {
+            const bool turns = u < turning;
+            const int i0 = turns ? (kHalf ? 1 : 2) * u * kV : p.rot + 2 * (u - turning) * kV;
+            const int i1 = turns && kHalf ? i0 + pairs : i0 + kV;
+            const bool two = turns || 2 * (u - turning) + 1 < rest;
+            X x0[kAtOnce], x1[kAtOnce];
+            auto load = [&](int h) {
+#pragma unroll
+                for (int q = 0; q < kAtOnce; ++q, h += hop) {
+                    const bool first = h < p.H[0];
+                    const T *f = (first ? in0 : in1) + h * (first ? p.is[0][2] : p.is[1][2]);
+                    if (h < heads) x0[q] = *reinterpret_cast<const X *>(f + i0);
+                    if (h < heads && two) x1[q] = *reinterpret_cast<const X *>(f + i1);
+                }
+            };
+            if (h0 < heads) load(h0);
+            float c[kV], s[kV];
+            if (turns)
+#pragma unroll
+                for (int j = 0; j < kV; ++j) {
+                    turned<T>(rates[u * kV + j], at, s[j], c[j]);
+                    c[j] *= p.scale;
+                    s[j] *= p.inverse ? -p.scale : p.scale;
+                }
+            for (int h = h0; h < heads; h += hop * kAtOnce) {
+                if (h != h0) load(h);
+#pragma unroll
+                for (int q = 0; q < kAtOnce; ++q) {
+                    const int hq = h + q * hop;
+                    if (turns) {
+                        float v[2 * kV];
+                        x0[q].get(v);
+                        x1[q].get(v + kV);
+#pragma unroll
+                        for (int j = 0; j < kV; ++j) {   // pair j: values j and kV + j, or 2 j and 2 j + 1
+                            float &a = v[kHalf ? j : 2 * j], &e = v[kHalf ? kV + j : 2 * j + 1];
+                            const float old = a;
+                            a = fmaf(old, c[j], -e * s[j]);
+                            e = fmaf(e, c[j], old * s[j]);
+                        }
+                        x0[q].set(v);
+                        x1[q].set(v + kV);
+                    }
+                    const bool first = hq < p.H[0];
+                    T *o = (first ? out0 : out1) + hq * (first ? p.os[0][2] : p.os[1][2]);
+                    if (hq < heads) *reinterpret_cast<X *>(o + i0) = x0[q];
+                    if (hq < heads && two) *reinterpret_cast<X *>(o + i1) = x1[q];
+                }
             }
         }
+    }
 }
 
-template <typename T>
+template <typename T, int kV>
 cudaError_t run(const RotaryArgs &p, bool half, cudaStream_t s) {
-    const unsigned grid = static_cast<unsigned>(p.tokens);
-    const size_t smem = p.rot / 2 * sizeof(float2);
-    if (half) rotary_kernel<T, true><<<grid, 256, smem, s>>>(p);
-    else rotary_kernel<T, false><<<grid, 256, smem, s>>>(p);
+    constexpr int kSms = 152, kWarps = kBlock / 32, kCtas = ctas(sizeof(T) * kV);
+    const int units = p.rot / 2 / kV + ((p.d - p.rot) / kV + 1) / 2, side = units >= 32 ? 1 : 32 / units;
+    const int heads = p.H[0] + p.H[1];
+    // few tokens: a token's heads over several warps, as long as there are SMs without one
+    int64_t parts = static_cast<int64_t>(kSms) * kWarps / p.tokens;
+    const int most = (heads + side - 1) / side;
+    parts = parts < 1 ? 1 : parts > most ? most : parts;
+    int64_t grid = (p.tokens * parts + kWarps - 1) / kWarps;
+    if (grid > kSms * kCtas) grid = kSms * kCtas;
+    const size_t smem = p.rot / 2 * sizeof(unsigned long long);
+    if (half) rotary_kernel<T, kV, true><<<static_cast<unsigned>(grid), kBlock, smem, s>>>(p, static_cast<int>(parts));
+    else rotary_kernel<T, kV, false><<<static_cast<unsigned>(grid), kBlock, smem, s>>>(p, static_cast<int>(parts));
     return cudaGetLastError();
+}
+// By the widest access that every head's start and both parts of it allow.
+template <typename T>
+cudaError_t run(const RotaryArgs &p, int B, bool half, cudaStream_t s) {
+    constexpr int kFull = 16 / sizeof(T);
+    auto fits = [&](int v) {
+        if (p.rot / 2 % v || (p.d - p.rot) % v) return false;
+        const int size[2][3] = {{B, p.T, p.H[0]}, {B, p.T, p.H[1]}};
+        for (int m = 0; m < 2; ++m) {
+            if (!aligned(p.in[m], v * sizeof(T)) || !aligned(p.out[m], v * sizeof(T))) return false;
+            for (int a = 0; a < 3; ++a)
+                if (size[m][a] > 1 && (p.is[m][a] % v || p.os[m][a] % v)) return false;
+        }
+        return true;
+    };
+    if (fits(kFull)) return run<T, kFull>(p, half, s);
+    if (sizeof(T) == 2 && fits(2)) return run<T, sizeof(T) == 2 ? 2 : 1>(p, half, s);
+    return run<T, 1>(p, half, s);
 }
 
 }  // namespace
@@ -148,6 +263,6 @@ extern "C" kla_status kla_rotary(const void *q, const void *k, void *q_out, void
     p.inverse = inverse != 0;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const bool half = layout == KLA_ROTARY_HALF;
-    const cudaError_t e = dtype == KLA_DTYPE_BF16 ? run<__nv_bfloat16>(p, half, cs) : run<float>(p, half, cs);
+    const cudaError_t e = dtype == KLA_DTYPE_BF16 ? run<__nv_bfloat16>(p, B, half, cs) : run<float>(p, B, half, cs);
     return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
 }
