@@ -80,101 +80,183 @@ struct alignas(sizeof(T) * kV) Values {
 
 // A warp takes tokens one after the other (or, where tokens are few, a part of one's heads). A lane has one unit of a
 // head, two accesses of kV values: kV pairs, whose sines and cosines it takes once for all of its heads, or values that
-// are copied. kAtOnce heads are on their way at once, the first of them while the sines are taken. Of the 64-bit rates
-// the CTA makes one table, as fp64 is slow.
-constexpr int kBlock = 256, kAtOnce = 4;
-constexpr int ctas(int bytes) { return bytes == 16 ? 3 : 4; }   // an SM's registers hold
-template <typename T, int kV, bool kHalf>
+// are copied. kAtOnce heads are on their way at once, the first of them while the sines are taken. Where a warp's
+// lanes hold all heads of a token (kTokens), it is as many tokens that are on their way at once, each with sines of its
+// own. Of the 64-bit rates the CTA makes one table, as fp64 is slow.
+constexpr int kBlock = 256;
+constexpr int at_once(int bytes, bool tokens) { return bytes == 16 || tokens ? 4 : 8; }
+constexpr int ctas(int bytes) { return bytes >= 8 ? 3 : 4; }   // an SM's registers hold
+// The units of a head, lanes of it and heads side by side in a warp.
+struct Units {
+    int turning, rest, all, across, side;
+    __host__ __device__ Units(int d, int rot, int v) {
+        turning = rot / 2 / v;
+        rest = (d - rot) / v;
+        all = turning + (rest + 1) / 2;
+        across = all < 32 ? all : 32;
+        side = 32 / across;
+    }
+};
+template <typename T, int kV, bool kHalf, bool kTokens>
 __global__ void __launch_bounds__(kBlock, ctas(sizeof(T) * kV)) rotary_kernel(RotaryArgs p, int parts) {
     using X = Values<T, kV>;
+    constexpr int kAtOnce = at_once(sizeof(T) * kV, kTokens);
     extern __shared__ unsigned long long rates[];
     const int pairs = p.rot / 2, lane = threadIdx.x & 31, heads = p.H[0] + p.H[1];
     for (int i = threadIdx.x; i < pairs; i += kBlock) rates[i] = turn_rate(p.freqs[i]);
     __syncthreads();
-    const int turning = pairs / kV, rest = (p.d - p.rot) / kV, units = turning + (rest + 1) / 2;
-    const int across = units < 32 ? units : 32, side = 32 / across;   // lanes of a head, heads side by side
-    const int lane_u = lane % across, lane_h = lane / across;
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kBlock / 32), jobs = p.tokens * parts;
-    for (int64_t job = static_cast<int64_t>(blockIdx.x) * (kBlock / 32) + threadIdx.x / 32; job < jobs; job += warps) {
-        const unsigned token = static_cast<unsigned>(job / parts), slice = static_cast<unsigned>(job % parts);
-        const unsigned b = token / static_cast<unsigned>(p.T), t = token - b * p.T;
-        const long long at = !p.positions ? t
-                             : p.wide     ? static_cast<const long long *>(p.positions)[token]
-                                          : static_cast<const int *>(p.positions)[token];
-        const T *in0 = static_cast<const T *>(p.in[0]) + b * p.is[0][0] + t * p.is[0][1];
-        const T *in1 = static_cast<const T *>(p.in[1]) + b * p.is[1][0] + t * p.is[1][1] - p.H[0] * p.is[1][2];
-        T *out0 = static_cast<T *>(p.out[0]) + b * p.os[0][0] + t * p.os[0][1];
-        T *out1 = static_cast<T *>(p.out[1]) + b * p.os[1][0] + t * p.os[1][1] - p.H[0] * p.os[1][2];
-        if (lane_h >= side) continue;
-        const int h0 = slice * side + lane_h, hop = side * parts;   // this lane's heads
-        for (int u = lane_u; u < units; u += across) {
-            const bool turns = u < turning;
-            const int i0 = turns ? (kHalf ? 1 : 2) * u * kV : p.rot + 2 * (u - turning) * kV;
-            const int i1 = turns && kHalf ? i0 + pairs : i0 + kV;
-            const bool two = turns || 2 * (u - turning) + 1 < rest;
+    const Units n(p.d, p.rot, kV);
+    const int lane_u = lane % n.across, lane_h = lane / n.across;
+    // kTokens: `side` of a warp's tokens side by side, and this lane's head and place among them
+    const int side = kTokens ? n.side / heads : n.side, head = lane_h % heads, place = lane_h / heads;
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kBlock / 32);
+    const int64_t first_job = static_cast<int64_t>(blockIdx.x) * (kBlock / 32) + threadIdx.x / 32;
+    // of a token and a head: position, and element offsets of its values
+    auto position = [&](unsigned token) -> long long {
+        if (!p.positions) return token % static_cast<unsigned>(p.T);
+        return p.wide ? static_cast<const long long *>(p.positions)[token] : static_cast<const int *>(p.positions)[token];
+    };
+    auto angles = [&](int u, long long at, float (&c)[kV], float (&s)[kV]) {
+#pragma unroll
+        for (int j = 0; j < kV; ++j) {
+            turned<T>(rates[u * kV + j], at, s[j], c[j]);
+            c[j] *= p.scale;
+            s[j] *= p.inverse ? -p.scale : p.scale;
+        }
+    };
+    auto turn = [&](X &x0, X &x1, const float (&c)[kV], const float (&s)[kV]) {
+        float v[2 * kV];
+        x0.get(v);
+        x1.get(v + kV);
+#pragma unroll
+        for (int j = 0; j < kV; ++j) {   // pair j: values j and kV + j, or 2 j and 2 j + 1
+            float &a = v[kHalf ? j : 2 * j], &e = v[kHalf ? kV + j : 2 * j + 1];
+            const float old = a;
+            a = fmaf(old, c[j], -e * s[j]);
+            e = fmaf(e, c[j], old * s[j]);
+        }
+        x0.set(v);
+        x1.set(v + kV);
+    };
+    struct Unit {   // its two accesses
+        bool turns, two;
+        int i0, i1;
+    };
+    auto unit = [&](int u) {
+        Unit r;
+        r.turns = u < n.turning;
+        r.i0 = r.turns ? (kHalf ? 1 : 2) * u * kV : p.rot + 2 * (u - n.turning) * kV;
+        r.i1 = r.turns && kHalf ? r.i0 + pairs : r.i0 + kV;
+        r.two = r.turns || 2 * (u - n.turning) + 1 < n.rest;
+        return r;
+    };
+    if constexpr (kTokens) {
+        const int m = head < p.H[0] ? 0 : 1;
+        const int64_t per = static_cast<int64_t>(side) * kAtOnce, jobs = (p.tokens + per - 1) / per;
+        const T *in = static_cast<const T *>(p.in[m]) + (m ? head - p.H[0] : head) * p.is[m][2];
+        T *out = static_cast<T *>(p.out[m]) + (m ? head - p.H[0] : head) * p.os[m][2];
+        if (place >= side) return;
+        const Unit w = unit(lane_u);
+        for (int64_t job = first_job; job < jobs; job += warps) {
             X x0[kAtOnce], x1[kAtOnce];
-            auto load = [&](int h) {
+            long long at[kAtOnce];
 #pragma unroll
-                for (int q = 0; q < kAtOnce; ++q, h += hop) {
-                    const bool first = h < p.H[0];
-                    const T *f = (first ? in0 : in1) + h * (first ? p.is[0][2] : p.is[1][2]);
-                    if (h < heads) x0[q] = *reinterpret_cast<const X *>(f + i0);
-                    if (h < heads && two) x1[q] = *reinterpret_cast<const X *>(f + i1);
+            for (int q = 0; q < kAtOnce; ++q) {
+                const int64_t token = job * per + q * side + place;
+                if (token >= p.tokens) continue;
+                const unsigned b = static_cast<unsigned>(token) / static_cast<unsigned>(p.T);
+                const unsigned t = static_cast<unsigned>(token) - b * p.T;
+                const T *f = in + b * p.is[m][0] + t * p.is[m][1];
+                at[q] = position(static_cast<unsigned>(token));
+                x0[q] = *reinterpret_cast<const X *>(f + w.i0);
+                if (w.two) x1[q] = *reinterpret_cast<const X *>(f + w.i1);
+            }
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q) {
+                const int64_t token = job * per + q * side + place;
+                if (token >= p.tokens) continue;
+                if (w.turns) {
+                    float c[kV], s[kV];
+                    angles(lane_u, at[q], c, s);
+                    turn(x0[q], x1[q], c, s);
                 }
-            };
-            if (h0 < heads) load(h0);
-            float c[kV], s[kV];
-            if (turns)
+                const unsigned b = static_cast<unsigned>(token) / static_cast<unsigned>(p.T);
+                const unsigned t = static_cast<unsigned>(token) - b * p.T;
+                T *o = out + b * p.os[m][0] + t * p.os[m][1];
+                *reinterpret_cast<X *>(o + w.i0) = x0[q];
+                if (w.two) *reinterpret_cast<X *>(o + w.i1) = x1[q];
+            }
+        }
+    } else {
+        const int64_t jobs = p.tokens * parts;
+        if (lane_h >= side) return;
+        for (int64_t job = first_job; job < jobs; job += warps) {
+            const unsigned token = static_cast<unsigned>(job / parts), slice = static_cast<unsigned>(job % parts);
+            const unsigned b = token / static_cast<unsigned>(p.T), t = token - b * p.T;
+            const long long at = position(token);
+            const T *in0 = static_cast<const T *>(p.in[0]) + b * p.is[0][0] + t * p.is[0][1];
+            const T *in1 = static_cast<const T *>(p.in[1]) + b * p.is[1][0] + t * p.is[1][1] - p.H[0] * p.is[1][2];
+            T *out0 = static_cast<T *>(p.out[0]) + b * p.os[0][0] + t * p.os[0][1];
+            T *out1 = static_cast<T *>(p.out[1]) + b * p.os[1][0] + t * p.os[1][1] - p.H[0] * p.os[1][2];
+            const int h0 = slice * side + lane_h, hop = side * parts;   // this lane's heads
+            for (int u = lane_u; u < n.all; u += n.across) {
+                const Unit w = unit(u);
+                X x0[kAtOnce], x1[kAtOnce];
+                auto load = [&](int h) {
 #pragma unroll
-                for (int j = 0; j < kV; ++j) {
-                    turned<T>(rates[u * kV + j], at, s[j], c[j]);
-                    c[j] *= p.scale;
-                    s[j] *= p.inverse ? -p.scale : p.scale;
-                }
-            for (int h = h0; h < heads; h += hop * kAtOnce) {
-                if (h != h0) load(h);
-#pragma unroll
-                for (int q = 0; q < kAtOnce; ++q) {
-                    const int hq = h + q * hop;
-                    if (turns) {
-                        float v[2 * kV];
-                        x0[q].get(v);
-                        x1[q].get(v + kV);
-#pragma unroll
-                        for (int j = 0; j < kV; ++j) {   // pair j: values j and kV + j, or 2 j and 2 j + 1
-                            float &a = v[kHalf ? j : 2 * j], &e = v[kHalf ? kV + j : 2 * j + 1];
-                            const float old = a;
-                            a = fmaf(old, c[j], -e * s[j]);
-                            e = fmaf(e, c[j], old * s[j]);
-                        }
-                        x0[q].set(v);
-                        x1[q].set(v + kV);
+                    for (int q = 0; q < kAtOnce; ++q, h += hop) {
+                        const bool first = h < p.H[0];
+                        const T *f = (first ? in0 : in1) + h * (first ? p.is[0][2] : p.is[1][2]);
+                        if (h < heads) x0[q] = *reinterpret_cast<const X *>(f + w.i0);
+                        if (h < heads && w.two) x1[q] = *reinterpret_cast<const X *>(f + w.i1);
                     }
-                    const bool first = hq < p.H[0];
-                    T *o = (first ? out0 : out1) + hq * (first ? p.os[0][2] : p.os[1][2]);
-                    if (hq < heads) *reinterpret_cast<X *>(o + i0) = x0[q];
-                    if (hq < heads && two) *reinterpret_cast<X *>(o + i1) = x1[q];
+                };
+                if (h0 < heads) load(h0);
+                float c[kV], s[kV];
+                if (w.turns) angles(u, at, c, s);
+                for (int h = h0; h < heads; h += hop * kAtOnce) {
+                    if (h != h0) load(h);
+#pragma unroll
+                    for (int q = 0; q < kAtOnce; ++q) {
+                        const int hq = h + q * hop;
+                        if (w.turns) turn(x0[q], x1[q], c, s);
+                        const bool first = hq < p.H[0];
+                        T *o = (first ? out0 : out1) + hq * (first ? p.os[0][2] : p.os[1][2]);
+                        if (hq < heads) *reinterpret_cast<X *>(o + w.i0) = x0[q];
+                        if (hq < heads && w.two) *reinterpret_cast<X *>(o + w.i1) = x1[q];
+                    }
                 }
             }
         }
     }
 }
 
-template <typename T, int kV>
-cudaError_t run(const RotaryArgs &p, bool half, cudaStream_t s) {
-    constexpr int kSms = 152, kWarps = kBlock / 32, kCtas = ctas(sizeof(T) * kV);
-    const int units = p.rot / 2 / kV + ((p.d - p.rot) / kV + 1) / 2, side = units >= 32 ? 1 : 32 / units;
+template <typename T, int kV, bool kHalf>
+cudaError_t run(const RotaryArgs &p, cudaStream_t s) {
+    constexpr int kSms = 152, kWarps = kBlock / 32, kCtas = ctas(sizeof(T) * kV), kAtOnce = 4;
+    const Units n(p.d, p.rot, kV);
     const int heads = p.H[0] + p.H[1];
+    // A warp's lanes hold all of a token's heads, and there are tokens enough for every warp to have several: 32 x 1024
+    // tokens of 2 heads of 128 bf16 took 31 us with one token at a time.
+    const bool tokens = n.all <= 32 && heads <= n.side &&
+                        p.tokens >= static_cast<int64_t>(kSms) * kWarps * (n.side / heads) * kAtOnce / 2;
     // few tokens: a token's heads over several warps, as long as there are SMs without one
-    int64_t parts = static_cast<int64_t>(kSms) * kWarps / p.tokens;
-    const int most = (heads + side - 1) / side;
+    int64_t parts = static_cast<int64_t>(kSms) * kWarps / p.tokens, jobs;
+    const int most = (heads + n.side - 1) / n.side;
     parts = parts < 1 ? 1 : parts > most ? most : parts;
-    int64_t grid = (p.tokens * parts + kWarps - 1) / kWarps;
+    if (tokens) jobs = (p.tokens + n.side / heads * kAtOnce - 1) / (n.side / heads * kAtOnce);
+    else jobs = p.tokens * parts;
+    int64_t grid = (jobs + kWarps - 1) / kWarps;
     if (grid > kSms * kCtas) grid = kSms * kCtas;
     const size_t smem = p.rot / 2 * sizeof(unsigned long long);
-    if (half) rotary_kernel<T, kV, true><<<static_cast<unsigned>(grid), kBlock, smem, s>>>(p, static_cast<int>(parts));
-    else rotary_kernel<T, kV, false><<<static_cast<unsigned>(grid), kBlock, smem, s>>>(p, static_cast<int>(parts));
+    const unsigned g = static_cast<unsigned>(grid);
+    if (tokens) rotary_kernel<T, kV, kHalf, true><<<g, kBlock, smem, s>>>(p, 1);
+    else rotary_kernel<T, kV, kHalf, false><<<g, kBlock, smem, s>>>(p, static_cast<int>(parts));
     return cudaGetLastError();
+}
+template <typename T, int kV>
+cudaError_t run(const RotaryArgs &p, bool half, cudaStream_t s) {
+    return half ? run<T, kV, true>(p, s) : run<T, kV, false>(p, s);
 }
 // By the widest access that every head's start and both parts of it allow.
 template <typename T>
@@ -191,6 +273,7 @@ cudaError_t run(const RotaryArgs &p, int B, bool half, cudaStream_t s) {
         return true;
     };
     if (fits(kFull)) return run<T, kFull>(p, half, s);
+    if (sizeof(T) == 2 && fits(4)) return run<T, sizeof(T) == 2 ? 4 : 1>(p, half, s);
     if (sizeof(T) == 2 && fits(2)) return run<T, sizeof(T) == 2 ? 2 : 1>(p, half, s);
     return run<T, 1>(p, half, s);
 }

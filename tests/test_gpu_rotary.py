@@ -69,6 +69,15 @@ def test_sizes_and_packed_projections(B, T, H, K, layout, packed):
     check(B, T, H, K, 128, 128, layout, torch.bfloat16, seed=T, packed=packed)
 
 
+@pytest.mark.parametrize("H,K,d,rot", [(1, 1, 128, 128), (1, 0, 128, 128), (3, 1, 64, 64), (2, 1, 64, 30), (1, 1, 32, 8),
+                                       (2, 1, 7, 6), (1, 0, 96, 0), (1, 1, 40, 20)])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_many_tokens_of_few_heads(H, K, d, rot, layout, dtype):
+    """A warp's lanes hold all heads of several tokens then, the last of them in part."""
+    check(3, 6007, H, K, d, rot, layout, dtype, seed=H, packed=True)
+
+
 @pytest.mark.parametrize("kind", [torch.int32, torch.int64])
 def test_positions(kind):
     """Given positions, far ones and negative ones among them: whole turns cost no bits. At 2^31 the frequency's own
