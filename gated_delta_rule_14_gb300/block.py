@@ -5,7 +5,9 @@ residual (``gated_norm_fwd``, ``gated_norm_bwd``, ``add_norm_fwd``, ``add_norm_b
 tokens (``verify_draft``).
 
 The binding checks and marshals; every operation runs in this package's CUDA kernels on the current stream of the
-tensors' device, whether or not that device is the current one.
+tensors' device, whether or not that device is the current one. Small calls are bound by the host, so the functions first
+ask in one expression whether everything is as it should be, and only where it is not go through the arguments one by one
+to name the one at fault or to take what strides they have.
 """
 from __future__ import annotations
 
@@ -23,6 +25,7 @@ _MODES = {"sigmoid": _native.KLA_SCAN_SIGMOID, "log": _native.KLA_SCAN_LOG}
 _LAYOUTS = {"half": _native.KLA_ROTARY_HALF, "interleaved": _native.KLA_ROTARY_INTERLEAVED}
 _NORMS = {"rms": _native.KLA_NORM_RMS, "layer": _native.KLA_NORM_LAYER}
 _ACTS = {"silu": _native.KLA_ACT_SILU, "sigmoid": _native.KLA_ACT_SIGMOID}
+_POSITIONS = {torch.int32: 0, torch.int64: 1}
 SCAN_SPAN = 128   # tokens between the states that gated_scan_fwd keeps for gated_scan_bwd
 
 
@@ -43,14 +46,23 @@ def _dense_last(*tensors) -> None:
 
 
 def _scan_shapes(x, gate, lengths):
-    device = _device("x", x)
-    code = _code("x", x)
-    if x.dim() != 3:
-        raise ValueError("x and gate must be [B, T, C]")
-    _check("gate", gate, x.shape, x.dtype, device, False)
+    """Sizes of the call, and whether x and gate are contiguous."""
+    try:
+        shape, dtype, at = x.shape, x.dtype, x.get_device()
+        dense = (at >= 0 and len(shape) == 3 and gate.shape == shape and gate.dtype is dtype and dtype in _CODE and
+                 gate.get_device() == at and x.is_contiguous() and gate.is_contiguous())
+    except AttributeError:
+        dense = False
+    if not dense:
+        device = _device("x", x)
+        _code("x", x)
+        if x.dim() != 3:
+            raise ValueError("x and gate must be [B, T, C]")
+        _check("gate", gate, x.shape, x.dtype, device, False)
+    device = x.device
     if lengths is not None:
-        _check("lengths", lengths, x.shape[:1], torch.int32, device)
-    return device, code, x.shape
+        _check("lengths", lengths, shape[:1], torch.int32, device)
+    return device, _CODE[dtype], shape, dense
 
 
 def gated_scan_workspace_size(B: int, T: int, C: int, dtype: torch.dtype = torch.bfloat16) -> int:
@@ -70,16 +82,16 @@ def gated_scan_fwd(x: torch.Tensor, gate: torch.Tensor, h0: Optional[torch.Tenso
     their outputs are 0. Returns (y = h [B,T,C] in x's dtype, h_T fp32 [B,C] or None, what ``gated_scan_bwd`` needs
     with ``states``, else None); ``h_T`` may be passed, and may be ``h0``.
     """
-    device, code, (B, T, C) = _scan_shapes(x, gate, lengths)
+    device, code, (B, T, C), dense = _scan_shapes(x, gate, lengths)
     mode = _choice("mode", _MODES, mode)
     strides = None
-    if not (x.is_contiguous() and gate.is_contiguous()):
+    if not dense:
         _dense_last(x, gate)
         strides = _Strides4(*x.stride()[:2], *gate.stride()[:2])
     if h0 is not None:
         _check("h0", h0, (B, C), _F32, device)
     if out is None:
-        out = torch.empty((B, T, C), dtype=x.dtype, device=device)
+        out = torch.empty_like(x) if dense else torch.empty((B, T, C), dtype=x.dtype, device=device)
     else:
         _check("out", out, (B, T, C), x.dtype, device)
     if h_T is not None:
@@ -103,11 +115,11 @@ def gated_scan_bwd(x: torch.Tensor, gate: torch.Tensor, dy: torch.Tensor, states
     """Gradients of ``gated_scan_fwd`` run with the same inputs, mode and lengths, given its ``states``, dy = dL/dy
     and dh_T = dL/dh_T. Returns dx and dgate [B,T,C] in x's dtype (zero at masked tokens) and dh0 fp32 [B,C] (None
     unless ``want_dh0``)."""
-    device, code, (B, T, C) = _scan_shapes(x, gate, lengths)
+    device, code, (B, T, C), dense = _scan_shapes(x, gate, lengths)
     mode = _choice("mode", _MODES, mode)
     _check("dy", dy, x.shape, x.dtype, device, False)
     strides = None
-    if not (x.is_contiguous() and gate.is_contiguous() and dy.is_contiguous()):
+    if not (dense and dy.is_contiguous()):
         _dense_last(x, gate, dy)
         strides = _Strides6(*x.stride()[:2], *gate.stride()[:2], *dy.stride()[:2])
     _check("states", states, (B, -(-T // SCAN_SPAN), C), _F32, device)
@@ -129,24 +141,33 @@ def gated_scan_step(x: torch.Tensor, gate: torch.Tensor, h: torch.Tensor, *, mod
                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """One token for B sequences of ``gated_scan_fwd``'s recurrence. x, gate: [B,C] (rows may be slices of a packed
     projection); h: fp32 [B,C], updated in place. Returns y [B,C]."""
-    device = _device("x", x)
-    code = _code("x", x)
-    if x.dim() != 2:
-        raise ValueError("x and gate must be [B, C]")
-    B, C = x.shape
-    if B > _MOST or C > _MOST:
-        _refuse("kla_gated_scan_step", _native.KLA_ERR_UNSUPPORTED)
-    _check("gate", gate, x.shape, x.dtype, device, False)
-    _dense_last(x, gate)
-    _check("h", h, (B, C), _F32, device)
+    try:
+        shape, dtype, at = x.shape, x.dtype, x.get_device()
+        B, C = shape
+        ok = (at >= 0 and gate.shape == shape and gate.dtype is dtype and gate.get_device() == at and dtype in _CODE and
+              x.is_contiguous() and gate.is_contiguous() and h.shape == shape and h.dtype is _F32 and
+              h.get_device() == at and h.is_contiguous() and 0 < B <= _MOST and 0 < C <= _MOST)
+    except (AttributeError, ValueError):
+        ok = False
+    xs = gs = C if ok else 0
+    if not ok:
+        device = _device("x", x)
+        _code("x", x)
+        if x.dim() != 2:
+            raise ValueError("x and gate must be [B, C]")
+        if B > _MOST or C > _MOST:
+            _refuse("kla_gated_scan_step", _native.KLA_ERR_UNSUPPORTED)
+        _check("gate", gate, shape, dtype, device, False)
+        _dense_last(x, gate)
+        _check("h", h, (B, C), _F32, device)
+        xs, gs = (x.stride(0), gate.stride(0)) if B > 1 else (C, C)   # one row may have any stride
+    device = x.device
     if out is None:
-        out = torch.empty((B, C), dtype=x.dtype, device=device)
+        out = torch.empty_like(x) if ok else torch.empty((B, C), dtype=dtype, device=device)
     else:
-        _check("out", out, (B, C), x.dtype, device)
-    # one row may have any stride
-    xs, gs = (x.stride(0), gate.stride(0)) if B > 1 else (C, C)
+        _check("out", out, (B, C), dtype, device)
     st = _native.on(device).kla_gated_scan_step(x.data_ptr(), xs, gate.data_ptr(), gs, h.data_ptr(), out.data_ptr(),
-                                                B, C, code, _choice("mode", _MODES, mode), _stream(device))
+                                                B, C, _CODE[dtype], _choice("mode", _MODES, mode), _stream(device))
     if st:
         _native.check(st, "kla_gated_scan_step")
     return out
@@ -192,50 +213,68 @@ def rotary_freqs(rot: int, base: float = 10000.0, *, scaling: Optional[str] = No
     return freqs.to(_F32).to(device), scale
 
 
-def _rotary(entry, q, k, freqs, positions, layout, scale, out_q, out_k, inverse):
-    device = _device("q", q)
-    code = _code("q", q)
-    layout = _choice("layout", _LAYOUTS, layout)
-    if q.dim() != 4:
-        raise ValueError("q and k must be [B, T, H, d]")
-    B, T, H, d = q.shape
-    if max(q.shape) > _MOST:
-        _refuse(entry, _native.KLA_ERR_UNSUPPORTED)
-    Hk = 0
-    if k is not None:
-        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+def _rotary_shapes(entry, q, k, freqs, positions):
+    """Sizes of the call, and whether q and k are contiguous."""
+    try:
+        shape, dtype, at = q.shape, q.dtype, q.get_device()
+        B, T, H, d = shape
+        ok = (at >= 0 and dtype in _CODE and q.is_contiguous() and freqs.dtype is _F32 and len(freqs.shape) == 1 and
+              freqs.get_device() == at and freqs.is_contiguous() and 2 * freqs.shape[0] <= d and max(shape) <= _MOST and
+              (positions is None or (positions.dtype in _POSITIONS and positions.shape == shape[:2] and
+                                     positions.get_device() == at and positions.is_contiguous())))
+        if k is not None:
+            kshape = k.shape
+            Hk = kshape[2]
+            ok = (ok and k.dtype is dtype and kshape == (B, T, Hk, d) and k.get_device() == at and k.is_contiguous() and
+                  Hk <= _MOST)
+        else:
+            Hk = 0
+    except (AttributeError, ValueError, IndexError):
+        ok = False
+    if not ok:
+        device = _device("q", q)
+        _code("q", q)
+        if q.dim() != 4 or (k is not None and (not isinstance(k, torch.Tensor) or k.dim() != 4)):
             raise ValueError("q and k must be [B, T, H, d]")
-        Hk = k.shape[2]
-        if Hk > _MOST:
+        Hk = 0 if k is None else k.shape[2]
+        if max(q.shape) > _MOST or Hk > _MOST:
             _refuse(entry, _native.KLA_ERR_UNSUPPORTED)
-        _check("k", k, (B, T, Hk, d), q.dtype, device, False)
-    if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
-        raise ValueError("freqs must be [rot / 2]")
-    _check("freqs", freqs, freqs.shape, _F32, device)
-    if 2 * freqs.shape[0] > d:
-        _refuse(entry, _native.KLA_ERR_INVALID_ARG)
-    if positions is not None:
-        if positions.dtype not in (torch.int32, torch.int64):
-            raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
-        _check("positions", positions, (B, T), positions.dtype, device)
+        if k is not None:
+            _check("k", k, (B, T, Hk, d), dtype, device, False)
+        if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
+            raise ValueError("freqs must be [rot / 2]")
+        _check("freqs", freqs, freqs.shape, _F32, device)
+        if 2 * freqs.shape[0] > d:
+            _refuse(entry, _native.KLA_ERR_INVALID_ARG)
+        if positions is not None:
+            if positions.dtype not in _POSITIONS:
+                raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
+            _check("positions", positions, (B, T), positions.dtype, device)
+    return B, T, H, Hk, d, ok
 
-    def output(name, x, out):
-        if x is None:
-            return None
-        if out is None:
-            return torch.empty(x.shape, dtype=x.dtype, device=device)
-        _check(name, out, x.shape, x.dtype, device, False)
-        return out
-    out_q, out_k = output("out_q", q, out_q), output("out_k", k, out_k)
-    tensors = [t for t in (q, k, out_q, out_k) if t is not None]
+
+def _rotary_out(name, x, out, dense):
+    if out is None:
+        return torch.empty_like(x) if dense else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _check(name, out, x.shape, x.dtype, x.device, False)
+    return out
+
+
+def _rotary(entry, q, k, freqs, positions, layout, scale, out_q, out_k, inverse):
+    B, T, H, Hk, d, dense = _rotary_shapes(entry, q, k, freqs, positions)
+    layout = _choice("layout", _LAYOUTS, layout)
+    device = q.device
+    given = out_q is not None or out_k is not None
+    out_q = _rotary_out("out_q", q, out_q, dense)
+    out_k = None if k is None else _rotary_out("out_k", k, out_k, dense)
     strides = None
-    if not all(t.is_contiguous() for t in tensors):
-        _dense_last(*tensors)
+    if not dense or given:
+        _dense_last(*(t for t in (q, k, out_q, out_k) if t is not None))
         strides = _Strides12(*(s for t in (q, k, out_q, out_k) for s in ((0, 0, 0) if t is None else t.stride()[:3])))
     st = _native.on(device).kla_rotary(
         q.data_ptr(), _ptr(k), out_q.data_ptr(), _ptr(out_k), strides, freqs.data_ptr(), _ptr(positions),
-        int(positions is not None and positions.dtype == torch.int64), B, T, H, Hk, d, 2 * freqs.shape[0], layout,
-        code, scale, inverse, _stream(device))
+        0 if positions is None else _POSITIONS[positions.dtype], B, T, H, Hk, d, 2 * freqs.shape[0], layout,
+        _CODE[q.dtype], scale, inverse, _stream(device))
     if st:
         _native.check(st, entry)
     return out_q, out_k
@@ -288,17 +327,25 @@ def _heads(x, gate, weight):
 
 
 def _norm_inputs(entry, x, gate, weight):
-    device = _device("x", x)
-    code = _code("x", x)
-    if not x.is_contiguous():
-        raise ValueError("x must be contiguous")
-    _check("gate", gate, x.shape, x.dtype, device, False)
+    try:
+        all_of, dtype, at = x.shape, x.dtype, x.get_device()
+        ok = (at >= 0 and dtype in _CODE and gate.shape == all_of and gate.dtype is dtype and
+              gate.get_device() == at and x.is_contiguous())
+    except AttributeError:
+        ok = False
+    if not ok:
+        device = _device("x", x)
+        _code("x", x)
+        if not x.is_contiguous():
+            raise ValueError("x must be contiguous")
+        _check("gate", gate, x.shape, x.dtype, device, False)
+    device = x.device
     rows, groups, n, own, stride, shape = _heads(x, gate, weight)
     if n > _MOST or groups > _MOST:
         _refuse(entry, _native.KLA_ERR_UNSUPPORTED)
     if weight is not None:
         _check("weight", weight, shape, _F32, device)
-    return device, code, rows, groups, n, own, stride, shape
+    return device, _CODE[dtype], rows, groups, n, own, stride, shape
 
 
 def _stats(x, layer, wanted, device):
@@ -354,19 +401,27 @@ def gated_norm_bwd(dy: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, weight
 
 
 def _added_inputs(entry, x, residual, weight, scale):
-    device = _device("residual", residual)
-    code = _code("residual", residual)
-    if residual.dim() < 1:
-        raise ValueError("residual must have an axis to normalise")
-    n = residual.shape[-1]
+    try:
+        all_of, dtype, at = residual.shape, residual.dtype, residual.get_device()
+        ok = (at >= 0 and dtype in _CODE and len(all_of) > 0 and residual.is_contiguous() and x.shape == all_of and
+              x.dtype is dtype and x.get_device() == at and x.is_contiguous())
+    except AttributeError:
+        ok = False
+    if not ok:
+        device = _device("residual", residual)
+        _code("residual", residual)
+        if residual.dim() < 1:
+            raise ValueError("residual must have an axis to normalise")
+        _check("residual", residual, residual.shape, residual.dtype, device)
+        _check("x", x, residual.shape, residual.dtype, device)
+    device, n = residual.device, all_of[-1]
     if n > _MOST:
         _refuse(entry, _native.KLA_ERR_UNSUPPORTED)
-    _check("residual", residual, residual.shape, residual.dtype, device)
-    _check("x", x, residual.shape, residual.dtype, device)
-    for label, t in (("weight", weight), ("scale", scale)):
-        if t is not None:
-            _check(label, t, (n,), _F32, device)
-    return device, code, residual.numel() // max(1, n), n
+    if weight is not None:
+        _check("weight", weight, (n,), _F32, device)
+    if scale is not None:
+        _check("scale", scale, (n,), _F32, device)
+    return device, _CODE[dtype], residual.numel() // max(1, n), n
 
 
 def add_norm_fwd(x: torch.Tensor, residual: torch.Tensor, weight: Optional[torch.Tensor] = None,
@@ -448,29 +503,44 @@ def verify_draft(draft: torch.Tensor, draft_probs: Optional[torch.Tensor], targe
     states runs on over ``accepted + 1`` tokens (the last one of before and the accepted drafts): ``linear_fwd`` and
     ``gated_scan_fwd`` take those as their ``lengths``.
     """
-    device = _device("target_probs", target_probs)
-    code = _code("target_probs", target_probs)
-    if target_probs.dim() != 3 or target_probs.shape[1] < 1:
-        raise ValueError("target_probs must be [B, K + 1, V]")
-    B, rows, V = target_probs.shape
-    K = rows - 1
-    if max(B, rows, V) > _MOST:
-        _refuse("kla_verify_draft", _native.KLA_ERR_UNSUPPORTED)
-    _check("draft", draft, (B, K), torch.int32, device)
-    _check("uniforms", uniforms, (B, rows), _F32, device)
-    _dense_last(target_probs)
-    qs = (K * V, V)
-    if draft_probs is not None:
-        _check("draft_probs", draft_probs, (B, K, V), target_probs.dtype, device, False)
-        _dense_last(draft_probs)
-        qs = draft_probs.stride()[:2]
+    try:
+        shape, dtype, at = target_probs.shape, target_probs.dtype, target_probs.get_device()
+        B, rows, V = shape
+        K = rows - 1
+        ok = (at >= 0 and dtype in _CODE and rows > 0 and target_probs.is_contiguous() and max(shape) <= _MOST and
+              draft.shape == (B, K) and draft.dtype is torch.int32 and draft.get_device() == at and
+              draft.is_contiguous() and uniforms.shape == (B, rows) and uniforms.dtype is _F32 and
+              uniforms.get_device() == at and uniforms.is_contiguous() and
+              (draft_probs is None or (draft_probs.shape == (B, K, V) and draft_probs.dtype is dtype and
+                                       draft_probs.get_device() == at and draft_probs.is_contiguous())))
+    except (AttributeError, ValueError):
+        ok = False
+    strides = None
+    if not ok:
+        device = _device("target_probs", target_probs)
+        _code("target_probs", target_probs)
+        if target_probs.dim() != 3 or target_probs.shape[1] < 1:
+            raise ValueError("target_probs must be [B, K + 1, V]")
+        if max(shape) > _MOST:
+            _refuse("kla_verify_draft", _native.KLA_ERR_UNSUPPORTED)
+        _check("draft", draft, (B, K), torch.int32, device)
+        _check("uniforms", uniforms, (B, rows), _F32, device)
+        _dense_last(target_probs)
+        qs = (K * V, V)
+        if draft_probs is not None:
+            _check("draft_probs", draft_probs, (B, K, V), dtype, device, False)
+            _dense_last(draft_probs)
+            qs = draft_probs.stride()[:2]
+        strides = _Strides4(*qs, *target_probs.stride()[:2])
+    device = target_probs.device
     if lengths is not None:
         _check("lengths", lengths, (B,), torch.int32, device)
     accepted = torch.empty((B,), dtype=torch.int32, device=device)
     tokens = torch.empty((B, rows), dtype=torch.int32, device=device)
     st = _native.on(device).kla_verify_draft(
-        draft.data_ptr(), _ptr(draft_probs), target_probs.data_ptr(), _Strides4(*qs, *target_probs.stride()[:2]),
-        uniforms.data_ptr(), _ptr(lengths), accepted.data_ptr(), tokens.data_ptr(), B, K, V, code, _stream(device))
+        draft.data_ptr(), _ptr(draft_probs), target_probs.data_ptr(), strides,
+        uniforms.data_ptr(), _ptr(lengths), accepted.data_ptr(), tokens.data_ptr(), B, K, V, _CODE[dtype],
+        _stream(device))
     if st:
         _native.check(st, "kla_verify_draft")
     return accepted, tokens
