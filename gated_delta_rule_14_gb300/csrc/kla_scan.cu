@@ -455,8 +455,16 @@ __global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(ScanArgs p) {
         }
 }
 
-// Tokens of a thread, warps of a CTA and CTAs of an SM.
-constexpr int kFwdTok = 32, kFwdWarps = 8, kFwdCtas = 2, kBwdTok = 16, kBwdWarps = 8, kBwdCtas = 2;
+// Tokens of a thread, warps at them and CTAs of an SM. Each side of the choice at 8 x 4096 x 2048 bf16 and, in fp32, 8 x
+// 2048 x 2048, us: forward 32 tokens x 8 warps x 2 CTAs 82 and 102, 16 x 8 x 3 89 and 95; backward 16 x 8 x 2 138 and 181,
+// 16 x 4 x 4 134 and 179, but 609 instead of 525 at 1 x 131072 x 2048, whose chain gets twice as long (all before the
+// backward pass had its warp for the chain).
+struct Shape {
+    int tok, warps, ctas;
+    constexpr int tile() const { return tok * warps; }
+};
+constexpr Shape fwd_shape(int esz, bool ring) { return ring && esz == 2 ? Shape{32, 8, 2} : Shape{16, 8, 3}; }
+constexpr Shape bwd_shape() { return Shape{16, 8, 2}; }
 
 // ---- tiles through shared memory: rows of 128 bytes (64 channels of bf16, 32 of fp32), 4 bytes a lane
 constexpr int kRow = 128;
@@ -584,8 +592,8 @@ __device__ __forceinline__ void by_full(bool full, F f) {
 
 // As above, with tiles one after the other: while a CTA waits for the state that enters one and writes its outputs, the
 // next one's rows are on their way.
-template <typename T, bool kLog, int kTok, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps, kFwdCtas) scan_fwd_ring_kernel(ScanArgs p, bool wide) {
+template <typename T, bool kLog, int kTok, int kWarps, int kCtas>
+__global__ void __launch_bounds__(32 * kWarps, kCtas) scan_fwd_ring_kernel(ScanArgs p, bool wide) {
     using L = Lane<T, kLog, false>;
     using V = typename L::V;
     constexpr int kTile = kTok * kWarps, kV = L::kV, kWidth = 32 * kV;
@@ -596,6 +604,7 @@ __global__ void __launch_bounds__(32 * kWarps, kFwdCtas) scan_fwd_ring_kernel(Sc
     uint8_t *const mine = buf + warp * kTok * kRow;
     uint8_t *const gates = mine + 2 * kTile * kRow;
     Turns turns(p);
+    if (p.head) dependency_wait();
     auto fetch = [&](unsigned ticket, int stage) {
         const Tile at(p, ticket, kWidth);
         const int t0 = at.at * kTile + warp * kTok, m = min(valid_tokens(p, at.b) - t0, kTok);
@@ -690,21 +699,108 @@ __global__ void __launch_bounds__(32 * kWarps, kFwdCtas) scan_fwd_ring_kernel(Sc
     }
 }
 
-template <typename T, bool kLog, int kTok, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps, kBwdCtas) scan_bwd_ring_kernel(ScanArgs p, bool wide) {
+// The backward pass has a warp for the chain beside those for the tokens (138 -> 122 us at 8 x 4096 x 2048; the forward
+// pass needs its registers more and lost by it, 82 -> 87). Barriers: `maps` completes when every warp has left the map of
+// its tokens, `carry` when what enters them is there; next[i] when the ticket of the tile after one of parity i is.
+template <typename V, int kWarps>
+struct Shared {
+    V a[2][kWarps][32], h[2][kWarps][32], d[kWarps][32];
+    V enter[kWarps][32];
+    unsigned ticket[2];
+    uint64_t maps, carry, next[2];
+};
+constexpr uint32_t kWaits = 400000;   // of 20 us at most, more than `entering` takes to give up
+
+template <typename L, int kWarps>
+__device__ __forceinline__ void carry_warp(const ScanArgs &p, Shared<typename L::V, kWarps> &sh, Turns &turns,
+                                           unsigned ticket, int tile_tokens) {
+    using V = typename L::V;
+    constexpr int kV = L::kV;
+    using namespace ptx;
+    const int lane = threadIdx.x & 31;
+    const uint32_t b_maps = smem_u32(&sh.maps), b_carry = smem_u32(&sh.carry), b_next = smem_u32(sh.next);
+    for (unsigned i = 0; ticket < turns.total; ++i) {
+        const Tile at(p, ticket, 32 * kV);
+        const int b = at.b, c = at.c0 + lane * kV, n = valid_tokens(p, b), tile = p.tiles - 1 - at.at;
+        const int last = n > 0 ? (n - 1) / tile_tokens : 0;
+        const bool live = c < p.C;
+        uint2 *here = p.carry + (static_cast<int64_t>(b) * p.tiles + tile) * p.C + c;
+        turns.now = ticket;
+        unsigned next = 0;
+        auto ask = [&] {   // and let the others fetch that tile
+            if (lane == 0) {
+                next = turns.ask();
+                sh.ticket[i & 1] = next;
+                mbar_arrive(b_next + 8 * (i & 1));
+            }
+            next = __shfl_sync(0xffffffffu, next, 0);
+        };
+        if (i > 0) ask();   // of a CTA's first tile later: other CTAs may not have one yet
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(b_maps, i & 1, kWaits))) {
+            give_up(p);
+            return;
+        }
+        if (i == 0) ask();
+        if (tile <= last) {
+            V pa = L::all(1.f), pd = L::all(0.f), after_a[kWarps], after_d[kWarps];   // the maps of later tokens
+#pragma unroll
+            for (int w = kWarps - 1; w >= 0; --w) {
+                after_a[w] = pa;
+                after_d[w] = pd;
+                const V a = sh.a[i & 1][w][lane];
+                pd = L::fma(a, pd, sh.d[w][lane]);
+                pa = L::mul(pa, a);
+            }
+            float in[kV];
+            if (tile == last) {
+                start<kV>(p, b, c, live, in);
+            } else {
+                if (live && tile > 0) tell_map<kV>(here, parts(pa), parts(pd));
+                if (!entering<kV>(here + p.C, p.C, last - tile, live, p.head, in)) give_up(p);
+            }
+            const V e = whole<kV>(in), out = L::fma(pa, e, pd);
+            if (live && tile > 0) tell_state<kV>(here, parts(out));
+            else if (live) finish<kV>(p, b, c, parts(out));
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) sh.enter[w][lane] = L::fma(after_a[w], e, after_d[w]);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_carry);
+        ticket = next;
+    }
+}
+
+template <typename T, bool kLog, int kTok, int kWarps, int kCtas>
+__global__ void __launch_bounds__(32 * (kWarps + 1), kCtas) scan_bwd_ring_kernel(ScanArgs p, bool wide) {
+    using namespace ptx;
     using L = Lane<T, kLog, true>;
     using V = typename L::V;
     constexpr int kTile = kTok * kWarps, kV = L::kV, kWidth = 32 * kV;
     static_assert(kTile == KLA_SCAN_SPAN, "");
     extern __shared__ __align__(128) uint8_t buf[];   // x and dy twice, gate once: kTile rows each
-    __shared__ V map_a[kWarps][32], map_h[kWarps][32], map_d[kWarps][32], enter[32];
-    __shared__ unsigned s_next;
+    __shared__ Shared<V, kWarps> sh;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    Turns turns(p);
+    if (p.head) dependency_wait();
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(&sh.maps), kWarps);
+        mbar_init(smem_u32(&sh.carry), 1);
+        mbar_init(smem_u32(&sh.next[0]), 1);
+        mbar_init(smem_u32(&sh.next[1]), 1);
+        fence_mbar_init();
+        sh.ticket[1] = p.head ? turns.ask() : blockIdx.x;
+    }
+    __syncthreads();
+    unsigned ticket = sh.ticket[1];
+    if (warp == kWarps) {
+        carry_warp<L, kWarps>(p, sh, turns, ticket, kTile);
+        return;
+    }
+    const uint32_t b_maps = smem_u32(&sh.maps), b_carry = smem_u32(&sh.carry), b_next = smem_u32(sh.next);
     uint8_t *const mine = buf + warp * kTok * kRow;
     uint8_t *const gates = mine + 4 * kTile * kRow;
-    Turns turns(p);
-    auto fetch = [&](unsigned ticket, int stage) {
-        const Tile at(p, ticket, kWidth);
+    auto fetch = [&](unsigned of, int stage) {
+        const Tile at(p, of, kWidth);
         const int t0 = (p.tiles - 1 - at.at) * kTile + warp * kTok, m = min(valid_tokens(p, at.b) - t0, kTok);
         const int left = min(p.C - at.c0, kWidth) * static_cast<int>(sizeof(T));
         uint8_t *to = mine + 2 * stage * kTile * kRow;
@@ -716,35 +812,23 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) scan_bwd_ring_kernel(Sc
                         p.dt * sizeof(T), m, left, wide);
         copies_commit();
     };
-    unsigned ticket = blockIdx.x;
-    if (p.head) {
-        if (threadIdx.x == 0) s_next = turns.ask();
-        __syncthreads();
-        ticket = s_next;
-        __syncthreads();
-    }
     if (ticket < turns.total) fetch(ticket, 0);
-    for (int stage = 0; ticket < turns.total; stage ^= 1) {
+    for (unsigned turn = 0; ticket < turns.total; ++turn) {
         const Tile at(p, ticket, kWidth);
-        turns.now = ticket;
-        unsigned asked = 0;
-        const int b = at.b, c = at.c0 + lane * kV, n = valid_tokens(p, b), tile = p.tiles - 1 - at.at;
-        const int t0 = tile * kTile + warp * kTok;
+        const int stage = turn & 1, b = at.b, c = at.c0 + lane * kV, n = valid_tokens(p, b), tile = p.tiles - 1 - at.at;
+        const int t0 = tile * kTile + warp * kTok, m = min(max(n - t0, 0), kTok);
         const bool live = c < p.C;
-        const int last = n > 0 ? (n - 1) / kTile : 0;
-        const int m = min(max(n - t0, 0), kTok);
         const uint8_t *xs = mine + 2 * stage * kTile * kRow + lane * 4, *ds = xs + kTile * kRow, *gs = gates + lane * 4;
         V k[kTok], A = L::all(1.f), H = L::all(0.f), D = H, h;
         {
             const float *s = p.states + (static_cast<int64_t>(b) * p.tiles + tile) * p.C + c;
             float in[kV];
 #pragma unroll
-            for (int v = 0; v < kV; ++v) in[v] = live && n > 0 && tile <= last ? s[v] : 0.f;
+            for (int v = 0; v < kV; ++v) in[v] = live && m > 0 ? s[v] : 0.f;
             h = whole<kV>(in);
         }
         copies_wait();
         __syncwarp();
-        if (threadIdx.x == 0) asked = turns.ask();
         by_full(m == kTok, [&](auto full) {
 #pragma unroll
             for (int i = 0; i < kTok; ++i)
@@ -755,36 +839,19 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) scan_bwd_ring_kernel(Sc
                     D = L::fma(A, L::load(ds + i * kRow), D);
                 }
         });
-        map_a[warp][lane] = A;
-        map_h[warp][lane] = H;
-        map_d[warp][lane] = D;
-        if (threadIdx.x == 0) s_next = asked;
-        __syncthreads();
-        const unsigned next = s_next;
-        V sa = L::all(1.f), sd = L::all(0.f);   // the map of the tile's tokens after this warp's
-        for (int w = kWarps - 1; w > warp; --w) {
-            sd = L::fma(map_a[w][lane], sd, map_d[w][lane]);
-            sa = L::mul(sa, map_a[w][lane]);
-        }
-        const bool teller = warp == 0 && tile <= last;
-        uint2 *here = p.carry + (static_cast<int64_t>(b) * p.tiles + tile) * p.C + c;
-        if (teller) {
-            D = L::fma(A, sd, D);
-            A = L::mul(A, sa);
-            if (tile > 0 && tile < last && live) tell_map<kV>(here, parts(A), parts(D));
-        }
+        sh.a[turn & 1][warp][lane] = A;
+        sh.h[turn & 1][warp][lane] = H;
+        sh.d[warp][lane] = D;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_maps);
+        bool ok = mbar_wait_bounded(b_next + 8 * (turn & 1), turn >> 1 & 1, kWaits);
+        const unsigned next = ok ? sh.ticket[turn & 1] : turns.total;
         if (next < turns.total) fetch(next, stage ^ 1);
-        if (teller) {
-            float in[kV];
-            if (tile == last) start<kV>(p, b, c, live, in);
-            else if (!entering<kV>(here + p.C, p.C, last - tile, live, p.head, in)) give_up(p);
-            enter[lane] = whole<kV>(in);
-            D = L::fma(A, enter[lane], D);
-            if (live && tile > 0) tell_state<kV>(here, parts(D));
-            else if (live) finish<kV>(p, b, c, parts(D));
-        }
-        // the states before this warp's tokens
-        for (int w = 0; w < warp; ++w) h = L::fma(map_a[w][lane], h, map_h[w][lane]);
+        ok = ok && mbar_wait_bounded(b_maps, turn & 1, kWaits);
+        // the states before this warp's tokens, while the chain's are on their way
+#pragma unroll
+        for (int w = 0; w < kWarps - 1; ++w)
+            if (w < warp) h = L::fma(sh.a[turn & 1][w][lane], h, sh.h[turn & 1][w][lane]);
         V lead[kTok];   // h_{t-1}, of which the sigmoid's gradient takes x_t
         by_full(m == kTok, [&](auto full) {
 #pragma unroll
@@ -795,9 +862,14 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) scan_bwd_ring_kernel(Sc
                     h = L::advance(h, x, k[i]);
                 }
         });
-        __syncthreads();
+        ok = ok && mbar_wait_bounded(b_carry, turn & 1, kWaits);
+        if (!__all_sync(0xffffffffu, ok)) {
+            copies_wait();
+            give_up(p);
+            return;
+        }
         if (live) {
-            V e = L::fma(sa, enter[lane], sd);   // what reaches the state behind the token
+            V e = sh.enter[warp][lane];   // what reaches the state behind the token
             const int64_t out = (static_cast<int64_t>(b) * p.T + t0) * p.C + c;
             T *dx = static_cast<T *>(p.y) + out + (kTok - 1) * static_cast<int64_t>(p.C);
             T *dg = static_cast<T *>(p.dg) + out + (kTok - 1) * static_cast<int64_t>(p.C);
@@ -820,6 +892,13 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdCtas) scan_bwd_ring_kernel(Sc
     }
 }
 
+// A workspace that says nothing yet. A kernel of the library, that the scan's CTAs may be set up while it runs.
+__global__ void __launch_bounds__(256) clear_kernel(uint4 *p, size_t words) {
+    dependency_release();
+    for (size_t i = blockIdx.x * 256 + threadIdx.x; i < words; i += gridDim.x * 256)
+        p[i] = make_uint4(kEmpty, kEmpty, kEmpty, kEmpty);
+}
+
 template <typename T, bool kLog>
 __global__ void scan_step_kernel(const T *x, int64_t xs, const T *gate, int64_t gs, float *h, T *y, int C) {
     const int c = blockIdx.x * blockDim.x + threadIdx.x, b = blockIdx.y;
@@ -831,8 +910,6 @@ __global__ void scan_step_kernel(const T *x, int64_t xs, const T *gate, int64_t 
     h[at] = v;
     y[at] = from_f32<T>(v);
 }
-
-static_assert(kFwdTok * kFwdWarps % KLA_SCAN_SPAN == 0 && KLA_SCAN_SPAN % kFwdTok == 0, "");
 
 int tiles_of(int T, int tile) { return T > tile ? (T + tile - 1) / tile : 1; }
 
@@ -872,7 +949,10 @@ cudaError_t lay_out(ScanArgs &p, int tile, int width, void *workspace, cudaStrea
     p.head = static_cast<Head *>(workspace);
     p.carry = reinterpret_cast<uint2 *>(p.head + 1);
     const cudaError_t e = device_error_word(&p.err);
-    return e == cudaSuccess ? cudaMemsetAsync(workspace, 0xff, carry_bytes(p.B, p.T, p.C, tile), s) : e;
+    if (e != cudaSuccess) return e;
+    const size_t words = carry_bytes(p.B, p.T, p.C, tile) / sizeof(uint4), ctas = (words + 1023) / 1024;
+    clear_kernel<<<static_cast<unsigned>(ctas < 608 ? ctas : 608), 256, 0, s>>>(static_cast<uint4 *>(workspace), words);
+    return cudaGetLastError();
 }
 unsigned tiles_in_all(const ScanArgs &p) { return static_cast<unsigned>(p.B) * p.blocks * p.tiles; }
 
@@ -892,7 +972,9 @@ cudaError_t run_ring(const ScanArgs &p, bool wide, int tile, int block, cudaStre
         done[dev].store(true, std::memory_order_release);
     }
     const unsigned most = kCtas * kSms, tiles = tiles_in_all(p);
-    kKernel<<<tiles < most ? tiles : most, block, smem, s>>>(p, wide);
+    const unsigned grid = tiles < most ? tiles : most;
+    if (p.head) return launch_dependent(kKernel, dim3(grid), dim3(block), smem, s, p, wide);
+    kKernel<<<grid, block, smem, s>>>(p, wide);
     return cudaGetLastError();
 }
 
@@ -911,8 +993,7 @@ extern "C" {
 size_t kla_gated_scan_workspace_size(int B, int T, int C, kla_dtype dtype) {
     using namespace kla;
     if (check(B, T, C, dtype, KLA_SCAN_SIGMOID) != KLA_OK) return 0;
-    const size_t f = carry_bytes(B, T, C, kFwdTok * kFwdWarps), b = carry_bytes(B, T, C, kBwdTok * kBwdWarps);
-    return f > b ? f : b;
+    return carry_bytes(B, T, C, KLA_SCAN_SPAN);   // no kernel has a shorter tile
 }
 
 kla_status kla_gated_scan_fwd(const void *x, const void *gate, const int64_t *strides, const int *lengths,
@@ -950,14 +1031,18 @@ kla_status kla_gated_scan_fwd(const void *x, const void *gate, const int64_t *st
     }
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const bool ring = rows_fit(p, esz, 4), wide = rows_fit(p, esz, 16);
-    if (lay_out(p, kFwdTok * kFwdWarps, ring ? kRow / static_cast<int>(esz) : 32, workspace, cs) != cudaSuccess)
+    if (lay_out(p, fwd_shape(static_cast<int>(esz), ring).tile(), ring ? kRow / static_cast<int>(esz) : 32, workspace, cs) != cudaSuccess)
         return KLA_ERR_CUDA;
     const cudaError_t e = by_type(dtype, mode, [&](auto t, auto log) {
         using E = decltype(t);
         constexpr bool kLog = decltype(log)::value;
-        if (ring) return run_ring<3, kFwdCtas, scan_fwd_ring_kernel<E, kLog, kFwdTok, kFwdWarps>>(p, wide, kFwdTok * kFwdWarps, 32 * kFwdWarps, cs);
+        constexpr Shape r = fwd_shape(sizeof(E), true), o = fwd_shape(sizeof(E), false);
+        static_assert(r.tile() % KLA_SCAN_SPAN == 0 && o.tile() % KLA_SCAN_SPAN == 0 && KLA_SCAN_SPAN % r.tok == 0, "");
+        if (ring)
+            return run_ring<3, r.ctas, scan_fwd_ring_kernel<E, kLog, r.tok, r.warps, r.ctas>>(p, wide, r.tile(),
+                                                                                          32 * r.warps, cs);
         if constexpr (sizeof(E) == 2)   // rows of odd bf16
-            scan_fwd_kernel<E, kLog, 1, kFwdTok, kFwdWarps><<<tiles_in_all(p), 32 * kFwdWarps, 0, cs>>>(p);
+            scan_fwd_kernel<E, kLog, 1, o.tok, o.warps><<<tiles_in_all(p), 32 * o.warps, 0, cs>>>(p);
         return cudaGetLastError();
     });
     return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
@@ -1000,14 +1085,18 @@ kla_status kla_gated_scan_bwd(const void *x, const void *gate, const void *dy, c
     }
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const bool ring = rows_fit(p, esz, 4), wide = rows_fit(p, esz, 16);
-    if (lay_out(p, kBwdTok * kBwdWarps, ring ? kRow / static_cast<int>(esz) : 32, workspace, cs) != cudaSuccess)
+    if (lay_out(p, bwd_shape().tile(), ring ? kRow / static_cast<int>(esz) : 32, workspace, cs) != cudaSuccess)
         return KLA_ERR_CUDA;
     const cudaError_t e = by_type(dtype, mode, [&](auto t, auto log) {
         using E = decltype(t);
         constexpr bool kLog = decltype(log)::value;
-        if (ring) return run_ring<5, kBwdCtas, scan_bwd_ring_kernel<E, kLog, kBwdTok, kBwdWarps>>(p, wide, kBwdTok * kBwdWarps, 32 * kBwdWarps, cs);
+        constexpr Shape r = bwd_shape(), o = r;
+        static_assert(r.tile() % KLA_SCAN_SPAN == 0 && o.tile() % KLA_SCAN_SPAN == 0 && KLA_SCAN_SPAN % r.tok == 0, "");
+        if (ring)
+            return run_ring<5, r.ctas, scan_bwd_ring_kernel<E, kLog, r.tok, r.warps, r.ctas>>(p, wide, r.tile(),
+                                                                                          32 * (r.warps + 1), cs);
         if constexpr (sizeof(E) == 2)   // rows of odd bf16
-            scan_bwd_kernel<E, kLog, 1, kBwdTok, kBwdWarps><<<tiles_in_all(p), 32 * kBwdWarps, 0, cs>>>(p);
+            scan_bwd_kernel<E, kLog, 1, o.tok, o.warps><<<tiles_in_all(p), 32 * o.warps, 0, cs>>>(p);
         return cudaGetLastError();
     });
     return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
