@@ -147,9 +147,9 @@ block_norm_kernel(NormArgs p, int width) {
     __shared__ float2 sums[2][kBlock / 32];
     const int team = threadIdx.x / width, lane = threadIdx.x % width, teams = kBlock / width;
     const int groups = p.w_groups ? p.groups : 1, g = blockIdx.x % groups;   // whose weights this CTA has
-    const int first = blockIdx.x / groups * teams, mine = static_cast<int>(p.rows) / groups;
+    const int64_t first = blockIdx.x / groups * teams, mine = p.rows / groups;   // 64 bits: sums pass the last row
     const int step = gridDim.x / groups * teams;
-    const int turns = first < mine ? (mine - first + step - 1) / step : 0;
+    const int turns = first < mine ? static_cast<int>((mine - first + step - 1) / step) : 0;
     const bool four = kOp == kAddBwd && p.in[3] != nullptr;
     float *const stats = reinterpret_cast<float *>(ring + kStages * kIns * kNV * kBlock * kBytes);
     auto slot = [&](int stage, int i, int k) {
@@ -159,9 +159,10 @@ block_norm_kernel(NormArgs p, int width) {
 #pragma unroll
     for (int k = 0; k < kNV; ++k) there[k] = (k * width + lane) * kV < p.n;
     // the next row to be copied, and the one at hand: their index, and the first of their values of this thread
-    const int row0 = (first + team) * groups + g, hop = step * groups, rows = static_cast<int>(p.rows);
-    const int64_t off0 = static_cast<int64_t>(row0) * p.n + lane * kV, off_hop = static_cast<int64_t>(hop) * p.n;
-    int64_t ahead = row0, ahead_off = off0;   // 64 bits: it runs past the last row
+    const int64_t row0 = (first + team) * groups + g, rows = p.rows;
+    const int hop = step * groups;
+    const int64_t off0 = row0 * p.n + lane * kV, off_hop = static_cast<int64_t>(hop) * p.n;
+    int64_t ahead = row0, ahead_off = off0;
     auto source = [&](int i, int64_t row, int64_t off) {   // this thread's first values of a row
         if (kGated && i == 1 && p.z_stride) {
             const unsigned r = static_cast<unsigned>(row), outer = r / static_cast<unsigned>(p.groups);

@@ -130,7 +130,7 @@ __device__ __forceinline__ void finish(const ScanArgs &p, int b, int c, const fl
 __device__ __forceinline__ void give_up(const ScanArgs &p) {
     if ((threadIdx.x & 31) == 0) {
         atomicOr(p.err, kErrTimeout);
-        *const_cast<volatile unsigned *>(&p.head->abort) = 0u;
+        if (p.head) *const_cast<volatile unsigned *>(&p.head->abort) = 0u;
     }
 }
 __device__ __forceinline__ uint2 hear(const uint2 *p) {
@@ -917,7 +917,7 @@ kla_status check(int B, int T, int C, kla_dtype dtype, kla_scan_mode mode) {
     if (B < 1 || T < 0 || C < 1) return KLA_ERR_INVALID_ARG;
     if (dtype != KLA_DTYPE_F32 && dtype != KLA_DTYPE_BF16) return KLA_ERR_INVALID_ARG;
     if (mode != KLA_SCAN_SIGMOID && mode != KLA_SCAN_LOG) return KLA_ERR_INVALID_ARG;
-    if (T > INT_MAX - 65536 || B > 65535) return KLA_ERR_UNSUPPORTED;
+    if (T > INT_MAX - 65536 || C > INT_MAX - 65536 || B > 65535) return KLA_ERR_UNSUPPORTED;
     // a ticket for every tile of 32 channels
     if (static_cast<int64_t>(B) * ((C + 31) / 32) > INT_MAX / tiles_of(T, KLA_SCAN_SPAN)) return KLA_ERR_UNSUPPORTED;
     return KLA_OK;
@@ -945,11 +945,10 @@ bool rows_fit(const ScanArgs &p, size_t esz, int bytes) {
 cudaError_t lay_out(ScanArgs &p, int tile, int width, void *workspace, cudaStream_t s) {
     p.blocks = (p.C + width - 1) / width;
     p.tiles = tiles_of(p.T, tile);
-    if (p.tiles == 1) return cudaSuccess;
+    const cudaError_t e = device_error_word(&p.err);
+    if (e != cudaSuccess || p.tiles == 1) return e;
     p.head = static_cast<Head *>(workspace);
     p.carry = reinterpret_cast<uint2 *>(p.head + 1);
-    const cudaError_t e = device_error_word(&p.err);
-    if (e != cudaSuccess) return e;
     const size_t words = carry_bytes(p.B, p.T, p.C, tile) / sizeof(uint4), ctas = (words + 1023) / 1024;
     clear_kernel<<<static_cast<unsigned>(ctas < 608 ? ctas : 608), 256, 0, s>>>(static_cast<uint4 *>(workspace), words);
     return cudaGetLastError();

@@ -43,6 +43,7 @@ def scan(lib, **kw):
     (dict(h0=A + 3 * M, hT=A + 3 * M + 4), 1),              # h_T over a part of h0
     (dict(st=strides(M // 4, 16, 128, 16)), 1),             # x reaches into the gate's buffer, and y's
     (dict(T=2**31 - 1), 2), (dict(T=2**31 - 65536), 2), (dict(B=1 << 20), 2),
+    (dict(C=2**31 - 1), 2), (dict(C=2**31 - 20, B=1, T=1), 2), (dict(B=65535, C=2**21, T=1000), 2),
     (dict(T=1000, ws=None, wb=0), 1), (dict(T=1000, wb=64), 1), (dict(T=1000, ws=A + 9 * M + 8), 1),
     (dict(T=1000, ws=A), 1),
 ])

@@ -172,6 +172,19 @@ def test_extreme_gates_and_zero_rows():
     assert rel(dx, torch.full_like(dx, 2 * 0.7310585786300049 / 1e-5 ** 0.5)) <= 1e-5
 
 
+def test_rows_near_32_bits():
+    """65535 heads of three values in 32768 rows: the row behind the last one's team is past 2^31."""
+    import gated_delta_rule_14_gb300 as kla
+    rows, G = 32768, 65535
+    x, z = torch.zeros(rows, G, 3, dtype=BF, device=DEV), torch.zeros(rows, G, 3, dtype=BF, device=DEV)
+    r = rnd(21)
+    x[-1], z[-1], w = r(G, 3).to(BF), r(G, 3).to(BF), r(G, 3)
+    y, _, rstd = kla.gated_norm_fwd(x, z, w)
+    kla.device_status(DEV)
+    want = normed(x[-1].double(), w.double(), 1e-5, "rms") * active(z[-1].double(), "silu")
+    assert rel(y[-1], want) <= 4e-3 and not y[:-1].any()
+
+
 def test_no_rows():
     import gated_delta_rule_14_gb300 as kla
     x, w = torch.empty(0, 32, device=DEV), torch.ones(32, device=DEV)

@@ -132,18 +132,22 @@ def test_gates_that_keep_and_forget():
     """Gates of +-inf and near them: a state is kept or dropped at once, and no NaN comes of it."""
     import gated_delta_rule_14_gb300 as kla
     inf = float("inf")
-    for mode, keep, drop in (("sigmoid", inf, -inf), ("log", 0.0, -inf), ("sigmoid", 200.0, -200.0)):
-        T, C = 300, 33
-        x = torch.randn(1, T, C, device=DEV)
-        gate = torch.full((1, T, C), keep, device=DEV)
+    for mode, keep, drop, dtype, C in (("sigmoid", inf, -inf, torch.float32, 33), ("log", 0.0, -inf, torch.float32, 33),
+                                       ("sigmoid", 200.0, -200.0, torch.float32, 33),
+                                       ("sigmoid", inf, -inf, torch.bfloat16, 34),
+                                       ("sigmoid", 200.0, -200.0, torch.bfloat16, 33),
+                                       ("log", 0.0, -inf, torch.bfloat16, 34)):
+        T = 300
+        x = torch.randn(1, T, C, device=DEV).to(dtype)
+        gate = torch.full((1, T, C), keep, device=DEV, dtype=dtype)
         gate[:, 150] = drop
         xs = torch.zeros_like(x) if mode == "log" else x
         xs = xs.clone()
         xs[:, 150] = x[:, 150]
-        h0 = torch.randn(1, C, device=DEV)
+        h0 = torch.randn(1, C, device=DEV).to(dtype).float()
         y, h_T, s = kla.gated_scan_fwd(xs, gate, h0, mode=mode, states=True)
         g = kla.gated_scan_bwd(xs, gate, torch.ones_like(x), s, None, mode=mode)
-        assert torch.equal(y[:, :150], h0[:, None].expand(1, 150, C)), mode
+        assert torch.equal(y[:, :150].float(), h0[:, None].expand(1, 150, C)), mode
         assert torch.equal(y[:, 150:], x[:, 150:151].expand(1, 150, C)), mode
         assert all(t.isfinite().all() for t in g.values()), mode
 
