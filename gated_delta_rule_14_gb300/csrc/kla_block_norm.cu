@@ -4,6 +4,15 @@
 //   gated   y = xh w act(z)                 dx = N(dy w act(z)),  dz = dy xh w act'(z),  dw = sum dy act(z) xh
 //   added   s = r + l x,  y = xh(s) w       dr = ds + N(dy w),  dx = l dr,  dw = sum dy xh,  dl = sum x dr
 //   xh = (x - mean) rstd, N(u) = rstd (u - mean(u) - xh mean(u xh)); without the means' terms where mean = 0 (RMS)
+//
+// What bounds them is the memory: 3 and 5 elements a value for the gated norm, 4 and 6 for the residual's (5 where it is
+// not scaled). Backward, the residual's sum is formed again from x and the residual: read back as it was rounded to bf16
+// it would leave 9 bits of dw.
+// Measured, bf16: 32768 x 16 heads of 128 gated forward 74 us (5.4 TB/s, 80 % of a copy's rate), backward with dw 119 us
+// (5.6 TB/s); 16397 x 2048 residual forward 50 us (5.4 TB/s), backward with dw and dl 79 us (5.1 TB/s); in fp32 91 and
+// 141 us (5.9 and 5.7 TB/s). By the counters (16384 rows of the same) 39 to 60 instructions a value backward and forward at
+// 1.7 to 2.3 of 4 a cycle with 16 warps an SM: arithmetic and memory each fill about two thirds of the time. CTAs that add up
+// row by row with barriers and read twice took 3650 us for the first, 709 for the second.
 #include <atomic>
 #include <cfloat>
 #include <climits>

@@ -4,6 +4,10 @@
 // position in integers, whose overflow is whole turns. Its upper 32 bits, as a signed number of half turns, are what
 // sine and cosine take. The product in fp32 would lose a bit with every doubling of the position, and one in fp64
 // would cost tens of instructions of a pipe that does two a cycle and SM.
+// What bounds it is the memory, one read and one write of every value. Measured: 8 x 4096 tokens of 32 heads of 128
+// bf16, slices of one projection, 88 us in a row of calls (6.1 TB/s, 90 % of a copy's rate), 93 after other work; 40 heads
+// in fp32 214 us (6.3 TB/s). Heads whose parts fit only 4-byte accesses (80 values, 20 of them turned) take three times
+// their floor: 5 loads of 4 bytes a lane and head do not fill the memory's trip.
 #include <type_traits>
 
 #include "layer_dev.cuh"

@@ -8,7 +8,8 @@
  * `stream` (whose device has to be the current one), argument errors found on the host before
  * anything is launched (KLA_ERR_INVALID_ARG / KLA_ERR_UNSUPPORTED, nothing written), bounded device
  * waits reported by kla_device_status.
- * Outputs and workspaces must not overlap each other or any input unless said otherwise.
+ * Outputs and workspaces must not overlap each other or any input unless said otherwise; a workspace
+ * serves one call at a time, whatever stream it runs on.
  */
 #ifndef KLA_BLOCK_H
 #define KLA_BLOCK_H
@@ -23,6 +24,7 @@ extern "C" {
 #endif
 
 /* ---------------------------------------------------------------------------------- gated scan
+ * Equal calls give equal bits.
  *
  * For every sequence b and channel c, a state h that starts as h0 (zero where NULL):
  *
