@@ -235,6 +235,104 @@ __global__ void __launch_bounds__(kBlock, ctas(sizeof(T) * kV)) rotary_kernel(Ro
     }
 }
 
+// Heads that start on 16 bytes but whose pairs fit no such accesses (126 of 128 values turned, 20 of 80): a warp takes
+// whole heads of a token into shared memory, as many as 4 KB hold, turns them there value by value, a lane the same
+// pairs of all of them, and sends them on.
+template <typename T, bool kHalf>
+__global__ void __launch_bounds__(kBlock, 5) rotary_rows_kernel(RotaryArgs p, int at_once) {
+    constexpr int kV = 16 / sizeof(T), kLoads = 4, kRows = 4;
+    extern __shared__ __align__(16) unsigned char shared[];
+    const int pairs = p.rot / 2, lane = threadIdx.x & 31, heads = p.H[0] + p.H[1], per_row = p.d / kV;
+    unsigned long long *const rates = reinterpret_cast<unsigned long long *>(shared);
+    for (int i = threadIdx.x; i < pairs; i += kBlock) rates[i] = turn_rate(p.freqs[i]);
+    __syncthreads();
+    T *const buf = reinterpret_cast<T *>(shared + (pairs + 1) / 2 * 16) + (threadIdx.x / 32) * at_once * p.d;
+    uint4 *const wide = reinterpret_cast<uint4 *>(buf);
+    const int slices = (heads + at_once - 1) / at_once;
+    const int row_hop = 32 / per_row, col_hop = 32 % per_row;   // of a lane's next access
+    const int64_t jobs = p.tokens * slices, warps = static_cast<int64_t>(gridDim.x) * (kBlock / 32);
+    for (int64_t job = static_cast<int64_t>(blockIdx.x) * (kBlock / 32) + threadIdx.x / 32; job < jobs; job += warps) {
+        const unsigned token = static_cast<unsigned>(job / slices), slice = static_cast<unsigned>(job - static_cast<int64_t>(token) * slices);
+        const unsigned b = token / static_cast<unsigned>(p.T), t = token - b * p.T;
+        const int first = slice * at_once, here = min(heads - first, at_once), accesses = here * per_row;
+        const long long at = !p.positions ? t
+                             : p.wide     ? static_cast<const long long *>(p.positions)[token]
+                                          : static_cast<const int *>(p.positions)[token];
+        const T *in0 = static_cast<const T *>(p.in[0]) + b * p.is[0][0] + t * p.is[0][1];
+        const T *in1 = static_cast<const T *>(p.in[1]) + b * p.is[1][0] + t * p.is[1][1] - p.H[0] * p.is[1][2];
+        T *out0 = static_cast<T *>(p.out[0]) + b * p.os[0][0] + t * p.os[0][1];
+        T *out1 = static_cast<T *>(p.out[1]) + b * p.os[1][0] + t * p.os[1][1] - p.H[0] * p.os[1][2];
+        int head = first + lane / per_row, col = lane % per_row;
+        for (int i = lane; i < accesses; i += 32 * kLoads) {
+            uint4 x[kLoads];
+#pragma unroll
+            for (int q = 0; q < kLoads; ++q) {
+                const bool q0 = head < p.H[0];
+                if (i + 32 * q < accesses)
+                    x[q] = *reinterpret_cast<const uint4 *>((q0 ? in0 : in1) + head * (q0 ? p.is[0][2] : p.is[1][2]) + col * kV);
+                col += col_hop;
+                head += row_hop + (col >= per_row);
+                if (col >= per_row) col -= per_row;
+            }
+#pragma unroll
+            for (int q = 0; q < kLoads; ++q)
+                if (i + 32 * q < accesses) wide[i + 32 * q] = x[q];
+        }
+        __syncwarp();
+        for (int u = lane; u < pairs; u += 32) {
+            const int i0 = kHalf ? u : 2 * u, i1 = kHalf ? u + pairs : 2 * u + 1;
+            float s, c;
+            turned<T>(rates[u], at, s, c);
+            c *= p.scale;
+            s *= p.inverse ? -p.scale : p.scale;
+            T *x = buf;
+            for (int row = 0; row < here; row += kRows, x += kRows * p.d) {
+                float a[kRows], e[kRows];
+#pragma unroll
+                for (int r = 0; r < kRows; ++r)
+                    if (row + r < here) {
+                        a[r] = to_f32(x[r * p.d + i0]);
+                        e[r] = to_f32(x[r * p.d + i1]);
+                    }
+#pragma unroll
+                for (int r = 0; r < kRows; ++r)
+                    if (row + r < here) {
+                        x[r * p.d + i0] = from_f32<T>(fmaf(a[r], c, -e[r] * s));
+                        x[r * p.d + i1] = from_f32<T>(fmaf(e[r], c, a[r] * s));
+                    }
+            }
+        }
+        __syncwarp();
+        head = first + lane / per_row;
+        col = lane % per_row;
+        for (int i = lane; i < accesses; i += 32) {
+            const bool q0 = head < p.H[0];
+            *reinterpret_cast<uint4 *>((q0 ? out0 : out1) + head * (q0 ? p.os[0][2] : p.os[1][2]) + col * kV) = wide[i];
+            col += col_hop;
+            head += row_hop + (col >= per_row);
+            if (col >= per_row) col -= per_row;
+        }
+        __syncwarp();
+    }
+}
+template <typename T>
+cudaError_t run_rows(const RotaryArgs &p, bool half, cudaStream_t s) {
+    constexpr int kSms = 152, kWarps = kBlock / 32, kCtas = 5;
+    const int row = p.d * static_cast<int>(sizeof(T)), heads = p.H[0] + p.H[1];
+    int at_once = row < 4096 ? 4096 / row : 1;
+    if (at_once > heads) at_once = heads;
+    // few tokens: fewer heads at once, as long as there are warps without any
+    const int64_t each = (p.tokens * heads + kSms * kWarps - 1) / (kSms * kWarps);
+    if (at_once > each) at_once = static_cast<int>(each);
+    int64_t grid = (p.tokens * ((heads + at_once - 1) / at_once) + kWarps - 1) / kWarps;
+    if (grid > kSms * kCtas) grid = kSms * kCtas;
+    const size_t smem = (p.rot / 2 + 1) / 2 * 16 + static_cast<size_t>(kWarps) * at_once * row;   // 36 KB at most
+    const unsigned g = static_cast<unsigned>(grid);
+    if (half) rotary_rows_kernel<T, true><<<g, kBlock, smem, s>>>(p, at_once);
+    else rotary_rows_kernel<T, false><<<g, kBlock, smem, s>>>(p, at_once);
+    return cudaGetLastError();
+}
+
 template <typename T, int kV, bool kHalf>
 cudaError_t run(const RotaryArgs &p, cudaStream_t s) {
     constexpr int kSms = 152, kWarps = kBlock / 32, kCtas = ctas(sizeof(T) * kV), kAtOnce = 4;
@@ -262,12 +360,11 @@ template <typename T, int kV>
 cudaError_t run(const RotaryArgs &p, bool half, cudaStream_t s) {
     return half ? run<T, kV, true>(p, s) : run<T, kV, false>(p, s);
 }
-// By the widest access that every head's start and both parts of it allow.
+// By the widest access that every head's start, and both parts of it, allow.
 template <typename T>
 cudaError_t run(const RotaryArgs &p, int B, bool half, cudaStream_t s) {
     constexpr int kFull = 16 / sizeof(T);
-    auto fits = [&](int v) {
-        if (p.rot / 2 % v || (p.d - p.rot) % v) return false;
+    auto starts = [&](int v) {
         const int size[2][3] = {{B, p.T, p.H[0]}, {B, p.T, p.H[1]}};
         for (int m = 0; m < 2; ++m) {
             if (!aligned(p.in[m], v * sizeof(T)) || !aligned(p.out[m], v * sizeof(T))) return false;
@@ -276,7 +373,9 @@ cudaError_t run(const RotaryArgs &p, int B, bool half, cudaStream_t s) {
         }
         return true;
     };
+    auto fits = [&](int v) { return p.rot / 2 % v == 0 && (p.d - p.rot) % v == 0 && starts(v); };
     if (fits(kFull)) return run<T, kFull>(p, half, s);
+    if (p.rot > 0 && p.d % kFull == 0 && starts(kFull)) return run_rows<T>(p, half, s);
     if (sizeof(T) == 2 && fits(4)) return run<T, sizeof(T) == 2 ? 4 : 1>(p, half, s);
     if (sizeof(T) == 2 && fits(2)) return run<T, sizeof(T) == 2 ? 2 : 1>(p, half, s);
     return run<T, 1>(p, half, s);
