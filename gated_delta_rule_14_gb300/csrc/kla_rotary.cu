@@ -6,8 +6,7 @@
 // would cost tens of instructions of a pipe that does two a cycle and SM.
 // What bounds it is the memory, one read and one write of every value. Measured: 8 x 4096 tokens of 32 heads of 128
 // bf16, slices of one projection, 88 us in a row of calls (6.1 TB/s, 90 % of a copy's rate), 93 after other work; 40 heads
-// in fp32 214 us (6.3 TB/s). Heads whose parts fit only 4-byte accesses (80 values, 20 of them turned) take three times
-// their floor: 5 loads of 4 bytes a lane and head do not fill the memory's trip.
+// in fp32 214 us (6.3 TB/s); 126 of 128 values turned, whose pairs fit no wide accesses, 132 us.
 #include <type_traits>
 
 #include "layer_dev.cuh"
@@ -375,8 +374,11 @@ cudaError_t run(const RotaryArgs &p, int B, bool half, cudaStream_t s) {
     };
     auto fits = [&](int v) { return p.rot / 2 % v == 0 && (p.d - p.rot) % v == 0 && starts(v); };
     if (fits(kFull)) return run<T, kFull>(p, half, s);
-    if (p.rot > 0 && p.d % kFull == 0 && starts(kFull)) return run_rows<T>(p, half, s);
     if (sizeof(T) == 2 && fits(4)) return run<T, sizeof(T) == 2 ? 4 : 1>(p, half, s);
+    // through shared memory but where accesses of 4 bytes fit heads of less than 128: 8 x 4096 x 32 heads took 97 us
+    // instead of 154 of 80 bf16 with 20 turned, 52 instead of 31 of 16 with 4; of single values 132 instead of 222 (126 of 128)
+    if (p.rot > 0 && p.d % kFull == 0 && starts(kFull) && !(sizeof(T) == 2 && fits(2) && p.d < 64))
+        return run_rows<T>(p, half, s);
     if (sizeof(T) == 2 && fits(2)) return run<T, sizeof(T) == 2 ? 2 : 1>(p, half, s);
     return run<T, 1>(p, half, s);
 }

@@ -98,38 +98,39 @@ __device__ __forceinline__ void put(T *p, const float (&v)[1]) { *p = from_f32<T
 constexpr unsigned kEmpty = 0xffffffffu, kWhole = 0xfffffffeu, kNan = 0x7fffffffu;
 __device__ __forceinline__ unsigned factor_bits(float a) { return a == a ? __float_as_uint(a) : kNan; }
 template <int kV>
-__device__ __forceinline__ void tell(uint2 *p, const uint2 (&v)[kV]) {
+__device__ __forceinline__ void tell(uint2 *p, int count, const uint2 (&v)[kV]) {   // of the first `count` channels
 #pragma unroll
     for (int i = 0; i < kV; ++i)
-        asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(p + i),
+        if (i < count) asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(p + i),
                      "l"(static_cast<unsigned long long>(v[i].y) << 32 | v[i].x)
                      : "memory");
 }
 template <int kV>
-__device__ __forceinline__ void tell_map(uint2 *p, const float (&A)[kV], const float (&H)[kV]) {
+__device__ __forceinline__ void tell_map(uint2 *p, int count, const float (&A)[kV], const float (&H)[kV]) {
     uint2 w[kV];
 #pragma unroll
     for (int v = 0; v < kV; ++v) w[v] = make_uint2(factor_bits(A[v]), __float_as_uint(H[v]));
-    tell<kV>(p, w);
+    tell<kV>(p, count, w);
 }
 template <int kV>
-__device__ __forceinline__ void tell_state(uint2 *p, const float (&h)[kV]) {
+__device__ __forceinline__ void tell_state(uint2 *p, int count, const float (&h)[kV]) {
     uint2 w[kV];
 #pragma unroll
     for (int v = 0; v < kV; ++v) w[v] = make_uint2(kWhole, __float_as_uint(h[v]));
-    tell<kV>(p, w);
+    tell<kV>(p, count, w);
 }
 // The state at the chain's start (zeros where none is given), and at its end where that is wanted.
 template <int kV>
-__device__ __forceinline__ void start(const ScanArgs &p, int b, int c, bool live, float (&h)[kV]) {
+__device__ __forceinline__ void start(const ScanArgs &p, int b, int c, int count, float (&h)[kV]) {
 #pragma unroll
-    for (int v = 0; v < kV; ++v) h[v] = p.h0 && live ? p.h0[static_cast<int64_t>(b) * p.C + c + v] : 0.f;
+    for (int v = 0; v < kV; ++v) h[v] = p.h0 && v < count ? p.h0[static_cast<int64_t>(b) * p.C + c + v] : 0.f;
 }
 template <int kV>
-__device__ __forceinline__ void finish(const ScanArgs &p, int b, int c, const float (&h)[kV]) {
+__device__ __forceinline__ void finish(const ScanArgs &p, int b, int c, int count, const float (&h)[kV]) {
     if (p.h_T)
 #pragma unroll
-        for (int v = 0; v < kV; ++v) p.h_T[static_cast<int64_t>(b) * p.C + c + v] = h[v];
+        for (int v = 0; v < kV; ++v)
+            if (v < count) p.h_T[static_cast<int64_t>(b) * p.C + c + v] = h[v];
 }
 __device__ __forceinline__ void give_up(const ScanArgs &p) {
     if ((threadIdx.x & 31) == 0) {
@@ -150,7 +151,7 @@ __device__ __forceinline__ uint2 hear(const uint2 *p) {
 // taken by ticket in the order of the chain, so that all of those are running or done and none of them waits for a
 // later one: the wait ends. Its limit is for what cannot be foreseen. Run by a whole warp; false where it gave up.
 template <int kV>
-__device__ __forceinline__ bool entering(const uint2 *p, int64_t hop, int left, bool live, const Head *head,
+__device__ __forceinline__ bool entering(const uint2 *p, int64_t hop, int left, int count, const Head *head,
                                          float (&h)[kV]) {
     constexpr int kAhead = 4;
     constexpr unsigned kLimit = 1u << 21;
@@ -161,7 +162,7 @@ __device__ __forceinline__ bool entering(const uint2 *p, int64_t hop, int left, 
 #pragma unroll
         for (int j = 0; j < kAhead; ++j)
 #pragma unroll
-            for (int v = 0; v < kV; ++v) w[j][v] = live && j < left ? hear(p + j * hop + v) : make_uint2(kEmpty, 0u);
+            for (int v = 0; v < kV; ++v) w[j][v] = v < count && j < left ? hear(p + j * hop + v) : make_uint2(kEmpty, 0u);
         int found[kV];
         bool known = true;
 #pragma unroll
@@ -173,9 +174,9 @@ __device__ __forceinline__ bool entering(const uint2 *p, int64_t hop, int left, 
                 if (told && found[v] < 0 && w[j][v].x == kWhole) found[v] = j;
                 told &= w[j][v].x != kEmpty;
             }
-            known &= found[v] >= 0;
+            known &= found[v] >= 0 || v >= count;
         }
-        if (__all_sync(0xffffffffu, known || !live)) {
+        if (__all_sync(0xffffffffu, known)) {
 #pragma unroll
             for (int j = kAhead - 1; j >= 0; --j)
 #pragma unroll
@@ -210,7 +211,7 @@ __device__ __forceinline__ unsigned take_ticket(const ScanArgs &p) {
     return mine;
 }
 
-// ---- rows of odd bf16, which no asynchronous copy takes
+// ---- bf16 tensors that start in the middle of 4 bytes, of which no asynchronous copy takes all rows
 // A tile is kWarps x kTok tokens of 32 channels; a thread holds kTok tokens of one channel in registers, all of its
 // loads on their way at once. Every warp finds how its tokens map a state, the last one joins those maps, tells
 // the tile's own, hears the state that enters the tile and tells the one that leaves it; then every warp walks its tokens.
@@ -282,7 +283,7 @@ __global__ void __launch_bounds__(32 * kWarps) scan_fwd_kernel(ScanArgs p) {
             H[v] = fmaf(A[v], ph[v], H[v]);
             A[v] *= pa[v];
         }
-        if (at.at > 0 && at.at < last && live) tell_map<kV>(here, A, H);
+        if (at.at > 0 && at.at < last) tell_map<kV>(here, live, A, H);
         if (at.at == 0) start<kV>(p, b, c, live, in);
         else if (!entering<kV>(here - p.C, -static_cast<int64_t>(p.C), at.at, live, p.head, in)) give_up(p);
 #pragma unroll
@@ -290,8 +291,8 @@ __global__ void __launch_bounds__(32 * kWarps) scan_fwd_kernel(ScanArgs p) {
             enter[v][lane] = in[v];
             H[v] = fmaf(A[v], in[v], H[v]);
         }
-        if (live && at.at < last) tell_state<kV>(here, H);
-        else if (live) finish<kV>(p, b, c, H);
+        if (at.at < last) tell_state<kV>(here, live, H);
+        else finish<kV>(p, b, c, live, H);
     }
     __syncthreads();
     if (!live) return;
@@ -405,7 +406,7 @@ __global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(ScanArgs p) {
             D[v] = fmaf(A[v], sd[v], D[v]);
             A[v] *= sa[v];
         }
-        if (tile > 0 && tile < last && live) tell_map<kV>(here, A, D);
+        if (tile > 0 && tile < last) tell_map<kV>(here, live, A, D);
         if (tile == last) start<kV>(p, b, c, live, in);
         else if (!entering<kV>(here + p.C, p.C, last - tile, live, p.head, in)) give_up(p);
 #pragma unroll
@@ -413,8 +414,8 @@ __global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(ScanArgs p) {
             enter[v][lane] = in[v];
             D[v] = fmaf(A[v], in[v], D[v]);
         }
-        if (live && tile > 0) tell_state<kV>(here, D);
-        else if (live) finish<kV>(p, b, c, D);
+        if (tile > 0) tell_state<kV>(here, live, D);
+        else finish<kV>(p, b, c, live, D);
     }
     // the states before this warp's tokens
     for (int w = 0; w < warp; ++w)
@@ -471,8 +472,10 @@ struct Shape {
 constexpr Shape fwd_shape(int esz, bool ring) { return ring && esz == 2 ? Shape{32, 8, 2} : Shape{16, 8, 3}; }
 constexpr Shape bwd_shape() { return Shape{16, 8, 2}; }
 
-// ---- tiles through shared memory: rows of 128 bytes (64 channels of bf16, 32 of fp32), 4 bytes a lane
-constexpr int kRow = 128;
+// ---- tiles through shared memory: rows of 128 bytes (64 channels of bf16, 32 of fp32), 4 bytes a lane; of bf16 rows that
+// start in the middle of 4 bytes, or end there, 132
+constexpr int kEvenRow = 128, kOddRow = 132;
+
 // What a lane has of a row: two channels of bf16, whose arithmetic is paired, or one of fp32. A gate is kept as one
 // number: bf16: w, or a where KLA_SCAN_LOG, with h = a h + w x and a = 1 - w, whose rounding of 2^-25 is that of a
 // itself where it is near 1 (and whose exponential and reciprocal are the hardware's, off by 2^-21 at gates of 10, far
@@ -484,10 +487,10 @@ template <bool kLog, bool kBwd>
 struct Lane<__nv_bfloat16, kLog, kBwd> {
     static constexpr int kV = 2;
     using V = float2;
-    static __device__ __forceinline__ V load(const uint8_t *p) {
-        const uint32_t r = *reinterpret_cast<const uint32_t *>(p);
+    static __device__ __forceinline__ V unpack(uint32_t r) {
         return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
     }
+    static __device__ __forceinline__ V load(const uint8_t *p) { return unpack(*reinterpret_cast<const uint32_t *>(p)); }
     static __device__ __forceinline__ void store(__nv_bfloat16 *p, V v) {
         *reinterpret_cast<uint32_t *>(p) = ptx::pack_bf16(v.x, v.y);
     }
@@ -551,28 +554,91 @@ __device__ __forceinline__ void copy16(uint32_t to, const void *from) {
 __device__ __forceinline__ void copy4(uint32_t to, const void *from) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
 }
+__device__ __forceinline__ void copy4(uint32_t to, const void *from, int size) {   // the rest zeros
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(size) : "memory");
+}
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
-// Rows 0 .. m - 1 of kTok into this warp's part of a buffer; `left` bytes of a row are there.
-template <int kTok>
-__device__ __forceinline__ void copy_rows(uint8_t *to, const void *from, int64_t pitch, int m, int left, bool wide) {
+// Rows 0 .. m - 1 of kTok, `pitch` values apart, into this warp's part of a buffer; `left` channels there are from the
+// rows' first on. kOdd: rows of bf16 that start in the middle of 4 bytes or end there. Their words are copied as they lie,
+// so that a row may take 33 of them; the word that a row starts in the middle of begins with a value of the tensor's too,
+// as the tensor starts on 4 bytes, and of the one that a row ends in the middle of only that half is read.
+template <typename T, int kTok, bool kOdd>
+__device__ __forceinline__ void copy_rows(uint8_t *to, const T *from, int64_t pitch, int m, int left, bool wide) {
     const int lane = threadIdx.x & 31;
     const uint32_t s = ptx::smem_u32(to);
-    const char *f = static_cast<const char *>(from);
-    if (wide) {
+    const char *f = reinterpret_cast<const char *>(from);
+    pitch *= sizeof(T);
+    if constexpr (kOdd) {
+        static_assert(kTok <= 32, "");
+        // even and odd rows: where the lane's word is, whether and how much of it is there
+        const uint32_t odd = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(f) >> 1) & 1;
+        const char *at[2];
+        int size[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int half = r ? (odd ^ (static_cast<uint32_t>(pitch) >> 1)) & 1 : odd, first = 2 * lane - half;
+            at[r] = f + r * pitch + 2 * first;
+            size[r] = first >= left ? 0 : first + 1 < left ? 4 : 2;
+        }
+#pragma unroll
+        for (int i = 0; i < kTok; ++i) {
+            if (i < m && size[i & 1]) copy4(s + i * kOddRow + lane * 4, at[i & 1], size[i & 1]);
+            at[i & 1] += 2 * pitch;
+        }
+        // the 33rd words, a row a lane
+        const char *row = f + lane * pitch;
+        if (lane < m && (reinterpret_cast<uintptr_t>(row) & 2) && left > 63)
+            copy4(s + lane * kOddRow + 128, row + 126, left > 64 ? 4 : 2);
+    } else if (wide) {
         const int off = (lane & 7) * 16;
+        const bool in = off < left * static_cast<int64_t>(sizeof(T));
 #pragma unroll
         for (int i = 0; i < kTok; i += 4) {
             const int r = i + lane / 8;
-            if (r < m && off < left) copy16(s + r * kRow + off, f + r * pitch + off);
+            if (r < m && in) copy16(s + r * kEvenRow + off, f + r * pitch + off);
         }
     } else {
         const int off = lane * 4;
+        const bool in = off < left * static_cast<int64_t>(sizeof(T));
 #pragma unroll
         for (int i = 0; i < kTok; ++i)
-            if (i < m && off < left) copy4(s + i * kRow + off, f + i * pitch + off);
+            if (i < m && in) copy4(s + i * kEvenRow + off, f + i * pitch + off);
     }
 }
+// A lane's two values of a row that starts in the middle of 4 bytes, or not: rows of one tensor alternate, or none does.
+template <bool kOdd>
+struct Parity {
+    uint32_t shift[2];   // of even and odd rows, in bits
+    template <typename T>
+    __device__ __forceinline__ Parity(const T *first, int64_t pitch) {
+        if (kOdd) {
+            const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(first) >> 1) & 1;
+            shift[0] = 16 * at;
+            shift[1] = 16 * (at ^ (static_cast<uint32_t>(pitch) & 1));
+        }
+    }
+    template <typename L>
+    __device__ __forceinline__ typename L::V load(const uint8_t *p, int row) const {
+        if constexpr (!kOdd) {
+            return L::load(p);
+        } else {
+            const uint32_t *w = reinterpret_cast<const uint32_t *>(p);
+            return L::unpack(__funnelshift_r(w[0], w[1], shift[row & 1]));
+        }
+    }
+    template <typename L, typename T>
+    __device__ __forceinline__ void store(T *p, typename L::V v, int row, int count) const {
+        if constexpr (!kOdd) {
+            L::store(p, v);
+        } else if (shift[row & 1] == 0 && count == 2) {
+            L::store(p, v);
+        } else {
+            p[0] = from_f32<T>(part(v, 0));
+            if (count == 2) p[1] = from_f32<T>(part(v, 1));
+        }
+    }
+};
 
 // Tiles one after the other. A CTA takes a ticket for its next tile while it works on one, not earlier, so that where
 // tiles are few no CTA has two of them and another none.
@@ -588,6 +654,12 @@ struct Turns {
     }
 };
 
+// How many channels a lane has from c on: kV or none where rows have an even number.
+template <bool kOdd, int kV>
+__device__ __forceinline__ int channels(const ScanArgs &p, int c) {
+    return kOdd ? min(max(p.C - c, 0), kV) : c < p.C ? kV : 0;
+}
+
 // Runs f with whether all of a warp's kTok tokens are valid: the loops over them have no conditions then.
 template <typename F>
 __device__ __forceinline__ void by_full(bool full, F f) {
@@ -597,11 +669,11 @@ __device__ __forceinline__ void by_full(bool full, F f) {
 
 // As above, with tiles one after the other: while a CTA waits for the state that enters one and writes its outputs, the
 // next one's rows are on their way.
-template <typename T, bool kLog, int kTok, int kWarps, int kCtas>
+template <typename T, bool kLog, bool kOdd, int kTok, int kWarps, int kCtas>
 __global__ void __launch_bounds__(32 * kWarps, kCtas) scan_fwd_ring_kernel(ScanArgs p, bool wide) {
     using L = Lane<T, kLog, false>;
     using V = typename L::V;
-    constexpr int kTile = kTok * kWarps, kV = L::kV, kWidth = 32 * kV;
+    constexpr int kTile = kTok * kWarps, kV = L::kV, kWidth = 32 * kV, kRow = kOdd ? kOddRow : kEvenRow;
     extern __shared__ __align__(128) uint8_t buf[];   // x twice, gate once: kTile rows each
     __shared__ V map_a[kWarps][32], map_h[kWarps][32], enter[32];
     __shared__ unsigned s_next;
@@ -613,11 +685,11 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) scan_fwd_ring_kernel(ScanA
     auto fetch = [&](unsigned ticket, int stage) {
         const Tile at(p, ticket, kWidth);
         const int t0 = at.at * kTile + warp * kTok, m = min(valid_tokens(p, at.b) - t0, kTok);
-        const int left = min(p.C - at.c0, kWidth) * static_cast<int>(sizeof(T));
-        copy_rows<kTok>(gates, static_cast<const T *>(p.gate) + at.b * p.gb + t0 * p.gt + at.c0, p.gt * sizeof(T), m,
-                        left, wide);
-        copy_rows<kTok>(mine + stage * kTile * kRow, static_cast<const T *>(p.x) + at.b * p.xb + t0 * p.xt + at.c0,
-                        p.xt * sizeof(T), m, left, wide);
+        const int left = p.C - at.c0;
+        copy_rows<T, kTok, kOdd>(gates, static_cast<const T *>(p.gate) + at.b * p.gb + t0 * p.gt + at.c0, p.gt, m, left,
+                                 wide);
+        copy_rows<T, kTok, kOdd>(mine + stage * kTile * kRow,
+                                 static_cast<const T *>(p.x) + at.b * p.xb + t0 * p.xt + at.c0, p.xt, m, left, wide);
         copies_commit();
     };
     unsigned ticket = blockIdx.x;
@@ -633,10 +705,12 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) scan_fwd_ring_kernel(ScanA
         turns.now = ticket;
         unsigned asked = 0;
         const int b = at.b, c = at.c0 + lane * kV, n = valid_tokens(p, b), t0 = at.at * kTile + warp * kTok;
-        const bool live = c < p.C;
+        const int count = channels<kOdd, kV>(p, c);
         const int last = n > 0 ? (n - 1) / kTile : 0;
         const int m = min(max(n - t0, 0), kTok);   // of this warp's tokens, how many are valid
         const uint8_t *xs = mine + stage * kTile * kRow + lane * 4, *gs = gates + lane * 4;
+        const Parity<kOdd> of_x(static_cast<const T *>(p.x) + b * p.xb + t0 * p.xt + at.c0, p.xt);
+        const Parity<kOdd> of_g(static_cast<const T *>(p.gate) + b * p.gb + t0 * p.gt + at.c0, p.gt);
         V k[kTok], A = L::all(1.f), H = L::all(0.f);
         copies_wait();
         __syncwarp();
@@ -645,9 +719,9 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) scan_fwd_ring_kernel(ScanA
 #pragma unroll
             for (int i = 0; i < kTok; ++i)
                 if (full || i < m) {
-                    k[i] = L::keep(L::load(gs + i * kRow));
+                    k[i] = L::keep(of_g.template load<L>(gs + i * kRow, i));
                     A = L::shrink(A, k[i]);
-                    H = L::advance(H, L::load(xs + i * kRow), k[i]);
+                    H = L::advance(H, of_x.template load<L>(xs + i * kRow, i), k[i]);
                 }
         });
         map_a[warp][lane] = A;
@@ -666,36 +740,38 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) scan_fwd_ring_kernel(ScanA
         if (teller) {
             H = L::fma(A, ph, H);
             A = L::mul(A, pa);
-            if (at.at > 0 && at.at < last && live) tell_map<kV>(here, parts(A), parts(H));
+            if (at.at > 0 && at.at < last) tell_map<kV>(here, count, parts(A), parts(H));
         }
         if (next < turns.total) fetch(next, stage ^ 1);
         if (teller) {
             float in[kV];
-            if (at.at == 0) start<kV>(p, b, c, live, in);
-            else if (!entering<kV>(here - p.C, -static_cast<int64_t>(p.C), at.at, live, p.head, in)) give_up(p);
+            if (at.at == 0) start<kV>(p, b, c, count, in);
+            else if (!entering<kV>(here - p.C, -static_cast<int64_t>(p.C), at.at, count, p.head, in)) give_up(p);
             enter[lane] = whole<kV>(in);
             H = L::fma(A, enter[lane], H);
-            if (live && at.at < last) tell_state<kV>(here, parts(H));
-            else if (live) finish<kV>(p, b, c, parts(H));
+            if (at.at < last) tell_state<kV>(here, count, parts(H));
+            else finish<kV>(p, b, c, count, parts(H));
         }
         __syncthreads();
-        if (live) {
+        if (count > 0) {
             V h = L::fma(pa, enter[lane], ph);
             if (p.states && m > 0 && t0 % KLA_SCAN_SPAN == 0) {
                 const int64_t spans = (p.T + KLA_SCAN_SPAN - 1) / KLA_SCAN_SPAN;
                 float *s = p.states + (b * spans + t0 / KLA_SCAN_SPAN) * p.C + c;
 #pragma unroll
-                for (int v = 0; v < kV; ++v) s[v] = part(h, v);
+                for (int v = 0; v < kV; ++v)
+                    if (v < count) s[v] = part(h, v);
             }
             T *y = static_cast<T *>(p.y) + (static_cast<int64_t>(b) * p.T + t0) * p.C + c;
+            const Parity<kOdd> of_y(y, p.C);
             by_full(m == kTok, [&](auto full) {
 #pragma unroll
                 for (int i = 0; i < kTok; ++i, y += p.C)
                     if (full || i < m) {
-                        h = L::advance(h, L::load(xs + i * kRow), k[i]);
-                        L::store(y, h);
+                        h = L::advance(h, of_x.template load<L>(xs + i * kRow, i), k[i]);
+                        of_y.template store<L>(y, h, i, count);
                     } else if (t0 + i < p.T) {
-                        L::store(y, L::all(0.f));
+                        of_y.template store<L>(y, L::all(0.f), i, count);
                     }
             });
         }
@@ -716,7 +792,7 @@ struct Shared {
 };
 constexpr uint32_t kWaits = 400000;   // of 20 us at most, more than `entering` takes to give up
 
-template <typename L, int kWarps>
+template <typename L, bool kOdd, int kWarps>
 __device__ __forceinline__ void carry_warp(const ScanArgs &p, Shared<typename L::V, kWarps> &sh, Turns &turns,
                                            unsigned ticket, int tile_tokens) {
     using V = typename L::V;
@@ -728,7 +804,7 @@ __device__ __forceinline__ void carry_warp(const ScanArgs &p, Shared<typename L:
         const Tile at(p, ticket, 32 * kV);
         const int b = at.b, c = at.c0 + lane * kV, n = valid_tokens(p, b), tile = p.tiles - 1 - at.at;
         const int last = n > 0 ? (n - 1) / tile_tokens : 0;
-        const bool live = c < p.C;
+        const int count = channels<kOdd, kV>(p, c);
         uint2 *here = p.carry + (static_cast<int64_t>(b) * p.tiles + tile) * p.C + c;
         turns.now = ticket;
         unsigned next = 0;
@@ -758,14 +834,14 @@ __device__ __forceinline__ void carry_warp(const ScanArgs &p, Shared<typename L:
             }
             float in[kV];
             if (tile == last) {
-                start<kV>(p, b, c, live, in);
+                start<kV>(p, b, c, count, in);
             } else {
-                if (live && tile > 0) tell_map<kV>(here, parts(pa), parts(pd));
-                if (!entering<kV>(here + p.C, p.C, last - tile, live, p.head, in)) give_up(p);
+                if (tile > 0) tell_map<kV>(here, count, parts(pa), parts(pd));
+                if (!entering<kV>(here + p.C, p.C, last - tile, count, p.head, in)) give_up(p);
             }
             const V e = whole<kV>(in), out = L::fma(pa, e, pd);
-            if (live && tile > 0) tell_state<kV>(here, parts(out));
-            else if (live) finish<kV>(p, b, c, parts(out));
+            if (tile > 0) tell_state<kV>(here, count, parts(out));
+            else finish<kV>(p, b, c, count, parts(out));
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) sh.enter[w][lane] = L::fma(after_a[w], e, after_d[w]);
         }
@@ -775,12 +851,12 @@ __device__ __forceinline__ void carry_warp(const ScanArgs &p, Shared<typename L:
     }
 }
 
-template <typename T, bool kLog, int kTok, int kWarps, int kCtas>
+template <typename T, bool kLog, bool kOdd, int kTok, int kWarps, int kCtas>
 __global__ void __launch_bounds__(32 * (kWarps + 1), kCtas) scan_bwd_ring_kernel(ScanArgs p, bool wide) {
     using namespace ptx;
     using L = Lane<T, kLog, true>;
     using V = typename L::V;
-    constexpr int kTile = kTok * kWarps, kV = L::kV, kWidth = 32 * kV;
+    constexpr int kTile = kTok * kWarps, kV = L::kV, kWidth = 32 * kV, kRow = kOdd ? kOddRow : kEvenRow;
     static_assert(kTile == KLA_SCAN_SPAN, "");
     extern __shared__ __align__(128) uint8_t buf[];   // x and dy twice, gate once: kTile rows each
     __shared__ Shared<V, kWarps> sh;
@@ -798,7 +874,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kCtas) scan_bwd_ring_kernel
     __syncthreads();
     unsigned ticket = sh.ticket[1];
     if (warp == kWarps) {
-        carry_warp<L, kWarps>(p, sh, turns, ticket, kTile);
+        carry_warp<L, kOdd, kWarps>(p, sh, turns, ticket, kTile);
         return;
     }
     const uint32_t b_maps = smem_u32(&sh.maps), b_carry = smem_u32(&sh.carry), b_next = smem_u32(sh.next);
@@ -807,14 +883,13 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kCtas) scan_bwd_ring_kernel
     auto fetch = [&](unsigned of, int stage) {
         const Tile at(p, of, kWidth);
         const int t0 = (p.tiles - 1 - at.at) * kTile + warp * kTok, m = min(valid_tokens(p, at.b) - t0, kTok);
-        const int left = min(p.C - at.c0, kWidth) * static_cast<int>(sizeof(T));
+        const int left = p.C - at.c0;
         uint8_t *to = mine + 2 * stage * kTile * kRow;
-        copy_rows<kTok>(gates, static_cast<const T *>(p.gate) + at.b * p.gb + t0 * p.gt + at.c0, p.gt * sizeof(T), m,
-                        left, wide);
-        copy_rows<kTok>(to, static_cast<const T *>(p.x) + at.b * p.xb + t0 * p.xt + at.c0, p.xt * sizeof(T), m, left,
-                        wide);
-        copy_rows<kTok>(to + kTile * kRow, static_cast<const T *>(p.dy) + at.b * p.db + t0 * p.dt + at.c0,
-                        p.dt * sizeof(T), m, left, wide);
+        copy_rows<T, kTok, kOdd>(gates, static_cast<const T *>(p.gate) + at.b * p.gb + t0 * p.gt + at.c0, p.gt, m, left,
+                                 wide);
+        copy_rows<T, kTok, kOdd>(to, static_cast<const T *>(p.x) + at.b * p.xb + t0 * p.xt + at.c0, p.xt, m, left, wide);
+        copy_rows<T, kTok, kOdd>(to + kTile * kRow, static_cast<const T *>(p.dy) + at.b * p.db + t0 * p.dt + at.c0, p.dt,
+                                 m, left, wide);
         copies_commit();
     };
     if (ticket < turns.total) fetch(ticket, 0);
@@ -822,14 +897,17 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kCtas) scan_bwd_ring_kernel
         const Tile at(p, ticket, kWidth);
         const int stage = turn & 1, b = at.b, c = at.c0 + lane * kV, n = valid_tokens(p, b), tile = p.tiles - 1 - at.at;
         const int t0 = tile * kTile + warp * kTok, m = min(max(n - t0, 0), kTok);
-        const bool live = c < p.C;
+        const int count = channels<kOdd, kV>(p, c);
         const uint8_t *xs = mine + 2 * stage * kTile * kRow + lane * 4, *ds = xs + kTile * kRow, *gs = gates + lane * 4;
+        const Parity<kOdd> of_x(static_cast<const T *>(p.x) + b * p.xb + t0 * p.xt + at.c0, p.xt);
+        const Parity<kOdd> of_g(static_cast<const T *>(p.gate) + b * p.gb + t0 * p.gt + at.c0, p.gt);
+        const Parity<kOdd> of_d(static_cast<const T *>(p.dy) + b * p.db + t0 * p.dt + at.c0, p.dt);
         V k[kTok], A = L::all(1.f), H = L::all(0.f), D = H, h;
         {
             const float *s = p.states + (static_cast<int64_t>(b) * p.tiles + tile) * p.C + c;
             float in[kV];
 #pragma unroll
-            for (int v = 0; v < kV; ++v) in[v] = live && m > 0 ? s[v] : 0.f;
+            for (int v = 0; v < kV; ++v) in[v] = v < count && m > 0 ? s[v] : 0.f;
             h = whole<kV>(in);
         }
         copies_wait();
@@ -838,10 +916,10 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kCtas) scan_bwd_ring_kernel
 #pragma unroll
             for (int i = 0; i < kTok; ++i)
                 if (full || i < m) {
-                    k[i] = L::keep(L::load(gs + i * kRow));
+                    k[i] = L::keep(of_g.template load<L>(gs + i * kRow, i));
                     A = L::shrink(A, k[i]);
-                    H = L::advance(H, L::load(xs + i * kRow), k[i]);
-                    D = L::fma(A, L::load(ds + i * kRow), D);
+                    H = L::advance(H, of_x.template load<L>(xs + i * kRow, i), k[i]);
+                    D = L::fma(A, of_d.template load<L>(ds + i * kRow, i), D);
                 }
         });
         sh.a[turn & 1][warp][lane] = A;
@@ -862,7 +940,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kCtas) scan_bwd_ring_kernel
 #pragma unroll
             for (int i = 0; i < kTok; ++i)
                 if (full || i < m) {
-                    const V x = L::load(xs + i * kRow);
+                    const V x = of_x.template load<L>(xs + i * kRow, i);
                     lead[i] = kLog ? h : L::fma(x, L::all(-1.f), h);
                     h = L::advance(h, x, k[i]);
                 }
@@ -873,22 +951,23 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kCtas) scan_bwd_ring_kernel
             give_up(p);
             return;
         }
-        if (live) {
+        if (count > 0) {
             V e = sh.enter[warp][lane];   // what reaches the state behind the token
             const int64_t out = (static_cast<int64_t>(b) * p.T + t0) * p.C + c;
+            const Parity<kOdd> of_dx(static_cast<T *>(p.y) + out, p.C), of_dg(static_cast<T *>(p.dg) + out, p.C);
             T *dx = static_cast<T *>(p.y) + out + (kTok - 1) * static_cast<int64_t>(p.C);
             T *dg = static_cast<T *>(p.dg) + out + (kTok - 1) * static_cast<int64_t>(p.C);
             by_full(m == kTok, [&](auto full) {
 #pragma unroll
                 for (int i = kTok - 1; i >= 0; --i, dx -= p.C, dg -= p.C)
                     if (full || i < m) {
-                        const V dh = L::add(L::load(ds + i * kRow), e), w = L::w(k[i]);
+                        const V dh = L::add(of_d.template load<L>(ds + i * kRow, i), e), w = L::w(k[i]);
                         e = L::mul(L::a(k[i]), dh);
-                        L::store(dx, kLog ? dh : L::mul(w, dh));
-                        L::store(dg, L::mul(kLog ? lead[i] : L::mul(w, lead[i]), e));
+                        of_dx.template store<L>(dx, kLog ? dh : L::mul(w, dh), i, count);
+                        of_dg.template store<L>(dg, L::mul(kLog ? lead[i] : L::mul(w, lead[i]), e), i, count);
                     } else if (t0 + i < p.T) {
-                        L::store(dx, L::all(0.f));
-                        L::store(dg, L::all(0.f));
+                        of_dx.template store<L>(dx, L::all(0.f), i, count);
+                        of_dg.template store<L>(dg, L::all(0.f), i, count);
                     }
             });
         }
@@ -962,10 +1041,10 @@ unsigned tiles_in_all(const ScanArgs &p) { return static_cast<unsigned>(p.B) * p
 
 // kBuffers of `tile` rows a CTA; as many CTAs as the SMs hold at once.
 template <int kBuffers, int kCtas, auto kKernel>
-cudaError_t run_ring(const ScanArgs &p, bool wide, int tile, int block, cudaStream_t s) {
+cudaError_t run_ring(const ScanArgs &p, bool wide, int row, int tile, int block, cudaStream_t s) {
     constexpr int kMaxDevices = 64, kSms = 152;
     static std::atomic<bool> done[kMaxDevices];
-    const int smem = kBuffers * tile * kRow;
+    const int smem = kBuffers * tile * row;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -1034,19 +1113,24 @@ kla_status kla_gated_scan_fwd(const void *x, const void *gate, const int64_t *st
             if (overlaps(outs[i], outs[j])) return KLA_ERR_INVALID_ARG;
     }
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    const bool ring = rows_fit(p, esz, 4), wide = rows_fit(p, esz, 16);
-    if (lay_out(p, fwd_shape(static_cast<int>(esz), ring).tile(), ring ? kRow / static_cast<int>(esz) : 32, workspace, cs) != cudaSuccess)
+    const bool even = rows_fit(p, esz, 4), wide = rows_fit(p, esz, 16);
+    const bool ring = even || (aligned(x, 4) && aligned(gate, 4));
+    if (lay_out(p, fwd_shape(static_cast<int>(esz), ring).tile(), ring ? kEvenRow / static_cast<int>(esz) : 32, workspace, cs) != cudaSuccess)
         return KLA_ERR_CUDA;
     const cudaError_t e = by_type(dtype, mode, [&](auto t, auto log) {
         using E = decltype(t);
         constexpr bool kLog = decltype(log)::value;
         constexpr Shape r = fwd_shape(sizeof(E), true), o = fwd_shape(sizeof(E), false);
         static_assert(r.tile() % KLA_SCAN_SPAN == 0 && o.tile() % KLA_SCAN_SPAN == 0 && KLA_SCAN_SPAN % r.tok == 0, "");
-        if (ring)
-            return run_ring<3, r.ctas, scan_fwd_ring_kernel<E, kLog, r.tok, r.warps, r.ctas>>(p, wide, r.tile(),
-                                                                                          32 * r.warps, cs);
-        if constexpr (sizeof(E) == 2)   // rows of odd bf16
+        if (even)
+            return run_ring<3, r.ctas, scan_fwd_ring_kernel<E, kLog, false, r.tok, r.warps, r.ctas>>(
+                p, wide, kEvenRow, r.tile(), 32 * r.warps, cs);
+        if constexpr (sizeof(E) == 2) {
+            if (ring)
+                return run_ring<3, r.ctas, scan_fwd_ring_kernel<E, kLog, true, r.tok, r.warps, r.ctas>>(
+                    p, false, kOddRow, r.tile(), 32 * r.warps, cs);
             scan_fwd_kernel<E, kLog, o.tok, o.warps><<<tiles_in_all(p), 32 * o.warps, 0, cs>>>(p);
+        }
         return cudaGetLastError();
     });
     return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
@@ -1088,19 +1172,24 @@ kla_status kla_gated_scan_bwd(const void *x, const void *gate, const void *dy, c
             if (overlaps(outs[i], outs[j])) return KLA_ERR_INVALID_ARG;
     }
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    const bool ring = rows_fit(p, esz, 4), wide = rows_fit(p, esz, 16);
-    if (lay_out(p, bwd_shape().tile(), ring ? kRow / static_cast<int>(esz) : 32, workspace, cs) != cudaSuccess)
+    const bool even = rows_fit(p, esz, 4), wide = rows_fit(p, esz, 16);
+    const bool ring = even || (aligned(x, 4) && aligned(gate, 4) && aligned(dy, 4));
+    if (lay_out(p, bwd_shape().tile(), ring ? kEvenRow / static_cast<int>(esz) : 32, workspace, cs) != cudaSuccess)
         return KLA_ERR_CUDA;
     const cudaError_t e = by_type(dtype, mode, [&](auto t, auto log) {
         using E = decltype(t);
         constexpr bool kLog = decltype(log)::value;
         constexpr Shape r = bwd_shape(), o = r;
         static_assert(r.tile() % KLA_SCAN_SPAN == 0 && o.tile() % KLA_SCAN_SPAN == 0 && KLA_SCAN_SPAN % r.tok == 0, "");
-        if (ring)
-            return run_ring<5, r.ctas, scan_bwd_ring_kernel<E, kLog, r.tok, r.warps, r.ctas>>(p, wide, r.tile(),
-                                                                                          32 * (r.warps + 1), cs);
-        if constexpr (sizeof(E) == 2)   // rows of odd bf16
+        if (even)
+            return run_ring<5, r.ctas, scan_bwd_ring_kernel<E, kLog, false, r.tok, r.warps, r.ctas>>(
+                p, wide, kEvenRow, r.tile(), 32 * (r.warps + 1), cs);
+        if constexpr (sizeof(E) == 2) {
+            if (ring)
+                return run_ring<5, r.ctas, scan_bwd_ring_kernel<E, kLog, true, r.tok, r.warps, r.ctas>>(
+                    p, false, kOddRow, r.tile(), 32 * (r.warps + 1), cs);
             scan_bwd_kernel<E, kLog, o.tok, o.warps><<<tiles_in_all(p), 32 * o.warps, 0, cs>>>(p);
+        }
         return cudaGetLastError();
     });
     return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;

@@ -78,6 +78,16 @@ def test_many_tokens_of_few_heads(H, K, d, rot, layout, dtype):
     check(3, 6007, H, K, d, rot, layout, dtype, seed=H, packed=True)
 
 
+@pytest.mark.parametrize("H,K,d,rot", [(16, 16, 128, 126), (5, 1, 80, 20), (3, 3, 64, 62), (40, 8, 256, 130),
+                                       (2, 0, 1024, 1022), (9, 2, 32, 30), (33, 11, 16, 14), (6, 2, 104, 104), (4, 4, 128, 2)])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_pairs_that_fit_no_wide_accesses(H, K, d, rot, layout, dtype):
+    """Heads through shared memory, whole tokens and parts of them, few tokens and many."""
+    check(2, 3, H, K, d, rot, layout, dtype, seed=d, packed=True)
+    check(3, 701, H, K, d, rot, layout, dtype, seed=d + 1)
+
+
 @pytest.mark.parametrize("kind", [torch.int32, torch.int64])
 def test_positions(kind):
     """Given positions, far ones and negative ones among them: whole turns cost no bits. At 2^31 the frequency's own

@@ -222,6 +222,30 @@ def test_unaligned_starts(shift, dtype):
     assert all(rel(gb[n], ga[n]) <= TOL[dtype] for n in ga)
 
 
+@pytest.mark.parametrize("C,pad,T", [(64, 1, 300), (65, 0, 600), (130, 3, 260), (127, 2, 1000), (1, 0, 700), (129, 0, 129)])
+@pytest.mark.parametrize("mode", ["sigmoid", "log"])
+def test_rows_that_start_in_the_middle_of_4_bytes(C, pad, T, mode):
+    """bf16 rows an odd number of values apart, or of odd length, in tensors that start on 4 bytes; past the last channel lie
+    NaN that nothing may take up, and past the outputs' last value one that nothing may overwrite."""
+    import gated_delta_rule_14_gb300 as kla
+    x, gate, dy, h0, dh, _, _ = make(2, T, C, torch.bfloat16, mode, C)
+
+    def place(t):
+        wide = torch.full((2 * T * (C + pad) + 2,), float("nan"), dtype=t.dtype, device=DEV)
+        view = wide.as_strided((2, T, C), (T * (C + pad), C + pad, 1))
+        view.copy_(t)
+        return view
+    a = kla.gated_scan_fwd(x, gate, h0, mode=mode, states=True)
+    room = torch.full((2 * T * C + 1,), 7.0, dtype=torch.bfloat16, device=DEV)
+    b = kla.gated_scan_fwd(place(x), place(gate), h0, mode=mode, states=True, out=room[:-1].view(2, T, C))
+    assert all(torch.equal(u, v) for u, v in zip(a, b)) and float(room[-1]) == 7.0
+    ga, gb = kla.gated_scan_bwd(x, gate, dy, a[2], dh, mode=mode), kla.gated_scan_bwd(place(x), place(gate), place(dy),
+                                                                                      b[2], dh, mode=mode)
+    assert all(torch.equal(ga[n], gb[n]) for n in ga)
+    want, wh = reference(x.double(), gate.double(), h0.double(), mode, torch.full((2,), T, device=DEV))
+    assert rel(b[0], want) <= 4e-3 and rel(b[1], wh) <= 3e-5
+
+
 def test_offsets_past_32_bits():
     """Sequences 2^31 + 64 values apart."""
     import gated_delta_rule_14_gb300 as kla
