@@ -19,6 +19,8 @@
 // walks all tokens took 120 ms for the first. By the counters (8 x 2048 x 2048) 21 instructions a value forward, at 1.8
 // of 4 a cycle, of whose warps' time a quarter waits for the chain, and 40 backward at 2.2 of 4: registers hold 16 warps
 // an SM, and with those neither the issue slots nor the memory (3.9 TB/s there) are full.
+#include <cuda.h>
+
 #include <atomic>
 #include <climits>
 
@@ -475,6 +477,18 @@ constexpr Shape bwd_shape() { return Shape{16, 8, 2}; }
 // ---- tiles through shared memory: rows of 128 bytes (64 channels of bf16, 32 of fp32), 4 bytes a lane; of bf16 rows that
 // start in the middle of 4 bytes, or end there, 132
 constexpr int kEvenRow = 128, kOddRow = 132;
+// How rows get there: one instruction of the tensor memory accelerator a tile and tensor, asynchronous copies by the warps
+// that need them, or those of rows as they lie.
+enum Copies { kTma, kEven, kOdd };
+struct Maps {
+    CUtensorMap x, gate, dy;
+};
+__device__ __forceinline__ void load_tile(uint32_t to, const CUtensorMap *map, uint32_t bar, int c, int t, int b) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(to),
+        "l"(map), "r"(bar), "r"(c), "r"(t), "r"(b)
+        : "memory");
+}
 
 // What a lane has of a row: two channels of bf16, whose arithmetic is paired, or one of fp32. A gate is kept as one
 // number: bf16: w, or a where KLA_SCAN_LOG, with h = a h + w x and a = 1 - w, whose rounding of 2^-25 is that of a
@@ -563,13 +577,13 @@ __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_grou
 // rows' first on. kOdd: rows of bf16 that start in the middle of 4 bytes or end there. Their words are copied as they lie,
 // so that a row may take 33 of them; the word that a row starts in the middle of begins with a value of the tensor's too,
 // as the tensor starts on 4 bytes, and of the one that a row ends in the middle of only that half is read.
-template <typename T, int kTok, bool kOdd>
+template <typename T, int kTok, Copies kBy>
 __device__ __forceinline__ void copy_rows(uint8_t *to, const T *from, int64_t pitch, int m, int left, bool wide) {
     const int lane = threadIdx.x & 31;
     const uint32_t s = ptx::smem_u32(to);
     const char *f = reinterpret_cast<const char *>(from);
     pitch *= sizeof(T);
-    if constexpr (kOdd) {
+    if constexpr (kBy == kOdd) {
         static_assert(kTok <= 32, "");
         // even and odd rows: where the lane's word is, whether and how much of it is there
         const uint32_t odd = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(f) >> 1) & 1;
@@ -607,12 +621,12 @@ __device__ __forceinline__ void copy_rows(uint8_t *to, const T *from, int64_t pi
     }
 }
 // A lane's two values of a row that starts in the middle of 4 bytes, or not: rows of one tensor alternate, or none does.
-template <bool kOdd>
+template <Copies kBy>
 struct Parity {
     uint32_t shift[2];   // of even and odd rows, in bits
     template <typename T>
     __device__ __forceinline__ Parity(const T *first, int64_t pitch) {
-        if (kOdd) {
+        if (kBy == kOdd) {
             const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(first) >> 1) & 1;
             shift[0] = 16 * at;
             shift[1] = 16 * (at ^ (static_cast<uint32_t>(pitch) & 1));
@@ -620,7 +634,7 @@ struct Parity {
     }
     template <typename L>
     __device__ __forceinline__ typename L::V load(const uint8_t *p, int row) const {
-        if constexpr (!kOdd) {
+        if constexpr (kBy != kOdd) {
             return L::load(p);
         } else {
             const uint32_t *w = reinterpret_cast<const uint32_t *>(p);
@@ -629,7 +643,7 @@ struct Parity {
     }
     template <typename L, typename T>
     __device__ __forceinline__ void store(T *p, typename L::V v, int row, int count) const {
-        if constexpr (!kOdd) {
+        if constexpr (kBy != kOdd) {
             L::store(p, v);
         } else if (shift[row & 1] == 0 && count == 2) {
             L::store(p, v);
@@ -654,10 +668,12 @@ struct Turns {
     }
 };
 
+constexpr uint32_t kWaits = 400000;   // of 20 us at most, more than `entering` takes to give up
+
 // How many channels a lane has from c on: kV or none where rows have an even number.
-template <bool kOdd, int kV>
+template <Copies kBy, int kV>
 __device__ __forceinline__ int channels(const ScanArgs &p, int c) {
-    return kOdd ? min(max(p.C - c, 0), kV) : c < p.C ? kV : 0;
+    return kBy == kOdd ? min(max(p.C - c, 0), kV) : c < p.C ? kV : 0;
 }
 
 // Runs f with whether all of a warp's kTok tokens are valid: the loops over them have no conditions then.
@@ -669,26 +685,46 @@ __device__ __forceinline__ void by_full(bool full, F f) {
 
 // As above, with tiles one after the other: while a CTA waits for the state that enters one and writes its outputs, the
 // next one's rows are on their way.
-template <typename T, bool kLog, bool kOdd, int kTok, int kWarps, int kCtas>
-__global__ void __launch_bounds__(32 * kWarps, kCtas) scan_fwd_ring_kernel(ScanArgs p, bool wide) {
+template <typename T, bool kLog, Copies kBy, int kTok, int kWarps, int kCtas>
+__global__ void __launch_bounds__(32 * kWarps, kCtas) scan_fwd_ring_kernel(ScanArgs p, bool wide, const __grid_constant__ Maps maps) {
     using L = Lane<T, kLog, false>;
     using V = typename L::V;
-    constexpr int kTile = kTok * kWarps, kV = L::kV, kWidth = 32 * kV, kRow = kOdd ? kOddRow : kEvenRow;
+    constexpr int kTile = kTok * kWarps, kV = L::kV, kWidth = 32 * kV, kRow = kBy == kOdd ? kOddRow : kEvenRow;
     extern __shared__ __align__(128) uint8_t buf[];   // x twice, gate once: kTile rows each
     __shared__ V map_a[kWarps][32], map_h[kWarps][32], enter[32];
     __shared__ unsigned s_next;
+    __shared__ uint64_t full[2];   // kTma: the rows of an even or odd turn's tile are there
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     uint8_t *const mine = buf + warp * kTok * kRow;
     uint8_t *const gates = mine + 2 * kTile * kRow;
     Turns turns(p);
     if (p.head) dependency_wait();
+    const uint32_t b_full = ptx::smem_u32(full);
+    if (kBy == kTma && threadIdx.x == 0) {
+        ptx::mbar_init(b_full, 1);
+        ptx::mbar_init(b_full + 8, 1);
+        ptx::fence_mbar_init();
+    }
+    if (kBy == kTma) __syncthreads();
+    // every warp its own rows, or one thread the tile (after a barrier: all warps are done with what it replaces)
     auto fetch = [&](unsigned ticket, int stage) {
         const Tile at(p, ticket, kWidth);
+        if constexpr (kBy == kTma) {
+            if (threadIdx.x == 0 && at.at * kTile < valid_tokens(p, at.b)) {
+                const uint32_t bar = b_full + 8 * stage, to = ptx::smem_u32(buf);
+                ptx::mbar_arrive_expect_tx(bar, 2 * kTile * kRow);
+                load_tile(to + 2 * kTile * kRow, &maps.gate, bar, at.c0, at.at * kTile, at.b);
+                load_tile(to + stage * kTile * kRow, &maps.x, bar, at.c0, at.at * kTile, at.b);
+            } else if (threadIdx.x == 0) {
+                ptx::mbar_arrive(b_full + 8 * stage);
+            }
+            return;
+        }
         const int t0 = at.at * kTile + warp * kTok, m = min(valid_tokens(p, at.b) - t0, kTok);
         const int left = p.C - at.c0;
-        copy_rows<T, kTok, kOdd>(gates, static_cast<const T *>(p.gate) + at.b * p.gb + t0 * p.gt + at.c0, p.gt, m, left,
+        copy_rows<T, kTok, kBy>(gates, static_cast<const T *>(p.gate) + at.b * p.gb + t0 * p.gt + at.c0, p.gt, m, left,
                                  wide);
-        copy_rows<T, kTok, kOdd>(mine + stage * kTile * kRow,
+        copy_rows<T, kTok, kBy>(mine + stage * kTile * kRow,
                                  static_cast<const T *>(p.x) + at.b * p.xb + t0 * p.xt + at.c0, p.xt, m, left, wide);
         copies_commit();
     };
@@ -700,20 +736,26 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) scan_fwd_ring_kernel(ScanA
         __syncthreads();
     }
     if (ticket < turns.total) fetch(ticket, 0);
-    for (int stage = 0; ticket < turns.total; stage ^= 1) {
+    for (unsigned turn = 0; ticket < turns.total; ++turn) {
+        const int stage = turn & 1;
         const Tile at(p, ticket, kWidth);
         turns.now = ticket;
         unsigned asked = 0;
         const int b = at.b, c = at.c0 + lane * kV, n = valid_tokens(p, b), t0 = at.at * kTile + warp * kTok;
-        const int count = channels<kOdd, kV>(p, c);
+        const int count = channels<kBy, kV>(p, c);
         const int last = n > 0 ? (n - 1) / kTile : 0;
         const int m = min(max(n - t0, 0), kTok);   // of this warp's tokens, how many are valid
         const uint8_t *xs = mine + stage * kTile * kRow + lane * 4, *gs = gates + lane * 4;
-        const Parity<kOdd> of_x(static_cast<const T *>(p.x) + b * p.xb + t0 * p.xt + at.c0, p.xt);
-        const Parity<kOdd> of_g(static_cast<const T *>(p.gate) + b * p.gb + t0 * p.gt + at.c0, p.gt);
+        const Parity<kBy> of_x(static_cast<const T *>(p.x) + b * p.xb + t0 * p.xt + at.c0, p.xt);
+        const Parity<kBy> of_g(static_cast<const T *>(p.gate) + b * p.gb + t0 * p.gt + at.c0, p.gt);
         V k[kTok], A = L::all(1.f), H = L::all(0.f);
-        copies_wait();
-        __syncwarp();
+        if constexpr (kBy == kTma) {
+            if (!__all_sync(0xffffffffu, ptx::mbar_wait_bounded(b_full + 8 * stage, turn >> 1 & 1, kWaits)))
+                give_up(p);   // and on, with whatever is there: the other warps meet this one at their barriers
+        } else {
+            copies_wait();
+            __syncwarp();
+        }
         if (threadIdx.x == 0) asked = turns.ask();
         by_full(m == kTok, [&](auto full) {
 #pragma unroll
@@ -763,7 +805,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) scan_fwd_ring_kernel(ScanA
                     if (v < count) s[v] = part(h, v);
             }
             T *y = static_cast<T *>(p.y) + (static_cast<int64_t>(b) * p.T + t0) * p.C + c;
-            const Parity<kOdd> of_y(y, p.C);
+            const Parity<kBy> of_y(y, p.C);
             by_full(m == kTok, [&](auto full) {
 #pragma unroll
                 for (int i = 0; i < kTok; ++i, y += p.C)
@@ -788,13 +830,12 @@ struct Shared {
     V a[2][kWarps][32], h[2][kWarps][32], d[kWarps][32];
     V enter[kWarps][32];
     unsigned ticket[2];
-    uint64_t maps, carry, next[2];
+    uint64_t maps, carry, next[2], full[2];
 };
-constexpr uint32_t kWaits = 400000;   // of 20 us at most, more than `entering` takes to give up
 
-template <typename L, bool kOdd, int kWarps>
+template <typename L, Copies kBy, int kWarps, typename F>
 __device__ __forceinline__ void carry_warp(const ScanArgs &p, Shared<typename L::V, kWarps> &sh, Turns &turns,
-                                           unsigned ticket, int tile_tokens) {
+                                           unsigned ticket, int tile_tokens, F fetch_tile) {
     using V = typename L::V;
     constexpr int kV = L::kV;
     using namespace ptx;
@@ -804,7 +845,7 @@ __device__ __forceinline__ void carry_warp(const ScanArgs &p, Shared<typename L:
         const Tile at(p, ticket, 32 * kV);
         const int b = at.b, c = at.c0 + lane * kV, n = valid_tokens(p, b), tile = p.tiles - 1 - at.at;
         const int last = n > 0 ? (n - 1) / tile_tokens : 0;
-        const int count = channels<kOdd, kV>(p, c);
+        const int count = channels<kBy, kV>(p, c);
         uint2 *here = p.carry + (static_cast<int64_t>(b) * p.tiles + tile) * p.C + c;
         turns.now = ticket;
         unsigned next = 0;
@@ -822,6 +863,7 @@ __device__ __forceinline__ void carry_warp(const ScanArgs &p, Shared<typename L:
             return;
         }
         if (i == 0) ask();
+        if (kBy == kTma && next < turns.total) fetch_tile(next, (i + 1) & 1);   // the gates' rows and that half are read
         if (tile <= last) {
             V pa = L::all(1.f), pd = L::all(0.f), after_a[kWarps], after_d[kWarps];   // the maps of later tokens
 #pragma unroll
@@ -851,12 +893,12 @@ __device__ __forceinline__ void carry_warp(const ScanArgs &p, Shared<typename L:
     }
 }
 
-template <typename T, bool kLog, bool kOdd, int kTok, int kWarps, int kCtas>
-__global__ void __launch_bounds__(32 * (kWarps + 1), kCtas) scan_bwd_ring_kernel(ScanArgs p, bool wide) {
+template <typename T, bool kLog, Copies kBy, int kTok, int kWarps, int kCtas>
+__global__ void __launch_bounds__(32 * (kWarps + 1), kCtas) scan_bwd_ring_kernel(ScanArgs p, bool wide, const __grid_constant__ Maps maps) {
     using namespace ptx;
     using L = Lane<T, kLog, true>;
     using V = typename L::V;
-    constexpr int kTile = kTok * kWarps, kV = L::kV, kWidth = 32 * kV, kRow = kOdd ? kOddRow : kEvenRow;
+    constexpr int kTile = kTok * kWarps, kV = L::kV, kWidth = 32 * kV, kRow = kBy == kOdd ? kOddRow : kEvenRow;
     static_assert(kTile == KLA_SCAN_SPAN, "");
     extern __shared__ __align__(128) uint8_t buf[];   // x and dy twice, gate once: kTile rows each
     __shared__ Shared<V, kWarps> sh;
@@ -868,13 +910,31 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kCtas) scan_bwd_ring_kernel
         mbar_init(smem_u32(&sh.carry), 1);
         mbar_init(smem_u32(&sh.next[0]), 1);
         mbar_init(smem_u32(&sh.next[1]), 1);
+        mbar_init(smem_u32(&sh.full[0]), 1);
+        mbar_init(smem_u32(&sh.full[1]), 1);
         fence_mbar_init();
         sh.ticket[1] = p.head ? turns.ask() : blockIdx.x;
     }
     __syncthreads();
     unsigned ticket = sh.ticket[1];
+    const uint32_t b_full = smem_u32(sh.full);
+    auto fetch_tile = [&](unsigned of, int stage) {   // kTma: by one lane of the chain's warp
+        const Tile at(p, of, kWidth);
+        const int t0 = (p.tiles - 1 - at.at) * kTile;
+        const uint32_t bar = b_full + 8 * stage, to = smem_u32(buf);
+        if (lane != 0) return;
+        if (t0 >= valid_tokens(p, at.b)) {
+            mbar_arrive(bar);
+            return;
+        }
+        mbar_arrive_expect_tx(bar, 3 * kTile * kRow);
+        load_tile(to + 4 * kTile * kRow, &maps.gate, bar, at.c0, t0, at.b);
+        load_tile(to + 2 * stage * kTile * kRow, &maps.x, bar, at.c0, t0, at.b);
+        load_tile(to + (2 * stage + 1) * kTile * kRow, &maps.dy, bar, at.c0, t0, at.b);
+    };
     if (warp == kWarps) {
-        carry_warp<L, kOdd, kWarps>(p, sh, turns, ticket, kTile);
+        if (kBy == kTma && ticket < turns.total) fetch_tile(ticket, 0);
+        carry_warp<L, kBy, kWarps>(p, sh, turns, ticket, kTile, fetch_tile);
         return;
     }
     const uint32_t b_maps = smem_u32(&sh.maps), b_carry = smem_u32(&sh.carry), b_next = smem_u32(sh.next);
@@ -885,23 +945,23 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kCtas) scan_bwd_ring_kernel
         const int t0 = (p.tiles - 1 - at.at) * kTile + warp * kTok, m = min(valid_tokens(p, at.b) - t0, kTok);
         const int left = p.C - at.c0;
         uint8_t *to = mine + 2 * stage * kTile * kRow;
-        copy_rows<T, kTok, kOdd>(gates, static_cast<const T *>(p.gate) + at.b * p.gb + t0 * p.gt + at.c0, p.gt, m, left,
+        copy_rows<T, kTok, kBy>(gates, static_cast<const T *>(p.gate) + at.b * p.gb + t0 * p.gt + at.c0, p.gt, m, left,
                                  wide);
-        copy_rows<T, kTok, kOdd>(to, static_cast<const T *>(p.x) + at.b * p.xb + t0 * p.xt + at.c0, p.xt, m, left, wide);
-        copy_rows<T, kTok, kOdd>(to + kTile * kRow, static_cast<const T *>(p.dy) + at.b * p.db + t0 * p.dt + at.c0, p.dt,
+        copy_rows<T, kTok, kBy>(to, static_cast<const T *>(p.x) + at.b * p.xb + t0 * p.xt + at.c0, p.xt, m, left, wide);
+        copy_rows<T, kTok, kBy>(to + kTile * kRow, static_cast<const T *>(p.dy) + at.b * p.db + t0 * p.dt + at.c0, p.dt,
                                  m, left, wide);
         copies_commit();
     };
-    if (ticket < turns.total) fetch(ticket, 0);
+    if (kBy != kTma && ticket < turns.total) fetch(ticket, 0);
     for (unsigned turn = 0; ticket < turns.total; ++turn) {
         const Tile at(p, ticket, kWidth);
         const int stage = turn & 1, b = at.b, c = at.c0 + lane * kV, n = valid_tokens(p, b), tile = p.tiles - 1 - at.at;
         const int t0 = tile * kTile + warp * kTok, m = min(max(n - t0, 0), kTok);
-        const int count = channels<kOdd, kV>(p, c);
+        const int count = channels<kBy, kV>(p, c);
         const uint8_t *xs = mine + 2 * stage * kTile * kRow + lane * 4, *ds = xs + kTile * kRow, *gs = gates + lane * 4;
-        const Parity<kOdd> of_x(static_cast<const T *>(p.x) + b * p.xb + t0 * p.xt + at.c0, p.xt);
-        const Parity<kOdd> of_g(static_cast<const T *>(p.gate) + b * p.gb + t0 * p.gt + at.c0, p.gt);
-        const Parity<kOdd> of_d(static_cast<const T *>(p.dy) + b * p.db + t0 * p.dt + at.c0, p.dt);
+        const Parity<kBy> of_x(static_cast<const T *>(p.x) + b * p.xb + t0 * p.xt + at.c0, p.xt);
+        const Parity<kBy> of_g(static_cast<const T *>(p.gate) + b * p.gb + t0 * p.gt + at.c0, p.gt);
+        const Parity<kBy> of_d(static_cast<const T *>(p.dy) + b * p.db + t0 * p.dt + at.c0, p.dt);
         V k[kTok], A = L::all(1.f), H = L::all(0.f), D = H, h;
         {
             const float *s = p.states + (static_cast<int64_t>(b) * p.tiles + tile) * p.C + c;
@@ -910,8 +970,13 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kCtas) scan_bwd_ring_kernel
             for (int v = 0; v < kV; ++v) in[v] = v < count && m > 0 ? s[v] : 0.f;
             h = whole<kV>(in);
         }
-        copies_wait();
-        __syncwarp();
+        bool ok = true;
+        if constexpr (kBy == kTma) {
+            ok = mbar_wait_bounded(b_full + 8 * stage, turn >> 1 & 1, kWaits);
+        } else {
+            copies_wait();
+            __syncwarp();
+        }
         by_full(m == kTok, [&](auto full) {
 #pragma unroll
             for (int i = 0; i < kTok; ++i)
@@ -927,9 +992,9 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kCtas) scan_bwd_ring_kernel
         sh.d[warp][lane] = D;
         __syncwarp();
         if (lane == 0) mbar_arrive(b_maps);
-        bool ok = mbar_wait_bounded(b_next + 8 * (turn & 1), turn >> 1 & 1, kWaits);
+        ok = ok && mbar_wait_bounded(b_next + 8 * (turn & 1), turn >> 1 & 1, kWaits);
         const unsigned next = ok ? sh.ticket[turn & 1] : turns.total;
-        if (next < turns.total) fetch(next, stage ^ 1);
+        if (kBy != kTma && next < turns.total) fetch(next, stage ^ 1);
         ok = ok && mbar_wait_bounded(b_maps, turn & 1, kWaits);
         // the states before this warp's tokens, while the chain's are on their way
 #pragma unroll
@@ -954,7 +1019,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kCtas) scan_bwd_ring_kernel
         if (count > 0) {
             V e = sh.enter[warp][lane];   // what reaches the state behind the token
             const int64_t out = (static_cast<int64_t>(b) * p.T + t0) * p.C + c;
-            const Parity<kOdd> of_dx(static_cast<T *>(p.y) + out, p.C), of_dg(static_cast<T *>(p.dg) + out, p.C);
+            const Parity<kBy> of_dx(static_cast<T *>(p.y) + out, p.C), of_dg(static_cast<T *>(p.dg) + out, p.C);
             T *dx = static_cast<T *>(p.y) + out + (kTok - 1) * static_cast<int64_t>(p.C);
             T *dg = static_cast<T *>(p.dg) + out + (kTok - 1) * static_cast<int64_t>(p.C);
             by_full(m == kTok, [&](auto full) {
@@ -1039,9 +1104,46 @@ cudaError_t lay_out(ScanArgs &p, int tile, int width, void *workspace, cudaStrea
 }
 unsigned tiles_in_all(const ScanArgs &p) { return static_cast<unsigned>(p.B) * p.blocks * p.tiles; }
 
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn() {
+    static const EncodeTiledFn fn = []() -> EncodeTiledFn {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return nullptr;
+        return reinterpret_cast<EncodeTiledFn>(f);
+    }();
+    return fn;
+}
+// A strided [B, T, C] tensor; box = 128 bytes of channels x `tokens` tokens of one sequence.
+bool make_map(CUtensorMap *m, const void *base, int64_t sb, int64_t st, const ScanArgs &p, size_t esz, int tokens) {
+    const EncodeTiledFn fn = encode_fn();
+    constexpr int64_t kMost = int64_t(1) << 38;   // of a stride in bytes: 2^40
+    if (!fn || st <= 0 || st > kMost || (p.B > 1 && (sb <= 0 || sb > kMost))) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.C), static_cast<cuuint64_t>(p.T), static_cast<cuuint64_t>(p.B)};
+    // the stride of an axis of one element is never used
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(st) * esz, p.B > 1 ? static_cast<cuuint64_t>(sb) * esz : 256};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(kEvenRow / esz), static_cast<cuuint32_t>(tokens), 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, esz == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void *>(base),
+              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// By tensor maps where rows fit 16 bytes, none is broadcast, and there are tiles enough for the maps' making (a
+// microsecond of the host's) to be worth it: more than the SMs take at once.
+bool by_maps(Maps &m, const ScanArgs &p, bool wide, size_t esz, int tile, int ctas) {
+    if (!wide || tiles_in_all(p) <= 152u * ctas) return false;
+    return make_map(&m.x, p.x, p.xb, p.xt, p, esz, tile) && make_map(&m.gate, p.gate, p.gb, p.gt, p, esz, tile) &&
+           (!p.dy || make_map(&m.dy, p.dy, p.db, p.dt, p, esz, tile));
+}
+
 // kBuffers of `tile` rows a CTA; as many CTAs as the SMs hold at once.
 template <int kBuffers, int kCtas, auto kKernel>
-cudaError_t run_ring(const ScanArgs &p, bool wide, int row, int tile, int block, cudaStream_t s) {
+cudaError_t run_ring(const ScanArgs &p, bool wide, const Maps &maps, int row, int tile, int block, cudaStream_t s) {
     constexpr int kMaxDevices = 64, kSms = 152;
     static std::atomic<bool> done[kMaxDevices];
     const int smem = kBuffers * tile * row;
@@ -1056,8 +1158,8 @@ cudaError_t run_ring(const ScanArgs &p, bool wide, int row, int tile, int block,
     }
     const unsigned most = kCtas * kSms, tiles = tiles_in_all(p);
     const unsigned grid = tiles < most ? tiles : most;
-    if (p.head) return launch_dependent(kKernel, dim3(grid), dim3(block), smem, s, p, wide);
-    kKernel<<<grid, block, smem, s>>>(p, wide);
+    if (p.head) return launch_dependent(kKernel, dim3(grid), dim3(block), smem, s, p, wide, maps);
+    kKernel<<<grid, block, smem, s>>>(p, wide, maps);
     return cudaGetLastError();
 }
 
@@ -1122,13 +1224,17 @@ kla_status kla_gated_scan_fwd(const void *x, const void *gate, const int64_t *st
         constexpr bool kLog = decltype(log)::value;
         constexpr Shape r = fwd_shape(sizeof(E), true), o = fwd_shape(sizeof(E), false);
         static_assert(r.tile() % KLA_SCAN_SPAN == 0 && o.tile() % KLA_SCAN_SPAN == 0 && KLA_SCAN_SPAN % r.tok == 0, "");
+        Maps maps{};
+        if (even && by_maps(maps, p, wide, esz, r.tile(), r.ctas))
+            return run_ring<3, r.ctas, scan_fwd_ring_kernel<E, kLog, kTma, r.tok, r.warps, r.ctas>>(
+                p, wide, maps, kEvenRow, r.tile(), 32 * r.warps, cs);
         if (even)
-            return run_ring<3, r.ctas, scan_fwd_ring_kernel<E, kLog, false, r.tok, r.warps, r.ctas>>(
-                p, wide, kEvenRow, r.tile(), 32 * r.warps, cs);
+            return run_ring<3, r.ctas, scan_fwd_ring_kernel<E, kLog, kEven, r.tok, r.warps, r.ctas>>(
+                p, wide, maps, kEvenRow, r.tile(), 32 * r.warps, cs);
         if constexpr (sizeof(E) == 2) {
             if (ring)
-                return run_ring<3, r.ctas, scan_fwd_ring_kernel<E, kLog, true, r.tok, r.warps, r.ctas>>(
-                    p, false, kOddRow, r.tile(), 32 * r.warps, cs);
+                return run_ring<3, r.ctas, scan_fwd_ring_kernel<E, kLog, kOdd, r.tok, r.warps, r.ctas>>(
+                    p, false, maps, kOddRow, r.tile(), 32 * r.warps, cs);
             scan_fwd_kernel<E, kLog, o.tok, o.warps><<<tiles_in_all(p), 32 * o.warps, 0, cs>>>(p);
         }
         return cudaGetLastError();
@@ -1181,13 +1287,17 @@ kla_status kla_gated_scan_bwd(const void *x, const void *gate, const void *dy, c
         constexpr bool kLog = decltype(log)::value;
         constexpr Shape r = bwd_shape(), o = r;
         static_assert(r.tile() % KLA_SCAN_SPAN == 0 && o.tile() % KLA_SCAN_SPAN == 0 && KLA_SCAN_SPAN % r.tok == 0, "");
+        Maps maps{};
+        if (even && by_maps(maps, p, wide, esz, r.tile(), r.ctas))
+            return run_ring<5, r.ctas, scan_bwd_ring_kernel<E, kLog, kTma, r.tok, r.warps, r.ctas>>(
+                p, wide, maps, kEvenRow, r.tile(), 32 * (r.warps + 1), cs);
         if (even)
-            return run_ring<5, r.ctas, scan_bwd_ring_kernel<E, kLog, false, r.tok, r.warps, r.ctas>>(
-                p, wide, kEvenRow, r.tile(), 32 * (r.warps + 1), cs);
+            return run_ring<5, r.ctas, scan_bwd_ring_kernel<E, kLog, kEven, r.tok, r.warps, r.ctas>>(
+                p, wide, maps, kEvenRow, r.tile(), 32 * (r.warps + 1), cs);
         if constexpr (sizeof(E) == 2) {
             if (ring)
-                return run_ring<5, r.ctas, scan_bwd_ring_kernel<E, kLog, true, r.tok, r.warps, r.ctas>>(
-                    p, false, kOddRow, r.tile(), 32 * (r.warps + 1), cs);
+                return run_ring<5, r.ctas, scan_bwd_ring_kernel<E, kLog, kOdd, r.tok, r.warps, r.ctas>>(
+                    p, false, maps, kOddRow, r.tile(), 32 * (r.warps + 1), cs);
             scan_bwd_kernel<E, kLog, o.tok, o.warps><<<tiles_in_all(p), 32 * o.warps, 0, cs>>>(p);
         }
         return cudaGetLastError();

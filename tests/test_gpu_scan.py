@@ -99,6 +99,14 @@ def test_ragged_batches(dtype, mode):
     check(2, 5, 8, dtype, mode, lengths=[9, -3])   # taken into [0, T]
 
 
+@pytest.mark.parametrize("C,dtype", [(2056, torch.bfloat16), (1992, torch.bfloat16), (1036, torch.float32)])
+@pytest.mark.parametrize("mode,packed", [("sigmoid", False), ("log", True)])
+def test_tiles_by_tensor_maps(C, dtype, mode, packed):
+    """More tiles than the SMs take at once, of rows that fit 16 bytes: the last channels' and the last tokens' are there in
+    part, sequences end within a tile, at its border and before any."""
+    check(4, 700, C, dtype, mode, seed=C, lengths=[700, 513, 0, 256], packed=packed)
+
+
 def test_without_states():
     check(2, 200, 40, torch.float32, "sigmoid", state=False)
     check(2, 200, 40, torch.bfloat16, "log", state=False)
