@@ -155,7 +155,7 @@ __device__ __forceinline__ uint2 hear(const uint2 *p) {
 template <int kV>
 __device__ __forceinline__ bool entering(const uint2 *p, int64_t hop, int left, int count, const Head *head,
                                          float (&h)[kV]) {
-    constexpr int kAhead = 4;
+    constexpr int kAhead = 3;
     constexpr unsigned kLimit = 1u << 21;
 #pragma unroll
     for (int v = 0; v < kV; ++v) h[v] = 0.f;
