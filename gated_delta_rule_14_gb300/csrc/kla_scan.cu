@@ -14,9 +14,10 @@
 // tell each other through the workspace, in one pass; a pass for the tiles' maps and one for the outputs would move 10
 // bytes forward. Backward, the states are walked again from one kept every 128 tokens (0.03 bytes a value), which is
 // exact and cheaper than reading the outputs back.
-// Measured: 131072 x 2048 forward 289 us (5.6 TB/s, 82 % of a copy's rate), backward 530 us (5.1 TB/s); 8 x 4096 x 2048
-// forward 79 us (5.1 TB/s), backward 120 us (5.6 TB/s); in fp32 8 x 2048 x 2048 95 and 146 us. A thread per channel that
-// walks all tokens took 120 ms for the first. By the counters (8 x 2048 x 2048) 21 instructions a value forward, at 1.8
+// Measured: 131072 x 2048 forward 281 us (5.7 TB/s, 84 % of a copy's rate; in a row 273), backward 508 us (5.3 TB/s); 8 x
+// 4096 x 2048 forward 71 us (5.6 TB/s), backward 111 us (6.0 TB/s); in fp32 8 x 2048 x 2048 85 and 130 us. Where channels
+// are few the chain of tiles is what is waited for, four of them a trip to L2, 0.7 us: 131072 x 512 128 and 233 us,
+// 131072 x 64 92 and 154. A thread per channel that walks all tokens took 120 ms for the first. By the counters (8 x 2048 x 2048) 21 instructions a value forward, at 1.8
 // of 4 a cycle, of whose warps' time a quarter waits for the chain, and 40 backward at 2.2 of 4: registers hold 16 warps
 // an SM, and with those neither the issue slots nor the memory (3.9 TB/s there) are full.
 #include <cuda.h>
@@ -96,30 +97,35 @@ __device__ __forceinline__ void put(T *p, const float (&v)[1]) { *p = from_f32<T
 
 // What a tile tells the next ones of a channel, in one 64-bit word (whose two halves arrive together, so that no
 // fences are needed): first how it maps the state that enters it, {A, H}: h -> A h + H; then, once that state is
-// known, {kWhole, the state that leaves it}. A workspace of set bits says nothing yet.
+// known, {kWhole, the state that leaves it}. A workspace of set bits says nothing yet. A lane's words of two channels are
+// told and heard by one access where they lie on 16 bytes (kPairs), of which each is whole by itself.
 constexpr unsigned kEmpty = 0xffffffffu, kWhole = 0xfffffffeu, kNan = 0x7fffffffu;
 __device__ __forceinline__ unsigned factor_bits(float a) { return a == a ? __float_as_uint(a) : kNan; }
-template <int kV>
+__device__ __forceinline__ unsigned long long bits(uint2 v) { return static_cast<unsigned long long>(v.y) << 32 | v.x; }
+template <int kV, bool kPairs>
 __device__ __forceinline__ void tell(uint2 *p, int count, const uint2 (&v)[kV]) {   // of the first `count` channels
+    if constexpr (kPairs) {
+        if (count > 0)
+            asm volatile("st.relaxed.gpu.global.v2.b64 [%0], {%1, %2};" ::"l"(p), "l"(bits(v[0])), "l"(bits(v[1])) : "memory");
+    } else {
 #pragma unroll
-    for (int i = 0; i < kV; ++i)
-        if (i < count) asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(p + i),
-                     "l"(static_cast<unsigned long long>(v[i].y) << 32 | v[i].x)
-                     : "memory");
+        for (int i = 0; i < kV; ++i)
+            if (i < count) asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(p + i), "l"(bits(v[i])) : "memory");
+    }
 }
-template <int kV>
+template <int kV, bool kPairs = false>
 __device__ __forceinline__ void tell_map(uint2 *p, int count, const float (&A)[kV], const float (&H)[kV]) {
     uint2 w[kV];
 #pragma unroll
     for (int v = 0; v < kV; ++v) w[v] = make_uint2(factor_bits(A[v]), __float_as_uint(H[v]));
-    tell<kV>(p, count, w);
+    tell<kV, kPairs>(p, count, w);
 }
-template <int kV>
+template <int kV, bool kPairs = false>
 __device__ __forceinline__ void tell_state(uint2 *p, int count, const float (&h)[kV]) {
     uint2 w[kV];
 #pragma unroll
     for (int v = 0; v < kV; ++v) w[v] = make_uint2(kWhole, __float_as_uint(h[v]));
-    tell<kV>(p, count, w);
+    tell<kV, kPairs>(p, count, w);
 }
 // The state at the chain's start (zeros where none is given), and at its end where that is wanted.
 template <int kV>
@@ -140,31 +146,41 @@ __device__ __forceinline__ void give_up(const ScanArgs &p) {
         if (p.head) *const_cast<volatile unsigned *>(&p.head->abort) = 0u;
     }
 }
-__device__ __forceinline__ uint2 hear(const uint2 *p) {
-    unsigned long long v;
-    asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
-    return make_uint2(static_cast<unsigned>(v), static_cast<unsigned>(v >> 32));
+template <int kV, bool kPairs>
+__device__ __forceinline__ void hear(const uint2 *p, int count, uint2 (&v)[kV]) {
+    unsigned long long w[kV];
+#pragma unroll
+    for (int i = 0; i < kV; ++i) w[i] = kEmpty;
+    if constexpr (kPairs) {
+        if (count > 0) asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];" : "=l"(w[0]), "=l"(w[1]) : "l"(p) : "memory");
+    } else {
+#pragma unroll
+        for (int i = 0; i < kV; ++i)
+            if (i < count) asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(w[i]) : "l"(p + i) : "memory");
+    }
+#pragma unroll
+    for (int i = 0; i < kV; ++i) v[i] = make_uint2(static_cast<unsigned>(w[i]), static_cast<unsigned>(w[i] >> 32));
 }
 
 // The state that enters a tile, from what the `left` tiles before it told: `p` is the nearest one's word of this
 // thread's first channel, `hop` leads to the next further one. Of the nearest kAhead tiles one has to know the state
 // that leaves it, and the maps of those in between are applied to that in their order, as they apply them
-// themselves: whatever is known when, the bits are the same. The chain's first tile tells kWhole at once. Tiles are
+// themselves: whatever is known when, the bits are the same. (kAhead of 3, 4 and 6, us, forward and backward: 131072 x 64
+// 109 + 194, 92 + 154, 79 + 180; 131072 x 1024 181 + 337, 172 + 312, 171 + 377; 131072 x 2048 279 + 509, 281 + 508,
+// 298 + 610.) The chain's first tile tells kWhole at once. Tiles are
 // taken by ticket in the order of the chain, so that all of those are running or done and none of them waits for a
 // later one: the wait ends. Its limit is for what cannot be foreseen. Run by a whole warp; false where it gave up.
-template <int kV>
+template <int kV, bool kPairs = false>
 __device__ __forceinline__ bool entering(const uint2 *p, int64_t hop, int left, int count, const Head *head,
                                          float (&h)[kV]) {
-    constexpr int kAhead = 3;
+    constexpr int kAhead = 4;
     constexpr unsigned kLimit = 1u << 21;
 #pragma unroll
     for (int v = 0; v < kV; ++v) h[v] = 0.f;
     for (unsigned polls = 0; polls < kLimit; ++polls) {
         uint2 w[kAhead][kV];
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-#pragma unroll
-            for (int v = 0; v < kV; ++v) w[j][v] = v < count && j < left ? hear(p + j * hop + v) : make_uint2(kEmpty, 0u);
+        for (int j = 0; j < kAhead; ++j) hear<kV, kPairs>(p + j * hop, j < left ? count : 0, w[j]);
         int found[kV];
         bool known = true;
 #pragma unroll
@@ -465,8 +481,8 @@ __global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(ScanArgs p) {
 
 // Tokens of a thread, warps at them and CTAs of an SM. Each side of the choice at 8 x 4096 x 2048 bf16 and, in fp32, 8 x
 // 2048 x 2048, us: forward 32 tokens x 8 warps x 2 CTAs 82 and 102, 16 x 8 x 3 89 and 95; backward 16 x 8 x 2 138 and 181,
-// 16 x 4 x 4 134 and 179, but 609 instead of 525 at 1 x 131072 x 2048, whose chain gets twice as long (all before the
-// backward pass had its warp for the chain).
+// 16 x 4 x 4 134 and 179, but 609 instead of 525 at 1 x 131072 x 2048, whose chain gets twice as long (all by copies of the
+// warps' own, and before the backward pass had its warp for the chain: 71 and 85, 111 and 130 since).
 struct Shape {
     int tok, warps, ctas;
     constexpr int tile() const { return tok * warps; }
@@ -690,6 +706,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) scan_fwd_ring_kernel(ScanA
     using L = Lane<T, kLog, false>;
     using V = typename L::V;
     constexpr int kTile = kTok * kWarps, kV = L::kV, kWidth = 32 * kV, kRow = kBy == kOdd ? kOddRow : kEvenRow;
+    constexpr bool kPairs = kV == 2 && kBy != kOdd;
     extern __shared__ __align__(128) uint8_t buf[];   // x twice, gate once: kTile rows each
     __shared__ V map_a[kWarps][32], map_h[kWarps][32], enter[32];
     __shared__ unsigned s_next;
@@ -782,16 +799,16 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) scan_fwd_ring_kernel(ScanA
         if (teller) {
             H = L::fma(A, ph, H);
             A = L::mul(A, pa);
-            if (at.at > 0 && at.at < last) tell_map<kV>(here, count, parts(A), parts(H));
+            if (at.at > 0 && at.at < last) tell_map<kV, kPairs>(here, count, parts(A), parts(H));
         }
         if (next < turns.total) fetch(next, stage ^ 1);
         if (teller) {
             float in[kV];
             if (at.at == 0) start<kV>(p, b, c, count, in);
-            else if (!entering<kV>(here - p.C, -static_cast<int64_t>(p.C), at.at, count, p.head, in)) give_up(p);
+            else if (!entering<kV, kPairs>(here - p.C, -static_cast<int64_t>(p.C), at.at, count, p.head, in)) give_up(p);
             enter[lane] = whole<kV>(in);
             H = L::fma(A, enter[lane], H);
-            if (at.at < last) tell_state<kV>(here, count, parts(H));
+            if (at.at < last) tell_state<kV, kPairs>(here, count, parts(H));
             else finish<kV>(p, b, c, count, parts(H));
         }
         __syncthreads();
@@ -822,8 +839,8 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) scan_fwd_ring_kernel(ScanA
     }
 }
 
-// The backward pass has a warp for the chain beside those for the tokens (138 -> 122 us at 8 x 4096 x 2048; the forward
-// pass needs its registers more and lost by it, 82 -> 87). Barriers: `maps` completes when every warp has left the map of
+// The backward pass has a warp for the chain beside those for the tokens (138 -> 122 us at 8 x 4096 x 2048, before tiles
+// came by tensor maps; the forward pass needs its registers more and lost by it, 82 -> 87). Barriers: `maps` completes when every warp has left the map of
 // its tokens, `carry` when what enters them is there; next[i] when the ticket of the tile after one of parity i is.
 template <typename V, int kWarps>
 struct Shared {
@@ -838,6 +855,7 @@ __device__ __forceinline__ void carry_warp(const ScanArgs &p, Shared<typename L:
                                            unsigned ticket, int tile_tokens, F fetch_tile) {
     using V = typename L::V;
     constexpr int kV = L::kV;
+    constexpr bool kPairs = kV == 2 && kBy != kOdd;
     using namespace ptx;
     const int lane = threadIdx.x & 31;
     const uint32_t b_maps = smem_u32(&sh.maps), b_carry = smem_u32(&sh.carry), b_next = smem_u32(sh.next);
@@ -878,11 +896,11 @@ __device__ __forceinline__ void carry_warp(const ScanArgs &p, Shared<typename L:
             if (tile == last) {
                 start<kV>(p, b, c, count, in);
             } else {
-                if (tile > 0) tell_map<kV>(here, count, parts(pa), parts(pd));
-                if (!entering<kV>(here + p.C, p.C, last - tile, count, p.head, in)) give_up(p);
+                if (tile > 0) tell_map<kV, kPairs>(here, count, parts(pa), parts(pd));
+                if (!entering<kV, kPairs>(here + p.C, p.C, last - tile, count, p.head, in)) give_up(p);
             }
             const V e = whole<kV>(in), out = L::fma(pa, e, pd);
-            if (tile > 0) tell_state<kV>(here, count, parts(out));
+            if (tile > 0) tell_state<kV, kPairs>(here, count, parts(out));
             else finish<kV>(p, b, c, count, parts(out));
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) sh.enter[w][lane] = L::fma(after_a[w], e, after_d[w]);
@@ -1011,8 +1029,12 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kCtas) scan_bwd_ring_kernel
                 }
         });
         ok = ok && mbar_wait_bounded(b_carry, turn & 1, kWaits);
-        if (!__all_sync(0xffffffffu, ok)) {
+        if (!__all_sync(0xffffffffu, ok)) {   // not before what is on its way here has come
             copies_wait();
+            if (kBy == kTma) {
+                mbar_wait_bounded(b_full + 8 * stage, turn >> 1 & 1, kWaits);
+                mbar_wait_bounded(b_full + 8 * (stage ^ 1), (turn + 1) >> 1 & 1, kWaits);
+            }
             give_up(p);
             return;
         }
@@ -1134,7 +1156,8 @@ bool make_map(CUtensorMap *m, const void *base, int64_t sb, int64_t st, const Sc
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 // By tensor maps where rows fit 16 bytes, none is broadcast, and there are tiles enough for the maps' making (a
-// microsecond of the host's) to be worth it: more than the SMs take at once.
+// microsecond of the host's) to be worth it: more than the SMs take at once. 8 x 4096 x 2048 by the warps' copies and by
+// maps: forward 79 and 72 us, backward 120 and 111; fp32 8 x 2048 x 2048 97 and 85, 146 and 130.
 bool by_maps(Maps &m, const ScanArgs &p, bool wide, size_t esz, int tile, int ctas) {
     if (!wide || tiles_in_all(p) <= 152u * ctas) return false;
     return make_map(&m.x, p.x, p.xb, p.xt, p, esz, tile) && make_map(&m.gate, p.gate, p.gb, p.gt, p, esz, tile) &&
