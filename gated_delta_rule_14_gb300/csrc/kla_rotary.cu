@@ -383,6 +383,56 @@ cudaError_t run(const RotaryArgs &p, int B, bool half, cudaStream_t s) {
     return run<T, 1>(p, half, s);
 }
 
+// Whether two tensors of equal strides share an element: whether `apart`, the distance of their starts in values, is a sum
+// of strides times differences of indexes, which lie within lo and hi. Axes come in the order of their strides, so that
+// those behind one reach a little further than its stride at most, and leave two or three differences to try.
+struct Axis {
+    int64_t stride, lo, hi;
+};
+bool meet(const Axis *axes, int n, int64_t apart) {
+    int64_t least = 0, most = 0;
+    for (int i = 0; i < n; ++i) {
+        least += axes[i].stride * axes[i].lo;
+        most += axes[i].stride * axes[i].hi;
+    }
+    if (apart < least || apart > most) return false;
+    if (n == 0) return true;
+    const Axis &a = axes[0];
+    if (a.stride == 0) return meet(axes + 1, n - 1, apart);
+    least -= a.stride * a.lo;
+    most -= a.stride * a.hi;
+    // stride * i within apart - most .. apart - least
+    auto below = [&](int64_t v) { return v >= 0 ? v / a.stride : -((-v + a.stride - 1) / a.stride); };   // rounded down
+    int64_t i = -below(most - apart), last = below(apart - least);
+    if (i < a.lo) i = a.lo;
+    if (last > a.hi) last = a.hi;
+    if (last - i > 8) return true;   // strides that overlap among themselves
+    for (; i <= last; ++i)
+        if (meet(axes + 1, n - 1, apart - a.stride * i)) return true;
+    return false;
+}
+// The same of queries and keys, where an output of the one may lie over an input of the other: slices of a packed
+// projection reach over each other without sharing anything. Those have equal strides; of others it is not asked.
+bool share(const void *q, const int64_t *qs, const void *k, const int64_t *ks, const int *H, int B, int T, int d, int esz) {
+    const int64_t bytes = static_cast<const char *>(k) - static_cast<const char *>(q);
+    if (bytes % esz) return true;
+    const int64_t size[2][4] = {{B, T, H[0], d}, {B, T, H[1], d}};
+    Axis axes[4];
+    for (int a = 0; a < 4; ++a) {   // k's index less q's, times the stride, is minus their distance
+        const int64_t sq = a < 3 ? qs[a] : 1, sk = a < 3 ? ks[a] : 1;
+        if (size[0][a] > 1 && size[1][a] > 1 && sq != sk) return true;
+        axes[a] = {size[0][a] > 1 ? sq : sk, 1 - size[1][a], size[0][a] - 1};
+    }
+    for (int a = 0; a < 4; ++a)
+        for (int b = a + 1; b < 4; ++b)
+            if (axes[b].stride > axes[a].stride) {
+                const Axis t = axes[a];
+                axes[a] = axes[b];
+                axes[b] = t;
+            }
+    return meet(axes, 4, bytes / esz);
+}
+
 }  // namespace
 }  // namespace kla
 
@@ -440,6 +490,10 @@ extern "C" kla_status kla_rotary(const void *q, const void *k, void *q_out, void
         if (in_place[m]) continue;
         if (overlaps(os[m], is[0]) || overlaps(os[m], is[1]) || overlaps(os[m], os[1 - m])) return KLA_ERR_INVALID_ARG;
     }
+    // in place: the other's input, which may be read later, is not written over
+    if (H[1] > 0 && (in_place[0] || in_place[1]) && overlaps(is[0], is[1]) &&
+        share(q, p.is[0], k, p.is[1], H, B, T, d, static_cast<int>(esz)))
+        return KLA_ERR_INVALID_ARG;
     p.freqs = freqs;
     p.positions = positions;
     p.wide = positions_are_64 != 0;

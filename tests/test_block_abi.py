@@ -104,6 +104,18 @@ def test_rotary(lib, kw, code):
     assert rotary(lib, **kw) == code
 
 
+@pytest.mark.parametrize("kw", [
+    dict(k=A, oq=A, ok=A, K=4),                                        # queries and keys are one tensor, both in place
+    dict(k=A, K=4, oq=A),                                              # the keys read what the queries write over
+    dict(k=A + 3 * 16 * 4, oq=A),                                      # the keys start at the queries' last head
+    dict(k=A + 64 * 4, K=4, oq=A, st=strides(192, 64, 16, 192, 64, 16, 192, 64, 16, 192, 64, 16)),   # a token later
+    # slices of [2, 3, 5, 16], where the keys' two heads are the queries' last and the one behind
+    dict(k=A + 3 * 16 * 4, oq=A, ok=A + 3 * 16 * 4, st=strides(240, 80, 16, 240, 80, 16, 240, 80, 16, 240, 80, 16)),
+])
+def test_rotary_of_queries_and_keys_that_share_values(lib, kw):
+    assert rotary(lib, dt=0, **kw) == 1
+
+
 def test_gated_norm(lib):
     def f(**kw):
         p = at(6)

@@ -124,6 +124,29 @@ def test_in_place_and_given_outputs():
     assert none is None and torch.equal(single, want[0])
 
 
+@pytest.mark.parametrize("order", [(0, 1, 2, 3), (0, 2, 1, 3), (2, 0, 1, 3), (1, 0, 2, 3)])
+@pytest.mark.parametrize("B,T,H,K", [(2, 50, 4, 4), (3, 7, 6, 2), (1, 9, 3, 1), (4, 1, 1, 1), (2, 16, 2, 8)])
+def test_slices_of_one_tensor_in_place(order, B, T, H, K):
+    """Queries, keys and values of any number of heads beside each other, batch, tokens and heads in any order."""
+    import gated_delta_rule_14_gb300 as kla
+    gen = torch.Generator(device=DEV).manual_seed(16)
+    freqs, _ = kla.rotary_freqs(64, device=DEV)
+    sizes = (B, T, H + 2 * K, 64)
+    packed = torch.randn([sizes[a] for a in order], generator=gen, device=DEV).bfloat16()
+    keep = packed.clone()
+
+    def views(x):
+        x = x.permute([order.index(a) for a in range(4)])
+        return x[:, :, :H], x[:, :, H:H + K], x[:, :, H + K:]
+    (q, k, v), old = views(packed), views(keep)
+    want = kla.rotary_fwd(old[0].contiguous(), old[1].contiguous(), freqs)
+    kla.rotary_fwd(q, k, freqs, out_q=q, out_k=k)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(v, old[2])
+    only, beside = views(keep.clone())[:2]
+    _, turned = kla.rotary_fwd(only, beside, freqs, out_q=only, out_k=torch.empty_like(want[1]))
+    assert torch.equal(only, want[0]) and torch.equal(turned, want[1])
+
+
 def test_no_tokens():
     import gated_delta_rule_14_gb300 as kla
     freqs, _ = kla.rotary_freqs(16, device=DEV)
