@@ -40,6 +40,7 @@ struct NormArgs {
     float *part;              // [parts][sums][n] of dw (and dl), or NULL
     int64_t rows;             // of all groups
     int groups, n;
+    int classes;              // a CTA has rows of one remainder by this: of equal weights, and kOdd: of even or odd number
     float eps;
     int layer, silu;
 };
@@ -87,6 +88,9 @@ __device__ __forceinline__ void copy_in(void *to, const void *from) {
     else
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ptx::smem_u32(to)), "l"(from) : "memory");
 }
+__device__ __forceinline__ void copy_half(void *to, const void *from) {   // 2 bytes, and zeros for the next 2
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, 2;" ::"r"(ptx::smem_u32(to)), "l"(from) : "memory");
+}
 template <int kGroups>
 __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(kGroups) : "memory");
@@ -131,9 +135,11 @@ __device__ __forceinline__ void pack(void *p, const float *v) {
 // A row belongs to a team of `width` threads (4 to 32 lanes of a warp, or whole warps up to the CTA), each with kNV
 // accesses of kBytes at fixed columns, so that weights and the sums of dw and dl stay in registers. Every thread
 // copies its own values of the next kStages - 1 rows into shared memory and takes them from there: no barrier stands
-// between copy and use, and what is on its way does not cost registers. CTAs are persistent. Rows that start on odd
-// bf16, which no such copy takes, and rows of which shared memory holds no two, are loaded as they are needed
-// (kDirect).
+// between copy and use, and what is on its way does not cost registers. CTAs are persistent. Of rows of an odd number of bf16
+// every second one starts in the middle of 4 bytes: a CTA has rows of even or of odd number, and so a thread the same
+// columns of all of them, those of the words as they lie (kOdd). Where the tensors' rows start differently, and of rows of
+// which shared memory holds no two, values are loaded as they are needed (kDirect).
+enum Rows { kRing, kOdd, kDirect };
 constexpr int kMostBlock = 512;
 // Of the operation and the values of a thread: how many CTAs an SM's registers and shared memory hold.
 constexpr int ctas(Op op, int values, int block) {
@@ -145,32 +151,38 @@ constexpr int stages(Op op, int values, int bytes, int block) {   // bytes: of a
     return most > 6 ? 6 : most < 2 ? 2 : most;
 }
 
-template <typename T, int kBytes, int kNV, Op kOp, int kBlock, bool kDirect>
+template <typename T, int kBytes, int kNV, Op kOp, int kBlock, Rows kBy>
 __global__ void __launch_bounds__(kBlock, ctas(kOp, kNV *kBytes / static_cast<int>(sizeof(T)), kBlock))
 block_norm_kernel(NormArgs p, int width) {
     constexpr int kV = kBytes / sizeof(T), kE = kV * kNV, kP = kE / 2, kIns = inputs(kOp);
     constexpr int kStages = stages(kOp, kE, kNV * kBytes, kBlock);
-    constexpr bool kGated = gated(kOp), kBwd = backward(kOp);
+    constexpr bool kGated = gated(kOp), kBwd = backward(kOp), kLoad = kBy == kDirect, kHalves = kBy == kOdd;
     dependency_release();
     extern __shared__ __align__(16) uint8_t ring[];   // [stage][input][access][thread], then [stage][2][thread] of stats
     __shared__ float2 sums[2][kBlock / 32];
     const int team = threadIdx.x / width, lane = threadIdx.x % width, teams = kBlock / width;
-    const int groups = p.w_groups ? p.groups : 1, g = blockIdx.x % groups;   // whose weights this CTA has
-    const int64_t first = blockIdx.x / groups * teams, mine = p.rows / groups;   // 64 bits: sums pass the last row
-    const int step = gridDim.x / groups * teams;
+    const int classes = p.classes, g = blockIdx.x % classes, group = p.w_groups ? g % p.groups : 0;
+    // 64 bits: sums pass the last row
+    const int64_t first = blockIdx.x / classes * teams, mine = (p.rows - g + classes - 1) / classes;
+    const int step = gridDim.x / classes * teams;
     const int turns = first < mine ? static_cast<int>((mine - first + step - 1) / step) : 0;
     const bool four = kOp == kAddBwd && p.in[3] != nullptr;
     float *const stats = reinterpret_cast<float *>(ring + kStages * kIns * kNV * kBlock * kBytes);
     auto slot = [&](int stage, int i, int k) {
         return ring + (((stage * kIns + i) * kNV + k) * kBlock + threadIdx.x) * kBytes;
     };
-    bool there[kNV];   // columns of this thread
-#pragma unroll
-    for (int k = 0; k < kNV; ++k) there[k] = (k * width + lane) * kV < p.n;
     // the next row to be copied, and the one at hand: their index, and the first of their values of this thread
-    const int64_t row0 = (first + team) * groups + g, rows = p.rows;
-    const int hop = step * groups;
-    const int64_t off0 = row0 * p.n + lane * kV, off_hop = static_cast<int64_t>(hop) * p.n;
+    const int64_t row0 = (first + team) * classes + g, rows = p.rows;
+    const int hop = step * classes, before = kHalves ? g & 1 : 0;   // values in front of the row's in its first word
+    const int64_t off0 = row0 * p.n + lane * kV - before, off_hop = static_cast<int64_t>(hop) * p.n;
+    // columns of this thread; kHalves: which of its words has the row's first value alone, and which the last
+    bool there[kNV];
+#pragma unroll
+    for (int k = 0; k < kNV; ++k) there[k] = (k * width + lane) * kV - before < p.n;
+    const int head = kHalves && before && lane == 0 ? 0 : -1;
+    const int tail = kHalves && !before && p.n / 2 % width == lane ? p.n / 2 / width : -1;
+    auto column = [&](int u) { return (u / kV * width + lane) * kV + u % kV - before; };
+    auto inside = [&](int u) { return kHalves ? column(u) >= 0 && column(u) < p.n : there[u / kV]; };
     int64_t ahead = row0, ahead_off = off0;
     auto source = [&](int i, int64_t row, int64_t off) {   // this thread's first values of a row
         if (kGated && i == 1 && p.z_stride) {
@@ -180,7 +192,7 @@ block_norm_kernel(NormArgs p, int width) {
         return static_cast<const T *>(p.in[i]) + off;
     };
     auto fetch = [&](int stage) {
-        if (kDirect) return;
+        if (kLoad) return;
         if (ahead < rows) {
 #pragma unroll
             for (int i = 0; i < kIns; ++i) {
@@ -188,7 +200,8 @@ block_norm_kernel(NormArgs p, int width) {
                 const T *from = source(i, ahead, ahead_off);
 #pragma unroll
                 for (int k = 0; k < kNV; ++k)
-                    if (there[k]) copy_in<kBytes>(slot(stage, i, k), from + k * width * kV);
+                    if (kHalves && k == tail) copy_half(slot(stage, i, k), from + k * width * kV);
+                    else if (there[k]) copy_in<kBytes>(slot(stage, i, k), from + k * width * kV);
             }
             if (kBwd) {
                 copy_in<4>(stats + (stage * 2) * kBlock + threadIdx.x, p.rstd + ahead);
@@ -204,9 +217,10 @@ block_norm_kernel(NormArgs p, int width) {
     float2 w[kP], l[kGated ? 1 : kP], dw[kBwd ? kP : 1], dl[kOp == kAddBwd ? kP : 1];
 #pragma unroll
     for (int u = 0; u < kE; ++u) {
-        const int c = (u / kV * width + lane) * kV + u % kV;
-        set(w[u / 2], u % 2, p.w && c < p.n ? p.w[static_cast<int64_t>(g) * p.n + c] : 1.f);
-        if (!kGated) set(l[u / 2], u % 2, p.l && c < p.n ? p.l[c] : 1.f);
+        const int c = column(u);
+        const bool in = c >= 0 && c < p.n;
+        set(w[u / 2], u % 2, p.w && in ? p.w[static_cast<int64_t>(group) * p.n + c] : 1.f);
+        if (!kGated) set(l[u / 2], u % 2, p.l && in ? p.l[c] : 1.f);
     }
 #pragma unroll
     for (int u = 0; u < kP; ++u) {
@@ -235,14 +249,15 @@ block_norm_kernel(NormArgs p, int width) {
         const bool live = row < rows;
         auto get = [&](int i, float2 (&v)[kP]) {   // zeros past the row's end
             Raw<kBytes> raw[kNV];
-            const T *from = kDirect ? source(i, row, off) : nullptr;
+            const T *from = kLoad ? source(i, row, off) : nullptr;
 #pragma unroll
             for (int k = 0; k < kNV; ++k) {   // all loads before the first use
                 raw[k] = Raw<kBytes>{};
                 if (live && there[k])
-                    raw[k] = kDirect ? *reinterpret_cast<const Raw<kBytes> *>(from + k * width * kV)
-                                     : *reinterpret_cast<const Raw<kBytes> *>(slot(stage, i, k));
+                    raw[k] = kLoad ? *reinterpret_cast<const Raw<kBytes> *>(from + k * width * kV)
+                                   : *reinterpret_cast<const Raw<kBytes> *>(slot(stage, i, k));
             }
+            if (kHalves && head == 0) raw[0].r[0] &= 0xffff0000u;   // its other half is the row's before
 #pragma unroll
             for (int k = 0; k < kNV; ++k) {
                 float e[kV];
@@ -258,7 +273,12 @@ block_norm_kernel(NormArgs p, int width) {
                 float e[kV];
 #pragma unroll
                 for (int j = 0; j < kV; ++j) e[j] = part(v[(k * kV + j) / 2], (k * kV + j) % 2);
-                if (live && there[k]) pack<T, kBytes>(to + k * width * kV, e);
+                if (kHalves && live && (k == head || k == tail)) {
+                    if (k == head) to[1] = from_f32<T>(e[kV - 1]);
+                    else to[k * width * kV] = from_f32<T>(e[0]);
+                } else if (live && there[k]) {
+                    pack<T, kBytes>(to + k * width * kV, e);
+                }
             }
         };
         float2 x[kP];   // what the norm is of, then xh
@@ -271,7 +291,7 @@ block_norm_kernel(NormArgs p, int width) {
         }
         if constexpr (!kBwd) {
             float2 z[kP];
-            if (kGated && kDirect) get(1, z);   // its trip beside the first sum's
+            if (kGated && kLoad) get(1, z);   // its trip beside the first sum's
             if (kOp == kAddFwd) put(1, x);
             float mu = 0.f;
             if (p.layer) {
@@ -282,8 +302,8 @@ block_norm_kernel(NormArgs p, int width) {
 #pragma unroll
                 for (int u = 0; u < kP; ++u) {
                     x[u] = add2(x[u], both(-mu));
-                    if (!there[2 * u / kV]) x[u].x = 0.f;
-                    if (!there[(2 * u + 1) / kV]) x[u].y = 0.f;
+                    if (!inside(2 * u)) x[u].x = 0.f;
+                    if (!inside(2 * u + 1)) x[u].y = 0.f;
                 }
             }
             float2 q = both(0.f);
@@ -294,7 +314,7 @@ block_norm_kernel(NormArgs p, int width) {
                 if (p.mean) p.mean[row] = mu;
                 if (p.rstd) p.rstd[row] = rs;
             }
-            if (kGated && !kDirect) get(1, z);
+            if (kGated && !kLoad) get(1, z);
 #pragma unroll
             for (int u = 0; u < kP; ++u) {
                 x[u] = mul2(mul2(x[u], both(rs)), w[u]);
@@ -302,10 +322,10 @@ block_norm_kernel(NormArgs p, int width) {
             }
             put(0, x);
         } else {
-            const float rs = !live ? 0.f : kDirect ? p.rstd[row] : stats[(stage * 2) * kBlock + threadIdx.x];
+            const float rs = !live ? 0.f : kLoad ? p.rstd[row] : stats[(stage * 2) * kBlock + threadIdx.x];
             const float mu =
-                !live || !p.layer ? 0.f : kDirect ? p.mean[row] : stats[(stage * 2 + 1) * kBlock + threadIdx.x];
-            constexpr bool kEarly = kOp == kAddBwd && kDirect && kE <= 8;   // what is used after the sums, asked for here
+                !live || !p.layer ? 0.f : kLoad ? p.mean[row] : stats[(stage * 2 + 1) * kBlock + threadIdx.x];
+            constexpr bool kEarly = kOp == kAddBwd && kLoad && kE <= 8;   // what is used after the sums, asked for here
             float2 x0[kEarly ? kP : 1], ds[kEarly ? kP : 1];
             if constexpr (kEarly) {
                 get(0, x0);
@@ -385,8 +405,8 @@ block_norm_kernel(NormArgs p, int width) {
                 const float2 &pair = which ? dl[kOp == kAddBwd ? u / 2 : 0] : dw[u / 2];
                 float v = part(pair, u % 2);
                 for (int off = width; off < 32; off *= 2) v += across(v, off);
-                const int c = (u / kV * width + lane) * kV + u % kV;
-                if (c < p.n && (threadIdx.x & 31) == lane % 32) acc[owner * p.n + c] = v;
+                const int c = column(u);
+                if (c >= 0 && c < p.n && (threadIdx.x & 31) == lane % 32) acc[owner * p.n + c] = v;
             }
             __syncthreads();
             for (int c = threadIdx.x; c < p.n; c += kBlock) {
@@ -585,15 +605,15 @@ bool apart(const Span (&outs)[kOuts], const Span (&ins)[kIns]) {
 // CTA.
 struct Plan {
     int bytes, nv, width, block;
-    int grid;   // CTAs, a multiple of the groups with weights of their own
+    int grid;   // CTAs, a multiple of the classes of rows
     bool direct() const { return bytes == 2 || nv > (bytes == 16 ? 2 : 8); }
 };
-// Rows start on `bytes` bytes. A thread takes 32 bytes of a row, so that a row's share of the sums, the addresses and
+// Rows start on `bytes` bytes, or are of odd bf16 (4). A thread takes 32 bytes of a row, so that a row's share of the sums, the addresses and
 // the loop is spread over many values (with 16 bytes 32768 x 16 heads of 128 took 85 us instead of 78, and 124
 // instead of 120), or 64 of rows of fp32 that shared memory holds no two of.
-Plan plan(int64_t rows, int groups, int n, int esz, int bytes, Op op) {
+Plan plan(int64_t rows, int classes, int n, int esz, int bytes, Op op) {
     Plan p{bytes, bytes == 16 ? 2 : 8, 4, 256, 0};
-    const int accesses = n * esz / bytes;
+    const int accesses = (n * esz + bytes - 1) / bytes;
     if ((esz == 4 || bytes == 2) && accesses > kMostBlock * p.nv) p.nv *= 2;
     if (accesses > kMostBlock * p.nv) {
         p.bytes = 0;
@@ -603,12 +623,14 @@ Plan plan(int64_t rows, int groups, int n, int esz, int bytes, Op op) {
     }
     while (p.width * p.nv < accesses) p.width *= 2;
     if (p.width > p.block || p.nv == (bytes == 16 ? 4 : 16)) p.block = kMostBlock;
-    const int64_t teams = p.block / p.width, of_group = (rows / groups + teams - 1) / teams;
-    int64_t want = (static_cast<int64_t>(kSms) * ctas(op, p.nv * bytes / esz, p.block) + groups - 1) / groups;
-    if (want > of_group) want = of_group;
-    p.grid = static_cast<int>((want < 1 ? 1 : want) * groups);
+    const int64_t teams = p.block / p.width, of_class = (rows / classes + teams - 1) / teams;
+    int64_t want = (static_cast<int64_t>(kSms) * ctas(op, p.nv * bytes / esz, p.block) + classes - 1) / classes;
+    if (want > of_class) want = of_class;
+    p.grid = static_cast<int>((want < 1 ? 1 : want) * classes);
     return p;
 }
+// Of groups with weights of their own, each of even or odd rows where that matters.
+int classes_of(int groups, bool odd) { return odd && groups % 2 ? 2 * groups : groups; }
 // Parts of the rows that block_norm_any_sums_kernel takes side by side.
 int any_parts(int64_t rows, int groups, int n) {
     const int64_t tiles = static_cast<int64_t>((n + 31) / 32) * groups, most = (rows / groups + 255) / 256;
@@ -623,26 +645,26 @@ size_t workspace_bytes_of(int64_t rows, int groups, int n, int esz, Op op) {
     size_t most = any_means_bytes(rows) + static_cast<size_t>(any_parts(rows, groups, n)) * groups * sums * n * 4;
     for (int bytes : {16, 4, 2}) {
         if (bytes < esz) continue;
-        const Plan p = plan(rows, groups, n, esz, bytes, op);
+        const Plan p = plan(rows, classes_of(groups, esz == 2 && bytes == 4 && n % 2), n, esz, bytes, op);
         const size_t need = p.bytes ? static_cast<size_t>(p.grid) * sums * n * 4 : 0;
         if (need > most) most = need;
     }
     return most;
 }
 
-template <typename T, int kBytes, int kNV, Op kOp, int kBlock, bool kDirect>
+template <typename T, int kBytes, int kNV, Op kOp, int kBlock, Rows kBy>
 cudaError_t run_rows(const NormArgs &a, const Plan &p, cudaStream_t s) {
     constexpr int kMaxDevices = 64;
     static std::atomic<bool> done[kMaxDevices];
     constexpr int kS = stages(kOp, kNV * kBytes / static_cast<int>(sizeof(T)), kNV * kBytes, kBlock);
     constexpr int kSums = backward(kOp) ? kBlock * kNV * kBytes / static_cast<int>(sizeof(T)) * 4 : 0;
     constexpr int kRing =
-        kDirect ? kSums : kS * kBlock * (inputs(kOp) * kNV * kBytes + (backward(kOp) ? 8 : 0));
+        kBy == kDirect ? kSums : kS * kBlock * (inputs(kOp) * kNV * kBytes + (backward(kOp) ? 8 : 0));
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    auto kernel = block_norm_kernel<T, kBytes, kNV, kOp, kBlock, kDirect>;
+    auto kernel = block_norm_kernel<T, kBytes, kNV, kOp, kBlock, kBy>;
     if (!done[dev].load(std::memory_order_acquire)) {   // once per device and kernel: the attribute outlasts the call
         if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing)) != cudaSuccess)
             return e;
@@ -658,32 +680,37 @@ template <typename T, Op kOp>
 cudaError_t run(NormArgs a, float *dw, float *dl, void *workspace, cudaStream_t s) {
     constexpr int kSums = kOp == kAddBwd ? 2 : 1;
     const int groups = a.w_groups ? a.groups : 1, esz = sizeof(T);
-    auto fits = [&](int bytes) {
-        if (a.n * esz % bytes || (a.z_stride * esz) % bytes) return false;
+    auto start = [&](int bytes) {
         for (const void *q : {a.in[0], a.in[1], a.in[2], a.in[3], static_cast<const void *>(a.out[0]),
                               static_cast<const void *>(a.out[1])})
             if (!aligned(q, bytes)) return false;
         return true;
     };
-    const Plan p = plan(a.rows, groups, a.n, esz, fits(16) ? 16 : fits(4) ? 4 : 2, kOp);
+    auto fits = [&](int bytes) { return a.n * esz % bytes == 0 && (a.z_stride * esz) % bytes == 0 && start(bytes); };
+    const bool odd = esz == 2 && a.n % 2 && a.z_stride == 0 && start(4);
+    a.classes = classes_of(groups, odd);
+    const Plan p = plan(a.rows, a.classes, a.n, esz, fits(16) ? 16 : odd || fits(4) ? 4 : 2, kOp);
     cudaError_t e;
     if (p.bytes) {
         a.part = static_cast<float *>(workspace);
         const bool large = p.block == 512;
         if constexpr (sizeof(T) == 4) {
             if (p.direct())
-                e = p.bytes == 16 ? run_rows<T, 16, 4, kOp, 512, true>(a, p, s) : run_rows<T, 4, 16, kOp, 512, true>(a, p, s);
+                e = p.bytes == 16 ? run_rows<T, 16, 4, kOp, 512, kDirect>(a, p, s)
+                                  : run_rows<T, 4, 16, kOp, 512, kDirect>(a, p, s);
         } else {
             if (p.direct())
-                e = !large      ? run_rows<T, 2, 8, kOp, 256, true>(a, p, s)
-                    : p.nv == 8 ? run_rows<T, 2, 8, kOp, 512, true>(a, p, s)
-                                : run_rows<T, 2, 16, kOp, 512, true>(a, p, s);
+                e = !large      ? run_rows<T, 2, 8, kOp, 256, kDirect>(a, p, s)
+                    : p.nv == 8 ? run_rows<T, 2, 8, kOp, 512, kDirect>(a, p, s)
+                                : run_rows<T, 2, 16, kOp, 512, kDirect>(a, p, s);
+            else if (odd)
+                e = large ? run_rows<T, 4, 8, kOp, 512, kOdd>(a, p, s) : run_rows<T, 4, 8, kOp, 256, kOdd>(a, p, s);
         }
-        if (p.direct()) {
+        if (p.direct() || odd) {
         } else if (large) {
-            e = p.bytes == 16 ? run_rows<T, 16, 2, kOp, 512, false>(a, p, s) : run_rows<T, 4, 8, kOp, 512, false>(a, p, s);
+            e = p.bytes == 16 ? run_rows<T, 16, 2, kOp, 512, kRing>(a, p, s) : run_rows<T, 4, 8, kOp, 512, kRing>(a, p, s);
         } else {
-            e = p.bytes == 16 ? run_rows<T, 16, 2, kOp, 256, false>(a, p, s) : run_rows<T, 4, 8, kOp, 256, false>(a, p, s);
+            e = p.bytes == 16 ? run_rows<T, 16, 2, kOp, 256, kRing>(a, p, s) : run_rows<T, 4, 8, kOp, 256, kRing>(a, p, s);
         }
         if (e != cudaSuccess || !workspace) return e;
         return launch_dependent(block_norm_join_kernel, dim3((a.n + 31) / 32, groups), 1024, 0, s, a.part, dw, dl,

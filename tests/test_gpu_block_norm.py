@@ -142,6 +142,44 @@ def test_unaligned_starts(shift, n, dtype):
     added((5, n), dtype, shift=shift)
 
 
+@pytest.mark.parametrize("rows,G,n", [(1, 1, 3), (2, 1, 5), (3, 1, 1001), (301, 1, 33), (300, 3, 65), (7, 5, 101),
+                                      (1, 3, 127), (64, 2, 63), (9, 4, 2049), (2000, 1, 511), (5, 1, 8191), (4, 1, 8193)])
+@pytest.mark.parametrize("own,norm", [(False, "rms"), (True, "layer")])
+@pytest.mark.parametrize("slices,shift", [(0, 0), (2, 0), (0, 1)])
+def test_rows_of_odd_length(rows, G, n, own, norm, slices, shift):
+    """Of bf16 every second one starts in the middle of 4 bytes."""
+    gated((rows, G, n), (G, n) if own else (n,), BF, norm, seed=n, slices=slices, shift=shift)
+    added((rows * G, n), BF, norm, seed=n, given=own, shift=shift)
+
+
+@pytest.mark.parametrize("n", [3, 65, 1001, 2047])
+@pytest.mark.parametrize("rows", [1, 2, 41])
+def test_rows_of_odd_length_keep_to_themselves(rows, n):
+    """NaN in a row reach no other, and nothing is written behind the last row."""
+    import gated_delta_rule_14_gb300 as kla
+    r = rnd(n + rows)
+    x, z, dy, ds = (r(rows, n).to(BF) for _ in range(4))
+    w, scale = r(n), r(n)
+    want = kla.gated_norm_fwd(x, z, w), kla.add_norm_fwd(x, z, w, scale)
+    bad = torch.arange(rows, device=DEV) % 2 == 1
+    others = [t.masked_fill(bad[:, None], float("nan")) for t in (x, z)]
+    back = torch.full((2, rows * n + 1), 7.0, dtype=BF, device=DEV)
+    if rows * n % 2:   # the second buffer's rows would start in the middle of 4 bytes
+        back = torch.full((2, rows * n + 3), 7.0, dtype=BF, device=DEV)
+    out = [b[:rows * n].view(rows, n) for b in back]
+    got = kla.gated_norm_fwd(*others, w, out=out[0]), kla.add_norm_fwd(*others, w, scale, out=out[0], out_residual=out[1])
+    y = kla.gated_norm_fwd(*others, w)[0]
+    assert torch.equal(y[~bad], want[0][0][~bad]) and bool(y[bad].isnan().all())
+    assert torch.equal(out[0][~bad], want[1][0][~bad]) and torch.equal(out[1][~bad], want[1][1][~bad])
+    assert bool(out[0][bad].isnan().all()) and bool((back[:, rows * n:] == 7).all())
+    clean = kla.gated_norm_bwd(dy, x, z, w, None, want[0][2]), kla.add_norm_bwd(dy, ds, x, z, w, scale, None, want[1][3])
+    with_nan = (kla.gated_norm_bwd(dy, *others, w, None, got[0][2]),
+                kla.add_norm_bwd(dy, ds, *others, w, scale, None, got[1][3]))
+    for a, b in zip(clean, with_nan):
+        for i in (0, 1):
+            assert torch.equal(a[i][~bad], b[i][~bad]) and bool(b[i][bad].isnan().all())
+
+
 def test_large_offset():
     """Values about 1000 with a spread of 1: the mean is subtracted before squares are summed. A value's fp32 rounding
     is 1000 * 2^-24 = 6e-5 of the spread in the mean: 2e-4."""
