@@ -40,7 +40,7 @@ struct NormArgs {
     float *part;              // [parts][sums][n] of dw (and dl), or NULL
     int64_t rows;             // of all groups
     int groups, n;
-    int classes;              // a CTA has rows of one remainder by this: of equal weights, and kOdd: of even or odd number
+    int classes;              // a CTA has rows of one remainder by this: of equal weights, and kLie: of equal start
     float eps;
     int layer, silu;
 };
@@ -88,8 +88,9 @@ __device__ __forceinline__ void copy_in(void *to, const void *from) {
     else
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ptx::smem_u32(to)), "l"(from) : "memory");
 }
-__device__ __forceinline__ void copy_half(void *to, const void *from) {   // 2 bytes, and zeros for the next 2
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, 2;" ::"r"(ptx::smem_u32(to)), "l"(from) : "memory");
+// The first `size` of 16 bytes, the rest zeros.
+__device__ __forceinline__ void copy_start(void *to, const void *from, int size) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_u32(to)), "l"(from), "r"(size) : "memory");
 }
 template <int kGroups>
 __device__ __forceinline__ void copies_wait() {
@@ -135,11 +136,12 @@ __device__ __forceinline__ void pack(void *p, const float *v) {
 // A row belongs to a team of `width` threads (4 to 32 lanes of a warp, or whole warps up to the CTA), each with kNV
 // accesses of kBytes at fixed columns, so that weights and the sums of dw and dl stay in registers. Every thread
 // copies its own values of the next kStages - 1 rows into shared memory and takes them from there: no barrier stands
-// between copy and use, and what is on its way does not cost registers. CTAs are persistent. Of rows of an odd number of bf16
-// every second one starts in the middle of 4 bytes: a CTA has rows of even or of odd number, and so a thread the same
-// columns of all of them, those of the words as they lie (kOdd). Where the tensors' rows start differently, and of rows of
-// which shared memory holds no two, values are loaded as they are needed (kDirect).
-enum Rows { kRing, kOdd, kDirect };
+// between copy and use, and what is on its way does not cost registers. CTAs are persistent. Rows whose length is no
+// multiple of 16 bytes start in the middle of 16, every second, fourth or eighth at the same place: a CTA has rows of one
+// place, and so a thread the same columns of all of them, those of the 16 bytes as they lie (kLie). Where the tensors' rows
+// start differently that leaves accesses of 4 bytes; of odd bf16 those too are none, and values are loaded as they are
+// needed (kDirect), as are rows of which shared memory holds no two.
+enum Rows { kRing, kLie, kDirect };
 constexpr int kMostBlock = 512;
 // Of the operation and the values of a thread: how many CTAs an SM's registers and shared memory hold.
 constexpr int ctas(Op op, int values, int block) {
@@ -156,7 +158,7 @@ __global__ void __launch_bounds__(kBlock, ctas(kOp, kNV *kBytes / static_cast<in
 block_norm_kernel(NormArgs p, int width) {
     constexpr int kV = kBytes / sizeof(T), kE = kV * kNV, kP = kE / 2, kIns = inputs(kOp);
     constexpr int kStages = stages(kOp, kE, kNV * kBytes, kBlock);
-    constexpr bool kGated = gated(kOp), kBwd = backward(kOp), kLoad = kBy == kDirect, kHalves = kBy == kOdd;
+    constexpr bool kGated = gated(kOp), kBwd = backward(kOp), kLoad = kBy == kDirect;
     dependency_release();
     extern __shared__ __align__(16) uint8_t ring[];   // [stage][input][access][thread], then [stage][2][thread] of stats
     __shared__ float2 sums[2][kBlock / 32];
@@ -173,21 +175,29 @@ block_norm_kernel(NormArgs p, int width) {
     };
     // the next row to be copied, and the one at hand: their index, and the first of their values of this thread
     const int64_t row0 = (first + team) * classes + g, rows = p.rows;
-    const int hop = step * classes, before = kHalves ? g & 1 : 0;   // values in front of the row's in its first word
+    const int hop = step * classes;
+    const int before = kBy == kLie ? static_cast<int>(row0 * p.n % kV) : 0;   // values in front of the row's in its first access
     const int64_t off0 = row0 * p.n + lane * kV - before, off_hop = static_cast<int64_t>(hop) * p.n;
-    // columns of this thread; kHalves: which of its words has the row's first value alone, and which the last
+    int64_t ahead = row0, ahead_off = off0;
+    // columns of this thread; kLie: which of its accesses are the row's first and last, of which it has a part
     bool there[kNV];
 #pragma unroll
     for (int k = 0; k < kNV; ++k) there[k] = (k * width + lane) * kV - before < p.n;
-    const int head = kHalves && before && lane == 0 ? 0 : -1;
-    const int tail = kHalves && !before && p.n / 2 % width == lane ? p.n / 2 / width : -1;
+    const int end = (p.n - 1 + before) / kV, of_end = p.n + before - end * kV;
+    const int head = kBy == kLie && before > 0 && lane == 0 ? 0 : -1;
+    const int tail = kBy == kLie && of_end < kV && end % width == lane ? end / width : -1;
+    uint32_t keep[kBy == kLie ? 4 : 1];   // of the first access
+#pragma unroll
+    for (int i = 0; i < (kBy == kLie ? 4 : 1); ++i) {
+        const int gone = head == 0 ? before * static_cast<int>(sizeof(T)) - 4 * i : 0;
+        keep[i] = gone >= 4 ? 0u : gone == 2 ? 0xffff0000u : ~0u;
+    }
     auto column = [&](int u) { return (u / kV * width + lane) * kV + u % kV - before; };
-    auto inside = [&](int u) { return kHalves ? column(u) >= 0 && column(u) < p.n : there[u / kV]; };
-    int64_t ahead = row0, ahead_off = off0;
+    auto inside = [&](int u) { return kBy == kLie ? column(u) >= 0 && column(u) < p.n : there[u / kV]; };
     auto source = [&](int i, int64_t row, int64_t off) {   // this thread's first values of a row
         if (kGated && i == 1 && p.z_stride) {
             const unsigned r = static_cast<unsigned>(row), outer = r / static_cast<unsigned>(p.groups);
-            off = outer * p.z_stride + static_cast<int64_t>(r - outer * p.groups) * p.n + lane * kV;
+            off = outer * p.z_stride + static_cast<int64_t>(r - outer * p.groups) * p.n + lane * kV - before;
         }
         return static_cast<const T *>(p.in[i]) + off;
     };
@@ -200,7 +210,8 @@ block_norm_kernel(NormArgs p, int width) {
                 const T *from = source(i, ahead, ahead_off);
 #pragma unroll
                 for (int k = 0; k < kNV; ++k)
-                    if (kHalves && k == tail) copy_half(slot(stage, i, k), from + k * width * kV);
+                    if (kBy == kLie && k == tail)
+                        copy_start(slot(stage, i, k), from + k * width * kV, of_end * static_cast<int>(sizeof(T)));
                     else if (there[k]) copy_in<kBytes>(slot(stage, i, k), from + k * width * kV);
             }
             if (kBwd) {
@@ -257,7 +268,9 @@ block_norm_kernel(NormArgs p, int width) {
                     raw[k] = kLoad ? *reinterpret_cast<const Raw<kBytes> *>(from + k * width * kV)
                                    : *reinterpret_cast<const Raw<kBytes> *>(slot(stage, i, k));
             }
-            if (kHalves && head == 0) raw[0].r[0] &= 0xffff0000u;   // its other half is the row's before
+            if constexpr (kBy == kLie)   // what is in front is another row's
+#pragma unroll
+                for (int q = 0; q < 4; ++q) raw[0].r[q] &= keep[q];
 #pragma unroll
             for (int k = 0; k < kNV; ++k) {
                 float e[kV];
@@ -273,9 +286,10 @@ block_norm_kernel(NormArgs p, int width) {
                 float e[kV];
 #pragma unroll
                 for (int j = 0; j < kV; ++j) e[j] = part(v[(k * kV + j) / 2], (k * kV + j) % 2);
-                if (kHalves && live && (k == head || k == tail)) {
-                    if (k == head) to[1] = from_f32<T>(e[kV - 1]);
-                    else to[k * width * kV] = from_f32<T>(e[0]);
+                if (kBy == kLie && live && (k == head || k == tail)) {
+#pragma unroll
+                    for (int j = 0; j < kV; ++j)
+                        if (inside(k * kV + j)) to[k * width * kV + j] = from_f32<T>(e[j]);
                 } else if (live && there[k]) {
                     pack<T, kBytes>(to + k * width * kV, e);
                 }
@@ -601,6 +615,25 @@ bool apart(const Span (&outs)[kOuts], const Span (&ins)[kIns]) {
     return true;
 }
 
+// Rows as they lie: how many start differently, and of how many accesses one is at most.
+int starts_of(int n, int esz) {
+    int m = 1;
+    while (static_cast<int64_t>(n) * esz * m % 16) m *= 2;
+    return m;
+}
+int most_of(int n, int esz) { return (n * esz + 2 * (16 - esz)) / 16; }
+// Classes of rows: of groups with weights of their own, and of those that start alike.
+int classes_of(int groups, int starts) {
+    int m = groups;
+    while (m % starts) m *= 2;
+    return m;
+}
+// Whether rows are taken as they lie, given that all of a row's tensors start alike: where a team holds them, and a part
+// of the sums for each class is not too many.
+bool lies(int groups, int n, int esz) {
+    const int starts = starts_of(n, esz);
+    return starts > 1 && most_of(n, esz) <= 2 * kMostBlock && classes_of(groups, starts) <= 4 * kSms;
+}
 // How rows are taken: `bytes` of an access (0: by block_norm_any_*), accesses of a thread, threads of a team and of a
 // CTA.
 struct Plan {
@@ -608,12 +641,12 @@ struct Plan {
     int grid;   // CTAs, a multiple of the classes of rows
     bool direct() const { return bytes == 2 || nv > (bytes == 16 ? 2 : 8); }
 };
-// Rows start on `bytes` bytes, or are of odd bf16 (4). A thread takes 32 bytes of a row, so that a row's share of the sums, the addresses and
+// Rows start on `bytes` bytes, or as they lie (`lie`, 16). A thread takes 32 bytes of a row, so that a row's share of the sums, the addresses and
 // the loop is spread over many values (with 16 bytes 32768 x 16 heads of 128 took 85 us instead of 78, and 124
 // instead of 120), or 64 of rows of fp32 that shared memory holds no two of.
-Plan plan(int64_t rows, int classes, int n, int esz, int bytes, Op op) {
+Plan plan(int64_t rows, int classes, int n, int esz, int bytes, bool lie, Op op) {
     Plan p{bytes, bytes == 16 ? 2 : 8, 4, 256, 0};
-    const int accesses = (n * esz + bytes - 1) / bytes;
+    const int accesses = lie ? most_of(n, esz) : n * esz / bytes;
     if ((esz == 4 || bytes == 2) && accesses > kMostBlock * p.nv) p.nv *= 2;
     if (accesses > kMostBlock * p.nv) {
         p.bytes = 0;
@@ -629,8 +662,6 @@ Plan plan(int64_t rows, int classes, int n, int esz, int bytes, Op op) {
     p.grid = static_cast<int>((want < 1 ? 1 : want) * classes);
     return p;
 }
-// Of groups with weights of their own, each of even or odd rows where that matters.
-int classes_of(int groups, bool odd) { return odd && groups % 2 ? 2 * groups : groups; }
 // Parts of the rows that block_norm_any_sums_kernel takes side by side.
 int any_parts(int64_t rows, int groups, int n) {
     const int64_t tiles = static_cast<int64_t>((n + 31) / 32) * groups, most = (rows / groups + 255) / 256;
@@ -645,7 +676,8 @@ size_t workspace_bytes_of(int64_t rows, int groups, int n, int esz, Op op) {
     size_t most = any_means_bytes(rows) + static_cast<size_t>(any_parts(rows, groups, n)) * groups * sums * n * 4;
     for (int bytes : {16, 4, 2}) {
         if (bytes < esz) continue;
-        const Plan p = plan(rows, classes_of(groups, esz == 2 && bytes == 4 && n % 2), n, esz, bytes, op);
+        const bool lie = bytes == 16 && lies(groups, n, esz);
+        const Plan p = plan(rows, lie ? classes_of(groups, starts_of(n, esz)) : groups, n, esz, bytes, lie, op);
         const size_t need = p.bytes ? static_cast<size_t>(p.grid) * sums * n * 4 : 0;
         if (need > most) most = need;
     }
@@ -687,9 +719,11 @@ cudaError_t run(NormArgs a, float *dw, float *dl, void *workspace, cudaStream_t 
         return true;
     };
     auto fits = [&](int bytes) { return a.n * esz % bytes == 0 && (a.z_stride * esz) % bytes == 0 && start(bytes); };
-    const bool odd = esz == 2 && a.n % 2 && a.z_stride == 0 && start(4);
-    a.classes = classes_of(groups, odd);
-    const Plan p = plan(a.rows, a.classes, a.n, esz, fits(16) ? 16 : odd || fits(4) ? 4 : 2, kOp);
+    // the gate's rows start as x's do
+    const bool alike = a.z_stride == 0 || (a.z_stride - static_cast<int64_t>(a.groups) * a.n) * esz % 16 == 0;
+    const bool lie = alike && start(16) && lies(groups, a.n, esz);
+    a.classes = lie ? classes_of(groups, starts_of(a.n, esz)) : groups;
+    const Plan p = plan(a.rows, a.classes, a.n, esz, lie || fits(16) ? 16 : fits(4) ? 4 : 2, lie, kOp);
     cudaError_t e;
     if (p.bytes) {
         a.part = static_cast<float *>(workspace);
@@ -703,10 +737,10 @@ cudaError_t run(NormArgs a, float *dw, float *dl, void *workspace, cudaStream_t 
                 e = !large      ? run_rows<T, 2, 8, kOp, 256, kDirect>(a, p, s)
                     : p.nv == 8 ? run_rows<T, 2, 8, kOp, 512, kDirect>(a, p, s)
                                 : run_rows<T, 2, 16, kOp, 512, kDirect>(a, p, s);
-            else if (odd)
-                e = large ? run_rows<T, 4, 8, kOp, 512, kOdd>(a, p, s) : run_rows<T, 4, 8, kOp, 256, kOdd>(a, p, s);
         }
-        if (p.direct() || odd) {
+        if (p.direct()) {
+        } else if (lie) {
+            e = large ? run_rows<T, 16, 2, kOp, 512, kLie>(a, p, s) : run_rows<T, 16, 2, kOp, 256, kLie>(a, p, s);
         } else if (large) {
             e = p.bytes == 16 ? run_rows<T, 16, 2, kOp, 512, kRing>(a, p, s) : run_rows<T, 4, 8, kOp, 512, kRing>(a, p, s);
         } else {

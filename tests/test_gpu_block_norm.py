@@ -152,6 +152,16 @@ def test_rows_of_odd_length(rows, G, n, own, norm, slices, shift):
     added((rows * G, n), BF, norm, seed=n, given=own, shift=shift)
 
 
+@pytest.mark.parametrize("rows,G,n", [(50, 4, 100), (60, 8, 33), (30, 8, 1001), (2, 8, 5), (700, 1, 60), (33, 6, 20),
+                                      (1, 1, 6), (3, 7, 129), (40, 16, 9), (5, 1, 4090), (2, 200, 11)])
+@pytest.mark.parametrize("own,norm", [(False, "layer"), (True, "rms")])
+@pytest.mark.parametrize("dtype,slices", [(BF, 0), (BF, 2), (F, 0), (F, 2)])
+def test_rows_that_start_in_the_middle_of_16_bytes(rows, G, n, own, norm, dtype, slices):
+    """At two, four or eight places, with the gate's rows alike or not."""
+    gated((rows, G, n), (G, n) if own else (n,), dtype, norm, seed=n, slices=slices)
+    added((rows * G, n), dtype, norm, seed=n, scaled=own)
+
+
 @pytest.mark.parametrize("n", [3, 65, 1001, 2047])
 @pytest.mark.parametrize("rows", [1, 2, 41])
 def test_rows_of_odd_length_keep_to_themselves(rows, n):
@@ -163,9 +173,8 @@ def test_rows_of_odd_length_keep_to_themselves(rows, n):
     want = kla.gated_norm_fwd(x, z, w), kla.add_norm_fwd(x, z, w, scale)
     bad = torch.arange(rows, device=DEV) % 2 == 1
     others = [t.masked_fill(bad[:, None], float("nan")) for t in (x, z)]
-    back = torch.full((2, rows * n + 1), 7.0, dtype=BF, device=DEV)
-    if rows * n % 2:   # the second buffer's rows would start in the middle of 4 bytes
-        back = torch.full((2, rows * n + 3), 7.0, dtype=BF, device=DEV)
+    # bits are compared, and tensors that start elsewhere may be added up in another order: both on 16 bytes, as the others
+    back = torch.full((2, (rows * n + 15) // 8 * 8), 7.0, dtype=BF, device=DEV)
     out = [b[:rows * n].view(rows, n) for b in back]
     got = kla.gated_norm_fwd(*others, w, out=out[0]), kla.add_norm_fwd(*others, w, scale, out=out[0], out_residual=out[1])
     y = kla.gated_norm_fwd(*others, w)[0]
