@@ -218,20 +218,24 @@ def _rotary_shapes(entry, q, k, freqs, positions):
     try:
         shape, dtype, at = q.shape, q.dtype, q.get_device()
         B, T, H, d = shape
-        ok = (at >= 0 and dtype in _CODE and q.is_contiguous() and freqs.dtype is _F32 and len(freqs.shape) == 1 and
+        dense = q.is_contiguous()
+        ok = (at >= 0 and dtype in _CODE and (dense or q.stride(3) == 1) and freqs.dtype is _F32 and len(freqs.shape) == 1 and
               freqs.get_device() == at and freqs.is_contiguous() and 2 * freqs.shape[0] <= d and max(shape) <= _MOST and
               (positions is None or (positions.dtype in _POSITIONS and positions.shape == shape[:2] and
                                      positions.get_device() == at and positions.is_contiguous())))
         if k is not None:
             kshape = k.shape
             Hk = kshape[2]
-            ok = (ok and k.dtype is dtype and kshape == (B, T, Hk, d) and k.get_device() == at and k.is_contiguous() and
-                  Hk <= _MOST)
+            dense_k = k.is_contiguous()
+            ok = (ok and k.dtype is dtype and kshape == (B, T, Hk, d) and k.get_device() == at and
+                  (dense_k or k.stride(3) == 1) and Hk <= _MOST)
+            dense = dense and dense_k
         else:
             Hk = 0
     except (AttributeError, ValueError, IndexError):
         ok = False
     if not ok:
+        dense = False
         device = _device("q", q)
         _code("q", q)
         if q.dim() != 4 or (k is not None and (not isinstance(k, torch.Tensor) or k.dim() != 4)):
@@ -239,8 +243,10 @@ def _rotary_shapes(entry, q, k, freqs, positions):
         Hk = 0 if k is None else k.shape[2]
         if max(q.shape) > _MOST or Hk > _MOST:
             _refuse(entry, _native.KLA_ERR_UNSUPPORTED)
+        _dense_last(q)
         if k is not None:
             _check("k", k, (B, T, Hk, d), dtype, device, False)
+            _dense_last(k)
         if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
             raise ValueError("freqs must be [rot / 2]")
         _check("freqs", freqs, freqs.shape, _F32, device)
@@ -250,7 +256,7 @@ def _rotary_shapes(entry, q, k, freqs, positions):
             if positions.dtype not in _POSITIONS:
                 raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
             _check("positions", positions, (B, T), positions.dtype, device)
-    return B, T, H, Hk, d, ok
+    return B, T, H, Hk, d, dense
 
 
 def _rotary_out(name, x, out, dense):
@@ -269,8 +275,11 @@ def _rotary(entry, q, k, freqs, positions, layout, scale, out_q, out_k, inverse)
     out_k = None if k is None else _rotary_out("out_k", k, out_k, dense)
     strides = None
     if not dense or given:
-        _dense_last(*(t for t in (q, k, out_q, out_k) if t is not None))
-        strides = _Strides12(*(s for t in (q, k, out_q, out_k) for s in ((0, 0, 0) if t is None else t.stride()[:3])))
+        if given:
+            _dense_last(*(t for t in (out_q, out_k) if t is not None))
+        a, b = q.stride(), out_q.stride()
+        c, e = (b, b) if k is None else (k.stride(), out_k.stride())   # without keys: not looked at
+        strides = _Strides12(a[0], a[1], a[2], c[0], c[1], c[2], b[0], b[1], b[2], e[0], e[1], e[2])
     st = _native.on(device).kla_rotary(
         q.data_ptr(), _ptr(k), out_q.data_ptr(), _ptr(out_k), strides, freqs.data_ptr(), _ptr(positions),
         0 if positions is None else _POSITIONS[positions.dtype], B, T, H, Hk, d, 2 * freqs.shape[0], layout,
