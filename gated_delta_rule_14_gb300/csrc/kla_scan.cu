@@ -17,9 +17,10 @@
 // Measured: 131072 x 2048 forward 281 us (5.7 TB/s, 84 % of a copy's rate; in a row 273), backward 508 us (5.3 TB/s); 8 x
 // 4096 x 2048 forward 71 us (5.6 TB/s), backward 111 us (6.0 TB/s); in fp32 8 x 2048 x 2048 85 and 130 us. Where channels
 // are few the chain of tiles is what is waited for, four of them a trip to L2, 0.7 us: 131072 x 512 128 and 233 us,
-// 131072 x 64 92 and 154. A thread per channel that walks all tokens took 120 ms for the first. By the counters (8 x 2048 x 2048) 21 instructions a value forward, at 1.8
-// of 4 a cycle, of whose warps' time a quarter waits for the chain, and 40 backward at 2.2 of 4: registers hold 16 warps
-// an SM, and with those neither the issue slots nor the memory (3.9 TB/s there) are full.
+// 131072 x 64 92 and 154. A thread per channel that walks all tokens took 120 ms for the first. By the counters
+// (8 x 2048 x 2048) 18 instructions a value forward and 30 backward, both at 2.0 of 4 a cycle; warps wait for the chain
+// (forward) and for tiles on their way: registers hold 16 warps an SM, whose tiles and those that follow are what is under
+// way at once.
 #include <cuda.h>
 
 #include <atomic>
