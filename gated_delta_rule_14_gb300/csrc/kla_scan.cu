@@ -14,10 +14,10 @@
 // tell each other through the workspace, in one pass; a pass for the tiles' maps and one for the outputs would move 10
 // bytes forward. Backward, the states are walked again from one kept every 128 tokens (0.03 bytes a value), which is
 // exact and cheaper than reading the outputs back.
-// Measured: 131072 x 2048 forward 281 us (5.7 TB/s, 84 % of a copy's rate; in a row 273), backward 508 us (5.3 TB/s); 8 x
-// 4096 x 2048 forward 71 us (5.6 TB/s), backward 111 us (6.0 TB/s); in fp32 8 x 2048 x 2048 85 and 130 us. Where channels
-// are few the chain of tiles is what is waited for, four of them a trip to L2, 0.7 us: 131072 x 512 128 and 233 us,
-// 131072 x 64 92 and 154. A thread per channel that walks all tokens took 120 ms for the first. By the counters
+// Measured: 131072 x 2048 forward 281 us (5.7 TB/s, 84 % of a copy's rate; in a row 273), backward 484 us (5.5 TB/s); 8 x
+// 4096 x 2048 forward 72 us (5.6 TB/s), backward 105 us (6.4 TB/s); in fp32 8 x 2048 x 2048 85 and 128 us. Where channels
+// are few the chain of tiles is what is waited for, four or eight of them a trip to L2, 0.7 us: 131072 x 512 117 and 232 us,
+// 131072 x 64 74 and 154. A thread per channel that walks all tokens took 120 ms for the first. By the counters
 // (8 x 2048 x 2048) 18 instructions a value forward and 30 backward, both at 2.0 of 4 a cycle; warps wait for the chain
 // (forward) and for tiles on their way: registers hold 16 warps an SM, whose tiles and those that follow are what is under
 // way at once.
@@ -166,15 +166,12 @@ __device__ __forceinline__ void hear(const uint2 *p, int count, uint2 (&v)[kV]) 
 // The state that enters a tile, from what the `left` tiles before it told: `p` is the nearest one's word of this
 // thread's first channel, `hop` leads to the next further one. Of the nearest kAhead tiles one has to know the state
 // that leaves it, and the maps of those in between are applied to that in their order, as they apply them
-// themselves: whatever is known when, the bits are the same. (kAhead of 3, 4 and 6, us, forward and backward: 131072 x 64
-// 109 + 194, 92 + 154, 79 + 180; 131072 x 1024 181 + 337, 172 + 312, 171 + 377; 131072 x 2048 279 + 509, 281 + 508,
-// 298 + 610.) The chain's first tile tells kWhole at once. Tiles are
+// themselves: whatever is known when, the bits are the same. The chain's first tile tells kWhole at once. Tiles are
 // taken by ticket in the order of the chain, so that all of those are running or done and none of them waits for a
 // later one: the wait ends. Its limit is for what cannot be foreseen. Run by a whole warp; false where it gave up.
-template <int kV, bool kPairs = false>
-__device__ __forceinline__ bool entering(const uint2 *p, int64_t hop, int left, int count, const Head *head,
+template <int kV, bool kPairs, int kAhead>
+__device__ __forceinline__ bool hear_state(const uint2 *p, int64_t hop, int left, int count, const Head *head,
                                          float (&h)[kV]) {
-    constexpr int kAhead = 4;
     constexpr unsigned kLimit = 1u << 21;
 #pragma unroll
     for (int v = 0; v < kV; ++v) h[v] = 0.f;
@@ -209,6 +206,20 @@ __device__ __forceinline__ bool entering(const uint2 *p, int64_t hop, int left, 
         if ((polls & 63u) == 63u && *reinterpret_cast<const volatile unsigned *>(&head->abort) == 0u) return false;
     }
     return false;
+}
+
+// How far away that may be: four tiles, or kFar where chains are few. Then the SMs hold many tiles of each, and the chain
+// is what is waited for, a trip to L2 every so many tiles; with more chains hearing from further costs more than it gives.
+// us, of 4 and 8: forward 131072 x 64 97 and 74, x 512 134 and 117, x 1024 (16 chains) 174 and 175, x 2048 (32) 286 and 316;
+// fp32 x 128 172 and 122, x 512 (16) 259 and 230. Backward fp32 x 128 180 and 146, x 512 345 and 349; bf16, whose words
+// are two a lane, x 64 158 and 168, x 512 232 and 292, so that it stays at four. (3 and 6 tiles instead of four: x 1024 181
+// and 171 forward, 337 and 377 backward, four 172 and 312; x 2048 279 and 298, 509 and 610, four 281 and 508.)
+template <int kV, bool kPairs, int kFar>
+__device__ __forceinline__ bool entering(const ScanArgs &p, const uint2 *from, int64_t hop, int left, int count,
+                                         float (&h)[kV]) {
+    constexpr int kFew = 16;
+    if (kFar > 4 && p.B * p.blocks <= kFew) return hear_state<kV, kPairs, kFar>(from, hop, left, count, p.head, h);
+    return hear_state<kV, kPairs, 4>(from, hop, left, count, p.head, h);
 }
 
 // The tile of a ticket: `at` tiles along the chain, of channels c0 ..
@@ -304,7 +315,7 @@ __global__ void __launch_bounds__(32 * kWarps) scan_fwd_kernel(ScanArgs p) {
         }
         if (at.at > 0 && at.at < last) tell_map<kV>(here, live, A, H);
         if (at.at == 0) start<kV>(p, b, c, live, in);
-        else if (!entering<kV>(here - p.C, -static_cast<int64_t>(p.C), at.at, live, p.head, in)) give_up(p);
+        else if (!entering<kV, false, 4>(p, here - p.C, -static_cast<int64_t>(p.C), at.at, live, in)) give_up(p);
 #pragma unroll
         for (int v = 0; v < kV; ++v) {
             enter[v][lane] = in[v];
@@ -427,7 +438,7 @@ __global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(ScanArgs p) {
         }
         if (tile > 0 && tile < last) tell_map<kV>(here, live, A, D);
         if (tile == last) start<kV>(p, b, c, live, in);
-        else if (!entering<kV>(here + p.C, p.C, last - tile, live, p.head, in)) give_up(p);
+        else if (!entering<kV, false, 4>(p, here + p.C, p.C, last - tile, live, in)) give_up(p);
 #pragma unroll
         for (int v = 0; v < kV; ++v) {
             enter[v][lane] = in[v];
@@ -483,7 +494,7 @@ __global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(ScanArgs p) {
 // Tokens of a thread, warps at them and CTAs of an SM. Each side of the choice at 8 x 4096 x 2048 bf16 and, in fp32, 8 x
 // 2048 x 2048, us: forward 32 tokens x 8 warps x 2 CTAs 82 and 102, 16 x 8 x 3 89 and 95; backward 16 x 8 x 2 138 and 181,
 // 16 x 4 x 4 134 and 179, but 609 instead of 525 at 1 x 131072 x 2048, whose chain gets twice as long (all by copies of the
-// warps' own, and before the backward pass had its warp for the chain: 71 and 85, 111 and 130 since).
+// warps' own, and before the backward pass had its warp for the chain: 71 and 85, 105 and 128 since).
 struct Shape {
     int tok, warps, ctas;
     constexpr int tile() const { return tok * warps; }
@@ -806,7 +817,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) scan_fwd_ring_kernel(ScanA
         if (teller) {
             float in[kV];
             if (at.at == 0) start<kV>(p, b, c, count, in);
-            else if (!entering<kV, kPairs>(here - p.C, -static_cast<int64_t>(p.C), at.at, count, p.head, in)) give_up(p);
+            else if (!entering<kV, kPairs, 8>(p, here - p.C, -static_cast<int64_t>(p.C), at.at, count, in)) give_up(p);
             enter[lane] = whole<kV>(in);
             H = L::fma(A, enter[lane], H);
             if (at.at < last) tell_state<kV, kPairs>(here, count, parts(H));
@@ -884,11 +895,9 @@ __device__ __forceinline__ void carry_warp(const ScanArgs &p, Shared<typename L:
         if (i == 0) ask();
         if (kBy == kTma && next < turns.total) fetch_tile(next, (i + 1) & 1);   // the gates' rows and that half are read
         if (tile <= last) {
-            V pa = L::all(1.f), pd = L::all(0.f), after_a[kWarps], after_d[kWarps];   // the maps of later tokens
+            V pa = L::all(1.f), pd = L::all(0.f);   // the tile's map
 #pragma unroll
             for (int w = kWarps - 1; w >= 0; --w) {
-                after_a[w] = pa;
-                after_d[w] = pd;
                 const V a = sh.a[i & 1][w][lane];
                 pd = L::fma(a, pd, sh.d[w][lane]);
                 pa = L::mul(pa, a);
@@ -898,13 +907,17 @@ __device__ __forceinline__ void carry_warp(const ScanArgs &p, Shared<typename L:
                 start<kV>(p, b, c, count, in);
             } else {
                 if (tile > 0) tell_map<kV, kPairs>(here, count, parts(pa), parts(pd));
-                if (!entering<kV, kPairs>(here + p.C, p.C, last - tile, count, p.head, in)) give_up(p);
+                if (!entering<kV, kPairs, kV == 1 ? 8 : 4>(p, here + p.C, p.C, last - tile, count, in)) give_up(p);
             }
-            const V e = whole<kV>(in), out = L::fma(pa, e, pd);
+            V e = whole<kV>(in);
+            const V out = L::fma(pa, e, pd);
             if (tile > 0) tell_state<kV, kPairs>(here, count, parts(out));
             else finish<kV>(p, b, c, count, parts(out));
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) sh.enter[w][lane] = L::fma(after_a[w], e, after_d[w]);
+            for (int w = kWarps - 1; w >= 0; --w) {
+                sh.enter[w][lane] = e;
+                e = L::fma(sh.a[i & 1][w][lane], e, sh.d[w][lane]);
+            }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(b_carry);
