@@ -14,10 +14,10 @@
 // tell each other through the workspace, in one pass; a pass for the tiles' maps and one for the outputs would move 10
 // bytes forward. Backward, the states are walked again from one kept every 128 tokens (0.03 bytes a value), which is
 // exact and cheaper than reading the outputs back.
-// Measured: 131072 x 2048 forward 281 us (5.7 TB/s, 84 % of a copy's rate; in a row 273), backward 484 us (5.5 TB/s); 8 x
+// Measured: 131072 x 2048 forward 275 us (5.9 TB/s, 86 % of a copy's rate), backward 484 us (5.5 TB/s); 8 x
 // 4096 x 2048 forward 72 us (5.6 TB/s), backward 105 us (6.4 TB/s); in fp32 8 x 2048 x 2048 85 and 128 us. Where channels
-// are few the chain of tiles is what is waited for, four or eight of them a trip to L2, 0.7 us: 131072 x 512 117 and 232 us,
-// 131072 x 64 74 and 154. A thread per channel that walks all tokens took 120 ms for the first. By the counters
+// are few the chain of tiles is what is waited for, four or eight of them a trip to L2, 0.7 us: 131072 x 512 111 and 232 us,
+// 131072 x 64 72 and 154. A thread per channel that walks all tokens took 120 ms for the first. By the counters
 // (8 x 2048 x 2048) 18 instructions a value forward and 30 backward, both at 2.0 of 4 a cycle; warps wait for the chain
 // (forward) and for tiles on their way: registers hold 16 warps an SM, whose tiles and those that follow are what is under
 // way at once.
@@ -800,12 +800,14 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) scan_fwd_ring_kernel(ScanA
         if (threadIdx.x == 0) s_next = asked;
         __syncthreads();
         const unsigned next = s_next;
-        // the map of the tile's tokens before this warp's
+        // the map of the tile's tokens before this warp's: all loads on their way at once, as the chain waits for the last warp
         V pa = L::all(1.f), ph = L::all(0.f);
-        for (int w = 0; w < warp; ++w) {
-            ph = L::fma(map_a[w][lane], ph, map_h[w][lane]);
-            pa = L::mul(pa, map_a[w][lane]);
-        }
+#pragma unroll
+        for (int w = 0; w < kWarps - 1; ++w)
+            if (w < warp) {
+                ph = L::fma(map_a[w][lane], ph, map_h[w][lane]);
+                pa = L::mul(pa, map_a[w][lane]);
+            }
         const bool teller = warp == kWarps - 1 && at.at <= last;
         uint2 *here = p.carry + (static_cast<int64_t>(b) * p.tiles + at.at) * p.C + c;
         if (teller) {
@@ -813,15 +815,17 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) scan_fwd_ring_kernel(ScanA
             A = L::mul(A, pa);
             if (at.at > 0 && at.at < last) tell_map<kV, kPairs>(here, count, parts(A), parts(H));
         }
-        if (next < turns.total) fetch(next, stage ^ 1);
+        if (next < turns.total && (kBy == kTma || !teller)) fetch(next, stage ^ 1);
         if (teller) {
             float in[kV];
             if (at.at == 0) start<kV>(p, b, c, count, in);
             else if (!entering<kV, kPairs, 8>(p, here - p.C, -static_cast<int64_t>(p.C), at.at, count, in)) give_up(p);
-            enter[lane] = whole<kV>(in);
-            H = L::fma(A, enter[lane], H);
+            const V e = whole<kV>(in);
+            H = L::fma(A, e, H);
             if (at.at < last) tell_state<kV, kPairs>(here, count, parts(H));
             else finish<kV>(p, b, c, count, parts(H));
+            enter[lane] = e;
+            if (kBy != kTma && next < turns.total) fetch(next, stage ^ 1);   // which nobody waits for
         }
         __syncthreads();
         if (count > 0) {
