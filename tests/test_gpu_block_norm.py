@@ -254,6 +254,21 @@ def test_in_place_residual():
         assert same is keep and torch.equal(s, keep) and torch.equal(y, y2)
 
 
+@pytest.mark.parametrize("n", [3, 33, 100, 1001, 2047])
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_in_place_rows_off_16_bytes(n, dtype):
+    """Two rows may share 16 bytes, of which each writes its own."""
+    import gated_delta_rule_14_gb300 as kla
+    r = rnd(n)
+    x, res, w, scale = r(5003, n).to(dtype), r(5003, n).to(dtype), r(n), r(n)
+    y, s, _, rstd = kla.add_norm_fwd(x, res, w, scale)
+    keep = res.clone()
+    y2, same, _, rstd2 = kla.add_norm_fwd(x, keep, w, scale, out_residual=keep)
+    assert same is keep and torch.equal(s, keep) and torch.equal(y, y2) and torch.equal(rstd, rstd2)
+    want = res.double() + scale.double() * x.double()
+    assert rel(s, want) <= (4e-3 if dtype == BF else 1e-5)
+
+
 def test_equal_calls_give_equal_bits():
     import gated_delta_rule_14_gb300 as kla
     r = rnd(7)

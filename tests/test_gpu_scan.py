@@ -118,6 +118,27 @@ def test_many_spans(mode):
     check(1, 20000, 34, torch.float32, mode, seed=5)
 
 
+@pytest.mark.parametrize("B,T,C,dtype", [(1, 9001, 64, torch.bfloat16), (2, 5000, 33, torch.float32),
+                                         (1, 6000, 513, torch.float32), (3, 7000, 101, torch.bfloat16)])
+@pytest.mark.parametrize("mode", ["sigmoid", "log"])
+def test_long_prompts_of_few_channels(B, T, C, dtype, mode):
+    """Many tiles of few chains at once; equal calls give equal bits, whichever tile was heard first."""
+    import gated_delta_rule_14_gb300 as kla
+    x, gate, dy, h0, dh, n, _ = make(B, T, C, dtype, mode, C, [T, 1, 4097][:B])
+    first = None
+    for _ in range(5):
+        y, h_T, states = kla.gated_scan_fwd(x, gate, h0, mode=mode, lengths=n, states=True)
+        grads = kla.gated_scan_bwd(x, gate, dy, states, dh, mode=mode, lengths=n)
+        got = [y, h_T, *grads.values()]
+        if first is None:
+            first = got
+        assert all(torch.equal(a, b) for a, b in zip(first, got))
+    kla.device_status(DEV)
+    clean = [t.double().nan_to_num(0.0) for t in (x, gate)]
+    wy, wh = reference(clean[0], clean[1], h0.double(), mode, n)
+    assert rel(first[0], wy) <= TOL[dtype] and rel(first[1], wh) <= 3e-5
+
+
 def test_more_tiles_than_fit_at_once():
     """Equal calls give equal bits, whatever order the tiles finish in, and the state that enters a late token is that
     of the whole prompt: against the same prompt cut in two."""
