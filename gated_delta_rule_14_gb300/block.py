@@ -204,7 +204,8 @@ def rotary_freqs(rot: int, base: float = 10000.0, *, scaling: Optional[str] = No
         # the place along the frequencies at which one turns `turns` times within original_length
         def place(turns):
             return n * math.log(original_length / (turns * 2 * math.pi)) / math.log(base)
-        low, high = max(0.0, math.floor(place(fast))), min(n - 1.0, math.ceil(place(slow)))
+        # the ramp may end beyond the last frequency, which is on it then
+        low, high = max(0.0, math.floor(place(fast))), min(rot - 1.0, math.ceil(place(slow)))
         ramp = ((at - low) / max(high - low, 1e-3)).clamp(0, 1)
         freqs = freqs * (1 - ramp) + freqs / factor * ramp
         scale = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
