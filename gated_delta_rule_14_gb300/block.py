@@ -189,8 +189,8 @@ def rotary_freqs(rot: int, base: float = 10000.0, *, scaling: Optional[str] = No
     """
     if rot < 0 or rot % 2:
         raise ValueError("rot must be even")
-    if not (base > 0 and factor > 0):
-        raise ValueError("base and factor must be positive")
+    if not (0 < base < math.inf and 0 < factor < math.inf):
+        raise ValueError("base and factor must be positive and finite")
     n, scale = rot // 2, 1.0
     at = torch.arange(n, dtype=torch.float64)
     if scaling == "ntk" and n > 1:
@@ -199,14 +199,15 @@ def rotary_freqs(rot: int, base: float = 10000.0, *, scaling: Optional[str] = No
     if scaling == "linear":
         freqs = freqs / factor
     elif scaling == "yarn":
-        if original_length is None or original_length < 1 or not fast > slow > 0:
-            raise ValueError('"yarn" needs original_length and fast > slow > 0')
+        if original_length is None or original_length < 1 or not fast > slow > 0 or base <= 1:
+            raise ValueError('"yarn" needs original_length, fast > slow > 0 and a base above 1')
         # the place along the frequencies at which one turns `turns` times within original_length
         def place(turns):
             return n * math.log(original_length / (turns * 2 * math.pi)) / math.log(base)
         # the ramp may end beyond the last frequency, which is on it then
         low, high = max(0.0, math.floor(place(fast))), min(rot - 1.0, math.ceil(place(slow)))
-        ramp = ((at - low) / max(high - low, 1e-3)).clamp(0, 1)
+        low = min(low, high - 1e-3)   # nothing turns `slow` times (or all do `fast` times): no ramp among the frequencies
+        ramp = ((at - low) / (high - low)).clamp(0, 1)
         freqs = freqs * (1 - ramp) + freqs / factor * ramp
         scale = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
     elif scaling not in (None, "ntk"):

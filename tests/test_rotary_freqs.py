@@ -39,3 +39,19 @@ def test_yarn_keeps_most_of_a_frequency_that_still_turns():
     plain, _ = rotary_freqs(128, device="cpu")
     got, _ = rotary_freqs(128, scaling="yarn", factor=4.0, original_length=131072, device="cpu")
     assert 2.4 <= 131072 * float(plain[-1]) / (2 * math.pi) <= 2.5 and 0.45 <= float(got[-1] / plain[-1]) <= 0.47
+
+
+def test_yarn_of_contexts_in_which_nothing_turns():
+    """Trained on fewer tokens than the highest frequency needs for `slow` turns: every one is divided."""
+    plain, _ = rotary_freqs(16, device="cpu")
+    for length, slow in ((6, 1.0), (2, 1.0), (40, 10.0)):
+        got, _ = rotary_freqs(16, scaling="yarn", factor=4.0, original_length=length, slow=slow, device="cpu")
+        assert length / (2 * math.pi) < slow and torch.equal(got, plain / 4), (length, slow)
+
+
+@pytest.mark.parametrize("bad", [dict(base=1.0, scaling="yarn", original_length=4096),
+                                 dict(base=0.5, scaling="yarn", original_length=4096), dict(base=math.inf),
+                                 dict(factor=math.inf), dict(base=math.nan), dict(factor=math.nan)])
+def test_frequencies_that_have_no_meaning_are_refused(bad):
+    with pytest.raises(ValueError):
+        rotary_freqs(8, device="cpu", **bad)
