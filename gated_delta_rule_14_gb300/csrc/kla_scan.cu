@@ -7,7 +7,9 @@
 // In fp32 the sigmoid's recurrence is taken as h + w (x - h) where w is the smaller of the two factors, as x + a (h - x)
 // where a is: where a gate keeps its state for thousands of tokens a is within 2^-11 of 1 and its rounding to 24 bits
 // would leave 12 of w, and where one drops a large state nothing of it may stay behind as a difference of roundings.
-// In bf16, whose values are known to 2^-9, as a h + w x with a = 1 - w in paired arithmetic.
+// In bf16 as a h + w x with a = 1 - w in paired arithmetic, whose rounding of 2^-23 is far below the values' own 2^-9 as
+// long as a is not small; a warp with gates below -5 takes its tokens as in fp32 (`Exact`), as a gate that forgets leaves
+// nothing but a of the state, and of the gradient.
 //
 // Every value is read once: 6 bytes a value forward and 10 backward in bf16, which at a copy's rate is 237 us for a
 // prompt of 131072 x 2048. Time is therefore cut into tiles that are worked on side by side and joined by what they
@@ -520,8 +522,8 @@ __device__ __forceinline__ void load_tile(uint32_t to, const CUtensorMap *map, u
 
 // What a lane has of a row: two channels of bf16, whose arithmetic is paired, or one of fp32. A gate is kept as one
 // number: bf16: w, or a where KLA_SCAN_LOG, with h = a h + w x and a = 1 - w, whose rounding of 2^-25 is that of a
-// itself where it is near 1 (and whose exponential and reciprocal are the hardware's, off by 2^-21 at gates of 10, far
-// below the gate's own 2^-9). fp32: the coefficient of above in the forward pass; exp(gate) in the backward pass, from
+// itself where it is near 1 (and whose exponential and reciprocal are the hardware's, off by 2^-21 at gates of 10; where a
+// is small Exact takes the warp's tokens). fp32: the coefficient of above in the forward pass; exp(gate) in the backward pass, from
 // which both factors come to their last bits.
 template <typename T, bool kLog, bool kBwd>
 struct Lane;
@@ -555,6 +557,7 @@ struct Lane<__nv_bfloat16, kLog, kBwd> {
     // h, a token on; prod a, a token on
     static __device__ __forceinline__ V advance(V h, V x, V k) { return fma2(a(k), h, kLog ? x : mul2(k, x)); }
     static __device__ __forceinline__ V shrink(V A, V k) { return mul2(A, a(k)); }
+    static __device__ __forceinline__ V reach(V dh, V k) { return mul2(a(k), dh); }   // a dh
 };
 template <bool kLog, bool kBwd>
 struct Lane<float, kLog, kBwd> {
@@ -578,9 +581,54 @@ struct Lane<float, kLog, kBwd> {
     static __device__ __forceinline__ V shrink(V A, V k) {
         return kla::shrink<kLog>(A, kBwd ? coefficient<kLog>(a(k), w(k)) : k);
     }
+    static __device__ __forceinline__ V reach(V dh, V k) { return a(k) * dh; }
+};
+// The bf16 sigmoid of a warp with gates that Lane does not hold: a gate kept as its coefficient, of which both factors come
+// to their last bits.
+struct Exact {
+    using V = float2;
+    static __device__ __forceinline__ float keep(float gate) {
+        float a, w;
+        factors<__nv_bfloat16, false>(gate_exp<__nv_bfloat16, false>(gate), a, w);
+        return coefficient<false>(a, w);
+    }
+    static __device__ __forceinline__ V keep(V gate) { return make_float2(keep(gate.x), keep(gate.y)); }
+    static __device__ __forceinline__ float w(float c) { return c > 0.f ? c : 1.f + c; }
+    static __device__ __forceinline__ V w(V k) { return make_float2(w(k.x), w(k.y)); }
+    static __device__ __forceinline__ V advance(V h, V x, V k) {
+        return make_float2(kla::advance<false>(h.x, x.x, k.x), kla::advance<false>(h.y, x.y, k.y));
+    }
+    static __device__ __forceinline__ V shrink(V A, V k) {
+        return make_float2(kla::shrink<false>(A.x, k.x), kla::shrink<false>(A.y, k.y));
+    }
+    static __device__ __forceinline__ V reach(V dh, V k) { return shrink(dh, k); }
 };
 __device__ __forceinline__ float part(float v, int) { return v; }
 __device__ __forceinline__ float part(float2 v, int i) { return i ? v.y : v.x; }
+// The largest w of a lane's tokens, where it matters: bf16, sigmoid.
+template <typename T, bool kLog>
+struct Most {
+    static constexpr bool kAsks = sizeof(T) == 2 && !kLog;
+    float w = 0.f;
+    template <typename V>
+    __device__ __forceinline__ void see(V k) {
+        if (kAsks) w = fmaxf(fmaxf(w, part(k, 0)), part(k, 1));
+    }
+    // Whether the warp's tokens are Exact's: of any lane a gate below -5 among its `count` channels. There 1 - w is off by
+    // 2^-23, 2^-16 of a. In other channels there may be anything: where there is one, the gates are looked at once more.
+    // A warp as a whole, as lanes that go apart cost the others more: 8 x 4096 x 2048 66.7 and 109.1 us without Exact, 67.1
+    // and 109.6 with it, 118.8 and 177 where all warps take it; lane by lane 66.7 and 113.6.
+    template <typename F>
+    __device__ __forceinline__ bool any(int count, int m, F gate) const {
+        if (!kAsks) return false;
+        bool here = count > 0 && w > 0.9933071f;   // sigmoid(5)
+        if (here && count == 1) {
+            here = false;
+            for (int i = 0; i < m; ++i) here |= part(gate(i), 0) < -5.f;
+        }
+        return __any_sync(0xffffffffu, here);
+    }
+};
 using One = float[1];
 using Two = float[2];
 __device__ __forceinline__ const One &parts(const float &v) { return reinterpret_cast<const One &>(v); }
@@ -704,11 +752,13 @@ __device__ __forceinline__ int channels(const ScanArgs &p, int c) {
     return kBy == kOdd ? min(max(p.C - c, 0), kV) : c < p.C ? kV : 0;
 }
 
-// Runs f with whether all of a warp's kTok tokens are valid: the loops over them have no conditions then.
-template <typename F>
-__device__ __forceinline__ void by_full(bool full, F f) {
-    if (full) f(std::true_type{});
-    else f(std::false_type{});
+// Runs f with whether all of a warp's kTok tokens are valid, as the loops over them have no conditions then, and by which
+// functions the warp takes them.
+template <typename L, typename X, typename F>
+__device__ __forceinline__ void by_case(bool full, bool exact, F f) {
+    if (exact) f(std::false_type{}, X{});
+    else if (full) f(std::true_type{}, L{});
+    else f(std::false_type{}, L{});
 }
 
 // As above, with tiles one after the other: while a CTA waits for the state that enters one and writes its outputs, the
@@ -716,6 +766,7 @@ __device__ __forceinline__ void by_full(bool full, F f) {
 template <typename T, bool kLog, Copies kBy, int kTok, int kWarps, int kCtas>
 __global__ void __launch_bounds__(32 * kWarps, kCtas) scan_fwd_ring_kernel(ScanArgs p, bool wide, const __grid_constant__ Maps maps) {
     using L = Lane<T, kLog, false>;
+    using X = typename std::conditional<Most<T, kLog>::kAsks, Exact, L>::type;
     using V = typename L::V;
     constexpr int kTile = kTok * kWarps, kV = L::kV, kWidth = 32 * kV, kRow = kBy == kOdd ? kOddRow : kEvenRow;
     constexpr bool kPairs = kV == 2 && kBy != kOdd;
@@ -786,15 +837,23 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) scan_fwd_ring_kernel(ScanA
             __syncwarp();
         }
         if (threadIdx.x == 0) asked = turns.ask();
-        by_full(m == kTok, [&](auto full) {
+        Most<T, kLog> most;
+        auto map_tokens = [&](auto full, auto by) {
+            using K = decltype(by);
+            A = L::all(1.f);
+            H = L::all(0.f);
 #pragma unroll
             for (int i = 0; i < kTok; ++i)
                 if (full || i < m) {
-                    k[i] = L::keep(of_g.template load<L>(gs + i * kRow, i));
-                    A = L::shrink(A, k[i]);
-                    H = L::advance(H, of_x.template load<L>(xs + i * kRow, i), k[i]);
+                    k[i] = K::keep(of_g.template load<L>(gs + i * kRow, i));
+                    if (std::is_same<K, L>::value) most.see(k[i]);
+                    A = K::shrink(A, k[i]);
+                    H = K::advance(H, of_x.template load<L>(xs + i * kRow, i), k[i]);
                 }
-        });
+        };
+        by_case<L, L>(m == kTok, false, map_tokens);
+        const bool exact = most.any(count, m, [&](int i) { return of_g.template load<L>(gs + i * kRow, i); });
+        if (exact) map_tokens(std::false_type{}, X{});
         map_a[warp][lane] = A;
         map_h[warp][lane] = H;
         if (threadIdx.x == 0) s_next = asked;
@@ -839,11 +898,12 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) scan_fwd_ring_kernel(ScanA
             }
             T *y = static_cast<T *>(p.y) + (static_cast<int64_t>(b) * p.T + t0) * p.C + c;
             const Parity<kBy> of_y(y, p.C);
-            by_full(m == kTok, [&](auto full) {
+            by_case<L, X>(m == kTok, exact, [&](auto full, auto by) {
+                using K = decltype(by);
 #pragma unroll
                 for (int i = 0; i < kTok; ++i, y += p.C)
                     if (full || i < m) {
-                        h = L::advance(h, of_x.template load<L>(xs + i * kRow, i), k[i]);
+                        h = K::advance(h, of_x.template load<L>(xs + i * kRow, i), k[i]);
                         of_y.template store<L>(y, h, i, count);
                     } else if (t0 + i < p.T) {
                         of_y.template store<L>(y, L::all(0.f), i, count);
@@ -933,6 +993,7 @@ template <typename T, bool kLog, Copies kBy, int kTok, int kWarps, int kCtas>
 __global__ void __launch_bounds__(32 * (kWarps + 1), kCtas) scan_bwd_ring_kernel(ScanArgs p, bool wide, const __grid_constant__ Maps maps) {
     using namespace ptx;
     using L = Lane<T, kLog, true>;
+    using X = typename std::conditional<Most<T, kLog>::kAsks, Exact, L>::type;
     using V = typename L::V;
     constexpr int kTile = kTok * kWarps, kV = L::kV, kWidth = 32 * kV, kRow = kBy == kOdd ? kOddRow : kEvenRow;
     static_assert(kTile == KLA_SCAN_SPAN, "");
@@ -1013,16 +1074,24 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kCtas) scan_bwd_ring_kernel
             copies_wait();
             __syncwarp();
         }
-        by_full(m == kTok, [&](auto full) {
+        Most<T, kLog> most;
+        auto map_tokens = [&](auto full, auto by) {
+            using K = decltype(by);
+            A = L::all(1.f);
+            H = D = L::all(0.f);
 #pragma unroll
             for (int i = 0; i < kTok; ++i)
                 if (full || i < m) {
-                    k[i] = L::keep(of_g.template load<L>(gs + i * kRow, i));
-                    A = L::shrink(A, k[i]);
-                    H = L::advance(H, of_x.template load<L>(xs + i * kRow, i), k[i]);
+                    k[i] = K::keep(of_g.template load<L>(gs + i * kRow, i));
+                    if (std::is_same<K, L>::value) most.see(k[i]);
+                    A = K::shrink(A, k[i]);
+                    H = K::advance(H, of_x.template load<L>(xs + i * kRow, i), k[i]);
                     D = L::fma(A, of_d.template load<L>(ds + i * kRow, i), D);
                 }
-        });
+        };
+        by_case<L, L>(m == kTok, false, map_tokens);
+        const bool exact = most.any(count, m, [&](int i) { return of_g.template load<L>(gs + i * kRow, i); });
+        if (exact) map_tokens(std::false_type{}, X{});
         sh.a[turn & 1][warp][lane] = A;
         sh.h[turn & 1][warp][lane] = H;
         sh.d[warp][lane] = D;
@@ -1037,13 +1106,14 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kCtas) scan_bwd_ring_kernel
         for (int w = 0; w < kWarps - 1; ++w)
             if (w < warp) h = L::fma(sh.a[turn & 1][w][lane], h, sh.h[turn & 1][w][lane]);
         V lead[kTok];   // h_{t-1}, of which the sigmoid's gradient takes x_t
-        by_full(m == kTok, [&](auto full) {
+        by_case<L, X>(m == kTok, exact, [&](auto full, auto by) {
+            using K = decltype(by);
 #pragma unroll
             for (int i = 0; i < kTok; ++i)
                 if (full || i < m) {
                     const V x = of_x.template load<L>(xs + i * kRow, i);
                     lead[i] = kLog ? h : L::fma(x, L::all(-1.f), h);
-                    h = L::advance(h, x, k[i]);
+                    h = K::advance(h, x, k[i]);
                 }
         });
         ok = ok && mbar_wait_bounded(b_carry, turn & 1, kWaits);
@@ -1062,12 +1132,13 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kCtas) scan_bwd_ring_kernel
             const Parity<kBy> of_dx(static_cast<T *>(p.y) + out, p.C), of_dg(static_cast<T *>(p.dg) + out, p.C);
             T *dx = static_cast<T *>(p.y) + out + (kTok - 1) * static_cast<int64_t>(p.C);
             T *dg = static_cast<T *>(p.dg) + out + (kTok - 1) * static_cast<int64_t>(p.C);
-            by_full(m == kTok, [&](auto full) {
+            by_case<L, X>(m == kTok, exact, [&](auto full, auto by) {
+                using K = decltype(by);
 #pragma unroll
                 for (int i = kTok - 1; i >= 0; --i, dx -= p.C, dg -= p.C)
                     if (full || i < m) {
-                        const V dh = L::add(of_d.template load<L>(ds + i * kRow, i), e), w = L::w(k[i]);
-                        e = L::mul(L::a(k[i]), dh);
+                        const V dh = L::add(of_d.template load<L>(ds + i * kRow, i), e), w = K::w(k[i]);
+                        e = K::reach(dh, k[i]);
                         of_dx.template store<L>(dx, kLog ? dh : L::mul(w, dh), i, count);
                         of_dg.template store<L>(dg, L::mul(kLog ? lead[i] : L::mul(w, lead[i]), e), i, count);
                     } else if (t0 + i < p.T) {

@@ -1,0 +1,81 @@
+"""The gated scan where its gates are far from the ordinary, value by value against 64 bits: states and gradients that such
+a gate leaves are small, and a norm over a whole tensor does not see them."""
+import pytest
+import torch
+
+from gpu_util import DEV
+
+pytestmark = pytest.mark.gpu
+HALF = {torch.bfloat16: 2.0**-8, torch.float32: 2.0**-24}   # of a stored value: half a step
+
+# how rows reach the kernels: 16-byte and 4-byte copies, rows off 4 bytes, tensors that start off 4 bytes, tensor maps
+LAYOUTS = [(2, 64, 0), (2, 34, 0), (2, 65, 0), (2, 64, 1), (8, 1024, 0)]
+
+
+def scan(x, gate, h0, mode, dy=None, dh=None):
+    """y, h_T and, with dy, the gradients (dx, dgate, dh0) from the definition in 64 bits, token by token."""
+    x, gate, h0 = x.double(), gate.double(), h0.double()
+    a = torch.exp(gate) if mode == "log" else torch.sigmoid(gate)
+    w = torch.ones_like(a) if mode == "log" else torch.sigmoid(-gate)
+    before = torch.empty_like(x)
+    y = torch.empty_like(x)
+    h = h0
+    for t in range(x.shape[1]):
+        before[:, t] = h
+        h = a[:, t] * h + w[:, t] * x[:, t]
+        y[:, t] = h
+    if dy is None:
+        return y, h
+    dx, dg, e = torch.empty_like(x), torch.empty_like(x), dh.double()
+    for t in range(x.shape[1] - 1, -1, -1):
+        full = dy[:, t].double() + e
+        e = a[:, t] * full
+        dx[:, t] = w[:, t] * full
+        dg[:, t] = before[:, t] * e if mode == "log" else w[:, t] * (before[:, t] - x[:, t]) * e
+    return y, h, dx, dg, e
+
+
+def place(t, shift):
+    """The same values `shift` of them behind a 16-byte border."""
+    flat = torch.empty(t.numel() + shift, dtype=t.dtype, device=DEV)
+    flat[shift:] = t.reshape(-1)
+    return flat[shift:].view(t.shape)
+
+
+def run(x, gate, h0, mode, dy, dh):
+    import gated_delta_rule_14_gb300 as kla
+    y, h_T, s = kla.gated_scan_fwd(x, gate, h0, mode=mode, states=True)
+    g = kla.gated_scan_bwd(x, gate, dy, s, dh, mode=mode)
+    kla.device_status(DEV)
+    return y, h_T, g["dx"], g["dgate"], g["dh0"]
+
+
+def close(got, want, tol):
+    """Every value within `tol` of itself, and of what is stored in few bits half a step more."""
+    for name, a, b in zip(("y", "h_T", "dx", "dgate", "dh0"), got, want):
+        off = ((a.double() - b).abs() / b.abs().clamp(min=1e-30)).max()
+        assert float(off) <= tol + (HALF[a.dtype] if name in ("y", "dx", "dgate") else 0.0), (name, float(off))
+
+
+@pytest.mark.parametrize("B,C,shift", LAYOUTS)
+def test_gates_that_forget(B, C, shift):
+    """bf16, sigmoid: three tokens with gates of -3 to -20 among such as keep, x of zero, so that all that there is of
+    a state and of dgate is what these leave. 600 steps of the state at 2^-24 for each product and its factor, 7e-5; at a
+    forgetting token the exponent's rounding, 29 x 2^-24, the exponential's 2^-22 and the reciprocal's 2^-23, or where a is
+    still 1 - w 2^-23 / sigmoid(-5) = 1.8e-5: 6e-5 for three. dgate has two such states: 2.6e-4."""
+    import gated_delta_rule_14_gb300 as kla
+    T, gen = 600, torch.Generator(device=DEV).manual_seed(C)
+
+    def some(*shape):
+        return torch.rand(shape, generator=gen, device=DEV) + 0.5
+    gate = torch.full((B, T, C), 6.0, device=DEV)
+    gate[:, [7, 70, 431]] = -3 - 17 * torch.arange(C, device=DEV) / (C - 1)
+    gate, x, dy = gate.bfloat16(), torch.zeros(B, T, C, device=DEV).bfloat16(), some(B, T, C).bfloat16()
+    h0, dh = 1e4 * some(B, C), some(B, C)
+    want = scan(x, gate, h0, "sigmoid", dy, dh)
+    assert float(want[1].min()) > 1e-25
+    close(run(place(x, shift), place(gate, shift), h0, "sigmoid", place(dy, shift), dh), want, 2.6e-4)
+    h = h0.clone()   # token by token
+    for t in range(T):
+        kla.gated_scan_step(x[:, t], gate[:, t], h)
+    assert float((h / want[1] - 1).abs().max()) <= 2.6e-4
