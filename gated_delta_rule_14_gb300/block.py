@@ -75,7 +75,8 @@ def gated_scan_fwd(x: torch.Tensor, gate: torch.Tensor, h0: Optional[torch.Tenso
                    final_state: bool = True, h_T: Optional[torch.Tensor] = None, states: bool = False,
                    workspace: Optional[torch.Tensor] = None):
     """A recurrence with one gate per channel over whole prompts: ``h_t = a_t h_{t-1} + (1 - a_t) x_t`` with
-    ``a = sigmoid(gate)`` (mode "sigmoid"), or ``h_t = a_t h_{t-1} + x_t`` with ``a = exp(gate)`` (mode "log").
+    ``a = sigmoid(gate)`` (mode "sigmoid"), or ``h_t = a_t h_{t-1} + x_t`` with ``a = exp(gate)`` (mode "log", gates of
+    at most 0; where larger ones take the product of 256 neighbouring factors or fewer past fp32, ``device_status`` says so).
 
     x, gate: [B,T,C] (bf16 or fp32; any strides with a dense last axis, as the slices of a packed projection); h0: fp32
     [B,C] or None (zeros). ``lengths`` (int32 [B]) masks the tokens from lengths[b] on: they leave the state alone and

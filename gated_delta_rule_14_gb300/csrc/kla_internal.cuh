@@ -12,7 +12,7 @@ namespace kla {
 // Device-side error bits, OR-ed into one word per device (see kla_device_status).
 enum : unsigned {
     kErrTimeout = 1u,      // a bounded wait gave up
-    kErrGateRange = 2u,    // per-channel log-decay outside the exact range of a factorised product
+    kErrGateRange = 2u,    // gates outside the exact range: of a factorised product (per channel), of a scan's products
 };
 
 // Everything a chunk-forward launcher needs; pointers are device pointers.

@@ -26,6 +26,7 @@
 #include <cuda.h>
 
 #include <atomic>
+#include <cfloat>
 #include <climits>
 
 #include "layer_dev.cuh"
@@ -129,6 +130,16 @@ __device__ __forceinline__ void tell_state(uint2 *p, int count, const float (&h)
 #pragma unroll
     for (int v = 0; v < kV; ++v) w[v] = make_uint2(kWhole, __float_as_uint(h[v]));
     tell<kV, kPairs>(p, count, w);
+}
+// Gates that grow: a product of factors that fp32 does not hold makes a NaN of a state of zero, and is reported. `a` is
+// the product of a channel's neighbouring tokens.
+template <bool kLog>
+__device__ __forceinline__ void watch(const ScanArgs &p, bool live, float a) {
+    if (kLog && live && a > FLT_MAX) atomicOr(p.err, kErrGateRange);
+}
+template <bool kLog>
+__device__ __forceinline__ void watch(const ScanArgs &p, int count, float2 a) {
+    watch<kLog>(p, (count > 0 && a.x > FLT_MAX) || (count > 1 && a.y > FLT_MAX), fmaxf(a.x, a.y));
 }
 // The state at the chain's start (zeros where none is given), and at its end where that is wanted.
 template <int kV>
@@ -307,6 +318,8 @@ __global__ void __launch_bounds__(32 * kWarps) scan_fwd_kernel(ScanArgs p) {
             ph[v] = fmaf(f.x, ph[v], f.y);
             pa[v] *= f.x;
         }
+    watch<kLog>(p, live, A[0]);
+    watch<kLog>(p, live, pa[0] * A[0]);
     float in[kV];
     if (warp == kWarps - 1) {
         uint2 *here = p.carry + (static_cast<int64_t>(b) * p.tiles + at.at) * p.C + c;
@@ -430,6 +443,8 @@ __global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(ScanArgs p) {
             sd[v] = fmaf(f, sd[v], backs[w][v * 32 + lane]);
             sa[v] *= f;
         }
+    watch<kLog>(p, live, A[0]);
+    watch<kLog>(p, live, sa[0] * A[0]);
     if (warp == 0) {
         float in[kV];
         uint2 *here = p.carry + (static_cast<int64_t>(b) * p.tiles + tile) * p.C + c;
@@ -603,6 +618,8 @@ struct Exact {
     }
     static __device__ __forceinline__ V reach(V dh, V k) { return shrink(dh, k); }
 };
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ float2 larger(float2 a, float2 b) { return make_float2(fmaxf(a.x, b.x), fmaxf(a.y, b.y)); }
 __device__ __forceinline__ float part(float v, int) { return v; }
 __device__ __forceinline__ float part(float2 v, int i) { return i ? v.y : v.x; }
 // The largest w of a lane's tokens, where it matters: bf16, sigmoid.
@@ -867,6 +884,8 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) scan_fwd_ring_kernel(ScanA
                 ph = L::fma(map_a[w][lane], ph, map_h[w][lane]);
                 pa = L::mul(pa, map_a[w][lane]);
             }
+        watch<kLog>(p, count, A);
+        watch<kLog>(p, count, L::mul(A, pa));
         const bool teller = warp == kWarps - 1 && at.at <= last;
         uint2 *here = p.carry + (static_cast<int64_t>(b) * p.tiles + at.at) * p.C + c;
         if (teller) {
@@ -926,7 +945,7 @@ struct Shared {
     uint64_t maps, carry, next[2], full[2];
 };
 
-template <typename L, Copies kBy, int kWarps, typename F>
+template <typename L, bool kLog, Copies kBy, int kWarps, typename F>
 __device__ __forceinline__ void carry_warp(const ScanArgs &p, Shared<typename L::V, kWarps> &sh, Turns &turns,
                                            unsigned ticket, int tile_tokens, F fetch_tile) {
     using V = typename L::V;
@@ -959,12 +978,13 @@ __device__ __forceinline__ void carry_warp(const ScanArgs &p, Shared<typename L:
         if (i == 0) ask();
         if (kBy == kTma && next < turns.total) fetch_tile(next, (i + 1) & 1);   // the gates' rows and that half are read
         if (tile <= last) {
-            V pa = L::all(1.f), pd = L::all(0.f);   // the tile's map
+            V pa = L::all(1.f), pd = L::all(0.f), most = pa;   // the tile's map, and the largest product on the way to it
 #pragma unroll
             for (int w = kWarps - 1; w >= 0; --w) {
                 const V a = sh.a[i & 1][w][lane];
                 pd = L::fma(a, pd, sh.d[w][lane]);
                 pa = L::mul(pa, a);
+                if (kLog) most = larger(most, pa);
             }
             float in[kV];
             if (tile == last) {
@@ -977,6 +997,7 @@ __device__ __forceinline__ void carry_warp(const ScanArgs &p, Shared<typename L:
             const V out = L::fma(pa, e, pd);
             if (tile > 0) tell_state<kV, kPairs>(here, count, parts(out));
             else finish<kV>(p, b, c, count, parts(out));
+            watch<kLog>(p, count, most);
 #pragma unroll
             for (int w = kWarps - 1; w >= 0; --w) {
                 sh.enter[w][lane] = e;
@@ -1031,7 +1052,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kCtas) scan_bwd_ring_kernel
     };
     if (warp == kWarps) {
         if (kBy == kTma && ticket < turns.total) fetch_tile(ticket, 0);
-        carry_warp<L, kBy, kWarps>(p, sh, turns, ticket, kTile, fetch_tile);
+        carry_warp<L, kLog, kBy, kWarps>(p, sh, turns, ticket, kTile, fetch_tile);
         return;
     }
     const uint32_t b_maps = smem_u32(&sh.maps), b_carry = smem_u32(&sh.carry), b_next = smem_u32(sh.next);
@@ -1092,6 +1113,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kCtas) scan_bwd_ring_kernel
         by_case<L, L>(m == kTok, false, map_tokens);
         const bool exact = most.any(count, m, [&](int i) { return of_g.template load<L>(gs + i * kRow, i); });
         if (exact) map_tokens(std::false_type{}, X{});
+        watch<kLog>(p, count, A);
         sh.a[turn & 1][warp][lane] = A;
         sh.h[turn & 1][warp][lane] = H;
         sh.d[warp][lane] = D;

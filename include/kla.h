@@ -301,7 +301,8 @@ size_t kla_chunk_bwd_workspace_size_ex(int B, int T, int H, int d_k, int d_v, kl
  * Synchronises `stream`, then reads and clears the device-side error flags that
  * bounded waits and range checks of earlier calls on this device may have set.
  * Returns KLA_OK, KLA_ERR_TIMEOUT, KLA_ERR_INVALID_ARG (a per-channel gate outside
- * the exact range of the tensor-core path) or KLA_ERR_CUDA.
+ * the exact range of the tensor-core path, or products of a scan's gates past that of fp32: see
+ * kla_gated_scan_fwd) or KLA_ERR_CUDA.
  */
 kla_status kla_device_status(void *stream);
 

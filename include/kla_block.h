@@ -31,7 +31,11 @@ extern "C" {
  *     KLA_SCAN_SIGMOID   h_t = a_t h_{t-1} + (1 - a_t) x_t,   a_t = 1 / (1 + exp(-gate_t))
  *     KLA_SCAN_LOG       h_t = a_t h_{t-1} + x_t,             a_t = exp(gate_t)
  *
- * and y_t = h_t, for t = 0 .. n_b - 1, where n_b = lengths[b] (T when lengths is NULL). Tokens
+ * A gate is at most 0 in KLA_SCAN_LOG, as a decay's is. Larger ones are taken as they are as long as fp32 holds the
+ * products of neighbouring a_t, of 256 tokens at most; where one passes that range, states may be NaN that are not, and
+ * kla_device_status reports KLA_ERR_INVALID_ARG.
+ *
+ * y_t = h_t, for t = 0 .. n_b - 1, where n_b = lengths[b] (T when lengths is NULL). Tokens
  * t >= n_b are masked: whatever x and gate hold there (NaN included) they leave the state as it is,
  * and y_t = 0. A gate of -inf forgets the state (a_t = 0; a state that is not finite leaves a NaN),
  * one of +inf keeps it in KLA_SCAN_SIGMOID.

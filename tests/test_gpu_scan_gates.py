@@ -79,3 +79,51 @@ def test_gates_that_forget(B, C, shift):
     for t in range(T):
         kla.gated_scan_step(x[:, t], gate[:, t], h)
     assert float((h / want[1] - 1).abs().max()) <= 2.6e-4
+
+
+TYPED = [(*at, dtype) for dtype in (torch.bfloat16, torch.float32) for at in LAYOUTS if dtype == torch.bfloat16 or at[1] != 34]
+
+
+@pytest.mark.parametrize("B,C,shift,dtype", TYPED)
+def test_gates_that_grow(B, C, shift, dtype):
+    """Logarithms above 0: factors whose products fp32 holds (e^30 here) give what the definition does. Of 600 factors each
+    is off by 2^-22 and its products by 2^-24, with nothing that cancels: 600 x 1.25 x 2^-22 = 1.8e-4, twice that for
+    dgate, which has a state and a gradient. Masked tokens' gates count for nothing."""
+    import gated_delta_rule_14_gb300 as kla
+    T, gen = 600, torch.Generator(device=DEV).manual_seed(C)
+
+    def some(*shape):
+        return torch.rand(shape, generator=gen, device=DEV) + 0.5
+    gate = torch.where(torch.arange(T, device=DEV) % 300 < 150, 0.2, -0.2)[None, :, None] * some(1, 1, C)
+    gate = gate.expand(B, T, C).to(dtype)
+    x, dy, h0, dh = some(B, T, C).to(dtype), some(B, T, C).to(dtype), some(B, C), some(B, C)
+    want = scan(x, gate, h0, "log", dy, dh)
+    close(run(place(x, shift), place(gate, shift), h0, "log", place(dy, shift), dh), want, 3.6e-4)
+    n = torch.full((B,), T - 170, dtype=torch.int32, device=DEV)
+    far = gate.clone()
+    far[:, T - 170:] = 90.0
+    y, h_T, _ = kla.gated_scan_fwd(place(x, shift), place(far, shift), h0, mode="log", lengths=n)
+    kla.device_status(DEV)
+    assert float(((h_T / want[0][:, T - 171]) - 1).abs().max()) <= 1.8e-4 and float(y[:, T - 170:].abs().max()) == 0.0
+
+
+@pytest.mark.parametrize("B,C,shift,dtype", TYPED)
+def test_products_past_fp32_are_reported(B, C, shift, dtype):
+    """128 factors of e, times a state of zero: the product of a stretch is infinite, and a NaN may come of it. The call says
+    so, forward and backward, and the next one is as good as any."""
+    import gated_delta_rule_14_gb300 as kla
+    T = 600
+    x = torch.zeros(B, T, C, dtype=dtype, device=DEV)
+    x, grow, calm = place(x, shift), place(torch.full_like(x, 1.0), shift), place(torch.full_like(x, -1.0), shift)
+    kla.device_status(DEV)
+    kla.gated_scan_fwd(x, grow, mode="log")
+    with pytest.raises(kla.KlaError):
+        kla.device_status(DEV)
+    states = torch.zeros(B, -(-T // 128), C, device=DEV)
+    kla.gated_scan_bwd(x, grow, x, states, mode="log")
+    with pytest.raises(kla.KlaError):
+        kla.device_status(DEV)
+    y, h_T, s = kla.gated_scan_fwd(x, calm, mode="log", states=True)
+    g = kla.gated_scan_bwd(x, calm, x, s, mode="log")
+    kla.device_status(DEV)
+    assert all(float(t.abs().max()) == 0.0 for t in (y, h_T, *g.values()))
