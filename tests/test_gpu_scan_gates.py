@@ -127,3 +127,54 @@ def test_products_past_fp32_are_reported(B, C, shift, dtype):
     g = kla.gated_scan_bwd(x, calm, x, s, mode="log")
     kla.device_status(DEV)
     assert all(float(t.abs().max()) == 0.0 for t in (y, h_T, *g.values()))
+
+
+# losses of 1e-5 to 1e-3 a token, one for every channel
+def slow_gates(C, dtype, mode):
+    rate = 10.0 ** (-5 + 2 * torch.arange(C, device=DEV, dtype=torch.float64) / (C - 1))
+    return (-rate if mode == "log" else torch.log((1 - rate) / rate)).to(dtype)
+
+
+@pytest.mark.parametrize("mode", ["log", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B,T,C,shift", [(1, 100000, 64, 0), (1, 100000, 65, 0), (1, 100000, 34, 1), (2, 50000, 512, 0)])
+def test_memory_of_100000_tokens(B, T, C, shift, dtype, mode):
+    """Constant gates, whose errors all go to one side, and x, dy above zero, so that nothing cancels. What is told of 128
+    tokens or more has 8 stretches' products, 7 of those and a state, each rounded by 2^-25: of the decay per token r that
+    is 2^-28 / r, 3.7e-4 at 1e-5. Within a stretch of at most 32 tokens a factor's 2^-22 make 8e-6 and sums 32 x 2^-24 as
+    much: 3e-5 more."""
+    gen = torch.Generator(device=DEV).manual_seed(C)
+
+    def some(*shape):
+        return torch.rand(shape, generator=gen, device=DEV) + 0.5
+    one = slow_gates(C, dtype, mode)
+    x, dy, dh = some(B, T, C).to(dtype), some(B, T, C).to(dtype), some(B, C)
+    gate = place(one.expand(B, T, C).contiguous(), shift)
+    y, h_T, dx, dg, dh0 = run(place(x, shift), gate, torch.zeros(B, C, device=DEV), mode, place(dy, shift), dh)
+    g = one.double()
+    log_a, w = (g, torch.ones_like(g)) if mode == "log" else (torch.nn.functional.logsigmoid(g), torch.sigmoid(-g))
+    past = torch.exp(torch.arange(T, device=DEV)[:, None] * log_a)
+    state = (x.double() * past.flip(0)).sum(1) * w
+    reach = torch.exp(log_a) * (dh.double() * past[-1] + (dy.double() * past).sum(1))
+    tol = 2.0**-28 / (1 - torch.exp(log_a)) + 3e-5
+    for name, a, b in (("h_T", h_T, state), ("dh0", dh0, reach)):
+        off = (a.double() / b - 1).abs() / tol
+        assert float(off.max()) <= 1, (name, float(off.max()))
+
+
+@pytest.mark.parametrize("mode", ["log", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_steps_with_long_memory(dtype, mode):
+    """4096 single tokens with the same gates: every step rounds the state by 2^-24, in the mean of a random walk 4e-6;
+    ten times that."""
+    import gated_delta_rule_14_gb300 as kla
+    C, T, gen = 64, 4096, torch.Generator(device=DEV).manual_seed(7)
+    one = slow_gates(C, dtype, mode)
+    x = (torch.rand((T, 1, C), generator=gen, device=DEV) + 0.5).to(dtype)
+    h, gate = torch.zeros(1, C, device=DEV), one[None].contiguous()
+    for t in range(T):
+        kla.gated_scan_step(x[t], gate, h, mode=mode)
+    g = one.double()
+    log_a, w = (g, torch.ones_like(g)) if mode == "log" else (torch.nn.functional.logsigmoid(g), torch.sigmoid(-g))
+    want = (x[:, 0].double() * torch.exp(torch.arange(T, device=DEV).flip(0)[:, None] * log_a)).sum(0) * w
+    assert float((h[0].double() / want - 1).abs().max()) <= 4e-5
