@@ -80,7 +80,7 @@ def gated_scan_fwd(x: torch.Tensor, gate: torch.Tensor, h0: Optional[torch.Tenso
 
     x, gate: [B,T,C] (bf16 or fp32; any strides with a dense last axis, as the slices of a packed projection); h0: fp32
     [B,C] or None (zeros). ``lengths`` (int32 [B]) masks the tokens from lengths[b] on: they leave the state alone and
-    their outputs are 0. Returns (y = h [B,T,C] in x's dtype, h_T fp32 [B,C] or None, what ``gated_scan_bwd`` needs
+    their outputs are 0. A channel whose state is infinite or NaN stays one or the other. Returns (y = h [B,T,C] in x's dtype, h_T fp32 [B,C] or None, what ``gated_scan_bwd`` needs
     with ``states``, else None); ``h_T`` may be passed, and may be ``h0``.
     """
     device, code, (B, T, C), dense = _scan_shapes(x, gate, lengths)

@@ -37,8 +37,9 @@ extern "C" {
  *
  * y_t = h_t, for t = 0 .. n_b - 1, where n_b = lengths[b] (T when lengths is NULL). Tokens
  * t >= n_b are masked: whatever x and gate hold there (NaN included) they leave the state as it is,
- * and y_t = 0. A gate of -inf forgets the state (a_t = 0; a state that is not finite leaves a NaN),
- * one of +inf keeps it in KLA_SCAN_SIGMOID.
+ * and y_t = 0. A gate of -inf forgets the state (a_t = 0), one of +inf keeps it in KLA_SCAN_SIGMOID (to
+ * 2^-100 of x). A channel whose state is infinite or NaN stays one or the other from there on, whatever
+ * its gates, and which of the two is not said; what is less than 2^-126 of a state may count as nothing.
  *
  *   x, gate  [B, T, C] dtype, last axis contiguous. `strides` gives the element strides of the batch
  *            and token axes of x, then of gate (4 values, none negative); NULL means contiguous

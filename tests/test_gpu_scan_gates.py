@@ -178,3 +178,28 @@ def test_steps_with_long_memory(dtype, mode):
     log_a, w = (g, torch.ones_like(g)) if mode == "log" else (torch.nn.functional.logsigmoid(g), torch.sigmoid(-g))
     want = (x[:, 0].double() * torch.exp(torch.arange(T, device=DEV).flip(0)[:, None] * log_a)).sum(0) * w
     assert float((h[0].double() / want - 1).abs().max()) <= 4e-5
+
+
+@pytest.mark.parametrize("mode", ["log", "sigmoid"])
+@pytest.mark.parametrize("B,C,shift,dtype", TYPED)
+def test_states_that_are_not_finite(B, C, shift, dtype, mode):
+    """A state that begins as infinity, one that an infinite input makes so, one that a NaN does: from there on nothing
+    finite comes of these channels, whether their gates keep or forget, and the others keep their bits, gradients too."""
+    import gated_delta_rule_14_gb300 as kla
+    T, gen = 600, torch.Generator(device=DEV).manual_seed(C)
+    x, dy = (torch.randn((B, T, C), generator=gen, device=DEV).to(dtype) for _ in range(2))
+    gate = torch.randn((B, T, C), generator=gen, device=DEV)
+    gate = (-torch.nn.functional.softplus(gate) if mode == "log" else gate).to(dtype)
+    gate[:, 400, 5:9] = -float("inf")
+    h0, dh = torch.randn((B, C), generator=gen, device=DEV), torch.zeros(B, C, device=DEV)
+    clean = run(place(x, shift), place(gate, shift), h0, mode, place(dy, shift), dh)
+    x, h0 = x.clone(), h0.clone()
+    h0[:, 5] = float("inf")
+    x[:, 270, 6] = -float("inf")
+    x[:, 0, 7] = float("nan")
+    got = run(place(x, shift), place(gate, shift), h0, mode, place(dy, shift), dh)
+    y, h_T = got[0].float(), got[1]
+    assert not y[:, :, 5].isfinite().any() and not y[:, 270:, 6].isfinite().any() and not y[:, :, 7].isfinite().any()
+    assert not h_T[:, 5:8].isfinite().any() and torch.equal(y[:, :270, 6], clean[0][:, :270, 6].float())
+    rest = [c for c in range(C) if c not in (5, 6, 7)]
+    assert all(torch.equal(a[..., rest], b[..., rest]) for a, b in zip(got, clean))
