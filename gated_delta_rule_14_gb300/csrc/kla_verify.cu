@@ -1,10 +1,11 @@
 // kla_verify.cu -- verification of drafted tokens: which of them the target accepts, and the token after those.
 //
-// Comparisons are exact: u q of two 24-bit numbers fits the 53 bits of a double. Running sums are held to 2^-46 of the
+// Comparisons are exact: u q of two 24-bit numbers fits the 53 bits of a double. Running sums are held to 2^-39 of the
 // whole or better, so that a token's border is off by far less than what lies between two values of a 24-bit random
 // number; sums in fp32 over 100000 tokens would move borders by whole tokens. The SM adds doubles at a 64th of the rate
 // of floats, so 16 weights at a time are added as pairs of floats, a sum and what it has lost, and only those join as
-// doubles.
+// doubles. What 16 weights of sum S lose is 16 x 2^-24 S at most, each addition to it rounds by 2^-24 of that, and 16
+// of them make 2^-40 S.
 // Measured: 64 sequences of 8 drafts, 100003 tokens fp32, 25 us in a row of calls (floor 7.5); one of 4 drafts, 32000
 // tokens, 9.6 us on the GPU, which is a chain of trips: lengths and drafts, their probabilities, the rows, the sums across the
 // cluster, the piece, the walk. With all sums in doubles, and every thread adding up all stretches, 156 and 62 us.

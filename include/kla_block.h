@@ -179,9 +179,9 @@ size_t kla_add_norm_bwd_workspace_size(int64_t rows, int n, kla_dtype dtype);
  * with p = target[b, i, :] and q = draft_probs[b, i, :]; the product is exact. After `a` accepted
  * drafts the next token is drawn by uniforms[b, K]: from target[b, n_b, :] where all were accepted,
  * else from max(p - q, 0) at position a (from p where that is zero everywhere): the lowest token
- * whose running sum, held to 2^-46 of the whole or better, is above uniforms[b, K] times the whole. Tokens are thus distributed
+ * whose running sum, held to 2^-39 of the whole or better, is above uniforms[b, K] times the whole. Tokens are thus distributed
  * as the target's, whatever the draft. Rows need not sum to one; values that are not above zero (NaN
- * among them) count as zero, +inf as the largest finite value.
+ * among them) count as zero, +inf (in bf16 too) as the largest finite value of fp32.
  *   draft        int32 [B, K]; a token outside [0, V) is not accepted, and has q = 0
  *   draft_probs  [B, K, V] dtype, or NULL: the draft was sure of its tokens (q = 1 there, 0 elsewhere)
  *   target       [B, K + 1, V] dtype

@@ -185,3 +185,46 @@ def test_refusals():
         kla.verify_draft(draft, q, p[0], u)
     with pytest.raises(ValueError):
         kla.verify_draft(draft.cpu(), q, p, u)
+
+
+@pytest.mark.parametrize("dtype", [F, BF])
+@pytest.mark.parametrize("V", [2048, 2049])
+def test_one_large_weight_and_many_small_ones(V, dtype):
+    """A token of nearly all the weight and 2^-25 to 2^-24 of it for each of the others, the sums' worst case: running sums
+    are off by 2^-39 of the whole at most, and marks that lie 2^-38 or more from a border find their token. Once from the
+    row itself, once from what a draft leaves of it."""
+    import gated_delta_rule_14_gb300 as kla
+    g = torch.Generator().manual_seed(V)
+    small = (2.0**-25 * (1 + torch.rand(V, generator=g))).to(dtype)
+    row = small.clone()
+    at = [0, 5, 700, V - 1]
+    rows = []
+    for i in at:
+        r = row.clone()
+        r[i] = 1.0
+        rows.append(r)
+    B = 256
+    target = torch.stack([rows[b % 4] for b in range(B)])
+    u = 1 - torch.randint(1, 2**11, (B,), generator=g).float() * 2.0**-24
+    run = target.double().cumsum(1)
+    mark = u.double()[:, None] * run[:, -1:]
+    clear = ((run - mark).abs() > 2.0**-38 * run[:, -1:]).all(1)
+    assert int(clear.sum()) >= 200
+    want = (run > mark).int().argmax(1)
+    empty = torch.empty(B, 0, dtype=torch.int32, device=DEV)
+    _, tokens = kla.verify_draft(empty, None, target[:, None].contiguous().to(DEV), u[:, None].to(DEV))
+    assert torch.equal(tokens[:, 0].cpu()[clear].long(), want[clear])
+    # a draft refused whose row covers a quarter of every weight: exact in either type
+    draft, us = torch.full((B, 1), 1, dtype=torch.int32, device=DEV), torch.stack([torch.full((B,), 1 - 2.0**-24), u], 1)
+    two = target[:, None].expand(B, 2, V).contiguous()
+    q = target[:, None] * 0.25
+    q[:, 0, 1] = 1.0   # above the target's: refused, and nothing left of token 1
+    rest = (target.double() - q[:, 0].double()).clamp(min=0)
+    run = rest.cumsum(1)
+    mark = u.double()[:, None] * run[:, -1:]
+    clear = ((run - mark).abs() > 2.0**-38 * run[:, -1:]).all(1)
+    assert int(clear.sum()) >= 200
+    took, tokens = kla.verify_draft(draft, q.to(DEV), two.to(DEV), us.to(DEV))
+    kla.device_status(DEV)
+    assert int(took.sum()) == 0
+    assert torch.equal(tokens[:, 0].cpu()[clear].long(), (run > mark).int().argmax(1)[clear])
