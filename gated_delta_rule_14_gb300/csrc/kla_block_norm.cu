@@ -599,10 +599,12 @@ __global__ void __launch_bounds__(1024) block_norm_join_kernel(const float *part
 // ------------------------------------------------------------------------------------ host side
 constexpr int kSms = 152;
 
-kla_status check(int64_t rows, int groups, int n, kla_dtype dtype) {
+// Groups with weights of their own are a grid's axis; others are the gate's rows between two strides, as many as there are
+// tokens.
+kla_status check(int64_t rows, int groups, int n, kla_dtype dtype, bool own) {
     if (rows < 0 || groups < 1 || n < 1) return KLA_ERR_INVALID_ARG;
     if (dtype != KLA_DTYPE_F32 && dtype != KLA_DTYPE_BF16) return KLA_ERR_INVALID_ARG;
-    if (n < 3 || n > 65536 || groups > 65535 || rows > INT_MAX / groups) return KLA_ERR_UNSUPPORTED;
+    if (n < 3 || n > 65536 || (own && groups > 65535) || rows > INT_MAX / groups) return KLA_ERR_UNSUPPORTED;
     return KLA_OK;
 }
 
@@ -786,7 +788,7 @@ kla_status kla_gated_norm_fwd(const void *x, const void *gate, int64_t gate_stri
                               int weight_groups, void *y, float *mean, float *rstd, int64_t rows, int groups, int n,
                               kla_dtype dtype, kla_norm_kind norm, kla_activation act, float eps, void *stream) {
     using namespace kla;
-    const kla_status st = check(rows, groups, n, dtype);
+    const kla_status st = check(rows, groups, n, dtype, weight_groups != 0);
     if (st != KLA_OK) return st;
     if (!(eps >= 0.f) || eps - eps != 0.f) return KLA_ERR_INVALID_ARG;
     if ((norm != KLA_NORM_RMS && norm != KLA_NORM_LAYER) || (act != KLA_ACT_SILU && act != KLA_ACT_SIGMOID))
@@ -813,7 +815,7 @@ kla_status kla_gated_norm_fwd(const void *x, const void *gate, int64_t gate_stri
 }
 
 size_t kla_gated_norm_bwd_workspace_size(int64_t rows, int groups, int n, kla_dtype dtype, int weight_groups) {
-    if (kla::check(rows, groups, n, dtype) != KLA_OK || rows == 0) return 0;
+    if (kla::check(rows, groups, n, dtype, weight_groups != 0) != KLA_OK || rows == 0) return 0;
     return kla::workspace_bytes_of(rows * groups, weight_groups ? groups : 1, n, dtype == KLA_DTYPE_BF16 ? 2 : 4,
                                    kla::kGatedBwd);
 }
@@ -823,7 +825,7 @@ kla_status kla_gated_norm_bwd(const void *dy, const void *x, const void *gate, i
                               void *dgate, float *dweight, int64_t rows, int groups, int n, kla_dtype dtype,
                               kla_activation act, void *workspace, size_t workspace_bytes, void *stream) {
     using namespace kla;
-    const kla_status st = check(rows, groups, n, dtype);
+    const kla_status st = check(rows, groups, n, dtype, weight_groups != 0);
     if (st != KLA_OK) return st;
     if (act != KLA_ACT_SILU && act != KLA_ACT_SIGMOID) return KLA_ERR_INVALID_ARG;
     if (gate_stride < static_cast<int64_t>(groups) * n) return KLA_ERR_INVALID_ARG;
@@ -856,7 +858,7 @@ kla_status kla_add_norm_fwd(const void *x, const void *residual, const float *we
                             void *sum, float *mean, float *rstd, int64_t rows, int n, kla_dtype dtype,
                             kla_norm_kind norm, float eps, void *stream) {
     using namespace kla;
-    const kla_status st = check(rows, 1, n, dtype);
+    const kla_status st = check(rows, 1, n, dtype, false);
     if (st != KLA_OK) return st;
     if (!(eps >= 0.f) || eps - eps != 0.f) return KLA_ERR_INVALID_ARG;
     if (norm != KLA_NORM_RMS && norm != KLA_NORM_LAYER) return KLA_ERR_INVALID_ARG;
@@ -879,7 +881,7 @@ kla_status kla_add_norm_fwd(const void *x, const void *residual, const float *we
 }
 
 size_t kla_add_norm_bwd_workspace_size(int64_t rows, int n, kla_dtype dtype) {
-    if (kla::check(rows, 1, n, dtype) != KLA_OK || rows == 0) return 0;
+    if (kla::check(rows, 1, n, dtype, false) != KLA_OK || rows == 0) return 0;
     return kla::workspace_bytes_of(rows, 1, n, dtype == KLA_DTYPE_BF16 ? 2 : 4, kla::kAddBwd);
 }
 
@@ -888,7 +890,7 @@ kla_status kla_add_norm_bwd(const void *dy, const void *dsum, const void *x, con
                             void *dresidual, float *dweight, float *dscale, int64_t rows, int n, kla_dtype dtype,
                             void *workspace, size_t workspace_bytes, void *stream) {
     using namespace kla;
-    const kla_status st = check(rows, 1, n, dtype);
+    const kla_status st = check(rows, 1, n, dtype, false);
     if (st != KLA_OK) return st;
     if (!scale && (dx || dscale)) return KLA_ERR_INVALID_ARG;
     if (rows > 0 && (!dy || !x || !residual || !rstd || !dresidual || (scale && !dx))) return KLA_ERR_INVALID_ARG;
