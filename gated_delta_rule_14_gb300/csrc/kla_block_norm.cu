@@ -51,27 +51,37 @@ __device__ __forceinline__ float2 add(float2 a, float2 b) { return add2(a, b); }
 __device__ __forceinline__ float across(float v, int off) { return __shfl_xor_sync(0xffffffffu, v, off); }
 __device__ __forceinline__ float2 across(float2 v, int off) { return make_float2(across(v.x, off), across(v.y, off)); }
 
+// The sigmoid, and exp(-z).
 template <typename T>
-__device__ __forceinline__ float2 sigmoid(float2 z) {
-    if (sizeof(T) == 4) return make_float2(1.f / (1.f + expf(-z.x)), 1.f / (1.f + expf(-z.y)));
+__device__ __forceinline__ float2 sigmoid(float2 z, float2 &e) {
+    if (sizeof(T) == 4) {
+        e = make_float2(expf(-z.x), expf(-z.y));
+        return make_float2(1.f / (1.f + e.x), 1.f / (1.f + e.y));
+    }
     // bf16: the hardware's exponential and reciprocal, off by 2^-21 at z of 10, far below z's own 2^-9
-    float2 e = mul2(z, both(-1.4426950408889634f));
+    e = mul2(z, both(-1.4426950408889634f));
     asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
     asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
-    e = add2(e, both(1.f));
-    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.x));
-    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.y));
-    return e;
+    float2 s = add2(e, both(1.f));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(s.x));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(s.y));
+    return s;
 }
-// act(z), and act'(z)
+// act(z), and act'(z). The sigmoid's slope is s (1 - s), where 1 - s is taken as exp(-z) s: as a difference it would have
+// lost 2^-10 of itself at z of 10 and all at 17. (At most 1: an infinite exponential and s = 0 make a NaN, which is not
+// the smaller.)
 template <typename T>
 __device__ __forceinline__ float2 activation(float2 z, int silu) {
-    const float2 s = sigmoid<T>(z);
+    float2 e;
+    const float2 s = sigmoid<T>(z, e);
     return silu ? mul2(z, s) : s;
 }
 template <typename T>
 __device__ __forceinline__ float2 activation(float2 z, int silu, float2 &slope) {
-    const float2 s = sigmoid<T>(z), rest = fma2(s, both(-1.f), both(1.f));
+    float2 e;
+    const float2 s = sigmoid<T>(z, e);
+    e = mul2(e, s);
+    const float2 rest = make_float2(fminf(e.x, 1.f), fminf(e.y, 1.f));
     slope = mul2(s, silu ? fma2(z, rest, both(1.f)) : rest);
     return silu ? mul2(z, s) : s;
 }
