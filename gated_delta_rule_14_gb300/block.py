@@ -301,7 +301,7 @@ def rotary_fwd(q: torch.Tensor, k: Optional[torch.Tensor], freqs: torch.Tensor,
     q: [B,T,H,d], k: [B,T,K,d] or None (bf16 or fp32; any strides with a dense last axis, as the slices of a packed
     projection); freqs: fp32 [rot / 2] (``rotary_freqs``); positions: int64 or int32 [B,T], or None (token t has
     position t). ``layout``: "half" pairs values i and i + rot / 2, "interleaved" 2 i and 2 i + 1. Returns (q, k)
-    turned, contiguous unless ``out_q`` and ``out_k`` are given, which may be q and k themselves.
+    turned, contiguous unless ``out_q`` and ``out_k`` are given, which may be q and k themselves, or slices of one tensor.
     """
     return _rotary("kla_rotary_fwd", q, k, freqs, positions, layout, scale, out_q, out_k, 0)
 

@@ -411,12 +411,12 @@ bool meet(const Axis *axes, int n, int64_t apart) {
         if (meet(axes + 1, n - 1, apart - a.stride * i)) return true;
     return false;
 }
-// The same of queries and keys, where an output of the one may lie over an input of the other: slices of a packed
-// projection reach over each other without sharing anything. Those have equal strides; of others it is not asked.
-bool share(const void *q, const int64_t *qs, const void *k, const int64_t *ks, const int *H, int B, int T, int d, int esz) {
+// The same of an output and an input, or another output: slices of a packed projection reach over each other without
+// sharing anything. Those have equal strides; of others it is not asked.
+bool share(const void *q, const int64_t *qs, int Hq, const void *k, const int64_t *ks, int Hk, int B, int T, int d, int esz) {
     const int64_t bytes = static_cast<const char *>(k) - static_cast<const char *>(q);
     if (bytes % esz) return true;
-    const int64_t size[2][4] = {{B, T, H[0], d}, {B, T, H[1], d}};
+    const int64_t size[2][4] = {{B, T, Hq, d}, {B, T, Hk, d}};
     Axis axes[4];
     for (int a = 0; a < 4; ++a) {   // k's index less q's, times the stride, is minus their distance
         const int64_t sq = a < 3 ? qs[a] : 1, sk = a < 3 ? ks[a] : 1;
@@ -484,16 +484,17 @@ extern "C" kla_status kla_rotary(const void *q, const void *k, void *q_out, void
     const Span sf = span(freqs, rot / 2 * 4ull);
     const Span sp = span(positions, static_cast<size_t>(B) * T * (positions_are_64 ? 8 : 4));
     if (!aligned(freqs, 4) || !aligned(positions, positions_are_64 ? 8 : 4)) return KLA_ERR_INVALID_ARG;
-    for (int m = 0; m < 2; ++m) {
+    for (int m = 0; m < 2; ++m)
         if (overlaps(os[m], sf) || overlaps(os[m], sp)) return KLA_ERR_INVALID_ARG;
-        // slices of one packed tensor reach over each other: in place, an output covers what its input covers
-        if (in_place[m]) continue;
-        if (overlaps(os[m], is[0]) || overlaps(os[m], is[1]) || overlaps(os[m], os[1 - m])) return KLA_ERR_INVALID_ARG;
-    }
-    // in place: the other's input, which may be read later, is not written over
-    if (H[1] > 0 && (in_place[0] || in_place[1]) && overlaps(is[0], is[1]) &&
-        share(q, p.is[0], k, p.is[1], H, B, T, d, static_cast<int>(esz)))
-        return KLA_ERR_INVALID_ARG;
+    auto apart = [&](const Span &a, const void *pa, const int64_t *sa, int ha, const Span &b, const void *pb,
+                     const int64_t *sb, int hb) {
+        return !overlaps(a, b) || !share(pa, sa, ha, pb, sb, hb, B, T, d, static_cast<int>(esz));
+    };
+    for (int m = 0; m < 2; ++m)
+        for (int j = 0; j < 2; ++j)   // in place: its own input apart, and what the other reads later is not written over
+            if (!(m == j && in_place[m]) && !apart(os[m], out[m], p.os[m], H[m], is[j], in[j], p.is[j], H[j]))
+                return KLA_ERR_INVALID_ARG;
+    if (!apart(os[0], out[0], p.os[0], H[0], os[1], out[1], p.os[1], H[1])) return KLA_ERR_INVALID_ARG;
     p.freqs = freqs;
     p.positions = positions;
     p.wide = positions_are_64 != 0;

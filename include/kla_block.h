@@ -99,7 +99,8 @@ kla_status kla_gated_scan_step(const void *x, int64_t x_stride, const void *gate
  *   q_out, k_out  the same shapes
  *   strides    element strides of the batch, token and head axes of q, k, q_out, k_out (12 values,
  *              none negative); NULL means contiguous tensors. An output may be its own input in place
- *              (the same address and strides; q and k share no value then), else it overlaps no input
+ *              (the same address and strides; q and k share no value then), else it shares no value with an
+ *              input or the other output: slices of one tensor, of equal strides, may reach over each other
  *   freqs      fp32 [rot / 2], finite
  *   positions  [B, T] int64 (positions_are_64 != 0) or int32, contiguous, or NULL: token t has position t
  *   scale      finite

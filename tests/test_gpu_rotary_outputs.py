@@ -1,0 +1,58 @@
+"""Rotary positions into slices of one tensor: outputs that reach over each other, or over an input, and share no value."""
+import ctypes
+
+import pytest
+import torch
+
+from gpu_util import DEV
+
+A = 1 << 40   # addresses that nothing is read from: refusals come before any launch
+
+
+def call(q, k, oq, ok, st, H=4, K=2):
+    from gated_delta_rule_14_gb300 import _native
+    strides = (ctypes.c_int64 * 12)(*st)
+    return _native.lib().kla_rotary(q, k, oq, ok, strides, ctypes.cast(A - (1 << 20), ctypes.POINTER(ctypes.c_float)), None, 0, 2, 3,
+                                    H, K, 16, 16, 0, 1, 1.0, 0, None)
+
+
+DENSE, PACKED = (3 * 4 * 16, 4 * 16, 16), (3 * 6 * 16, 6 * 16, 16)
+DENSE_K = (3 * 2 * 16, 2 * 16, 16)
+
+
+@pytest.mark.parametrize("ok", [A, A + 3 * 16 * 2, A + 4 * 16 * 2 - 2, A + 6 * 16 * 2])   # keys from the queries' heads, or a token's
+def test_outputs_that_share_values_are_refused(ok):
+    far = A + (1 << 30)
+    assert call(far, far + (1 << 20), A, ok, (*DENSE, *DENSE_K, *PACKED, *PACKED)) == 1
+
+
+def test_outputs_over_inputs_are_refused():
+    far = A + (1 << 30)
+    assert call(A, far, A + 32, far + (1 << 20), (*PACKED, *DENSE_K, *PACKED, *DENSE_K)) == 1   # a head further on
+    assert call(A, far, far + (1 << 20), A + 3 * 32, (*PACKED, *DENSE_K, *DENSE, *PACKED)) == 1   # the keys over the queries' last
+    assert call(A, far, A, A + 3 * 32, (*PACKED, *DENSE_K, *PACKED, *PACKED)) == 1   # the same, queries in place
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,K,d,rot", [(4, 4, 64, 64), (4, 1, 128, 126), (2, 8, 16, 4), (1, 1, 7, 6)])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_outputs_into_one_tensor(H, K, d, rot, layout, dtype):
+    import gated_delta_rule_14_gb300 as kla
+    B, T, gen = 3, 50, torch.Generator(device=DEV).manual_seed(d)
+    freqs, _ = kla.rotary_freqs(rot, device=DEV)
+    q, k = (torch.randn((B, T, h, d), generator=gen, device=DEV).to(dtype) for h in (H, K))
+    want = kla.rotary_fwd(q, k, freqs, layout=layout)
+    kv = torch.full((B, T, H + 2 * K, d), 7.0, dtype=dtype, device=DEV)
+    oq, ok, rest = kv.split([H, K, K], 2)
+    kla.rotary_fwd(q, k, freqs, layout=layout, out_q=oq, out_k=ok)   # both, beside what is left as it was
+    assert torch.equal(oq, want[0]) and torch.equal(ok, want[1]) and bool((rest == 7.0).all())
+    kv.fill_(7.0)
+    oq.copy_(q)
+    kla.rotary_fwd(oq, k, freqs, layout=layout, out_q=oq, out_k=ok)   # queries in place, keys into the same tensor
+    assert torch.equal(oq, want[0]) and torch.equal(ok, want[1]) and bool((rest == 7.0).all())
+    kv.fill_(7.0)
+    rest.copy_(k)
+    kla.rotary_fwd(q, rest, freqs, layout=layout, out_q=oq, out_k=ok)   # keys from one slice into another
+    assert torch.equal(oq, want[0]) and torch.equal(ok, want[1]) and torch.equal(rest, k)
+    kla.device_status(DEV)
