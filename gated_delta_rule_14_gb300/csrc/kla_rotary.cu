@@ -28,7 +28,8 @@ struct RotaryArgs {
     int inverse;
 };
 
-// Turns a token, as a fraction of 2^64.
+// Turns a token, as a fraction of 2^64. Of f / 2 pi two roundings of 2^-53 are lost, 2^-54.6 f of a turn, and the position
+// times as much of the angle; of its sign and upper 32 bits fp32 keeps 2^-26 of a turn.
 __device__ __forceinline__ unsigned long long turn_rate(float freq) {
     double t = static_cast<double>(freq) * 0.15915494309189533577;
     t -= floor(t);

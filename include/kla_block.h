@@ -106,7 +106,8 @@ kla_status kla_gated_scan_step(const void *x, int64_t x_stride, const void *gate
  *   scale      finite
  *   sizes      B, T, Hk >= 0, Hq >= 1, 1 <= d <= 1024, rot even, 0 <= rot <= d
  * Angles are held as a 64-bit fraction of a turn, so that they do not lose bits with the position
- * (2^-24 of a turn at most at positions up to 2^28); only sine and cosine are taken in fp32.
+ * (2^-24 of a turn at most for frequencies up to 4 at positions up to 2^28, in proportion to both
+ * beyond); only sine and cosine are taken in fp32.
  */
 typedef enum { KLA_ROTARY_HALF = 0, KLA_ROTARY_INTERLEAVED = 1 } kla_rotary_layout;
 

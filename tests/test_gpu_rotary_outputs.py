@@ -56,3 +56,27 @@ def test_outputs_into_one_tensor(H, K, d, rot, layout, dtype):
     kla.rotary_fwd(q, rest, freqs, layout=layout, out_q=oq, out_k=ok)   # keys from one slice into another
     assert torch.equal(oq, want[0]) and torch.equal(ok, want[1]) and torch.equal(rest, k)
     kla.device_status(DEV)
+
+
+@pytest.mark.gpu
+def test_frequencies_above_one_at_far_positions():
+    """The angle's fraction of a turn by whole numbers, from 2 pi to 60 digits: off by 2^-24 of a turn at most, sine and
+    cosine by 2^-22 more."""
+    import math
+    from decimal import Decimal, getcontext
+
+    import gated_delta_rule_14_gb300 as kla
+    getcontext().prec = 70
+    two_pi = Decimal("6.28318530717958647692528676655900576839433879875021164194989")
+    freqs = torch.tensor([4.0, 3.9375, 2.7182817459106445, 1.0, 0.3333333432674408], device=DEV)
+    at = torch.tensor([[2**28, 2**28 - 1, 123456789, 5, -(2**28)]], device=DEV)
+    x = torch.zeros(1, 5, 1, 10, device=DEV)
+    x[..., :5] = 1.0
+    y = kla.rotary_fwd(x, None, freqs, at)[0][0, :, 0].double().cpu()
+    kla.device_status(DEV)
+    tol = 2 * math.pi * 2.0**-24 + 2.0**-22
+    for t, p in enumerate(at[0].tolist()):
+        for i, f in enumerate(freqs.tolist()):
+            turn = Decimal(f) * p / two_pi
+            angle = float((turn - turn.to_integral_value()) * two_pi)
+            assert abs(float(y[t, i]) - math.cos(angle)) <= tol and abs(float(y[t, 5 + i]) - math.sin(angle)) <= tol
