@@ -112,6 +112,8 @@ def _declare(lib):
     lib.kla_selftest_team_timeout.restype = ctypes.c_int
     lib.kla_selftest_warp_timeout.argtypes = [ctypes.c_uint, vp, vp]
     lib.kla_selftest_warp_timeout.restype = ctypes.c_int
+    lib.kla_selftest_scan_timeout.argtypes = [ctypes.c_uint, i, vp, fp, vp, vp, i, i, i, i, vp, sz, vp]
+    lib.kla_selftest_scan_timeout.restype = ctypes.c_int
     lib.kla_device_status.argtypes = [vp]
     lib.kla_device_status.restype = ctypes.c_int
     lib.kla_status_string.argtypes = [ctypes.c_int]

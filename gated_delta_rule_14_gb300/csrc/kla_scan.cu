@@ -49,6 +49,7 @@ struct ScanArgs {
     struct Head *head;                // of the workspace; NULL with one tile along the tokens
     uint2 *carry;                     // [B][tiles][C]
     unsigned *err;
+    unsigned first, polls;            // the first ticket given out, and how often a tile asks for the state that enters it
 };
 // The workspace: this, then what tiles tell each other. All bits set before the kernel starts.
 struct Head {
@@ -203,13 +204,13 @@ __device__ __forceinline__ void hear(const uint2 *p, int count, uint2 (&v)[kV]) 
 // themselves: whatever is known when, the bits are the same. The chain's first tile tells kWhole at once. Tiles are
 // taken by ticket in the order of the chain, so that all of those are running or done and none of them waits for a
 // later one: the wait ends. Its limit is for what cannot be foreseen. Run by a whole warp; false where it gave up.
+constexpr unsigned kPolls = 1u << 21;   // a second or two
 template <int kV, bool kPairs, int kAhead>
 __device__ __forceinline__ bool hear_state(const uint2 *p, int64_t hop, int left, int count, const Head *head,
-                                         float (&h)[kV]) {
-    constexpr unsigned kLimit = 1u << 21;
+                                         unsigned limit, float (&h)[kV]) {
 #pragma unroll
     for (int v = 0; v < kV; ++v) h[v] = 0.f;
-    for (unsigned polls = 0; polls < kLimit; ++polls) {
+    for (unsigned polls = 0; polls < limit; ++polls) {
         uint2 w[kAhead][kV];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) hear<kV, kPairs>(p + j * hop, j < left ? count : 0, w[j]);
@@ -252,8 +253,8 @@ template <int kV, bool kPairs, int kFar>
 __device__ __forceinline__ bool entering(const ScanArgs &p, const uint2 *from, int64_t hop, int left, int count,
                                          float (&h)[kV]) {
     constexpr int kFew = 16;
-    if (kFar > 4 && p.B * p.blocks <= kFew) return hear_state<kV, kPairs, kFar>(from, hop, left, count, p.head, h);
-    return hear_state<kV, kPairs, 4>(from, hop, left, count, p.head, h);
+    if (kFar > 4 && p.B * p.blocks <= kFew) return hear_state<kV, kPairs, kFar>(from, hop, left, count, p.head, p.polls, h);
+    return hear_state<kV, kPairs, 4>(from, hop, left, count, p.head, p.polls, h);
 }
 
 // The tile of a ticket: `at` tiles along the chain, of channels c0 ..
@@ -1235,11 +1236,12 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kCtas) scan_bwd_ring_kernel
     }
 }
 
-// A workspace that says nothing yet. A kernel of the library, that the scan's CTAs may be set up while it runs.
-__global__ void __launch_bounds__(256) clear_kernel(uint4 *p, size_t words) {
+// A workspace that says nothing yet, with the ticket before the first. A kernel of the library, that the scan's CTAs may be
+// set up while it runs.
+__global__ void __launch_bounds__(256) clear_kernel(uint4 *p, size_t words, unsigned first) {
     dependency_release();
     for (size_t i = blockIdx.x * 256 + threadIdx.x; i < words; i += gridDim.x * 256)
-        p[i] = make_uint4(kEmpty, kEmpty, kEmpty, kEmpty);
+        p[i] = make_uint4(i == 0 ? first - 1u : kEmpty, kEmpty, kEmpty, kEmpty);
 }
 
 template <typename T, bool kLog>
@@ -1296,10 +1298,12 @@ cudaError_t lay_out(ScanArgs &p, int tile, int width, void *workspace, cudaStrea
     p.head = static_cast<Head *>(workspace);
     p.carry = reinterpret_cast<uint2 *>(p.head + 1);
     const size_t words = carry_bytes(p.B, p.T, p.C, tile) / sizeof(uint4), ctas = (words + 1023) / 1024;
-    clear_kernel<<<static_cast<unsigned>(ctas < 608 ? ctas : 608), 256, 0, s>>>(static_cast<uint4 *>(workspace), words);
+    clear_kernel<<<static_cast<unsigned>(ctas < 608 ? ctas : 608), 256, 0, s>>>(static_cast<uint4 *>(workspace), words, p.first);
     return cudaGetLastError();
 }
 unsigned tiles_in_all(const ScanArgs &p) { return static_cast<unsigned>(p.B) * p.blocks * p.tiles; }
+// CTAs of a kernel that takes one ticket each
+unsigned tickets(const ScanArgs &p) { return tiles_in_all(p) - (p.head ? p.first : 0); }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                    const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
@@ -1368,22 +1372,28 @@ cudaError_t by_type(kla_dtype dtype, kla_scan_mode mode, F f) {
     return mode == KLA_SCAN_LOG ? f(float{}, std::true_type{}) : f(float{}, std::false_type{});
 }
 
+// What the self-test sets otherwise: a first ticket of 1 leaves out the tile that all others of its chain wait for.
+struct Trial {
+    unsigned first, polls;
+};
+constexpr Trial kInEarnest{0, kPolls};
+
 }  // namespace
 }  // namespace kla
 
-extern "C" {
-
-size_t kla_gated_scan_workspace_size(int B, int T, int C, kla_dtype dtype) {
+extern "C" size_t kla_gated_scan_workspace_size(int B, int T, int C, kla_dtype dtype) {
     using namespace kla;
     if (check(B, T, C, dtype, KLA_SCAN_SIGMOID) != KLA_OK) return 0;
     return carry_bytes(B, T, C, KLA_SCAN_SPAN);   // no kernel has a shorter tile
 }
 
-kla_status kla_gated_scan_fwd(const void *x, const void *gate, const int64_t *strides, const int *lengths,
+namespace kla {
+namespace {
+
+kla_status scan_fwd(const void *x, const void *gate, const int64_t *strides, const int *lengths,
                               const float *h0, void *y, float *h_T, float *states, int B, int T, int C,
                               kla_dtype dtype, kla_scan_mode mode, void *workspace, size_t workspace_bytes,
-                              void *stream) {
-    using namespace kla;
+                              void *stream, Trial trial) {
     const kla_status st = check(B, T, C, dtype, mode);
     if (st != KLA_OK) return st;
     if (T > 0 && (!x || !gate || !y)) return KLA_ERR_INVALID_ARG;
@@ -1393,7 +1403,7 @@ kla_status kla_gated_scan_fwd(const void *x, const void *gate, const int64_t *st
         return KLA_ERR_INVALID_ARG;
     const int64_t tc = static_cast<int64_t>(T) * C;
     ScanArgs p{x, gate, nullptr, tc, C, tc, C, 0, 0, lengths, h0, y, nullptr, h_T, states, B, T, C,
-               0, 0, nullptr, nullptr, nullptr};
+               0, 0, nullptr, nullptr, nullptr, trial.first, trial.polls};
     if (strides) {
         for (int i = 0; i < 4; ++i)
             if (strides[i] < 0) return KLA_ERR_INVALID_ARG;
@@ -1433,18 +1443,17 @@ kla_status kla_gated_scan_fwd(const void *x, const void *gate, const int64_t *st
             if (ring)
                 return run_ring<3, r.ctas, scan_fwd_ring_kernel<E, kLog, kOdd, r.tok, r.warps, r.ctas>>(
                     p, false, maps, kOddRow, r.tile(), 32 * r.warps, cs);
-            scan_fwd_kernel<E, kLog, o.tok, o.warps><<<tiles_in_all(p), 32 * o.warps, 0, cs>>>(p);
+            scan_fwd_kernel<E, kLog, o.tok, o.warps><<<tickets(p), 32 * o.warps, 0, cs>>>(p);
         }
         return cudaGetLastError();
     });
     return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
 }
 
-kla_status kla_gated_scan_bwd(const void *x, const void *gate, const void *dy, const int64_t *strides,
+kla_status scan_bwd(const void *x, const void *gate, const void *dy, const int64_t *strides,
                               const int *lengths, const float *states, const float *dh_T, void *dx, void *dgate,
                               float *dh0, int B, int T, int C, kla_dtype dtype, kla_scan_mode mode, void *workspace,
-                              size_t workspace_bytes, void *stream) {
-    using namespace kla;
+                              size_t workspace_bytes, void *stream, Trial trial) {
     const kla_status st = check(B, T, C, dtype, mode);
     if (st != KLA_OK) return st;
     if (T > 0 && (!x || !gate || !dy || !dx || !dgate || !states)) return KLA_ERR_INVALID_ARG;
@@ -1455,7 +1464,7 @@ kla_status kla_gated_scan_bwd(const void *x, const void *gate, const void *dy, c
         return KLA_ERR_INVALID_ARG;
     const int64_t tc = static_cast<int64_t>(T) * C;
     ScanArgs p{x, gate, dy, tc, C, tc, C, tc, C, lengths, dh_T, dx, dgate, dh0, const_cast<float *>(states), B, T, C,
-               0, 0, nullptr, nullptr, nullptr};
+               0, 0, nullptr, nullptr, nullptr, trial.first, trial.polls};
     if (strides) {
         for (int i = 0; i < 6; ++i)
             if (strides[i] < 0) return KLA_ERR_INVALID_ARG;
@@ -1496,11 +1505,48 @@ kla_status kla_gated_scan_bwd(const void *x, const void *gate, const void *dy, c
             if (ring)
                 return run_ring<5, r.ctas, scan_bwd_ring_kernel<E, kLog, kOdd, r.tok, r.warps, r.ctas>>(
                     p, false, maps, kOddRow, r.tile(), 32 * (r.warps + 1), cs);
-            scan_bwd_kernel<E, kLog, o.tok, o.warps><<<tiles_in_all(p), 32 * o.warps, 0, cs>>>(p);
+            scan_bwd_kernel<E, kLog, o.tok, o.warps><<<tickets(p), 32 * o.warps, 0, cs>>>(p);
         }
         return cudaGetLastError();
     });
     return e == cudaSuccess ? KLA_OK : KLA_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace kla
+
+extern "C" {
+
+kla_status kla_gated_scan_fwd(const void *x, const void *gate, const int64_t *strides, const int *lengths,
+                              const float *h0, void *y, float *h_T, float *states, int B, int T, int C,
+                              kla_dtype dtype, kla_scan_mode mode, void *workspace, size_t workspace_bytes,
+                              void *stream) {
+    return kla::scan_fwd(x, gate, strides, lengths, h0, y, h_T, states, B, T, C, dtype, mode, workspace,
+                         workspace_bytes, stream, kla::kInEarnest);
+}
+
+kla_status kla_gated_scan_bwd(const void *x, const void *gate, const void *dy, const int64_t *strides,
+                              const int *lengths, const float *states, const float *dh_T, void *dx, void *dgate,
+                              float *dh0, int B, int T, int C, kla_dtype dtype, kla_scan_mode mode, void *workspace,
+                              size_t workspace_bytes, void *stream) {
+    return kla::scan_bwd(x, gate, dy, strides, lengths, states, dh_T, dx, dgate, dh0, B, T, C, dtype, mode, workspace,
+                         workspace_bytes, stream, kla::kInEarnest);
+}
+
+kla_status kla_selftest_scan_timeout(unsigned limit_polls, int backward, const void *x, float *states, void *out,
+                                     void *out2, int B, int T, int C, kla_dtype dtype, void *workspace,
+                                     size_t workspace_bytes, void *stream) {
+    using namespace kla;
+    if (limit_polls < 1 || limit_polls > kPolls) return KLA_ERR_INVALID_ARG;
+    const kla_status st = check(B, T, C, dtype, KLA_SCAN_SIGMOID);
+    if (st != KLA_OK) return st;
+    if (tiles_of(T, fwd_shape(2, true).tile()) < 2) return KLA_ERR_INVALID_ARG;   // nothing would wait
+    const Trial trial{1, limit_polls};
+    if (backward)
+        return scan_bwd(x, x, x, nullptr, nullptr, states, nullptr, out, out2, nullptr, B, T, C, dtype,
+                        KLA_SCAN_SIGMOID, workspace, workspace_bytes, stream, trial);
+    return scan_fwd(x, x, nullptr, nullptr, nullptr, out, nullptr, states, B, T, C, dtype, KLA_SCAN_SIGMOID, workspace,
+                    workspace_bytes, stream, trial);
 }
 
 kla_status kla_gated_scan_step(const void *x, int64_t x_stride, const void *gate, int64_t gate_stride, float *h,

@@ -86,6 +86,19 @@ kla_status kla_gated_scan_bwd(const void *x, const void *gate, const void *dy, c
 kla_status kla_gated_scan_step(const void *x, int64_t x_stride, const void *gate, int64_t gate_stride, float *h,
                                void *y, int B, int C, kla_dtype dtype, kla_scan_mode mode, void *stream);
 
+/*
+ * Self-test of the scan's bounded waits, as kla_selftest_wait_timeout of kla.h: kla_gated_scan_fwd, or
+ * with `backward` kla_gated_scan_bwd, in KLA_SCAN_SIGMOID with x as the gate (and as dy), of which the
+ * first sequence's first tile (backward: its last) of the first channels is left out, so that the tiles
+ * that it would tell its state wait for nothing. After `limit_polls` questions (1 .. 2^21, the calls'
+ * own limit, a second or two) they give up, which calls every other wait of the call off; all outputs
+ * are undefined then. The next kla_device_status() returns KLA_ERR_TIMEOUT.
+ *   out, out2   y (out2 unused), or dx and dgate;  T > 256;  the rest as the calls have it
+ */
+kla_status kla_selftest_scan_timeout(unsigned limit_polls, int backward, const void *x, float *states, void *out,
+                                     void *out2, int B, int T, int C, kla_dtype dtype, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+
 /* ------------------------------------------------------------------------------------- rotary
  *
  * The first `rot` of the d values of every head are turned by their token's position: pair i of
