@@ -376,9 +376,11 @@ cudaError_t run(const RotaryArgs &p, int B, bool half, cudaStream_t s) {
     auto fits = [&](int v) { return p.rot / 2 % v == 0 && (p.d - p.rot) % v == 0 && starts(v); };
     if (fits(kFull)) return run<T, kFull>(p, half, s);
     if (sizeof(T) == 2 && fits(4)) return run<T, sizeof(T) == 2 ? 4 : 1>(p, half, s);
-    // through shared memory but where accesses of 4 bytes fit heads of less than 128: 8 x 4096 x 32 heads took 97 us
-    // instead of 154 of 80 bf16 with 20 turned, 52 instead of 31 of 16 with 4; of single values 132 instead of 222 (126 of 128)
-    if (p.rot > 0 && p.d % kFull == 0 && starts(kFull) && !(sizeof(T) == 2 && fits(2) && p.d < 64))
+    // through shared memory, but where accesses of 4 bytes fit heads of less than 48 bf16: 8 x 4096 x 32 heads took, by those
+    // and through shared memory, 29 and 49 us of 16 values with 4 or 12 turned, 38 and 54 of 32, 54 and 60 of 40, 74 and 62
+    // of 48 (12 or 44), 75 and 64 of 56, 75 and 66 of 64, 152 and 95 of 80 (pairs "interleaved": 2 to 6 us less, in the same
+    // order); of single values 222 and 132 (126 of 128)
+    if (p.rot > 0 && p.d % kFull == 0 && starts(kFull) && !(sizeof(T) == 2 && fits(2) && p.d < 48))
         return run_rows<T>(p, half, s);
     if (sizeof(T) == 2 && fits(2)) return run<T, sizeof(T) == 2 ? 2 : 1>(p, half, s);
     return run<T, 1>(p, half, s);

@@ -80,3 +80,28 @@ def test_frequencies_above_one_at_far_positions():
             turn = Decimal(f) * p / two_pi
             angle = float((turn - turn.to_integral_value()) * two_pi)
             assert abs(float(y[t, i]) - math.cos(angle)) <= tol and abs(float(y[t, 5 + i]) - math.sin(angle)) <= tol
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,rot", [(40, 36), (48, 12), (48, 44), (56, 28), (56, 4), (64, 60)])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_heads_on_either_side_of_4_byte_accesses(d, rot, layout, dtype):
+    """A stored bf16 is off by 2^-8 of itself at most, and sine and cosine by 2^-20 of the pair; fp32 by 2^-21 in all."""
+    import gated_delta_rule_14_gb300 as kla
+    gen = torch.Generator(device=DEV).manual_seed(d + rot)
+    freqs, _ = kla.rotary_freqs(rot, device=DEV)
+    for B, T, H, K in ((2, 3, 5, 1), (3, 701, 9, 3)):
+        q, k = (torch.randn((B, T, h, d), generator=gen, device=DEV).to(dtype) for h in (H, K))
+        got = kla.rotary_fwd(q, k, freqs, layout=layout)
+        t = (torch.arange(T, device=DEV).double()[:, None] * freqs.double())[:, None]
+        for x, y in zip((q, k), got):
+            z = x.double()[..., :rot]
+            u, v = (z[..., :rot // 2], z[..., rot // 2:]) if layout == "half" else (z[..., ::2], z[..., 1::2])
+            new = (u * t.cos() - v * t.sin(), v * t.cos() + u * t.sin())
+            new = torch.cat(new, -1) if layout == "half" else torch.stack(new, -1).flatten(-2)
+            size = (u.square() + v.square()).sqrt()
+            size = torch.cat([size, size], -1) if layout == "half" else torch.stack([size, size], -1).flatten(-2)
+            tol = new.abs() * 2.0**-8 + size * 2.0**-19 if dtype == torch.bfloat16 else size * 2.0**-21
+            assert bool(((y.double()[..., :rot] - new).abs() <= tol).all()) and torch.equal(y[..., rot:], x[..., rot:])
+    kla.device_status(DEV)
