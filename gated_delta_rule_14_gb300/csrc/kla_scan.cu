@@ -665,11 +665,11 @@ __device__ __forceinline__ auto whole(const float (&v)[kV]) {
 // A lane's product of m factors, once more where it is close to 1. Few lanes need it: its loop unrolled, and with its
 // registers, costs the others 2 % of the backward pass.
 template <typename T, bool kLog, typename V, typename F>
-__device__ __forceinline__ V kept_product(V A, int m, F gate) {
+__device__ __forceinline__ V kept_product(V A, int count, int m, F gate) {
     constexpr int kV = sizeof(V) / sizeof(float);
     bool any = false;
 #pragma unroll
-    for (int v = 0; v < kV; ++v) any |= keeps(part(A, v), m);
+    for (int v = 0; v < kV; ++v) any |= v < count && keeps(part(A, v), m);   // past the last channel there is anything
     if (any) {
         float lost[kV] = {}, a[kV];
 #pragma unroll 1
@@ -929,7 +929,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) scan_fwd_ring_kernel(ScanA
         by_case<L, L>(m == kTok, false, map_tokens);
         const bool exact = most.any(count, m, [&](int i) { return of_g.template load<L>(gs + i * kRow, i); });
         if (exact) map_tokens(std::false_type{}, X{});
-        A = kept_product<T, kLog>(A, m, [&](int i) { return of_g.template load<L>(gs + i * kRow, i); });
+        A = kept_product<T, kLog>(A, count, m, [&](int i) { return of_g.template load<L>(gs + i * kRow, i); });
         __syncwarp();
         map_a[warp][lane] = A;
         map_h[warp][lane] = H;
@@ -1173,7 +1173,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kCtas) scan_bwd_ring_kernel
         by_case<L, L>(m == kTok, false, map_tokens);
         const bool exact = most.any(count, m, [&](int i) { return of_g.template load<L>(gs + i * kRow, i); });
         if (exact) map_tokens(std::false_type{}, X{});
-        A = kept_product<T, kLog>(A, m, [&](int i) { return of_g.template load<L>(gs + i * kRow, i); });
+        A = kept_product<T, kLog>(A, count, m, [&](int i) { return of_g.template load<L>(gs + i * kRow, i); });
         __syncwarp();
         watch<kLog>(p, count, A);
         sh.a[turn & 1][warp][lane] = A;
