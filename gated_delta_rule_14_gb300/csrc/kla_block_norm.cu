@@ -8,12 +8,14 @@
 // What bounds them is the memory: 3 and 5 elements a value for the gated norm, 4 and 6 for the residual's (5 where it is
 // not scaled). Backward, the residual's sum is formed again from x and the residual: read back as it was rounded to bf16
 // it would leave 9 bits of dw.
-// Measured, bf16: 32768 x 16 heads of 128 gated forward 74 us (5.4 TB/s, 80 % of a copy's rate), backward with dw 119 us
-// (5.6 TB/s); 16397 x 2048 residual forward 50 us (5.4 TB/s), backward with dw and dl 79 us (5.1 TB/s); in fp32 91 and
-// 141 us (5.9 and 5.7 TB/s). By the counters (16384 rows of the same) 39 to 60 instructions a value backward and forward at
-// 1.7 to 2.3 of 4 a cycle with 16 warps an SM: arithmetic and memory each fill about two thirds of the time. Rows of 100 to
-// 300 values fill their teams by three quarters: 65536 x 3 heads of 100 bf16 52 and 76 us (2.3 and 2.6 TB/s). CTAs that add
-// up row by row with barriers and read twice took 3650 us for the first, 709 for the second.
+// Measured, bf16: 32768 x 16 heads of 128 gated forward 72 us (5.6 TB/s, 82 % of a copy's rate), backward with dw 122 us
+// (5.5 TB/s), in fp32 146 and 221 us (5.5 and 6.1 TB/s); 16397 x 2048 residual forward 50 us (5.4 TB/s), backward with dw
+// and dl 75 us (5.4 TB/s), in fp32 92 and 141 us (5.8 and 5.7 TB/s). By the counters (16384 rows of the same) 19 to 20
+// instructions a value forward and 31 to 33 backward at 2.0 to 2.7 of 4 a cycle with 16 warps an SM: arithmetic and memory
+// each fill about two thirds of the time. Rows of 100 to 300 values fill their teams by three quarters, and a team has one
+// short row at hand, whose sums, addresses and loop are spread over few values: 65536 x 3 heads of 100 bf16 49 and 75 us
+// (2.4 and 2.6 TB/s). CTAs that add up row by row with barriers and read twice took 3650 us for the first, 709 for the
+// second.
 #include <atomic>
 #include <cfloat>
 #include <climits>
@@ -444,8 +446,10 @@ block_norm_kernel(NormArgs p, int width) {
     }
 }
 
-// ---- any other row, of any length and alignment: a CTA takes rows one after the other and reads each from memory and
-// then from L1 or L2
+// ---- any other row, of any length and alignment: bf16 above 8192 values, fp32 above 8192 (4096 where rows fit no 16 bytes: by
+// single loads above, without a ring). A CTA takes rows one after the other, value by value, and reads each twice, three
+// times with a mean; backward twice, and a third time for dw and dl. From memory and then from L1 or L2: 8192 x 12288 bf16
+// gated 450 and 712 us, residual 273 and 1274, where the bytes of one pass take 89, 148, 119 and 178.
 constexpr int kAnyBlock = 512;
 template <typename V>
 __device__ __forceinline__ V block_sum(V v, float2 *slots) {

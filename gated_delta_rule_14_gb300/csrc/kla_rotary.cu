@@ -6,7 +6,8 @@
 // would cost tens of instructions of a pipe that does two a cycle and SM.
 // What bounds it is the memory, one read and one write of every value. Measured: 8 x 4096 tokens of 32 heads of 128
 // bf16, slices of one projection, 88 us in a row of calls (6.1 TB/s, 90 % of a copy's rate), 93 after other work; 40 heads
-// in fp32 214 us (6.3 TB/s); 126 of 128 values turned, whose pairs fit no wide accesses, 132 us.
+// in fp32 212 us (6.3 TB/s). Of heads whose pairs fit no wide accesses single values in shared memory bound it: 126 of 128
+// values turned 130 us, 20 of 80 95 (floors 79 and 49); in fp32 179 and 114 (158 and 99).
 #include <type_traits>
 
 #include "layer_dev.cuh"

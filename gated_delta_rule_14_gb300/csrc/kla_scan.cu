@@ -7,7 +7,7 @@
 // In fp32 the sigmoid's recurrence is taken as h + w (x - h) where w is the smaller of the two factors, as x + a (h - x)
 // where a is: where a gate keeps its state for thousands of tokens a is within 2^-11 of 1 and its rounding to 24 bits
 // would leave 12 of w, and where one drops a large state nothing of it may stay behind as a difference of roundings.
-// In bf16 as a h + w x with a = 1 - w in paired arithmetic, whose rounding of 2^-23 is far below the values' own 2^-9 as
+// In bf16 as a h + w x with a = 1 - w in paired arithmetic, whose rounding of 2^-23 is far below the values' own 2^-8 as
 // long as a is not small; a warp with gates below -5 takes its tokens as in fp32 (`Exact`), as a gate that forgets leaves
 // nothing but a of the state, and of the gradient.
 //
@@ -16,13 +16,14 @@
 // tell each other through the workspace, in one pass; a pass for the tiles' maps and one for the outputs would move 10
 // bytes forward. Backward, the states are walked again from one kept every 128 tokens (0.03 bytes a value), which is
 // exact and cheaper than reading the outputs back.
-// Measured: 131072 x 2048 forward 275 us (5.9 TB/s, 86 % of a copy's rate), backward 484 us (5.5 TB/s); 8 x
-// 4096 x 2048 forward 72 us (5.6 TB/s), backward 105 us (6.4 TB/s); in fp32 8 x 2048 x 2048 85 and 128 us. Where channels
-// are few the chain of tiles is what is waited for, four or eight of them a trip to L2, 0.7 us: 131072 x 512 111 and 232 us,
-// 131072 x 64 72 and 154. A thread per channel that walks all tokens took 120 ms for the first. By the counters
-// (8 x 2048 x 2048) 18 instructions a value forward and 30 backward, both at 2.0 of 4 a cycle; warps wait for the chain
-// (forward) and for tiles on their way: registers hold 16 warps an SM, whose tiles and those that follow are what is under
-// way at once.
+// Measured, calls in a row: 131072 x 2048 forward 277 us (5.8 TB/s, 86 % of a copy's rate), backward 513 us (5.2 TB/s); 8 x
+// 4096 x 2048 forward 67 us (6.0 TB/s), backward 110 us (6.1 TB/s); in fp32 8 x 2048 x 2048 81 us (5.0 TB/s) and 129 us
+// (5.2 TB/s), log gates 65 and 104. Where channels are few the chain of tiles is what is waited for, four or eight of them a
+// trip to L2, 0.7 us: 131072 x 512 111 and 234 us, 131072 x 64 67 and 149. A thread per channel that walks all tokens took
+// 120 ms for the first. By the counters (8 x 2048 x 2048 bf16) 19 instructions a value forward and 31 backward, both at 2.0
+// of 4 a cycle; warps wait for the chain (forward) and for tiles on their way: registers hold 16 warps an SM, whose tiles
+// and those that follow are what is under way at once. In fp32, with its own exponential and reciprocal and a channel a
+// lane, they are 56 and 90 a value, at 2.5 and 2.4 a cycle: these bound it, at 73 and 77 % of the memory's time.
 #include <cuda.h>
 
 #include <atomic>

@@ -6,9 +6,10 @@
 // of floats, so 16 weights at a time are added as pairs of floats, a sum and what it has lost, and only those join as
 // doubles. What 16 weights of sum S lose is 16 x 2^-24 S at most, each addition to it rounds by 2^-24 of that, and 16
 // of them make 2^-40 S.
-// Measured: 64 sequences of 8 drafts, 100003 tokens fp32, 25 us in a row of calls (floor 7.5); one of 4 drafts, 32000
-// tokens, 9.6 us on the GPU, which is a chain of trips: lengths and drafts, their probabilities, the rows, the sums across the
-// cluster, the piece, the walk. With all sums in doubles, and every thread adding up all stretches, 156 and 62 us.
+// Measured: 64 sequences of 8 drafts, 100003 tokens fp32, 25 us in a row of calls (floor 7.5), bf16 25 (3.8), 100000 tokens,
+// whose rows fit 16 bytes, 23 either way; one of 4 drafts, 32000 tokens, 9.8 us on the GPU, bf16 13.9, which is a chain of
+// trips: lengths and drafts, their probabilities, the rows, the sums across the cluster, the piece, the walk. Odd rows of a
+// large vocabulary are single loads, a batch of which is asked for when the last one has been added up. With all sums in doubles, and every thread adding up all stretches, 156 and 62 us.
 #include <cfloat>
 
 #include "layer_dev.cuh"
