@@ -154,15 +154,15 @@ __device__ __forceinline__ void tell_state(uint2 *p, int count, const float (&h)
     for (int v = 0; v < kV; ++v) w[v] = make_uint2(kWhole, __float_as_uint(h[v]));
     tell<kV, kPairs>(p, count, w);
 }
-// Gates that grow: a product of factors that fp32 does not hold makes a NaN of a state of zero, and is reported. `a` is
-// the product of a channel's neighbouring tokens.
+// Gates that grow: a product of factors that fp32 does not hold makes a NaN of a state of zero, and is reported; one that has
+// become a NaN by a factor of zero, too. `a` is the product of a channel's neighbouring tokens.
 template <bool kLog>
 __device__ __forceinline__ void watch(const ScanArgs &p, bool live, float a) {
-    if (kLog && live && a > FLT_MAX) atomicOr(p.err, kErrGateRange);
+    if (kLog && live && !(a <= FLT_MAX)) atomicOr(p.err, kErrGateRange);
 }
 template <bool kLog>
 __device__ __forceinline__ void watch(const ScanArgs &p, int count, float2 a) {
-    watch<kLog>(p, (count > 0 && a.x > FLT_MAX) || (count > 1 && a.y > FLT_MAX), fmaxf(a.x, a.y));
+    if (kLog && ((count > 0 && !(a.x <= FLT_MAX)) || (count > 1 && !(a.y <= FLT_MAX)))) atomicOr(p.err, kErrGateRange);
 }
 // The state at the chain's start (zeros where none is given), and at its end where that is wanted.
 template <int kV>
@@ -199,13 +199,14 @@ __device__ __forceinline__ void hear(const uint2 *p, int count, uint2 (&v)[kV]) 
     for (int i = 0; i < kV; ++i) v[i] = make_uint2(static_cast<unsigned>(w[i]), static_cast<unsigned>(w[i] >> 32));
 }
 
+constexpr unsigned kPolls = 1u << 21;   // of the wait of below: a second or two
+
 // The state that enters a tile, from what the `left` tiles before it told: `p` is the nearest one's word of this
 // thread's first channel, `hop` leads to the next further one. Of the nearest kAhead tiles one has to know the state
 // that leaves it, and the maps of those in between are applied to that in their order, as they apply them
 // themselves: whatever is known when, the bits are the same. The chain's first tile tells kWhole at once. Tiles are
 // taken by ticket in the order of the chain, so that all of those are running or done and none of them waits for a
 // later one: the wait ends. Its limit is for what cannot be foreseen. Run by a whole warp; false where it gave up.
-constexpr unsigned kPolls = 1u << 21;   // a second or two
 template <int kV, bool kPairs, int kAhead>
 __device__ __forceinline__ bool hear_state(const uint2 *p, int64_t hop, int left, int count, const Head *head,
                                          unsigned limit, float (&h)[kV]) {

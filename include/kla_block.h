@@ -32,8 +32,9 @@ extern "C" {
  *     KLA_SCAN_LOG       h_t = a_t h_{t-1} + x_t,             a_t = exp(gate_t)
  *
  * A gate is at most 0 in KLA_SCAN_LOG, as a decay's is. Larger ones are taken as they are as long as fp32 holds the
- * products of neighbouring a_t, of 256 tokens at most; where one passes that range, states may be NaN that are not, and
- * kla_device_status reports KLA_ERR_INVALID_ARG.
+ * products of neighbouring a_t, of 256 tokens at most; where one that is formed passes that range, states may be NaN that
+ * are not, and kla_device_status reports KLA_ERR_INVALID_ARG, of this call as of kla_gated_scan_bwd (and of gates that are
+ * NaN). Which products are formed is not said: what is not reported is as the definition has it.
  *
  * y_t = h_t, for t = 0 .. n_b - 1, where n_b = lengths[b] (T when lengths is NULL). Tokens
  * t >= n_b are masked: whatever x and gate hold there (NaN included) they leave the state as it is,

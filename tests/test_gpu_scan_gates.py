@@ -203,3 +203,33 @@ def test_states_that_are_not_finite(B, C, shift, dtype, mode):
     assert not h_T[:, 5:8].isfinite().any() and torch.equal(y[:, :270, 6], clean[0][:, :270, 6].float())
     rest = [c for c in range(C) if c not in (5, 6, 7)]
     assert all(torch.equal(a[..., rest], b[..., rest]) for a, b in zip(got, clean))
+
+
+@pytest.mark.parametrize("B,C,shift,dtype", TYPED)
+def test_products_that_a_gate_of_minus_infinity_follows_are_reported(B, C, shift, dtype):
+    """An infinite product times zero is a NaN, not a state forgotten. In one stretch of tokens (e^180) it is there whatever
+    the stretches are. Across them, e^110 of tokens 10 to 119, it depends on them: with 32 tokens a stretch the products up
+    to token 95 are e^86, which fp32 holds, and that of the next one is zero, as the -inf is in it; so either the call is
+    reported, or all is as the definition has it, zero."""
+    import gated_delta_rule_14_gb300 as kla
+    T = 600
+    x = place(torch.zeros(B, T, C, dtype=dtype, device=DEV), shift)
+    states = torch.zeros(B, -(-T // 128), C, device=DEV)
+    for grow, drop in ((slice(0, 2), 3), (slice(10, 120), 125)):   # e^180 in one stretch, e^110 over several
+        gate = torch.full((B, T, C), -0.5, device=DEV)
+        gate[:, grow] = 90.0 if drop == 3 else 1.0
+        gate[:, drop] = -float("inf")
+        gate = place(gate.to(dtype), shift)
+        kla.device_status(DEV)
+        for call in (lambda: kla.gated_scan_fwd(x, gate, mode="log")[:2],
+                     lambda: kla.gated_scan_bwd(x, gate, x, states, mode="log").values()):
+            out = list(call())
+            try:
+                kla.device_status(DEV)
+                assert drop != 3 and all(float(t.abs().max()) == 0.0 for t in out)
+            except kla.KlaError:
+                pass
+    n = torch.zeros(B, dtype=torch.int32, device=DEV)   # masked, they are nobody's
+    kla.gated_scan_fwd(x, gate, mode="log", lengths=n)
+    kla.gated_scan_bwd(x, gate, x, states, mode="log", lengths=n)
+    kla.device_status(DEV)
