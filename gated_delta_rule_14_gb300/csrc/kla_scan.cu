@@ -8,7 +8,7 @@
 // where a is: where a gate keeps its state for thousands of tokens a is within 2^-11 of 1 and its rounding to 24 bits
 // would leave 12 of w, and where one drops a large state nothing of it may stay behind as a difference of roundings.
 // In bf16 as a h + w x with a = 1 - w in paired arithmetic, whose rounding of 2^-23 is far below the values' own 2^-8 as
-// long as a is not small; a warp with gates below -5 takes its tokens as in fp32 (`Exact`), as a gate that forgets leaves
+// long as a is not small; a warp with gates below -6 takes its tokens as in fp32 (`Exact`), as a gate that forgets leaves
 // nothing but a of the state, and of the gradient.
 //
 // Every value is read once: 6 bytes a value forward and 10 backward in bf16, which at a copy's rate is 237 us for a
@@ -695,18 +695,19 @@ struct Most {
     __device__ __forceinline__ void see(V k) {
         if (kAsks) w = fmaxf(fmaxf(w, part(k, 0)), part(k, 1));
     }
-    // Whether the warp's tokens are Exact's: of any lane a gate below -5 among its `count` channels. There 1 - w is off by
-    // 2^-23, 2^-16 of a. In other channels there may be anything: where there is one, the gates are looked at once more.
+    // Whether the warp's tokens are Exact's: of any lane a gate below -6 among its `count` channels. There 1 - w is off by
+    // 2^-23, 2^-14 of a (from -5 on, gates of N(0, 1) have one such in 2000 warps, and 8 x 4096 x 2048 took 70 us, not 67).
+    // In other channels there may be anything: where there is one, the gates are looked at once more.
     // A warp as a whole, as lanes that go apart cost the others more: 8 x 4096 x 2048 66.7 and 109.1 us without Exact, 67.1
     // and 109.6 with it, 118.8 and 177 where all warps take it; lane by lane 66.7 and 113.6.
     template <typename F>
     __device__ __forceinline__ bool any(int count, int m, F gate) const {
         if (!kAsks) return false;
-        bool here = count > 0 && w > 0.9933071f;   // sigmoid(5)
+        bool here = count > 0 && w > 0.9975274f;   // sigmoid(6)
         if (here && count == 1) {
             here = false;
 #pragma unroll 1
-            for (int i = 0; i < m; ++i) here |= part(gate(i), 0) < -5.f;
+            for (int i = 0; i < m; ++i) here |= part(gate(i), 0) < -6.f;
         }
         return __any_sync(0xffffffffu, here);
     }

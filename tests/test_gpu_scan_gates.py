@@ -62,7 +62,8 @@ def test_gates_that_forget(B, C, shift):
     """bf16, sigmoid: three tokens with gates of -3 to -20 among such as keep, x of zero, so that all that there is of
     a state and of dgate is what these leave. 600 steps of the state at 2^-24 for each product and its factor, 7e-5; at a
     forgetting token the exponent's rounding, 29 x 2^-24, the exponential's 2^-22 and the reciprocal's 2^-23, or where a is
-    still 1 - w 2^-23 / sigmoid(-5) = 1.8e-5: 6e-5 for three. dgate has two such states: 2.6e-4."""
+    still 1 - w 2^-23 / sigmoid(-6) = 4.8e-5: 6e-5 for three, or 1.5e-4 where all three are just above -6. dgate has a state
+    and a gradient, which three such tokens and the 600 steps are shared out between, and its own factor, one more: 2.6e-4."""
     import gated_delta_rule_14_gb300 as kla
     T, gen = 600, torch.Generator(device=DEV).manual_seed(C)
 
