@@ -610,6 +610,7 @@ struct Lane<__nv_bfloat16, kLog, kBwd> {
     static __device__ __forceinline__ V advance(V h, V x, V k) { return fma2(a(k), h, kLog ? x : mul2(k, x)); }
     static __device__ __forceinline__ V shrink(V A, V k) { return mul2(A, a(k)); }
     static __device__ __forceinline__ V reach(V dh, V k) { return mul2(a(k), dh); }   // a dh
+    static __device__ __forceinline__ V loss(V k) { return k; }                       // 1 - a, of KLA_SCAN_SIGMOID
 };
 template <bool kLog, bool kBwd>
 struct Lane<float, kLog, kBwd> {
@@ -634,6 +635,7 @@ struct Lane<float, kLog, kBwd> {
         return kla::shrink<kLog>(A, kBwd ? coefficient<kLog>(a(k), w(k)) : k);
     }
     static __device__ __forceinline__ V reach(V dh, V k) { return a(k) * dh; }
+    static __device__ __forceinline__ V loss(V k) { return kBwd ? w(k) : k > 0.f ? k : 1.f + k; }
 };
 // The bf16 sigmoid of a warp with gates that Lane does not hold: a gate kept as its coefficient, of which both factors come
 // to their last bits.
@@ -664,8 +666,9 @@ __device__ __forceinline__ auto whole(const float (&v)[kV]) {
     if constexpr (kV == 1) return v[0];
     else return make_float2(v[0], v[1]);
 }
-// A lane's product of m factors, once more where it is close to 1. Few lanes need it: its loop unrolled, and with its
-// registers, costs the others 2 % of the backward pass.
+// A lane's product of m factors, once more where it is close to 1, from the gates: log gates, or those of Exact. Few lanes need
+// it, and its loop unrolled costs the others 2 % of the backward pass. 8 x 4096 x 2048 bf16 with log gates that are all
+// such, of -softplus(N(-10, 1)), 86 and 132 us, others 65 and 105.
 template <typename T, bool kLog, typename V, typename F>
 __device__ __forceinline__ V kept_product(V A, int count, int m, F gate) {
     constexpr int kV = sizeof(V) / sizeof(float);
@@ -686,6 +689,26 @@ __device__ __forceinline__ V kept_product(V A, int count, int m, F gate) {
     }
     return A;
 }
+// The same from the losses that a sigmoid's tokens are kept by: with gates of N(10, 1) 70 and 114 us, others 67 and 109 (from
+// the gates 93 and 132).
+template <typename L, int kTok, typename V>
+__device__ __forceinline__ V kept_product(V A, int count, int m, const V (&k)[kTok]) {
+    constexpr int kV = sizeof(V) / sizeof(float);
+    bool any = false;
+#pragma unroll
+    for (int v = 0; v < kV; ++v) any |= v < count && keeps(part(A, v), m);
+    if (any) {
+        V lost = L::all(0.f);
+#pragma unroll
+        for (int i = 0; i < kTok; ++i)
+            if (i < m) lost = L::fma(L::loss(k[i]), L::fma(lost, L::all(-1.f), L::all(1.f)), lost);
+        float a[kV];
+#pragma unroll
+        for (int v = 0; v < kV; ++v) a[v] = keeps(part(A, v), m) ? 1.f - part(lost, v) : part(A, v);
+        A = whole<kV>(a);
+    }
+    return A;
+}
 // The largest w of a lane's tokens, where it matters: bf16, sigmoid.
 template <typename T, bool kLog>
 struct Most {
@@ -699,7 +722,7 @@ struct Most {
     // 2^-23, 2^-14 of a (from -5 on, gates of N(0, 1) have one such in 2000 warps, and 8 x 4096 x 2048 took 70 us, not 67).
     // In other channels there may be anything: where there is one, the gates are looked at once more.
     // A warp as a whole, as lanes that go apart cost the others more: 8 x 4096 x 2048 66.7 and 109.1 us without Exact, 67.1
-    // and 109.6 with it, 118.8 and 177 where all warps take it; lane by lane 66.7 and 113.6.
+    // and 109.6 with it, 119.8 and 171 where all warps take it; lane by lane 66.7 and 113.6.
     template <typename F>
     __device__ __forceinline__ bool any(int count, int m, F gate) const {
         if (!kAsks) return false;
@@ -932,7 +955,8 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas) scan_fwd_ring_kernel(ScanA
         by_case<L, L>(m == kTok, false, map_tokens);
         const bool exact = most.any(count, m, [&](int i) { return of_g.template load<L>(gs + i * kRow, i); });
         if (exact) map_tokens(std::false_type{}, X{});
-        A = kept_product<T, kLog>(A, count, m, [&](int i) { return of_g.template load<L>(gs + i * kRow, i); });
+        if (kLog || exact) A = kept_product<T, kLog>(A, count, m, [&](int i) { return of_g.template load<L>(gs + i * kRow, i); });
+        else A = kept_product<L>(A, count, m, k);
         __syncwarp();
         map_a[warp][lane] = A;
         map_h[warp][lane] = H;
@@ -1176,7 +1200,8 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), kCtas) scan_bwd_ring_kernel
         by_case<L, L>(m == kTok, false, map_tokens);
         const bool exact = most.any(count, m, [&](int i) { return of_g.template load<L>(gs + i * kRow, i); });
         if (exact) map_tokens(std::false_type{}, X{});
-        A = kept_product<T, kLog>(A, count, m, [&](int i) { return of_g.template load<L>(gs + i * kRow, i); });
+        if (kLog || exact) A = kept_product<T, kLog>(A, count, m, [&](int i) { return of_g.template load<L>(gs + i * kRow, i); });
+        else A = kept_product<L>(A, count, m, k);
         __syncwarp();
         watch<kLog>(p, count, A);
         sh.a[turn & 1][warp][lane] = A;
